@@ -78,7 +78,8 @@ enum {
     PKV_DEV_BAD_SLOT = 4u,        /* slot >= num_blocks*block_size                           */
     PKV_DEV_BAD_PAIR = 8u,        /* copy pair id outside [0, num_blocks)                    */
     PKV_DEV_WAIT_TIMEOUT = 16u,   /* a bounded wait on an asynchronous copy gave up          */
-    PKV_DEV_BAD_QUERY_RANGE = 32u /* prefill: query_start / chunk length inconsistent         */
+    PKV_DEV_BAD_QUERY_RANGE = 32u,/* prefill: query_start / chunk length inconsistent         */
+    PKV_DEV_BAD_KEEP = 64u        /* eviction: kept length < 0 or > max_keep                 */
 };
 
 /*
@@ -392,6 +393,146 @@ int pkv_copy_blocks(const pkv_cache_desc* desc, void* k_pool, void* v_pool, cons
  */
 int pkv_upload_metadata(void* dst, const void* src_host, size_t bytes, void* stream);
 
+/* ---- 8-bit pools --------------------------------------------------------------------- */
+
+/*
+ * A cache that holds its rows in 8 bits: half the bytes of a 16-bit cache, in memory and for every
+ * decode step to read. (The pages have no counterpart.)
+ *   codes   K and V pools uint8 [n_layers][num_blocks][n_kv_heads][16][head_dim], each an e4m3 number
+ *           (sign, 4 exponent bits of bias 7, 3 mantissa bits; largest 448; 0x7f / 0xff are NaN)
+ *   scales  K and V float [n_layers][num_blocks][n_kv_heads]: one for each block and KV head
+ * A code stands for code * scale. The descriptor is that of the activations (q, k, v, out): fp16 or
+ * bf16; fp32 returns PKV_ERR_UNSUPPORTED. Zero-fill the scales before first use.
+ *
+ * pkv_q8_append writes powers of two: the least 2^e (e >= -15 for fp16 rows, -117 for bf16) that lets
+ * the block's largest finite element in, |x| <= 448 * 2^e. The attention calls take any scale >= 0.
+ * Values within a factor 2^14 of the block's largest keep e4m3's relative precision (2^-4); smaller
+ * ones lose bits, below 2^-10 * 2^e they round to zero.
+ */
+
+/* Bytes of one pool of codes (K or V), and of one array of scales, over all layers; 0 if unsupported. */
+uint64_t pkv_q8_pool_bytes(const pkv_cache_desc* desc);
+uint64_t pkv_q8_scale_bytes(const pkv_cache_desc* desc);
+
+/*
+ * pkv_kv_append into 8-bit pools: the rows of n_tokens new tokens are rounded (to nearest even) and
+ * written to their slots. A block's scale fits all the rows the call writes in it:
+ *   - a call that writes offset 0 of a block starts the block: what it held, scale included, is
+ *     forgotten (rows the call does not write keep their codes, whose values change with the scale);
+ *   - otherwise the scale grows if a new row needs it, and the block's other codes are brought to the
+ *     new scale: exactly, except where a code falls below 2^-6 and is rounded again. It never shrinks.
+ * Infinite and NaN elements become NaN codes and do not move the scale.
+ *   k, v          device [n_tokens][n_kv_heads][head_dim] of desc->dtype, 16-byte aligned
+ *   slot_mapping  device int64 [n_tokens], as pkv_kv_append (slot < 0 skipped; beyond the pool skipped
+ *                 and PKV_DEV_BAD_SLOT). Slots must be distinct and the tokens of one block lie within
+ *                 32 consecutive entries, as the block manager hands them out (else that block's
+ *                 content is unspecified)
+ *   k_codes .. v_scales  device, whole arrays (all layers); codes 16-byte aligned
+ */
+int pkv_q8_append(const pkv_cache_desc* desc, int32_t layer, const void* k, const void* v,
+                  const int64_t* slot_mapping, int32_t n_tokens, void* k_codes, void* v_codes, float* k_scales,
+                  float* v_scales, void* stream);
+
+/* pkv_copy_blocks for 8-bit pools: codes and scales of all layers; same arguments and errors otherwise. */
+int pkv_q8_copy_blocks(const pkv_cache_desc* desc, void* k_codes, void* v_codes, float* k_scales, float* v_scales,
+                       const int32_t* pairs, int32_t n_pairs, void* stream);
+
+/*
+ * Scratch bytes pkv_q8_decode_attention needs on the current device (scored: it is given scores);
+ * 0 when none is needed, and also for an unsupported descriptor, a bad count or no usable device.
+ */
+size_t pkv_q8_decode_workspace_bytes(const pkv_cache_desc* desc, int32_t n_seqs, int32_t max_blocks_per_seq,
+                                     int32_t scored);
+
+/*
+ * pkv_paged_decode_attention over 8-bit pools. Arguments, empty contexts, bad device values, limits
+ * and errors as there; a NaN among a row's own logits makes that output row NaN.
+ *   scores        NULL, or device float [n_seqs][n_kv_heads][score_stride], score_stride >=
+ *                 max_blocks_per_seq * 16: scores[s][g][j] += the attention weights of position j
+ *                 summed over the query heads of KV head g, for j < context_lens[s]. Row s of the
+ *                 batch owns row s of scores, also when sequences share blocks. Other entries are
+ *                 left as they are. fp32, each entry written by one thread: reproducible
+ *   workspace     device, >= pkv_q8_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
+ *                 initialisation; calls that overlap on the GPU must not share one
+ */
+int pkv_q8_decode_attention(const pkv_cache_desc* desc, int32_t layer, const void* q, const void* k_codes,
+                            const void* v_codes, const float* k_scales, const float* v_scales,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t n_seqs, float scale, void* out, float* scores, int64_t score_stride,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch bytes of pkv_q8_prefill_attention: one layer of K and V in the activations' type. */
+size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
+
+/*
+ * pkv_paged_prefill_attention over 8-bit pools (the chunk's rows already appended by pkv_q8_append).
+ * Two launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
+ * physical block like one layer of a 16-bit pool, and attended to from there. The first costs a little
+ * over a read of the codes and a write of twice their size; chunks of hundreds of tokens hide it.
+ * Widened values are exact in bf16; in fp16 too, but for 65,536, which is read as 65,504. Arguments,
+ * bad device values, limits and errors as pkv_paged_prefill_attention.
+ *   workspace     device, >= pkv_q8_prefill_workspace_bytes(desc) bytes, 16-byte aligned, memory of
+ *                 the current device; calls that overlap on the GPU must not share one
+ */
+int pkv_q8_prefill_attention(const pkv_cache_desc* desc, int32_t layer, const void* q, const void* k_codes,
+                             const void* v_codes, const float* k_scales, const float* v_scales,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* query_start, int32_t n_seqs, int32_t n_tokens, int32_t max_query_len,
+                             float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- eviction by accumulated attention weight ------------------------------------------ */
+
+/* Scratch bytes of pkv_paged_decode_attention_scored; 0 as pkv_q8_decode_workspace_bytes. */
+size_t pkv_scored_workspace_bytes(const pkv_cache_desc* desc, int32_t n_seqs, int32_t max_blocks_per_seq);
+
+/*
+ * pkv_paged_decode_attention that also adds each position's attention weight to the sequence's scores
+ * (scores, score_stride and workspace as pkv_q8_decode_attention; scores must be given). fp16 and bf16
+ * pools; fp32 returns PKV_ERR_UNSUPPORTED. To weigh a prompt by its last tokens, call it with rows of
+ * the same table and growing context_lens.
+ */
+int pkv_paged_decode_attention_scored(const pkv_cache_desc* desc, int32_t layer, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t n_seqs, float scale, void* out,
+                                      float* scores, int64_t score_stride, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/* Scratch bytes of pkv_evict_tokens: 0 for pools of desc->dtype, the old scales for 8-bit pools (q8). */
+size_t pkv_evict_workspace_bytes(const pkv_cache_desc* desc, int32_t n_seqs, int32_t max_blocks_per_seq, int32_t q8);
+
+/*
+ * Shorten sequences to the positions that attention has used most. For every layer, sequence s and KV
+ * head g, with c = context_lens[s], k = min(keep_lens[s], c) and R = min(recent, k): the last R
+ * positions stay, and of the others the k - R with the largest scores (ties: the lower position; NaN
+ * counts as the largest, so does +inf, which a caller may write to protect a position). Their K and V
+ * rows move, in order, to logical positions 0 .. k-1 of dst_tables, so the sequence's length is k
+ * afterwards in every layer and head, each with rows of its own choice. Keys move as they are: a
+ * position baked into them stays what it was.
+ *   k_pool, v_pool  device, whole pools (all layers), 16-byte aligned, of desc->dtype; or, with
+ *                   k_scales and v_scales, codes of 8-bit pools (else both NULL). A destination
+ *                   block's new scale is the largest among its rows' old ones; codes of smaller ones
+ *                   are brought to it (exactly, except where they fall below 2^-6)
+ *   src_tables, dst_tables  device int32 [n_seqs][max_blocks_per_seq]. dst_tables[s][i], i < ceil(k/16),
+ *                   is either src_tables[s][i] (in place; then no other sequence may hold that block)
+ *                   or a block in none of the src_tables rows; no block is listed twice.
+ *                   pkv_mgr_compact gives such tables
+ *   context_lens, keep_lens  device int32 [n_seqs]
+ *   scores, new_scores  device float [n_layers][n_seqs][n_kv_heads][score_stride], the same array or
+ *                   disjoint: new_scores[..][i] = the score of the i-th kept position for i < k, 0 for
+ *                   k <= i < c, left as it is beyond
+ *   kept            device int32 [n_layers][n_seqs][n_kv_heads][max_keep]: the positions kept, i < k;
+ *                   left as it is beyond
+ *   workspace       device, >= pkv_evict_workspace_bytes(...), 4-byte aligned
+ * Two launches. A sequence whose length is outside [0, max_blocks_per_seq*16] (PKV_DEV_BAD_CONTEXT_LEN),
+ * or whose keep_lens is negative or leaves more than max_keep (PKV_DEV_BAD_KEEP), is skipped whole. A
+ * row whose source or destination block lies outside the pool is not moved (PKV_DEV_BAD_BLOCK_ID).
+ */
+int pkv_evict_tokens(const pkv_cache_desc* desc, void* k_pool, void* v_pool, float* k_scales, float* v_scales,
+                     const int32_t* src_tables, const int32_t* dst_tables, int32_t max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* keep_lens, int32_t n_seqs, int32_t recent,
+                     const float* scores, float* new_scores, int64_t score_stride, int32_t* kept, int32_t max_keep,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Synchronise `stream`, then read and clear this library's device status word on the
  * current device (PKV_DEV_* bits, 0 if every device-side value was in range). For tests
@@ -505,6 +646,19 @@ int pkv_mgr_extend(pkv_mgr* mgr, int64_t seq_id, int32_t n_tokens, int64_t* slot
  */
 int pkv_mgr_append_batch(pkv_mgr* mgr, const int64_t* seq_ids, int32_t n, int64_t* slots_out,
                          int32_t* cow_pairs_out, int32_t* n_cow, int32_t* n_done);
+
+/*
+ * Shorten n distinct sequences to n_tokens[i] <= their length, all or nothing, as an eviction does: the
+ * first ceil(n_tokens[i]/16) blocks of a table stay, except that a block some other sequence holds too
+ * (before the call) is replaced by a fresh one, for the kept rows to move into; everything behind is
+ * released. A sequence that keeps its length keeps its table. All fresh blocks are taken before any
+ * block is released, so none of them is a block whose rows are still to be read. Take the source tables
+ * (pkv_mgr_pack_tables) before this call, the destination tables after it, and run pkv_evict_tokens
+ * before anything else is written to the pools. PKV_ERR_NO_BLOCKS (nothing changed, alloc_failures + 1)
+ * if the fresh blocks are not there; PKV_ERR_INVALID_ARG for an unknown or repeated id or a length that
+ * is negative or above the sequence's.
+ */
+int pkv_mgr_compact(pkv_mgr* mgr, const int64_t* seq_ids, int32_t n, const int32_t* n_tokens);
 
 /*
  * Release seq_id ("La idea de PagedAttention", step 4): each block loses one reference and

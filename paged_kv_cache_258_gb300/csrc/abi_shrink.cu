@@ -1,0 +1,386 @@
+// abi_shrink.cu -- the C ABI of 8-bit pools, of decode that sums its attention weights and of eviction:
+// argument validation, workspace layout, dispatch.
+#include "shrink.h"
+
+namespace pkv {
+
+cudaError_t launch_frag_q8_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_q8_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_scored_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_scored_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t frag_ctas_per_sm_q8_f16(int, int, int*);
+cudaError_t frag_ctas_per_sm_q8_bf16(int, int, int*);
+cudaError_t frag_ctas_per_sm_scored_f16(int, int, int*);
+cudaError_t frag_ctas_per_sm_scored_bf16(int, int, int*);
+
+cudaError_t frag_ctas_per_sm(int dtype, bool q8, int head_dim, int group, int* out) {
+    if (q8) return dtype == PKV_F16 ? frag_ctas_per_sm_q8_f16(head_dim, group, out) : frag_ctas_per_sm_q8_bf16(head_dim, group, out);
+    return dtype == PKV_F16 ? frag_ctas_per_sm_scored_f16(head_dim, group, out) : frag_ctas_per_sm_scored_bf16(head_dim, group, out);
+}
+
+cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, const FragArgs& a, cudaStream_t stream) {
+    const long long rows = (long long)a.d.num_blocks * a.d.n_kv * kBlock;
+    const int type = q8 ? kCodesE4M3 : dtype;
+    CUtensorMap tk, tv;
+    cudaError_t err = kv_tensor_map(a.d.k_layer, rows, head_dim, type, PKV_BOX_PANEL, &tk);
+    if (err == cudaSuccess) err = kv_tensor_map(a.d.v_layer, rows, head_dim, type, PKV_BOX_PANEL, &tv);
+    if (err != cudaSuccess) return err;
+    if (q8)
+        return dtype == PKV_F16 ? launch_frag_q8_f16(head_dim, group, a, tk, tv, stream)
+                                : launch_frag_q8_bf16(head_dim, group, a, tk, tv, stream);
+    return dtype == PKV_F16 ? launch_frag_scored_f16(head_dim, group, a, tk, tv, stream)
+                            : launch_frag_scored_bf16(head_dim, group, a, tk, tv, stream);
+}
+
+}  // namespace pkv
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t layer_elems(const pkv_cache_desc* d) { return (size_t)d->num_blocks * d->n_kv_heads * d->block_size * d->head_dim; }
+size_t layer_scales(const pkv_cache_desc* d) { return (size_t)d->num_blocks * d->n_kv_heads; }
+long long pool_rows(const pkv_cache_desc* d) { return (long long)d->num_blocks * d->n_kv_heads * d->block_size; }
+int group_of(const pkv_cache_desc* d) { return d->n_q_heads / d->n_kv_heads; }
+
+// A descriptor whose activations are 16-bit.
+int validate16(const pkv_cache_desc* d) {
+    const int rc = pkv_validate_desc(d);
+    if (rc != PKV_OK) return rc;
+    return d->dtype == PKV_F32 ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+// Partition geometry of the fragment kernel: the rule of the other decode calls with this kernel's
+// CTAs per SM (read once per device and kernel by the CUDA runtime's occupancy calculator).
+cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, int* bpp, int* n_parts) {
+    int sms = 0, per_sm = 0;
+    cudaError_t err = pkv::current_sm_count(&sms);
+    if (err == cudaSuccess) err = pkv::frag_ctas_per_sm(d->dtype, q8, d->head_dim, group_of(d), &per_sm);
+    if (err != cudaSuccess) return err;
+    *bpp = pkv::decode_blocks_per_partition(n_seqs, d->n_kv_heads, max_blocks, sms, per_sm, pkv::kMaxBppStreamed);
+    *n_parts = pkv::decode_partitions(max_blocks, *bpp);
+    return cudaSuccess;
+}
+
+struct FragLayout {
+    size_t ml, cnt, z, bytes;  // offsets; the partial outputs lie at 0
+};
+
+// Partial outputs, counters: split contexts only. (max, sum) pairs: those, or summed weights. Logits:
+// summed weights.
+FragLayout frag_layout(const pkv_cache_desc* d, int n_seqs, int max_blocks, int n_parts, bool scored) {
+    auto up = [](size_t x) { return (x + 15) / 16 * 16; };
+    const size_t rows = (size_t)n_seqs * d->n_q_heads;
+    FragLayout l{};
+    l.ml = n_parts > 1 ? up(rows * n_parts * d->head_dim * sizeof(float)) : 0;
+    l.cnt = l.ml + (n_parts > 1 || scored ? up(rows * n_parts * 2 * sizeof(float)) : 0);
+    l.z = l.cnt + (n_parts > 1 ? up((size_t)n_seqs * d->n_kv_heads * sizeof(unsigned long long)) : 0);
+    l.bytes = l.z + (scored ? up(rows * max_blocks * pkv::kBlock * sizeof(float)) : 0);
+    return l;
+}
+
+size_t frag_workspace(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, bool scored) {
+    if (validate16(d) != PKV_OK || n_seqs <= 0 || max_blocks <= 0) return 0;
+    int bpp = 0, n_parts = 0;
+    if (frag_geometry(d, q8, n_seqs, max_blocks, &bpp, &n_parts) != cudaSuccess) {
+        cudaGetLastError();  // no usable device: report nothing rather than a guess
+        return 0;
+    }
+    return frag_layout(d, n_seqs, max_blocks, n_parts, scored).bytes;
+}
+
+// Shared body of decode over 8-bit pools (q8) and of decode with summed weights (scores).
+int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, const void* k_pool, const void* v_pool,
+                const float* k_scales, const float* v_scales, const int32_t* tables, int32_t max_blocks,
+                const int32_t* lens, int32_t n_seqs, float scale, void* out, float* scores, int64_t score_stride,
+                void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = validate16(d);
+    if (rc != PKV_OK) return rc;
+    if (layer < 0 || layer >= d->n_layers || n_seqs < 0) return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0) return PKV_OK;
+    if (max_blocks <= 0 || max_blocks > (1 << 24)) return PKV_ERR_INVALID_ARG;
+    if (n_seqs > 65535 || d->n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (!q || !k_pool || !v_pool || !tables || !lens || !out) return PKV_ERR_INVALID_ARG;
+    if (q8 && (!k_scales || !v_scales || !aligned4(k_scales) || !aligned4(v_scales))) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID_ARG;
+    if (scores && (!aligned4(scores) || score_stride < (int64_t)max_blocks * pkv::kBlock)) return PKV_ERR_INVALID_ARG;
+    if (pool_rows(d) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;  // tensor-copy rows are 32-bit
+    int bpp = 0, n_parts = 0;
+    if (frag_geometry(d, q8, n_seqs, max_blocks, &bpp, &n_parts) != cudaSuccess) return PKV_ERR_CUDA;
+    const FragLayout l = frag_layout(d, n_seqs, max_blocks, n_parts, scores != nullptr);
+    if (l.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < l.bytes)) return PKV_ERR_INVALID_ARG;
+
+    pkv::FragArgs a;
+    const size_t elems = layer_elems(d) * (size_t)layer * (q8 ? 1 : 2);
+    char* ws = static_cast<char*>(workspace);
+    a.d.q = q;
+    a.d.k_layer = static_cast<const char*>(k_pool) + elems;
+    a.d.v_layer = static_cast<const char*>(v_pool) + elems;
+    a.d.tables = tables;
+    a.d.lens = lens;
+    a.d.out = out;
+    a.d.part_o = n_parts > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+    a.d.part_ml = n_parts > 1 || scores ? reinterpret_cast<float*>(ws + l.ml) : nullptr;
+    a.d.counters = n_parts > 1 ? reinterpret_cast<unsigned long long*>(ws + l.cnt) : nullptr;
+    a.d.call_tag = pkv::next_call_tag();
+    a.d.n_seqs = n_seqs;
+    a.d.n_q = d->n_q_heads;
+    a.d.n_kv = d->n_kv_heads;
+    a.d.num_blocks = d->num_blocks;
+    a.d.max_blocks = max_blocks;
+    a.d.n_parts = n_parts;
+    a.d.bpp = bpp;
+    a.d.scale_log2 = scale * 1.4426950408889634f;
+    if (q8) {
+        a.k_scales = k_scales + layer_scales(d) * layer;
+        a.v_scales = v_scales + layer_scales(d) * layer;
+    }
+    a.z = scores ? reinterpret_cast<float*>(ws + l.z) : nullptr;
+    if (pkv::device_status_word(&a.d.status) != cudaSuccess) return PKV_ERR_CUDA;
+    cudaError_t err = pkv::launch_frag_decode(d->dtype, q8, d->head_dim, group_of(d), a, static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return pkv::launch_status(err);
+    pkv::count_launches(1);
+    if (scores) {
+        pkv::ScoreArgs s;
+        s.z = a.z;
+        s.part_ml = a.d.part_ml;
+        s.lens = lens;
+        s.scores = scores;
+        s.stride = score_stride;
+        s.n_seqs = n_seqs;
+        s.n_kv = d->n_kv_heads;
+        s.group = group_of(d);
+        s.max_blocks = max_blocks;
+        s.n_parts = n_parts;
+        s.bpp = bpp;
+        if (pkv::launch_scores(s, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+        pkv::count_launches(1);
+    }
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t pkv_q8_pool_bytes(const pkv_cache_desc* d) {
+    return validate16(d) == PKV_OK ? (uint64_t)d->n_layers * layer_elems(d) : 0;
+}
+
+uint64_t pkv_q8_scale_bytes(const pkv_cache_desc* d) {
+    return validate16(d) == PKV_OK ? (uint64_t)d->n_layers * layer_scales(d) * sizeof(float) : 0;
+}
+
+int pkv_q8_append(const pkv_cache_desc* d, int32_t layer, const void* k, const void* v, const int64_t* slot_mapping,
+                  int32_t n_tokens, void* k_codes, void* v_codes, float* k_scales, float* v_scales, void* stream) {
+    int rc = validate16(d);
+    if (rc != PKV_OK) return rc;
+    if (layer < 0 || layer >= d->n_layers || n_tokens < 0) return PKV_ERR_INVALID_ARG;
+    if (n_tokens == 0) return PKV_OK;
+    if (!k || !v || !slot_mapping || !k_codes || !v_codes || !k_scales || !v_scales) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||
+        !aligned4(v_scales))
+        return PKV_ERR_INVALID_ARG;
+    if ((long long)n_tokens * d->n_kv_heads >= (1LL << 32)) return PKV_ERR_UNSUPPORTED;  // the grid is one warp per item
+    pkv::Q8AppendArgs a;
+    a.k = k;
+    a.v = v;
+    a.slots = slot_mapping;
+    a.k_codes = static_cast<uint8_t*>(k_codes) + layer_elems(d) * layer;
+    a.v_codes = static_cast<uint8_t*>(v_codes) + layer_elems(d) * layer;
+    a.k_scales = k_scales + layer_scales(d) * layer;
+    a.v_scales = v_scales + layer_scales(d) * layer;
+    a.n_tok = n_tokens;
+    a.n_kv = d->n_kv_heads;
+    a.num_blocks = d->num_blocks;
+    a.min_exp = pkv::q8_min_exp(d->dtype);
+    if (pkv::device_status_word(&a.status) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_q8_append(d->dtype, d->head_dim, a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+int pkv_q8_copy_blocks(const pkv_cache_desc* d, void* k_codes, void* v_codes, float* k_scales, float* v_scales,
+                       const int32_t* pairs, int32_t n_pairs, void* stream) {
+    int rc = validate16(d);
+    if (rc != PKV_OK) return rc;
+    if (n_pairs < 0) return PKV_ERR_INVALID_ARG;
+    if (n_pairs == 0) return PKV_OK;
+    if (!k_codes || !v_codes || !k_scales || !v_scales || !pairs) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) || !aligned4(v_scales)) return PKV_ERR_INVALID_ARG;
+    if (d->n_layers > 65535) return PKV_ERR_UNSUPPORTED;
+    pkv::Q8CopyArgs a;
+    a.k_codes = static_cast<uint8_t*>(k_codes);
+    a.v_codes = static_cast<uint8_t*>(v_codes);
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.pairs = pairs;
+    a.n_pairs = n_pairs;
+    a.n_layers = d->n_layers;
+    a.n_kv = d->n_kv_heads;
+    a.num_blocks = d->num_blocks;
+    a.block_bytes = (size_t)d->n_kv_heads * d->block_size * d->head_dim;
+    if (pkv::device_status_word(&a.status) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_q8_copy(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+size_t pkv_q8_decode_workspace_bytes(const pkv_cache_desc* d, int32_t n_seqs, int32_t max_blocks_per_seq, int32_t scored) {
+    return frag_workspace(d, true, n_seqs, max_blocks_per_seq, scored != 0);
+}
+
+int pkv_q8_decode_attention(const pkv_cache_desc* d, int32_t layer, const void* q, const void* k_codes,
+                            const void* v_codes, const float* k_scales, const float* v_scales,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t n_seqs, float scale, void* out, float* scores, int64_t score_stride, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    return frag_decode(true, d, layer, q, k_codes, v_codes, k_scales, v_scales, block_tables, max_blocks_per_seq,
+                       context_lens, n_seqs, scale, out, scores, score_stride, workspace, workspace_bytes, stream);
+}
+
+size_t pkv_scored_workspace_bytes(const pkv_cache_desc* d, int32_t n_seqs, int32_t max_blocks_per_seq) {
+    return frag_workspace(d, false, n_seqs, max_blocks_per_seq, true);
+}
+
+int pkv_paged_decode_attention_scored(const pkv_cache_desc* d, int32_t layer, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t n_seqs, float scale, void* out, float* scores,
+                                      int64_t score_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    if (n_seqs > 0 && !scores) return PKV_ERR_INVALID_ARG;
+    return frag_decode(false, d, layer, q, k_pool, v_pool, nullptr, nullptr, block_tables, max_blocks_per_seq,
+                       context_lens, n_seqs, scale, out, scores, score_stride, workspace, workspace_bytes, stream);
+}
+
+size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* d) {
+    return validate16(d) == PKV_OK ? 2 * layer_elems(d) * 2 : 0;
+}
+
+int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void* q, const void* k_codes,
+                             const void* v_codes, const float* k_scales, const float* v_scales,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* query_start, int32_t n_seqs, int32_t n_tokens, int32_t max_query_len,
+                             float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = validate16(d);
+    if (rc != PKV_OK) return rc;
+    if (layer < 0 || layer >= d->n_layers || n_seqs < 0 || n_tokens < 0 || max_query_len < 0 || max_query_len > n_tokens)
+        return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0 || max_query_len == 0) return PKV_OK;
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24)) return PKV_ERR_INVALID_ARG;
+    if (n_seqs > 65535 || pool_rows(d) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * d->n_kv_heads >= (1LL << 33)) return PKV_ERR_UNSUPPORTED;  // one warp per block and head
+    if (!q || !k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !context_lens || !query_start || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||
+        !aligned4(v_scales))
+        return PKV_ERR_INVALID_ARG;
+    const size_t need = pkv_q8_prefill_workspace_bytes(d);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return PKV_ERR_INVALID_ARG;
+
+    pkv::Q8WidenArgs w;
+    w.k_codes = static_cast<const uint8_t*>(k_codes) + layer_elems(d) * layer;
+    w.v_codes = static_cast<const uint8_t*>(v_codes) + layer_elems(d) * layer;
+    w.k_scales = k_scales + layer_scales(d) * layer;
+    w.v_scales = v_scales + layer_scales(d) * layer;
+    w.tables = block_tables;
+    w.lens = context_lens;
+    w.k_out = workspace;
+    w.v_out = static_cast<char*>(workspace) + need / 2;
+    w.n_seqs = n_seqs;
+    w.n_kv = d->n_kv_heads;
+    w.num_blocks = d->num_blocks;
+    w.max_blocks = max_blocks_per_seq;
+    if (pkv::device_status_word(&w.status) != cudaSuccess) return PKV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // the attention of 16-bit pools over the widened layer, a pool of one layer with the same blocks
+    const int per_cta = pkv::prefill_tokens_per_cta(d->dtype, d->head_dim, group_of(d));
+    pkv::PrefillArgs a;
+    a.q = q;
+    a.out = out;
+    a.k_layer = w.k_out;
+    a.v_layer = w.v_out;
+    a.tables = block_tables;
+    a.lens = context_lens;
+    a.q_start = query_start;
+    a.status = w.status;
+    a.n_seqs = n_seqs;
+    a.n_q = d->n_q_heads;
+    a.n_kv = d->n_kv_heads;
+    a.num_blocks = d->num_blocks;
+    a.max_blocks = max_blocks_per_seq;
+    a.n_tokens = n_tokens;
+    a.q_tiles = (max_query_len + per_cta - 1) / per_cta;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    if (pkv::launch_q8_widen(d->dtype, d->head_dim, w, st) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    cudaError_t err = pkv::launch_prefill(d->dtype, d->head_dim, group_of(d), a, st);
+    if (err != cudaSuccess) return pkv::launch_status(err);
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+size_t pkv_evict_workspace_bytes(const pkv_cache_desc* d, int32_t n_seqs, int32_t max_blocks_per_seq, int32_t q8) {
+    if (pkv_validate_desc(d) != PKV_OK || n_seqs <= 0 || max_blocks_per_seq <= 0 || !q8) return 0;
+    return 2 * (size_t)d->n_layers * n_seqs * d->n_kv_heads * max_blocks_per_seq * sizeof(float);
+}
+
+int pkv_evict_tokens(const pkv_cache_desc* d, void* k_pool, void* v_pool, float* k_scales, float* v_scales,
+                     const int32_t* src_tables, const int32_t* dst_tables, int32_t max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* keep_lens, int32_t n_seqs, int32_t recent,
+                     const float* scores, float* new_scores, int64_t score_stride, int32_t* kept, int32_t max_keep,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const bool q8 = k_scales != nullptr || v_scales != nullptr;
+    int rc = q8 ? validate16(d) : pkv_validate_desc(d);
+    if (rc != PKV_OK) return rc;
+    if (n_seqs < 0 || recent < 0 || max_keep < 0) return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0) return PKV_OK;
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24) || max_keep < 1) return PKV_ERR_INVALID_ARG;
+    if (n_seqs > 65535 || d->n_layers > 65535) return PKV_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool || !src_tables || !dst_tables || !context_lens || !keep_lens || !scores || !new_scores || !kept)
+        return PKV_ERR_INVALID_ARG;
+    if (q8 && (!k_scales || !v_scales || !aligned4(k_scales) || !aligned4(v_scales))) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(scores) || !aligned4(new_scores) || !aligned4(kept))
+        return PKV_ERR_INVALID_ARG;
+    if (score_stride < (int64_t)max_blocks_per_seq * pkv::kBlock) return PKV_ERR_INVALID_ARG;
+    const size_t need = pkv_evict_workspace_bytes(d, n_seqs, max_blocks_per_seq, q8);
+    if (need > 0 && (!workspace || !aligned4(workspace) || workspace_bytes < need)) return PKV_ERR_INVALID_ARG;
+
+    pkv::EvictArgs a;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.src = src_tables;
+    a.dst = dst_tables;
+    a.lens = context_lens;
+    a.keep = keep_lens;
+    a.scores = scores;
+    a.new_scores = new_scores;
+    a.kept = kept;
+    a.old_scales = static_cast<float*>(workspace);
+    a.stride = score_stride;
+    a.n_layers = d->n_layers;
+    a.n_seqs = n_seqs;
+    a.n_kv = d->n_kv_heads;
+    a.num_blocks = d->num_blocks;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_keep = max_keep;
+    a.recent = recent;
+    a.row_bytes = d->head_dim * (q8 ? 1 : d->dtype == PKV_F32 ? 4 : 2);
+    int sms = 0;
+    if (pkv::current_sm_count(&sms) != cudaSuccess || pkv::device_status_word(&a.status) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    // A row's columns are cut among CTAs while there would be fewer than 8 CTAs an SM, to pieces of 32
+    // bytes (one DRAM sector) at least.
+    const long long pairs = (long long)n_seqs * d->n_kv_heads;
+    a.slices = 1;
+    while (a.row_bytes / (2 * a.slices) >= 32 && 2 * pairs * d->n_layers * a.slices < 8LL * sms) a.slices *= 2;
+    if (pairs * a.slices > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    if (pkv::launch_evict(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::count_launches(2);
+    return PKV_OK;
+}
+
+}  // extern "C"

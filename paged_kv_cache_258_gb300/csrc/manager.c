@@ -462,6 +462,84 @@ int pkv_mgr_free_seq(pkv_mgr* m, int64_t seq_id) {
     return PKV_OK;
 }
 
+static int cmp_i64(const void* a, const void* b) {
+    const int64_t x = *(const int64_t*)a, y = *(const int64_t*)b;
+    return x < y ? -1 : (x > y);
+}
+
+int pkv_mgr_compact(pkv_mgr* m, const int64_t* seq_ids, int32_t n, const int32_t* n_tokens) {
+    if (!m || n < 0 || (n > 0 && (!seq_ids || !n_tokens))) return PKV_ERR_INVALID_ARG;
+    if (n == 0) return PKV_OK;
+    int64_t fresh = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const int64_t pos = map_find(m, seq_ids[i]);
+        if (pos < 0 || n_tokens[i] < 0 || n_tokens[i] > m->map[pos].ctx) return PKV_ERR_INVALID_ARG;
+        const seq_rec* s = &m->map[pos];
+        if (n_tokens[i] == s->ctx) continue;
+        const int32_t keep = blocks_for(m, n_tokens[i]);
+        for (int32_t b = 0; b < keep; ++b) fresh += m->ref[s->table[b]] > 1;
+    }
+    int64_t* ids = (int64_t*)malloc(sizeof(int64_t) * (size_t)n);
+    int32_t* got = (int32_t*)malloc(sizeof(int32_t) * (size_t)(fresh > 0 ? fresh : 1));
+    if (!ids || !got) {
+        free(ids);
+        free(got);
+        return PKV_ERR_BAD_STATE;
+    }
+    memcpy(ids, seq_ids, sizeof(int64_t) * (size_t)n);
+    qsort(ids, (size_t)n, sizeof(int64_t), cmp_i64);
+    int rc = PKV_OK;
+    for (int32_t i = 1; i < n; ++i)
+        if (ids[i] == ids[i - 1]) rc = PKV_ERR_INVALID_ARG;
+    free(ids);
+    if (rc == PKV_OK && fresh > m->n_free) {
+        m->alloc_failures++;
+        rc = PKV_ERR_NO_BLOCKS;
+    }
+    for (int64_t i = 0; rc == PKV_OK && i < fresh; ++i) {
+        got[i] = alloc_one(m);
+        if (got[i] < 0) { /* injected failure: undo in reverse so the free list is restored exactly */
+            for (int64_t k = i - 1; k >= 0; --k) {
+                m->ref[got[k]] = 0;
+                ring_push_front(m, got[k]);
+            }
+            m->alloc_failures++;
+            rc = PKV_ERR_NO_BLOCKS;
+        }
+    }
+    if (rc != PKV_OK) {
+        free(got);
+        return rc;
+    }
+    /* shared blocks first, judged by the reference counts before any of them drops: mark the entries
+     * with their fresh block and drop the references afterwards */
+    int64_t at = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        seq_rec* s = &m->map[map_find(m, seq_ids[i])];
+        if (n_tokens[i] == s->ctx) continue;
+        const int32_t keep = blocks_for(m, n_tokens[i]);
+        for (int32_t b = 0; b < keep; ++b)
+            if (m->ref[s->table[b]] > 1) {
+                const int32_t old = s->table[b];
+                s->table[b] = got[at];
+                got[at++] = old;
+            }
+    }
+    at = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        seq_rec* s = &m->map[map_find(m, seq_ids[i])];
+        const int32_t keep = blocks_for(m, n_tokens[i]);
+        for (int32_t b = keep; b < s->n_blocks; ++b)
+            if (--m->ref[s->table[b]] == 0) ring_push_back(m, s->table[b]);
+        s->n_blocks = keep;
+        s->ctx = n_tokens[i];
+    }
+    for (; at < fresh; ++at)
+        if (--m->ref[got[at]] == 0) ring_push_back(m, got[at]);
+    free(got);
+    return PKV_OK;
+}
+
 int pkv_mgr_block_table(const pkv_mgr* m, int64_t seq_id, int32_t* out, int32_t cap, int32_t* n_blocks,
                         int32_t* ctx_len) {
     if (!m) return PKV_ERR_INVALID_ARG;

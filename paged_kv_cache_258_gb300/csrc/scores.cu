@@ -1,0 +1,111 @@
+// scores.cu -- attention weights from the logits a decode launch left behind, added to each sequence's
+// running sums (sm_103a).
+//
+//   scores[s][g][j] += sum_{h in group g} 2^(z_hj - m_h) / l_h,   j < len_s,
+// m_h and l_h the row's final maximum and sum, joined here from the partitions' pairs. A position's
+// weight needs them, and they exist only when the whole row has been read, so this is a launch of its
+// own, a programmatic dependent of the attention: its CTAs are resident and wait when the last
+// attention CTA ends. It reads 4 G bytes and reads and writes 4 bytes a token and head (the logits of
+// moderate batches still lie in L2). Sums are fp32; every score is written by one thread and heads are
+// added in order, so results do not depend on timing.
+#include <math.h>
+
+#include "common.cuh"
+#include "shrink.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = 4;  // positions of a thread, kThreads apart
+
+template <int G>
+__device__ __forceinline__ void load_logits(const float* p, float* z) {
+    if constexpr (G == 1) {
+        z[0] = __ldcs(p);
+    } else if constexpr (G == 2) {
+        const float2 u = __ldcs(reinterpret_cast<const float2*>(p));
+        z[0] = u.x;
+        z[1] = u.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < G / 4; ++i) {
+            const float4 u = __ldcs(reinterpret_cast<const float4*>(p) + i);
+            z[4 * i] = u.x;
+            z[4 * i + 1] = u.y;
+            z[4 * i + 2] = u.z;
+            z[4 * i + 3] = u.w;
+        }
+    }
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a) {
+    __shared__ float s_m[8], s_inv[8];
+    const int s = blockIdx.z, g = blockIdx.y;
+    const int cap = a.max_blocks * kBlock;
+    const int ctx = min(max(a.lens[s], 0), cap);
+    const int j0 = blockIdx.x * kThreads * kPerThread;
+    if (j0 >= ctx) return;
+    const int nb = (ctx + kBlock - 1) / kBlock;
+    const int np = (nb + a.bpp - 1) / a.bpp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    if (warp < G) {
+        const size_t row = ((size_t)s * a.n_kv + g) * G + warp;
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.n_parts;
+        float m = -INFINITY, l = 0.f;
+        for (int q = lane; q < np; q += 32) m = fmaxf(m, __ldcg(ml + q).x);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int q = lane; q < np; q += 32) {
+            const float2 u = __ldcg(ml + q);
+            l += u.y * (u.x == -INFINITY ? 0.f : exp2f(u.x - m));
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+            s_m[warp] = m == -INFINITY ? 0.f : m;
+            s_inv[warp] = l == 0.f ? 0.f : 1.f / l;
+        }
+    }
+    __syncthreads();
+    const size_t base = ((size_t)s * a.n_kv + g);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int j = j0 + i * kThreads + threadIdx.x;
+        if (j < ctx) {
+            float z[G], w = 0.f;
+            load_logits<G>(a.z + (base * cap + j) * G, z);
+#pragma unroll
+            for (int r = 0; r < G; ++r) w += exp2f(z[r] - s_m[r]) * s_inv[r];
+            a.scores[base * a.stride + j] += w;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scores(const ScoreArgs& a, cudaStream_t stream) {
+    constexpr int kChunk = kThreads * kPerThread;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)a.max_blocks * kBlock + kChunk - 1) / kChunk), a.n_kv, a.n_seqs);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err;
+    switch (a.group) {
+    case 1: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<1>, a); break;
+    case 2: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<2>, a); break;
+    case 4: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<4>, a); break;
+    case 8: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<8>, a); break;
+    default: return cudaErrorInvalidValue;
+    }
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace pkv

@@ -10,6 +10,8 @@
 //                  of prefill, read by the tensor cores one 16-key block at a time);
 //   PKV_BOX_BLOCK_HALF  the same with a 64 x 16 x D/128 box: half of the chunk's columns (the V
 //                  blocks of a prefill CTA pair, whose CTAs each hold half of every V block).
+// A pool of 8-bit codes has PKV_BOX_PANEL maps alone: a 128-column x 16-row box, or at D = 64 the
+// whole 64-byte row with the 64-byte swizzle.
 // Encoding goes through the driver entry point cuTensorMapEncodeTiled, found once through the
 // runtime; maps are cached by (address, shape, type, box, device) in a hash table so steady-state
 // calls do not re-encode: a step touches up to 3 maps per layer (K panels, V panels, V blocks), so
@@ -26,6 +28,7 @@
 #include <unordered_map>
 
 #include "internal.h"
+#include "shrink.h"
 
 namespace pkv {
 namespace {
@@ -78,7 +81,8 @@ cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 
 cudaError_t kv_tensor_map(const void* layer_base, long long rows, int head_dim, int dtype, int box,
                           CUtensorMap* out) {
-    if (dtype != PKV_F16 && dtype != PKV_BF16) return cudaErrorInvalidValue;
+    if (dtype != PKV_F16 && dtype != PKV_BF16 && !(dtype == kCodesE4M3 && box == PKV_BOX_PANEL))
+        return cudaErrorInvalidValue;
     if (box != PKV_BOX_PANEL && box != PKV_BOX_BLOCK && box != PKV_BOX_BLOCK_HALF) return cudaErrorInvalidValue;
     if (box == PKV_BOX_BLOCK_HALF && (head_dim % 128) != 0) return cudaErrorInvalidValue;
     if (rows <= 0 || rows >= (1LL << 31) || (head_dim % 64) != 0) return cudaErrorInvalidValue;
@@ -108,15 +112,21 @@ cudaError_t kv_tensor_map(const void* layer_base, long long rows, int head_dim, 
     const cuuint32_t rank = blk ? 3 : 2;
     // dims / box innermost first; strides (bytes) of dims 1.. (the panel dim of the 3-D form steps
     // 64 elements = 128 bytes inside a row)
+    // 8-bit codes: panels of 128 columns (128 bytes), or the whole 64-byte row with the 64-byte swizzle
+    const bool codes = dtype == kCodesE4M3;
+    const cuuint32_t panel = codes ? (head_dim < 128 ? (cuuint32_t)head_dim : 128u) : 64u;
     const cuuint64_t dims[3] = {blk ? 64u : (cuuint64_t)head_dim, (cuuint64_t)rows, (cuuint64_t)(head_dim / 64)};
-    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, 128};
-    const cuuint32_t boxdim[3] = {64, (cuuint32_t)kBlock,
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * (codes ? 1 : 2), 128};
+    const cuuint32_t boxdim[3] = {panel, (cuuint32_t)kBlock,
                                   (cuuint32_t)(box == PKV_BOX_BLOCK_HALF ? head_dim / 128 : head_dim / 64)};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     CUtensorMap map;
-    CUresult r = encode(&map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+    CUresult r = encode(&map,
+                        codes               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         rank, const_cast<void*>(layer_base), dims, strides, boxdim, elem_strides,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, codes && head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     if (g_maps->size() >= kMaxMaps) g_maps->clear();

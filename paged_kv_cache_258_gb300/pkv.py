@@ -19,6 +19,7 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_NO_BLOCKS, PKV_ERR_BAD
 STATUS_NAMES = {0: "ok", 1: "invalid", 2: "unsupported", 3: "no_blocks", 4: "bad_state", 5: "cuda"}
 PKV_DEV_BAD_BLOCK_ID, PKV_DEV_BAD_CONTEXT_LEN, PKV_DEV_BAD_SLOT, PKV_DEV_BAD_PAIR, PKV_DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 PKV_DEV_BAD_QUERY_RANGE = 32
+PKV_DEV_BAD_KEEP = 64
 PKV_DECODE_OVERLAP_PREVIOUS = 1
 PKV_PREFILL_OVERLAP_PREVIOUS = 1
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
@@ -94,6 +95,23 @@ def lib():
         "pkv_launch_count": (c_u64, []),
         "pkv_hbm_read_probe": (ctypes.c_int, [vp, c_sz, vp, vp]),
         "pkv_selftest_wait_timeout": (ctypes.c_int, [vp]),
+        "pkv_q8_pool_bytes": (c_u64, [dp]),
+        "pkv_q8_scale_bytes": (c_u64, [dp]),
+        "pkv_q8_append": (ctypes.c_int, [dp, c_i32, vp, vp, vp, c_i32, vp, vp, vp, vp, vp]),
+        "pkv_q8_copy_blocks": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, c_i32, vp]),
+        "pkv_q8_decode_workspace_bytes": (c_sz, [dp, c_i32, c_i32, c_i32]),
+        "pkv_q8_decode_attention": (ctypes.c_int, [dp, c_i32, vp, vp, vp, vp, vp, vp, c_i32, vp, c_i32,
+                                                   ctypes.c_float, vp, vp, c_i64, vp, c_sz, vp]),
+        "pkv_q8_prefill_workspace_bytes": (c_sz, [dp]),
+        "pkv_q8_prefill_attention": (ctypes.c_int, [dp, c_i32, vp, vp, vp, vp, vp, vp, c_i32, vp, vp, c_i32, c_i32,
+                                                    c_i32, ctypes.c_float, vp, vp, c_sz, vp]),
+        "pkv_scored_workspace_bytes": (c_sz, [dp, c_i32, c_i32]),
+        "pkv_paged_decode_attention_scored": (ctypes.c_int, [dp, c_i32, vp, vp, vp, vp, c_i32, vp, c_i32,
+                                                             ctypes.c_float, vp, vp, c_i64, vp, c_sz, vp]),
+        "pkv_evict_workspace_bytes": (c_sz, [dp, c_i32, c_i32, c_i32]),
+        "pkv_evict_tokens": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, c_i32, vp, vp, c_i32, c_i32, vp, vp, c_i64,
+                                            vp, c_i32, vp, c_sz, vp]),
+        "pkv_mgr_compact": (ctypes.c_int, [vp, vp, c_i32, vp]),
         "pkv_mgr_create": (vp, [c_i32, c_i32, vp]),
         "pkv_mgr_clone": (vp, [vp]),
         "pkv_mgr_destroy": (None, [vp]),
@@ -531,6 +549,220 @@ def append_launcher(desc: CacheDesc, k, v, slot_mapping, k_pool, v_pool, stream=
     return launch
 
 
+# ---- 8-bit pools, decode that sums its attention weights, eviction ----------------------------------
+#
+# An 8-bit pool is a torch.float8_e4m3fn tensor of pool_shape(desc) (the codes) and a float32 tensor of
+# scale_shape(desc); a code stands for code * scale of its block and KV head. desc.dtype is that of the
+# activations, "f16" or "bf16".
+
+def scale_shape(desc: CacheDesc):
+    """[n_layers, num_blocks, n_kv]: one scale for each block and KV head of an 8-bit pool."""
+    return (desc.n_layers, desc.num_blocks, desc.n_kv_heads)
+
+
+def _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur):
+    t = _torch()
+    pool, sc = pool_shape(desc), scale_shape(desc)
+    return (_dev(k_codes, "k_codes", t.float8_e4m3fn, pool, cur=cur), _dev(v_codes, "v_codes", t.float8_e4m3fn, pool, cur=cur),
+            _dev(k_scales, "k_scales", t.float32, sc, cur=cur), _dev(v_scales, "v_scales", t.float32, sc, cur=cur))
+
+
+def _workspace(workspace, cur):
+    if workspace is None:
+        return ctypes.c_void_p(0), 0
+    return _dev(workspace, "workspace", cur=cur), workspace.numel() * workspace.element_size()
+
+
+def _scores(scores, name, lead, max_blocks: int, cur):
+    """(pointer, stride) of float32 scores [*lead, S], S >= max_blocks * 16."""
+    if scores.dim() != len(lead) + 1 or scores.shape[-1] < max_blocks * BLOCK:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, at least {max_blocks * BLOCK}], "
+                         f"got {tuple(scores.shape)}")
+    stride = int(scores.shape[-1])
+    return _dev(scores, name, _torch().float32, (*lead, stride), cur=cur), stride
+
+
+def _table_width(block_tables) -> int:
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [n_seqs, max_blocks]")
+    return int(block_tables.shape[1])
+
+
+def _bytes_tensor(n: int, device):
+    t = _torch()
+    return t.empty(-(-n // 16) * 4, dtype=t.float32, device=device) if n else None
+
+
+def pkv_q8_pool_bytes(desc: CacheDesc) -> int:
+    return int(lib().pkv_q8_pool_bytes(ctypes.byref(desc)))
+
+
+def pkv_q8_scale_bytes(desc: CacheDesc) -> int:
+    return int(lib().pkv_q8_scale_bytes(ctypes.byref(desc)))
+
+
+def pkv_q8_decode_workspace_bytes(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, scored: bool = False) -> int:
+    return int(lib().pkv_q8_decode_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(max_blocks_per_seq), int(scored)))
+
+
+def pkv_scored_workspace_bytes(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int) -> int:
+    return int(lib().pkv_scored_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(max_blocks_per_seq)))
+
+
+def pkv_q8_prefill_workspace_bytes(desc: CacheDesc) -> int:
+    return int(lib().pkv_q8_prefill_workspace_bytes(ctypes.byref(desc)))
+
+
+def pkv_evict_workspace_bytes(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, q8: bool) -> int:
+    return int(lib().pkv_evict_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(max_blocks_per_seq), int(q8)))
+
+
+def alloc_q8_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, scored: bool = False, device="cuda"):
+    """A device buffer for pkv_q8_decode_attention (None where it needs none)."""
+    return _bytes_tensor(pkv_q8_decode_workspace_bytes(desc, n_seqs, max_blocks_per_seq, scored), device)
+
+
+def alloc_scored_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, device="cuda"):
+    """A device buffer for pkv_paged_decode_attention_scored."""
+    return _bytes_tensor(pkv_scored_workspace_bytes(desc, n_seqs, max_blocks_per_seq), device)
+
+
+def alloc_q8_prefill_workspace(desc: CacheDesc, device="cuda"):
+    """A device buffer for pkv_q8_prefill_attention: one layer of K and V in 16 bits."""
+    return _bytes_tensor(pkv_q8_prefill_workspace_bytes(desc), device)
+
+
+def alloc_evict_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, device="cuda"):
+    """A device buffer for pkv_evict_tokens over 8-bit pools."""
+    return _bytes_tensor(pkv_evict_workspace_bytes(desc, n_seqs, max_blocks_per_seq, True), device)
+
+
+def pkv_q8_append(desc: CacheDesc, layer: int, k, v, slot_mapping, k_codes, v_codes, k_scales, v_scales,
+                  stream=None) -> None:
+    """pkv_kv_append into 8-bit pools: rows k, v [n_tokens, n_kv, d] are rounded to codes."""
+    t = _torch()
+    dt = torch_dtype(desc.dtype_name)
+    cur = _current_device()
+    n_tok = int(k.shape[0])
+    row = (n_tok, desc.n_kv_heads, desc.head_dim)
+    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
+    rc = lib().pkv_q8_append(ctypes.byref(desc), int(layer), _dev(k, "k", dt, row, cur=cur), _dev(v, "v", dt, row, cur=cur),
+                             _dev(slot_mapping, "slot_mapping", t.int64, (n_tok,), cur=cur), n_tok, kc, vc, ks, vs,
+                             _stream_handle(stream))
+    _check(rc, "pkv_q8_append")
+
+
+def pkv_q8_copy_blocks(desc: CacheDesc, k_codes, v_codes, k_scales, v_scales, pairs, stream=None) -> None:
+    t = _torch()
+    cur = _current_device()
+    n_pairs = int(pairs.shape[0])
+    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
+    rc = lib().pkv_q8_copy_blocks(ctypes.byref(desc), kc, vc, ks, vs, _dev(pairs, "pairs", t.int32, (n_pairs, 2), cur=cur),
+                                  n_pairs, _stream_handle(stream))
+    _check(rc, "pkv_q8_copy_blocks")
+
+
+def pkv_q8_decode_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k_scales, v_scales, block_tables,
+                            context_lens, scale: float, out, workspace=None, scores=None, stream=None) -> None:
+    """pkv_paged_decode_attention over 8-bit pools; scores float32 [n_seqs, n_kv, S] gain each
+    position's attention weight (workspace then from alloc_q8_workspace(..., scored=True))."""
+    t = _torch()
+    dt = torch_dtype(desc.dtype_name)
+    cur = _current_device()
+    n_seqs, max_blocks = int(q.shape[0]), _table_width(block_tables)
+    qshape = (n_seqs, desc.n_q_heads, desc.head_dim)
+    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
+    sp, stride = (None, 0) if scores is None else _scores(scores, "scores", (n_seqs, desc.n_kv_heads), max_blocks, cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    rc = lib().pkv_q8_decode_attention(
+        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur), kc, vc, ks, vs,
+        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
+        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur), n_seqs, float(scale),
+        _dev(out, "out", dt, qshape, cur=cur), sp, stride, ws, ws_bytes, _stream_handle(stream))
+    _check(rc, "pkv_q8_decode_attention")
+
+
+def pkv_q8_prefill_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k_scales, v_scales, block_tables,
+                             context_lens, query_start, max_query_len: int, scale: float, out, workspace,
+                             stream=None) -> None:
+    """pkv_paged_prefill_attention over 8-bit pools (workspace from alloc_q8_prefill_workspace)."""
+    t = _torch()
+    dt = torch_dtype(desc.dtype_name)
+    cur = _current_device()
+    n_tokens, max_blocks, n_seqs = int(q.shape[0]), _table_width(block_tables), int(block_tables.shape[0])
+    qshape = (n_tokens, desc.n_q_heads, desc.head_dim)
+    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    rc = lib().pkv_q8_prefill_attention(
+        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur), kc, vc, ks, vs,
+        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
+        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur),
+        _dev(query_start, "query_start", t.int32, (n_seqs + 1,), cur=cur), n_seqs, n_tokens, int(max_query_len),
+        float(scale), _dev(out, "out", dt, qshape, cur=cur), ws, ws_bytes, _stream_handle(stream))
+    _check(rc, "pkv_q8_prefill_attention")
+
+
+def pkv_paged_decode_attention_scored(desc: CacheDesc, layer: int, q, k_pool, v_pool, block_tables, context_lens,
+                                      scale: float, out, scores, workspace, stream=None) -> None:
+    """pkv_paged_decode_attention that adds each position's attention weight to scores, float32
+    [n_seqs, n_kv, S] (workspace from alloc_scored_workspace)."""
+    t = _torch()
+    dt = torch_dtype(desc.dtype_name)
+    cur = _current_device()
+    n_seqs, max_blocks = int(q.shape[0]), _table_width(block_tables)
+    qshape = (n_seqs, desc.n_q_heads, desc.head_dim)
+    sp, stride = _scores(scores, "scores", (n_seqs, desc.n_kv_heads), max_blocks, cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    rc = lib().pkv_paged_decode_attention_scored(
+        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur),
+        _dev(k_pool, "k_pool", dt, pool_shape(desc), cur=cur), _dev(v_pool, "v_pool", dt, pool_shape(desc), cur=cur),
+        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
+        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur), n_seqs, float(scale),
+        _dev(out, "out", dt, qshape, cur=cur), sp, stride, ws, ws_bytes, _stream_handle(stream))
+    _check(rc, "pkv_paged_decode_attention_scored")
+
+
+def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent: int,
+                     scores, new_scores, kept, stream=None, k_scales=None, v_scales=None, workspace=None) -> None:
+    """Shorten each sequence to its `recent` last and its highest-scored positions, keep_lens[s] in all.
+
+    scores, new_scores float32 [n_layers, n_seqs, n_kv, S] (the same tensor, or two disjoint ones);
+    kept int32 [n_layers, n_seqs, n_kv, max_keep]. For 8-bit pools k_pool / v_pool are the codes, with
+    k_scales, v_scales and a workspace from alloc_evict_workspace.
+    """
+    t = _torch()
+    cur = _current_device()
+    n_seqs, max_blocks = int(src_tables.shape[0]), _table_width(src_tables)
+    q8 = k_scales is not None or v_scales is not None
+    if q8:
+        if k_scales is None or v_scales is None:
+            raise ValueError("8-bit pools need k_scales and v_scales")
+        kp, vp, ks, vs = _q8_pools(desc, k_pool, v_pool, k_scales, v_scales, cur)
+    else:
+        dt = torch_dtype(desc.dtype_name)
+        kp, vp = _dev(k_pool, "k_pool", dt, pool_shape(desc), cur=cur), _dev(v_pool, "v_pool", dt, pool_shape(desc), cur=cur)
+        ks = vs = None
+    lead = (desc.n_layers, n_seqs, desc.n_kv_heads)
+    sp, stride = _scores(scores, "scores", lead, max_blocks, cur)
+    np_, _ = _scores(new_scores, "new_scores", lead, max_blocks, cur)
+    if tuple(new_scores.shape) != tuple(scores.shape):
+        raise ValueError("new_scores must have the shape of scores")
+    nbytes = scores.numel() * 4
+    if sp.value is not None and sp.value != np_.value and abs((sp.value or 0) - (np_.value or 0)) < nbytes:
+        raise ValueError("new_scores must be scores itself or not overlap it")
+    if kept.dim() != 4:
+        raise ValueError("kept must be [n_layers, n_seqs, n_kv, max_keep]")
+    max_keep = int(kept.shape[3])
+    ws, ws_bytes = _workspace(workspace, cur)
+    rc = lib().pkv_evict_tokens(
+        ctypes.byref(desc), kp, vp, ks, vs, _dev(src_tables, "src_tables", t.int32, (n_seqs, max_blocks), cur=cur),
+        _dev(dst_tables, "dst_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
+        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur),
+        _dev(keep_lens, "keep_lens", t.int32, (n_seqs,), cur=cur), n_seqs, int(recent), sp, np_, stride,
+        _dev(kept, "kept", t.int32, (*lead, max_keep), cur=cur), max_keep, ws, ws_bytes, _stream_handle(stream))
+    _check(rc, "pkv_evict_tokens")
+
+
 def pkv_get_device_status(stream=None) -> int:
     flags = ctypes.c_uint32(0)
     _check(lib().pkv_get_device_status(_stream_handle(stream), ctypes.byref(flags)), "pkv_get_device_status")
@@ -653,6 +885,14 @@ class BlockManager:
         rc = lib().pkv_mgr_append_batch(self._h, _i64p(ids), n, _i64p(slots), _i32p(pairs),
                                         ctypes.byref(n_cow), ctypes.byref(n_done))
         return rc, slots[:n_done.value], pairs[:2 * n_cow.value].reshape(-1, 2), int(n_done.value)
+
+    def compact(self, seq_ids, n_tokens) -> int:
+        """Shorten distinct sequences to n_tokens[i] tokens each, all or nothing (pkv_mgr_compact)."""
+        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        lens = np.ascontiguousarray(np.asarray(n_tokens, dtype=np.int32))
+        if ids.shape != lens.shape or ids.ndim != 1:
+            raise ValueError("one length for each sequence")
+        return lib().pkv_mgr_compact(self._h, _i64p(ids), len(ids), _i32p(lens))
 
     def free_seq(self, seq_id: int) -> int:
         return lib().pkv_mgr_free_seq(self._h, int(seq_id))

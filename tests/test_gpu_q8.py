@@ -1,0 +1,392 @@
+"""8-bit pools on the GPU: quantising append, block copies, decode (with and without summed weights) and
+prefill, against 64-bit restatements."""
+import numpy as np
+import pytest
+import torch
+
+import shrink_oracle as R
+from helpers import as_f64, to_host, to_torch
+from paged_kv_cache_258_gb300 import pkv
+from paged_kv_cache_258_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+BLOCK = 16
+
+
+def codes_to_torch(c):
+    return torch.from_numpy(np.ascontiguousarray(c)).cuda().view(torch.float8_e4m3fn)
+
+
+def codes_to_host(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def values(rng, shape, dtype):
+    """(storage array, the same in float64)"""
+    x = W.normal_values(rng, shape, dtype)
+    return x, as_f64(to_torch(x, dtype, device="cpu"))
+
+
+def same_codes(a, b):
+    """Equal codes; the two NaN codes count as one."""
+    return np.array_equal(np.where(a & 127 == 127, 127, a), np.where(b & 127 == 127, 127, b))
+
+
+def filled_pools(rng, nb, n_kv, d, spread=3):
+    """Random codes (no NaN) and power-of-two scales over 2 * spread binades."""
+    c = rng.integers(0, 256, size=(1, nb, n_kv, BLOCK, d), dtype=np.uint8)
+    c[c & 127 == 127] ^= 1
+    s = 2.0 ** rng.integers(-spread, spread + 1, size=(1, nb, n_kv)).astype(np.float64) / 64
+    return c, s.astype(np.float32)
+
+
+def gpu_append(desc, x, y, slots, kc, vc, ks, vs, dtype):
+    t = [codes_to_torch(kc), codes_to_torch(vc), torch.from_numpy(ks).cuda(), torch.from_numpy(vs).cuda()]
+    pkv.pkv_q8_append(desc, 0, to_torch(x, dtype), to_torch(y, dtype), torch.from_numpy(slots).cuda(), *t)
+    return codes_to_host(t[0]), codes_to_host(t[1]), t[2].cpu().numpy(), t[3].cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n_kv", [1, 3, 8])
+def test_append_is_bit_exact(dtype, d, n_kv):
+    """Whole blocks, blocks continued (their scale grows or not), blocks started, padding in between."""
+    rng = np.random.default_rng(d + n_kv)
+    nb = 12
+    kc, ks = filled_pools(rng, nb, n_kv, d)
+    vc, vs = filled_pools(rng, nb, n_kv, d)
+    ks[0, 7], vs[0, 7] = 64.0, 64.0                 # large enough: stays
+    ks[0, 8], vs[0, 8] = 2.0 ** -12, 2.0 ** -12     # far too small: old rows fall below the grid
+    slots = [3 * 16 + i for i in range(16)]          # a whole block
+    slots += [7 * 16 + i for i in (5, 6, 7)]         # a block continued
+    slots += [8 * 16 + 15]
+    slots += [-1, 2 * 16 + 0, -1, 2 * 16 + 1]        # a block started, padding inside
+    slots += [9 * 16 + i for i in (9, 4, 12)]        # not in order
+    slots = np.array(slots, dtype=np.int64)
+    x, xf = values(rng, (len(slots), n_kv, d), dtype)
+    y, yf = values(rng, (len(slots), n_kv, d), dtype)
+    desc = pkv.make_desc(dtype, 1, nb, n_kv, n_kv, d)
+    got = gpu_append(desc, x, y, slots, kc, vc, ks, vs, dtype)
+    assert pkv.pkv_get_device_status() == 0
+    R.append(xf, slots, kc[0], ks[0], dtype)
+    R.append(yf, slots, vc[0], vs[0], dtype)
+    assert np.array_equal(got[2], ks) and np.array_equal(got[3], vs)
+    assert same_codes(got[0], kc) and same_codes(got[1], vc)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_append_of_special_values(dtype):
+    """Zeros, subnormals, the largest finite value, infinities and NaN; a scale's borders."""
+    rng = np.random.default_rng(1)
+    d, nb = 64, 8
+    big = 65504.0 if dtype == "f16" else 3.3895313892515355e38
+    tiny = 2.0 ** -24 if dtype == "f16" else 2.0 ** -133
+    rows = np.zeros((7, 1, d))
+    rows[1, 0, :4] = [tiny, -tiny, 3 * tiny, 0]
+    rows[2, 0, :4] = [big, -big, 1.0, -1.0]
+    rows[3] = rng.standard_normal(d)
+    rows[3, 0, :3] = [np.inf, -np.inf, np.nan]
+    rows[4, 0, :3] = [448.0, 447.0, 1.0]             # exactly the border of a scale
+    rows[5, 0, :3] = [450.0 if dtype == "bf16" else 448.25, 1.0, -0.0]  # just above it
+    rows[6, 0, :2] = [np.inf, np.nan]                # nothing finite but zeros
+    x = torch.from_numpy(rows).to(pkv.torch_dtype(dtype))
+    xf = x.double().numpy()
+    slots = np.arange(7, dtype=np.int64) * 16        # each starts a block of its own
+    kc, vc = np.full((2, 1, nb, 1, BLOCK, d), 0x55, dtype=np.uint8)
+    ks, vs = np.full((2, 1, nb, 1), 8.0, dtype=np.float32)
+    desc = pkv.make_desc(dtype, 1, nb, 1, 1, d)
+    t = [codes_to_torch(kc), codes_to_torch(vc), torch.from_numpy(ks).cuda(), torch.from_numpy(vs).cuda()]
+    pkv.pkv_q8_append(desc, 0, x.cuda(), (2 * x).clamp(-big, big).cuda(), torch.from_numpy(slots).cuda(), *t)
+    R.append(xf, slots, kc[0], ks[0], dtype)
+    assert np.array_equal(t[2].cpu().numpy(), ks)
+    assert same_codes(codes_to_host(t[0]), kc)
+    assert np.array_equal(t[3].cpu().numpy()[0, 7], vs[0, 7])  # untouched
+
+
+def test_append_skips_bad_slots_and_flags_them():
+    rng = np.random.default_rng(2)
+    d, nb = 128, 4
+    kc, ks = filled_pools(rng, nb, 2, d)
+    vc, vs = filled_pools(rng, nb, 2, d)
+    slots = np.array([-5, nb * 16, 17, nb * 16 + 3, -1], dtype=np.int64)
+    x, xf = values(rng, (5, 2, d), "bf16")
+    desc = pkv.make_desc("bf16", 1, nb, 2, 2, d)
+    got = gpu_append(desc, x, x, slots, kc, vc, ks, vs, "bf16")
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_SLOT
+    R.append(xf, slots, kc[0], ks[0], "bf16")
+    assert np.array_equal(got[2], ks) and same_codes(got[0], kc)
+
+
+@pytest.mark.parametrize("d,n_kv", [(64, 1), (128, 4), (256, 3)])
+def test_token_by_token_equals_the_definition(d, n_kv):
+    """A block filled one row at a time, its scale growing on the way; then started anew."""
+    rng = np.random.default_rng(3)
+    dtype, nb = "bf16", 2
+    kc, ks = filled_pools(rng, nb, n_kv, d)
+    vc, vs = filled_pools(rng, nb, n_kv, d)
+    desc = pkv.make_desc(dtype, 1, nb, n_kv, n_kv, d)
+    t = [codes_to_torch(kc), codes_to_torch(vc), torch.from_numpy(ks).cuda(), torch.from_numpy(vs).cuda()]
+    for step in range(20):
+        rows = rng.standard_normal((1, n_kv, d)) * 2.0 ** rng.integers(-6, 7)
+        x = torch.from_numpy(rows).to(torch.bfloat16)
+        slots = np.array([16 + step % 16], dtype=np.int64)
+        pkv.pkv_q8_append(desc, 0, x.cuda(), (-x).cuda(), torch.from_numpy(slots).cuda(), *t)
+        R.append(x.double().numpy(), slots, kc[0], ks[0], dtype)
+        R.append(-x.double().numpy(), slots, vc[0], vs[0], dtype)
+        assert np.array_equal(t[2].cpu().numpy(), ks) and np.array_equal(t[3].cpu().numpy(), vs), step
+        assert same_codes(codes_to_host(t[0]), kc) and same_codes(codes_to_host(t[1]), vc), step
+
+
+def test_copy_blocks_moves_codes_and_scales():
+    rng = np.random.default_rng(4)
+    L, nb, n_kv, d = 3, 9, 5, 64
+    c = rng.integers(0, 256, size=(2, L, nb, n_kv, BLOCK, d), dtype=np.uint8)
+    s = rng.random((2, L, nb, n_kv), dtype=np.float32)
+    t = [codes_to_torch(c[0]), codes_to_torch(c[1]), torch.from_numpy(s[0].copy()).cuda(), torch.from_numpy(s[1].copy()).cuda()]
+    desc = pkv.make_desc("f16", L, nb, n_kv, n_kv, d)
+    pairs = np.array([[0, 4], [8, 2], [3, 99], [-1, 5]], dtype=np.int32)
+    pkv.pkv_q8_copy_blocks(desc, *t, torch.from_numpy(pairs).cuda())
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_PAIR
+    for a, b in pairs[:2]:
+        c[:, :, b], s[:, :, b] = c[:, :, a], s[:, :, a]
+    assert np.array_equal(codes_to_host(t[0]), c[0]) and np.array_equal(codes_to_host(t[1]), c[1])
+    assert np.array_equal(t[2].cpu().numpy(), s[0]) and np.array_equal(t[3].cpu().numpy(), s[1])
+
+
+def q8_case(dtype, lens, n_q, n_kv, d, seed, spread=3, slack=3, max_blocks=None):
+    """Pools whose unused rows hold NaN codes and whose unused blocks have NaN scales."""
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens, dtype=np.int32)
+    nbs = -(-lens.astype(np.int64) // BLOCK)
+    nb = int(nbs.sum()) + slack
+    tables = W.shuffled_tables(lens, nb, seed, max_blocks=max_blocks or max(1, int(nbs.max())))
+    kc, ks = filled_pools(rng, nb, n_kv, d, spread)
+    vc, vs = filled_pools(rng, nb, n_kv, d, spread)
+    used = np.zeros((nb, BLOCK), dtype=bool)
+    for s, c in enumerate(lens):
+        for j in range(int(c)):
+            used[tables[s, j // BLOCK], j % BLOCK] = True
+    for c in (kc, vc):
+        c[0] = np.where(used[:, None, :, None], c[0], 0x7F)
+    for s in (ks, vs):
+        s[0, ~used.any(1)] = np.nan
+    q, qf = values(rng, (len(lens), n_q, d), dtype)
+    desc = pkv.make_desc(dtype, 1, nb, n_q, n_kv, d)
+    dev = dict(q=to_torch(q, dtype), k=codes_to_torch(kc), v=codes_to_torch(vc), ks=torch.from_numpy(ks).cuda(),
+               vs=torch.from_numpy(vs).cuda(), tables=torch.from_numpy(np.ascontiguousarray(tables)).cuda(),
+               lens=torch.from_numpy(lens).cuda())
+    return desc, dev, qf, R.widen(kc[0], ks[0]), R.widen(vc[0], vs[0]), tables, lens
+
+
+def run_decode(desc, t, scale, scores=None, stream=None, ws=True):
+    out = torch.full_like(t["q"], float("nan"))
+    w = pkv.alloc_q8_workspace(desc, t["q"].shape[0], t["tables"].shape[1], scored=scores is not None) if ws else None
+    if w is not None:
+        w.fill_(float("nan"))
+    pkv.pkv_q8_decode_attention(desc, 0, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"], scale, out, w,
+                                scores=scores, stream=stream)
+    return out
+
+
+def check_decode(desc, t, qf, kf, vf, tables, lens, dtype, scale, scored=True):
+    want, tol, w, w_tol = R.decode(qf, np.nan_to_num(kf), np.nan_to_num(vf), tables, lens, scale, dtype, 2.0 ** -11)
+    out = run_decode(desc, t, scale)
+    assert pkv.pkv_get_device_status() == 0
+    err = np.abs(as_f64(out) - want)
+    assert np.all(err <= tol), (float((err / np.maximum(tol, 1e-300)).max()),)
+    if scored:
+        S = tables.shape[1] * BLOCK + 5                      # a stride of its own, not a multiple of anything
+        start = torch.rand((len(lens), desc.n_kv_heads, S), device="cuda")
+        scores = start.clone()
+        out2 = run_decode(desc, t, scale, scores)
+        assert torch.equal(out2, out)                        # summing weights does not change the output
+        got, was = scores.double().cpu().numpy(), start.double().cpu().numpy()
+        total = was[:, :, :w.shape[2]] + w
+        e = np.abs(got[:, :, :w.shape[2]] - total)
+        assert np.all(e <= w_tol + 2.0 ** -23 * total)
+        j = np.arange(S)[None, None] >= lens[:, None, None]
+        assert np.array_equal(got[np.broadcast_to(j, got.shape)], was[np.broadcast_to(j, was.shape)])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_decode_matches(dtype, d, G):
+    lens = [0, 1, 15, 16, 17, 33, 100, 511]
+    case = q8_case(dtype, lens, 2 * G, 2, d, seed=d + G)
+    check_decode(*case, dtype, 1 / np.sqrt(d) / 16)
+
+
+@pytest.mark.parametrize("d,G,n_kv,lens", [(128, 4, 1, [5000, 3, 0, 1024, 1025]), (256, 8, 2, [2049, 4097]),
+                                           (64, 1, 3, [9000]), (128, 1, 32, [700, 1300, 64, 2048])])
+def test_decode_of_split_contexts(d, G, n_kv, lens):
+    case = q8_case("bf16", lens, G * n_kv, n_kv, d, seed=7, max_blocks=max(lens) // 16 + 9)
+    check_decode(*case, "bf16", 1 / np.sqrt(d) / 16)
+
+
+def test_decode_keeps_small_blocks_beside_huge_ones():
+    """Scales 2^60 apart: a block of tiny V that holds all the weight is not lost beside a huge one that
+    holds none. The huge block's keys point away from the query."""
+    dtype, d = "bf16", 128
+    desc, t, qf, kf, vf, tables, lens = q8_case(dtype, [64], 1, 1, d, seed=11, spread=0)
+    first, last = int(tables[0, 0]), int(tables[0, 3])
+    t["vs"][0, first], t["vs"][0, last] = 2.0 ** 30, 2.0 ** -30
+    q = torch.ones_like(t["q"])
+    codes = t["k"].view(torch.uint8)
+    codes[0] = 0x38                                      # 1.0
+    codes[0, first] = 0xB8                               # -1.0
+    codes[0, int(tables[0, 1])] = codes[0, int(tables[0, 2])] = 0xB8
+    t["q"], t["ks"][:] = q, 1.0
+    k = R.VALUES[codes_to_host(t["k"])[0]]
+    v = R.VALUES[codes_to_host(t["v"])[0]] * t["vs"][0].double().cpu().numpy()[..., None, None]
+    want, tol, _, _ = R.decode(np.ones((1, 1, d)), k, v, tables, lens, 1.0, dtype, 2.0 ** -11)
+    out = run_decode(desc, t, 1.0)
+    # exp(-256) of 2^30-sized rows is far below the rest: both terms of the tolerance are the small block's
+    assert np.all(np.abs(as_f64(out) - want) <= tol) and np.abs(want).max() < 2.0 ** -20
+
+
+def test_decode_reads_any_scale_and_zero():
+    """Scales that are no powers of two, and zero (its rows read as zeros)."""
+    desc, t, qf, kf, vf, tables, lens = q8_case("f16", [50, 20], 4, 2, 64, seed=12)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for n in ("ks", "vs"):
+        t[n].copy_(torch.rand(t[n].shape, device="cuda", generator=g) / 32)
+    t["vs"][0, int(tables[0, 1])] = 0.0
+    t["ks"][0, int(tables[0, 2])] = 0.0
+    pools = [R.widen(codes_to_host(t[a])[0], t[b][0].double().cpu().numpy()) for a, b in (("k", "ks"), ("v", "vs"))]
+    check_decode(desc, t, qf, pools[0], pools[1], tables, lens, "f16", 0.125)
+
+
+def test_decode_nan_and_infinite_inputs_reach_the_row_only():
+    desc, t, qf, kf, vf, tables, lens = q8_case("bf16", [1500, 40, 300], 8, 2, 64, seed=13)
+    t["k"].view(torch.uint8)[0, int(tables[0, 3]), 0, 2, 5] = 0x7F      # a NaN key of sequence 0, head 0
+    t["q"][1, 6, 3] = float("nan")                                      # query head 6 of sequence 1
+    out = run_decode(desc, t, 0.02)
+    scores = torch.zeros((3, 2, tables.shape[1] * BLOCK), device="cuda")
+    again = run_decode(desc, t, 0.02, scores)
+    assert torch.equal(torch.isnan(out), torch.isnan(again))
+    nan = torch.isnan(out).cpu().numpy()
+    assert nan[0, :4].all() and not nan[0, 4:].any()
+    assert nan[1, 6].all() and not nan[1, :6].any() and not nan[1, 7].any()
+    assert not nan[2].any()
+    assert torch.isnan(scores[0, 0, :1500]).all() and not torch.isnan(scores[0, 1]).any()
+    assert torch.isnan(scores[1, 1, :40]).all() and not torch.isnan(scores[2]).any()
+
+
+def test_decode_of_large_queries():
+    """bf16 queries past fp16's range, and far below it."""
+    for size in (2.0 ** 40, 2.0 ** -60, 2.0 ** -130):
+        desc, t, qf, kf, vf, tables, lens = q8_case("bf16", [100, 7], 2, 1, 128, seed=14)
+        t["q"] = (t["q"].double() * size).to(torch.bfloat16)
+        # a scale that brings the logits back; 2^120 twice for the smallest
+        scale = float(np.float32(min(1 / size, 2.0 ** 120))) / 200
+        want, tol, _, _ = R.decode(as_f64(t["q"]), np.nan_to_num(kf), np.nan_to_num(vf), tables, lens, scale, "bf16",
+                                   2.0 ** -11)
+        assert np.all(np.abs(as_f64(run_decode(desc, t, scale)) - want) <= tol), size
+
+
+def test_decode_skips_and_flags_bad_device_values():
+    desc, t, qf, kf, vf, tables, lens = q8_case("f16", [64, 30], 2, 1, 128, seed=15)
+    t["tables"][0, 2] = desc.num_blocks + 7
+    scores = torch.zeros((2, 1, tables.shape[1] * BLOCK), device="cuda")
+    out = run_decode(desc, t, 0.1, scores)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_BLOCK_ID
+    live = [j for j in range(64) if j // 16 != 2]
+    k, v = R.rows_of(kf, tables[0], 64, 0)[live], R.rows_of(vf, tables[0], 64, 0)[live]
+    for h in range(2):
+        want, w = R.attend(qf[0, h], k, v, 0.1)
+        assert np.allclose(as_f64(out)[0, h], want, rtol=0, atol=2.0 ** -9 * np.abs(v).max())
+    got = scores[0, 0].cpu().numpy()
+    assert np.all(got[32:48] == 0) and abs(got.sum() - 2) < 1e-4
+    t["lens"][1] = 16 * tables.shape[1] + 1                 # clamped to the table's width
+    t["tables"][0, 2] = int(tables[0, 2])
+    t["tables"][1] = t["tables"][0]
+    out = run_decode(desc, t, 0.1)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_CONTEXT_LEN
+    assert torch.isfinite(out).all()
+    t["lens"][1] = -3
+    out = run_decode(desc, t, 0.1)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_CONTEXT_LEN
+    assert torch.all(out[1] == 0)
+
+
+def test_decode_sequences_that_share_blocks_keep_their_own_scores():
+    desc, t, qf, kf, vf, tables, lens = q8_case("bf16", [200, 200], 4, 2, 64, seed=16)
+    t["tables"][1] = t["tables"][0]
+    t["lens"][1] = 77
+    tables = t["tables"].cpu().numpy()
+    check_decode(desc, t, qf, kf, vf, tables, np.array([200, 77]), "bf16", 0.01)
+
+
+def test_decode_in_a_graph_and_on_another_stream():
+    desc, t, qf, kf, vf, tables, lens = q8_case("bf16", [1800, 40], 8, 2, 128, seed=17)
+    scores = torch.zeros((2, 2, tables.shape[1] * BLOCK), device="cuda")
+    want = run_decode(desc, t, 0.01, scores)
+    once = scores.clone()
+    side = torch.cuda.Stream()
+    ws = pkv.alloc_q8_workspace(desc, 2, tables.shape[1], scored=True)
+    out = torch.zeros_like(want)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        scores.zero_()
+        args = (desc, 0, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"], 0.01, out, ws)
+        pkv.pkv_q8_decode_attention(*args, scores=scores)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            pkv.pkv_q8_decode_attention(*args, scores=scores)
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(scores, once)
+        out.zero_()
+        for _ in range(3):
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert torch.allclose(scores, 4 * once, rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 8), (128, 4), (256, 2), (256, 4)])
+def test_prefill_matches(dtype, d, G):
+    """Chunks of 1 to 200 tokens, one over an empty cache, one inside a block; rows owned by no sequence."""
+    lens, counts = [5, 200, 333, 40], [5, 63, 1, 40]
+    n_kv = 2
+    desc, t, _, kf, vf, tables, lens = q8_case(dtype, lens, G * n_kv, n_kv, d, seed=d * G)
+    rng = np.random.default_rng(5)
+    start = np.array([0, 5, 68, 69, 109], dtype=np.int32)
+    q, qf = values(rng, (112, G * n_kv, d), dtype)
+    out = torch.full((112, G * n_kv, d), 7.0, dtype=pkv.torch_dtype(dtype), device="cuda")
+    ws = pkv.alloc_q8_prefill_workspace(desc)
+    ws.fill_(float("nan"))
+    scale = 1 / np.sqrt(d) / 16
+    pkv.pkv_q8_prefill_attention(desc, 0, to_torch(q, dtype), t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"],
+                                 torch.from_numpy(start).cuda(), 63, scale, out, ws)
+    assert pkv.pkv_get_device_status() == 0
+    got = as_f64(out)
+    assert np.all(got[109:] == 7.0)
+    step = R.HALF_STEP[dtype]                               # the 16-bit prefill rounds its weights to the storage type
+    for s in range(4):
+        for i in range(counts[s]):
+            p = int(lens[s]) - counts[s] + i
+            row = start[s] + i
+            want, tol, _, _ = R.decode(qf[row:row + 1], np.nan_to_num(kf), np.nan_to_num(vf), tables[s:s + 1],
+                                       np.array([p + 1]), scale, dtype, step)
+            # weights up to 2^8 of the running maximum's: their sum may be of unrounded ones (one more half step)
+            assert np.all(np.abs(got[row] - want[0]) <= 2 * tol[0]), (s, i)
+
+
+def test_prefill_reads_the_largest_halves():
+    """65,504 is held as 65,536 in codes; prefill reads it as 65,504, decode as what the code stands for."""
+    d = 64
+    desc = pkv.make_desc("f16", 1, 2, 1, 1, d)
+    kc = torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vc, sc = torch.zeros_like(kc.view(torch.uint8)).view(torch.float8_e4m3fn), torch.zeros(pkv.scale_shape(desc), device="cuda")
+    sv = torch.zeros_like(sc)
+    x = torch.full((1, 1, d), 65504.0, dtype=torch.float16, device="cuda")
+    pkv.pkv_q8_append(desc, 0, x, x, torch.zeros(1, dtype=torch.int64, device="cuda"), kc, vc, sc, sv)
+    tables, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    out = torch.empty((1, 1, d), dtype=torch.float16, device="cuda")
+    q = torch.zeros_like(x)
+    pkv.pkv_q8_prefill_attention(desc, 0, q, kc, vc, sc, sv, tables, lens, torch.tensor([0, 1], dtype=torch.int32).cuda(), 1,
+                                 1.0, out, pkv.alloc_q8_prefill_workspace(desc))
+    assert torch.all(out == 65504.0)
+    assert float(sv[0, 0, 0]) == 256.0
