@@ -48,19 +48,19 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
     return r;
 }
 
-template <bool Q8, int D, int NW, int ST>
+// NW warps, each with a ring of ST stages of BPI blocks (K tiles, then V tiles).
+template <bool Q8, int D, int NW, int ST, int BPI>
 struct FragGeom {
     static constexpr int ROWB = D * (Q8 ? 1 : 2);            // bytes of a row
     static constexpr int PANB = ROWB < 128 ? ROWB : 128;     // bytes of a panel's row (one TMA box)
     static constexpr int PANELS = ROWB / PANB;
     static constexpr int PANEL = kBlock * PANB;
     static constexpr uint32_t TILE = kBlock * ROWB;
+    static constexpr uint32_t STAGE = 2 * BPI * TILE;
     static constexpr int KCH = ROWB / 64;                    // 16-byte chunks of a K row per lane
-    static constexpr size_t STAGES = (size_t)NW * ST * 2 * TILE;
-    static constexpr size_t BARS = STAGES;                               // uint64 [NW][ST][K, V]
-    static constexpr size_t PHYS = BARS + (size_t)NW * ST * 16;          // int [NW][ST]
-    static constexpr size_t SCALE = (PHYS + (size_t)NW * ST * 4 + 7) / 8 * 8;  // float2 [NW][ST] (K, V)
-    static constexpr size_t ML = (SCALE + (size_t)NW * ST * 8 + 15) / 16 * 16;  // float [NW][8][2]
+    static constexpr size_t STAGES = (size_t)NW * ST * STAGE;
+    static constexpr size_t BARS = STAGES;                            // uint64 [NW][ST][K, V]
+    static constexpr size_t ML = BARS + (size_t)NW * ST * 16;         // float [NW][8][2]
     static constexpr size_t TOTAL = ML + (size_t)NW * 8 * 2 * 4;
     static constexpr size_t ALLOC = TOTAL + 1024;             // room to align the base
     static constexpr size_t MERGE = (size_t)NW * 8 * D * 4;  // merge scratch, after the combine buffer
@@ -104,6 +104,13 @@ __device__ __forceinline__ void load4(const T* p, float* f) {
     f[3] = b.y;
 }
 
+// 2^x, x <= 0 in every use or a rounding above it; 2 ulp, results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 constexpr float kWeightExp = 15.f;  // exponent of the largest fp16 weight
 
 // Split-K epilogue of the CTA (s, g, p) of a sequence with np > 1 partitions: the CTA that arrives last
@@ -125,7 +132,7 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(cnt);
+        unsigned long long cur = 0;  // what the first arrival finds: one round trip less than reading it
         unsigned long long next;
         while (true) {
             next = ((cur >> 24) == a.call_tag) ? cur + 1 : ((a.call_tag << 24) | 1ull);
@@ -142,9 +149,9 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     const int lane = threadIdx.x & 31;
     const size_t row0 = (size_t)s * a.n_q + (size_t)g * G;
     for (int r = warp; r < G; r += NWARP) {
-        const float* ml = a.part_ml + (row0 + r) * a.n_parts * 2;
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (row0 + r) * a.n_parts;
         float m = -INFINITY;
-        for (int q = lane; q < np; q += 32) m = fmaxf(m, __ldcg(ml + 2 * q));
+        for (int q = lane; q < np; q += 32) m = fmaxf(m, __ldcg(ml + q).x);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) {
@@ -158,13 +165,13 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     for (int c0 = 0; c0 < np; c0 += kMergeChunk) {
         __syncthreads();  // maxima visible; the previous chunk's weights consumed
         for (int r = warp; r < G; r += NWARP) {
-            const float* ml = a.part_ml + (row0 + r) * a.n_parts * 2;
+            const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (row0 + r) * a.n_parts;
             const int q = c0 + lane;
             float w = 0.f, lw = 0.f;
             if (q < np) {
-                const float m = __ldcg(ml + 2 * q);
-                w = m == -INFINITY ? 0.f : exp2f(m - sM[r]);
-                lw = __ldcg(ml + 2 * q + 1) * w;
+                const float2 u = __ldcg(ml + q);
+                w = u.x == -INFINITY ? 0.f : ex2(u.x - sM[r]);
+                lw = u.y * w;
             }
             sW[r * kMergeChunk + lane] = w;
 #pragma unroll
@@ -208,11 +215,13 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     if (threadIdx.x == 0) *cnt = 0ull;
 }
 
-template <typename T, bool Q8, int D, int G, int NW, int ST>
-__global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa, const __grid_constant__ CUtensorMap tm_k,
-                                                              const __grid_constant__ CUtensorMap tm_v) {
+template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS>
+__global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragArgs fa,
+                                                                    const __grid_constant__ CUtensorMap tm_k,
+                                                                    const __grid_constant__ CUtensorMap tm_v) {
     static_assert(G <= 8, "at most 8 query rows per KV head");
-    using S = FragGeom<Q8, D, NW, ST>;
+    static_assert(BPI == 1 || BPI == 2, "one or two blocks per iteration");
+    using S = FragGeom<Q8, D, NW, ST, BPI>;
     using MT = typename std::conditional<Q8, __half, T>::type;  // type of the matrix instructions' operands
     using M = MmaType<MT>;
     constexpr int KSTEPS = D / 16;  // QK k-steps = PV m-tiles
@@ -234,17 +243,13 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
     const int s = blockIdx.z;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // Table entries of this warp's blocks, 32 per chunk in registers: the chunk in use, the next one
-    // (with its blocks' scales already on their way) and the one after.
+    // This warp's i-th block (i = BPI k + u) is block BPI (warp + k NW) + u of the partition. Table
+    // entries come in chunks of 32 held in registers (lane l: entry 32 c + l): the chunk whose copies
+    // are being issued, the next, and the one after; scales follow a chunk behind the tables.
+    auto local_block = [&](int i) -> long long { return (long long)(i / BPI) * (NW * BPI) + warp * BPI + i % BPI; };
     auto load_chunk = [&](int c) -> int {
-        const long long kk = (long long)c * 32 + lane;
-        const long long idx = (long long)p * a.bpp + warp + kk * NW;
-        return kk * NW + warp < a.bpp && idx < a.max_blocks ? a.tables[(size_t)s * a.max_blocks + idx] : -1;
-    };
-    auto load_scales = [&](int phys) -> float2 {
-        if (!Q8 || (unsigned)phys >= (unsigned)a.num_blocks) return make_float2(0.f, 0.f);
-        const size_t i = (size_t)phys * a.n_kv + g;
-        return make_float2(__ldg(fa.k_scales + i), __ldg(fa.v_scales + i));
+        const long long b = local_block(c * 32 + lane), idx = (long long)p * a.bpp + b;
+        return b < a.bpp && idx < a.max_blocks ? a.tables[(size_t)s * a.max_blocks + idx] : -1;
     };
     int t0 = load_chunk(0);
     int t1 = a.bpp > 32 * NW ? load_chunk(1) : -1;
@@ -266,79 +271,95 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
     }
     const int nblk = min(a.bpp, nb - b0);
     const bool single = nb <= a.bpp;
-    const int nk = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;
-    // entries past the sequence's last block may be anything: their scales are not read
-    auto mine = [&](int c, int phys) { return c * 32 + lane < nk ? phys : -1; };
-    float2 s0 = load_scales(mine(0, t0));
-    float2 s1 = load_scales(mine(1, t1));
+    // iterations of this warp, and its blocks (the last iteration may have one less than BPI)
+    const int nk = nblk > warp * BPI ? (nblk - warp * BPI + NW * BPI - 1) / (NW * BPI) : 0;
+    const int ni = nk == 0 ? 0 : (nk - 1) * BPI + min(BPI, nblk - (int)local_block((nk - 1) * BPI));
 
     if (threadIdx.x < 2 * NW * ST) mbar_init(&bars[threadIdx.x], 1);
     fence_mbar_init();
     __syncthreads();
 
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]
-    int* wphys = reinterpret_cast<int*>(smem + S::PHYS) + warp * ST;
-    float2* wscale = reinterpret_cast<float2*>(smem + S::SCALE) + warp * ST;
-    const uint32_t wstage = smem_addr(smem) + (uint32_t)(warp * ST) * 2 * TILE;
+    const uint32_t wstage = smem_addr(smem) + (uint32_t)(warp * ST) * S::STAGE;
     const uint64_t policy = l2_evict_first_policy();
 
-    struct Entry {
-        int phys;
-        float ks, vs;
+    struct Blocks {
+        int phys[BPI];
     };
-    // Every lane: this warp's k-th block and its scales, for k = 0, 1, 2, ... in order (each once).
-    auto entry = [&](int k) -> Entry {
-        if ((k & 31) == 0 && k > 0) {
-            const int c = k >> 5;
+    // Every lane: the blocks of iteration k (-1: none), for k = 0, 1, 2, ... in order (each once).
+    auto entries = [&](int k) -> Blocks {
+        const int i = k * BPI;
+        if ((i & 31) == 0 && i > 0) {
             t0 = t1;
             t1 = t2;
-            t2 = load_chunk(c + 2);
-            if (Q8) {
-                s0 = s1;
-                s1 = load_scales(mine(c + 1, t1));
-            }
+            t2 = load_chunk((i >> 5) + 2);
         }
-        Entry e;
-        e.phys = __shfl_sync(0xffffffffu, t0, k & 31);
-        e.ks = Q8 ? __shfl_sync(0xffffffffu, s0.x, k & 31) : 1.f;
-        e.vs = Q8 ? __shfl_sync(0xffffffffu, s0.y, k & 31) : 1.f;
+        Blocks e;
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) {
+            e.phys[u] = __shfl_sync(0xffffffffu, t0, (i & 31) + u);
+            const bool inside = (unsigned)e.phys[u] < (unsigned)a.num_blocks;
+            if (i + u < ni && !inside && lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
+            if (i + u >= ni || !inside) e.phys[u] = -1;
+        }
         return e;
     };
-    // lane 0: start the copy of the K (v = 0) or V (v = 1) tile of this warp's k-th block
-    auto issue = [&](int k, int v, const Entry& e) {
+    // lane 0: start the copies of the K (v = 0) or V (v = 1) tiles of iteration k; none: the phase
+    // completes with nothing copied
+    auto issue = [&](int k, int v, const Blocks& e) {
         const int st = k % ST;
-        const bool ok = (unsigned)e.phys < (unsigned)a.num_blocks;
         uint64_t* bar = &wbars[st * 2 + v];
-        if (v == 0) {
-            wphys[st] = ok ? e.phys : -1;
-            if (Q8) wscale[st] = make_float2(e.ks, e.vs);
-        }
-        if (ok) {
-            const int row0 = (int)(((long long)e.phys * a.n_kv + g) * kBlock);
-            const uint32_t dst = wstage + (uint32_t)st * 2 * TILE + (uint32_t)v * TILE;
-            mbar_arrive_expect_tx(bar, TILE);
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) bytes += e.phys[u] >= 0 ? TILE : 0u;
+        if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
+        else mbar_arrive(bar);
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) {
+            if (e.phys[u] < 0) continue;
+            const int row0 = (int)(((long long)e.phys[u] * a.n_kv + g) * kBlock);
+            const uint32_t dst = wstage + (uint32_t)st * S::STAGE + (uint32_t)(v * BPI + u) * TILE;
 #pragma unroll
             for (int pn = 0; pn < S::PANELS; ++pn)
                 tma_load_2d(dst + pn * S::PANEL, v ? &tm_v : &tm_k, pn * (Q8 ? S::PANB : S::PANB / 2), row0, bar, policy);
-        } else {
-            if (v == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
-            mbar_arrive(bar);  // completes the phase with nothing copied: the block is masked
         }
     };
-    // after a timed-out wait: wait (bounded) for the tiles of blocks [k0, k1) of kind v still in flight
+    // after a timed-out wait: wait (bounded) for the tiles of iterations [k0, k1) of kind v still in flight
     auto drain = [&](int k0, int k1, int v) {
         for (int kk = k0; kk < k1 && kk < nk; ++kk) mbar_wait_bounded(&wbars[(kk % ST) * 2 + v], (uint32_t)(kk / ST) & 1u);
     };
+    // Valid blocks of the iterations in the ring, as bits (iteration k: bits BPI (k % ST) ..).
+    unsigned ring = 0;
+    auto note = [&](int k, const Blocks& e) {
+        const int at = (k % ST) * BPI;
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) ring = (ring & ~(1u << (at + u))) | ((e.phys[u] >= 0 ? 1u : 0u) << (at + u));
+    };
+    static_assert(ST * BPI <= 16, "a ring's blocks fit the bits and one chunk of the table");
     for (int k = 0; k < ST && k < nk; ++k) {
-        const Entry e = entry(k);
+        const Blocks e = entries(k);
+        note(k, e);
         if (lane == 0) {
             issue(k, 0, e);
             issue(k, 1, e);
         }
     }
+    // Scales of the blocks of t0's chunk at the time, lane l: entry 32 c + l. They are consumed up to ST
+    // iterations behind the copies, so their chunk moves when the consumer enters it: t0 has entered it
+    // already (ST BPI <= 16 entries ago) and not left it.
+    float2 s0 = make_float2(1.f, 1.f), s1 = s0;
+    auto load_scales = [&](int c, int phys) -> float2 {
+        if (!Q8 || c * 32 + lane >= ni || (unsigned)phys >= (unsigned)a.num_blocks) return make_float2(0.f, 0.f);
+        const size_t i = (size_t)phys * a.n_kv + g;
+        return make_float2(__ldg(fa.k_scales + i), __ldg(fa.v_scales + i));
+    };
+    if (Q8) {
+        s0 = load_scales(0, t0);
+        s1 = load_scales(1, t1);
+    }
 
-    // Q^T fragments: k-step `ks` of row gid takes the four dims of one 32-bit (codes) or 64-bit word
-    // pair of the lane's K chunks; rows >= G are 0.
+    // Q^T fragments: k-step `ks` of row gid takes four dims of one of the lane's K chunks (one 32-bit
+    // word of codes, two words of halves); rows >= G are 0.
     uint32_t qb[KSTEPS][2];
     float zf[2];  // factor of the logits of query rows 2 tig, 2 tig + 1
     {
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
         }
     }
 
-    float acc[KSTEPS][4];  // m-tile mt: (dims dA, dA + 1 of dim_of(mt)) x (row 2tig | 2tig+1)
+    float acc[KSTEPS][4];  // m-tile mt: (dims dA, dA + 1) x (row 2tig | 2tig+1)
 #pragma unroll
     for (int mt = 0; mt < KSTEPS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY};  // of z
@@ -395,124 +416,189 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
     for (int k = 0; k < nk; ++k) {
         const int st = k % ST;
         const uint32_t par = (uint32_t)(k / ST) & 1u;
-        Entry next = {-1, 0.f, 0.f};
-        if (k + ST < nk) next = entry(k + ST);  // the block whose copies go next
+        const unsigned have = (ring >> (st * BPI)) & ((1u << BPI) - 1);
+        Blocks next;
+        if (k + ST < nk) {  // the blocks whose copies go next
+            next = entries(k + ST);
+            note(k + ST, next);
+        }
+        float2 sc2[BPI];
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) {
+            const int i = k * BPI + u;
+            if (Q8) {
+                if ((i & 31) == 0 && i > 0) {
+                    s0 = s1;
+                    s1 = load_scales((i >> 5) + 1, t1);
+                }
+                sc2[u] = make_float2(__shfl_sync(0xffffffffu, s0.x, i & 31), __shfl_sync(0xffffffffu, s0.y, i & 31));
+            } else {
+                sc2[u] = make_float2(1.f, 1.f);
+            }
+        }
         if (!mbar_wait_bounded(&wbars[st * 2], par)) {
             if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
-            drain(k, k + ST, 0);  // K tiles of blocks k .. k+ST-1 may be in flight
+            drain(k, k + ST, 0);  // K tiles of iterations k .. k+ST-1 may be in flight
             drain(k, k + ST, 1);  // and their V tiles
             break;
         }
-        const int jb = (b0 + warp + k * NW) * kBlock;
-        const int live = min(kBlock, ctx - jb);
-        const int nvalid = wphys[st] >= 0 ? live : 0;
-        const float2 sc2 = Q8 ? wscale[st] : make_float2(1.f, 1.f);
-        const uint32_t sK = wstage + (uint32_t)st * 2 * TILE;
-        const uint32_t sV = sK + TILE;
-        uint32_t b0f = 0u, b1f = 0u;
-        if (nvalid > 0) {
-            // ---- S = K Q^T (16 tokens x 8 rows), fp32; two chains hide the instruction's latency ----
-            float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        const int jb = (b0 + (int)local_block(k * BPI)) * kBlock;
+        const uint32_t sK = wstage + (uint32_t)st * S::STAGE;
+        const uint32_t sV = sK + BPI * TILE;
+        int nvalid[BPI];
 #pragma unroll
-            for (int i = 0; i < S::KCH; ++i) {
-                const int c = S::k_chunk(tig, i);
-                const uint4 lo = lds128(sK + S::at(gid, c)), hi = lds128(sK + S::at(gid + 8, c));
-                const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-                if constexpr (Q8) {
+        for (int u = 0; u < BPI; ++u) nvalid[u] = (have >> u) & 1 ? min(kBlock, ctx - jb - u * kBlock) : 0;
+        uint32_t b0f[BPI], b1f[BPI];
+        if (have) {
+            // ---- S = K Q^T (16 tokens x 8 rows a block), fp32; two chains hide the instruction's latency ----
+            float z[BPI][4];  // tokens gid (0, 1) and gid + 8 (2, 3) x rows 2tig, 2tig+1
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t af[4] = {e4m3x2_to_half2(wl[w]), e4m3x2_to_half2(wh[w]),
-                                                e4m3x2_to_half2(wl[w] >> 16), e4m3x2_to_half2(wh[w] >> 16)};
-                        M::mma((w & 1) ? sb : sa, af, qb[i * 4 + w][0], qb[i * 4 + w][1]);
-                    }
-                } else {
+            for (int u = 0; u < BPI; ++u) {
+                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t af[4] = {wl[2 * u], wh[2 * u], wl[2 * u + 1], wh[2 * u + 1]};
-                        M::mma(u ? sb : sa, af, qb[i * 2 + u][0], qb[i * 2 + u][1]);
+                for (int i = 0; i < S::KCH; ++i) {
+                    const int c = S::k_chunk(tig, i);
+                    const uint32_t tile = sK + u * TILE;
+                    const uint4 lo = lds128(tile + S::at(gid, c)), hi = lds128(tile + S::at(gid + 8, c));
+                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+                    if constexpr (Q8) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t af[4] = {e4m3x2_to_half2(wl[w]), e4m3x2_to_half2(wh[w]),
+                                                    e4m3x2_to_half2(wl[w] >> 16), e4m3x2_to_half2(wh[w] >> 16)};
+                            M::mma((w & 1) ? sb : sa, af, qb[i * 4 + w][0], qb[i * 4 + w][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const uint32_t af[4] = {wl[2 * w], wh[2 * w], wl[2 * w + 1], wh[2 * w + 1]};
+                            M::mma(w ? sb : sa, af, qb[i * 2 + w][0], qb[i * 2 + w][1]);
+                        }
                     }
                 }
+                const bool v0 = gid < nvalid[u], v1 = gid + 8 < nvalid[u];
+                const float f0 = zf[0] * sc2[u].x, f1 = zf[1] * sc2[u].x;
+                z[u][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
+                z[u][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
+                z[u][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
+                z[u][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
             }
-            // ---- online softmax: lane holds tokens gid, gid+8 of rows 2tig, 2tig+1 ----
-            const bool v0 = gid < nvalid, v1 = gid + 8 < nvalid;
-            const float f0 = zf[0] * sc2.x, f1 = zf[1] * sc2.x;
-            const float z0 = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;  // token gid,   row 2tig
-            const float z1 = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;  // token gid,   row 2tig+1
-            const float z2 = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;  // token gid+8, row 2tig
-            const float z3 = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;  // token gid+8, row 2tig+1
+            // ---- online softmax ----
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+            float ev[BPI], mo0 = m_out[0], mo1 = m_out[1];
+            if constexpr (Q8) {
+                // the largest z + log2 S_V of the iteration needs each block's own maximum
+#pragma unroll
+                for (int u = 0; u < BPI; ++u) {
+                    float a0 = fmaxf(z[u][0], z[u][2]), a1 = fmaxf(z[u][1], z[u][3]);
+                    mx0 = fmaxf(mx0, a0);
+                    mx1 = fmaxf(mx1, a1);
+                    ev[u] = nvalid[u] > 0 ? __log2f(sc2[u].y) : 0.f;  // of a power of two; -inf for 0
+                    mo0 = fmaxf(mo0, a0 + ev[u]);
+                    mo1 = fmaxf(mo1, a1 + ev[u]);
+                }
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                    mo0 = fmaxf(mo0, __shfl_xor_sync(0xffffffffu, mo0, o));
+                    mo1 = fmaxf(mo1, __shfl_xor_sync(0xffffffffu, mo1, o));
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < BPI; ++u) {
+                    mx0 = fmaxf(mx0, fmaxf(z[u][0], z[u][2]));
+                    mx1 = fmaxf(mx1, fmaxf(z[u][1], z[u][3]));
+                }
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                }
+            }
             if (zrow != nullptr && 2 * tig < G) {
-                float* zt = zrow + (size_t)(jb + gid) * G + 2 * tig;
-                if constexpr (G == 1) {
-                    if (v0) zt[0] = z0;
-                    if (v1) zt[8] = z2;
-                } else {
-                    if (v0) *reinterpret_cast<float2*>(zt) = make_float2(z0, z1);
-                    if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(z2, z3);
+#pragma unroll
+                for (int u = 0; u < BPI; ++u) {
+                    float* zt = zrow + (size_t)(jb + u * kBlock + gid) * G + 2 * tig;
+                    const bool v0 = jb + u * kBlock + gid < ctx, v1 = jb + u * kBlock + gid + 8 < ctx;
+                    if constexpr (G == 1) {
+                        if (v0) zt[0] = z[u][0];
+                        if (v1) zt[8] = z[u][2];
+                    } else {
+                        if (v0) *reinterpret_cast<float2*>(zt) = make_float2(z[u][0], z[u][1]);
+                        if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(z[u][2], z[u][3]);
+                    }
                 }
             }
-            float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-            }
+            // A maximum of -inf (nothing but -inf or NaN logits so far) stands for 0: 2^(-inf - 0) is 0.
             const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
-            float al0 = (m_run[0] == -INFINITY) ? 0.f : exp2f(m_run[0] - mn0);
-            float al1 = (m_run[1] == -INFINITY) ? 0.f : exp2f(m_run[1] - mn1);
+            const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;
+            float al0 = ex2(m_run[0] - ms0), al1 = ex2(m_run[1] - ms1);
             m_run[0] = mn0;
             m_run[1] = mn1;
-            const float p0 = (z0 == -INFINITY) ? 0.f : exp2f(z0 - mn0);
-            const float p1 = (z1 == -INFINITY) ? 0.f : exp2f(z1 - mn1);
-            const float p2 = (z2 == -INFINITY) ? 0.f : exp2f(z2 - mn0);
-            const float p3 = (z3 == -INFINITY) ? 0.f : exp2f(z3 - mn1);
-            uint32_t pa, pb;  // tokens gid, gid + 8: rows 2tig, 2tig+1
-            // the sum is of the weights before rounding: the scores divide by it in fp32
-            l_run[0] = l_run[0] * al0 + (p0 + p2);
-            l_run[1] = l_run[1] * al1 + (p1 + p3);
+            float sum0 = 0.f, sum1 = 0.f;
+            float c0 = 0.f, c1 = 0.f, be0 = 1.f, be1 = 1.f;
             if constexpr (Q8) {
-                const float ev = log2f(sc2.y);  // exact for the power of two that the scale is; -inf for 0
-                const float o0 = fmaxf(m_out[0], mx0 + ev), o1 = fmaxf(m_out[1], mx1 + ev);
-                al0 = (m_out[0] == -INFINITY) ? 0.f : exp2f(m_out[0] - o0);
-                al1 = (m_out[1] == -INFINITY) ? 0.f : exp2f(m_out[1] - o1);
-                m_out[0] = o0;
-                m_out[1] = o1;
-                const float c0 = o0 == -INFINITY ? -INFINITY : ev + (kWeightExp - o0);
-                const float c1 = o1 == -INFINITY ? -INFINITY : ev + (kWeightExp - o1);
-                pa = M::pack(z0 == -INFINITY ? 0.f : exp2f(z0 + c0), z1 == -INFINITY ? 0.f : exp2f(z1 + c1));
-                pb = M::pack(z2 == -INFINITY ? 0.f : exp2f(z2 + c0), z3 == -INFINITY ? 0.f : exp2f(z3 + c1));
+                const float os0 = mo0 == -INFINITY ? 0.f : mo0, os1 = mo1 == -INFINITY ? 0.f : mo1;
+                be0 = ex2(m_out[0] - os0);
+                be1 = ex2(m_out[1] - os1);
+                m_out[0] = mo0;
+                m_out[1] = mo1;
+                c0 = kWeightExp - os0;
+                c1 = kWeightExp - os1;
             } else {
-                pa = M::pack(p0, p1);
-                pb = M::pack(p2, p3);
+                be0 = al0;
+                be1 = al1;
             }
-            b0f = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
-            b1f = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
-            if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) {
+                // the sum is of the weights before rounding: the scores divide by it in fp32
+                const float p0 = ex2(z[u][0] - ms0), p1 = ex2(z[u][1] - ms1), p2 = ex2(z[u][2] - ms0), p3 = ex2(z[u][3] - ms1);
+                sum0 += p0 + p2;
+                sum1 += p1 + p3;
+                uint32_t pa, pb;  // tokens gid, gid + 8: rows 2tig, 2tig+1
+                if constexpr (Q8) {
+                    const float e0 = ev[u] + c0, e1 = ev[u] + c1;
+                    pa = M::pack(ex2(z[u][0] + e0), ex2(z[u][1] + e1));
+                    pb = M::pack(ex2(z[u][2] + e0), ex2(z[u][3] + e1));
+                } else {
+                    pa = M::pack(p0, p1);
+                    pb = M::pack(p2, p3);
+                }
+                b0f[u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
+                b1f[u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
+            }
+            l_run[0] = fmaf(l_run[0], al0, sum0);
+            l_run[1] = fmaf(l_run[1], al1, sum1);
+            if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {
 #pragma unroll
                 for (int mt = 0; mt < KSTEPS; ++mt) {
-                    acc[mt][0] *= al0;
-                    acc[mt][1] *= al1;
-                    acc[mt][2] *= al0;
-                    acc[mt][3] *= al1;
+                    acc[mt][0] *= be0;
+                    acc[mt][1] *= be1;
+                    acc[mt][2] *= be0;
+                    acc[mt][3] *= be1;
                 }
             }
-        } else if (zrow != nullptr && 2 * tig < G) {  // a block outside the pool: its positions weigh nothing
-            for (int r = gid; r < live; r += 8)
-                for (int x = 2 * tig; x < min(G, 2 * tig + 2); ++x) zrow[(size_t)(jb + r) * G + x] = -INFINITY;
+        } else if (zrow != nullptr) {  // blocks outside the pool: their positions weigh nothing
+            for (int x = lane; x < BPI * kBlock * G; x += 32)
+                if (jb + x / G < ctx) zrow[(size_t)jb * G + x] = -INFINITY;
         }
-        __syncwarp();  // the K tile has been read by every lane
+        __syncwarp();  // the K tiles have been read by every lane
         if (lane == 0 && k + ST < nk) {
             fence_proxy_async_smem();
             issue(k + ST, 0, next);
         }
         if (!mbar_wait_bounded(&wbars[st * 2 + 1], par)) {
             if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
-            drain(k + 1, k + ST + 1, 0);  // K tiles of blocks k+1 .. k+ST may be in flight
-            drain(k, k + ST, 1);          // V tiles of blocks k .. k+ST-1
+            drain(k + 1, k + ST + 1, 0);  // K tiles of iterations k+1 .. k+ST may be in flight
+            drain(k, k + ST, 1);          // V tiles of iterations k .. k+ST-1
             break;
         }
-        if (nvalid > 0) {
-            // ---- O^T += V^T P^T: this lane's tokens are 2tig, 2tig+1, 2tig+8, 2tig+9 ----
-            const bool keep[4] = {2 * tig < nvalid, 2 * tig + 1 < nvalid, 2 * tig + 8 < nvalid, 2 * tig + 9 < nvalid};
+        // ---- O^T += V^T P^T: this lane's tokens are 2tig, 2tig+1, 2tig+8, 2tig+9 ----
+#pragma unroll
+        for (int u = 0; u < BPI; ++u) {
+            if (nvalid[u] <= 0) continue;
+            const uint32_t tile = sV + u * TILE;
 #pragma unroll
             for (int pn = 0; pn < S::PANELS; ++pn) {
                 constexpr int WORDS = S::PANB / 32;  // 32-bit words of a row and panel per lane
@@ -521,22 +607,23 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
                 for (int j = 0; j < 4; ++j) {
                     const int tok = 2 * tig + (j & 1) + 8 * (j >> 1);
                     if constexpr (WORDS == 4) {
-                        const uint4 u = lds128(sV + S::at(tok, pn * 8 + gid));
-                        w[j][0] = u.x;
-                        w[j][1] = u.y;
-                        w[j][2] = u.z;
-                        w[j][3] = u.w;
+                        const uint4 x = lds128(tile + S::at(tok, pn * 8 + gid));
+                        w[j][0] = x.x;
+                        w[j][1] = x.y;
+                        w[j][2] = x.z;
+                        w[j][3] = x.w;
                     } else {
-                        const uint2 u = lds64(sV + S::at(tok, gid >> 1) + (gid & 1) * 8);
-                        w[j][0] = u.x;
-                        w[j][1] = u.y;
+                        const uint2 x = lds64(tile + S::at(tok, gid >> 1) + (gid & 1) * 8);
+                        w[j][0] = x.x;
+                        w[j][1] = x.y;
                     }
                 }
-                if (nvalid < kBlock) {
+                if (nvalid[u] < kBlock) {  // rows past the context may hold anything
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int x = 0; x < WORDS; ++x) w[j][x] = keep[j] ? w[j][x] : 0u;
+                        for (int x = 0; x < WORDS; ++x)
+                            w[j][x] = 2 * tig + (j & 1) + 8 * (j >> 1) < nvalid[u] ? w[j][x] : 0u;
                 }
 #pragma unroll
                 for (int x = 0; x < WORDS; ++x) {
@@ -548,17 +635,17 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
                             const uint32_t x23 = __byte_perm(w[2][x], w[3][x], sel);
                             const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
                                                     e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
-                            M::mma(acc[(pn * WORDS + x) * 2 + h], af, b0f, b1f);
+                            M::mma(acc[(pn * WORDS + x) * 2 + h], af, b0f[u], b1f[u]);
                         }
                     } else {
                         const uint32_t af[4] = {__byte_perm(w[0][x], w[1][x], 0x5410u), __byte_perm(w[0][x], w[1][x], 0x7632u),
                                                 __byte_perm(w[2][x], w[3][x], 0x5410u), __byte_perm(w[2][x], w[3][x], 0x7632u)};
-                        M::mma(acc[pn * WORDS + x], af, b0f, b1f);
+                        M::mma(acc[pn * WORDS + x], af, b0f[u], b1f[u]);
                     }
                 }
             }
         }
-        __syncwarp();  // the V tile has been read by every lane
+        __syncwarp();  // the V tiles have been read by every lane
         if (lane == 0 && k + ST < nk) {
             fence_proxy_async_smem();
             issue(k + ST, 1, next);
@@ -634,21 +721,23 @@ __global__ void __launch_bounds__(NW * 32) frag_decode_kernel(const FragArgs fa,
 template <typename T, bool Q8, int D, int G>
 struct FragKernel {
     static constexpr int NW = 4;
-    // 64 KiB of tiles per CTA: 3 CTAs per SM
-    static constexpr int ST = 64 * 1024 / (NW * 2 * kBlock * D * (Q8 ? 1 : 2));
-    static constexpr size_t smem = FragGeom<Q8, D, NW, ST>::ALLOC;
+    static constexpr int BPI = Q8 ? 2 : 1;
+    static constexpr int CTAS = 3;
+    // 64 KiB of tiles per CTA
+    static constexpr int ST = 64 * 1024 / (NW * 2 * BPI * kBlock * D * (Q8 ? 1 : 2));
+    static constexpr size_t smem = FragGeom<Q8, D, NW, ST, BPI>::ALLOC;
     static unsigned long long attr_done;
-    static cudaError_t prepare() { return allow_dynamic_smem(frag_decode_kernel<T, Q8, D, G, NW, ST>, smem, &attr_done); }
+    static constexpr auto kernel = frag_decode_kernel<T, Q8, D, G, NW, ST, BPI, CTAS>;
+    static cudaError_t prepare() { return allow_dynamic_smem(kernel, smem, &attr_done); }
     static cudaError_t ctas_per_sm(int* out) {
         cudaError_t err = prepare();
         if (err != cudaSuccess) return err;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, frag_decode_kernel<T, Q8, D, G, NW, ST>, NW * 32, smem);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kernel, NW * 32, smem);
     }
     static cudaError_t launch(const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
         cudaError_t err = prepare();
         if (err != cudaSuccess) return err;
-        frag_decode_kernel<T, Q8, D, G, NW, ST>
-            <<<dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs), NW * 32, smem, stream>>>(a, tk, tv);
+        kernel<<<dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs), NW * 32, smem, stream>>>(a, tk, tv);
         return cudaGetLastError();
     }
 };
