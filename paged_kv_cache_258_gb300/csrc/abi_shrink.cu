@@ -51,15 +51,34 @@ int validate16(const pkv_cache_desc* d) {
     return d->dtype == PKV_F32 ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
-// Partition geometry of the fragment kernel: the rule of the other decode calls with this kernel's
-// CTAs per SM (read once per device and kernel by the CUDA runtime's occupancy calculator).
-cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, int* bpp, int* n_parts) {
+// Partition geometry of the fragment kernel. pairs = (sequence, KV head) pairs, slots = CTAs the GPU
+// holds at once.
+//  * pairs < slots / 2: one wave. A context is cut into slots / pairs partitions, but none shorter than
+//    kMinPart blocks (one iteration of each of a CTA's warps).
+//  * otherwise kMaxBpp blocks a partition: several CTAs a slot, short enough to even out ragged lengths.
+// When the whole grid is at most one CTA per SM and a context has at most kMaxCluster partitions, these
+// form a cluster and are joined through shared memory.
+constexpr int kMinPart = 8, kMaxCluster = 8;
+
+struct FragGeometry {
+    int bpp, n_parts, cluster;
+};
+
+cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, FragGeometry* out) {
     int sms = 0, per_sm = 0;
     cudaError_t err = pkv::current_sm_count(&sms);
     if (err == cudaSuccess) err = pkv::frag_ctas_per_sm(d->dtype, q8, d->head_dim, group_of(d), &per_sm);
     if (err != cudaSuccess) return err;
-    *bpp = pkv::decode_blocks_per_partition(n_seqs, d->n_kv_heads, max_blocks, sms, per_sm, pkv::kMaxBppStreamed);
-    *n_parts = pkv::decode_partitions(max_blocks, *bpp);
+    const long long pairs = (long long)n_seqs * d->n_kv_heads, slots = (long long)sms * per_sm;
+    int bpp = pkv::kMaxBpp;
+    if (2 * pairs < slots) {
+        const long long parts = slots / pairs;
+        bpp = (int)((max_blocks + parts - 1) / parts);
+        if (bpp < kMinPart) bpp = kMinPart;
+    }
+    out->bpp = bpp;
+    out->n_parts = pkv::decode_partitions(max_blocks, bpp);
+    out->cluster = out->n_parts <= kMaxCluster && pairs * out->n_parts <= sms ? out->n_parts : 1;
     return cudaSuccess;
 }
 
@@ -69,25 +88,27 @@ struct FragLayout {
 
 // Partial outputs, counters: split contexts only. (max, sum) pairs: those, or summed weights. Logits:
 // summed weights.
-FragLayout frag_layout(const pkv_cache_desc* d, int n_seqs, int max_blocks, int n_parts, bool scored) {
+FragLayout frag_layout(const pkv_cache_desc* d, int n_seqs, int max_blocks, const FragGeometry& geo, bool scored) {
     auto up = [](size_t x) { return (x + 15) / 16 * 16; };
     const size_t rows = (size_t)n_seqs * d->n_q_heads;
+    const int n_parts = geo.n_parts;
+    const bool split = n_parts > 1 && geo.cluster == 1;
     FragLayout l{};
-    l.ml = n_parts > 1 ? up(rows * n_parts * d->head_dim * sizeof(float)) : 0;
-    l.cnt = l.ml + (n_parts > 1 || scored ? up(rows * n_parts * 2 * sizeof(float)) : 0);
-    l.z = l.cnt + (n_parts > 1 ? up((size_t)n_seqs * d->n_kv_heads * sizeof(unsigned long long)) : 0);
+    l.ml = split ? up(rows * n_parts * d->head_dim * sizeof(float)) : 0;
+    l.cnt = l.ml + (split || scored ? up(rows * n_parts * 2 * sizeof(float)) : 0);
+    l.z = l.cnt + (split ? up((size_t)n_seqs * d->n_kv_heads * sizeof(unsigned long long)) : 0);
     l.bytes = l.z + (scored ? up(rows * max_blocks * pkv::kBlock * sizeof(float)) : 0);
     return l;
 }
 
 size_t frag_workspace(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, bool scored) {
     if (validate16(d) != PKV_OK || n_seqs <= 0 || max_blocks <= 0) return 0;
-    int bpp = 0, n_parts = 0;
-    if (frag_geometry(d, q8, n_seqs, max_blocks, &bpp, &n_parts) != cudaSuccess) {
+    FragGeometry geo;
+    if (frag_geometry(d, q8, n_seqs, max_blocks, &geo) != cudaSuccess) {
         cudaGetLastError();  // no usable device: report nothing rather than a guess
         return 0;
     }
-    return frag_layout(d, n_seqs, max_blocks, n_parts, scored).bytes;
+    return frag_layout(d, n_seqs, max_blocks, geo, scored).bytes;
 }
 
 // Shared body of decode over 8-bit pools (q8) and of decode with summed weights (scores).
@@ -106,9 +127,10 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID_ARG;
     if (scores && (!aligned4(scores) || score_stride < (int64_t)max_blocks * pkv::kBlock)) return PKV_ERR_INVALID_ARG;
     if (pool_rows(d) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;  // tensor-copy rows are 32-bit
-    int bpp = 0, n_parts = 0;
-    if (frag_geometry(d, q8, n_seqs, max_blocks, &bpp, &n_parts) != cudaSuccess) return PKV_ERR_CUDA;
-    const FragLayout l = frag_layout(d, n_seqs, max_blocks, n_parts, scores != nullptr);
+    FragGeometry geo;
+    if (frag_geometry(d, q8, n_seqs, max_blocks, &geo) != cudaSuccess) return PKV_ERR_CUDA;
+    const FragLayout l = frag_layout(d, n_seqs, max_blocks, geo, scores != nullptr);
+    const bool split = geo.n_parts > 1 && geo.cluster == 1;
     if (l.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < l.bytes)) return PKV_ERR_INVALID_ARG;
 
     pkv::FragArgs a;
@@ -120,17 +142,18 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     a.d.tables = tables;
     a.d.lens = lens;
     a.d.out = out;
-    a.d.part_o = n_parts > 1 ? reinterpret_cast<float*>(ws) : nullptr;
-    a.d.part_ml = n_parts > 1 || scores ? reinterpret_cast<float*>(ws + l.ml) : nullptr;
-    a.d.counters = n_parts > 1 ? reinterpret_cast<unsigned long long*>(ws + l.cnt) : nullptr;
+    a.d.part_o = split ? reinterpret_cast<float*>(ws) : nullptr;
+    a.d.part_ml = split || scores ? reinterpret_cast<float*>(ws + l.ml) : nullptr;
+    a.d.counters = split ? reinterpret_cast<unsigned long long*>(ws + l.cnt) : nullptr;
     a.d.call_tag = pkv::next_call_tag();
     a.d.n_seqs = n_seqs;
     a.d.n_q = d->n_q_heads;
     a.d.n_kv = d->n_kv_heads;
     a.d.num_blocks = d->num_blocks;
     a.d.max_blocks = max_blocks;
-    a.d.n_parts = n_parts;
-    a.d.bpp = bpp;
+    a.d.n_parts = geo.n_parts;
+    a.d.bpp = geo.bpp;
+    a.cluster = geo.cluster;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     if (q8) {
         a.k_scales = k_scales + layer_scales(d) * layer;
@@ -152,8 +175,8 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
         s.n_kv = d->n_kv_heads;
         s.group = group_of(d);
         s.max_blocks = max_blocks;
-        s.n_parts = n_parts;
-        s.bpp = bpp;
+        s.n_parts = geo.n_parts;
+        s.bpp = geo.bpp;
         if (pkv::launch_scores(s, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
         pkv::count_launches(1);
     }

@@ -64,7 +64,8 @@ struct FragGeom {
     static constexpr size_t TOTAL = ML + (size_t)NW * 8 * 2 * 4;
     static constexpr size_t ALLOC = TOTAL + 1024;             // room to align the base
     static constexpr size_t MERGE = (size_t)NW * 8 * D * 4;  // merge scratch, after the combine buffer
-    static_assert(MERGE + MergeScratch<8>::BYTES <= STAGES, "combine buffer and merge scratch must fit");
+    static_assert(MERGE + MergeScratch<8>::BYTES <= STAGES && MERGE + 8 * (D + 2) * 4 <= STAGES,
+                  "combine buffer and merge scratch must fit");
     // byte of 16-byte chunk `c` of row `r`: the copy's swizzle XORs the chunk with the 128-byte line's
     // number modulo the pattern (8 rows of 128 bytes, or 4 lines of two 64-byte rows)
     __device__ __forceinline__ static uint32_t at(int r, int c) {
@@ -215,6 +216,58 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     if (threadIdx.x == 0) *cnt = 0ull;
 }
 
+// The same join for a cluster of the sequence's partitions, through the CTAs' shared memory: no trip to
+// L2 for the partials and none for a counter. Every CTA p < np has its (max, sum) pairs in ml [G][2] and
+// its partial outputs in po [G * D], and writes every np-th piece of the output.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t a) {
+    float r;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
+    return r;
+}
+// All threads of the cluster's CTAs that have not left (CTAs past the context leave at once and count
+// as arrived).
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+constexpr int kMaxCluster = 8;  // the portable limit
+
+template <typename T, int D, int G, int NT>
+__device__ __forceinline__ void cluster_merge(T* out, int p, int np, const float* ml, const float* po) {
+    cluster_barrier();
+    const uint32_t ml0 = smem_addr(ml), po0 = smem_addr(po);
+    for (int idx = p * NT + threadIdx.x; idx < G * D; idx += np * NT) {
+        const int r = idx / D;
+        float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q < np) {
+                m[q] = cluster_load(cluster_addr(ml0 + (2 * r) * 4, q));
+                l[q] = cluster_load(cluster_addr(ml0 + (2 * r + 1) * 4, q));
+                o[q] = cluster_load(cluster_addr(po0 + idx * 4, q));
+            }
+        }
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+            if (q < np) M = fmaxf(M, m[q]);
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q < np) {
+                const float w = m[q] == -INFINITY ? 0.f : ex2(m[q] - M);
+                L = fmaf(l[q], w, L);
+                O = fmaf(o[q], w, O);
+            }
+        }
+        out[idx] = from_float<T>(L == 0.f ? 0.f : O / L);
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+}
+
 template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS>
 __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragArgs fa,
                                                                     const __grid_constant__ CUtensorMap tm_k,
@@ -241,7 +294,15 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     const int p = blockIdx.x;
     const int g = blockIdx.y;
     const int s = blockIdx.z;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+    if (threadIdx.x < 2 * NW * ST) mbar_init(&bars[threadIdx.x], 1);
+    fence_mbar_init();
+    __syncthreads();
+    grid_dependency_wait();  // nothing in global memory has been touched so far
 
     // This warp's i-th block (i = BPI k + u) is block BPI (warp + k NW) + u of the partition. Table
     // entries come in chunks of 32 held in registers (lane l: entry 32 c + l): the chunk whose copies
@@ -274,10 +335,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     // iterations of this warp, and its blocks (the last iteration may have one less than BPI)
     const int nk = nblk > warp * BPI ? (nblk - warp * BPI + NW * BPI - 1) / (NW * BPI) : 0;
     const int ni = nk == 0 ? 0 : (nk - 1) * BPI + min(BPI, nblk - (int)local_block((nk - 1) * BPI));
-
-    if (threadIdx.x < 2 * NW * ST) mbar_init(&bars[threadIdx.x], 1);
-    fence_mbar_init();
-    __syncthreads();
 
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]
     const uint32_t wstage = smem_addr(smem) + (uint32_t)(warp * ST) * S::STAGE;
@@ -687,6 +744,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         s_ml[(warp * 8 + r0 + 1) * 2 + 1] = l_run[1];
     }
     __syncthreads();
+    float* s_po = reinterpret_cast<float*>(smem + S::MERGE);  // [G][D], then [G][2]: a cluster's partials
+    float* s_pml = s_po + G * D;
     for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
         const int r = idx / D;
         const int d = idx % D;
@@ -704,16 +763,26 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         }
         const size_t row = (size_t)s * a.n_q + (size_t)g * G + r;
         if (single) reinterpret_cast<T*>(a.out)[row * D + d] = from_float<T>(L == 0.f ? 0.f : O / L);
-        if (!single || fa.z) {
+        if (!single && fa.cluster > 1) {
+            s_po[idx] = O;
+            if (d == 0) {
+                s_pml[2 * r] = Mx;
+                s_pml[2 * r + 1] = L;
+            }
+        }
+        if ((!single && fa.cluster == 1) || fa.z) {
             const size_t prow = row * a.n_parts + p;
-            if (!single) a.part_o[prow * D + d] = O;
+            if (!single && fa.cluster == 1) a.part_o[prow * D + d] = O;
             if (d == 0) {
                 a.part_ml[prow * 2] = Mx;
                 a.part_ml[prow * 2 + 1] = L;
             }
         }
     }
-    if (!single)
+    if (!single && fa.cluster > 1)
+        cluster_merge<T, D, G, NW * 32>(reinterpret_cast<T*>(a.out) + ((size_t)s * a.n_q + (size_t)g * G) * D, p,
+                                        (nb + a.bpp - 1) / a.bpp, s_pml, s_po);
+    else if (!single)
         frag_merge_if_last<T, D, G, NW * 32>(a, s, g, (nb + a.bpp - 1) / a.bpp,
                                              reinterpret_cast<float*>(smem + S::MERGE));
 }
@@ -727,22 +796,36 @@ struct FragKernel {
     static constexpr int ST = 64 * 1024 / (NW * 2 * BPI * kBlock * D * (Q8 ? 1 : 2));
     static constexpr size_t smem = FragGeom<Q8, D, NW, ST, BPI>::ALLOC;
     static unsigned long long attr_done;
+    static int resident[64];
     static constexpr auto kernel = frag_decode_kernel<T, Q8, D, G, NW, ST, BPI, CTAS>;
     static cudaError_t prepare() { return allow_dynamic_smem(kernel, smem, &attr_done); }
+    // CTAs one SM of the current device holds at once; asked of the occupancy calculator once per device
     static cudaError_t ctas_per_sm(int* out) {
-        cudaError_t err = prepare();
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
         if (err != cudaSuccess) return err;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kernel, NW * 32, smem);
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        int n = __atomic_load_n(&resident[dev], __ATOMIC_RELAXED);
+        if (n == 0) {
+            err = prepare();
+            if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NW * 32, smem);
+            if (err != cudaSuccess) return err;
+            if (n <= 0) return cudaErrorInvalidConfiguration;
+            __atomic_store_n(&resident[dev], n, __ATOMIC_RELAXED);
+        }
+        *out = n;
+        return cudaSuccess;
     }
     static cudaError_t launch(const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
         cudaError_t err = prepare();
         if (err != cudaSuccess) return err;
-        kernel<<<dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs), NW * 32, smem, stream>>>(a, tk, tv);
-        return cudaGetLastError();
+        return launch_dependent(kernel, dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs), NW * 32, smem, stream, a.cluster, a, tk, tv);
     }
 };
 template <typename T, bool Q8, int D, int G>
 unsigned long long FragKernel<T, Q8, D, G>::attr_done = 0;
+template <typename T, bool Q8, int D, int G>
+int FragKernel<T, Q8, D, G>::resident[64] = {};
 
 #define PKV_FRAG_CASES                                                  \
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)     \

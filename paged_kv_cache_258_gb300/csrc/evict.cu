@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const long long pair = blockIdx.x;  // s * n_kv + g
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
     const int cap = a.max_blocks * kBlock;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int c = a.lens[s], want = a.keep[s];
     if (c < 0 || c > cap || want < 0 || min(want, c) > a.max_keep) {
         if (threadIdx.x == 0 && g == 0 && layer == 0)
@@ -230,6 +232,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int slice = (int)(blockIdx.x % a.slices);
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
     const int cap = a.max_blocks * kBlock;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int c = a.lens[s], want = a.keep[s];
     if (c < 0 || c > cap || want < 0 || min(want, c) > a.max_keep) return;  // flagged by the selection
     const int k = min(want, c);
@@ -288,15 +292,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
     const unsigned pairs = (unsigned)a.n_seqs * (unsigned)a.n_kv;
-    evict_select_kernel<<<dim3(pairs, a.n_layers), kSelThreads, 0, stream>>>(a);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err = launch_dependent(evict_select_kernel, dim3(pairs, a.n_layers), kSelThreads, 0, stream, 1, a);
     if (err != cudaSuccess) return err;
     const dim3 grid(pairs * (unsigned)a.slices, a.n_layers, 2);
-    if (a.k_scales)
-        evict_move_kernel<true><<<grid, kMoveThreads, 0, stream>>>(a);
-    else
-        evict_move_kernel<false><<<grid, kMoveThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(a.k_scales ? evict_move_kernel<true> : evict_move_kernel<false>, grid, kMoveThreads, 0, stream, 1, a);
 }
 
 }  // namespace pkv

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8Ap
     const long long item = (long long)blockIdx.x * kAppendWarps + warp;
     const long long per_tok = 2LL * a.n_kv;
     if (item >= a.n_tok * per_tok) return;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int t = (int)(item / per_tok);
     const int rest = (int)(item % per_tok);
     const bool is_v = rest >= a.n_kv;
@@ -145,6 +147,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8Ap
 // grid (pair, layer, K/V): each CTA copies one block of one layer, codes and scales.
 __global__ void __launch_bounds__(256) q8_copy_kernel(const Q8CopyArgs a) {
     const int layer = blockIdx.y;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int src = a.pairs[2 * blockIdx.x];
     const int dst = a.pairs[2 * blockIdx.x + 1];
     if ((unsigned)src >= (unsigned)a.num_blocks || (unsigned)dst >= (unsigned)a.num_blocks) {
@@ -199,6 +203,7 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.z;
     const int cap = a.max_blocks * kBlock;
+    grid_dependency_wait();
     const int ctx = a.lens[s];
     if (ctx <= 0 || ctx > cap) return;  // the attention launch flags such a sequence
     const int nb = (ctx + kBlock - 1) / kBlock;
@@ -241,14 +246,13 @@ cudaError_t append_of(int head_dim, const Q8AppendArgs& a, cudaStream_t stream) 
     const long long items = 2LL * a.n_tok * a.n_kv;
     const long long ctas = (items + kAppendWarps - 1) / kAppendWarps;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)ctas;
+    const dim3 grid((unsigned)ctas);
     switch (head_dim) {
-    case 64: q8_append_kernel<T, 64><<<grid, kAppendWarps * 32, 0, stream>>>(a); break;
-    case 128: q8_append_kernel<T, 128><<<grid, kAppendWarps * 32, 0, stream>>>(a); break;
-    case 256: q8_append_kernel<T, 256><<<grid, kAppendWarps * 32, 0, stream>>>(a); break;
+    case 64: return launch_dependent(q8_append_kernel<T, 64>, grid, kAppendWarps * 32, 0, stream, 1, a);
+    case 128: return launch_dependent(q8_append_kernel<T, 128>, grid, kAppendWarps * 32, 0, stream, 1, a);
+    case 256: return launch_dependent(q8_append_kernel<T, 256>, grid, kAppendWarps * 32, 0, stream, 1, a);
     default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 template <typename T>
@@ -257,12 +261,11 @@ cudaError_t widen_of(int head_dim, const Q8WidenArgs& a, cudaStream_t stream) {
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)ctas, 1, a.n_seqs);
     switch (head_dim) {
-    case 64: q8_widen_kernel<T, 64><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
-    case 128: q8_widen_kernel<T, 128><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
-    case 256: q8_widen_kernel<T, 256><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
+    case 64: return launch_dependent(q8_widen_kernel<T, 64>, grid, kWidenWarps * 32, 0, stream, 1, a);
+    case 128: return launch_dependent(q8_widen_kernel<T, 128>, grid, kWidenWarps * 32, 0, stream, 1, a);
+    case 256: return launch_dependent(q8_widen_kernel<T, 256>, grid, kWidenWarps * 32, 0, stream, 1, a);
     default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -272,8 +275,7 @@ cudaError_t launch_q8_append(int dtype, int head_dim, const Q8AppendArgs& a, cud
 }
 
 cudaError_t launch_q8_copy(const Q8CopyArgs& a, cudaStream_t stream) {
-    q8_copy_kernel<<<dim3(a.n_pairs, a.n_layers, 2), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(q8_copy_kernel, dim3(a.n_pairs, a.n_layers, 2), 256, 0, stream, 1, a);
 }
 
 cudaError_t launch_q8_widen(int dtype, int head_dim, const Q8WidenArgs& a, cudaStream_t stream) {

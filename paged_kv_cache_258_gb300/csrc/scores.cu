@@ -44,13 +44,14 @@ __global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a)
     __shared__ float s_m[8], s_inv[8];
     const int s = blockIdx.z, g = blockIdx.y;
     const int cap = a.max_blocks * kBlock;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int ctx = min(max(a.lens[s], 0), cap);
     const int j0 = blockIdx.x * kThreads * kPerThread;
     if (j0 >= ctx) return;
     const int nb = (ctx + kBlock - 1) / kBlock;
     const int np = (nb + a.bpp - 1) / a.bpp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dependency_wait();
     if (warp < G) {
         const size_t row = ((size_t)s * a.n_kv + g) * G + warp;
         const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.n_parts;
@@ -88,24 +89,14 @@ __global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a)
 
 cudaError_t launch_scores(const ScoreArgs& a, cudaStream_t stream) {
     constexpr int kChunk = kThreads * kPerThread;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)a.max_blocks * kBlock + kChunk - 1) / kChunk), a.n_kv, a.n_seqs);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t err;
+    const dim3 grid((unsigned)(((long long)a.max_blocks * kBlock + kChunk - 1) / kChunk), a.n_kv, a.n_seqs);
     switch (a.group) {
-    case 1: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<1>, a); break;
-    case 2: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<2>, a); break;
-    case 4: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<4>, a); break;
-    case 8: err = cudaLaunchKernelEx(&cfg, add_scores_kernel<8>, a); break;
+    case 1: return launch_dependent(add_scores_kernel<1>, grid, kThreads, 0, stream, 1, a);
+    case 2: return launch_dependent(add_scores_kernel<2>, grid, kThreads, 0, stream, 1, a);
+    case 4: return launch_dependent(add_scores_kernel<4>, grid, kThreads, 0, stream, 1, a);
+    case 8: return launch_dependent(add_scores_kernel<8>, grid, kThreads, 0, stream, 1, a);
     default: return cudaErrorInvalidValue;
     }
-    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace pkv

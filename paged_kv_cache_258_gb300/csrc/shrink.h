@@ -9,6 +9,11 @@ namespace pkv {
 // Tensor-map element code of an 8-bit pool (beside the pkv_dtype values kv_tensor_map takes).
 constexpr int kCodesE4M3 = 3;
 
+#ifdef __CUDACC__
+// Lets the next launch on the stream, if it is a programmatic dependent, be placed from here on.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // Least exponent of a block's scale: below it the scale of all-tiny rows stops shrinking, so that
 // code * scale (codes go down to 2^-9) stays a normal number of the rows' type (bf16: 2^-126) or a
 // multiple of its least step (fp16: 2^-24).
@@ -20,6 +25,7 @@ struct FragArgs {
     DecodeArgs d;
     const float* k_scales = nullptr;  // [num_blocks][n_kv] of this layer (8-bit pools)
     const float* v_scales = nullptr;
+    int cluster = 1;                  // CTAs of a cluster: n_parts where the partials are joined through shared memory
     float* z = nullptr;               // [n_seqs][n_kv][max_blocks*16][G] base-2 logits, or null: weights not summed
 };
 
@@ -90,6 +96,30 @@ struct EvictArgs {
     int row_bytes;         // one row of one head
     int slices;            // CTAs that share the columns of one (sequence, head)
 };
+
+// Launches `kernel` as a programmatic dependent of the kernel before it on the stream: its CTAs may be
+// placed while that one drains, and wait (griddepcontrol.wait) for its end before they touch anything
+// in global memory. So the order is that of an ordinary launch, without its start-up.
+// cluster > 1: thread-block clusters of that many CTAs along x.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                             const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
 
 cudaError_t frag_ctas_per_sm(int dtype, bool q8, int head_dim, int group, int* out);
 cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, const FragArgs& a, cudaStream_t stream);

@@ -555,22 +555,57 @@ def append_launcher(desc: CacheDesc, k, v, slot_mapping, k_pool, v_pool, stream=
 # scale_shape(desc); a code stands for code * scale of its block and KV head. desc.dtype is that of the
 # activations, "f16" or "bf16".
 
+class _Facts:
+    """What the checks of a call need of a descriptor, worked out once for each set of field values."""
+    __slots__ = ("dtype", "pool", "scales", "n_layers", "n_q", "n_kv", "d")
+
+    def __init__(self, desc: CacheDesc):
+        self.dtype = torch_dtype(desc.dtype_name) if desc.dtype in DTYPE_CODES.values() else None
+        self.pool, self.scales = pool_shape(desc), scale_shape(desc)
+        self.n_layers, self.n_q, self.n_kv, self.d = desc.n_layers, desc.n_q_heads, desc.n_kv_heads, desc.head_dim
+
+
+_facts_by_value: dict = {}
+
+
+def _facts(desc: CacheDesc) -> _Facts:
+    key = bytes(desc)
+    f = _facts_by_value.get(key)
+    if f is None:
+        if len(_facts_by_value) >= 256:
+            _facts_by_value.clear()
+        f = _facts_by_value[key] = _Facts(desc)
+    return f
+
+
+def _ptr(x, name, dtype, shape, cur) -> int:
+    """The address of a tensor that _dev accepts; where it does not, _dev's error."""
+    if x.dtype is dtype and x.shape == shape and x.get_device() == cur and x.is_contiguous():
+        return x.data_ptr()
+    return _dev(x, name, dtype, shape, cur=cur).value
+
+
+def _raw(stream, cur: int) -> int:
+    """The handle of `stream`, or of the current stream of the current device."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(cur) if cur >= 0 else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def scale_shape(desc: CacheDesc):
     """[n_layers, num_blocks, n_kv]: one scale for each block and KV head of an 8-bit pool."""
     return (desc.n_layers, desc.num_blocks, desc.n_kv_heads)
 
 
-def _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur):
-    t = _torch()
-    pool, sc = pool_shape(desc), scale_shape(desc)
-    return (_dev(k_codes, "k_codes", t.float8_e4m3fn, pool, cur=cur), _dev(v_codes, "v_codes", t.float8_e4m3fn, pool, cur=cur),
-            _dev(k_scales, "k_scales", t.float32, sc, cur=cur), _dev(v_scales, "v_scales", t.float32, sc, cur=cur))
+def _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur):
+    return (_ptr(k_codes, "k_codes", t.float8_e4m3fn, f.pool, cur), _ptr(v_codes, "v_codes", t.float8_e4m3fn, f.pool, cur),
+            _ptr(k_scales, "k_scales", t.float32, f.scales, cur), _ptr(v_scales, "v_scales", t.float32, f.scales, cur))
 
 
 def _workspace(workspace, cur):
     if workspace is None:
-        return ctypes.c_void_p(0), 0
-    return _dev(workspace, "workspace", cur=cur), workspace.numel() * workspace.element_size()
+        return None, 0
+    return _dev(workspace, "workspace", cur=cur).value, workspace.nbytes
 
 
 def _scores(scores, name, lead, max_blocks: int, cur):
@@ -579,7 +614,7 @@ def _scores(scores, name, lead, max_blocks: int, cur):
         raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, at least {max_blocks * BLOCK}], "
                          f"got {tuple(scores.shape)}")
     stride = int(scores.shape[-1])
-    return _dev(scores, name, _torch().float32, (*lead, stride), cur=cur), stride
+    return _ptr(scores, name, _torch().float32, (*lead, stride), cur), stride
 
 
 def _table_width(block_tables) -> int:
@@ -640,25 +675,22 @@ def alloc_evict_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int,
 def pkv_q8_append(desc: CacheDesc, layer: int, k, v, slot_mapping, k_codes, v_codes, k_scales, v_scales,
                   stream=None) -> None:
     """pkv_kv_append into 8-bit pools: rows k, v [n_tokens, n_kv, d] are rounded to codes."""
-    t = _torch()
-    dt = torch_dtype(desc.dtype_name)
-    cur = _current_device()
-    n_tok = int(k.shape[0])
-    row = (n_tok, desc.n_kv_heads, desc.head_dim)
-    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
-    rc = lib().pkv_q8_append(ctypes.byref(desc), int(layer), _dev(k, "k", dt, row, cur=cur), _dev(v, "v", dt, row, cur=cur),
-                             _dev(slot_mapping, "slot_mapping", t.int64, (n_tok,), cur=cur), n_tok, kc, vc, ks, vs,
-                             _stream_handle(stream))
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_tok = k.shape[0]
+    row = (n_tok, f.n_kv, f.d)
+    kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    rc = lib().pkv_q8_append(ctypes.byref(desc), int(layer), _ptr(k, "k", f.dtype, row, cur), _ptr(v, "v", f.dtype, row, cur),
+                             _ptr(slot_mapping, "slot_mapping", t.int64, (n_tok,), cur), n_tok, kc, vc, ks, vs,
+                             _raw(stream, cur))
     _check(rc, "pkv_q8_append")
 
 
 def pkv_q8_copy_blocks(desc: CacheDesc, k_codes, v_codes, k_scales, v_scales, pairs, stream=None) -> None:
-    t = _torch()
-    cur = _current_device()
-    n_pairs = int(pairs.shape[0])
-    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
-    rc = lib().pkv_q8_copy_blocks(ctypes.byref(desc), kc, vc, ks, vs, _dev(pairs, "pairs", t.int32, (n_pairs, 2), cur=cur),
-                                  n_pairs, _stream_handle(stream))
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_pairs = pairs.shape[0]
+    kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    rc = lib().pkv_q8_copy_blocks(ctypes.byref(desc), kc, vc, ks, vs, _ptr(pairs, "pairs", t.int32, (n_pairs, 2), cur),
+                                  n_pairs, _raw(stream, cur))
     _check(rc, "pkv_q8_copy_blocks")
 
 
@@ -666,19 +698,17 @@ def pkv_q8_decode_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k_
                             context_lens, scale: float, out, workspace=None, scores=None, stream=None) -> None:
     """pkv_paged_decode_attention over 8-bit pools; scores float32 [n_seqs, n_kv, S] gain each
     position's attention weight (workspace then from alloc_q8_workspace(..., scored=True))."""
-    t = _torch()
-    dt = torch_dtype(desc.dtype_name)
-    cur = _current_device()
-    n_seqs, max_blocks = int(q.shape[0]), _table_width(block_tables)
-    qshape = (n_seqs, desc.n_q_heads, desc.head_dim)
-    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
-    sp, stride = (None, 0) if scores is None else _scores(scores, "scores", (n_seqs, desc.n_kv_heads), max_blocks, cur)
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_seqs, max_blocks = q.shape[0], _table_width(block_tables)
+    qshape = (n_seqs, f.n_q, f.d)
+    kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    sp, stride = (None, 0) if scores is None else _scores(scores, "scores", (n_seqs, f.n_kv), max_blocks, cur)
     ws, ws_bytes = _workspace(workspace, cur)
     rc = lib().pkv_q8_decode_attention(
-        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur), kc, vc, ks, vs,
-        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
-        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur), n_seqs, float(scale),
-        _dev(out, "out", dt, qshape, cur=cur), sp, stride, ws, ws_bytes, _stream_handle(stream))
+        ctypes.byref(desc), int(layer), _ptr(q, "q", f.dtype, qshape, cur), kc, vc, ks, vs,
+        _ptr(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur), max_blocks,
+        _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur), n_seqs, scale,
+        _ptr(out, "out", f.dtype, qshape, cur), sp, stride, ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_q8_decode_attention")
 
 
@@ -686,19 +716,17 @@ def pkv_q8_prefill_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k
                              context_lens, query_start, max_query_len: int, scale: float, out, workspace,
                              stream=None) -> None:
     """pkv_paged_prefill_attention over 8-bit pools (workspace from alloc_q8_prefill_workspace)."""
-    t = _torch()
-    dt = torch_dtype(desc.dtype_name)
-    cur = _current_device()
-    n_tokens, max_blocks, n_seqs = int(q.shape[0]), _table_width(block_tables), int(block_tables.shape[0])
-    qshape = (n_tokens, desc.n_q_heads, desc.head_dim)
-    kc, vc, ks, vs = _q8_pools(desc, k_codes, v_codes, k_scales, v_scales, cur)
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_tokens, max_blocks, n_seqs = q.shape[0], _table_width(block_tables), block_tables.shape[0]
+    qshape = (n_tokens, f.n_q, f.d)
+    kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
     ws, ws_bytes = _workspace(workspace, cur)
     rc = lib().pkv_q8_prefill_attention(
-        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur), kc, vc, ks, vs,
-        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
-        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur),
-        _dev(query_start, "query_start", t.int32, (n_seqs + 1,), cur=cur), n_seqs, n_tokens, int(max_query_len),
-        float(scale), _dev(out, "out", dt, qshape, cur=cur), ws, ws_bytes, _stream_handle(stream))
+        ctypes.byref(desc), int(layer), _ptr(q, "q", f.dtype, qshape, cur), kc, vc, ks, vs,
+        _ptr(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur), max_blocks,
+        _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur),
+        _ptr(query_start, "query_start", t.int32, (n_seqs + 1,), cur), n_seqs, n_tokens, int(max_query_len),
+        scale, _ptr(out, "out", f.dtype, qshape, cur), ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_q8_prefill_attention")
 
 
@@ -706,19 +734,17 @@ def pkv_paged_decode_attention_scored(desc: CacheDesc, layer: int, q, k_pool, v_
                                       scale: float, out, scores, workspace, stream=None) -> None:
     """pkv_paged_decode_attention that adds each position's attention weight to scores, float32
     [n_seqs, n_kv, S] (workspace from alloc_scored_workspace)."""
-    t = _torch()
-    dt = torch_dtype(desc.dtype_name)
-    cur = _current_device()
-    n_seqs, max_blocks = int(q.shape[0]), _table_width(block_tables)
-    qshape = (n_seqs, desc.n_q_heads, desc.head_dim)
-    sp, stride = _scores(scores, "scores", (n_seqs, desc.n_kv_heads), max_blocks, cur)
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_seqs, max_blocks = q.shape[0], _table_width(block_tables)
+    qshape = (n_seqs, f.n_q, f.d)
+    sp, stride = _scores(scores, "scores", (n_seqs, f.n_kv), max_blocks, cur)
     ws, ws_bytes = _workspace(workspace, cur)
     rc = lib().pkv_paged_decode_attention_scored(
-        ctypes.byref(desc), int(layer), _dev(q, "q", dt, qshape, cur=cur),
-        _dev(k_pool, "k_pool", dt, pool_shape(desc), cur=cur), _dev(v_pool, "v_pool", dt, pool_shape(desc), cur=cur),
-        _dev(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
-        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur), n_seqs, float(scale),
-        _dev(out, "out", dt, qshape, cur=cur), sp, stride, ws, ws_bytes, _stream_handle(stream))
+        ctypes.byref(desc), int(layer), _ptr(q, "q", f.dtype, qshape, cur), _ptr(k_pool, "k_pool", f.dtype, f.pool, cur),
+        _ptr(v_pool, "v_pool", f.dtype, f.pool, cur),
+        _ptr(block_tables, "block_tables", t.int32, (n_seqs, max_blocks), cur), max_blocks,
+        _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur), n_seqs, scale,
+        _ptr(out, "out", f.dtype, qshape, cur), sp, stride, ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_paged_decode_attention_scored")
 
 
@@ -730,36 +756,33 @@ def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, co
     kept int32 [n_layers, n_seqs, n_kv, max_keep]. For 8-bit pools k_pool / v_pool are the codes, with
     k_scales, v_scales and a workspace from alloc_evict_workspace.
     """
-    t = _torch()
-    cur = _current_device()
-    n_seqs, max_blocks = int(src_tables.shape[0]), _table_width(src_tables)
-    q8 = k_scales is not None or v_scales is not None
-    if q8:
+    t, f, cur = _torch(), _facts(desc), _current_device()
+    n_seqs, max_blocks = src_tables.shape[0], _table_width(src_tables)
+    if k_scales is not None or v_scales is not None:
         if k_scales is None or v_scales is None:
             raise ValueError("8-bit pools need k_scales and v_scales")
-        kp, vp, ks, vs = _q8_pools(desc, k_pool, v_pool, k_scales, v_scales, cur)
+        kp, vp, ks, vs = _q8_pools(t, f, k_pool, v_pool, k_scales, v_scales, cur)
     else:
-        dt = torch_dtype(desc.dtype_name)
-        kp, vp = _dev(k_pool, "k_pool", dt, pool_shape(desc), cur=cur), _dev(v_pool, "v_pool", dt, pool_shape(desc), cur=cur)
+        kp, vp = _ptr(k_pool, "k_pool", f.dtype, f.pool, cur), _ptr(v_pool, "v_pool", f.dtype, f.pool, cur)
         ks = vs = None
-    lead = (desc.n_layers, n_seqs, desc.n_kv_heads)
+    lead = (f.n_layers, n_seqs, f.n_kv)
     sp, stride = _scores(scores, "scores", lead, max_blocks, cur)
-    np_, _ = _scores(new_scores, "new_scores", lead, max_blocks, cur)
-    if tuple(new_scores.shape) != tuple(scores.shape):
+    if new_scores.shape != scores.shape:
         raise ValueError("new_scores must have the shape of scores")
-    nbytes = scores.numel() * 4
-    if sp.value is not None and sp.value != np_.value and abs((sp.value or 0) - (np_.value or 0)) < nbytes:
+    new, _ = _scores(new_scores, "new_scores", lead, max_blocks, cur)
+    if sp != new and abs(sp - new) < scores.nbytes:
         raise ValueError("new_scores must be scores itself or not overlap it")
     if kept.dim() != 4:
         raise ValueError("kept must be [n_layers, n_seqs, n_kv, max_keep]")
-    max_keep = int(kept.shape[3])
+    max_keep = kept.shape[3]
     ws, ws_bytes = _workspace(workspace, cur)
+    tables = (n_seqs, max_blocks)
     rc = lib().pkv_evict_tokens(
-        ctypes.byref(desc), kp, vp, ks, vs, _dev(src_tables, "src_tables", t.int32, (n_seqs, max_blocks), cur=cur),
-        _dev(dst_tables, "dst_tables", t.int32, (n_seqs, max_blocks), cur=cur), max_blocks,
-        _dev(context_lens, "context_lens", t.int32, (n_seqs,), cur=cur),
-        _dev(keep_lens, "keep_lens", t.int32, (n_seqs,), cur=cur), n_seqs, int(recent), sp, np_, stride,
-        _dev(kept, "kept", t.int32, (*lead, max_keep), cur=cur), max_keep, ws, ws_bytes, _stream_handle(stream))
+        ctypes.byref(desc), kp, vp, ks, vs, _ptr(src_tables, "src_tables", t.int32, tables, cur),
+        _ptr(dst_tables, "dst_tables", t.int32, tables, cur), max_blocks,
+        _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur),
+        _ptr(keep_lens, "keep_lens", t.int32, (n_seqs,), cur), n_seqs, int(recent), sp, new, stride,
+        _ptr(kept, "kept", t.int32, (*lead, max_keep), cur), max_keep, ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_evict_tokens")
 
 
