@@ -452,9 +452,13 @@ size_t pkv_q8_decode_workspace_bytes(const pkv_cache_desc* desc, int32_t n_seqs,
  *                 summed over the query heads of KV head g, for j < context_lens[s]. Row s of the
  *                 batch owns row s of scores, also when sequences share blocks. Other entries are
  *                 left as they are. fp32, each entry written by one thread: reproducible
- *   workspace     device, >= pkv_q8_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
- *                 initialisation; calls that overlap on the GPU must not share one
+ *   workspace     device, >= pkv_q8_decode_workspace_bytes(...) bytes, 16-byte aligned. Its first
+ *                 PKV_ARRIVAL_BYTES are zero before the first call; every call leaves them zero again,
+ *                 whatever its shape (after PKV_DEV_WAIT_TIMEOUT zero them anew), the rest needs no
+ *                 initialisation. pkv_paged_decode_attention_scored may use the same buffer, other
+ *                 calls must not write there; calls that overlap on the GPU must not share one
  */
+#define PKV_ARRIVAL_BYTES 8192
 int pkv_q8_decode_attention(const pkv_cache_desc* desc, int32_t layer, const void* q, const void* k_codes,
                             const void* v_codes, const float* k_scales, const float* v_scales,
                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,

@@ -51,17 +51,15 @@ int validate16(const pkv_cache_desc* d) {
     return d->dtype == PKV_F32 ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
-// Partition geometry of the fragment kernel. pairs = (sequence, KV head) pairs, slots = CTAs the GPU
-// holds at once.
-//  * pairs < slots / 2: one wave. A context is cut into slots / pairs partitions, but none shorter than
-//    kMinPart blocks (one iteration of each of a CTA's warps).
-//  * otherwise kMaxBpp blocks a partition: several CTAs a slot, short enough to even out ragged lengths.
-// When the whole grid is at most one CTA per SM and a context has at most kMaxCluster partitions, these
-// form a cluster and are joined through shared memory.
-constexpr int kMinPart = 8, kMaxCluster = 8;
+// Geometry of the fragment kernel. Runs: as many CTAs as the GPU holds at once. Partitions: when every
+// (sequence, KV head) pair can have its context cut into a cluster's worth of partitions of at most
+// kMaxPartition blocks with no more than one CTA per SM: small calls, where latency counts.
+constexpr int kMaxCluster = 8;
+
+static_assert(pkv::kMaxRuns * sizeof(unsigned int) == PKV_ARRIVAL_BYTES, "one counter a run");
 
 struct FragGeometry {
-    int bpp, n_parts, cluster;
+    int ctas, partition;  // CTAs along x; blocks of a partition, 0 for runs
 };
 
 cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, FragGeometry* out) {
@@ -69,34 +67,35 @@ cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_
     cudaError_t err = pkv::current_sm_count(&sms);
     if (err == cudaSuccess) err = pkv::frag_ctas_per_sm(d->dtype, q8, d->head_dim, group_of(d), &per_sm);
     if (err != cudaSuccess) return err;
-    const long long pairs = (long long)n_seqs * d->n_kv_heads, slots = (long long)sms * per_sm;
-    int bpp = pkv::kMaxBpp;
-    if (2 * pairs < slots) {
-        const long long parts = slots / pairs;
-        bpp = (int)((max_blocks + parts - 1) / parts);
-        if (bpp < kMinPart) bpp = kMinPart;
+    const long long pairs = (long long)n_seqs * d->n_kv_heads;
+    const long long parts = pairs >= sms ? 1 : sms / pairs < kMaxCluster ? sms / pairs : kMaxCluster;
+    const int partition = (int)((max_blocks + parts - 1) / parts);
+    if (pairs <= sms && partition <= pkv::kMaxPartition) {
+        out->partition = partition < pkv::kMinRun ? pkv::kMinRun : partition;
+        out->ctas = pkv::decode_partitions(max_blocks, out->partition);
+    } else {
+        out->partition = 0;
+        out->ctas = sms * per_sm < pkv::kMaxRuns ? sms * per_sm : pkv::kMaxRuns;
     }
-    out->bpp = bpp;
-    out->n_parts = pkv::decode_partitions(max_blocks, bpp);
-    out->cluster = out->n_parts <= kMaxCluster && pairs * out->n_parts <= sms ? out->n_parts : 1;
     return cudaSuccess;
 }
 
 struct FragLayout {
-    size_t ml, cnt, z, bytes;  // offsets; the partial outputs lie at 0
+    size_t o, ml, row_ml, z, bytes;  // offsets; the arrival counters lie at 0
 };
 
-// Partial outputs, counters: split contexts only. (max, sum) pairs: those, or summed weights. Logits:
-// summed weights.
+// Runs: arrival counters (always the same bytes at the front), partials, and for summed weights every
+// row's (max, sum) and the logits. Partitions need nothing.
 FragLayout frag_layout(const pkv_cache_desc* d, int n_seqs, int max_blocks, const FragGeometry& geo, bool scored) {
     auto up = [](size_t x) { return (x + 15) / 16 * 16; };
     const size_t rows = (size_t)n_seqs * d->n_q_heads;
-    const int n_parts = geo.n_parts;
-    const bool split = n_parts > 1 && geo.cluster == 1;
+    if (geo.partition > 0) scored = false;
+    const size_t partials = geo.partition > 0 ? 0 : (size_t)geo.ctas * 2 * group_of(d);
     FragLayout l{};
-    l.ml = split ? up(rows * n_parts * d->head_dim * sizeof(float)) : 0;
-    l.cnt = l.ml + (split || scored ? up(rows * n_parts * 2 * sizeof(float)) : 0);
-    l.z = l.cnt + (split ? up((size_t)n_seqs * d->n_kv_heads * sizeof(unsigned long long)) : 0);
+    l.o = partials ? PKV_ARRIVAL_BYTES : 0;
+    l.ml = l.o + up(partials * d->head_dim * sizeof(float));
+    l.row_ml = l.ml + up(partials * sizeof(float2));
+    l.z = l.row_ml + (scored ? up(rows * sizeof(float2)) : 0);
     l.bytes = l.z + (scored ? up(rows * max_blocks * pkv::kBlock * sizeof(float)) : 0);
     return l;
 }
@@ -130,7 +129,6 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     FragGeometry geo;
     if (frag_geometry(d, q8, n_seqs, max_blocks, &geo) != cudaSuccess) return PKV_ERR_CUDA;
     const FragLayout l = frag_layout(d, n_seqs, max_blocks, geo, scores != nullptr);
-    const bool split = geo.n_parts > 1 && geo.cluster == 1;
     if (l.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < l.bytes)) return PKV_ERR_INVALID_ARG;
 
     pkv::FragArgs a;
@@ -142,32 +140,38 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     a.d.tables = tables;
     a.d.lens = lens;
     a.d.out = out;
-    a.d.part_o = split ? reinterpret_cast<float*>(ws) : nullptr;
-    a.d.part_ml = split || scores ? reinterpret_cast<float*>(ws + l.ml) : nullptr;
-    a.d.counters = split ? reinterpret_cast<unsigned long long*>(ws + l.cnt) : nullptr;
-    a.d.call_tag = pkv::next_call_tag();
+    if (geo.partition == 0) {
+        a.arrivals = reinterpret_cast<unsigned int*>(ws);
+        a.d.part_o = reinterpret_cast<float*>(ws + l.o);
+        a.d.part_ml = reinterpret_cast<float*>(ws + l.ml);
+    }
     a.d.n_seqs = n_seqs;
     a.d.n_q = d->n_q_heads;
     a.d.n_kv = d->n_kv_heads;
     a.d.num_blocks = d->num_blocks;
     a.d.max_blocks = max_blocks;
-    a.d.n_parts = geo.n_parts;
-    a.d.bpp = geo.bpp;
-    a.cluster = geo.cluster;
+    a.d.n_parts = geo.ctas;
+    a.partition = geo.partition;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     if (q8) {
         a.k_scales = k_scales + layer_scales(d) * layer;
         a.v_scales = v_scales + layer_scales(d) * layer;
     }
-    a.z = scores ? reinterpret_cast<float*>(ws + l.z) : nullptr;
+    if (scores && geo.partition > 0) {
+        a.scores = scores;
+        a.score_stride = score_stride;
+    } else if (scores) {
+        a.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
+        a.z = reinterpret_cast<float*>(ws + l.z);
+    }
     if (pkv::device_status_word(&a.d.status) != cudaSuccess) return PKV_ERR_CUDA;
     cudaError_t err = pkv::launch_frag_decode(d->dtype, q8, d->head_dim, group_of(d), a, static_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return pkv::launch_status(err);
     pkv::count_launches(1);
-    if (scores) {
+    if (scores && geo.partition == 0) {
         pkv::ScoreArgs s;
         s.z = a.z;
-        s.part_ml = a.d.part_ml;
+        s.row_ml = a.row_ml;
         s.lens = lens;
         s.scores = scores;
         s.stride = score_stride;
@@ -175,8 +179,6 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
         s.n_kv = d->n_kv_heads;
         s.group = group_of(d);
         s.max_blocks = max_blocks;
-        s.n_parts = geo.n_parts;
-        s.bpp = geo.bpp;
         if (pkv::launch_scores(s, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
         pkv::count_launches(1);
     }

@@ -7,8 +7,19 @@
 // token and head for codes, against 4 D for 16-bit rows, so a kernel that keeps up with memory takes
 // half the time -- and has half as long for the arithmetic of each token.
 //
-// The grid, the partitions, the split-K merge and the per-warp rings of TMA copies are those of
-// decode_mma.cuh. What differs is how a 16-token tile gets from shared memory into fragments:
+// Work is cut by blocks, not by sequences: the blocks of all (sequence, KV head) pairs form one list,
+// and each of the CTAs the GPU holds at once takes an equal run of it, whatever the lengths are (a pair
+// counts kPairCost blocks on top of its own, what starting and ending it costs). A run
+// covers the end of one pair, some whole pairs and the start of another; only its first and its last
+// pair can be shared with other CTAs, so two partial results a CTA are all that is kept in memory, and
+// the CTA that arrives last at a shared pair joins its partials. (A grid over table-width partitions
+// gave a ragged batch -- 32 sequences of 0..8,192 tokens, 8 heads x 8 queries -- 70 us of which a third
+// were starts, joins and a tail of half-empty SMs.) Calls of a few small contexts take a grid of
+// (partition, head, sequence) instead, the partitions of a context being a thread-block cluster that
+// joins through shared memory.
+//
+// Per-warp rings of TMA copies feed the warps as in decode_mma.cuh. What differs is how a 16-token tile
+// gets from shared memory into fragments:
 //  * The contraction of S = K Q^T runs over head dims in any order, as long as Q's fragment uses the
 //    same one. A lane therefore takes whole 16-byte chunks of a K row (one 128-bit read) and the dims
 //    that lie in them become its k indices: 16 codes are the k indices of four m16n8k16 steps.
@@ -48,8 +59,24 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
     return r;
 }
 
+constexpr int kMaxCluster = 8;  // the portable limit
+
+// What a pair costs a CTA beside its blocks, in blocks: 4.7 us (loads of the table, the query and the
+// first tiles, the warps' join, the output) against 0.19 us a block of codes. Without it a CTA whose run
+// holds 34 short contexts ended 66 us after one with long ones.
+template <bool Q8>
+constexpr int kPairCost = Q8 ? 24 : 12;
+
+constexpr int kJoinChunk = 128;  // partials whose weights are worked out at a time
+
+// Shared-memory floats the join of partials needs (flag, row maxima, sums, factors, a chunk's weights).
+template <int G>
+struct JoinScratch {
+    static constexpr size_t BYTES = (4 + 3 * G + G * kJoinChunk) * sizeof(float);
+};
+
 // NW warps, each with a ring of ST stages of BPI blocks (K tiles, then V tiles).
-template <bool Q8, int D, int NW, int ST, int BPI>
+template <bool Q8, int D, int G, int NW, int ST, int BPI>
 struct FragGeom {
     static constexpr int ROWB = D * (Q8 ? 1 : 2);            // bytes of a row
     static constexpr int PANB = ROWB < 128 ? ROWB : 128;     // bytes of a panel's row (one TMA box)
@@ -60,12 +87,15 @@ struct FragGeom {
     static constexpr int KCH = ROWB / 64;                    // 16-byte chunks of a K row per lane
     static constexpr size_t STAGES = (size_t)NW * ST * STAGE;
     static constexpr size_t BARS = STAGES;                            // uint64 [NW][ST][K, V]
-    static constexpr size_t ML = BARS + (size_t)NW * ST * 16;         // float [NW][8][2]
-    static constexpr size_t TOTAL = ML + (size_t)NW * 8 * 2 * 4;
+    static constexpr size_t ML = BARS + (size_t)NW * ST * 16;         // float2 [NW][8]: (max, sum) of a warp's rows
+    static constexpr size_t JOIN = ML + (size_t)NW * 8 * 8;           // float [8][NW] weights, [8] maxima, [8] sums
+    static constexpr size_t FIND = JOIN + (size_t)8 * (NW + 2) * 4;   // long long [NW + 2]
+    static constexpr size_t TOTAL = (FIND + (size_t)(NW + 2) * 8 + 15) / 16 * 16;
     static constexpr size_t ALLOC = TOTAL + 1024;             // room to align the base
-    static constexpr size_t MERGE = (size_t)NW * 8 * D * 4;  // merge scratch, after the combine buffer
-    static_assert(MERGE + MergeScratch<8>::BYTES <= STAGES && MERGE + 8 * (D + 2) * 4 <= STAGES,
-                  "combine buffer and merge scratch must fit");
+    static_assert(TOTAL % 16 == 0, "the logits of a partition follow");
+    static constexpr size_t MERGE = (size_t)NW * G * D * 4;  // join scratch, after the combine buffer
+    static_assert(MERGE + JoinScratch<G>::BYTES <= STAGES && MERGE + G * (D + 2) * 4 <= STAGES,
+                  "combine buffer and join scratch must fit");
     // byte of 16-byte chunk `c` of row `r`: the copy's swizzle XORs the chunk with the 128-byte line's
     // number modulo the pattern (8 rows of 128 bytes, or 4 lines of two 64-byte rows)
     __device__ __forceinline__ static uint32_t at(int r, int c) {
@@ -94,6 +124,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// f * v, rounded, to four consecutive elements.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v, float f) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(MmaType<T>::pack(v.x * f, v.y * f), MmaType<T>::pack(v.z * f, v.w * f));
+}
+
 // Four consecutive elements of a query row, widened.
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, float* f) {
@@ -114,92 +150,109 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kWeightExp = 15.f;  // exponent of the largest fp16 weight
 
-// Split-K epilogue of the CTA (s, g, p) of a sequence with np > 1 partitions: the CTA that arrives last
-// at the (s, g) counter joins the np partials of every row in partition order,
-//   out = sum_p o_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),  M = max_p m_p.
-// The counter protocol is splitk_merge_if_last's (decode.cuh): (call tag << 24) | arrivals, any other
-// tag reads as zero arrivals, the merging CTA leaves 0. Unlike there, a partial whose sum is NaN makes
-// the row NaN instead of being left out.
+// (max, sum) pairs and partial outputs a run leaves in memory: slot 0 for a pair it did not start, slot 1
+// for one it does not end. Partial i of a pair whose first CTA is `first` lies in:
+__device__ __forceinline__ int partial_slot(int first, int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); }
+
+// Ends a shared pair in the CTA that arrives last: joins the np partials in order,
+//   out = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M),  M = max_i m_i.
+// The arrival counter wraps to 0 with the last arrival (atomicInc), so it is ready for the next call; it
+// belongs to the pair's first CTA and always lies at the same place of the workspace. An addition, not a
+// compare-and-swap: the CTAs of one wave end together, and retries would queue at an L2 round trip each.
 template <typename T, int D, int G, int NT>
-__device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, int g, int np, float* scratch) {
+__device__ __forceinline__ void join_if_last(const FragArgs& fa, size_t row0, int first, int np, float* scratch) {
+    const DecodeArgs& a = fa.d;
     constexpr int NWARP = NT / 32;
-    constexpr int PER = (G * D + NT - 1) / NT;
-    constexpr int MQ = kMergeLoads / PER < 2 ? 2 : (kMergeLoads / PER > 16 ? 16 : kMergeLoads / PER);
+    constexpr int PER = (G * D / 4 + NT - 1) / NT;  // groups of four outputs of a thread
+    constexpr int MQ = 16 / PER;                     // partials of each in flight at once
     int* flag = reinterpret_cast<int*>(scratch);
     float* sM = scratch + 4;  // [G]
     float* sL = sM + G;       // [G]
-    float* sW = sL + G;       // [G][kMergeChunk]
-    unsigned long long* cnt = a.counters + (size_t)s * a.n_kv + g;
+    float* sF = sL + G;       // [G]
+    float* sW = sF + G;       // [G][kJoinChunk]
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        unsigned long long cur = 0;  // what the first arrival finds: one round trip less than reading it
-        unsigned long long next;
-        while (true) {
-            next = ((cur >> 24) == a.call_tag) ? cur + 1 : ((a.call_tag << 24) | 1ull);
-            const unsigned long long prev = atomicCAS(cnt, cur, next);
-            if (prev == cur) break;
-            cur = prev;
-        }
-        *flag = (next & 0xffffffull) == (unsigned long long)np;
+        *flag = atomicInc(fa.arrivals + first, (unsigned)np - 1) == (unsigned)np - 1;
         __threadfence();
     }
     __syncthreads();
     if (!*flag) return;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const size_t row0 = (size_t)s * a.n_q + (size_t)g * G;
-    for (int r = warp; r < G; r += NWARP) {
-        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (row0 + r) * a.n_parts;
-        float m = -INFINITY;
-        for (int q = lane; q < np; q += 32) m = fmaxf(m, __ldcg(ml + q).x);
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    // a warp per row: every pair is read once, a chunk's at the same time
+    float4 O[PER];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) {
-            sM[r] = m;
-            sL[r] = 0.f;
-        }
-    }
-    float O[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) O[k] = 0.f;
-    for (int c0 = 0; c0 < np; c0 += kMergeChunk) {
-        __syncthreads();  // maxima visible; the previous chunk's weights consumed
+    for (int k = 0; k < PER; ++k) O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < np; c0 += kJoinChunk) {
+        const int nq = min(kJoinChunk, np - c0);
+        if (c0 > 0) __syncthreads();  // the previous chunk's weights are consumed
         for (int r = warp; r < G; r += NWARP) {
-            const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (row0 + r) * a.n_parts;
-            const int q = c0 + lane;
-            float w = 0.f, lw = 0.f;
-            if (q < np) {
-                const float2 u = __ldcg(ml + q);
-                w = u.x == -INFINITY ? 0.f : ex2(u.x - sM[r]);
-                lw = u.y * w;
-            }
-            sW[r * kMergeChunk + lane] = w;
+            float2 u[kJoinChunk / 32];
+            float m = c0 > 0 ? sM[r] : -INFINITY;
+            const float before = m;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-            if (lane == 0) sL[r] += lw;
+            for (int i = 0; i < kJoinChunk / 32; ++i) {
+                const int q = i * 32 + lane;
+                u[i] = make_float2(-INFINITY, 0.f);
+                if (q < nq) u[i] = __ldcg(ml + (size_t)partial_slot(first, c0 + q) * G + r);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinChunk / 32; ++i) m = fmaxf(m, u[i].x);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinChunk / 32; ++i) {
+                const float w = u[i].x == -INFINITY ? 0.f : ex2(u[i].x - m);
+                sW[r * kJoinChunk + i * 32 + lane] = w;
+                l = fmaf(u[i].y, w, l);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) {
+                const float f = before == -INFINITY ? 0.f : ex2(before - m);
+                sL[r] = c0 > 0 ? fmaf(sL[r], f, l) : l;
+                sF[r] = f;
+                sM[r] = m;
+            }
         }
         __syncthreads();
-        const int nq = min(kMergeChunk, np - c0);
-        // groups of MQ partials: all MQ x PER loads of a group in flight before they are folded
-        for (int q0 = 0; q0 < nq; q0 += MQ) {
-            const int mq = min(MQ, nq - q0);
-            float v[PER][MQ];
+        if (c0 > 0) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                const int idx = threadIdx.x + k * NT;
-                const float* po = a.part_o + ((row0 + idx / D) * a.n_parts + c0 + q0) * D + idx % D;
+                const float f = sF[min((int)threadIdx.x + k * NT, G * D / 4 - 1) / (D / 4)];
+                O[k] = make_float4(O[k].x * f, O[k].y * f, O[k].z * f, O[k].w * f);
+            }
+        }
+        for (int q0 = 0; q0 < nq; q0 += MQ) {
+            float4 v[PER][MQ];
 #pragma unroll
-                for (int u = 0; u < MQ; ++u) v[k][u] = (idx < G * D && u < mq) ? __ldcg(po + (size_t)u * D) : 0.f;
+            for (int k = 0; k < PER; ++k) {
+                const int i4 = threadIdx.x + k * NT;
+#pragma unroll
+                for (int u = 0; u < MQ; ++u) {
+                    v[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i4 < G * D / 4 && q0 + u < nq)
+                        v[k][u] = __ldcg(reinterpret_cast<const float4*>(
+                                             a.part_o + (size_t)partial_slot(first, c0 + q0 + u) * G * D) + i4);
+                }
             }
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                const int idx = threadIdx.x + k * NT;
-                if (idx < G * D) {
-                    const float* w = sW + (idx / D) * kMergeChunk + q0;
+                const int i4 = threadIdx.x + k * NT;
+                if (i4 < G * D / 4) {
+                    const float* w = sW + (i4 / (D / 4)) * kJoinChunk + q0;
 #pragma unroll
-                    for (int u = 0; u < MQ; ++u)
-                        if (u < mq) O[k] = fmaf(w[u], v[k][u], O[k]);
+                    for (int u = 0; u < MQ; ++u) {
+                        if (q0 + u < nq) {
+                            O[k].x = fmaf(w[u], v[k][u].x, O[k].x);
+                            O[k].y = fmaf(w[u], v[k][u].y, O[k].y);
+                            O[k].z = fmaf(w[u], v[k][u].z, O[k].z);
+                            O[k].w = fmaf(w[u], v[k][u].w, O[k].w);
+                        }
+                    }
                 }
             }
         }
@@ -207,18 +260,18 @@ __device__ __forceinline__ void frag_merge_if_last(const DecodeArgs& a, int s, i
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int idx = threadIdx.x + k * NT;
-        if (idx < G * D) {
-            const float L = sL[idx / D];
-            reinterpret_cast<T*>(a.out)[row0 * D + idx] = from_float<T>(L == 0.f ? 0.f : O[k] / L);
+        const int i4 = threadIdx.x + k * NT;
+        if (i4 < G * D / 4) {
+            const float L = sL[i4 / (D / 4)];
+            store4(reinterpret_cast<T*>(a.out) + row0 * D + 4 * i4, O[k], L == 0.f ? 0.f : 1.f / L);
         }
     }
-    if (threadIdx.x == 0) *cnt = 0ull;
+    if (fa.row_ml && threadIdx.x < G) fa.row_ml[row0 + threadIdx.x] = make_float2(sM[threadIdx.x], sL[threadIdx.x]);
 }
 
-// The same join for a cluster of the sequence's partitions, through the CTAs' shared memory: no trip to
-// L2 for the partials and none for a counter. Every CTA p < np has its (max, sum) pairs in ml [G][2] and
-// its partial outputs in po [G * D], and writes every np-th piece of the output.
+// The same join for a cluster of a pair's partitions, through the CTAs' shared memory: no trip to L2 for
+// the partials and none for a counter. Every CTA p < np has its (max, sum) pairs in ml [G][2] and its
+// partial outputs in po [G * D], and writes every np-th piece of the output.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
@@ -234,38 +287,48 @@ __device__ __forceinline__ float cluster_load(uint32_t a) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-constexpr int kMaxCluster = 8;  // the portable limit
-
 template <typename T, int D, int G, int NT>
-__device__ __forceinline__ void cluster_merge(T* out, int p, int np, const float* ml, const float* po) {
+__device__ __forceinline__ void cluster_join(T* out, int p, int np, const float* ml, const float* po, float* s_max,
+                                             float* s_sum) {
     cluster_barrier();
     const uint32_t ml0 = smem_addr(ml), po0 = smem_addr(po);
-    for (int idx = p * NT + threadIdx.x; idx < G * D; idx += np * NT) {
-        const int r = idx / D;
-        float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster];
+    auto row = [&](int r, float* w, float* M, float* L) {  // the partials' weights, the row's maximum and sum
+        float m[kMaxCluster], l[kMaxCluster];
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) {
+            m[q] = -INFINITY;
+            l[q] = 0.f;
             if (q < np) {
                 m[q] = cluster_load(cluster_addr(ml0 + (2 * r) * 4, q));
                 l[q] = cluster_load(cluster_addr(ml0 + (2 * r + 1) * 4, q));
-                o[q] = cluster_load(cluster_addr(po0 + idx * 4, q));
             }
         }
-        float M = -INFINITY, L = 0.f, O = 0.f;
+        *M = -INFINITY;
+        *L = 0.f;
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-            if (q < np) M = fmaxf(M, m[q]);
+        for (int q = 0; q < kMaxCluster; ++q) *M = fmaxf(*M, m[q]);
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) {
-            if (q < np) {
-                const float w = m[q] == -INFINITY ? 0.f : ex2(m[q] - M);
-                L = fmaf(l[q], w, L);
-                O = fmaf(o[q], w, O);
-            }
+            w[q] = m[q] == -INFINITY ? 0.f : ex2(m[q] - *M);
+            *L = fmaf(l[q], w[q], *L);
         }
+    };
+    float w[kMaxCluster], M, L;
+    for (int idx = p * NT + threadIdx.x; idx < G * D; idx += np * NT) {
+        float o[kMaxCluster], O = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) o[q] = q < np ? cluster_load(cluster_addr(po0 + idx * 4, q)) : 0.f;
+        row(idx / D, w, &M, &L);
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) O = fmaf(o[q], w[q], O);
         out[idx] = from_float<T>(L == 0.f ? 0.f : O / L);
     }
-    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    if (s_max && threadIdx.x < G) {
+        row(threadIdx.x, w, &M, &L);
+        s_max[threadIdx.x] = M;
+        s_sum[threadIdx.x] = L;
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory; the statistics are written
 }
 
 template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS>
@@ -273,8 +336,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                                                                     const __grid_constant__ CUtensorMap tm_k,
                                                                     const __grid_constant__ CUtensorMap tm_v) {
     static_assert(G <= 8, "at most 8 query rows per KV head");
-    static_assert(BPI == 1 || BPI == 2, "one or two blocks per iteration");
-    using S = FragGeom<Q8, D, NW, ST, BPI>;
+    static_assert(BPI == 1 || BPI == 2 || BPI == 4, "blocks per iteration");
+    using S = FragGeom<Q8, D, G, NW, ST, BPI>;
     using MT = typename std::conditional<Q8, __half, T>::type;  // type of the matrix instructions' operands
     using M = MmaType<MT>;
     constexpr int KSTEPS = D / 16;  // QK k-steps = PV m-tiles
@@ -285,15 +348,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
-    float* s_ml = reinterpret_cast<float*>(smem + S::ML);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int gid = lane >> 2;  // token row of S, chunk of V
     const int tig = lane & 3;   // owns query rows 2 tig, 2 tig + 1
-    const int p = blockIdx.x;
-    const int g = blockIdx.y;
-    const int s = blockIdx.z;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -304,136 +363,232 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     __syncthreads();
     grid_dependency_wait();  // nothing in global memory has been touched so far
 
-    // This warp's i-th block (i = BPI k + u) is block BPI (warp + k NW) + u of the partition. Table
-    // entries come in chunks of 32 held in registers (lane l: entry 32 c + l): the chunk whose copies
-    // are being issued, the next, and the one after; scales follow a chunk behind the tables.
-    auto local_block = [&](int i) -> long long { return (long long)(i / BPI) * (NW * BPI) + warp * BPI + i % BPI; };
-    auto load_chunk = [&](int c) -> int {
-        const long long b = local_block(c * 32 + lane), idx = (long long)p * a.bpp + b;
-        return b < a.bpp && idx < a.max_blocks ? a.tables[(size_t)s * a.max_blocks + idx] : -1;
-    };
-    int t0 = load_chunk(0);
-    int t1 = a.bpp > 32 * NW ? load_chunk(1) : -1;
-    int t2 = a.bpp > 64 * NW ? load_chunk(2) : -1;
-    int ctx = a.lens[s];
     const int cap = a.max_blocks * kBlock;
-    if (ctx < 0 || ctx > cap) {
-        if (p == 0 && threadIdx.x == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
-        ctx = ctx < 0 ? 0 : cap;
-    }
-    const int nb = (ctx + kBlock - 1) / kBlock;
-    const int b0 = p * a.bpp;
-    if (b0 >= nb) {
-        if (p == 0) {
-            T* o = reinterpret_cast<T*>(a.out) + ((size_t)s * a.n_q + (size_t)g * G) * D;
-            for (int i = threadIdx.x; i < G * D; i += NW * 32) o[i] = from_float<T>(0.f);
-        }
-        return;
-    }
-    const int nblk = min(a.bpp, nb - b0);
-    const bool single = nb <= a.bpp;
-    // iterations of this warp, and its blocks (the last iteration may have one less than BPI)
-    const int nk = nblk > warp * BPI ? (nblk - warp * BPI + NW * BPI - 1) / (NW * BPI) : 0;
-    const int ni = nk == 0 ? 0 : (nk - 1) * BPI + min(BPI, nblk - (int)local_block((nk - 1) * BPI));
-
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]
     const uint32_t wstage = smem_addr(smem) + (uint32_t)(warp * ST) * S::STAGE;
     const uint64_t policy = l2_evict_first_policy();
+    auto length = [&](int seq) -> int { return min(max(a.lens[seq], 0), cap); };
+    auto blocks_of = [&](int len) -> int { return (len + kBlock - 1) / kBlock; };
+    // places a pair of so many blocks takes in the list: first its cost, then its blocks
+    auto span_of = [](int blocks) -> int { return blocks > 0 ? blocks + kPairCost<Q8> : 0; };
+    auto zero_row = [&](size_t row0, int n) {
+        for (int i = threadIdx.x; i < n * D / 8; i += NW * 32)
+            reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + row0 * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    };
 
-    struct Blocks {
-        int phys[BPI];
-    };
-    // Every lane: the blocks of iteration k (-1: none), for k = 0, 1, 2, ... in order (each once).
-    auto entries = [&](int k) -> Blocks {
-        const int i = k * BPI;
-        if ((i & 31) == 0 && i > 0) {
-            t0 = t1;
-            t1 = t2;
-            t2 = load_chunk((i >> 5) + 2);
+    // The run: [x, x_end) of the list, x lying at block `b` of pair (s, g). In a grid of partitions it is
+    // one partition of a context.
+    long long x, x_end, per = 0;
+    int s, g, b, ctx;
+    if (fa.partition > 0) {
+        s = blockIdx.z;
+        g = blockIdx.y;
+        b = blockIdx.x * fa.partition;
+        if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0 && (a.lens[s] < 0 || a.lens[s] > cap))
+            atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
+        ctx = length(s);
+        const int nb = blocks_of(ctx);
+        if (b >= nb) {
+            if (b == 0) zero_row((size_t)s * a.n_q + (size_t)g * G, G);
+            return;
         }
-        Blocks e;
-#pragma unroll
-        for (int u = 0; u < BPI; ++u) {
-            e.phys[u] = __shfl_sync(0xffffffffu, t0, (i & 31) + u);
-            const bool inside = (unsigned)e.phys[u] < (unsigned)a.num_blocks;
-            if (i + u < ni && !inside && lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
-            if (i + u >= ni || !inside) e.phys[u] = -1;
+        x = b;
+        x_end = min(b + fa.partition, nb);
+    } else {
+        // thread t sums the blocks of sequences [t per_t, (t + 1) per_t); a scan gives where they lie
+        long long* s_find = reinterpret_cast<long long*>(smem + S::FIND);
+        const int per_t = (a.n_seqs + NW * 32 - 1) / (NW * 32);
+        const int i0 = min((int)threadIdx.x * per_t, a.n_seqs), i1 = min(i0 + per_t, a.n_seqs);
+        long long mine = 0;
+        for (int i = i0; i < i1; ++i) {
+            const int len = a.lens[i];
+            if (blockIdx.x == 0 && (len < 0 || len > cap)) atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
+            mine += span_of(blocks_of(min(max(len, 0), cap)));
         }
-        return e;
-    };
-    // lane 0: start the copies of the K (v = 0) or V (v = 1) tiles of iteration k; none: the phase
-    // completes with nothing copied
-    auto issue = [&](int k, int v, const Blocks& e) {
-        const int st = k % ST;
-        uint64_t* bar = &wbars[st * 2 + v];
-        uint32_t bytes = 0;
+        long long before = mine;
 #pragma unroll
-        for (int u = 0; u < BPI; ++u) bytes += e.phys[u] >= 0 ? TILE : 0u;
-        if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
-        else mbar_arrive(bar);
-#pragma unroll
-        for (int u = 0; u < BPI; ++u) {
-            if (e.phys[u] < 0) continue;
-            const int row0 = (int)(((long long)e.phys[u] * a.n_kv + g) * kBlock);
-            const uint32_t dst = wstage + (uint32_t)st * S::STAGE + (uint32_t)(v * BPI + u) * TILE;
-#pragma unroll
-            for (int pn = 0; pn < S::PANELS; ++pn)
-                tma_load_2d(dst + pn * S::PANEL, v ? &tm_v : &tm_k, pn * (Q8 ? S::PANB : S::PANB / 2), row0, bar, policy);
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
         }
-    };
-    // after a timed-out wait: wait (bounded) for the tiles of iterations [k0, k1) of kind v still in flight
-    auto drain = [&](int k0, int k1, int v) {
-        for (int kk = k0; kk < k1 && kk < nk; ++kk) mbar_wait_bounded(&wbars[(kk % ST) * 2 + v], (uint32_t)(kk / ST) & 1u);
-    };
-    // Valid blocks of the iterations in the ring, as bits (iteration k: bits BPI (k % ST) ..).
-    unsigned ring = 0;
-    auto note = [&](int k, const Blocks& e) {
-        const int at = (k % ST) * BPI;
+        if (lane == 31) s_find[warp] = before;
+        __syncthreads();
+        long long total = 0;
 #pragma unroll
-        for (int u = 0; u < BPI; ++u) ring = (ring & ~(1u << (at + u))) | ((e.phys[u] >= 0 ? 1u : 0u) << (at + u));
-    };
-    static_assert(ST * BPI <= 16, "a ring's blocks fit the bits and one chunk of the table");
-    for (int k = 0; k < ST && k < nk; ++k) {
-        const Blocks e = entries(k);
-        note(k, e);
-        if (lane == 0) {
-            issue(k, 0, e);
-            issue(k, 1, e);
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += s_find[w];
+            total += s_find[w];
+        }
+        before -= mine;
+        total *= a.n_kv;
+        per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kMinRun + kPairCost<Q8>));
+        x = per * blockIdx.x;
+        x_end = min(x + per, total);
+        if (x >= before * a.n_kv && x < (before + mine) * a.n_kv) {  // one thread, if the run is not empty
+            int i = i0;
+            while (true) {
+                const int n = span_of(blocks_of(length(i)));
+                if (x < (before + n) * a.n_kv) break;
+                before += n;
+                ++i;
+            }
+            s_find[NW] = i;
+            s_find[NW + 1] = x - before * a.n_kv;
+        }
+        for (int i = blockIdx.x; i < a.n_seqs; i += gridDim.x)
+            if (a.lens[i] <= 0) zero_row((size_t)i * a.n_q, a.n_q);
+        __syncthreads();
+        if (x >= x_end) return;
+        s = (int)s_find[NW];
+        ctx = length(s);
+        const long long off = s_find[NW + 1];
+        const int span = span_of(blocks_of(ctx));
+        g = (int)(off / span);
+        b = (int)(off - (long long)g * span) - kPairCost<Q8>;
+        if (b < 0) {  // the run starts before the pair's first block
+            x -= b;
+            b = 0;
+            if (x >= x_end) return;
         }
     }
-    // Scales of the blocks of t0's chunk at the time, lane l: entry 32 c + l. They are consumed up to ST
-    // iterations behind the copies, so their chunk moves when the consumer enters it: t0 has entered it
-    // already (ST BPI <= 16 entries ago) and not left it.
-    float2 s0 = make_float2(1.f, 1.f), s1 = s0;
-    auto load_scales = [&](int c, int phys) -> float2 {
-        if (!Q8 || c * 32 + lane >= ni || (unsigned)phys >= (unsigned)a.num_blocks) return make_float2(0.f, 0.f);
-        const size_t i = (size_t)phys * a.n_kv + g;
-        return make_float2(__ldg(fa.k_scales + i), __ldg(fa.v_scales + i));
-    };
-    if (Q8) {
-        s0 = load_scales(0, t0);
-        s1 = load_scales(1, t1);
-    }
 
-    // Q^T fragments: k-step `ks` of row gid takes four dims of one of the lane's K chunks (one 32-bit
-    // word of codes, two words of halves); rows >= G are 0.
-    uint32_t qb[KSTEPS][2];
-    float zf[2];  // factor of the logits of query rows 2 tig, 2 tig + 1
-    {
-        const T* qrow = reinterpret_cast<const T*>(a.q) + ((size_t)s * a.n_q + (size_t)g * G + gid) * D;
-        constexpr int PER = KSTEPS / S::KCH;  // k-steps per chunk
+    float* s_join = reinterpret_cast<float*>(smem + S::JOIN);  // [8][NW] weights, [8] maxima, [8] sums
+    float2* s_ml = reinterpret_cast<float2*>(smem + S::ML);    // [NW][8]
+    int t_next = 0;     // this warp's first chunk of the next pair's table, read ahead
+    bool ahead = false; // and whether it has been
+    bool lost = false;  // a wait gave up
+    int done = 0;  // iterations of this warp in earlier pairs: the ring and its phases run on
+    while (true) {  // one pair (s, g), blocks [b, b + nblk) of its nb
+        const int nb = blocks_of(ctx);
+        const int nblk = (int)min(x_end - x, (long long)(nb - b));
+        const size_t row0 = (size_t)s * a.n_q + (size_t)g * G;
+
+        // This warp's i-th block (i = BPI k + u) is block BPI (warp + k NW) + u of the run's share. Table
+        // entries come in chunks of 32 held in registers (lane l: entry 32 c + l): the chunk whose copies
+        // are being issued, the next, and the one after; scales follow a chunk behind the tables.
+        auto local_block = [&](int i) -> int { return (i / BPI) * (NW * BPI) + warp * BPI + i % BPI; };
+        const int32_t* table = a.tables + (size_t)s * a.max_blocks + b;
+        auto load_chunk = [&](int c) -> int {
+            const int lb = local_block(c * 32 + lane);
+            return lb < nblk ? table[lb] : -1;
+        };
+        int t0 = ahead ? t_next : load_chunk(0);
+        int t1 = nblk > 32 * NW ? load_chunk(1) : -1;
+        int t2 = nblk > 64 * NW ? load_chunk(2) : -1;
+        constexpr int PER = KSTEPS / S::KCH;  // k-steps per chunk of a K row
+        uint2 qraw[KSTEPS];                   // the query row's words, on their way while the first tiles are
+        {
+            const T* qrow = reinterpret_cast<const T*>(a.q) + (row0 + gid) * D;
+#pragma unroll
+            for (int i = 0; i < KSTEPS; ++i) {
+                qraw[i] = make_uint2(0u, 0u);
+                if (gid < G)
+                    qraw[i] = __ldg(reinterpret_cast<const uint2*>(
+                        qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) + (i % PER) * 4));
+            }
+        }
+        // iterations of this warp, and its blocks (the last iteration may have one less than BPI)
+        const int nk = nblk > warp * BPI ? (nblk - warp * BPI + NW * BPI - 1) / (NW * BPI) : 0;
+        const int ni = nk == 0 ? 0 : (nk - 1) * BPI + min(BPI, nblk - local_block((nk - 1) * BPI));
+
+        // the pair after this one, if the run holds any of it
+        int s_next = s, g_next = g + 1, ctx_next = ctx;
+        ahead = fa.partition == 0 && x + nblk + kPairCost<Q8> < x_end;
+        if (ahead) {
+            if (g_next == a.n_kv) {
+                g_next = 0;
+                do ctx_next = length(++s_next);
+                while (ctx_next == 0);
+            }
+            const int n = blocks_of(ctx_next), lb = local_block(lane);
+            t_next = lb < n ? a.tables[(size_t)s_next * a.max_blocks + lb] : -1;
+        }
+
+        struct Blocks {
+            int phys[BPI];
+        };
+        // Every lane: the blocks of iteration k (-1: none), for k = 0, 1, 2, ... in order (each once).
+        auto entries = [&](int k) -> Blocks {
+            const int i = k * BPI;
+            if ((i & 31) == 0 && i > 0) {
+                t0 = t1;
+                t1 = t2;
+                t2 = load_chunk((i >> 5) + 2);
+            }
+            Blocks e;
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) {
+                e.phys[u] = __shfl_sync(0xffffffffu, t0, (i & 31) + u);
+                const bool inside = (unsigned)e.phys[u] < (unsigned)a.num_blocks;
+                if (i + u < ni && !inside && lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
+                if (i + u >= ni || !inside) e.phys[u] = -1;
+            }
+            return e;
+        };
+        // lane 0: start the copies of the K (v = 0) or V (v = 1) tiles of iteration k; none: the phase
+        // completes with nothing copied
+        auto issue = [&](int k, int v, const Blocks& e) {
+            const int st = (done + k) % ST;
+            uint64_t* bar = &wbars[st * 2 + v];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) bytes += e.phys[u] >= 0 ? TILE : 0u;
+            if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
+            else mbar_arrive(bar);
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) {
+                if (e.phys[u] < 0) continue;
+                const int row = (int)(((long long)e.phys[u] * a.n_kv + g) * kBlock);
+                const uint32_t dst = wstage + (uint32_t)st * S::STAGE + (uint32_t)(v * BPI + u) * TILE;
+#pragma unroll
+                for (int pn = 0; pn < S::PANELS; ++pn)
+                    tma_load_2d(dst + pn * S::PANEL, v ? &tm_v : &tm_k, pn * (Q8 ? S::PANB : S::PANB / 2), row, bar, policy);
+            }
+        };
+        auto phase = [&](int k) -> uint32_t { return (uint32_t)((done + k) / ST) & 1u; };
+        // after a timed-out wait: wait (bounded) for the tiles of iterations [k0, k1) of kind v still in flight
+        auto drain = [&](int k0, int k1, int v) {
+            for (int kk = k0; kk < k1 && kk < nk; ++kk) mbar_wait_bounded(&wbars[((done + kk) % ST) * 2 + v], phase(kk));
+        };
+        // Valid blocks of the iterations in the ring, as bits (iteration k: bits BPI (k % ST) ..).
+        unsigned ring = 0;
+        auto note = [&](int k, const Blocks& e) {
+            const int at = (k % ST) * BPI;
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) ring = (ring & ~(1u << (at + u))) | ((e.phys[u] >= 0 ? 1u : 0u) << (at + u));
+        };
+        static_assert(ST * BPI <= 16, "a ring's blocks fit the bits and one chunk of the table");
+        // Scales of the blocks of t0's chunk at the time, lane l: entry 32 c + l. They are consumed up to ST
+        // iterations behind the copies, so their chunk moves when the consumer enters it: t0 has entered it
+        // already (ST BPI <= 16 entries ago) and not left it.
+        auto load_scales = [&](int c, int phys) -> float2 {
+            if (!Q8 || c * 32 + lane >= ni || (unsigned)phys >= (unsigned)a.num_blocks) return make_float2(0.f, 0.f);
+            const size_t i = (size_t)phys * a.n_kv + g;
+            return make_float2(__ldg(fa.k_scales + i), __ldg(fa.v_scales + i));
+        };
+        float2 s0 = load_scales(0, t0), s1 = load_scales(1, t1);
+        for (int k = 0; k < ST && k < nk; ++k) {
+            const Blocks e = entries(k);
+            note(k, e);
+            if (lane == 0) {
+                issue(k, 0, e);
+                issue(k, 1, e);
+            }
+        }
+
+        // Q^T fragments: k-step `ks` of row gid takes four dims of one of the lane's K chunks (one 32-bit
+        // word of codes, two words of halves); rows >= G are 0.
+        uint32_t qb[KSTEPS][2];
+        float zf[2];  // factor of the logits of query rows 2 tig, 2 tig + 1
         if constexpr (Q8) {
-            float qf[KSTEPS][4];
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < KSTEPS; ++i) {
-                if (gid < G) load4(qrow + S::k_chunk(tig, i / PER) * 16 + (i % PER) * 4, qf[i]);
+                const float2 lo = MmaType<T>::unpack(qraw[i].x), hi = MmaType<T>::unpack(qraw[i].y);
+                const float f[4] = {fabsf(lo.x), fabsf(lo.y), fabsf(hi.x), fabsf(hi.y)};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (gid >= G) qf[i][e] = 0.f;
-                    const float x = fabsf(qf[i][e]);
-                    if (x <= 3.4028234e38f) amax = fmaxf(amax, x);
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (f[e] <= 3.4028234e38f) amax = fmaxf(amax, f[e]);
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -442,8 +597,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             const float down = pow2(-eq);
 #pragma unroll
             for (int i = 0; i < KSTEPS; ++i) {
-                qb[i][0] = M::pack(qf[i][0] * down, qf[i][1] * down);
-                qb[i][1] = M::pack(qf[i][2] * down, qf[i][3] * down);
+                const float2 lo = MmaType<T>::unpack(qraw[i].x), hi = MmaType<T>::unpack(qraw[i].y);
+                qb[i][0] = M::pack(lo.x * down, lo.y * down);
+                qb[i][1] = M::pack(hi.x * down, hi.y * down);
             }
             const float f = a.scale_log2 * pow2(eq);
             zf[0] = __shfl_sync(0xffffffffu, f, 8 * tig);
@@ -451,354 +607,410 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         } else {
 #pragma unroll
             for (int i = 0; i < KSTEPS; ++i) {
-                uint2 u = make_uint2(0u, 0u);
-                if (gid < G)
-                    u = *reinterpret_cast<const uint2*>(qrow + S::k_chunk(tig, i / PER) * 8 + (i % PER) * 4);
-                qb[i][0] = u.x;
-                qb[i][1] = u.y;
+                qb[i][0] = qraw[i].x;
+                qb[i][1] = qraw[i].y;
             }
             zf[0] = zf[1] = a.scale_log2;
         }
-    }
 
-    float acc[KSTEPS][4];  // m-tile mt: (dims dA, dA + 1) x (row 2tig | 2tig+1)
+        float acc[KSTEPS][4];  // m-tile mt: (dims dA, dA + 1) x (row 2tig | 2tig+1)
 #pragma unroll
-    for (int mt = 0; mt < KSTEPS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY};  // of z
-    float m_out[2] = {-INFINITY, -INFINITY};  // of z + log2 S_V (8-bit pools)
-    float l_run[2] = {0.f, 0.f};
+        for (int mt = 0; mt < KSTEPS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+        float m_run[2] = {-INFINITY, -INFINITY};  // of z
+        float m_out[2] = {-INFINITY, -INFINITY};  // of z + log2 S_V (8-bit pools)
+        float l_run[2] = {0.f, 0.f};
 
-    float* zrow = fa.z ? fa.z + ((size_t)s * a.n_kv + g) * cap * G : nullptr;
-
-    for (int k = 0; k < nk; ++k) {
-        const int st = k % ST;
-        const uint32_t par = (uint32_t)(k / ST) & 1u;
-        const unsigned have = (ring >> (st * BPI)) & ((1u << BPI) - 1);
-        Blocks next;
-        if (k + ST < nk) {  // the blocks whose copies go next
-            next = entries(k + ST);
-            note(k + ST, next);
+        // where logits go: memory, or behind the rings in a grid of partitions
+        float* zrow = nullptr;
+        int z0 = 0;  // the position it starts with
+        if (fa.partition > 0 && fa.scores) {
+            zrow = reinterpret_cast<float*>(smem + S::TOTAL);
+            z0 = b * kBlock;
+        } else if (fa.z) {
+            zrow = fa.z + ((size_t)s * a.n_kv + g) * cap * G;
         }
-        float2 sc2[BPI];
-#pragma unroll
-        for (int u = 0; u < BPI; ++u) {
-            const int i = k * BPI + u;
-            if (Q8) {
-                if ((i & 31) == 0 && i > 0) {
-                    s0 = s1;
-                    s1 = load_scales((i >> 5) + 1, t1);
-                }
-                sc2[u] = make_float2(__shfl_sync(0xffffffffu, s0.x, i & 31), __shfl_sync(0xffffffffu, s0.y, i & 31));
-            } else {
-                sc2[u] = make_float2(1.f, 1.f);
+        const int z_end = min(ctx, (b + nblk) * kBlock);  // positions behind belong to the next run
+
+        for (int k = 0; k < nk; ++k) {
+            const int st = (done + k) % ST;
+            const uint32_t par = phase(k);
+            const unsigned have = (ring >> ((k % ST) * BPI)) & ((1u << BPI) - 1);
+            Blocks next;
+            if (k + ST < nk) {  // the blocks whose copies go next
+                next = entries(k + ST);
+                note(k + ST, next);
             }
-        }
-        if (!mbar_wait_bounded(&wbars[st * 2], par)) {
-            if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
-            drain(k, k + ST, 0);  // K tiles of iterations k .. k+ST-1 may be in flight
-            drain(k, k + ST, 1);  // and their V tiles
-            break;
-        }
-        const int jb = (b0 + (int)local_block(k * BPI)) * kBlock;
-        const uint32_t sK = wstage + (uint32_t)st * S::STAGE;
-        const uint32_t sV = sK + BPI * TILE;
-        int nvalid[BPI];
-#pragma unroll
-        for (int u = 0; u < BPI; ++u) nvalid[u] = (have >> u) & 1 ? min(kBlock, ctx - jb - u * kBlock) : 0;
-        uint32_t b0f[BPI], b1f[BPI];
-        if (have) {
-            // ---- S = K Q^T (16 tokens x 8 rows a block), fp32; two chains hide the instruction's latency ----
-            float z[BPI][4];  // tokens gid (0, 1) and gid + 8 (2, 3) x rows 2tig, 2tig+1
+            float2 sc2[BPI];
 #pragma unroll
             for (int u = 0; u < BPI; ++u) {
-                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < S::KCH; ++i) {
-                    const int c = S::k_chunk(tig, i);
-                    const uint32_t tile = sK + u * TILE;
-                    const uint4 lo = lds128(tile + S::at(gid, c)), hi = lds128(tile + S::at(gid + 8, c));
-                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t af[4] = {e4m3x2_to_half2(wl[w]), e4m3x2_to_half2(wh[w]),
-                                                    e4m3x2_to_half2(wl[w] >> 16), e4m3x2_to_half2(wh[w] >> 16)};
-                            M::mma((w & 1) ? sb : sa, af, qb[i * 4 + w][0], qb[i * 4 + w][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const uint32_t af[4] = {wl[2 * w], wh[2 * w], wl[2 * w + 1], wh[2 * w + 1]};
-                            M::mma(w ? sb : sa, af, qb[i * 2 + w][0], qb[i * 2 + w][1]);
-                        }
+                const int i = k * BPI + u;
+                if (Q8) {
+                    if ((i & 31) == 0 && i > 0) {
+                        s0 = s1;
+                        s1 = load_scales((i >> 5) + 1, t1);
                     }
-                }
-                const bool v0 = gid < nvalid[u], v1 = gid + 8 < nvalid[u];
-                const float f0 = zf[0] * sc2[u].x, f1 = zf[1] * sc2[u].x;
-                z[u][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
-                z[u][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
-                z[u][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
-                z[u][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
-            }
-            // ---- online softmax ----
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-            float ev[BPI], mo0 = m_out[0], mo1 = m_out[1];
-            if constexpr (Q8) {
-                // the largest z + log2 S_V of the iteration needs each block's own maximum
-#pragma unroll
-                for (int u = 0; u < BPI; ++u) {
-                    float a0 = fmaxf(z[u][0], z[u][2]), a1 = fmaxf(z[u][1], z[u][3]);
-                    mx0 = fmaxf(mx0, a0);
-                    mx1 = fmaxf(mx1, a1);
-                    ev[u] = nvalid[u] > 0 ? __log2f(sc2[u].y) : 0.f;  // of a power of two; -inf for 0
-                    mo0 = fmaxf(mo0, a0 + ev[u]);
-                    mo1 = fmaxf(mo1, a1 + ev[u]);
-                }
-#pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                    mo0 = fmaxf(mo0, __shfl_xor_sync(0xffffffffu, mo0, o));
-                    mo1 = fmaxf(mo1, __shfl_xor_sync(0xffffffffu, mo1, o));
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < BPI; ++u) {
-                    mx0 = fmaxf(mx0, fmaxf(z[u][0], z[u][2]));
-                    mx1 = fmaxf(mx1, fmaxf(z[u][1], z[u][3]));
-                }
-#pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                }
-            }
-            if (zrow != nullptr && 2 * tig < G) {
-#pragma unroll
-                for (int u = 0; u < BPI; ++u) {
-                    float* zt = zrow + (size_t)(jb + u * kBlock + gid) * G + 2 * tig;
-                    const bool v0 = jb + u * kBlock + gid < ctx, v1 = jb + u * kBlock + gid + 8 < ctx;
-                    if constexpr (G == 1) {
-                        if (v0) zt[0] = z[u][0];
-                        if (v1) zt[8] = z[u][2];
-                    } else {
-                        if (v0) *reinterpret_cast<float2*>(zt) = make_float2(z[u][0], z[u][1]);
-                        if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(z[u][2], z[u][3]);
-                    }
-                }
-            }
-            // A maximum of -inf (nothing but -inf or NaN logits so far) stands for 0: 2^(-inf - 0) is 0.
-            const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
-            const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;
-            float al0 = ex2(m_run[0] - ms0), al1 = ex2(m_run[1] - ms1);
-            m_run[0] = mn0;
-            m_run[1] = mn1;
-            float sum0 = 0.f, sum1 = 0.f;
-            float c0 = 0.f, c1 = 0.f, be0 = 1.f, be1 = 1.f;
-            if constexpr (Q8) {
-                const float os0 = mo0 == -INFINITY ? 0.f : mo0, os1 = mo1 == -INFINITY ? 0.f : mo1;
-                be0 = ex2(m_out[0] - os0);
-                be1 = ex2(m_out[1] - os1);
-                m_out[0] = mo0;
-                m_out[1] = mo1;
-                c0 = kWeightExp - os0;
-                c1 = kWeightExp - os1;
-            } else {
-                be0 = al0;
-                be1 = al1;
-            }
-#pragma unroll
-            for (int u = 0; u < BPI; ++u) {
-                // the sum is of the weights before rounding: the scores divide by it in fp32
-                const float p0 = ex2(z[u][0] - ms0), p1 = ex2(z[u][1] - ms1), p2 = ex2(z[u][2] - ms0), p3 = ex2(z[u][3] - ms1);
-                sum0 += p0 + p2;
-                sum1 += p1 + p3;
-                uint32_t pa, pb;  // tokens gid, gid + 8: rows 2tig, 2tig+1
-                if constexpr (Q8) {
-                    const float e0 = ev[u] + c0, e1 = ev[u] + c1;
-                    pa = M::pack(ex2(z[u][0] + e0), ex2(z[u][1] + e1));
-                    pb = M::pack(ex2(z[u][2] + e0), ex2(z[u][3] + e1));
+                    sc2[u] = make_float2(__shfl_sync(0xffffffffu, s0.x, i & 31), __shfl_sync(0xffffffffu, s0.y, i & 31));
                 } else {
-                    pa = M::pack(p0, p1);
-                    pb = M::pack(p2, p3);
-                }
-                b0f[u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
-                b1f[u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
-            }
-            l_run[0] = fmaf(l_run[0], al0, sum0);
-            l_run[1] = fmaf(l_run[1], al1, sum1);
-            if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {
-#pragma unroll
-                for (int mt = 0; mt < KSTEPS; ++mt) {
-                    acc[mt][0] *= be0;
-                    acc[mt][1] *= be1;
-                    acc[mt][2] *= be0;
-                    acc[mt][3] *= be1;
+                    sc2[u] = make_float2(1.f, 1.f);
                 }
             }
-        } else if (zrow != nullptr) {  // blocks outside the pool: their positions weigh nothing
-            for (int x = lane; x < BPI * kBlock * G; x += 32)
-                if (jb + x / G < ctx) zrow[(size_t)jb * G + x] = -INFINITY;
-        }
-        __syncwarp();  // the K tiles have been read by every lane
-        if (lane == 0 && k + ST < nk) {
-            fence_proxy_async_smem();
-            issue(k + ST, 0, next);
-        }
-        if (!mbar_wait_bounded(&wbars[st * 2 + 1], par)) {
-            if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
-            drain(k + 1, k + ST + 1, 0);  // K tiles of iterations k+1 .. k+ST may be in flight
-            drain(k, k + ST, 1);          // V tiles of iterations k .. k+ST-1
-            break;
-        }
-        // ---- O^T += V^T P^T: this lane's tokens are 2tig, 2tig+1, 2tig+8, 2tig+9 ----
+            if (!mbar_wait_bounded(&wbars[st * 2], par)) {
+                if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
+                drain(k, k + ST, 0);  // K tiles of iterations k .. k+ST-1 may be in flight
+                drain(k, k + ST, 1);  // and their V tiles
+                lost = true;
+                break;
+            }
+            const int jb = (b + local_block(k * BPI)) * kBlock;
+            const uint32_t sK = wstage + (uint32_t)st * S::STAGE;
+            const uint32_t sV = sK + BPI * TILE;
+            int nvalid[BPI];
 #pragma unroll
-        for (int u = 0; u < BPI; ++u) {
-            if (nvalid[u] <= 0) continue;
-            const uint32_t tile = sV + u * TILE;
+            for (int u = 0; u < BPI; ++u) nvalid[u] = (have >> u) & 1 ? min(kBlock, ctx - jb - u * kBlock) : 0;
+            uint32_t b0f[BPI], b1f[BPI];
+            if (have) {
+                // ---- S = K Q^T (16 tokens x 8 rows a block), fp32; two chains hide the instruction's latency ----
+                float z[BPI][4];  // tokens gid (0, 1) and gid + 8 (2, 3) x rows 2tig, 2tig+1
 #pragma unroll
-            for (int pn = 0; pn < S::PANELS; ++pn) {
-                constexpr int WORDS = S::PANB / 32;  // 32-bit words of a row and panel per lane
-                uint32_t w[4][WORDS];
+                for (int u = 0; u < BPI; ++u) {
+                    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int tok = 2 * tig + (j & 1) + 8 * (j >> 1);
-                    if constexpr (WORDS == 4) {
-                        const uint4 x = lds128(tile + S::at(tok, pn * 8 + gid));
-                        w[j][0] = x.x;
-                        w[j][1] = x.y;
-                        w[j][2] = x.z;
-                        w[j][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(tile + S::at(tok, gid >> 1) + (gid & 1) * 8);
-                        w[j][0] = x.x;
-                        w[j][1] = x.y;
-                    }
-                }
-                if (nvalid[u] < kBlock) {  // rows past the context may hold anything
+                    for (int i = 0; i < S::KCH; ++i) {
+                        const int c = S::k_chunk(tig, i);
+                        const uint32_t tile = sK + u * TILE;
+                        const uint4 lo = lds128(tile + S::at(gid, c)), hi = lds128(tile + S::at(gid + 8, c));
+                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+                        if constexpr (Q8) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                            for (int w = 0; w < 4; ++w) {
+                                const uint32_t af[4] = {e4m3x2_to_half2(wl[w]), e4m3x2_to_half2(wh[w]),
+                                                        e4m3x2_to_half2(wl[w] >> 16), e4m3x2_to_half2(wh[w] >> 16)};
+                                M::mma((w & 1) ? sb : sa, af, qb[i * 4 + w][0], qb[i * 4 + w][1]);
+                            }
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < WORDS; ++x)
-                            w[j][x] = 2 * tig + (j & 1) + 8 * (j >> 1) < nvalid[u] ? w[j][x] : 0u;
-                }
-#pragma unroll
-                for (int x = 0; x < WORDS; ++x) {
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t sel = h ? 0x7362u : 0x5140u;  // bytes (t0.d, t1.d, t0.d+1, t1.d+1)
-                            const uint32_t x01 = __byte_perm(w[0][x], w[1][x], sel);
-                            const uint32_t x23 = __byte_perm(w[2][x], w[3][x], sel);
-                            const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
-                                                    e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
-                            M::mma(acc[(pn * WORDS + x) * 2 + h], af, b0f[u], b1f[u]);
+                            for (int w = 0; w < 2; ++w) {
+                                const uint32_t af[4] = {wl[2 * w], wh[2 * w], wl[2 * w + 1], wh[2 * w + 1]};
+                                M::mma(w ? sb : sa, af, qb[i * 2 + w][0], qb[i * 2 + w][1]);
+                            }
                         }
+                    }
+                    const bool v0 = gid < nvalid[u], v1 = gid + 8 < nvalid[u];
+                    const float f0 = zf[0] * sc2[u].x, f1 = zf[1] * sc2[u].x;
+                    z[u][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
+                    z[u][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
+                    z[u][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
+                    z[u][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
+                }
+                // ---- online softmax ----
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+                float ev[BPI], mo0 = m_out[0], mo1 = m_out[1];
+                if constexpr (Q8) {
+                    // the largest z + log2 S_V of the iteration needs each block's own maximum
+#pragma unroll
+                    for (int u = 0; u < BPI; ++u) {
+                        float a0 = fmaxf(z[u][0], z[u][2]), a1 = fmaxf(z[u][1], z[u][3]);
+                        mx0 = fmaxf(mx0, a0);
+                        mx1 = fmaxf(mx1, a1);
+                        ev[u] = nvalid[u] > 0 ? __log2f(sc2[u].y) : 0.f;  // of a power of two; -inf for 0
+                        mo0 = fmaxf(mo0, a0 + ev[u]);
+                        mo1 = fmaxf(mo1, a1 + ev[u]);
+                    }
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                        mo0 = fmaxf(mo0, __shfl_xor_sync(0xffffffffu, mo0, o));
+                        mo1 = fmaxf(mo1, __shfl_xor_sync(0xffffffffu, mo1, o));
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < BPI; ++u) {
+                        mx0 = fmaxf(mx0, fmaxf(z[u][0], z[u][2]));
+                        mx1 = fmaxf(mx1, fmaxf(z[u][1], z[u][3]));
+                    }
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                    }
+                }
+                if (zrow != nullptr && 2 * tig < G) {
+#pragma unroll
+                    for (int u = 0; u < BPI; ++u) {
+                        float* zt = zrow + (size_t)(jb - z0 + u * kBlock + gid) * G + 2 * tig;
+                        const bool v0 = jb + u * kBlock + gid < z_end, v1 = jb + u * kBlock + gid + 8 < z_end;
+                        if constexpr (G == 1) {
+                            if (v0) zt[0] = z[u][0];
+                            if (v1) zt[8] = z[u][2];
+                        } else {
+                            if (v0) *reinterpret_cast<float2*>(zt) = make_float2(z[u][0], z[u][1]);
+                            if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(z[u][2], z[u][3]);
+                        }
+                    }
+                }
+                // A maximum of -inf (nothing but -inf or NaN logits so far) stands for 0: 2^(-inf - 0) is 0.
+                const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
+                const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;
+                float al0 = ex2(m_run[0] - ms0), al1 = ex2(m_run[1] - ms1);
+                m_run[0] = mn0;
+                m_run[1] = mn1;
+                float sum0 = 0.f, sum1 = 0.f;
+                float c0 = 0.f, c1 = 0.f, be0 = 1.f, be1 = 1.f;
+                if constexpr (Q8) {
+                    const float os0 = mo0 == -INFINITY ? 0.f : mo0, os1 = mo1 == -INFINITY ? 0.f : mo1;
+                    be0 = ex2(m_out[0] - os0);
+                    be1 = ex2(m_out[1] - os1);
+                    m_out[0] = mo0;
+                    m_out[1] = mo1;
+                    c0 = kWeightExp - os0;
+                    c1 = kWeightExp - os1;
+                } else {
+                    be0 = al0;
+                    be1 = al1;
+                }
+#pragma unroll
+                for (int u = 0; u < BPI; ++u) {
+                    // the sum is of the weights before rounding: the scores divide by it in fp32
+                    const float p0 = ex2(z[u][0] - ms0), p1 = ex2(z[u][1] - ms1), p2 = ex2(z[u][2] - ms0), p3 = ex2(z[u][3] - ms1);
+                    sum0 += p0 + p2;
+                    sum1 += p1 + p3;
+                    uint32_t pa, pb;  // tokens gid, gid + 8: rows 2tig, 2tig+1
+                    if constexpr (Q8) {
+                        const float e0 = ev[u] + c0, e1 = ev[u] + c1;
+                        pa = M::pack(ex2(z[u][0] + e0), ex2(z[u][1] + e1));
+                        pb = M::pack(ex2(z[u][2] + e0), ex2(z[u][3] + e1));
                     } else {
-                        const uint32_t af[4] = {__byte_perm(w[0][x], w[1][x], 0x5410u), __byte_perm(w[0][x], w[1][x], 0x7632u),
-                                                __byte_perm(w[2][x], w[3][x], 0x5410u), __byte_perm(w[2][x], w[3][x], 0x7632u)};
-                        M::mma(acc[pn * WORDS + x], af, b0f[u], b1f[u]);
+                        pa = M::pack(p0, p1);
+                        pb = M::pack(p2, p3);
+                    }
+                    b0f[u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
+                    b1f[u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
+                }
+                l_run[0] = fmaf(l_run[0], al0, sum0);
+                l_run[1] = fmaf(l_run[1], al1, sum1);
+                if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {
+#pragma unroll
+                    for (int mt = 0; mt < KSTEPS; ++mt) {
+                        acc[mt][0] *= be0;
+                        acc[mt][1] *= be1;
+                        acc[mt][2] *= be0;
+                        acc[mt][3] *= be1;
+                    }
+                }
+            } else if (zrow != nullptr) {  // blocks outside the pool: their positions weigh nothing
+                for (int x = lane; x < BPI * kBlock * G; x += 32)
+                    if (jb + x / G < z_end) zrow[(size_t)(jb - z0) * G + x] = -INFINITY;
+            }
+            __syncwarp();  // the K tiles have been read by every lane
+            if (lane == 0 && k + ST < nk) {
+                fence_proxy_async_smem();
+                issue(k + ST, 0, next);
+            }
+            if (!mbar_wait_bounded(&wbars[st * 2 + 1], par)) {
+                if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
+                drain(k + 1, k + ST + 1, 0);  // K tiles of iterations k+1 .. k+ST may be in flight
+                drain(k, k + ST, 1);          // V tiles of iterations k .. k+ST-1
+                lost = true;
+                break;
+            }
+            // ---- O^T += V^T P^T: this lane's tokens are 2tig, 2tig+1, 2tig+8, 2tig+9 ----
+#pragma unroll
+            for (int u = 0; u < BPI; ++u) {
+                if (nvalid[u] <= 0) continue;
+                const uint32_t tile = sV + u * TILE;
+#pragma unroll
+                for (int pn = 0; pn < S::PANELS; ++pn) {
+                    constexpr int WORDS = S::PANB / 32;  // 32-bit words of a row and panel per lane
+                    uint32_t w[4][WORDS];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int tok = 2 * tig + (j & 1) + 8 * (j >> 1);
+                        if constexpr (WORDS == 4) {
+                            const uint4 x = lds128(tile + S::at(tok, pn * 8 + gid));
+                            w[j][0] = x.x;
+                            w[j][1] = x.y;
+                            w[j][2] = x.z;
+                            w[j][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(tile + S::at(tok, gid >> 1) + (gid & 1) * 8);
+                            w[j][0] = x.x;
+                            w[j][1] = x.y;
+                        }
+                    }
+                    if (nvalid[u] < kBlock) {  // rows past the context may hold anything
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int x = 0; x < WORDS; ++x)
+                                w[j][x] = 2 * tig + (j & 1) + 8 * (j >> 1) < nvalid[u] ? w[j][x] : 0u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < WORDS; ++x) {
+                        if constexpr (Q8) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t sel = h ? 0x7362u : 0x5140u;  // bytes (t0.d, t1.d, t0.d+1, t1.d+1)
+                                const uint32_t x01 = __byte_perm(w[0][x], w[1][x], sel);
+                                const uint32_t x23 = __byte_perm(w[2][x], w[3][x], sel);
+                                const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
+                                                        e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
+                                M::mma(acc[(pn * WORDS + x) * 2 + h], af, b0f[u], b1f[u]);
+                            }
+                        } else {
+                            const uint32_t af[4] = {__byte_perm(w[0][x], w[1][x], 0x5410u), __byte_perm(w[0][x], w[1][x], 0x7632u),
+                                                    __byte_perm(w[2][x], w[3][x], 0x5410u), __byte_perm(w[2][x], w[3][x], 0x7632u)};
+                            M::mma(acc[pn * WORDS + x], af, b0f[u], b1f[u]);
+                        }
                     }
                 }
             }
-        }
-        __syncwarp();  // the V tiles have been read by every lane
-        if (lane == 0 && k + ST < nk) {
-            fence_proxy_async_smem();
-            issue(k + ST, 1, next);
-        }
-    }
-
-    // ---- row sums over the 8 lanes sharing a row; the accumulator in units of 2^m_run ----
-#pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) {
-        l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
-        l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
-    }
-    float fo[2] = {1.f, 1.f};
-    if constexpr (Q8) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) fo[r] = m_out[r] == -INFINITY ? 0.f : exp2f(m_out[r] - kWeightExp - m_run[r]);
-    }
-
-    // ---- merge the warps ----
-    __syncthreads();
-    float* s_acc = reinterpret_cast<float*>(smem);  // [NW][8][D]
-#pragma unroll
-    for (int mt = 0; mt < KSTEPS; ++mt) {
-        constexpr int WORDS = S::PANB / 32;
-        constexpr int PER_PANEL = Q8 ? 2 * WORDS : WORDS;       // m-tiles per panel
-        constexpr int PAN_D = S::PANB / (Q8 ? 1 : 2);           // dims per panel
-        const int d0 = (mt / PER_PANEL) * PAN_D + gid * (2 * PER_PANEL) + 2 * (mt % PER_PANEL);
-        const int r0 = 2 * tig;
-        float* base = s_acc + (size_t)warp * 8 * D;
-        if (r0 < G) *reinterpret_cast<float2*>(base + r0 * D + d0) = make_float2(acc[mt][0] * fo[0], acc[mt][2] * fo[0]);
-        if (r0 + 1 < G)
-            *reinterpret_cast<float2*>(base + (r0 + 1) * D + d0) = make_float2(acc[mt][1] * fo[1], acc[mt][3] * fo[1]);
-    }
-    if (gid == 0) {
-        const int r0 = 2 * tig;
-        s_ml[(warp * 8 + r0) * 2] = m_run[0];
-        s_ml[(warp * 8 + r0) * 2 + 1] = l_run[0];
-        s_ml[(warp * 8 + r0 + 1) * 2] = m_run[1];
-        s_ml[(warp * 8 + r0 + 1) * 2 + 1] = l_run[1];
-    }
-    __syncthreads();
-    float* s_po = reinterpret_cast<float*>(smem + S::MERGE);  // [G][D], then [G][2]: a cluster's partials
-    float* s_pml = s_po + G * D;
-    for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
-        const int r = idx / D;
-        const int d = idx % D;
-        float Mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) Mx = fmaxf(Mx, s_ml[(w * 8 + r) * 2]);
-        float L = 0.f, O = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            // a warp without a finite maximum adds its sum times zero: nothing, or the NaN of its logits
-            const float mw = s_ml[(w * 8 + r) * 2];
-            const float sc = mw == -INFINITY ? 0.f : exp2f(mw - Mx);
-            L = fmaf(s_ml[(w * 8 + r) * 2 + 1], sc, L);
-            O = fmaf(s_acc[((size_t)w * 8 + r) * D + d], sc, O);
-        }
-        const size_t row = (size_t)s * a.n_q + (size_t)g * G + r;
-        if (single) reinterpret_cast<T*>(a.out)[row * D + d] = from_float<T>(L == 0.f ? 0.f : O / L);
-        if (!single && fa.cluster > 1) {
-            s_po[idx] = O;
-            if (d == 0) {
-                s_pml[2 * r] = Mx;
-                s_pml[2 * r + 1] = L;
+            __syncwarp();  // the V tiles have been read by every lane
+            if (lane == 0 && k + ST < nk) {
+                fence_proxy_async_smem();
+                issue(k + ST, 1, next);
             }
         }
-        if ((!single && fa.cluster == 1) || fa.z) {
-            const size_t prow = row * a.n_parts + p;
-            if (!single && fa.cluster == 1) a.part_o[prow * D + d] = O;
-            if (d == 0) {
-                a.part_ml[prow * 2] = Mx;
-                a.part_ml[prow * 2 + 1] = L;
+
+        // ---- row sums over the 8 lanes sharing a row; the accumulator in units of 2^m_run ----
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
+            l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
+        }
+        float fo[2] = {1.f, 1.f};
+        if constexpr (Q8) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) fo[r] = m_out[r] == -INFINITY ? 0.f : exp2f(m_out[r] - kWeightExp - m_run[r]);
+        }
+
+        // ---- join the warps ----
+        __syncthreads();  // the rings have been read
+        float* s_acc = reinterpret_cast<float*>(smem);  // [NW][G][D]
+#pragma unroll
+        for (int mt = 0; mt < KSTEPS; ++mt) {
+            constexpr int WORDS = S::PANB / 32;
+            constexpr int PER_PANEL = Q8 ? 2 * WORDS : WORDS;       // m-tiles per panel
+            constexpr int PAN_D = S::PANB / (Q8 ? 1 : 2);           // dims per panel
+            const int d0 = (mt / PER_PANEL) * PAN_D + gid * (2 * PER_PANEL) + 2 * (mt % PER_PANEL);
+            const int r0 = 2 * tig;
+            float* base = s_acc + (size_t)warp * G * D;
+            if (r0 < G) *reinterpret_cast<float2*>(base + r0 * D + d0) = make_float2(acc[mt][0] * fo[0], acc[mt][2] * fo[0]);
+            if (r0 + 1 < G)
+                *reinterpret_cast<float2*>(base + (r0 + 1) * D + d0) = make_float2(acc[mt][1] * fo[1], acc[mt][3] * fo[1]);
+        }
+        if (gid == 0) {
+            s_ml[warp * 8 + 2 * tig] = make_float2(m_run[0], l_run[0]);
+            s_ml[warp * 8 + 2 * tig + 1] = make_float2(m_run[1], l_run[1]);
+        }
+        __syncthreads();
+        float* s_max = s_join + 8 * NW;
+        float* s_sum = s_max + 8;
+        if (threadIdx.x < G) {
+            const int r = threadIdx.x;
+            float Mx = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) Mx = fmaxf(Mx, s_ml[w * 8 + r].x);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                // a warp without a finite maximum adds its sum times zero: nothing, or the NaN of its logits
+                const float2 u = s_ml[w * 8 + r];
+                const float f = u.x == -INFINITY ? 0.f : ex2(u.x - Mx);
+                s_join[r * NW + w] = f;
+                L = fmaf(u.y, f, L);
+            }
+            s_max[r] = Mx;
+            s_sum[r] = L;
+        }
+        __syncthreads();
+        // partials of this pair: one for each partition, or for each CTA whose run holds a piece of it
+        int np, first = 0;
+        if (fa.partition > 0) {
+            np = (nb + fa.partition - 1) / fa.partition;
+        } else {
+            const long long start = x - b;
+            first = (int)(start / per);
+            np = (int)((start + nb - 1) / per) - first + 1;
+        }
+        const int slot = partial_slot(first, (int)blockIdx.x - first);
+        float* s_po = reinterpret_cast<float*>(smem + S::MERGE);  // [G][D], then [G][2]: a cluster's partials
+        float* s_pml = s_po + G * D;
+        for (int i4 = threadIdx.x; i4 < G * D / 4; i4 += NW * 32) {
+            const int r = i4 / (D / 4);
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = s_join[r * NW + w];
+                const float4 v = reinterpret_cast<const float4*>(s_acc + (size_t)w * G * D)[i4];
+                O.x = fmaf(v.x, f, O.x);
+                O.y = fmaf(v.y, f, O.y);
+                O.z = fmaf(v.z, f, O.z);
+                O.w = fmaf(v.w, f, O.w);
+            }
+            if (np == 1) {
+                const float L = s_sum[r];
+                store4(reinterpret_cast<T*>(a.out) + row0 * D + 4 * i4, O, L == 0.f ? 0.f : 1.f / L);
+            } else if (fa.partition > 0) {
+                reinterpret_cast<float4*>(s_po)[i4] = O;
+            } else {
+                reinterpret_cast<float4*>(a.part_o + (size_t)slot * G * D)[i4] = O;
             }
         }
+        if (threadIdx.x < G) {
+            const float2 u = make_float2(s_max[threadIdx.x], s_sum[threadIdx.x]);
+            if (np == 1) {
+                if (fa.row_ml) fa.row_ml[row0 + threadIdx.x] = u;
+            } else if (fa.partition > 0) {
+                reinterpret_cast<float2*>(s_pml)[threadIdx.x] = u;
+            } else {
+                reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * G + threadIdx.x] = u;
+            }
+        }
+        if (fa.partition > 0) {
+            if (np > 1)
+                cluster_join<T, D, G, NW * 32>(reinterpret_cast<T*>(a.out) + row0 * D, (int)blockIdx.x, np, s_pml, s_po,
+                                               fa.scores ? s_max : nullptr, s_sum);
+            if (fa.scores) {  // weights of the partition's own positions (the barriers above order the logits)
+                float* to = fa.scores + ((size_t)s * a.n_kv + g) * fa.score_stride + z0;
+                for (int j = threadIdx.x; j < z_end - z0; j += NW * 32) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int r = 0; r < G; ++r) {
+                        const float M = s_max[r], L = s_sum[r];
+                        w += ex2(zrow[j * G + r] - (M == -INFINITY ? 0.f : M)) * (L == 0.f ? 0.f : 1.f / L);
+                    }
+                    to[j] += w;
+                }
+            }
+            return;
+        }
+        if (np > 1) join_if_last<T, D, G, NW * 32>(fa, row0, first, np, reinterpret_cast<float*>(smem + S::MERGE));
+        x += nblk + kPairCost<Q8>;  // the next pair's first block
+        if (x >= x_end) return;
+        // the next pair of the run
+        done += nk;
+        b = 0;
+        s = s_next;
+        g = g_next;
+        ctx = ctx_next;
+        if (__syncthreads_or(lost)) return;  // flagged: the ring's phases no longer match; the scratch has been read
+        fence_proxy_async_smem();            // before the copies that overwrite it
     }
-    if (!single && fa.cluster > 1)
-        cluster_merge<T, D, G, NW * 32>(reinterpret_cast<T*>(a.out) + ((size_t)s * a.n_q + (size_t)g * G) * D, p,
-                                        (nb + a.bpp - 1) / a.bpp, s_pml, s_po);
-    else if (!single)
-        frag_merge_if_last<T, D, G, NW * 32>(a, s, g, (nb + a.bpp - 1) / a.bpp,
-                                             reinterpret_cast<float*>(smem + S::MERGE));
 }
 
 template <typename T, bool Q8, int D, int G>
 struct FragKernel {
+    // Blocks per iteration, CTAs per SM: 64 to 128 KiB of tiles in flight an SM. More is slower (d = 128
+    // codes, 10 x 30,000 tokens, 8 x 4 heads: 64 KiB 105 us, 96 KiB 99, 128 KiB 103, 192 KiB 115).
     static constexpr int NW = 4;
-    static constexpr int BPI = Q8 ? 2 : 1;
-    static constexpr int CTAS = 3;
-    // 64 KiB of tiles per CTA
-    static constexpr int ST = 64 * 1024 / (NW * 2 * BPI * kBlock * D * (Q8 ? 1 : 2));
-    static constexpr size_t smem = FragGeom<Q8, D, NW, ST, BPI>::ALLOC;
+    static constexpr int ST = 1;
+    static constexpr int BPI = Q8 && D == 64 ? 4 : !Q8 && D == 256 ? 1 : 2;
+    static constexpr int CTAS = D == 256 ? 2 : !Q8 || D == 128 ? 3 : 4;
+    static constexpr size_t smem = FragGeom<Q8, D, G, NW, ST, BPI>::ALLOC;
     static unsigned long long attr_done;
     static int resident[64];
     static constexpr auto kernel = frag_decode_kernel<T, Q8, D, G, NW, ST, BPI, CTAS>;
-    static cudaError_t prepare() { return allow_dynamic_smem(kernel, smem, &attr_done); }
+    static cudaError_t prepare() { return allow_dynamic_smem(kernel, smem + kMaxPartition * kBlock * G * sizeof(float), &attr_done); }
     // CTAs one SM of the current device holds at once; asked of the occupancy calculator once per device
     static cudaError_t ctas_per_sm(int* out) {
         int dev = 0;
@@ -819,7 +1031,9 @@ struct FragKernel {
     static cudaError_t launch(const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
         cudaError_t err = prepare();
         if (err != cudaSuccess) return err;
-        return launch_dependent(kernel, dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs), NW * 32, smem, stream, a.cluster, a, tk, tv);
+        const dim3 grid = a.partition > 0 ? dim3(a.d.n_parts, a.d.n_kv, a.d.n_seqs) : dim3(a.d.n_parts);
+        const size_t logits = a.partition > 0 && a.scores ? (size_t)a.partition * kBlock * G * sizeof(float) : 0;
+        return launch_dependent(kernel, grid, NW * 32, smem + logits, stream, a.partition > 0 ? a.d.n_parts : 1, a, tk, tv);
     }
 };
 template <typename T, bool Q8, int D, int G>

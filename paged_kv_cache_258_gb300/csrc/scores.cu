@@ -2,8 +2,7 @@
 // running sums (sm_103a).
 //
 //   scores[s][g][j] += sum_{h in group g} 2^(z_hj - m_h) / l_h,   j < len_s,
-// m_h and l_h the row's final maximum and sum, joined here from the partitions' pairs. A position's
-// weight needs them, and they exist only when the whole row has been read, so this is a launch of its
+// m_h and l_h the row's maximum and sum. A position's weight needs them, and they exist only when the whole row has been read, so this is a launch of its
 // own, a programmatic dependent of the attention: its CTAs are resident and wait when the last
 // attention CTA ends. It reads 4 G bytes and reads and writes 4 bytes a token and head (the logits of
 // moderate batches still lie in L2). Sums are fp32; every score is written by one thread and heads are
@@ -49,26 +48,10 @@ __global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a)
     const int ctx = min(max(a.lens[s], 0), cap);
     const int j0 = blockIdx.x * kThreads * kPerThread;
     if (j0 >= ctx) return;
-    const int nb = (ctx + kBlock - 1) / kBlock;
-    const int np = (nb + a.bpp - 1) / a.bpp;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp < G) {
-        const size_t row = ((size_t)s * a.n_kv + g) * G + warp;
-        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.n_parts;
-        float m = -INFINITY, l = 0.f;
-        for (int q = lane; q < np; q += 32) m = fmaxf(m, __ldcg(ml + q).x);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        for (int q = lane; q < np; q += 32) {
-            const float2 u = __ldcg(ml + q);
-            l += u.y * (u.x == -INFINITY ? 0.f : exp2f(u.x - m));
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) {
-            s_m[warp] = m == -INFINITY ? 0.f : m;
-            s_inv[warp] = l == 0.f ? 0.f : 1.f / l;
-        }
+    if (threadIdx.x < G) {
+        const float2 u = __ldcg(a.row_ml + ((size_t)s * a.n_kv + g) * G + threadIdx.x);
+        s_m[threadIdx.x] = u.x == -INFINITY ? 0.f : u.x;
+        s_inv[threadIdx.x] = u.y == 0.f ? 0.f : 1.f / u.y;
     }
     __syncthreads();
     const size_t base = ((size_t)s * a.n_kv + g);

@@ -19,24 +19,36 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 // multiple of its least step (fp16: 2^-24).
 inline int q8_min_exp(int dtype) { return dtype == PKV_F16 ? -15 : -117; }
 
-// One decode launch over an 8-bit pool, or over a 16-bit pool with its weights summed. Inside `d`
-// k_layer / v_layer are codes for an 8-bit pool.
+// Least blocks of a CTA's run (one iteration of each of its warps), and arrival counters of a workspace
+// (one for each CTA of the widest launch).
+constexpr int kMinRun = 8;
+constexpr int kMaxRuns = 2048;
+// Most blocks of a partition in a grid of partitions (its logits stay in shared memory).
+constexpr int kMaxPartition = 32;
+
+// One decode launch over an 8-bit pool, or over a 16-bit pool with its weights summed. Inside `d`:
+// k_layer / v_layer are codes for an 8-bit pool; n_parts = CTAs along x; part_o [n_parts][2][G][D] and
+// part_ml [n_parts][2][G] (max, sum) are the runs' partials; dense, counters, call_tag and bpp are unused.
 struct FragArgs {
     DecodeArgs d;
     const float* k_scales = nullptr;  // [num_blocks][n_kv] of this layer (8-bit pools)
     const float* v_scales = nullptr;
-    int cluster = 1;                  // CTAs of a cluster: n_parts where the partials are joined through shared memory
-    float* z = nullptr;               // [n_seqs][n_kv][max_blocks*16][G] base-2 logits, or null: weights not summed
+    unsigned int* arrivals = nullptr; // [n_parts], zero between calls
+    float2* row_ml = nullptr;         // [n_seqs][n_q] each row's (max, sum), or null: weights not summed
+    float* z = nullptr;               // [n_seqs][n_kv][max_blocks*16][G] base-2 logits, or null
+    float* scores = nullptr;          // partitions: [n_seqs][n_kv][score_stride], or null
+    long long score_stride = 0;
+    int partition = 0;                // > 0: a grid of partitions of so many blocks, n_parts a cluster; 0: runs
 };
 
-// scores[s][g][j] += sum over the group's heads of 2^(z - lse), j < the sequence's length.
+// scores[s][g][j] += sum over the group's heads of 2^(z - max) / sum, j < the sequence's length.
 struct ScoreArgs {
     const float* z;
-    const float* part_ml;  // [n_seqs][n_q][n_parts][2]
+    const float2* row_ml;  // [n_seqs][n_q]
     const int32_t* lens;
     float* scores;         // [n_seqs][n_kv][stride]
     long long stride;
-    int n_seqs, n_kv, group, max_blocks, n_parts, bpp;
+    int n_seqs, n_kv, group, max_blocks;
 };
 
 struct Q8AppendArgs {

@@ -625,7 +625,7 @@ def _table_width(block_tables) -> int:
 
 def _bytes_tensor(n: int, device):
     t = _torch()
-    return t.empty(-(-n // 16) * 4, dtype=t.float32, device=device) if n else None
+    return t.zeros(-(-n // 16) * 4, dtype=t.float32, device=device) if n else None
 
 
 def pkv_q8_pool_bytes(desc: CacheDesc) -> int:

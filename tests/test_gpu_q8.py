@@ -11,6 +11,7 @@ from paged_kv_cache_258_gb300 import workloads as W
 
 pytestmark = pytest.mark.gpu
 BLOCK = 16
+COUNTERS = 2048  # words at the front of a decode workspace that are zero between calls
 
 
 def codes_to_torch(c):
@@ -182,7 +183,7 @@ def run_decode(desc, t, scale, scores=None, stream=None, ws=True):
     out = torch.full_like(t["q"], float("nan"))
     w = pkv.alloc_q8_workspace(desc, t["q"].shape[0], t["tables"].shape[1], scored=scores is not None) if ws else None
     if w is not None:
-        w.fill_(float("nan"))
+        w[COUNTERS:].fill_(float("nan"))
     pkv.pkv_q8_decode_attention(desc, 0, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"], scale, out, w,
                                 scores=scores, stream=stream)
     return out
