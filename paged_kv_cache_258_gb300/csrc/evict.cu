@@ -6,19 +6,21 @@
 // positions 0 .. k-1 of the destination table, their scores with them; scores in [k, c) become 0.
 // Heads and layers choose for themselves: a table is shared by all of them, but each has its own rows.
 //
-// Two launches. Both are bound by memory when they have enough (sequence, head, layer) triples, the
-// second by far the larger: 2 k row bytes each way against 8 c + 4 k of the first.
-//  1. select: one CTA per triple. The (k - R)-th largest score is found by a radix select over the
-//     scores' ordered bits (11 + 11 + 10 bits, histograms in shared memory), then one ordered sweep
-//     numbers the kept positions with a block-wide scan and writes them and their scores. The sweep may
-//     run in place: it writes index i only after every score up to that position has been read, and the
-//     i-th kept position is never below i.
+// Two launches; the second moves 2 k row bytes each way for K and V against 8 c + 4 k bytes of the first.
+//  1. select: one CTA per triple. A thread holds up to 16 scores as ordered integers in registers (all
+//     its loads in flight at once); a radix select over 11 + 11 + 10 bits, with histograms in shared
+//     memory, finds the (k - R)-th largest. Then every warp counts what it keeps of its consecutive
+//     positions, a scan over the warps numbers them, and ballots place each one. The scores are rebuilt
+//     from the registers, so they may move in place: what is written at index i was read, as were all
+//     scores up to the i-th kept position, which is never below i. Contexts longer than the CTA's
+//     registers go by in pieces, in order.
 //     For 8-bit pools it also reads the old scales of all the sequence's blocks aside and writes each
 //     destination block's new scale, the largest among its rows' (a power of two like them, so the
 //     codes only shift).
 //  2. move: CTAs own column slices of a triple's rows, so two CTAs never touch the same bytes and a
-//     sequence can be compacted in place without any order between CTAs. A CTA walks the kept list in
-//     chunks; the loads of a chunk are all done before its stores (a barrier). Row i of chunk n is read
+//     sequence can be compacted in place without any order between CTAs. A CTA works out the places of
+//     kIndex kept rows at a time in shared memory, then walks them in chunks with the next chunk's loads
+//     in flight: a chunk's stores follow a barrier behind all its loads, and row i of a chunk is read
 //     from a position >= i, so loads of later chunks never see an earlier chunk's stores.
 #include <math.h>
 
@@ -28,46 +30,28 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kKeys = 16;  // scores of a thread
 
-// Scores as integers in the same order; NaN above everything, -0 equal to 0.
+// Scores as integers in the same order; NaN above everything, -0 equal to 0. And back (NaN to a NaN).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0xffffffffu;
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-
-// Exclusive sums of two counts packed as (a in the low, b in the high half) over the CTA; *total gets
-// the whole sum. Counts stay below 2^16.
-__device__ __forceinline__ uint32_t scan2(uint32_t v, uint32_t* s_warp, uint32_t* total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();  // the previous scan's reads are done
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        const uint32_t y = s_warp[w];
-        if (w < warp) before += y;
-        all += y;
-    }
-    *total = all;
-    return before + x - v;
+__device__ __forceinline__ float key_score(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+template <int NT>
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
+    constexpr int NW = NT / 32;
     __shared__ uint32_t s_hist[kBins];
-    __shared__ uint32_t s_warp[kSelThreads / 32];
+    __shared__ uint32_t s_warp[NW], s_warp2[NW];
     __shared__ uint32_t s_pick[2];
     const long long pair = blockIdx.x;  // s * n_kv + g
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cap = a.max_blocks * kBlock;
     grid_launch_dependents();
     grid_dependency_wait();
@@ -86,6 +70,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     float* out = a.new_scores + triple * a.stride;
     int32_t* kept = a.kept + triple * a.max_keep;
 
+    // Positions go by in pieces of NT * rounds; warp w holds `rounds` * 32 consecutive ones.
+    const int rounds = min(kKeys, (c + NT - 1) / NT);
+    const int piece = NT * rounds;
+    const int pieces = c > 0 ? (c + piece - 1) / piece : 0;
+    uint32_t key[kKeys];
+    auto at = [&](int p, int r) -> int { return p * piece + (warp * rounds + r) * 32 + lane; };
+    auto load = [&](int p) {
+        float x[kKeys];
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r)
+            if (r < rounds) x[r] = at(p, r) < c ? score[at(p, r)] : 0.f;
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r)
+            if (r < rounds) key[r] = order_key(x[r]);
+    };
+    if (pieces == 1) load(0);
+
     // threshold: positions above it are kept, of those equal to it the first `ties`
     uint32_t threshold = 0xffffffffu, ties = 0;
     if (pick == older) {
@@ -97,31 +98,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const int bits = pass == 2 ? 10 : 11;
-            for (int i = threadIdx.x; i < kBins; i += kSelThreads) s_hist[i] = 0;
+            for (int i = threadIdx.x; i < kBins; i += NT) s_hist[i] = 0;
             __syncthreads();
-            for (int j = threadIdx.x; j < older; j += kSelThreads) {
-                const uint32_t key = order_key(score[j]);
-                if ((key & mask) == prefix) atomicAdd(&s_hist[(key >> shift) & ((1u << bits) - 1)], 1u);
+            for (int p = 0; p < pieces; ++p) {
+                if (pieces > 1) load(p);
+#pragma unroll
+                for (int r = 0; r < kKeys; ++r)
+                    if (r < rounds && at(p, r) < older && (key[r] & mask) == prefix)
+                        atomicAdd(&s_hist[(key[r] >> shift) & ((1u << bits) - 1)], 1u);
             }
             __syncthreads();
-            // bins from the top: thread t sums bins (kBins-1-4t .. kBins-4-4t)
-            constexpr int PER = kBins / kSelThreads;
+            // thread t takes PER bins from the top: the scan counts what lies above them
+            constexpr int PER = kBins / NT;
             uint32_t mine = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) mine += s_hist[kBins - 1 - (threadIdx.x * PER + i)];
             uint32_t above = mine;
-            {
-                const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
-                    if (lane >= o) above += y;
-                }
-                if (lane == 31) s_warp[warp] = above;
-                __syncthreads();
-                for (int w = 0; w < warp; ++w) above += s_warp[w];
-                above -= mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
+                if (lane >= o) above += y;
             }
+            if (lane == 31) s_warp[warp] = above;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                if (w < warp) above += s_warp[w];
+            above -= mine;
             if (above < left && above + mine >= left) {  // the bin that holds the left-th largest is here
                 uint32_t n = above;
                 for (int i = 0; i < PER; ++i) {
@@ -139,38 +142,60 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             prefix |= s_pick[0] << shift;
             mask |= ((1u << bits) - 1) << shift;
             left = s_pick[1];
-            __syncthreads();
         }
         threshold = prefix;
         ties = left;
     }
 
-    // ordered sweep: number the kept positions, move their scores
-    uint32_t n_above = 0, n_equal = 0;  // kept above the threshold and equal to it, so far
-    for (int j0 = 0; j0 < c; j0 += kSelThreads) {
-        const int j = j0 + threadIdx.x;
-        float x = 0.f;
+    uint32_t n_above = 0, n_equal = 0;  // positions above the threshold and equal to it, in earlier pieces
+    for (int p = 0; p < pieces; ++p) {
+        if (pieces > 1) load(p);
+        // positions of the recent window count as above
+        auto above_of = [&](int r) -> bool { return r < rounds && at(p, r) < c && (at(p, r) >= older || key[r] > threshold); };
+        auto equal_of = [&](int r) -> bool { return r < rounds && at(p, r) < older && key[r] == threshold; };
         uint32_t above = 0, equal = 0;
-        if (j < c) {
-            x = score[j];
-            const uint32_t key = order_key(x);
-            if (j >= older) above = 1;
-            else if (key > threshold) above = 1;
-            else if (key == threshold) equal = 1;
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r) {
+            if (r < rounds) {
+                above += __popc(__ballot_sync(0xffffffffu, above_of(r)));
+                equal += __popc(__ballot_sync(0xffffffffu, equal_of(r)));
+            }
         }
-        uint32_t total;
-        const uint32_t at = scan2(above | (equal << 16), s_warp, &total);  // its barriers end the reads of this chunk
-        const uint32_t eq_before = n_equal + (at >> 16), ab_before = n_above + (at & 0xffffu);
-        if (above || (equal && eq_before < ties)) {
-            const uint32_t i = ab_before + min(eq_before, ties);
-            kept[i] = j;
-            out[i] = x;
+        __syncthreads();  // the piece's scores are read by all; the counts of the last piece are consumed
+        if (lane == 0) {
+            s_warp[warp] = above;
+            s_warp2[warp] = equal;
         }
-        n_above += total & 0xffffu;
-        n_equal += total >> 16;
+        __syncthreads();
+        uint32_t ab = n_above, eq = n_equal;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) {
+                ab += s_warp[w];
+                eq += s_warp2[w];
+            }
+            n_above += s_warp[w];
+            n_equal += s_warp2[w];
+        }
+        const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r) {
+            if (r < rounds) {
+                const bool is_above = above_of(r), is_equal = equal_of(r);
+                const uint32_t ba = __ballot_sync(0xffffffffu, is_above), be = __ballot_sync(0xffffffffu, is_equal);
+                const uint32_t eq_before = eq + __popc(be & below);
+                if (is_above || (is_equal && eq_before < ties)) {
+                    const uint32_t i = ab + __popc(ba & below) + min(eq_before, ties);
+                    kept[i] = at(p, r);
+                    out[i] = key_score(key[r]);
+                }
+                ab += __popc(ba);
+                eq += __popc(be);
+            }
+        }
     }
     __syncthreads();
-    for (int j = k + threadIdx.x; j < c; j += kSelThreads) out[j] = 0.f;
+    for (int j = k + threadIdx.x; j < c; j += NT) out[j] = 0.f;
 
     if (a.k_scales != nullptr) {
         const int nb = (c + kBlock - 1) / kBlock, kb = (k + kBlock - 1) / kBlock;
@@ -181,24 +206,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         float* old_v = a.old_scales + (triples + triple) * a.max_blocks;
         float* ks = a.k_scales + (size_t)layer * a.num_blocks * a.n_kv + g;
         float* vs = a.v_scales + (size_t)layer * a.num_blocks * a.n_kv + g;
-        for (int b = threadIdx.x; b < nb; b += kSelThreads) {
+        for (int b = threadIdx.x; b < nb; b += NT) {
             const int phys = src[b];
             const bool ok = (unsigned)phys < (unsigned)a.num_blocks;
             old_k[b] = ok ? ks[(size_t)phys * a.n_kv] : 0.f;
             old_v[b] = ok ? vs[(size_t)phys * a.n_kv] : 0.f;
         }
         __syncthreads();  // the old scales are read, the kept list is written
-        for (int b = threadIdx.x; b < kb; b += kSelThreads) {
-            const int phys = dst[b];
-            if ((unsigned)phys >= (unsigned)a.num_blocks) continue;
+        for (int b = warp * 2 + (lane >> 4); b < (kb + 1) / 2 * 2; b += 2 * NW) {  // half a warp a block
+            const int i = b * kBlock + (lane & 15);
             float mk = 0.f, mv = 0.f;
-            for (int i = b * kBlock; i < min(k, (b + 1) * kBlock); ++i) {
+            if (i < k) {
                 const int sb = kept[i] / kBlock;
-                mk = fmaxf(mk, old_k[sb]);
-                mv = fmaxf(mv, old_v[sb]);
+                mk = old_k[sb];
+                mv = old_v[sb];
             }
-            ks[(size_t)phys * a.n_kv] = mk;
-            vs[(size_t)phys * a.n_kv] = mv;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) {
+                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            }
+            if ((lane & 15) == 0 && b < kb) {
+                const int phys = dst[b];
+                if ((unsigned)phys < (unsigned)a.num_blocks) {
+                    ks[(size_t)phys * a.n_kv] = mk;
+                    vs[(size_t)phys * a.n_kv] = mv;
+                }
+            }
         }
     }
 }
@@ -223,11 +257,14 @@ __device__ __forceinline__ uint4 rescale16(uint4 c, float f) {
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kIndex = 512;  // kept rows whose places are worked out at a time
 
 // grid ((sequence, head) x slices, layer, K/V)
 template <bool Q8>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a) {
     constexpr int U = 4;  // rows of a thread per chunk
+    __shared__ long long s_from[kIndex], s_to[kIndex];  // row numbers in the layer; s_to < 0: stays where it is
+    __shared__ float s_f[Q8 ? kIndex : 1];              // what the row's codes are multiplied with
     const long long pair = blockIdx.x / a.slices;
     const int slice = (int)(blockIdx.x % a.slices);
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
@@ -240,7 +277,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int lanes = a.row_bytes / a.slices / 16;  // threads that share a row
     const int rows = kMoveThreads / lanes;          // rows the CTA covers at once
     const int sub = threadIdx.x / lanes;
-    const size_t col = (size_t)slice * lanes * 16 + (threadIdx.x % lanes) * 16;
     const size_t triple = (size_t)layer * a.n_seqs * a.n_kv + pair;
     const size_t triples = (size_t)a.n_layers * a.n_seqs * a.n_kv;
     const int32_t* kept = a.kept + triple * a.max_keep;
@@ -248,42 +284,92 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int32_t* dst = a.dst + (size_t)s * a.max_blocks;
     const bool is_v = blockIdx.z != 0;
     const size_t layer_rows = (size_t)a.num_blocks * a.n_kv * kBlock;
-    char* pool = reinterpret_cast<char*>(is_v ? a.v_pool : a.k_pool) + (size_t)layer * layer_rows * a.row_bytes;
+    char* pool = reinterpret_cast<char*>(is_v ? a.v_pool : a.k_pool) + (size_t)layer * layer_rows * a.row_bytes +
+                 (size_t)slice * lanes * 16 + (threadIdx.x % lanes) * 16;
     const float* old_scale = Q8 ? a.old_scales + ((is_v ? triples : 0) + triple) * a.max_blocks : nullptr;
     const float* new_scale = Q8 ? (is_v ? a.v_scales : a.k_scales) + (size_t)layer * a.num_blocks * a.n_kv + g : nullptr;
 
-    for (int i0 = 0; i0 < k; i0 += rows * U) {
-        uint4 x[U];
-        char* to[U];
-        float f[U];
+    // The places of the next kIndex rows are on their way while these are moved: first the positions,
+    // one step ahead the blocks (and scales) they lie in.
+    constexpr int PER = kIndex / kMoveThreads;
+    int j_next[PER], ps[PER], pd[PER];
+    float so[PER], sn[PER];
+    auto fetch_kept = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * rows + sub;
-            to[u] = nullptr;
-            if (i < k) {
-                const int j = kept[i];
-                const int ps = src[j / kBlock], pd = dst[i / kBlock];
-                if ((unsigned)ps >= (unsigned)a.num_blocks || (unsigned)pd >= (unsigned)a.num_blocks) {
-                    atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
-                } else {
-                    f[u] = 1.f;
-                    if (Q8) {
-                        const float o = old_scale[j / kBlock], n = new_scale[(size_t)pd * a.n_kv];
-                        f[u] = o == n ? 1.f : o / n;
-                    }
-                    const size_t from_row = ((size_t)ps * a.n_kv + g) * kBlock + j % kBlock;
-                    const size_t to_row = ((size_t)pd * a.n_kv + g) * kBlock + i % kBlock;
-                    if (from_row != to_row || f[u] != 1.f) {
-                        to[u] = pool + to_row * a.row_bytes + col;
-                        x[u] = *reinterpret_cast<const uint4*>(pool + from_row * a.row_bytes + col);
-                    }
-                }
+        for (int t = 0; t < PER; ++t) {
+            const int i = i0 + t * kMoveThreads + threadIdx.x;
+            j_next[t] = i < k ? kept[i] : 0;
+        }
+    };
+    auto fetch_blocks = [&](int i0) {
+#pragma unroll
+        for (int t = 0; t < PER; ++t) {
+            const int i = i0 + t * kMoveThreads + threadIdx.x;
+            ps[t] = i < k ? src[j_next[t] / kBlock] : 0;
+            pd[t] = i < k ? dst[i / kBlock] : 0;
+        }
+        if (Q8) {
+#pragma unroll
+            for (int t = 0; t < PER; ++t) {
+                const int i = i0 + t * kMoveThreads + threadIdx.x;
+                so[t] = i < k ? old_scale[j_next[t] / kBlock] : 0.f;
+                sn[t] = i < k && (unsigned)pd[t] < (unsigned)a.num_blocks ? new_scale[(size_t)pd[t] * a.n_kv] : 0.f;
             }
         }
-        __syncthreads();  // the chunk's rows are in registers before any of its places is written
+    };
+    fetch_kept(0);
+    fetch_blocks(0);
+    for (int i0 = 0; i0 < k; i0 += kIndex) {
+        const int n = min(kIndex, k - i0);
+        __syncthreads();  // the last index has been read
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (to[u]) *reinterpret_cast<uint4*>(to[u]) = Q8 && f[u] != 1.f ? rescale16(x[u], f[u]) : x[u];
+        for (int t = 0; t < PER; ++t) {
+            const int e = t * kMoveThreads + threadIdx.x, i = i0 + e;
+            long long from = 0, to = -1;
+            float f = 1.f;
+            if (i < k) {
+                if ((unsigned)ps[t] >= (unsigned)a.num_blocks || (unsigned)pd[t] >= (unsigned)a.num_blocks) {
+                    atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
+                } else {
+                    if (Q8) f = so[t] == sn[t] ? 1.f : so[t] / sn[t];
+                    from = ((long long)ps[t] * a.n_kv + g) * kBlock + j_next[t] % kBlock;
+                    to = ((long long)pd[t] * a.n_kv + g) * kBlock + i % kBlock;
+                    if (from == to && f == 1.f) to = -1;
+                }
+            }
+            s_from[e] = from;
+            s_to[e] = to;
+            if (Q8) s_f[e] = f;
+        }
+        __syncthreads();
+        fetch_kept(i0 + kIndex);
+        uint4 x[2][U];
+        auto load = [&](int e0, uint4* v) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + u * rows + sub;
+                if (e < n && s_to[e] >= 0) v[u] = *reinterpret_cast<const uint4*>(pool + (size_t)s_from[e] * a.row_bytes);
+            }
+        };
+        auto store = [&](int e0, const uint4* v) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + u * rows + sub;
+                if (e < n && s_to[e] >= 0)
+                    *reinterpret_cast<uint4*>(pool + (size_t)s_to[e] * a.row_bytes) =
+                        Q8 && s_f[e] != 1.f ? rescale16(v[u], s_f[e]) : v[u];
+            }
+        };
+        const int chunk = rows * U;
+        load(0, x[0]);
+        for (int e0 = 0; e0 < n; e0 += 2 * chunk) {
+            load(e0 + chunk, x[1]);
+            if (e0 == 0) fetch_blocks(i0 + kIndex);  // the positions have arrived
+            __syncthreads();  // all of this chunk is in registers before any of its places is written
+            store(e0, x[0]);
+            load(e0 + 2 * chunk, x[0]);
+            __syncthreads();
+            store(e0 + chunk, x[1]);
         }
     }
 }
@@ -292,7 +378,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
     const unsigned pairs = (unsigned)a.n_seqs * (unsigned)a.n_kv;
-    cudaError_t err = launch_dependent(evict_select_kernel, dim3(pairs, a.n_layers), kSelThreads, 0, stream, 1, a);
+    // the fewest threads whose registers hold a context: more CTAs an SM, cheaper barriers
+    const int cap = a.max_blocks * kBlock;
+    cudaError_t err = cap <= 256 * kKeys
+                          ? launch_dependent(evict_select_kernel<256>, dim3(pairs, a.n_layers), 256, 0, stream, 1, a)
+                      : cap <= 512 * kKeys
+                          ? launch_dependent(evict_select_kernel<512>, dim3(pairs, a.n_layers), 512, 0, stream, 1, a)
+                          : launch_dependent(evict_select_kernel<1024>, dim3(pairs, a.n_layers), 1024, 0, stream, 1, a);
     if (err != cudaSuccess) return err;
     const dim3 grid(pairs * (unsigned)a.slices, a.n_layers, 2);
     return launch_dependent(a.k_scales ? evict_move_kernel<true> : evict_move_kernel<false>, grid, kMoveThreads, 0, stream, 1, a);

@@ -7,12 +7,14 @@
 // codes -- codes are rounded again only where they fall below 2^-6. The scale is the least that lets the
 // largest finite element of the block in.
 //
-// Append (one launch, a few bytes of arithmetic a byte): a block's scale is raised once for all the
-// call's rows in it, so one warp handles a (block, KV head, K or V): the warp of the block's first token
-// in the call. It reads slots[t-31 .. t+31], leaves if an earlier one lies in its block, and gathers the
-// later ones by ballot. A block is started when a row at offset 0 arrives: its old scale, the previous
-// owner's, is forgotten. Otherwise S' = max(S, what the new rows need) and, if that grew, the other rows
-// are brought to S'.
+// Append: a block's scale is raised once for all the call's rows in it, so somebody has to see these rows
+// together. A CTA takes a window of 16 tokens, one KV head and K or V, and the runs that start there: a
+// token whose block none of the 31 before it lies in starts a run, the tokens of that block up to 31
+// later belong to it. Each warp reads whole rows (all of a CTA's rows are in flight at once), the
+// largest elements meet in shared memory, and the warps write their rows as codes of the run's scale.
+// A block is started when a row at offset 0 arrives: its old scale, the previous owner's, is forgotten.
+// Otherwise S' = max(S, what the new rows need) and, if that grew, the other rows are brought to S'.
+// Bound by latency in a decode step (three dependent trips to memory), by bytes in a long chunk.
 #include <math.h>
 
 #include "common.cuh"
@@ -47,101 +49,172 @@ __device__ __forceinline__ int scale_exp(float amax, int min_exp) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// codes * f for the eight codes of two words, back to codes.
-__device__ __forceinline__ uint2 rescale8(uint2 c, float f) {
-    uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 a = from_e4m3x2(w[i]), b = from_e4m3x2(w[i] >> 16);
-        w[i] = to_e4m3x2(a.x * f, a.y * f) | (to_e4m3x2(b.x * f, b.y * f) << 16);
-    }
-    return make_uint2(w[0], w[1]);
-}
-
+constexpr int kWindow = 16;                  // tokens whose runs a CTA looks for
+constexpr int kReach = 31;                   // how far behind its first token a run may end
+constexpr int kSeen = kWindow + kReach;      // tokens that may belong to a CTA's runs
 constexpr int kAppendWarps = 8;
 
-// One warp per (token, KV head, K or V); warps of tokens that are not their block's first leave.
+// EPL elements of a lane, as loaded.
+template <int EPL>
+struct Piece;
+template <>
+struct Piece<2> {
+    using raw = uint32_t;
+    using codes = uint16_t;
+};
+template <>
+struct Piece<4> {
+    using raw = uint2;
+    using codes = uint32_t;
+};
+template <>
+struct Piece<8> {
+    using raw = uint4;
+    using codes = uint2;
+};
+
+template <typename T>
+__device__ __forceinline__ void widen_word(uint32_t w, float* f) {
+    Vec16<T>::word(w, f);
+}
+
+// grid: (window, KV head, K or V)
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8AppendArgs a) {
-    constexpr int NCH = D / 8;          // 8-element pieces of a row
-    constexpr int RPP = 32 / NCH;       // rows a warp covers at once (1, 2, 4)
-    constexpr int PASSES = kBlock / RPP;
-    __shared__ int s_tok[kAppendWarps][kBlock];
+    constexpr int EPL = D / 32;
+    constexpr int WORDS = EPL / 2;
+    constexpr int ROWS = (kSeen + kAppendWarps - 1) / kAppendWarps;  // rows of a warp
+    using Raw = typename Piece<EPL>::raw;
+    using Codes = typename Piece<EPL>::codes;
+    __shared__ long long s_slot[kReach + kSeen];  // of tokens first - 31 .. first + 46; -1: none, padding or bad
+    __shared__ int s_run[kSeen];                  // the window's token that starts this token's run, or -1
+    __shared__ int s_leader[kWindow];
+    __shared__ unsigned s_rows[kWindow];          // offsets a run writes
+    __shared__ unsigned s_amax[kWindow];
+    __shared__ float s_inv[kWindow], s_ratio[kWindow];  // 1 / S', and S / S' where the other rows need it (else 0)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * kAppendWarps + warp;
-    const long long per_tok = 2LL * a.n_kv;
-    if (item >= a.n_tok * per_tok) return;
+    const int parts = 2 * a.n_kv;
+    const long long window = blockIdx.x / parts;
+    const int part = (int)(blockIdx.x % parts);
+    const bool is_v = part >= a.n_kv;
+    const int g = is_v ? part - a.n_kv : part;
+    const long long first = window * kWindow;
     grid_launch_dependents();
     grid_dependency_wait();
-    const int t = (int)(item / per_tok);
-    const int rest = (int)(item % per_tok);
-    const bool is_v = rest >= a.n_kv;
-    const int g = is_v ? rest - a.n_kv : rest;
-    const long long slot = a.slots[t];
-    if (slot < 0) return;  // padding token
-    if (slot >= (long long)a.num_blocks * kBlock) {
-        if (lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_SLOT);
-        return;
+    if (threadIdx.x < kReach + kSeen) {
+        const long long t = first - kReach + threadIdx.x;
+        long long slot = t >= 0 && t < a.n_tok ? a.slots[t] : -1;
+        if (slot >= (long long)a.num_blocks * kBlock) {
+            if (part == 0 && threadIdx.x >= kReach) atomicOr(a.status, (unsigned)PKV_DEV_BAD_SLOT);
+            slot = -1;
+        }
+        s_slot[threadIdx.x] = slot < 0 ? -1 : slot;
     }
-    const long long block = slot / kBlock;
-    const long long before = lane > 0 && t - lane >= 0 ? a.slots[t - lane] : -1;
-    if (__any_sync(0xffffffffu, before >= 0 && before / kBlock == block)) return;
-    const long long after = (long long)t + lane < a.n_tok ? a.slots[t + lane] : -1;
-    const bool member = after >= 0 && after / kBlock == block;
-    if (lane < kBlock) s_tok[warp][lane] = -1;
-    __syncwarp();
-    if (member) s_tok[warp][after % kBlock] = t + lane;
-    __syncwarp();
+    if (threadIdx.x < kSeen) s_run[threadIdx.x] = -1;
+    if (threadIdx.x < kWindow) s_rows[threadIdx.x] = s_amax[threadIdx.x] = 0u;
+    __syncthreads();
+    {  // half a warp per token of the window: does its block lie among the 31 before?
+        const int u = threadIdx.x >> 4, l = threadIdx.x & 15;
+        const long long slot = s_slot[kReach + u];
+        bool seen = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int back = 1 + l + 16 * i;
+            if (back <= kReach && slot >= 0) {
+                const long long other = s_slot[kReach + u - back];
+                seen = seen || (other >= 0 && other / kBlock == slot / kBlock);
+            }
+        }
+        const unsigned b = __ballot_sync(0xffffffffu, seen);
+        if (l == 0) s_leader[u] = slot >= 0 && ((b >> (lane & 16)) & 0xffffu) == 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kSeen * kWindow; i += kAppendWarps * 32) {
+        const int u = i / kWindow, l = i % kWindow;
+        const long long slot = s_slot[kReach + u];
+        if (u >= l && u - l <= kReach && slot >= 0 && s_leader[l] && s_slot[kReach + l] / kBlock == slot / kBlock) {
+            s_run[u] = l;
+            atomicOr(&s_rows[l], 1u << (slot % kBlock));
+        }
+    }
+    __syncthreads();
 
-    const int c = lane % NCH, sub = lane / NCH;
+    float* scales = is_v ? a.v_scales : a.k_scales;
+    uint8_t* codes = is_v ? a.v_codes : a.k_codes;
+    auto cell_of = [&](int l) -> size_t { return (size_t)(s_slot[kReach + l] / kBlock) * a.n_kv + g; };
+    const bool starts = threadIdx.x < kWindow && s_leader[threadIdx.x];
+    const float old = starts ? scales[cell_of(threadIdx.x)] : 0.f;
     const T* src = reinterpret_cast<const T*>(is_v ? a.v : a.k);
-    uint4 x[PASSES];
-    float amax = 0.f;
+    Raw x[ROWS];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int tok = s_tok[warp][i * RPP + sub];
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tok >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)tok * a.n_kv + g) * D) + c);
+    for (int i = 0; i < ROWS; ++i) {
+        const int u = i * kAppendWarps + warp;
+        if (u < kSeen && s_run[u] >= 0) x[i] = __ldg(reinterpret_cast<const Raw*>(src + ((size_t)(first + u) * a.n_kv + g) * D) + lane);
     }
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        float f[8];
-        Vec16<T>::to_float(x[i], f);
+    for (int i = 0; i < ROWS; ++i) {
+        const int u = i * kAppendWarps + warp;
+        if (u < kSeen && s_run[u] >= 0) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+            float amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = fabsf(f[e]);
-            if (v <= kMaxFinite) amax = fmaxf(amax, v);
+            for (int e = 0; e < WORDS; ++e) {
+                float f[2];
+                widen_word<T>(w[e], f);
+                if (fabsf(f[0]) <= kMaxFinite) amax = fmaxf(amax, fabsf(f[0]));
+                if (fabsf(f[1]) <= kMaxFinite) amax = fmaxf(amax, fabsf(f[1]));
+            }
+            // non-negative floats are ordered like their bits
+            const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+            if (lane == 0) atomicMax(&s_amax[s_run[u]], m);
         }
     }
+    __syncthreads();
+    if (starts) {
+        const float need = pow2(scale_exp(__uint_as_float(s_amax[threadIdx.x]), a.min_exp));
+        const bool started = s_rows[threadIdx.x] & 1u;
+        const float now = started ? need : fmaxf(old, need);
+        s_inv[threadIdx.x] = 1.f / now;  // exact: a power of two (or a caller's own scale that was the larger)
+        s_ratio[threadIdx.x] = !started && now != old ? old / now : 0.f;
+        s_leader[threadIdx.x] = !started && now != old ? 2 : 1;
+        scales[cell_of(threadIdx.x)] = now;
+    }
+    __syncthreads();
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-
-    const size_t cell = (size_t)block * a.n_kv + g;
-    float* scale = (is_v ? a.v_scales : a.k_scales) + cell;
-    const float need = pow2(scale_exp(amax, a.min_exp));
-    const bool started = s_tok[warp][0] >= 0;
-    const float old = *scale;
-    const float now = started ? need : fmaxf(old, need);
-    const float inv = 1.f / now;  // exact: a power of two (or a caller's own scale that was the larger)
-    uint8_t* dst = (is_v ? a.v_codes : a.k_codes) + cell * kBlock * D;
-    const bool grew = !started && now != old;
+    for (int i = 0; i < ROWS; ++i) {
+        const int u = i * kAppendWarps + warp;
+        if (u < kSeen && s_run[u] >= 0) {
+            const int l = s_run[u];
+            const float inv = s_inv[l];
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
+            Codes c;
+            uint16_t* h = reinterpret_cast<uint16_t*>(&c);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = i * RPP + sub;
-        uint2* out = reinterpret_cast<uint2*>(dst + r * D) + c;
-        if (s_tok[warp][r] >= 0) {
-            float f[8];
-            Vec16<T>::to_float(x[i], f);
+            for (int e = 0; e < WORDS; ++e) {
+                float f[2];
+                widen_word<T>(w[e], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) <= kMaxFinite ? f[e] * inv : __int_as_float(0x7fc00000);
-            *out = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16),
-                              to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
-        } else if (grew) {
-            *out = rescale8(*out, old * inv);
+                for (int v = 0; v < 2; ++v) f[v] = fabsf(f[v]) <= kMaxFinite ? f[v] * inv : __int_as_float(0x7fc00000);
+                h[e] = (uint16_t)to_e4m3x2(f[0], f[1]);
+            }
+            reinterpret_cast<Codes*>(codes + (cell_of(l) * kBlock + s_slot[kReach + u] % kBlock) * D)[lane] = c;
         }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = now;
+    for (int l = 0; l < kWindow; ++l) {  // rare: a block continued with a larger scale
+        if (s_leader[l] != 2) continue;
+        for (int r = warp; r < kBlock; r += kAppendWarps) {
+            if ((s_rows[l] >> r) & 1u) continue;
+            Codes* p = reinterpret_cast<Codes*>(codes + (cell_of(l) * kBlock + r) * D) + lane;
+            Codes c = *p;
+            uint16_t* h = reinterpret_cast<uint16_t*>(&c);
+#pragma unroll
+            for (int e = 0; e < WORDS; ++e) {
+                const float2 f = from_e4m3x2(h[e]);
+                h[e] = (uint16_t)to_e4m3x2(f.x * s_ratio[l], f.y * s_ratio[l]);
+            }
+            *p = c;
+        }
+    }
 }
 
 // grid (pair, layer, K/V): each CTA copies one block of one layer, codes and scales.
@@ -203,7 +276,6 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.z;
     const int cap = a.max_blocks * kBlock;
-    grid_dependency_wait();
     const int ctx = a.lens[s];
     if (ctx <= 0 || ctx > cap) return;  // the attention launch flags such a sequence
     const int nb = (ctx + kBlock - 1) / kBlock;
@@ -243,8 +315,7 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
 
 template <typename T>
 cudaError_t append_of(int head_dim, const Q8AppendArgs& a, cudaStream_t stream) {
-    const long long items = 2LL * a.n_tok * a.n_kv;
-    const long long ctas = (items + kAppendWarps - 1) / kAppendWarps;
+    const long long ctas = ((long long)a.n_tok + kWindow - 1) / kWindow * 2 * a.n_kv;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)ctas);
     switch (head_dim) {
@@ -261,11 +332,12 @@ cudaError_t widen_of(int head_dim, const Q8WidenArgs& a, cudaStream_t stream) {
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)ctas, 1, a.n_seqs);
     switch (head_dim) {
-    case 64: return launch_dependent(q8_widen_kernel<T, 64>, grid, kWidenWarps * 32, 0, stream, 1, a);
-    case 128: return launch_dependent(q8_widen_kernel<T, 128>, grid, kWidenWarps * 32, 0, stream, 1, a);
-    case 256: return launch_dependent(q8_widen_kernel<T, 256>, grid, kWidenWarps * 32, 0, stream, 1, a);
+    case 64: q8_widen_kernel<T, 64><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
+    case 128: q8_widen_kernel<T, 128><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
+    case 256: q8_widen_kernel<T, 256><<<grid, kWidenWarps * 32, 0, stream>>>(a); break;
     default: return cudaErrorInvalidValue;
     }
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -568,19 +568,31 @@ class _Facts:
 _facts_by_value: dict = {}
 
 
-def _facts(desc: CacheDesc) -> _Facts:
+_t = None  # torch, once a call has needed it
+
+
+def _call(desc):
+    """(torch, facts of the descriptor, index of the current device) for a call's checks. Without a CUDA
+    device the index is -2, which no tensor's device equals."""
+    global _t
+    if _t is None:
+        _t = _torch()
+    try:
+        cur = _t.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        cur = -2
     key = bytes(desc)
     f = _facts_by_value.get(key)
     if f is None:
         if len(_facts_by_value) >= 256:
             _facts_by_value.clear()
         f = _facts_by_value[key] = _Facts(desc)
-    return f
+    return _t, f, cur
 
 
 def _ptr(x, name, dtype, shape, cur) -> int:
     """The address of a tensor that _dev accepts; where it does not, _dev's error."""
-    if x.dtype is dtype and x.shape == shape and x.get_device() == cur and x.is_contiguous():
+    if x.get_device() == cur and x.dtype is dtype and x.shape == shape and x.is_contiguous():
         return x.data_ptr()
     return _dev(x, name, dtype, shape, cur=cur).value
 
@@ -588,7 +600,7 @@ def _ptr(x, name, dtype, shape, cur) -> int:
 def _raw(stream, cur: int) -> int:
     """The handle of `stream`, or of the current stream of the current device."""
     if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(cur) if cur >= 0 else 0
+        return _t._C._cuda_getCurrentRawStream(cur)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -614,7 +626,7 @@ def _scores(scores, name, lead, max_blocks: int, cur):
         raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, at least {max_blocks * BLOCK}], "
                          f"got {tuple(scores.shape)}")
     stride = int(scores.shape[-1])
-    return _ptr(scores, name, _torch().float32, (*lead, stride), cur), stride
+    return _ptr(scores, name, _t.float32, (*lead, stride), cur), stride
 
 
 def _table_width(block_tables) -> int:
@@ -675,7 +687,7 @@ def alloc_evict_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int,
 def pkv_q8_append(desc: CacheDesc, layer: int, k, v, slot_mapping, k_codes, v_codes, k_scales, v_scales,
                   stream=None) -> None:
     """pkv_kv_append into 8-bit pools: rows k, v [n_tokens, n_kv, d] are rounded to codes."""
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_tok = k.shape[0]
     row = (n_tok, f.n_kv, f.d)
     kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
@@ -686,7 +698,7 @@ def pkv_q8_append(desc: CacheDesc, layer: int, k, v, slot_mapping, k_codes, v_co
 
 
 def pkv_q8_copy_blocks(desc: CacheDesc, k_codes, v_codes, k_scales, v_scales, pairs, stream=None) -> None:
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_pairs = pairs.shape[0]
     kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
     rc = lib().pkv_q8_copy_blocks(ctypes.byref(desc), kc, vc, ks, vs, _ptr(pairs, "pairs", t.int32, (n_pairs, 2), cur),
@@ -698,7 +710,7 @@ def pkv_q8_decode_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k_
                             context_lens, scale: float, out, workspace=None, scores=None, stream=None) -> None:
     """pkv_paged_decode_attention over 8-bit pools; scores float32 [n_seqs, n_kv, S] gain each
     position's attention weight (workspace then from alloc_q8_workspace(..., scored=True))."""
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_seqs, max_blocks = q.shape[0], _table_width(block_tables)
     qshape = (n_seqs, f.n_q, f.d)
     kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
@@ -716,7 +728,7 @@ def pkv_q8_prefill_attention(desc: CacheDesc, layer: int, q, k_codes, v_codes, k
                              context_lens, query_start, max_query_len: int, scale: float, out, workspace,
                              stream=None) -> None:
     """pkv_paged_prefill_attention over 8-bit pools (workspace from alloc_q8_prefill_workspace)."""
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_tokens, max_blocks, n_seqs = q.shape[0], _table_width(block_tables), block_tables.shape[0]
     qshape = (n_tokens, f.n_q, f.d)
     kc, vc, ks, vs = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
@@ -734,7 +746,7 @@ def pkv_paged_decode_attention_scored(desc: CacheDesc, layer: int, q, k_pool, v_
                                       scale: float, out, scores, workspace, stream=None) -> None:
     """pkv_paged_decode_attention that adds each position's attention weight to scores, float32
     [n_seqs, n_kv, S] (workspace from alloc_scored_workspace)."""
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_seqs, max_blocks = q.shape[0], _table_width(block_tables)
     qshape = (n_seqs, f.n_q, f.d)
     sp, stride = _scores(scores, "scores", (n_seqs, f.n_kv), max_blocks, cur)
@@ -756,7 +768,7 @@ def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, co
     kept int32 [n_layers, n_seqs, n_kv, max_keep]. For 8-bit pools k_pool / v_pool are the codes, with
     k_scales, v_scales and a workspace from alloc_evict_workspace.
     """
-    t, f, cur = _torch(), _facts(desc), _current_device()
+    t, f, cur = _call(desc)
     n_seqs, max_blocks = src_tables.shape[0], _table_width(src_tables)
     if k_scales is not None or v_scales is not None:
         if k_scales is None or v_scales is None:
