@@ -17,6 +17,10 @@ method needs ("04 - Hacia PagedAttention (vista previa)", "La idea de PagedAtten
              appends before attention (the new token attends to itself). By default the append
              and the attention of a layer are one kernel (pkv_paged_decode_append_attention).
 
+A cache with ``storage="q8"`` holds its rows in 8 bits (half the bytes; pkv_q8_*). A ``DecodeBatch``
+with ``scored=True`` sums every cached position's attention weight, and its ``evict`` shortens the
+sequences to the positions used most (pkv_evict_tokens). Both work together.
+
 All device work is in libpkv's kernels; this module only moves arguments.
 """
 from __future__ import annotations
@@ -81,12 +85,23 @@ def validate_step_metadata(num_blocks: int, block_size: int, tables, lens, slots
 
 
 class PagedKVCache:
-    def __init__(self, desc: pkv.CacheDesc, free_order=None, device=None, init: str = "zeros", seed: int = 0):
+    """The pools and the block manager. storage: None holds rows in desc's type; "q8" holds e4m3 codes with
+    a float32 scale for each (block, KV head) in k_scales / v_scales (desc then names the type of the
+    activations, fp16 or bf16)."""
+
+    def __init__(self, desc: pkv.CacheDesc, free_order=None, device=None, init: str = "zeros", seed: int = 0,
+                 storage: str | None = None):
         import torch
+        if storage not in (None, "q8"):
+            raise ValueError("storage must be None or 'q8'")
         self.desc = desc
+        self.q8 = storage == "q8"
+        if self.q8 and (desc.dtype_name == "f32" or init == "randn"):
+            raise ValueError("an 8-bit cache needs fp16 or bf16 activations and starts from zeros")
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        dt = pkv.torch_dtype(desc.dtype_name)
+        dt = torch.float8_e4m3fn if self.q8 else pkv.torch_dtype(desc.dtype_name)
         shape = pkv.pool_shape(desc)
+        self.k_scales = self.v_scales = None
         if init == "randn":
             g = torch.Generator(device=self.device)
             g.manual_seed(seed)
@@ -95,7 +110,45 @@ class PagedKVCache:
         else:
             self.k_pool = torch.zeros(shape, dtype=dt, device=self.device)
             self.v_pool = torch.zeros(shape, dtype=dt, device=self.device)
+        if self.q8:
+            self.k_scales = torch.zeros(pkv.scale_shape(desc), device=self.device)
+            self.v_scales = torch.zeros(pkv.scale_shape(desc), device=self.device)
         self.mgr = pkv.BlockManager(desc.num_blocks, desc.block_size, free_order=free_order)
+
+    def _arrays(self):
+        """What every call over the pools takes: the pools, and the scales of an 8-bit cache."""
+        return (self.k_pool, self.v_pool, self.k_scales, self.v_scales) if self.q8 else (self.k_pool, self.v_pool)
+
+    def append(self, layer: int, k, v, slots, stream=None) -> None:
+        """Write rows k, v [n_tokens, n_kv, d] of one layer to their slots."""
+        if self.q8:
+            pkv.pkv_q8_append(self.desc, layer, k, v, slots, *self._arrays(), stream=stream)
+        else:
+            pkv.pkv_kv_append(self.desc, layer, k, v, slots, self.k_pool, self.v_pool, stream=stream)
+
+    def copy_blocks(self, pairs, stream=None) -> None:
+        """Copy-on-write block copies of all layers."""
+        (pkv.pkv_q8_copy_blocks if self.q8 else pkv.pkv_copy_blocks)(self.desc, *self._arrays(), pairs, stream=stream)
+
+    def decode_workspace(self, n_seqs: int, max_blocks: int, scored: bool = False):
+        """The device buffer that decode needs (None where it needs none)."""
+        if self.q8:
+            return pkv.alloc_q8_workspace(self.desc, n_seqs, max_blocks, scored=scored, device=self.device)
+        alloc = pkv.alloc_scored_workspace if scored else pkv.alloc_workspace
+        return alloc(self.desc, n_seqs, max_blocks, device=self.device)
+
+    def decode(self, layer: int, q, tables, lens, scale: float, out, workspace=None, scores=None, stream=None) -> None:
+        """Decode attention of one layer over rows already appended; scores [n_seqs, n_kv, S] gain each
+        position's weight."""
+        if self.q8:
+            pkv.pkv_q8_decode_attention(self.desc, layer, q, *self._arrays(), tables, lens, scale, out, workspace,
+                                        scores=scores, stream=stream)
+        elif scores is not None:
+            pkv.pkv_paged_decode_attention_scored(self.desc, layer, q, self.k_pool, self.v_pool, tables, lens, scale, out,
+                                                  scores, workspace, stream=stream)
+        else:
+            pkv.pkv_paged_decode_attention(self.desc, layer, q, self.k_pool, self.v_pool, tables, lens, scale, out,
+                                           workspace, stream=stream)
 
     def add_sequence(self, seq_id: int, n_prompt: int, reserve_tokens: int = 0) -> np.ndarray:
         rc, slots = self.mgr.add_seq(seq_id, n_prompt, reserve_tokens)
@@ -115,13 +168,19 @@ class PagedKVCache:
 
     def kv_bytes_per_token_layer(self) -> int:
         d = self.desc
-        return 2 * d.n_kv_heads * d.head_dim * (4 if d.dtype_name == "f32" else 2)
+        return 2 * d.n_kv_heads * d.head_dim * (1 if self.q8 else 4 if d.dtype_name == "f32" else 2)
 
 
 class DecodeBatch:
-    """Decode steps for a batch of n sequences whose tables are at most max_blocks wide."""
+    """Decode steps for a batch of n sequences whose tables are at most max_blocks wide.
 
-    def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, stream=None, fused: bool = True):
+    scored: every step adds each cached position's attention weight, summed over the query heads of a KV
+    head, to ``scores`` [L, n, n_kv, max_blocks * 16] (row s belongs to the batch's s-th sequence), which
+    ``evict`` goes by. An 8-bit cache and scored steps append and attend in separate launches.
+    """
+
+    def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, stream=None, fused: bool = True,
+                 scored: bool = False):
         import torch
         self.cache = cache
         self.seq_ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
@@ -130,7 +189,7 @@ class DecodeBatch:
         self.max_blocks = int(max_blocks)
         self.stream = stream if stream is not None else torch.cuda.current_stream(cache.device)
         # fused: one kernel per layer appends the new rows and attends; else kv_append + decode
-        self.fused = bool(fused)
+        self.fused = bool(fused) and not cache.q8 and not scored
         # overlap: each layer's fused launch may start while the previous layer's finishes
         self.overlap = True
         dev = cache.device
@@ -153,7 +212,12 @@ class DecodeBatch:
                                   uploaded=torch.cuda.Event(), read=torch.cuda.Event(), used=False))
         self.d_slots, self.d_tables, self.d_lens, self.d_pairs = (self._dev[0][k] for k in ("slots", "tables", "lens",
                                                                                              "pairs"))
-        self.workspace = pkv.alloc_workspace(cache.desc, n, mb, device=dev)
+        self.workspace = cache.decode_workspace(n, mb, scored)
+        self.scores = None
+        if scored:
+            with torch.cuda.stream(self.stream):
+                self.scores = torch.zeros((cache.desc.n_layers, n, cache.desc.n_kv_heads, mb * pkv.BLOCK), device=dev)
+        self._evict_stage = None
         # two pinned staging images
         self._stage = []
         for _ in range(2):
@@ -203,6 +267,17 @@ class DecodeBatch:
         ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
         if len(ids) != self.n:
             raise ValueError("batch size is fixed")
+        if self.scores is not None and not np.array_equal(ids, self.seq_ids):
+            # a sequence keeps its sums in its new row; one that was not in the batch starts from zero
+            import torch
+            row = {int(x): i for i, x in enumerate(self.seq_ids)}
+            moved = [(i, row[int(x)]) for i, x in enumerate(ids) if int(x) in row]
+            with torch.cuda.stream(self.stream):
+                new = torch.zeros_like(self.scores)
+                if moved:
+                    to, frm = (torch.tensor(t, device=new.device) for t in zip(*moved))
+                    new[:, to] = self.scores[:, frm]
+                self.scores.copy_(new)
         self.seq_ids = ids
         self._p_ids = ids.ctypes.data_as(ctypes.POINTER(ctypes.c_int64))
 
@@ -254,7 +329,7 @@ class DecodeBatch:
         self.stream.wait_event(dv["uploaded"])
         self.d_slots, self.d_tables, self.d_lens, self.d_pairs = dv["slots"], dv["tables"], dv["lens"], dv["pairs"]
         if st["npairs"]:
-            pkv.pkv_copy_blocks(d, c.k_pool, c.v_pool, self.d_pairs[: st["npairs"]], stream=self.stream)
+            c.copy_blocks(self.d_pairs[: st["npairs"]], stream=self.stream)
         if self.fused:  # the step's tensors checked once (and again only when they change); each
             # layer is then one C call
             key = (q, k_new, v_new, out, float(scale))
@@ -277,12 +352,11 @@ class DecodeBatch:
                 # workspace, which the kernel touches after the previous launch has completed)
                 launch(layer, self.overlap and layer > 0 and on_decode is None)
             else:
-                pkv.pkv_kv_append(d, layer, k_new[layer], v_new[layer], self.d_slots, c.k_pool, c.v_pool,
-                                  stream=self.stream)
+                c.append(layer, k_new[layer], v_new[layer], self.d_slots, stream=self.stream)
                 if on_decode is not None:
                     on_decode(layer, "start")
-                pkv.pkv_paged_decode_attention(d, layer, q[layer], c.k_pool, c.v_pool, self.d_tables, self.d_lens,
-                                               scale, out[layer], self.workspace, stream=self.stream)
+                c.decode(layer, q[layer], self.d_tables, self.d_lens, scale, out[layer], self.workspace,
+                         scores=None if self.scores is None else self.scores[layer], stream=self.stream)
             if on_decode is not None:
                 on_decode(layer, "end")
         dv["read"].record(self.stream)
@@ -293,6 +367,51 @@ class DecodeBatch:
         self.upload(st)
         self.run_device(st, q, k_new, v_new, out, scale, on_decode)
         return st
+
+    def evict(self, keep_lens, recent: int):
+        """Between two steps of a scored batch: shorten each sequence to keep_lens[s] positions (an int: the
+        same for all), its `recent` last ones and those with the largest scores, by (layer, KV head).
+
+        The block manager shortens the tables first (blocks that other sequences hold too are replaced, so
+        those keep their rows; PkvError with nothing changed if there are not enough free blocks), then one
+        call moves rows and scores. Returns the positions kept, int32 [L, n, n_kv, max kept] (-1 behind a
+        sequence's last).
+        """
+        import torch
+        if self.scores is None:
+            raise ValueError("evict needs a batch with scored=True")
+        c, n, mb = self.cache, self.n, self.max_blocks
+        rc, src, lens = c.mgr.pack_tables(self.seq_ids, mb)
+        if rc != pkv.PKV_OK:
+            raise pkv.PkvError(rc, "pack_tables")
+        keep = np.broadcast_to(np.asarray(keep_lens, dtype=np.int64), (n,))
+        if keep.min(initial=0) < 0 or recent < 0:
+            raise ValueError("keep_lens and recent must not be negative")
+        keep = np.minimum(keep, lens).astype(np.int32)
+        words = 2 * n * mb + 2 * n
+        if self._evict_stage is None:
+            self._evict_stage = dict(host=torch.empty(words, dtype=torch.int32).pin_memory(),
+                                     dev=torch.empty(words, dtype=torch.int32, device=c.device), done=torch.cuda.Event(),
+                                     ws=pkv.alloc_evict_workspace(c.desc, n, mb, device=c.device) if c.q8 else None)
+        stage = self._evict_stage
+        stage["done"].synchronize()  # the last eviction has read its image
+        with torch.cuda.stream(self.stream):
+            kept = torch.full((*self.scores.shape[:3], max(1, int(keep.max(initial=0)))), -1, dtype=torch.int32,
+                              device=c.device)
+        rc = c.mgr.compact(self.seq_ids, keep)
+        if rc != pkv.PKV_OK:
+            raise pkv.PkvError(rc, "compact")
+        rc, dst, _ = c.mgr.pack_tables(self.seq_ids, mb)
+        if rc != pkv.PKV_OK:
+            raise pkv.PkvError(rc, "pack_tables")
+        stage["host"].numpy()[:] = np.concatenate([src.reshape(-1), dst.reshape(-1), lens, keep])
+        pkv.upload_metadata_ptr(stage["dev"].data_ptr(), stage["host"].data_ptr(), 4 * words, self.stream.cuda_stream)
+        stage["done"].record(self.stream)
+        m = stage["dev"]
+        pkv.pkv_evict_tokens(c.desc, c.k_pool, c.v_pool, m[:n * mb].view(n, mb), m[n * mb:2 * n * mb].view(n, mb),
+                             m[2 * n * mb:2 * n * mb + n], m[2 * n * mb + n:], recent, self.scores, self.scores, kept,
+                             stream=self.stream, k_scales=c.k_scales, v_scales=c.v_scales, workspace=stage["ws"])
+        return kept
 
     def kv_bytes_last_step(self) -> int:
         """Algorithmic KV bytes the last step's attention read: sum(ctx) * 2 * n_kv * d * e * L."""
@@ -334,6 +453,7 @@ class PrefillStep:
         self._o_pair = self._o_qs + S + 1
         self._words = self._o_pair + 2 * S
         self.d_meta = torch.empty(self._words, dtype=torch.int32, device=cache.device)
+        self.workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
         self._stage = []
         for _ in range(2):
             h = torch.empty(self._words, dtype=torch.int32).pin_memory()
@@ -407,7 +527,19 @@ class PrefillStep:
         d = c.desc
         slots, tables, lens, qs, pairs = self._dev_views(st["n_seqs"], st["n_tok"])
         if st["npairs"]:
-            pkv.pkv_copy_blocks(d, c.k_pool, c.v_pool, pairs[: st["npairs"]], stream=self.stream)
+            c.copy_blocks(pairs[: st["npairs"]], stream=self.stream)
+        if c.q8:
+            for layer in range(d.n_layers):
+                if on_attn is not None:
+                    on_attn(layer, "pre")
+                c.append(layer, k_new[layer], v_new[layer], slots, stream=self.stream)
+                if on_attn is not None:
+                    on_attn(layer, "start")
+                pkv.pkv_q8_prefill_attention(d, layer, q[layer], *c._arrays(), tables, lens, qs, st["max_q"], scale,
+                                             out[layer], self.workspace, stream=self.stream)
+                if on_attn is not None:
+                    on_attn(layer, "end")
+            return
         append = pkv.append_launcher(d, k_new, v_new, slots, c.k_pool, c.v_pool, stream=self.stream)
         attend = pkv.prefill_launcher(d, q, c.k_pool, c.v_pool, tables, lens, qs, st["max_q"], scale, out,
                                       stream=self.stream)
@@ -484,7 +616,8 @@ class StepExecutor:
             h = torch.empty(off, dtype=torch.int32).pin_memory()
             self._stage.append(dict(meta=h, np=h.numpy(), done=torch.cuda.Event(), used=False))
         self._turn = 0
-        self.workspace = pkv.alloc_workspace(cache.desc, max(D, 1), mb, device=cache.device)
+        self.workspace = cache.decode_workspace(max(D, 1), mb)
+        self.prefill_workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
 
     def _host(self, np_meta, name, dtype=np.int32):
         off, words = self._off[name]
@@ -537,8 +670,7 @@ class StepExecutor:
         d = c.desc
         u = self.upload(plan)
         if u["n_pairs"]:
-            pkv.pkv_copy_blocks(d, c.k_pool, c.v_pool, self._dev("pairs", 2 * u["n_pairs"], (-1, 2)),
-                                stream=self.stream)
+            c.copy_blocks(self._dev("pairs", 2 * u["n_pairs"], (-1, 2)), stream=self.stream)
         append, attend, decode = self._launchers(u, dec_io, pre_io, scale)
         if on_kernel is None and self.overlap:
             self._run_overlapped(u, append, attend, decode)
@@ -564,6 +696,8 @@ class StepExecutor:
         c = self.cache
         d = c.desc
         append = attend = decode = None
+        if c.q8:
+            return self._q8_launchers(u, dec_io, pre_io, scale)
         if u["n_pre"]:
             q, k, v, out = pre_io
             append = pkv.append_launcher(d, k, v, self._dev("pre_slots", u["n_tok"], i64=True), c.k_pool, c.v_pool,
@@ -577,6 +711,34 @@ class StepExecutor:
             decode = pkv.decode_append_launcher(
                 d, q, k, v, c.k_pool, c.v_pool, self._dev("dec_tables", u["n_dec"] * u["wd"], (-1, u["wd"])),
                 self._dev("dec_lens", u["n_dec"]), scale, out, self.workspace, stream=self.stream)
+        return append, attend, decode
+
+    def _q8_launchers(self, u, dec_io, pre_io, scale: float):
+        """_launchers over an 8-bit cache: ordinary launches (they overlap by themselves as far as they
+        may), decoding rows appended by a launch of their own."""
+        c, stream = self.cache, self.stream
+        append = attend = decode = None
+        if u["n_pre"]:
+            q, k, v, out = pre_io
+            slots = self._dev("pre_slots", u["n_tok"], i64=True)
+            tables = self._dev("pre_tables", u["n_pre"] * u["wp"], (-1, u["wp"]))
+            lens, qs = self._dev("pre_lens", u["n_pre"]), self._dev("pre_qs", u["n_pre"] + 1)
+
+            def append(layer: int) -> None:
+                c.append(layer, k[layer], v[layer], slots, stream=stream)
+
+            def attend(layer: int, overlap_previous: bool = False) -> None:
+                pkv.pkv_q8_prefill_attention(c.desc, layer, q[layer], *c._arrays(), tables, lens, qs, u["max_q"], scale,
+                                             out[layer], self.prefill_workspace, stream=stream)
+        if u["n_dec"]:
+            dq, dk, dv, dout = dec_io
+            dslots = self._dev("dec_slots", u["n_dec"], i64=True)
+            dtables = self._dev("dec_tables", u["n_dec"] * u["wd"], (-1, u["wd"]))
+            dlens = self._dev("dec_lens", u["n_dec"])
+
+            def decode(layer: int, overlap_previous: bool = False) -> None:
+                c.append(layer, dk[layer], dv[layer], dslots, stream=stream)
+                c.decode(layer, dq[layer], dtables, dlens, scale, dout[layer], self.workspace, stream=stream)
         return append, attend, decode
 
     def _run_overlapped(self, u, append, attend, decode) -> None:
