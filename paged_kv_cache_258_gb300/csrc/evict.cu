@@ -43,6 +43,17 @@ __device__ __forceinline__ float key_score(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
 template <int NT>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     constexpr int NW = NT / 32;
@@ -113,18 +124,16 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             uint32_t mine = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) mine += s_hist[kBins - 1 - (threadIdx.x * PER + i)];
-            uint32_t above = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
-                if (lane >= o) above += y;
-            }
+            uint32_t above = warp_scan(mine);
             if (lane == 31) s_warp[warp] = above;
             __syncthreads();
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                if (w < warp) above += s_warp[w];
-            above -= mine;
+            if (warp == 0) {
+                const uint32_t v = lane < NW ? s_warp[lane] : 0u;
+                const uint32_t before = warp_scan(v) - v;
+                if (lane < NW) s_warp[lane] = before;
+            }
+            __syncthreads();
+            above += s_warp[warp] - mine;
             if (above < left && above + mine >= left) {  // the bin that holds the left-th largest is here
                 uint32_t n = above;
                 for (int i = 0; i < PER; ++i) {
@@ -167,16 +176,22 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             s_warp2[warp] = equal;
         }
         __syncthreads();
-        uint32_t ab = n_above, eq = n_equal;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) {
-                ab += s_warp[w];
-                eq += s_warp2[w];
+        if (warp == 0) {  // sums over the warps before, and over all
+            const uint32_t va = lane < NW ? s_warp[lane] : 0u, ve = lane < NW ? s_warp2[lane] : 0u;
+            const uint32_t ia = warp_scan(va), ie = warp_scan(ve);
+            if (lane < NW) {
+                s_warp[lane] = ia - va;
+                s_warp2[lane] = ie - ve;
             }
-            n_above += s_warp[w];
-            n_equal += s_warp2[w];
+            if (lane == 31) {
+                s_pick[0] = ia;
+                s_pick[1] = ie;
+            }
         }
+        __syncthreads();
+        uint32_t ab = n_above + s_warp[warp], eq = n_equal + s_warp2[warp];
+        n_above += s_pick[0];
+        n_equal += s_pick[1];
         const uint32_t below = (1u << lane) - 1;
 #pragma unroll
         for (int r = 0; r < kKeys; ++r) {
@@ -237,40 +252,75 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     }
 }
 
-// Sixteen codes * f, back to codes.
+// Sixteen codes * f, back to codes (round to nearest even). A power of two f <= 1 multiplies in fp16: what
+// lies at or above 2^-10, half the least code, is exact there, and what lies below becomes 0 either way.
 __device__ __forceinline__ uint4 rescale16(uint4 c, float f) {
     uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const bool half_exact = f <= 1.f && (__float_as_uint(f) & 0x7fffffu) == 0;
+    const __half2 f2 = __float2half2_rn(f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t h[2];
+        uint16_t r[2];
         const uint16_t lo = (uint16_t)w[i], hi = (uint16_t)(w[i] >> 16);
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"(lo));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"(hi));
-        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h[0]));
-        const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h[1]));
-        uint16_t r0, r1;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r0) : "f"(x.y * f), "f"(x.x * f));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r1) : "f"(y.y * f), "f"(y.x * f));
-        w[i] = (uint32_t)r0 | ((uint32_t)r1 << 16);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            __half2 v = *reinterpret_cast<__half2*>(&h[e]);
+            if (half_exact) {
+                v = __hmul2(v, f2);
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r[e]) : "r"(*reinterpret_cast<uint32_t*>(&v)));
+            } else {
+                const float2 x = __half22float2(v);
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r[e]) : "f"(x.y * f), "f"(x.x * f));
+            }
+        }
+        w[i] = (uint32_t)r[0] | ((uint32_t)r[1] << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kRanked = 64;   // sequences up to which the move starts with the longest
 constexpr int kIndex = 512;  // kept rows whose places are worked out at a time
 
-// grid ((sequence, head) x slices, layer, K/V)
-template <bool Q8>
+// U: rows of a thread per chunk. 128 rows a chunk are best: with 256 of 64 bytes (8-bit pools, U = 4) the
+// CTAs that share rows drift apart, 101 us against 89; more chunks in flight are slower for the same reason
+// (16-bit pools: 107 us with the pipeline running on over the index, 93 with a stop every kIndex rows).
+template <bool Q8, int U>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a) {
-    constexpr int U = 4;  // rows of a thread per chunk
     __shared__ long long s_from[kIndex], s_to[kIndex];  // row numbers in the layer; s_to < 0: stays where it is
     __shared__ float s_f[Q8 ? kIndex : 1];              // what the row's codes are multiplied with
-    const long long pair = blockIdx.x / a.slices;
-    const int slice = (int)(blockIdx.x % a.slices);
-    const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
+    // grid x: (sequence, layer, K or V, head, slice), so that the sequences that keep most start first
+    long long rest = blockIdx.x;
+    const int slice = (int)(rest % a.slices);
+    rest /= a.slices;
+    const int g = (int)(rest % a.n_kv);
+    rest /= a.n_kv;
+    const bool is_v = rest % 2 != 0;
+    rest /= 2;
+    const int layer = (int)(rest % a.n_layers);
+    int s = (int)(rest / a.n_layers);
     const int cap = a.max_blocks * kBlock;
     grid_launch_dependents();
     grid_dependency_wait();
+    if (a.n_seqs > 1 && a.n_seqs <= kRanked) {
+        int* rank_k = reinterpret_cast<int*>(s_from);
+        int* by_rank = rank_k + kRanked;
+        if (threadIdx.x < a.n_seqs) rank_k[threadIdx.x] = min(a.keep[threadIdx.x], a.lens[threadIdx.x]);
+        __syncthreads();
+        if (threadIdx.x < a.n_seqs) {
+            const int mine = rank_k[threadIdx.x];
+            int r = 0;
+            for (int i = 0; i < a.n_seqs; ++i) r += rank_k[i] > mine || (rank_k[i] == mine && i < (int)threadIdx.x);
+            by_rank[r] = threadIdx.x;
+        }
+        __syncthreads();
+        s = by_rank[s];
+        __syncthreads();  // the index overwrites the ranks
+    }
+    const long long pair = (long long)s * a.n_kv + g;
     const int c = a.lens[s], want = a.keep[s];
     if (c < 0 || c > cap || want < 0 || min(want, c) > a.max_keep) return;  // flagged by the selection
     const int k = min(want, c);
@@ -282,7 +332,6 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     const int32_t* kept = a.kept + triple * a.max_keep;
     const int32_t* src = a.src + (size_t)s * a.max_blocks;
     const int32_t* dst = a.dst + (size_t)s * a.max_blocks;
-    const bool is_v = blockIdx.z != 0;
     const size_t layer_rows = (size_t)a.num_blocks * a.n_kv * kBlock;
     char* pool = reinterpret_cast<char*>(is_v ? a.v_pool : a.k_pool) + (size_t)layer * layer_rows * a.row_bytes +
                  (size_t)slice * lanes * 16 + (threadIdx.x % lanes) * 16;
@@ -386,8 +435,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
                           ? launch_dependent(evict_select_kernel<512>, dim3(pairs, a.n_layers), 512, 0, stream, 1, a)
                           : launch_dependent(evict_select_kernel<1024>, dim3(pairs, a.n_layers), 1024, 0, stream, 1, a);
     if (err != cudaSuccess) return err;
-    const dim3 grid(pairs * (unsigned)a.slices, a.n_layers, 2);
-    return launch_dependent(a.k_scales ? evict_move_kernel<true> : evict_move_kernel<false>, grid, kMoveThreads, 0, stream, 1, a);
+    const dim3 grid(pairs * (unsigned)a.slices * (unsigned)a.n_layers * 2u);
+    const bool wide = a.row_bytes / a.slices > 64;  // over four threads a row
+    auto move = a.k_scales ? (wide ? evict_move_kernel<true, 4> : evict_move_kernel<true, 2>)
+                           : (wide ? evict_move_kernel<false, 4> : evict_move_kernel<false, 2>);
+    return launch_dependent(move, grid, kMoveThreads, 0, stream, 1, a);
 }
 
 }  // namespace pkv

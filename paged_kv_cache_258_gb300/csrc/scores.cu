@@ -18,6 +18,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPerThread = 4;  // positions of a thread, kThreads apart
 
+// 2^x within 2 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <int G>
 __device__ __forceinline__ void load_logits(const float* p, float* z) {
     if constexpr (G == 1) {
@@ -48,22 +55,30 @@ __global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a)
     const int ctx = min(max(a.lens[s], 0), cap);
     const int j0 = blockIdx.x * kThreads * kPerThread;
     if (j0 >= ctx) return;
-    if (threadIdx.x < G) {
-        const float2 u = __ldcg(a.row_ml + ((size_t)s * a.n_kv + g) * G + threadIdx.x);
-        s_m[threadIdx.x] = u.x == -INFINITY ? 0.f : u.x;
-        s_inv[threadIdx.x] = u.y == 0.f ? 0.f : 1.f / u.y;
-    }
-    __syncthreads();
     const size_t base = ((size_t)s * a.n_kv + g);
+    float z[kPerThread][G], was[kPerThread];  // all of a thread's loads in flight with the statistics'
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int j = j0 + i * kThreads + threadIdx.x;
         if (j < ctx) {
-            float z[G], w = 0.f;
-            load_logits<G>(a.z + (base * cap + j) * G, z);
+            load_logits<G>(a.z + (base * cap + j) * G, z[i]);
+            was[i] = a.scores[base * a.stride + j];
+        }
+    }
+    if (threadIdx.x < G) {
+        const float2 u = __ldcg(a.row_ml + base * G + threadIdx.x);
+        s_m[threadIdx.x] = u.x == -INFINITY ? 0.f : u.x;
+        s_inv[threadIdx.x] = u.y == 0.f ? 0.f : 1.f / u.y;
+    }
+    __syncthreads();
 #pragma unroll
-            for (int r = 0; r < G; ++r) w += exp2f(z[r] - s_m[r]) * s_inv[r];
-            a.scores[base * a.stride + j] += w;
+    for (int i = 0; i < kPerThread; ++i) {
+        const int j = j0 + i * kThreads + threadIdx.x;
+        if (j < ctx) {
+            float w = 0.f;
+#pragma unroll
+            for (int r = 0; r < G; ++r) w += ex2(z[i][r] - s_m[r]) * s_inv[r];
+            a.scores[base * a.stride + j] = was[i] + w;
         }
     }
 }
