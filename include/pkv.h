@@ -407,7 +407,8 @@ int pkv_upload_metadata(void* dst, const void* src_host, size_t bytes, void* str
  * pkv_q8_append writes powers of two: the least 2^e (e >= -15 for fp16 rows, -117 for bf16) that lets
  * the block's largest finite element in, |x| <= 448 * 2^e. The attention calls take any scale >= 0.
  * Values within a factor 2^14 of the block's largest keep e4m3's relative precision (2^-4); smaller
- * ones lose bits, below 2^-10 * 2^e they round to zero.
+ * ones lose bits, below 2^-10 * 2^e they round to zero. fp16 elements above 63,488 are held as 65,536; the
+ * attention calls return no fp16 output beyond 65,504 for it.
  */
 
 /* Bytes of one pool of codes (K or V), and of one array of scales, over all layers; 0 if unsupported. */
@@ -465,18 +466,20 @@ int pkv_q8_decode_attention(const pkv_cache_desc* desc, int32_t layer, const voi
                             int32_t n_seqs, float scale, void* out, float* scores, int64_t score_stride,
                             void* workspace, size_t workspace_bytes, void* stream);
 
-/* Scratch bytes of pkv_q8_prefill_attention: one layer of K and V in the activations' type. */
+/* Scratch bytes of pkv_q8_prefill_attention: one layer of K and V in the activations' type, and partial
+ * results of up to 640 CTAs. */
 size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
 
 /*
  * pkv_paged_prefill_attention over 8-bit pools (the chunk's rows already appended by pkv_q8_append).
- * Two launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
- * physical block like one layer of a 16-bit pool, and attended to from there. The first costs a little
- * over a read of the codes and a write of twice their size; chunks of hundreds of tokens hide it.
- * Widened values are exact in bf16; in fp16 too, but for 65,536, which is read as 65,504. Arguments,
- * bad device values, limits and errors as pkv_paged_prefill_attention.
+ * Short chunks are attended to straight from the codes, 8 / G tokens at a time. Longer ones take two
+ * launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
+ * physical block like one layer of a 16-bit pool, and attended to from there by the kernel of 16-bit
+ * pools. The choice goes by the counts that are known on the host. Arguments, bad device values, limits and errors
+ * as pkv_paged_prefill_attention.
  *   workspace     device, >= pkv_q8_prefill_workspace_bytes(desc) bytes, 16-byte aligned, memory of
- *                 the current device; calls that overlap on the GPU must not share one
+ *                 the current device, its first PKV_ARRIVAL_BYTES as in pkv_q8_decode_attention; calls
+ *                 that overlap on the GPU must not share one
  */
 int pkv_q8_prefill_attention(const pkv_cache_desc* desc, int32_t layer, const void* q, const void* k_codes,
                              const void* v_codes, const float* k_scales, const float* v_scales,

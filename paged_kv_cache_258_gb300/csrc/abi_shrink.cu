@@ -8,6 +8,10 @@ cudaError_t launch_frag_q8_f16(int, int, const FragArgs&, const CUtensorMap&, co
 cudaError_t launch_frag_q8_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_frag_scored_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_frag_scored_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_multi_f16(int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_multi_bf16(int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t frag_multi_ctas_per_sm_f16(int, int*);
+cudaError_t frag_multi_ctas_per_sm_bf16(int, int*);
 cudaError_t frag_ctas_per_sm_q8_f16(int, int, int*);
 cudaError_t frag_ctas_per_sm_q8_bf16(int, int, int*);
 cudaError_t frag_ctas_per_sm_scored_f16(int, int, int*);
@@ -18,18 +22,35 @@ cudaError_t frag_ctas_per_sm(int dtype, bool q8, int head_dim, int group, int* o
     return dtype == PKV_F16 ? frag_ctas_per_sm_scored_f16(head_dim, group, out) : frag_ctas_per_sm_scored_bf16(head_dim, group, out);
 }
 
-cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, const FragArgs& a, cudaStream_t stream) {
+namespace {
+cudaError_t layer_maps(const FragArgs& a, int head_dim, int type, CUtensorMap* tk, CUtensorMap* tv) {
     const long long rows = (long long)a.d.num_blocks * a.d.n_kv * kBlock;
-    const int type = q8 ? kCodesE4M3 : dtype;
+    const cudaError_t err = kv_tensor_map(a.d.k_layer, rows, head_dim, type, PKV_BOX_PANEL, tk);
+    return err != cudaSuccess ? err : kv_tensor_map(a.d.v_layer, rows, head_dim, type, PKV_BOX_PANEL, tv);
+}
+}  // namespace
+
+cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, const FragArgs& a, cudaStream_t stream) {
     CUtensorMap tk, tv;
-    cudaError_t err = kv_tensor_map(a.d.k_layer, rows, head_dim, type, PKV_BOX_PANEL, &tk);
-    if (err == cudaSuccess) err = kv_tensor_map(a.d.v_layer, rows, head_dim, type, PKV_BOX_PANEL, &tv);
+    const cudaError_t err = layer_maps(a, head_dim, q8 ? kCodesE4M3 : dtype, &tk, &tv);
     if (err != cudaSuccess) return err;
     if (q8)
         return dtype == PKV_F16 ? launch_frag_q8_f16(head_dim, group, a, tk, tv, stream)
                                 : launch_frag_q8_bf16(head_dim, group, a, tk, tv, stream);
     return dtype == PKV_F16 ? launch_frag_scored_f16(head_dim, group, a, tk, tv, stream)
                             : launch_frag_scored_bf16(head_dim, group, a, tk, tv, stream);
+}
+
+cudaError_t frag_multi_ctas_per_sm(int dtype, int head_dim, int* out) {
+    return dtype == PKV_F16 ? frag_multi_ctas_per_sm_f16(head_dim, out) : frag_multi_ctas_per_sm_bf16(head_dim, out);
+}
+
+cudaError_t launch_frag_multi(int dtype, int head_dim, const FragArgs& a, cudaStream_t stream) {
+    CUtensorMap tk, tv;
+    const cudaError_t err = layer_maps(a, head_dim, kCodesE4M3, &tk, &tv);
+    if (err != cudaSuccess) return err;
+    return dtype == PKV_F16 ? launch_frag_multi_f16(head_dim, a, tk, tv, stream)
+                            : launch_frag_multi_bf16(head_dim, a, tk, tv, stream);
 }
 
 }  // namespace pkv
@@ -62,21 +83,26 @@ struct FragGeometry {
     int ctas, partition;  // CTAs along x; blocks of a partition, 0 for runs
 };
 
+FragGeometry geometry_of(long long pairs, int max_blocks, int sms, int per_sm, int max_runs) {
+    FragGeometry geo;
+    const long long parts = pairs >= sms ? 1 : sms / pairs < kMaxCluster ? sms / pairs : kMaxCluster;
+    const int partition = (int)((max_blocks + parts - 1) / parts);
+    if (pairs <= sms && partition <= pkv::kMaxPartition) {
+        geo.partition = partition < pkv::kMinRun ? pkv::kMinRun : partition;
+        geo.ctas = pkv::decode_partitions(max_blocks, geo.partition);
+    } else {
+        geo.partition = 0;
+        geo.ctas = sms * per_sm < max_runs ? sms * per_sm : max_runs;
+    }
+    return geo;
+}
+
 cudaError_t frag_geometry(const pkv_cache_desc* d, bool q8, int n_seqs, int max_blocks, FragGeometry* out) {
     int sms = 0, per_sm = 0;
     cudaError_t err = pkv::current_sm_count(&sms);
     if (err == cudaSuccess) err = pkv::frag_ctas_per_sm(d->dtype, q8, d->head_dim, group_of(d), &per_sm);
     if (err != cudaSuccess) return err;
-    const long long pairs = (long long)n_seqs * d->n_kv_heads;
-    const long long parts = pairs >= sms ? 1 : sms / pairs < kMaxCluster ? sms / pairs : kMaxCluster;
-    const int partition = (int)((max_blocks + parts - 1) / parts);
-    if (pairs <= sms && partition <= pkv::kMaxPartition) {
-        out->partition = partition < pkv::kMinRun ? pkv::kMinRun : partition;
-        out->ctas = pkv::decode_partitions(max_blocks, out->partition);
-    } else {
-        out->partition = 0;
-        out->ctas = sms * per_sm < pkv::kMaxRuns ? sms * per_sm : pkv::kMaxRuns;
-    }
+    *out = geometry_of((long long)n_seqs * d->n_kv_heads, max_blocks, sms, per_sm, pkv::kMaxRuns);
     return cudaSuccess;
 }
 
@@ -185,6 +211,36 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     return PKV_OK;
 }
 
+// Workspace of prefill: arrival counters, the runs' partials, one layer of K and V in 16 bits.
+struct ChunkLayout {
+    size_t o, ml, k, v, bytes;
+};
+ChunkLayout chunk_layout(const pkv_cache_desc* d) {
+    const size_t partials = (size_t)pkv::kChunkRuns * 2 * 8, layer = layer_elems(d) * 2;
+    ChunkLayout l;
+    l.o = PKV_ARRIVAL_BYTES;
+    l.ml = l.o + partials * d->head_dim * sizeof(float);
+    l.k = l.ml + partials * sizeof(float2);
+    l.v = l.k + layer;
+    l.bytes = l.v + layer;
+    return l;
+}
+
+// Whether a chunk is attended to group by group (8 / G tokens at a time, each reading the codes again) or
+// widened first and handed to the tensor-memory kernel of 16-bit pools. Nanoseconds per context token:
+// a group's read of a token (measured: 3.8, 6.7 and 8.5 TB/s of codes at head_dim 64, 128 and 256) against
+// that kernel's waves of 128-key tiles (1.0 us, 1.28 at 256), one CTA of 128 rows an SM, plus the widening's
+// three bytes a code. The context's length, which both scale with, drops out. 20,000 tokens, 8 heads x 4 x
+// 128: chunks of 1, 8, 32 and 64 tokens take 20, 34, 98 and 185 us by groups, 168 us each the other way.
+bool by_groups(const pkv_cache_desc* d, int n_seqs, int n_tokens, int max_query, int sms) {
+    const double G = group_of(d), per_group = 8 / G, row = 2.0 * d->head_dim * d->n_kv_heads;
+    const double groups = n_tokens / per_group + n_seqs * (1 - 1 / per_group);
+    const long long ctas = (long long)n_seqs * d->n_kv_heads * ((max_query * group_of(d) + 127) / 128);
+    const double waves = (double)((ctas + sms - 1) / sms);
+    const double rate = d->head_dim == 64 ? 3800 : d->head_dim == 128 ? 6700 : 8500;  // bytes a ns
+    return groups * row / rate < waves * (d->head_dim == 256 ? 1280.0 : 1000.0) / 128 + n_seqs * row * 3 / 6000.0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -280,7 +336,7 @@ int pkv_paged_decode_attention_scored(const pkv_cache_desc* d, int32_t layer, co
 }
 
 size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* d) {
-    return validate16(d) == PKV_OK ? 2 * layer_elems(d) * 2 : 0;
+    return validate16(d) == PKV_OK ? chunk_layout(d).bytes : 0;
 }
 
 int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void* q, const void* k_codes,
@@ -301,26 +357,72 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||
         !aligned4(v_scales))
         return PKV_ERR_INVALID_ARG;
-    const size_t need = pkv_q8_prefill_workspace_bytes(d);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return PKV_ERR_INVALID_ARG;
+    const ChunkLayout l = chunk_layout(d);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < l.bytes) return PKV_ERR_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    const uint8_t* k_layer = static_cast<const uint8_t*>(k_codes) + layer_elems(d) * layer;
+    const uint8_t* v_layer = static_cast<const uint8_t*>(v_codes) + layer_elems(d) * layer;
+    k_scales += layer_scales(d) * layer;
+    v_scales += layer_scales(d) * layer;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int group = group_of(d), per_group = 8 / group, groups = (max_query_len + per_group - 1) / per_group;
+    unsigned int* status = nullptr;
+    int sms = 0;
+    if (pkv::device_status_word(&status) != cudaSuccess || pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+
+    if ((long long)n_seqs * groups <= 65535 && by_groups(d, n_seqs, n_tokens, max_query_len, sms)) {
+        int per_sm = 0;
+        if (pkv::frag_multi_ctas_per_sm(d->dtype, d->head_dim, &per_sm) != cudaSuccess) return PKV_ERR_CUDA;
+        const FragGeometry geo =
+            geometry_of((long long)n_seqs * groups * d->n_kv_heads, max_blocks_per_seq, sms, per_sm, pkv::kChunkRuns);
+        pkv::FragArgs a;
+        a.d.q = q;
+        a.d.k_layer = k_layer;
+        a.d.v_layer = v_layer;
+        a.d.tables = block_tables;
+        a.d.lens = context_lens;
+        a.d.out = out;
+        a.d.part_o = reinterpret_cast<float*>(ws + l.o);
+        a.d.part_ml = reinterpret_cast<float*>(ws + l.ml);
+        a.d.status = status;
+        a.d.n_seqs = n_seqs * groups;
+        a.d.n_q = d->n_q_heads;
+        a.d.n_kv = d->n_kv_heads;
+        a.d.num_blocks = d->num_blocks;
+        a.d.max_blocks = max_blocks_per_seq;
+        a.d.n_parts = geo.ctas;
+        a.d.scale_log2 = scale * 1.4426950408889634f;
+        a.arrivals = reinterpret_cast<unsigned int*>(ws);
+        a.k_scales = k_scales;
+        a.v_scales = v_scales;
+        a.q_start = query_start;
+        a.n_tokens = n_tokens;
+        a.max_query = max_query_len;
+        a.groups = groups;
+        a.shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
+        a.partition = geo.partition;
+        const cudaError_t err = pkv::launch_frag_multi(d->dtype, d->head_dim, a, st);
+        if (err != cudaSuccess) return pkv::launch_status(err);
+        pkv::count_launches(1);
+        return PKV_OK;
+    }
 
     pkv::Q8WidenArgs w;
-    w.k_codes = static_cast<const uint8_t*>(k_codes) + layer_elems(d) * layer;
-    w.v_codes = static_cast<const uint8_t*>(v_codes) + layer_elems(d) * layer;
-    w.k_scales = k_scales + layer_scales(d) * layer;
-    w.v_scales = v_scales + layer_scales(d) * layer;
+    w.k_codes = k_layer;
+    w.v_codes = v_layer;
+    w.k_scales = k_scales;
+    w.v_scales = v_scales;
     w.tables = block_tables;
     w.lens = context_lens;
-    w.k_out = workspace;
-    w.v_out = static_cast<char*>(workspace) + need / 2;
+    w.k_out = ws + l.k;
+    w.v_out = ws + l.v;
     w.n_seqs = n_seqs;
     w.n_kv = d->n_kv_heads;
     w.num_blocks = d->num_blocks;
     w.max_blocks = max_blocks_per_seq;
-    if (pkv::device_status_word(&w.status) != cudaSuccess) return PKV_ERR_CUDA;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    w.status = status;
     // the attention of 16-bit pools over the widened layer, a pool of one layer with the same blocks
-    const int per_cta = pkv::prefill_tokens_per_cta(d->dtype, d->head_dim, group_of(d));
+    const int per_cta = pkv::prefill_tokens_per_cta(d->dtype, d->head_dim, group);
     pkv::PrefillArgs a;
     a.q = q;
     a.out = out;
@@ -329,7 +431,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     a.tables = block_tables;
     a.lens = context_lens;
     a.q_start = query_start;
-    a.status = w.status;
+    a.status = status;
     a.n_seqs = n_seqs;
     a.n_q = d->n_q_heads;
     a.n_kv = d->n_kv_heads;
@@ -340,7 +442,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     a.scale_log2 = scale * 1.4426950408889634f;
     if (pkv::launch_q8_widen(d->dtype, d->head_dim, w, st) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::count_launches(1);
-    cudaError_t err = pkv::launch_prefill(d->dtype, d->head_dim, group_of(d), a, st);
+    const cudaError_t err = pkv::launch_prefill(d->dtype, d->head_dim, group, a, st);
     if (err != cudaSuccess) return pkv::launch_status(err);
     pkv::count_launches(1);
     return PKV_OK;

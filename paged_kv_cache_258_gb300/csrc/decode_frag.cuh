@@ -18,6 +18,10 @@
 // (partition, head, sequence) instead, the partitions of a context being a thread-block cluster that
 // joins through shared memory.
 //
+// Short prompt chunks over an 8-bit pool run here too (MULTI): the eight query columns of an instruction
+// hold 8 / G tokens x G heads, a "sequence" of the list is such a group of tokens, and each column has
+// its own causal limit. Every group reads the context again, mostly from L2.
+//
 // Per-warp rings of TMA copies feed the warps as in decode_mma.cuh. What differs is how a 16-token tile
 // gets from shared memory into fragments:
 //  * The contraction of S = K Q^T runs over head dims in any order, as long as Q's fragment uses the
@@ -124,11 +128,33 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// An output before its rounding. Rows near 65,504 are held as 65,536, which fp16 has no room for: means up
+// to there come out as the largest half.
+template <typename T>
+__device__ __forceinline__ float in_range(float x) {
+    if constexpr (std::is_same<T, __half>::value) return fabsf(x) <= 65536.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+    return x;
+}
+
 // f * v, rounded, to four consecutive elements.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float4 v, float f) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(MmaType<T>::pack(v.x * f, v.y * f), MmaType<T>::pack(v.z * f, v.w * f));
+    *reinterpret_cast<uint2*>(p) = make_uint2(MmaType<T>::pack(in_range<T>(v.x * f), in_range<T>(v.y * f)),
+                                              MmaType<T>::pack(in_range<T>(v.z * f), in_range<T>(v.w * f)));
 }
+
+// The pair's rows in q or out: row r is head r of the sequence's row, or (MULTI) head r mod 2^shift of
+// token r / 2^shift, for r < rows.
+template <typename P, int D, bool MULTI>
+struct PairRows {
+    P* base;
+    int n_q, shift, rows;
+    __device__ __forceinline__ bool has(int r) const { return !MULTI || r < rows; }
+    __device__ __forceinline__ P* row(int r) const {
+        if constexpr (!MULTI) return base + (size_t)r * D;
+        return base + ((size_t)(r >> shift) * n_q + (r & ((1 << shift) - 1))) * D;
+    }
+};
 
 // Four consecutive elements of a query row, widened.
 template <typename T>
@@ -159,8 +185,9 @@ __device__ __forceinline__ int partial_slot(int first, int i) { return i == 0 ? 
 // The arrival counter wraps to 0 with the last arrival (atomicInc), so it is ready for the next call; it
 // belongs to the pair's first CTA and always lies at the same place of the workspace. An addition, not a
 // compare-and-swap: the CTAs of one wave end together, and retries would queue at an L2 round trip each.
-template <typename T, int D, int G, int NT>
-__device__ __forceinline__ void join_if_last(const FragArgs& fa, size_t row0, int first, int np, float* scratch) {
+template <typename T, int D, int G, int NT, bool MULTI>
+__device__ __forceinline__ void join_if_last(const FragArgs& fa, const PairRows<T, D, MULTI>& out, float2* row_ml, int first,
+                                             int np, float* scratch) {
     const DecodeArgs& a = fa.d;
     constexpr int NWARP = NT / 32;
     constexpr int PER = (G * D / 4 + NT - 1) / NT;  // groups of four outputs of a thread
@@ -262,11 +289,12 @@ __device__ __forceinline__ void join_if_last(const FragArgs& fa, size_t row0, in
     for (int k = 0; k < PER; ++k) {
         const int i4 = threadIdx.x + k * NT;
         if (i4 < G * D / 4) {
-            const float L = sL[i4 / (D / 4)];
-            store4(reinterpret_cast<T*>(a.out) + row0 * D + 4 * i4, O[k], L == 0.f ? 0.f : 1.f / L);
+            const int r = i4 / (D / 4);
+            const float L = sL[r];
+            if (out.has(r)) store4(out.row(r) + 4 * (i4 % (D / 4)), O[k], L == 0.f ? 0.f : 1.f / L);
         }
     }
-    if (fa.row_ml && threadIdx.x < G) fa.row_ml[row0 + threadIdx.x] = make_float2(sM[threadIdx.x], sL[threadIdx.x]);
+    if (row_ml && threadIdx.x < G) row_ml[threadIdx.x] = make_float2(sM[threadIdx.x], sL[threadIdx.x]);
 }
 
 // The same join for a cluster of a pair's partitions, through the CTAs' shared memory: no trip to L2 for
@@ -287,8 +315,8 @@ __device__ __forceinline__ float cluster_load(uint32_t a) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-template <typename T, int D, int G, int NT>
-__device__ __forceinline__ void cluster_join(T* out, int p, int np, const float* ml, const float* po, float* s_max,
+template <typename T, int D, int G, int NT, bool MULTI>
+__device__ __forceinline__ void cluster_join(const PairRows<T, D, MULTI>& out, int p, int np, const float* ml, const float* po, float* s_max,
                                              float* s_sum) {
     cluster_barrier();
     const uint32_t ml0 = smem_addr(ml), po0 = smem_addr(po);
@@ -321,7 +349,7 @@ __device__ __forceinline__ void cluster_join(T* out, int p, int np, const float*
         row(idx / D, w, &M, &L);
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) O = fmaf(o[q], w[q], O);
-        out[idx] = from_float<T>(L == 0.f ? 0.f : O / L);
+        if (out.has(idx / D)) out.row(idx / D)[idx % D] = from_float<T>(in_range<T>(L == 0.f ? 0.f : O / L));
     }
     if (s_max && threadIdx.x < G) {
         row(threadIdx.x, w, &M, &L);
@@ -331,11 +359,11 @@ __device__ __forceinline__ void cluster_join(T* out, int p, int np, const float*
     cluster_barrier();  // no CTA leaves while another reads its shared memory; the statistics are written
 }
 
-template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS>
+template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS, bool MULTI>
 __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragArgs fa,
                                                                     const __grid_constant__ CUtensorMap tm_k,
                                                                     const __grid_constant__ CUtensorMap tm_v) {
-    static_assert(G <= 8, "at most 8 query rows per KV head");
+    static_assert(G <= 8 && (!MULTI || (Q8 && G == 8)), "at most 8 query rows per KV head");
     static_assert(BPI == 1 || BPI == 2 || BPI == 4, "blocks per iteration");
     using S = FragGeom<Q8, D, G, NW, ST, BPI>;
     using MT = typename std::conditional<Q8, __half, T>::type;  // type of the matrix instructions' operands
@@ -367,7 +395,26 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]
     const uint32_t wstage = smem_addr(smem) + (uint32_t)(warp * ST) * S::STAGE;
     const uint64_t policy = l2_evict_first_policy();
-    auto length = [&](int seq) -> int { return min(max(a.lens[seq], 0), cap); };
+    // Sequence s of the list: its row of the table, the positions it sees; MULTI: its first token (a row of
+    // q and out), how many it has, and how many positions the first one sees.
+    struct Seq {
+        int ctx, row, tok0, tokens, first;
+    };
+    auto seq_of = [&](int i) -> Seq {
+        if constexpr (!MULTI) {
+            return Seq{min(max(a.lens[i], 0), cap), i, i, 1, 0};
+        } else {
+            const int row = i / fa.groups, j0 = i % fa.groups * (G >> fa.shift);
+            const int c = a.lens[row];
+            const long long q0 = fa.q_start[row], n = fa.q_start[row + 1] - q0;
+            const bool bad = q0 < 0 || n < 0 || n > fa.max_query || q0 + n > fa.n_tokens || n > c || c > cap;
+            if (bad && j0 == 0 && blockIdx.x == 0 && threadIdx.x % 32 == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_QUERY_RANGE);
+            if (bad || j0 >= n) return Seq{0, row, 0, 0, 0};
+            const int tokens = min(G >> fa.shift, (int)n - j0), first = c - (int)n + j0 + 1;
+            return Seq{first + tokens - 1, row, (int)q0 + j0, tokens, first};
+        }
+    };
+    auto length = [&](int i) -> int { return seq_of(i).ctx; };
     auto blocks_of = [&](int len) -> int { return (len + kBlock - 1) / kBlock; };
     // places a pair of so many blocks takes in the list: first its cost, then its blocks
     auto span_of = [](int blocks) -> int { return blocks > 0 ? blocks + kPairCost<Q8> : 0; };
@@ -384,12 +431,12 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         s = blockIdx.z;
         g = blockIdx.y;
         b = blockIdx.x * fa.partition;
-        if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0 && (a.lens[s] < 0 || a.lens[s] > cap))
+        if (!MULTI && threadIdx.x == 0 && blockIdx.x == 0 && g == 0 && (a.lens[s] < 0 || a.lens[s] > cap))
             atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
         ctx = length(s);
         const int nb = blocks_of(ctx);
         if (b >= nb) {
-            if (b == 0) zero_row((size_t)s * a.n_q + (size_t)g * G, G);
+            if (!MULTI && b == 0) zero_row((size_t)s * a.n_q + (size_t)g * G, G);
             return;
         }
         x = b;
@@ -401,9 +448,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         const int i0 = min((int)threadIdx.x * per_t, a.n_seqs), i1 = min(i0 + per_t, a.n_seqs);
         long long mine = 0;
         for (int i = i0; i < i1; ++i) {
-            const int len = a.lens[i];
-            if (blockIdx.x == 0 && (len < 0 || len > cap)) atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
-            mine += span_of(blocks_of(min(max(len, 0), cap)));
+            if (!MULTI && blockIdx.x == 0 && (a.lens[i] < 0 || a.lens[i] > cap))
+                atomicOr(a.status, (unsigned)PKV_DEV_BAD_CONTEXT_LEN);
+            mine += span_of(blocks_of(length(i)));
         }
         long long before = mine;
 #pragma unroll
@@ -435,7 +482,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             s_find[NW] = i;
             s_find[NW + 1] = x - before * a.n_kv;
         }
-        for (int i = blockIdx.x; i < a.n_seqs; i += gridDim.x)
+        for (int i = blockIdx.x; !MULTI && i < a.n_seqs; i += gridDim.x)
             if (a.lens[i] <= 0) zero_row((size_t)i * a.n_q, a.n_q);
         __syncthreads();
         if (x >= x_end) return;
@@ -461,13 +508,17 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     while (true) {  // one pair (s, g), blocks [b, b + nblk) of its nb
         const int nb = blocks_of(ctx);
         const int nblk = (int)min(x_end - x, (long long)(nb - b));
-        const size_t row0 = (size_t)s * a.n_q + (size_t)g * G;
+        const Seq seq = seq_of(s);
+        const size_t row0 = MULTI ? (size_t)seq.tok0 * a.n_q + (size_t)g * (1 << fa.shift) : (size_t)s * a.n_q + (size_t)g * G;
+        const PairRows<const T, D, MULTI> q_rows{reinterpret_cast<const T*>(a.q) + row0 * D, a.n_q, fa.shift,
+                                                 seq.tokens << fa.shift};
+        const PairRows<T, D, MULTI> out_rows{reinterpret_cast<T*>(a.out) + row0 * D, a.n_q, fa.shift, q_rows.rows};
 
         // This warp's i-th block (i = BPI k + u) is block BPI (warp + k NW) + u of the run's share. Table
         // entries come in chunks of 32 held in registers (lane l: entry 32 c + l): the chunk whose copies
         // are being issued, the next, and the one after; scales follow a chunk behind the tables.
         auto local_block = [&](int i) -> int { return (i / BPI) * (NW * BPI) + warp * BPI + i % BPI; };
-        const int32_t* table = a.tables + (size_t)s * a.max_blocks + b;
+        const int32_t* table = a.tables + (size_t)seq.row * a.max_blocks + b;
         auto load_chunk = [&](int c) -> int {
             const int lb = local_block(c * 32 + lane);
             return lb < nblk ? table[lb] : -1;
@@ -478,11 +529,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         constexpr int PER = KSTEPS / S::KCH;  // k-steps per chunk of a K row
         uint2 qraw[KSTEPS];                   // the query row's words, on their way while the first tiles are
         {
-            const T* qrow = reinterpret_cast<const T*>(a.q) + (row0 + gid) * D;
+            const T* qrow = q_rows.row(gid);
 #pragma unroll
             for (int i = 0; i < KSTEPS; ++i) {
                 qraw[i] = make_uint2(0u, 0u);
-                if (gid < G)
+                if (gid < G && q_rows.has(gid))
                     qraw[i] = __ldg(reinterpret_cast<const uint2*>(
                         qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) + (i % PER) * 4));
             }
@@ -501,7 +552,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                 while (ctx_next == 0);
             }
             const int n = blocks_of(ctx_next), lb = local_block(lane);
-            t_next = lb < n ? a.tables[(size_t)s_next * a.max_blocks + lb] : -1;
+            t_next = lb < n ? a.tables[(size_t)(MULTI ? s_next / fa.groups : s_next) * a.max_blocks + lb] : -1;
         }
 
         struct Blocks {
@@ -701,6 +752,14 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                     z[u][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
                     z[u][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
                     z[u][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
+                    if constexpr (MULTI) {  // each column's token sees the positions up to its own
+                        const int pos = jb + u * kBlock + gid;
+                        const int e0 = seq.first + (2 * tig >> fa.shift), e1 = seq.first + (2 * tig + 1 >> fa.shift);
+                        if (pos >= e0) z[u][0] = -INFINITY;
+                        if (pos >= e1) z[u][1] = -INFINITY;
+                        if (pos + 8 >= e0) z[u][2] = -INFINITY;
+                        if (pos + 8 >= e1) z[u][3] = -INFINITY;
+                    }
                 }
                 // ---- online softmax ----
                 float mx0 = -INFINITY, mx1 = -INFINITY;
@@ -845,6 +904,49 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                             for (int x = 0; x < WORDS; ++x)
                                 w[j][x] = 2 * tig + (j & 1) + 8 * (j >> 1) < nvalid[u] ? w[j][x] : 0u;
                     }
+                    if constexpr (MULTI) {
+                        // A NaN in a row that only some of the group's tokens see would reach the others as 0 x NaN:
+                        // such a panel goes token by token, each with the rows behind its own removed.
+                        bool nan = false;
+                        if (jb + (u + 1) * kBlock > seq.first) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int x = 0; x < WORDS; ++x)
+                                    nan = nan || __vcmpeq4(w[j][x] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+                        }
+                        if (__any_sync(0xffffffffu, nan)) {
+                            for (int i = 0; i < seq.tokens; ++i) {
+                                const int seen = seq.first + i - (jb + u * kBlock);  // rows of the block that token i sees
+                                const bool c0 = 2 * tig >> fa.shift == i, c1 = (2 * tig + 1) >> fa.shift == i;
+#pragma unroll
+                                for (int x = 0; x < WORDS; ++x) {
+                                    uint32_t v[4];
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) v[j] = 2 * tig + (j & 1) + 8 * (j >> 1) < seen ? w[j][x] : 0u;
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const uint32_t sel = h ? 0x7362u : 0x5140u;
+                                        const uint32_t x01 = __byte_perm(v[0], v[1], sel), x23 = __byte_perm(v[2], v[3], sel);
+                                        const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
+                                                                e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
+                                        float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                        M::mma(part, af, b0f[u], b1f[u]);
+                                        float* to = acc[(pn * WORDS + x) * 2 + h];
+                                        if (c0) {
+                                            to[0] += part[0];
+                                            to[2] += part[2];
+                                        }
+                                        if (c1) {
+                                            to[1] += part[1];
+                                            to[3] += part[3];
+                                        }
+                                    }
+                                }
+                            }
+                            continue;
+                        }
+                    }
 #pragma unroll
                     for (int x = 0; x < WORDS; ++x) {
                         if constexpr (Q8) {
@@ -949,7 +1051,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             }
             if (np == 1) {
                 const float L = s_sum[r];
-                store4(reinterpret_cast<T*>(a.out) + row0 * D + 4 * i4, O, L == 0.f ? 0.f : 1.f / L);
+                if (out_rows.has(r)) store4(out_rows.row(r) + 4 * (i4 % (D / 4)), O, L == 0.f ? 0.f : 1.f / L);
             } else if (fa.partition > 0) {
                 reinterpret_cast<float4*>(s_po)[i4] = O;
             } else {
@@ -968,8 +1070,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         }
         if (fa.partition > 0) {
             if (np > 1)
-                cluster_join<T, D, G, NW * 32>(reinterpret_cast<T*>(a.out) + row0 * D, (int)blockIdx.x, np, s_pml, s_po,
-                                               fa.scores ? s_max : nullptr, s_sum);
+                cluster_join<T, D, G, NW * 32, MULTI>(out_rows, (int)blockIdx.x, np, s_pml, s_po,
+                                                      fa.scores ? s_max : nullptr, s_sum);
             if (fa.scores) {  // weights of the partition's own positions (the barriers above order the logits)
                 float* to = fa.scores + ((size_t)s * a.n_kv + g) * fa.score_stride + z0;
                 for (int j = threadIdx.x; j < z_end - z0; j += NW * 32) {
@@ -984,7 +1086,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             }
             return;
         }
-        if (np > 1) join_if_last<T, D, G, NW * 32>(fa, row0, first, np, reinterpret_cast<float*>(smem + S::MERGE));
+        if (np > 1)
+            join_if_last<T, D, G, NW * 32, MULTI>(fa, out_rows, fa.row_ml ? fa.row_ml + row0 : nullptr, first, np,
+                                                  reinterpret_cast<float*>(smem + S::MERGE));
         x += nblk + kPairCost<Q8>;  // the next pair's first block
         if (x >= x_end) return;
         // the next pair of the run
@@ -998,7 +1102,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     }
 }
 
-template <typename T, bool Q8, int D, int G>
+template <typename T, bool Q8, int D, int G, bool MULTI = false>
 struct FragKernel {
     // Blocks per iteration, CTAs per SM: 64 to 128 KiB of tiles in flight an SM. More is slower (d = 128
     // codes, 10 x 30,000 tokens, 8 x 4 heads: 64 KiB 105 us, 96 KiB 99, 128 KiB 103, 192 KiB 115).
@@ -1009,7 +1113,7 @@ struct FragKernel {
     static constexpr size_t smem = FragGeom<Q8, D, G, NW, ST, BPI>::ALLOC;
     static unsigned long long attr_done;
     static int resident[64];
-    static constexpr auto kernel = frag_decode_kernel<T, Q8, D, G, NW, ST, BPI, CTAS>;
+    static constexpr auto kernel = frag_decode_kernel<T, Q8, D, G, NW, ST, BPI, CTAS, MULTI>;
     static cudaError_t prepare() { return allow_dynamic_smem(kernel, smem + kMaxPartition * kBlock * G * sizeof(float), &attr_done); }
     // CTAs one SM of the current device holds at once; asked of the occupancy calculator once per device
     static cudaError_t ctas_per_sm(int* out) {
@@ -1036,10 +1140,10 @@ struct FragKernel {
         return launch_dependent(kernel, grid, NW * 32, smem + logits, stream, a.partition > 0 ? a.d.n_parts : 1, a, tk, tv);
     }
 };
-template <typename T, bool Q8, int D, int G>
-unsigned long long FragKernel<T, Q8, D, G>::attr_done = 0;
-template <typename T, bool Q8, int D, int G>
-int FragKernel<T, Q8, D, G>::resident[64] = {};
+template <typename T, bool Q8, int D, int G, bool MULTI>
+unsigned long long FragKernel<T, Q8, D, G, MULTI>::attr_done = 0;
+template <typename T, bool Q8, int D, int G, bool MULTI>
+int FragKernel<T, Q8, D, G, MULTI>::resident[64] = {};
 
 #define PKV_FRAG_CASES                                                  \
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)     \
@@ -1063,6 +1167,28 @@ cudaError_t launch_frag_of(int head_dim, int group, const FragArgs& a, const CUt
     PKV_FRAG_CASES
 #undef PKV_CASE
     return cudaErrorInvalidValue;
+}
+
+// Prompt chunks (MULTI): eight columns whatever the group is.
+template <typename T>
+cudaError_t frag_multi_ctas_per_sm_of(int head_dim, int* out) {
+    switch (head_dim) {
+    case 64: return FragKernel<T, true, 64, 8, true>::ctas_per_sm(out);
+    case 128: return FragKernel<T, true, 128, 8, true>::ctas_per_sm(out);
+    case 256: return FragKernel<T, true, 256, 8, true>::ctas_per_sm(out);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+template <typename T>
+cudaError_t launch_frag_multi_of(int head_dim, const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 cudaStream_t stream) {
+    switch (head_dim) {
+    case 64: return FragKernel<T, true, 64, 8, true>::launch(a, tk, tv, stream);
+    case 128: return FragKernel<T, true, 128, 8, true>::launch(a, tk, tv, stream);
+    case 256: return FragKernel<T, true, 256, 8, true>::launch(a, tk, tv, stream);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace pkv

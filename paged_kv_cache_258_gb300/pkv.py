@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "ok", 1: "invalid", 2: "unsupported", 3: "no_blocks", 4: "bad
 PKV_DEV_BAD_BLOCK_ID, PKV_DEV_BAD_CONTEXT_LEN, PKV_DEV_BAD_SLOT, PKV_DEV_BAD_PAIR, PKV_DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 PKV_DEV_BAD_QUERY_RANGE = 32
 PKV_DEV_BAD_KEEP = 64
+PKV_ARRIVAL_BYTES = 8192
 PKV_DECODE_OVERLAP_PREVIOUS = 1
 PKV_PREFILL_OVERLAP_PREVIOUS = 1
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
@@ -637,7 +638,11 @@ def _table_width(block_tables) -> int:
 
 def _bytes_tensor(n: int, device):
     t = _torch()
-    return t.zeros(-(-n // 16) * 4, dtype=t.float32, device=device) if n else None
+    if not n:
+        return None
+    buf = t.empty(-(-n // 16) * 4, dtype=t.float32, device=device)
+    buf[:PKV_ARRIVAL_BYTES // 4].zero_()
+    return buf
 
 
 def pkv_q8_pool_bytes(desc: CacheDesc) -> int:

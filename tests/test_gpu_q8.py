@@ -357,7 +357,7 @@ def test_prefill_matches(dtype, d, G):
     q, qf = values(rng, (112, G * n_kv, d), dtype)
     out = torch.full((112, G * n_kv, d), 7.0, dtype=pkv.torch_dtype(dtype), device="cuda")
     ws = pkv.alloc_q8_prefill_workspace(desc)
-    ws.fill_(float("nan"))
+    ws[COUNTERS:].fill_(float("nan"))
     scale = 1 / np.sqrt(d) / 16
     pkv.pkv_q8_prefill_attention(desc, 0, to_torch(q, dtype), t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"],
                                  torch.from_numpy(start).cuda(), 63, scale, out, ws)
@@ -375,19 +375,122 @@ def test_prefill_matches(dtype, d, G):
             assert np.all(np.abs(got[row] - want[0]) <= 2 * tol[0]), (s, i)
 
 
-def test_prefill_reads_the_largest_halves():
-    """65,504 is held as 65,536 in codes; prefill reads it as 65,504, decode as what the code stands for."""
+@pytest.mark.parametrize("n", [1, 2000])
+def test_the_largest_halves_stay_finite(n):
+    """65,504 is held as 65,536 in codes; attention gives 65,504 back: decode, short and long chunks."""
     d = 64
-    desc = pkv.make_desc("f16", 1, 2, 1, 1, d)
+    nb = -(-n // 16)
+    desc = pkv.make_desc("f16", 1, nb, 1, 1, d)
     kc = torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
-    vc, sc = torch.zeros_like(kc.view(torch.uint8)).view(torch.float8_e4m3fn), torch.zeros(pkv.scale_shape(desc), device="cuda")
-    sv = torch.zeros_like(sc)
-    x = torch.full((1, 1, d), 65504.0, dtype=torch.float16, device="cuda")
-    pkv.pkv_q8_append(desc, 0, x, x, torch.zeros(1, dtype=torch.int64, device="cuda"), kc, vc, sc, sv)
-    tables, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    vc = torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sc, sv = torch.zeros((2, *pkv.scale_shape(desc)), device="cuda")
+    x = torch.full((n, 1, d), 65504.0, dtype=torch.float16, device="cuda")
+    pkv.pkv_q8_append(desc, 0, x, x, torch.arange(n, device="cuda"), kc, vc, sc, sv)
+    assert torch.all(sv == 256.0)
+    tables = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    lens = torch.full((1,), n, dtype=torch.int32, device="cuda")
     out = torch.empty((1, 1, d), dtype=torch.float16, device="cuda")
-    q = torch.zeros_like(x)
-    pkv.pkv_q8_prefill_attention(desc, 0, q, kc, vc, sc, sv, tables, lens, torch.tensor([0, 1], dtype=torch.int32).cuda(), 1,
-                                 1.0, out, pkv.alloc_q8_prefill_workspace(desc))
+    pkv.pkv_q8_decode_attention(desc, 0, torch.zeros_like(out), kc, vc, sc, sv, tables, lens, 1.0, out,
+                                pkv.alloc_q8_workspace(desc, 1, nb))
     assert torch.all(out == 65504.0)
-    assert float(sv[0, 0, 0]) == 256.0
+    for m in {1, n}:
+        out = torch.empty((m, 1, d), dtype=torch.float16, device="cuda")
+        pkv.pkv_q8_prefill_attention(desc, 0, torch.zeros_like(out), kc, vc, sc, sv, tables, lens,
+                                     torch.tensor([0, m], dtype=torch.int32).cuda(), m, 1.0, out,
+                                     pkv.alloc_q8_prefill_workspace(desc))
+        assert torch.all(out == 65504.0)
+
+
+def prefill(desc, t, q, lens, counts, scale, dtype, extra_rows=0):
+    """(outputs of a prefill call as float64, kernels launched)"""
+    start = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    out = torch.full((int(start[-1]) + extra_rows, *q.shape[1:]), 7.0, dtype=pkv.torch_dtype(dtype), device="cuda")
+    ws = pkv.alloc_q8_prefill_workspace(desc)
+    ws[COUNTERS:].fill_(float("nan"))
+    before = pkv.pkv_launch_count()
+    pkv.pkv_q8_prefill_attention(desc, 0, to_torch(q, dtype), t["k"], t["v"], t["ks"], t["vs"], t["tables"],
+                                 torch.from_numpy(np.asarray(lens, dtype=np.int32)).cuda(), torch.from_numpy(start).cuda(),
+                                 int(max(counts)), scale, out, ws)
+    torch.cuda.synchronize()
+    return as_f64(out), pkv.pkv_launch_count() - before
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_short_chunks_over_long_contexts(dtype, d, G):
+    """Chunks that go by groups of 8 / G tokens (one launch): counts around the group's size, an empty
+    chunk, contexts in runs and in partitions."""
+    n_kv = 2
+    for lens, counts in (([3000, 40, 9, 700], [11, 1, 9, 0]), ([130], [3])):
+        desc, t, _, kf, vf, tables, lens = q8_case(dtype, lens, G * n_kv, n_kv, d, seed=3 * d + G)
+        q, qf = values(np.random.default_rng(6), (sum(counts) + 2, G * n_kv, d), dtype)
+        scale = 1 / np.sqrt(d) / 16
+        got, launches = prefill(desc, t, q, lens, counts, scale, dtype, extra_rows=2)
+        assert launches == 1 and pkv.pkv_get_device_status() == 0
+        assert np.all(got[sum(counts):] == 7.0)
+        row = 0
+        for s, n in enumerate(counts):
+            for i in range(n):
+                want, tol, _, _ = R.decode(qf[row:row + 1], np.nan_to_num(kf), np.nan_to_num(vf), tables[s:s + 1],
+                                           np.array([lens[s] - n + i + 1]), scale, dtype, 2.0 ** -11)
+                assert np.all(np.abs(got[row] - want[0]) <= tol[0]), (s, i)
+                row += 1
+
+
+@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_short_chunks_are_causal_about_nan(G, where):
+    """A NaN in the row of one new token reaches that token and the later ones, not the earlier ones."""
+    d, n_kv = 128, 1
+    for length in (2000, 40):
+        desc, t, _, kf, vf, tables, lens = q8_case("bf16", [length], G, n_kv, d, seed=21)
+        bad = length - 3                                   # the third newest token
+        t[where].view(torch.uint8)[0, int(tables[0, bad // 16]), 0, bad % 16, 77] = 0x7F
+        q, _ = values(np.random.default_rng(7), (6, G, d), "bf16")
+        got, launches = prefill(desc, t, q, lens, [6], 0.01, "bf16")
+        assert launches == 1
+        nan = np.isnan(got)
+        assert not nan[:3].any()
+        if where == "k":
+            assert nan[3:].all()
+        else:
+            assert nan[3:, :, 77].all() and not np.delete(nan, 77, axis=2).any()
+
+
+def test_short_chunks_skip_and_flag_bad_ranges():
+    d, n_kv, G = 64, 2, 4
+    desc, t, _, kf, vf, tables, lens = q8_case("f16", [900, 60, 60, 60], G * n_kv, n_kv, d, seed=22)
+    q, qf = values(np.random.default_rng(8), (9, G * n_kv, d), "f16")
+    out = torch.full((9, G * n_kv, d), 7.0, dtype=torch.float16, device="cuda")
+    ws = pkv.alloc_q8_prefill_workspace(desc)
+    lens = np.array([900, 1, 60, tables.shape[1] * 16 + 1], dtype=np.int32)  # two new tokens of one; too long
+    start = np.array([0, 3, 5, 7, 9], dtype=np.int32)
+    args = (t["k"], t["v"], t["ks"], t["vs"], t["tables"], torch.from_numpy(lens).cuda(), torch.from_numpy(start).cuda())
+    pkv.pkv_q8_prefill_attention(desc, 0, to_torch(q, "f16"), *args, 3, 0.01, out, ws)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_QUERY_RANGE
+    got = as_f64(out)
+    assert np.all(got[3:5] == 7.0) and np.all(got[7:] == 7.0)
+    for row, s, p in [(0, 0, 897), (2, 0, 899), (5, 2, 58), (6, 2, 59)]:
+        want, tol, _, _ = R.decode(qf[row:row + 1], np.nan_to_num(kf), np.nan_to_num(vf), tables[s:s + 1], np.array([p + 1]),
+                                   0.01, "f16", 2.0 ** -11)
+        assert np.all(np.abs(got[row] - want[0]) <= tol[0])
+    args[5].fill_(60)
+    pkv.pkv_q8_prefill_attention(desc, 0, to_torch(q, "f16"), *args, 2, 0.01, out, ws)  # the first has three
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_QUERY_RANGE
+
+
+def test_chunk_paths_agree():
+    """The same rows as one long chunk (widened) and as short ones (by groups): equal within both roundings."""
+    d, G, n_kv, length = 128, 4, 2, 600
+    desc, t, _, kf, vf, tables, lens = q8_case("bf16", [length], G * n_kv, n_kv, d, seed=23)
+    q, _ = values(np.random.default_rng(9), (500, G * n_kv, d), "bf16")
+    whole, launches = prefill(desc, t, q, lens, [500], 0.01, "bf16")
+    assert launches == 2
+    for end in (length, length - 64):                     # the last tokens of a shorter context are the chunk
+        at = 500 - (length - end) - 5
+        part, launches = prefill(desc, t, q[at:at + 5], [end], [5], 0.01, "bf16")
+        assert launches == 1
+        # bf16 weights against fp16 ones, both outputs rounded to bf16
+        size = np.abs(np.nan_to_num(vf)).max()
+        assert np.all(np.abs(part - whole[at:at + 5]) <= (2.0 ** -8 + 2.0 ** -11 + 2 * 2.0 ** -8) * size)
