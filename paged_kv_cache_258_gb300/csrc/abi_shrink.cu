@@ -499,14 +499,15 @@ int pkv_evict_tokens(const pkv_cache_desc* d, void* k_pool, void* v_pool, float*
     int sms = 0;
     if (pkv::current_sm_count(&sms) != cudaSuccess || pkv::device_status_word(&a.status) != cudaSuccess)
         return PKV_ERR_CUDA;
-    // A row's columns are cut among CTAs while there would be fewer than 8 CTAs an SM, to pieces of 64
-    // bytes at least, or of 32 while SMs would have none: 32-byte pieces of busy grids cost DRAM half its
-    // rate (64 triples of 16-bit rows, 2,300 kept: 128-byte pieces 98 us, 64 104, 32 142).
+    // About 8 CTAs an SM share the rows. Column slices (rows moving in place) have 64 bytes at least, or 32
+    // while SMs would have none: 32-byte slices of busy grids cost DRAM half its rate (64 triples of 16-bit
+    // rows, 2,300 kept: 128-byte slices 98 us, 64 104, 32 142).
     const long long pairs = (long long)n_seqs * d->n_kv_heads;
-    auto ctas = [&] { return 2 * pairs * d->n_layers * a.slices; };
-    a.slices = 1;
-    while (a.row_bytes / (2 * a.slices) >= 64 && ctas() < 8LL * sms) a.slices *= 2;
-    while (a.row_bytes / (2 * a.slices) >= 32 && ctas() < sms) a.slices *= 2;
+    auto ctas = [&] { return 2 * pairs * d->n_layers * a.parts; };
+    a.parts = 1;
+    while (a.parts < 64 && ctas() < 8LL * sms) a.parts *= 2;
+    a.slices = a.row_bytes / 64;
+    if (2 * pairs * d->n_layers * a.slices < sms) a.slices *= 2;
     if (pairs > 0x7fffffffLL || ctas() > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     if (pkv::launch_evict(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::count_launches(2);

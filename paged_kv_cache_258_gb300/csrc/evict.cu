@@ -17,11 +17,13 @@
 //     For 8-bit pools it also reads the old scales of all the sequence's blocks aside and writes each
 //     destination block's new scale, the largest among its rows' (a power of two like them, so the
 //     codes only shift).
-//  2. move: CTAs own column slices of a triple's rows, so two CTAs never touch the same bytes and a
-//     sequence can be compacted in place without any order between CTAs. A CTA works out the places of
-//     kIndex kept rows at a time in shared memory, then walks them in chunks with the next chunk's loads
-//     in flight: a chunk's stores follow a barrier behind all its loads, and row i of a chunk is read
-//     from a position >= i, so loads of later chunks never see an earlier chunk's stores.
+//  2. move: `parts` CTAs share the rows of a triple (K or V). Where all of a sequence's destinations are
+//     blocks of their own, a CTA takes a run of whole rows. Where some are the blocks the rows come from,
+//     the CTAs take column slices instead, so that no two touch the same bytes and rows can move up in
+//     place without any order between CTAs: a CTA works through its rows in chunks, the next chunk's
+//     loads in flight, a chunk's stores behind a barrier behind all its loads; row i is read from a
+//     position >= i, so loads of later chunks never see an earlier chunk's stores. The places of kIndex
+//     rows at a time are worked out in shared memory.
 #include <math.h>
 
 #include "common.cuh"
@@ -285,17 +287,18 @@ constexpr int kMoveThreads = 256;
 constexpr int kRanked = 64;   // sequences up to which the move starts with the longest
 constexpr int kIndex = 512;  // kept rows whose places are worked out at a time
 
-// U: rows of a thread per chunk. 128 rows a chunk are best: with 256 of 64 bytes (8-bit pools, U = 4) the
-// CTAs that share rows drift apart, 101 us against 89; more chunks in flight are slower for the same reason
-// (16-bit pools: 107 us with the pipeline running on over the index, 93 with a stop every kIndex rows).
-template <bool Q8, int U>
+// Little in flight is best here: reads and writes share DRAM, and CTAs that share rows or blocks should not
+// drift apart. 8-bit pools, 128 triples of 2,250 to 4,096 kept rows: U = 2 79 us, 4 94, 8 101; a pipeline that
+// runs on over the index instead of stopping every kIndex rows 103 against 100.
+template <bool Q8>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a) {
+    constexpr int U = 2;  // rows of a thread per chunk
     __shared__ long long s_from[kIndex], s_to[kIndex];  // row numbers in the layer; s_to < 0: stays where it is
     __shared__ float s_f[Q8 ? kIndex : 1];              // what the row's codes are multiplied with
-    // grid x: (sequence, layer, K or V, head, slice), so that the sequences that keep most start first
+    // grid x: (sequence, layer, K or V, head, part), so that the sequences that keep most start first
     long long rest = blockIdx.x;
-    const int slice = (int)(rest % a.slices);
-    rest /= a.slices;
+    const int part = (int)(rest % a.parts);
+    rest /= a.parts;
     const int g = (int)(rest % a.n_kv);
     rest /= a.n_kv;
     const bool is_v = rest % 2 != 0;
@@ -324,17 +327,30 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     const int c = a.lens[s], want = a.keep[s];
     if (c < 0 || c > cap || want < 0 || min(want, c) > a.max_keep) return;  // flagged by the selection
     const int k = min(want, c);
-    const int lanes = a.row_bytes / a.slices / 16;  // threads that share a row
-    const int rows = kMoveThreads / lanes;          // rows the CTA covers at once
-    const int sub = threadIdx.x / lanes;
     const size_t triple = (size_t)layer * a.n_seqs * a.n_kv + pair;
     const size_t triples = (size_t)a.n_layers * a.n_seqs * a.n_kv;
     const int32_t* kept = a.kept + triple * a.max_keep;
     const int32_t* src = a.src + (size_t)s * a.max_blocks;
     const int32_t* dst = a.dst + (size_t)s * a.max_blocks;
+    const int kb = (k + kBlock - 1) / kBlock;
+    bool same = false;
+    for (int b = threadIdx.x; b < kb; b += kMoveThreads) same = same || src[b] == dst[b];
+    int lo = 0, hi = k, lanes = a.row_bytes / 16;  // the CTA's rows; threads that share a row
+    size_t column = 0;
+    if (__syncthreads_or(same)) {
+        const int slices = min(a.parts, a.slices);
+        if (part >= slices) return;
+        lanes /= slices;
+        column = (size_t)part * lanes * 16;
+    } else {
+        lo = (int)((long long)kb * part / a.parts) * kBlock;
+        hi = min(k, (int)((long long)kb * (part + 1) / a.parts) * kBlock);
+    }
+    const int rows = kMoveThreads / lanes;  // rows the CTA covers at once
+    const int sub = threadIdx.x / lanes;
     const size_t layer_rows = (size_t)a.num_blocks * a.n_kv * kBlock;
-    char* pool = reinterpret_cast<char*>(is_v ? a.v_pool : a.k_pool) + (size_t)layer * layer_rows * a.row_bytes +
-                 (size_t)slice * lanes * 16 + (threadIdx.x % lanes) * 16;
+    char* pool = reinterpret_cast<char*>(is_v ? a.v_pool : a.k_pool) + (size_t)layer * layer_rows * a.row_bytes + column +
+                 (threadIdx.x % lanes) * 16;
     const float* old_scale = Q8 ? a.old_scales + ((is_v ? triples : 0) + triple) * a.max_blocks : nullptr;
     const float* new_scale = Q8 ? (is_v ? a.v_scales : a.k_scales) + (size_t)layer * a.num_blocks * a.n_kv + g : nullptr;
 
@@ -347,36 +363,36 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
 #pragma unroll
         for (int t = 0; t < PER; ++t) {
             const int i = i0 + t * kMoveThreads + threadIdx.x;
-            j_next[t] = i < k ? kept[i] : 0;
+            j_next[t] = i < hi ? kept[i] : 0;
         }
     };
     auto fetch_blocks = [&](int i0) {
 #pragma unroll
         for (int t = 0; t < PER; ++t) {
             const int i = i0 + t * kMoveThreads + threadIdx.x;
-            ps[t] = i < k ? src[j_next[t] / kBlock] : 0;
-            pd[t] = i < k ? dst[i / kBlock] : 0;
+            ps[t] = i < hi ? src[j_next[t] / kBlock] : 0;
+            pd[t] = i < hi ? dst[i / kBlock] : 0;
         }
         if (Q8) {
 #pragma unroll
             for (int t = 0; t < PER; ++t) {
                 const int i = i0 + t * kMoveThreads + threadIdx.x;
-                so[t] = i < k ? old_scale[j_next[t] / kBlock] : 0.f;
-                sn[t] = i < k && (unsigned)pd[t] < (unsigned)a.num_blocks ? new_scale[(size_t)pd[t] * a.n_kv] : 0.f;
+                so[t] = i < hi ? old_scale[j_next[t] / kBlock] : 0.f;
+                sn[t] = i < hi && (unsigned)pd[t] < (unsigned)a.num_blocks ? new_scale[(size_t)pd[t] * a.n_kv] : 0.f;
             }
         }
     };
-    fetch_kept(0);
-    fetch_blocks(0);
-    for (int i0 = 0; i0 < k; i0 += kIndex) {
-        const int n = min(kIndex, k - i0);
+    fetch_kept(lo);
+    fetch_blocks(lo);
+    for (int i0 = lo; i0 < hi; i0 += kIndex) {
+        const int n = min(kIndex, hi - i0);
         __syncthreads();  // the last index has been read
 #pragma unroll
         for (int t = 0; t < PER; ++t) {
             const int e = t * kMoveThreads + threadIdx.x, i = i0 + e;
             long long from = 0, to = -1;
             float f = 1.f;
-            if (i < k) {
+            if (i < hi) {
                 if ((unsigned)ps[t] >= (unsigned)a.num_blocks || (unsigned)pd[t] >= (unsigned)a.num_blocks) {
                     atomicOr(a.status, (unsigned)PKV_DEV_BAD_BLOCK_ID);
                 } else {
@@ -435,11 +451,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
                           ? launch_dependent(evict_select_kernel<512>, dim3(pairs, a.n_layers), 512, 0, stream, 1, a)
                           : launch_dependent(evict_select_kernel<1024>, dim3(pairs, a.n_layers), 1024, 0, stream, 1, a);
     if (err != cudaSuccess) return err;
-    const dim3 grid(pairs * (unsigned)a.slices * (unsigned)a.n_layers * 2u);
-    const bool wide = a.row_bytes / a.slices > 64;  // over four threads a row
-    auto move = a.k_scales ? (wide ? evict_move_kernel<true, 4> : evict_move_kernel<true, 2>)
-                           : (wide ? evict_move_kernel<false, 4> : evict_move_kernel<false, 2>);
-    return launch_dependent(move, grid, kMoveThreads, 0, stream, 1, a);
+    const dim3 grid(pairs * (unsigned)a.parts * (unsigned)a.n_layers * 2u);
+    return launch_dependent(a.k_scales ? evict_move_kernel<true> : evict_move_kernel<false>, grid, kMoveThreads, 0, stream, 1, a);
 }
 
 }  // namespace pkv

@@ -113,7 +113,8 @@ struct EvictArgs {
     long long stride;
     int n_layers, n_seqs, n_kv, num_blocks, max_blocks, max_keep, recent;
     int row_bytes;         // one row of one head
-    int slices;            // CTAs that share the columns of one (sequence, head)
+    int parts;             // CTAs that share the rows of one (layer, sequence, head) of K or V
+    int slices;            // most column slices of a row, where rows move in place
 };
 
 // Launches `kernel` as a programmatic dependent of the kernel before it on the stream: its CTAs may be
