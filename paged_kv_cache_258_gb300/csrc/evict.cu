@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     constexpr int NW = NT / 32;
     __shared__ uint32_t s_hist[kBins];
     __shared__ uint32_t s_warp[NW], s_warp2[NW];
-    __shared__ uint32_t s_pick[2];
+    __shared__ uint32_t s_pick[3];
+    __shared__ float s_old[2][NT];  // old scales of K and V by block, while the CTA has a thread for each
     const long long pair = blockIdx.x;  // s * n_kv + g
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -98,6 +99,19 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         for (int r = 0; r < kKeys; ++r)
             if (r < rounds) key[r] = order_key(x[r]);
     };
+    // 8-bit pools: the old scales are on their way while the selection runs
+    const int nb = (c + kBlock - 1) / kBlock;
+    const size_t triples = (size_t)a.n_layers * a.n_seqs * a.n_kv;
+    float* ks = a.k_scales ? a.k_scales + (size_t)layer * a.num_blocks * a.n_kv + g : nullptr;
+    float* vs = a.k_scales ? a.v_scales + (size_t)layer * a.num_blocks * a.n_kv + g : nullptr;
+    auto old_scale = [&](int b, float* k_old, float* v_old) {
+        const int phys = a.src[(size_t)s * a.max_blocks + b];
+        const bool ok = (unsigned)phys < (unsigned)a.num_blocks;
+        *k_old = ok ? ks[(size_t)phys * a.n_kv] : 0.f;
+        *v_old = ok ? vs[(size_t)phys * a.n_kv] : 0.f;
+    };
+    float k_old = 0.f, v_old = 0.f;
+    if (ks && (int)threadIdx.x < nb) old_scale(threadIdx.x, &k_old, &v_old);
     if (pieces == 1) load(0);
 
     // threshold: positions above it are kept, of those equal to it the first `ties`
@@ -144,6 +158,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
                     if (n + h >= left) {
                         s_pick[0] = (uint32_t)bin;
                         s_pick[1] = left - n;
+                        s_pick[2] = h;
                         break;
                     }
                     n += h;
@@ -153,9 +168,12 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             prefix |= s_pick[0] << shift;
             mask |= ((1u << bits) - 1) << shift;
             left = s_pick[1];
+            if (left == s_pick[2]) break;  // the whole bin is kept: its lower bits do not matter
         }
-        threshold = prefix;
-        ties = left;
+        // keys from the bin's first on; or, where not all of it is kept, the first `left` of one value
+        const bool whole = left == s_pick[2];
+        threshold = whole && prefix > 0 ? prefix - 1 : prefix;  // (no score has key 0)
+        ties = whole ? 0u : left;
     }
 
     uint32_t n_above = 0, n_equal = 0;  // positions above the threshold and equal to it, in earlier pieces
@@ -214,20 +232,19 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     __syncthreads();
     for (int j = k + threadIdx.x; j < c; j += NT) out[j] = 0.f;
 
-    if (a.k_scales != nullptr) {
-        const int nb = (c + kBlock - 1) / kBlock, kb = (k + kBlock - 1) / kBlock;
-        const int32_t* src = a.src + (size_t)s * a.max_blocks;
+    if (ks) {
+        const int kb = (k + kBlock - 1) / kBlock;
         const int32_t* dst = a.dst + (size_t)s * a.max_blocks;
-        const size_t triples = (size_t)a.n_layers * a.n_seqs * a.n_kv;
-        float* old_k = a.old_scales + triple * a.max_blocks;
+        float* old_k = a.old_scales + triple * a.max_blocks;  // kept for the move
         float* old_v = a.old_scales + (triples + triple) * a.max_blocks;
-        float* ks = a.k_scales + (size_t)layer * a.num_blocks * a.n_kv + g;
-        float* vs = a.v_scales + (size_t)layer * a.num_blocks * a.n_kv + g;
         for (int b = threadIdx.x; b < nb; b += NT) {
-            const int phys = src[b];
-            const bool ok = (unsigned)phys < (unsigned)a.num_blocks;
-            old_k[b] = ok ? ks[(size_t)phys * a.n_kv] : 0.f;
-            old_v[b] = ok ? vs[(size_t)phys * a.n_kv] : 0.f;
+            if (b >= NT) old_scale(b, &k_old, &v_old);
+            old_k[b] = k_old;
+            old_v[b] = v_old;
+            if (b < NT) {
+                s_old[0][b] = k_old;
+                s_old[1][b] = v_old;
+            }
         }
         __syncthreads();  // the old scales are read, the kept list is written
         for (int b = warp * 2 + (lane >> 4); b < (kb + 1) / 2 * 2; b += 2 * NW) {  // half a warp a block
@@ -235,8 +252,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             float mk = 0.f, mv = 0.f;
             if (i < k) {
                 const int sb = kept[i] / kBlock;
-                mk = old_k[sb];
-                mv = old_v[sb];
+                mk = nb <= NT ? s_old[0][sb] : old_k[sb];
+                mv = nb <= NT ? s_old[1][sb] : old_v[sb];
             }
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) {

@@ -159,6 +159,15 @@ def test_evict_ties_zeros_and_special_scores():
     check_evict(tuple(case), 4, "bf16", same_scores=False)
 
 
+def test_evict_long_8_bit_sequence_in_pieces():
+    """More positions than the selection's registers hold, and more blocks than its threads."""
+    case = evict_case("bf16", [17000, 20000], [5000, 16001], 1, 64, 1, seed=9, in_place="mixed", q8=True)
+    check_evict(case, 33, "bf16", same_scores=False)
+    sc = case[7]
+    sc[...] = np.round(sc * 8) / 8                        # few different scores: ties across the pieces
+    check_evict(case, 33, "bf16", same_scores=True)
+
+
 def test_evict_everything_or_nothing():
     case = evict_case("f16", [50, 50, 50], [0, 50, 77], 1, 64, 2, seed=6, in_place=True, q8=True)
     check_evict(case, 5, "f16", same_scores=True)
