@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             const int c = a.lens[row];
             const long long q0 = fa.q_start[row], n = fa.q_start[row + 1] - q0;
             const bool bad = q0 < 0 || n < 0 || n > fa.max_query || q0 + n > fa.n_tokens || n > c || c > cap;
-            if (bad && j0 == 0 && blockIdx.x == 0 && threadIdx.x % 32 == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_QUERY_RANGE);
+            if (bad && j0 == 0 && blockIdx.x == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_QUERY_RANGE);
             if (bad || j0 >= n) return Seq{0, row, 0, 0, 0};
             const int tokens = min(G >> fa.shift, (int)n - j0), first = c - (int)n + j0 + 1;
             return Seq{first + tokens - 1, row, (int)q0 + j0, tokens, first};

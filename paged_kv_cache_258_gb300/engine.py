@@ -212,10 +212,12 @@ class DecodeBatch:
                                   uploaded=torch.cuda.Event(), read=torch.cuda.Event(), used=False))
         self.d_slots, self.d_tables, self.d_lens, self.d_pairs = (self._dev[0][k] for k in ("slots", "tables", "lens",
                                                                                              "pairs"))
-        self.workspace = cache.decode_workspace(n, mb, scored)
+        if scored and not cache.q8 and cache.desc.dtype_name == "f32":
+            raise ValueError("scored steps need an fp16, bf16 or 8-bit cache")
         self.scores = None
-        if scored:
-            with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self.stream):  # what a workspace needs zeroed is zeroed before the steps use it
+            self.workspace = cache.decode_workspace(n, mb, scored)
+            if scored:
                 self.scores = torch.zeros((cache.desc.n_layers, n, cache.desc.n_kv_heads, mb * pkv.BLOCK), device=dev)
         self._evict_stage = None
         # two pinned staging images
@@ -453,7 +455,8 @@ class PrefillStep:
         self._o_pair = self._o_qs + S + 1
         self._words = self._o_pair + 2 * S
         self.d_meta = torch.empty(self._words, dtype=torch.int32, device=cache.device)
-        self.workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
+        with torch.cuda.stream(self.stream):
+            self.workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
         self._stage = []
         for _ in range(2):
             h = torch.empty(self._words, dtype=torch.int32).pin_memory()
@@ -616,8 +619,9 @@ class StepExecutor:
             h = torch.empty(off, dtype=torch.int32).pin_memory()
             self._stage.append(dict(meta=h, np=h.numpy(), done=torch.cuda.Event(), used=False))
         self._turn = 0
-        self.workspace = cache.decode_workspace(max(D, 1), mb)
-        self.prefill_workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
+        with torch.cuda.stream(self.stream):
+            self.workspace = cache.decode_workspace(max(D, 1), mb)
+            self.prefill_workspace = pkv.alloc_q8_prefill_workspace(cache.desc, device=cache.device) if cache.q8 else None
 
     def _host(self, np_meta, name, dtype=np.int32):
         off, words = self._off[name]

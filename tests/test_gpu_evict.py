@@ -219,3 +219,40 @@ def test_evict_on_another_stream_and_in_a_graph():
     got = run_evict(desc, pools, scales, src, dst, lens, keep, scores, 6, "bf16", False)
     assert np.array_equal(tp[0].view(torch.uint8).cpu().numpy(), got[0][0])
     assert np.array_equal(new.cpu().numpy(), got[2]) and np.array_equal(kept.cpu().numpy(), got[3])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_evict_offsets_past_32_bits(q8):
+    """Pools of over 2^32 bytes, the sequence in the last blocks, moved in place and apart."""
+    d, n_kv, c, k = 256, 8, 150, 61
+    nb = 140_000 if q8 else 70_000
+    desc = pkv.make_desc("f16", 1, nb, n_kv, n_kv, d)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ids = torch.arange(nb - 20, nb, device="cuda")[torch.randperm(20, generator=torch.Generator().manual_seed(1))].int()
+    for in_place in (True, False):
+        if q8:
+            pools = [torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            for p in pools:
+                p[0, nb - 20:] = torch.randint(0, 120, (20, n_kv, 16, d), device="cuda", generator=g, dtype=torch.uint8)
+            sc = [torch.ones(pkv.scale_shape(desc), device="cuda") for _ in range(2)]
+            more = dict(k_scales=sc[0], v_scales=sc[1], workspace=pkv.alloc_evict_workspace(desc, 1, 10))
+            calls = [p.view(torch.float8_e4m3fn) for p in pools]
+        else:
+            pools = [torch.zeros(pkv.pool_shape(desc), dtype=torch.float16, device="cuda") for _ in range(2)]
+            for p in pools:
+                p[0, nb - 20:] = torch.randn((20, n_kv, 16, d), device="cuda", generator=g).half()
+            calls, more = pools, {}
+        src = ids[:10].contiguous()
+        dst = src if in_place else ids[10:].contiguous()
+        scores = torch.rand((1, 1, n_kv, 160), device="cuda", generator=g)
+        kept = torch.empty((1, 1, n_kv, k), dtype=torch.int32, device="cuda")
+        rows = [p[0, src.long()].transpose(0, 1).reshape(n_kv, 160, d).clone() for p in pools]
+        pkv.pkv_evict_tokens(desc, calls[0], calls[1], src[None], dst[None], torch.tensor([c], dtype=torch.int32, device="cuda"),
+                             torch.tensor([k], dtype=torch.int32, device="cuda"), 9, scores, torch.zeros_like(scores), kept, **more)
+        assert pkv.pkv_get_device_status() == 0
+        at = kept[0, 0].long()
+        for p, r in zip(pools, rows):
+            moved = p[0, dst.long()].transpose(0, 1).reshape(n_kv, 160, d)[:, :k]
+            assert torch.equal(moved, r.gather(1, at[..., None].expand(-1, -1, d)))
+        del pools, calls
+        torch.cuda.empty_cache()

@@ -458,9 +458,11 @@ def test_short_chunks_are_causal_about_nan(G, where):
             assert nan[3:, :, 77].all() and not np.delete(nan, 77, axis=2).any()
 
 
-def test_short_chunks_skip_and_flag_bad_ranges():
+@pytest.mark.parametrize("wide", [0, 1000])
+def test_short_chunks_skip_and_flag_bad_ranges(wide):
+    """wide: table columns beyond the contexts (the launch takes runs then, not partitions)"""
     d, n_kv, G = 64, 2, 4
-    desc, t, _, kf, vf, tables, lens = q8_case("f16", [900, 60, 60, 60], G * n_kv, n_kv, d, seed=22)
+    desc, t, _, kf, vf, tables, lens = q8_case("f16", [900, 60, 60, 60], G * n_kv, n_kv, d, seed=22, max_blocks=57 + wide)
     q, qf = values(np.random.default_rng(8), (9, G * n_kv, d), "f16")
     out = torch.full((9, G * n_kv, d), 7.0, dtype=torch.float16, device="cuda")
     ws = pkv.alloc_q8_prefill_workspace(desc)
@@ -494,3 +496,75 @@ def test_chunk_paths_agree():
         # bf16 weights against fp16 ones, both outputs rounded to bf16
         size = np.abs(np.nan_to_num(vf)).max()
         assert np.all(np.abs(part - whole[at:at + 5]) <= (2.0 ** -8 + 2.0 ** -11 + 2 * 2.0 ** -8) * size)
+
+
+def test_the_largest_batch_and_one_more():
+    """65,535 sequences of a token or two (every CTA scans their lengths), one refused beyond."""
+    n, d, n_kv = 65535, 64, 1
+    desc = pkv.make_desc("bf16", 1, n, 2, n_kv, d)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((2 * n, n_kv, d), device="cuda", generator=g).bfloat16() for _ in range(2))
+    kc, vc = (torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = torch.zeros((2, *pkv.scale_shape(desc)), device="cuda")
+    slots = (torch.arange(n, device="cuda") * 16)[:, None] + torch.arange(2, device="cuda")
+    pkv.pkv_q8_append(desc, 0, k, v, slots.reshape(-1), kc, vc, ks, vs)
+    lens = (torch.arange(n, device="cuda") % 3).int()
+    tables = torch.arange(n, device="cuda").int()[:, None].contiguous()
+    q = torch.randn((n, 2, d), device="cuda", generator=g).bfloat16()
+    out = torch.full_like(q, float("nan"))
+    scores = torch.zeros((n, n_kv, 16), device="cuda")
+    ws = pkv.alloc_q8_workspace(desc, n, 1, scored=True)
+    pkv.pkv_q8_decode_attention(desc, 0, q, kc, vc, ks, vs, tables, lens, 0.125, out, ws, scores=scores)
+    assert pkv.pkv_get_device_status() == 0
+    kf, vf = kc.float()[0] * ks[0][..., None, None], vc.float()[0] * vs[0][..., None, None]
+    z = torch.einsum("nhd,njd->nhj", q.double(), kf[:, 0, :2].double()) * 0.125
+    z = z.masked_fill(torch.arange(2, device="cuda") >= lens[:, None, None], -torch.inf)
+    w = torch.nan_to_num(torch.softmax(z, -1))
+    want = torch.einsum("nhj,njd->nhd", w, vf[:, 0, :2].double())
+    # two terms: the weights' rounding and the output's (2^-11, 2^-8), relative to at most sum w |v|
+    size = torch.einsum("nhj,njd->nhd", w, vf[:, 0, :2].double().abs())
+    assert torch.all((out.double() - want).abs() <= (2.0 ** -11 + 2.0 ** -8 + 2.0 ** -16) * size)
+    assert torch.allclose(scores[..., :2].double(), w.sum(1, keepdim=True), rtol=1e-5, atol=1e-7) and not scores[..., 2:].any()
+    more = torch.zeros((n + 1, 2, d), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(pkv.PkvError, match="UNSUPPORTED"):
+        pkv.pkv_q8_decode_attention(desc, 0, more, kc, vc, ks, vs, torch.zeros((n + 1, 1), dtype=torch.int32, device="cuda"),
+                                    torch.zeros(n + 1, dtype=torch.int32, device="cuda"), 1.0, more)
+
+
+def test_offsets_past_32_bits():
+    """Pools of over 2^32 bytes, the sequences in their last blocks: append, copy, decode and a chunk give
+    what a small pool gives."""
+    d, n_kv, G, n = 256, 8, 1, 2
+    lens = np.array([100, 37], dtype=np.int32)
+    small, big = 12, 140_000                              # 140,000 * 8 * 16 * 256 = 4.6e9 bytes
+    rng = np.random.default_rng(4)
+    x, y = (to_torch(W.normal_values(rng, (137, n_kv, d), "bf16"), "bf16") for _ in range(2))
+    q = to_torch(W.normal_values(rng, (n, n_kv * G, d), "bf16"), "bf16")
+    got = []
+    for nb in (small, big):
+        desc = pkv.make_desc("bf16", 1, nb, n_kv * G, n_kv, d)
+        kc, vc = (torch.zeros(pkv.pool_shape(desc), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = torch.zeros((2, *pkv.scale_shape(desc)), device="cuda")
+        ids = np.arange(nb - 12, nb)
+        tables = np.full((n, 7), -1, dtype=np.int32)
+        tables[0], tables[1, :3] = ids[[3, 1, 7, 11, 5, 0, 10]], ids[[2, 9, 4]]
+        slots = np.concatenate([tables[s][np.arange(c) // 16].astype(np.int64) * 16 + np.arange(c) % 16 for s, c in enumerate(lens)])
+        pkv.pkv_q8_append(desc, 0, x, y, torch.from_numpy(slots).cuda(), kc, vc, ks, vs)
+        pkv.pkv_q8_copy_blocks(desc, kc, vc, ks, vs, torch.tensor([[ids[4], ids[6]]], dtype=torch.int32, device="cuda"))
+        tables[1, 2] = ids[6]
+        tt, tl = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+        out = torch.empty_like(q)
+        pkv.pkv_q8_decode_attention(desc, 0, q, kc, vc, ks, vs, tt, tl, 0.0625, out, pkv.alloc_q8_workspace(desc, n, 7))
+        chunk = torch.empty_like(q)
+        pkv.pkv_q8_prefill_attention(desc, 0, q, kc, vc, ks, vs, tt, tl, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), 1,
+                                     0.0625, chunk, pkv.alloc_q8_prefill_workspace(desc))
+        wide = torch.empty((137, n_kv * G, d), dtype=torch.bfloat16, device="cuda")
+        pkv.pkv_q8_prefill_attention(desc, 0, x.contiguous(), kc, vc, ks, vs, tt, tl,
+                                     torch.tensor([0, 100, 137], dtype=torch.int32, device="cuda"), 100, 0.0625, wide,
+                                     pkv.alloc_q8_prefill_workspace(desc))
+        assert pkv.pkv_get_device_status() == 0
+        got.append((out, chunk, wide))
+        del kc, vc
+        torch.cuda.empty_cache()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

@@ -191,6 +191,9 @@ def test_evict_refusals():
         PagedKVCache(pkv.make_desc("f32", 1, 4, 2, 1, 64), storage="q8")
     with pytest.raises(ValueError):
         PagedKVCache(desc, storage="q4")
+    f32 = PagedKVCache(pkv.make_desc("f32", 1, 4, 2, 1, 64))
+    with pytest.raises(ValueError, match="scored"):
+        DecodeBatch(f32, [1], max_blocks=4, scored=True)
 
 
 @pytest.mark.parametrize("overlap", [True, False])
