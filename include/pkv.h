@@ -20,7 +20,8 @@
  *
  * Two halves:
  *   - device calls (kv append, paged decode attention -- optionally with the step's append
- *     fused in --, chunked-prefill attention, block copy, the upload of a step's metadata):
+ *     fused in --, chunked-prefill attention, block copy, the upload of a step's metadata; the
+ *     same over 8-bit pools; decode that sums its attention weights, and eviction by them):
  *     asynchronous on the caller's CUDA stream, no host synchronisation, no allocation; every
  *     device pointer is owned by the caller;
  *   - a host block manager (pure C, no CUDA): free list, block tables, reference counts,
@@ -527,7 +528,7 @@ size_t pkv_evict_workspace_bytes(const pkv_cache_desc* desc, int32_t n_seqs, int
  *   scores, new_scores  device float [n_layers][n_seqs][n_kv_heads][score_stride], the same array or
  *                   disjoint: new_scores[..][i] = the score of the i-th kept position for i < k, 0 for
  *                   k <= i < c, left as it is beyond
- *   kept            device int32 [n_layers][n_seqs][n_kv_heads][max_keep]: the positions kept, i < k;
+ *   kept            device int32 [n_layers][n_seqs][n_kv_heads][max_keep >= 1]: the positions kept, i < k;
  *                   left as it is beyond
  *   workspace       device, >= pkv_evict_workspace_bytes(...), 4-byte aligned
  * Two launches. A sequence whose length is outside [0, max_blocks_per_seq*16] (PKV_DEV_BAD_CONTEXT_LEN),

@@ -74,7 +74,9 @@ int validate16(const pkv_cache_desc* d) {
 
 // Geometry of the fragment kernel. Runs: as many CTAs as the GPU holds at once. Partitions: when every
 // (sequence, KV head) pair can have its context cut into a cluster's worth of partitions of at most
-// kMaxPartition blocks with no more than one CTA per SM: small calls, where latency counts.
+// kMaxPartition blocks with no more than one CTA per SM: small calls, where latency counts (8 heads of
+// 4,000 tokens: partitions 9.4 us, runs 13.8; at 64 blocks a partition four such sequences take 17.5 us
+// against 14.7).
 constexpr int kMaxCluster = 8;
 
 static_assert(pkv::kMaxRuns * sizeof(unsigned int) == PKV_ARRIVAL_BYTES, "one counter a run");
@@ -88,7 +90,7 @@ FragGeometry geometry_of(long long pairs, int max_blocks, int sms, int per_sm, i
     const long long parts = pairs >= sms ? 1 : sms / pairs < kMaxCluster ? sms / pairs : kMaxCluster;
     const int partition = (int)((max_blocks + parts - 1) / parts);
     if (pairs <= sms && partition <= pkv::kMaxPartition) {
-        geo.partition = partition < pkv::kMinRun ? pkv::kMinRun : partition;
+        geo.partition = partition < pkv::kMinPartition ? pkv::kMinPartition : partition;
         geo.ctas = pkv::decode_partitions(max_blocks, geo.partition);
     } else {
         geo.partition = 0;

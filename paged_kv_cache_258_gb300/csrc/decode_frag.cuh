@@ -9,14 +9,16 @@
 //
 // Work is cut by blocks, not by sequences: the blocks of all (sequence, KV head) pairs form one list,
 // and each of the CTAs the GPU holds at once takes an equal run of it, whatever the lengths are (a pair
-// counts kPairCost blocks on top of its own, what starting and ending it costs). A run
-// covers the end of one pair, some whole pairs and the start of another; only its first and its last
-// pair can be shared with other CTAs, so two partial results a CTA are all that is kept in memory, and
-// the CTA that arrives last at a shared pair joins its partials. (A grid over table-width partitions
-// gave a ragged batch -- 32 sequences of 0..8,192 tokens, 8 heads x 8 queries -- 70 us of which a third
-// were starts, joins and a tail of half-empty SMs.) Calls of a few small contexts take a grid of
+// counts kPairCost blocks on top of its own, what starting and ending it costs). A run covers the end
+// of one pair, some whole pairs and the start of another; only its first and its last pair can be
+// shared with other CTAs, so two partial results a CTA are all that is kept in memory, and the CTA that
+// arrives last at a shared pair joins its partials. (A grid over table-width partitions gave a ragged
+// batch -- 32 sequences of 0..8,192 tokens, 8 heads x 8 queries -- 70 us, of which a third were starts,
+// joins and a tail of half-empty SMs; runs take 50.) Calls of a few small contexts take a grid of
 // (partition, head, sequence) instead, the partitions of a context being a thread-block cluster that
-// joins through shared memory.
+// joins through shared memory (one sequence of 301 tokens: 10.2 us with partials in memory, 5.4).
+// Bound by memory: 10 x 30,000 tokens read at 6.4 TB/s (d = 256) and 6.5 (d = 128), 94 % of the copy
+// rate; the GPT-style batch at 6.0, its many short pairs' ends not wholly hidden.
 //
 // Short prompt chunks over an 8-bit pool run here too (MULTI): the eight query columns of an instruction
 // hold 8 / G tokens x G heads, a "sequence" of the list is such a group of tokens, and each column has
@@ -129,10 +131,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // An output before its rounding. Rows near 65,504 are held as 65,536, which fp16 has no room for: means up
-// to there come out as the largest half.
+// to there (and the 2^-11 that rounded weights may add) come out as the largest half.
 template <typename T>
 __device__ __forceinline__ float in_range(float x) {
-    if constexpr (std::is_same<T, __half>::value) return fabsf(x) <= 65536.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+    if constexpr (std::is_same<T, __half>::value) return fabsf(x) <= 65600.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
     return x;
 }
 
@@ -468,7 +470,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         }
         before -= mine;
         total *= a.n_kv;
-        per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kMinRun + kPairCost<Q8>));
+        // equal runs, but of 24 places at least: shorter ones of a small call are more partials to join than
+        // they save (2 heads of 16,000 tokens: 8 places 31 us, 16 22.7, 24 21.0, 32 21.1)
+        per = max((total + gridDim.x - 1) / gridDim.x, 24LL);
         x = per * blockIdx.x;
         x_end = min(x + per, total);
         if (x >= before * a.n_kv && x < (before + mine) * a.n_kv) {  // one thread, if the run is not empty

@@ -19,9 +19,9 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 // multiple of its least step (fp16: 2^-24).
 inline int q8_min_exp(int dtype) { return dtype == PKV_F16 ? -15 : -117; }
 
-// Least blocks of a CTA's run (one iteration of each of its warps), and arrival counters of a workspace
+// Least blocks of a partition (one iteration of each of a CTA's warps), and arrival counters of a workspace
 // (one for each CTA of the widest launch).
-constexpr int kMinRun = 8;
+constexpr int kMinPartition = 8;
 constexpr int kMaxRuns = 2048;
 // Runs of a prompt chunk's launch, whose workspace is sized without asking a device.
 constexpr int kChunkRuns = 640;
