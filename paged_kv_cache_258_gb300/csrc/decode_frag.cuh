@@ -38,8 +38,8 @@
 //    NaN). q is brought to fp16 with a power of two of its own row, so bf16's range cannot overflow:
 //    a query element keeps at least 11 bits unless it is 2^-29 of its row's largest, where what is
 //    lost is below fp32's own rounding of the dot product.
-//  * Weights for the PV product are fp16 too (11 bits; the 16-bit pools' kernel rounds to the storage
-//    type): w_j = 2^(z_j + log2 S_V(b) + 15 - m'), m' the running maximum of z + log2 S_V. So the
+//  * Weights for the PV product are fp16 too (11 bits; over 16-bit pools they have the pool's type, times
+//    2^15 for fp16: its subnormals begin at 2^-14, and many small weights may make up a large sum): w_j = 2^(z_j + log2 S_V(b) + 15 - m'), m' the running maximum of z + log2 S_V. So the
 //    largest w is 2^15 whatever the blocks' scales, and one keeps 11 bits down to 2^-29 of it. The
 //    sum of weights runs in fp32 beside it with its own maximum m.
 //  * Positions past the length are removed by selection (logits) and by zeroing V's words, so NaN in
@@ -372,6 +372,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     using M = MmaType<MT>;
     constexpr int KSTEPS = D / 16;  // QK k-steps = PV m-tiles
     constexpr uint32_t TILE = S::TILE;
+    // what weights over 16-bit pools are multiplied with before their rounding; bf16 has fp32's range
+    constexpr float kUp = std::is_same<T, __half>::value ? 32768.f : 1.f;
+    static_assert(kWeightExp == 15.f, "both kinds of pools use the same room");
     const DecodeArgs& a = fa.d;
 
     extern __shared__ unsigned char smem_raw[];
@@ -391,7 +394,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     if (threadIdx.x < 2 * NW * ST) mbar_init(&bars[threadIdx.x], 1);
     fence_mbar_init();
     __syncthreads();
-    grid_dependency_wait();  // nothing in global memory has been touched so far
+    // Nothing in global memory has been touched so far. Loads behind the wait are plain ones: the read-only
+    // path is for data that nobody writes while this grid lives, and the grid before may still be writing.
+    grid_dependency_wait();
 
     const int cap = a.max_blocks * kBlock;
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]
@@ -538,8 +543,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             for (int i = 0; i < KSTEPS; ++i) {
                 qraw[i] = make_uint2(0u, 0u);
                 if (gid < G && q_rows.has(gid))
-                    qraw[i] = __ldg(reinterpret_cast<const uint2*>(
-                        qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) + (i % PER) * 4));
+                    qraw[i] = *reinterpret_cast<const uint2*>(qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) +
+                                                              (i % PER) * 4);
             }
         }
         // iterations of this warp, and its blocks (the last iteration may have one less than BPI)
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         auto load_scales = [&](int c, int phys) -> float2 {
             if (!Q8 || c * 32 + lane >= ni || (unsigned)phys >= (unsigned)a.num_blocks) return make_float2(0.f, 0.f);
             const size_t i = (size_t)phys * a.n_kv + g;
-            return make_float2(__ldg(fa.k_scales + i), __ldg(fa.v_scales + i));
+            return make_float2(fa.k_scales[i], fa.v_scales[i]);
         };
         float2 s0 = load_scales(0, t0), s1 = load_scales(1, t1);
         for (int k = 0; k < ST && k < nk; ++k) {
@@ -844,8 +849,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                         pa = M::pack(ex2(z[u][0] + e0), ex2(z[u][1] + e1));
                         pb = M::pack(ex2(z[u][2] + e0), ex2(z[u][3] + e1));
                     } else {
-                        pa = M::pack(p0, p1);
-                        pb = M::pack(p2, p3);
+                        pa = M::pack(p0 * kUp, p1 * kUp);
+                        pb = M::pack(p2 * kUp, p3 * kUp);
                     }
                     b0f[u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
                     b1f[u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
@@ -984,7 +989,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
             l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
         }
-        float fo[2] = {1.f, 1.f};
+        float fo[2] = {1.f / kUp, 1.f / kUp};
         if constexpr (Q8) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) fo[r] = m_out[r] == -INFINITY ? 0.f : exp2f(m_out[r] - kWeightExp - m_run[r]);

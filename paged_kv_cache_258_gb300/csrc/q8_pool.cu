@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8Ap
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int u = i * kAppendWarps + warp;
-        if (u < kSeen && s_run[u] >= 0) x[i] = __ldg(reinterpret_cast<const Raw*>(src + ((size_t)(first + u) * a.n_kv + g) * D) + lane);
+        if (u < kSeen && s_run[u] >= 0) x[i] = reinterpret_cast<const Raw*>(src + ((size_t)(first + u) * a.n_kv + g) * D)[lane];
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {

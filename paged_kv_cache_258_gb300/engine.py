@@ -176,7 +176,8 @@ class DecodeBatch:
 
     scored: every step adds each cached position's attention weight, summed over the query heads of a KV
     head, to ``scores`` [L, n, n_kv, max_blocks * 16] (row s belongs to the batch's s-th sequence), which
-    ``evict`` goes by. An 8-bit cache and scored steps append and attend in separate launches.
+    ``evict`` goes by. An 8-bit cache and scored steps append and attend in separate launches. Sums stay with
+    their seq_id: zero the row of ``scores`` if an id is given to a new sequence.
     """
 
     def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, stream=None, fused: bool = True,

@@ -798,7 +798,7 @@ def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, co
         ctypes.byref(desc), kp, vp, ks, vs, _ptr(src_tables, "src_tables", t.int32, tables, cur),
         _ptr(dst_tables, "dst_tables", t.int32, tables, cur), max_blocks,
         _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur),
-        _ptr(keep_lens, "keep_lens", t.int32, (n_seqs,), cur), n_seqs, int(recent), sp, new, stride,
+        _ptr(keep_lens, "keep_lens", t.int32, (n_seqs,), cur), n_seqs, min(int(recent), 2 ** 31 - 1), sp, new, stride,
         _ptr(kept, "kept", t.int32, (*lead, max_keep), cur), max_keep, ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_evict_tokens")
 

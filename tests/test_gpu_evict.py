@@ -44,6 +44,30 @@ def test_scored_decode_matches(dtype, d, G):
         assert np.array_equal(got[s, :, c:], was[s, :, c:])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("G", [1, 4])
+def test_scored_decode_of_many_small_weights(dtype, G):
+    """One key outweighs each of 40,000 others by 2^23.5, below fp16's last subnormal's half step at 1, and
+    only the others have values: each of their weights still rounds by half a step of its own."""
+    d, c = 64, 40000
+    nb = c // BLOCK
+    k, v = np.zeros((nb, 1, BLOCK, d), dtype=np.float32), np.full((nb, 1, BLOCK, d), 8.0, dtype=np.float32)
+    k[nb // 2, 0, 3], v[nb // 2, 0, 3] = 2.03125, 0.0     # logit 64 * 2.03125 / 8 = 16.25 = 23.44 ln 2
+    tk, tv = (torch.from_numpy(x[None]).cuda().to(pkv.torch_dtype(dtype)) for x in (k, v))
+    q = np.ones((1, G, d))
+    tables, lens = np.arange(nb, dtype=np.int32)[None], np.array([c], dtype=np.int32)
+    want, tol, w, w_tol = R.decode(q, k.astype(np.float64), v.astype(np.float64), tables, lens, 0.125, dtype,
+                                   R.HALF_STEP[dtype])
+    desc = pkv.make_desc(dtype, 1, nb, G, 1, d)
+    tq = torch.ones((1, G, d), device="cuda", dtype=pkv.torch_dtype(dtype))
+    out, scores = torch.empty_like(tq), torch.zeros((1, 1, c), device="cuda")
+    pkv.pkv_paged_decode_attention_scored(desc, 0, tq, tk, tv, torch.from_numpy(tables).cuda(),
+                                          torch.from_numpy(lens).cuda(), 0.125, out, scores,
+                                          pkv.alloc_scored_workspace(desc, 1, nb))
+    assert np.all(np.abs(as_f64(out) - want) <= tol) and np.all(tol < 0.02 * want)
+    assert np.all(np.abs(scores.double().cpu().numpy() - w) <= w_tol + 2.0 ** -23 * w)
+
+
 def evict_case(dtype, lens, keep, n_kv, d, layers, seed, in_place, q8, max_blocks=None, stride_more=0):
     rng = np.random.default_rng(seed)
     lens, keep = np.asarray(lens, dtype=np.int32), np.asarray(keep, dtype=np.int32)
@@ -132,7 +156,7 @@ def test_evict_matches(in_place, dtype, d, q8):
     assert pkv.pkv_get_device_status() == 0
 
 
-@pytest.mark.parametrize("recent", [0, 1, 50, 10 ** 6])
+@pytest.mark.parametrize("recent", [0, 1, 50, 10 ** 6, 2 ** 40])
 def test_evict_recent_window(recent):
     case = evict_case("bf16", [700, 64], [300, 33], 3, 64, 1, seed=2, in_place=True, q8=False)
     check_evict(case, recent, "bf16", same_scores=True)
