@@ -150,6 +150,18 @@ class PagedKVCache:
             pkv.pkv_paged_decode_attention(self.desc, layer, q, self.k_pool, self.v_pool, tables, lens, scale, out,
                                            workspace, stream=stream)
 
+    def append_launcher(self, k, v, slots, stream=None):
+        """append as launch(layer), rows [L, n_tokens, n_kv, d] checked once."""
+        return (pkv.q8_append_launcher if self.q8 else pkv.append_launcher)(self.desc, k, v, slots, *self._arrays(),
+                                                                            stream=stream)
+
+    def decode_launcher(self, q, tables, lens, scale: float, out, workspace=None, scores=None, stream=None):
+        """decode as launch(layer), q and out [L, n, n_q, d], scores [L, n, n_kv, S]: of an 8-bit cache, or
+        with scores (the other steps append in the same launch: pkv.decode_append_launcher)."""
+        make = pkv.q8_decode_launcher if self.q8 else pkv.scored_decode_launcher
+        return make(self.desc, q, *self._arrays(), tables, lens, scale, out, workspace=workspace, scores=scores,
+                    stream=stream)
+
     def add_sequence(self, seq_id: int, n_prompt: int, reserve_tokens: int = 0) -> np.ndarray:
         rc, slots = self.mgr.add_seq(seq_id, n_prompt, reserve_tokens)
         if rc != pkv.PKV_OK:
@@ -333,16 +345,22 @@ class DecodeBatch:
         self.d_slots, self.d_tables, self.d_lens, self.d_pairs = dv["slots"], dv["tables"], dv["lens"], dv["pairs"]
         if st["npairs"]:
             c.copy_blocks(self.d_pairs[: st["npairs"]], stream=self.stream)
-        if self.fused:  # the step's tensors checked once (and again only when they change); each
-            # layer is then one C call
+        apart = c.q8 or self.scores is not None  # append and attention in launches of their own
+        if self.fused or apart:  # the step's tensors checked once (and again only when they change);
+            # each layer is then one C call, or two
             key = (q, k_new, v_new, out, float(scale))
             hit = self._launchers[st["buf"]]
             if hit is not None and len(hit[0]) == len(key) and all(a is b for a, b in zip(hit[0][:4], key[:4])) \
                     and hit[0][4] == key[4]:
                 launch = hit[1]
             else:
-                launch = pkv.decode_append_launcher(d, q, k_new, v_new, c.k_pool, c.v_pool, self.d_tables,
-                                                    self.d_lens, scale, out, self.workspace, stream=self.stream)
+                if apart:
+                    launch = (c.append_launcher(k_new, v_new, self.d_slots, stream=self.stream),
+                              c.decode_launcher(q, self.d_tables, self.d_lens, scale, out, self.workspace, self.scores,
+                                                stream=self.stream))
+                else:
+                    launch = pkv.decode_append_launcher(d, q, k_new, v_new, c.k_pool, c.v_pool, self.d_tables,
+                                                        self.d_lens, scale, out, self.workspace, stream=self.stream)
                 self._launchers[st["buf"]] = (key, launch)
         for layer in range(d.n_layers):
             if on_decode is not None:
@@ -354,12 +372,17 @@ class DecodeBatch:
                 # it may start while that one finishes (they share only the tables, lengths and the
                 # workspace, which the kernel touches after the previous launch has completed)
                 launch(layer, self.overlap and layer > 0 and on_decode is None)
+            elif apart:
+                launch[0](layer)
+                if on_decode is not None:
+                    on_decode(layer, "start")
+                launch[1](layer)
             else:
                 c.append(layer, k_new[layer], v_new[layer], self.d_slots, stream=self.stream)
                 if on_decode is not None:
                     on_decode(layer, "start")
                 c.decode(layer, q[layer], self.d_tables, self.d_lens, scale, out[layer], self.workspace,
-                         scores=None if self.scores is None else self.scores[layer], stream=self.stream)
+                         stream=self.stream)
             if on_decode is not None:
                 on_decode(layer, "end")
         dv["read"].record(self.stream)
@@ -533,14 +556,16 @@ class PrefillStep:
         if st["npairs"]:
             c.copy_blocks(pairs[: st["npairs"]], stream=self.stream)
         if c.q8:
+            append = c.append_launcher(k_new, v_new, slots, stream=self.stream)
+            attend = pkv.q8_prefill_launcher(d, q, *c._arrays(), tables, lens, qs, st["max_q"], scale, out,
+                                             self.workspace, stream=self.stream)
             for layer in range(d.n_layers):
                 if on_attn is not None:
                     on_attn(layer, "pre")
-                c.append(layer, k_new[layer], v_new[layer], slots, stream=self.stream)
+                append(layer)
                 if on_attn is not None:
                     on_attn(layer, "start")
-                pkv.pkv_q8_prefill_attention(d, layer, q[layer], *c._arrays(), tables, lens, qs, st["max_q"], scale,
-                                             out[layer], self.workspace, stream=self.stream)
+                attend(layer)
                 if on_attn is not None:
                     on_attn(layer, "end")
             return
@@ -729,21 +754,22 @@ class StepExecutor:
             tables = self._dev("pre_tables", u["n_pre"] * u["wp"], (-1, u["wp"]))
             lens, qs = self._dev("pre_lens", u["n_pre"]), self._dev("pre_qs", u["n_pre"] + 1)
 
-            def append(layer: int) -> None:
-                c.append(layer, k[layer], v[layer], slots, stream=stream)
+            append = c.append_launcher(k, v, slots, stream=stream)
+            attend_layer = pkv.q8_prefill_launcher(c.desc, q, *c._arrays(), tables, lens, qs, u["max_q"], scale, out,
+                                                   self.prefill_workspace, stream=stream)
 
             def attend(layer: int, overlap_previous: bool = False) -> None:
-                pkv.pkv_q8_prefill_attention(c.desc, layer, q[layer], *c._arrays(), tables, lens, qs, u["max_q"], scale,
-                                             out[layer], self.prefill_workspace, stream=stream)
+                attend_layer(layer)
         if u["n_dec"]:
             dq, dk, dv, dout = dec_io
-            dslots = self._dev("dec_slots", u["n_dec"], i64=True)
-            dtables = self._dev("dec_tables", u["n_dec"] * u["wd"], (-1, u["wd"]))
-            dlens = self._dev("dec_lens", u["n_dec"])
+            tables = self._dev("dec_tables", u["n_dec"] * u["wd"], (-1, u["wd"]))
+            append_row = c.append_launcher(dk, dv, self._dev("dec_slots", u["n_dec"], i64=True), stream=stream)
+            decode_layer = c.decode_launcher(dq, tables, self._dev("dec_lens", u["n_dec"]), scale, dout, self.workspace,
+                                             stream=stream)
 
             def decode(layer: int, overlap_previous: bool = False) -> None:
-                c.append(layer, dk[layer], dv[layer], dslots, stream=stream)
-                c.decode(layer, dq[layer], dtables, dlens, scale, dout[layer], self.workspace, stream=stream)
+                append_row(layer)
+                decode_layer(layer)
         return append, attend, decode
 
     def _run_overlapped(self, u, append, attend, decode) -> None:

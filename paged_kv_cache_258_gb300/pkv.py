@@ -621,12 +621,17 @@ def _workspace(workspace, cur):
     return _dev(workspace, "workspace", cur=cur).value, workspace.nbytes
 
 
-def _scores(scores, name, lead, max_blocks: int, cur):
-    """(pointer, stride) of float32 scores [*lead, S], S >= max_blocks * 16."""
+def _scores_width(scores, name, lead, max_blocks: int) -> int:
+    """S of scores [*lead, S], S >= max_blocks * 16."""
     if scores.dim() != len(lead) + 1 or scores.shape[-1] < max_blocks * BLOCK:
         raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, at least {max_blocks * BLOCK}], "
                          f"got {tuple(scores.shape)}")
-    stride = int(scores.shape[-1])
+    return int(scores.shape[-1])
+
+
+def _scores(scores, name, lead, max_blocks: int, cur):
+    """(pointer, stride) of float32 scores [*lead, S]."""
+    stride = _scores_width(scores, name, lead, max_blocks)
     return _ptr(scores, name, _t.float32, (*lead, stride), cur), stride
 
 
@@ -763,6 +768,91 @@ def pkv_paged_decode_attention_scored(desc: CacheDesc, layer: int, q, k_pool, v_
         _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur), n_seqs, scale,
         _ptr(out, "out", f.dtype, qshape, cur), sp, stride, ws, ws_bytes, _raw(stream, cur))
     _check(rc, "pkv_paged_decode_attention_scored")
+
+
+# A step's launchers, as above: launch(layer), with tensors [L, ...] validated once.
+
+def q8_append_launcher(desc: CacheDesc, k, v, slot_mapping, k_codes, v_codes, k_scales, v_scales, stream=None):
+    """launch(layer): pkv_q8_append of one layer, with k/v [L, n_tokens, n_kv, d]."""
+    t, f, cur = _call(desc)
+    n_tok = int(k.shape[1])
+    k0, k_step = _layered(k, "k", f.dtype, f.n_layers, (n_tok, f.n_kv, f.d), cur=cur)
+    v0, v_step = _layered(v, "v", f.dtype, f.n_layers, (n_tok, f.n_kv, f.d), cur=cur)
+    sl = _ptr(slot_mapping, "slot_mapping", t.int64, (n_tok,), cur)
+    pools = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    fn, dref, sh = lib().pkv_q8_append, ctypes.byref(desc), _raw(stream, cur)
+
+    def launch(layer: int) -> None:
+        rc = fn(dref, layer, k0 + layer * k_step, v0 + layer * v_step, sl, n_tok, *pools, sh)
+        if rc:
+            raise PkvError(rc, "pkv_q8_append")
+    return launch
+
+
+def _decode_launcher(name, desc: CacheDesc, q, pools, block_tables, context_lens, scale, out, scores, workspace, stream):
+    t, f, cur = _call(desc)
+    n, mb = int(q.shape[1]), _table_width(block_tables)
+    q0, q_step = _layered(q, "q", f.dtype, f.n_layers, (n, f.n_q, f.d), cur=cur)
+    o0, o_step = _layered(out, "out", f.dtype, f.n_layers, (n, f.n_q, f.d), cur=cur)
+    tb = _ptr(block_tables, "block_tables", t.int32, (n, mb), cur)
+    ln = _ptr(context_lens, "context_lens", t.int32, (n,), cur)
+    s0 = s_step = stride = 0
+    if scores is not None:
+        stride = _scores_width(scores, "scores", (f.n_layers, n, f.n_kv), mb)
+        s0, s_step = _layered(scores, "scores", t.float32, f.n_layers, (n, f.n_kv, stride), cur=cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    fn, dref, scale, sh = getattr(lib(), name), ctypes.byref(desc), float(scale), _raw(stream, cur)
+
+    def launch(layer: int) -> None:
+        rc = fn(dref, layer, q0 + layer * q_step, *pools, tb, mb, ln, n, scale, o0 + layer * o_step,
+                s0 + layer * s_step, stride, ws, ws_bytes, sh)  # (no scores: 0, a null pointer)
+        if rc:
+            raise PkvError(rc, name)
+    return launch
+
+
+def q8_decode_launcher(desc: CacheDesc, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens,
+                       scale: float, out, workspace=None, scores=None, stream=None):
+    """launch(layer): pkv_q8_decode_attention of one layer, with q/out [L, n, n_q, d] and, if given, scores
+    [L, n, n_kv, S]."""
+    t, f, cur = _call(desc)
+    pools = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    return _decode_launcher("pkv_q8_decode_attention", desc, q, pools, block_tables, context_lens, scale, out, scores,
+                            workspace, stream)
+
+
+def scored_decode_launcher(desc: CacheDesc, q, k_pool, v_pool, block_tables, context_lens, scale: float, out, scores,
+                           workspace=None, stream=None):
+    """launch(layer): pkv_paged_decode_attention_scored of one layer, with q/out [L, n, n_q, d] and scores
+    [L, n, n_kv, S]."""
+    t, f, cur = _call(desc)
+    pools = _ptr(k_pool, "k_pool", f.dtype, f.pool, cur), _ptr(v_pool, "v_pool", f.dtype, f.pool, cur)
+    if scores is None:
+        raise ValueError("scores must be given")
+    return _decode_launcher("pkv_paged_decode_attention_scored", desc, q, pools, block_tables, context_lens, scale, out,
+                            scores, workspace, stream)
+
+
+def q8_prefill_launcher(desc: CacheDesc, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens,
+                        query_start, max_query_len: int, scale: float, out, workspace, stream=None):
+    """launch(layer): pkv_q8_prefill_attention of one layer, with q/out [L, n_tokens, n_q, d]."""
+    t, f, cur = _call(desc)
+    n_tok, n_seqs, mb, mq = int(q.shape[1]), int(block_tables.shape[0]), _table_width(block_tables), int(max_query_len)
+    q0, q_step = _layered(q, "q", f.dtype, f.n_layers, (n_tok, f.n_q, f.d), cur=cur)
+    o0, o_step = _layered(out, "out", f.dtype, f.n_layers, (n_tok, f.n_q, f.d), cur=cur)
+    pools = _q8_pools(t, f, k_codes, v_codes, k_scales, v_scales, cur)
+    tb = _ptr(block_tables, "block_tables", t.int32, (n_seqs, mb), cur)
+    ln = _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur)
+    qs = _ptr(query_start, "query_start", t.int32, (n_seqs + 1,), cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    fn, dref, scale, sh = lib().pkv_q8_prefill_attention, ctypes.byref(desc), float(scale), _raw(stream, cur)
+
+    def launch(layer: int) -> None:
+        rc = fn(dref, layer, q0 + layer * q_step, *pools, tb, mb, ln, qs, n_seqs, n_tok, mq, scale, o0 + layer * o_step,
+                ws, ws_bytes, sh)
+        if rc:
+            raise PkvError(rc, "pkv_q8_prefill_attention")
+    return launch
 
 
 def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent: int,

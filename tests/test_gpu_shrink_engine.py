@@ -259,3 +259,57 @@ def test_continuous_batching_over_an_8_bit_cache(overlap):
     assert all(r.state == "done" for r in reqs)
     assert seen["dec"] > 0 and seen["pre"] > 0 and seen["pairs"] > 0
     assert pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,q8,scored", [("bf16", True, True), ("f16", True, False), ("f16", False, True)])
+def test_launchers_equal_the_calls(dtype, q8, scored):
+    """A step's launchers over views of larger buffers against the call for each layer, bit for bit."""
+    L, n, n_q, n_kv, d, nb, mb = 3, 3, 8, 2, 128, 40, 9
+    desc = pkv.make_desc(dtype, L, nb, n_q, n_kv, d)
+    rng = np.random.default_rng(21)
+    got = []
+    big = [to_torch(x, dtype) for x in io(rng, L, n + 2, n_q, n_kv, d, dtype)[:3]]
+    rows = [to_torch(x, dtype) for x in io(rng, L, 90, n_q, n_kv, d, dtype)[:3]]
+    q, k, v = (x[:, 1:n + 1] for x in big)
+    for launchers in (False, True):
+        cache = PagedKVCache(desc, storage="q8" if q8 else None)
+        slots = torch.from_numpy(np.concatenate([cache.add_sequence(i, c) for i, c in enumerate((60, 29, 1))])).cuda()
+        _, tables, lens = cache.mgr.pack_tables([0, 1, 2], mb)
+        tables, lens = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+        starts = torch.tensor([0, 60, 89, 90], dtype=torch.int32, device="cuda")
+        last = slots[torch.tensor([59, 88, 89], device="cuda")]
+        out = torch.zeros((L, n + 1, n_q, d), device="cuda", dtype=pkv.torch_dtype(dtype))[:, :n]
+        p_out = torch.zeros((L, 90, n_q, d), device="cuda", dtype=pkv.torch_dtype(dtype))
+        scores = torch.zeros((L, n, n_kv, mb * 16 + 1), device="cuda") if scored else None
+        ws = cache.decode_workspace(n, mb, scored)
+        p_ws = pkv.alloc_q8_prefill_workspace(desc) if q8 else None
+        if launchers:
+            fill = cache.append_launcher(rows[1], rows[2], slots)
+            append = cache.append_launcher(k, v, last)
+            decode = cache.decode_launcher(q, tables, lens, 0.1, out, ws, scores)
+            prefill = pkv.q8_prefill_launcher(desc, rows[0], *cache._arrays(), tables, lens, starts, 60, 0.1, p_out,
+                                              p_ws) if q8 else None
+        for layer in range(L):
+            if launchers:
+                fill(layer), append(layer), decode(layer)
+                if q8:
+                    prefill(layer)
+            else:
+                cache.append(layer, rows[1][layer], rows[2][layer], slots)
+                cache.append(layer, k[layer], v[layer], last)
+                cache.decode(layer, q[layer], tables, lens, 0.1, out[layer], ws, None if scores is None else scores[layer])
+                if q8:
+                    pkv.pkv_q8_prefill_attention(desc, layer, rows[0][layer], *cache._arrays(), tables, lens, starts, 60, 0.1,
+                                                 p_out[layer], p_ws)
+        assert pkv.pkv_get_device_status() == 0
+        got.append([x.contiguous().view(torch.uint8).cpu() for x in (*cache._arrays(), out, p_out, *([scores] if scored else []))])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][-1].any()
+    with pytest.raises(ValueError):
+        cache.decode_launcher(q[:2], tables, lens, 0.1, out, ws, scores)
+    with pytest.raises(ValueError):
+        cache.append_launcher(k[:, :, :1], v, last)
+    with pytest.raises(ValueError):
+        cache.decode_launcher(q, tables, lens, 0.1, out, ws, torch.zeros((L, n, n_kv, 16), device="cuda"))
+    if not q8:
+        with pytest.raises(ValueError, match="scores"):
+            cache.decode_launcher(q, tables, lens, 0.1, out, ws)
