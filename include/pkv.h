@@ -473,8 +473,8 @@ size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
 
 /*
  * pkv_paged_prefill_attention over 8-bit pools (the chunk's rows already appended by pkv_q8_append).
- * Short chunks are attended to straight from the codes, 8 / G tokens at a time. Longer ones take two
- * launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
+ * Short chunks are attended to straight from the codes, 8 to 32 rows (tokens x G heads) at a time. Longer
+ * ones take two launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
  * physical block like one layer of a 16-bit pool, and attended to from there by the kernel of 16-bit
  * pools. The choice goes by the counts that are known on the host. Arguments, bad device values, limits and errors
  * as pkv_paged_prefill_attention.

@@ -1,5 +1,7 @@
 // abi_shrink.cu -- the C ABI of 8-bit pools, of decode that sums its attention weights and of eviction:
 // argument validation, workspace layout, dispatch.
+#include <math.h>
+
 #include "shrink.h"
 
 namespace pkv {
@@ -8,10 +10,10 @@ cudaError_t launch_frag_q8_f16(int, int, const FragArgs&, const CUtensorMap&, co
 cudaError_t launch_frag_q8_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_frag_scored_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_frag_scored_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
-cudaError_t launch_frag_multi_f16(int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
-cudaError_t launch_frag_multi_bf16(int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
-cudaError_t frag_multi_ctas_per_sm_f16(int, int*);
-cudaError_t frag_multi_ctas_per_sm_bf16(int, int*);
+cudaError_t launch_frag_multi_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_frag_multi_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t frag_multi_ctas_per_sm_f16(int, int, int*);
+cudaError_t frag_multi_ctas_per_sm_bf16(int, int, int*);
 cudaError_t frag_ctas_per_sm_q8_f16(int, int, int*);
 cudaError_t frag_ctas_per_sm_q8_bf16(int, int, int*);
 cudaError_t frag_ctas_per_sm_scored_f16(int, int, int*);
@@ -41,16 +43,17 @@ cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, cons
                             : launch_frag_scored_bf16(head_dim, group, a, tk, tv, stream);
 }
 
-cudaError_t frag_multi_ctas_per_sm(int dtype, int head_dim, int* out) {
-    return dtype == PKV_F16 ? frag_multi_ctas_per_sm_f16(head_dim, out) : frag_multi_ctas_per_sm_bf16(head_dim, out);
+cudaError_t frag_multi_ctas_per_sm(int dtype, int head_dim, int columns, int* out) {
+    return dtype == PKV_F16 ? frag_multi_ctas_per_sm_f16(head_dim, columns, out)
+                            : frag_multi_ctas_per_sm_bf16(head_dim, columns, out);
 }
 
-cudaError_t launch_frag_multi(int dtype, int head_dim, const FragArgs& a, cudaStream_t stream) {
+cudaError_t launch_frag_multi(int dtype, int head_dim, int columns, const FragArgs& a, cudaStream_t stream) {
     CUtensorMap tk, tv;
     const cudaError_t err = layer_maps(a, head_dim, kCodesE4M3, &tk, &tv);
     if (err != cudaSuccess) return err;
-    return dtype == PKV_F16 ? launch_frag_multi_f16(head_dim, a, tk, tv, stream)
-                            : launch_frag_multi_bf16(head_dim, a, tk, tv, stream);
+    return dtype == PKV_F16 ? launch_frag_multi_f16(head_dim, columns, a, tk, tv, stream)
+                            : launch_frag_multi_bf16(head_dim, columns, a, tk, tv, stream);
 }
 
 }  // namespace pkv
@@ -213,12 +216,16 @@ int frag_decode(bool q8, const pkv_cache_desc* d, int32_t layer, const void* q, 
     return PKV_OK;
 }
 
+// The most query rows (tokens x heads of the group) that one pass of the chunk kernel over a context holds: as
+// many column tiles as have 64 registers of sums a lane.
+int wide_columns(const pkv_cache_desc* d) { return d->head_dim < 256 ? 2048 / d->head_dim : 8; }
+
 // Workspace of prefill: arrival counters, the runs' partials, one layer of K and V in 16 bits.
 struct ChunkLayout {
     size_t o, ml, k, v, bytes;
 };
 ChunkLayout chunk_layout(const pkv_cache_desc* d) {
-    const size_t partials = (size_t)pkv::kChunkRuns * 2 * 8, layer = layer_elems(d) * 2;
+    const size_t partials = (size_t)pkv::kChunkRuns * 2 * wide_columns(d), layer = layer_elems(d) * 2;
     ChunkLayout l;
     l.o = PKV_ARRIVAL_BYTES;
     l.ml = l.o + partials * d->head_dim * sizeof(float);
@@ -228,19 +235,35 @@ ChunkLayout chunk_layout(const pkv_cache_desc* d) {
     return l;
 }
 
-// Whether a chunk is attended to group by group (8 / G tokens at a time, each reading the codes again) or
-// widened first and handed to the tensor-memory kernel of 16-bit pools. Nanoseconds per context token:
-// a group's read of a token (measured: 3.8, 6.7 and 8.5 TB/s of codes at head_dim 64, 128 and 256) against
-// that kernel's waves of 128-key tiles (1.0 us, 1.28 at 256), one CTA of 128 rows an SM, plus the widening's
-// three bytes a code. The context's length, which both scale with, drops out. 20,000 tokens, 8 heads x 4 x
-// 128: chunks of 1, 8, 32 and 64 tokens take 20, 34, 98 and 185 us by groups, 168 us each the other way.
-bool by_groups(const pkv_cache_desc* d, int n_seqs, int n_tokens, int max_query, int sms) {
-    const double G = group_of(d), per_group = 8 / G, row = 2.0 * d->head_dim * d->n_kv_heads;
-    const double groups = n_tokens / per_group + n_seqs * (1 - 1 / per_group);
-    const long long ctas = (long long)n_seqs * d->n_kv_heads * ((max_query * group_of(d) + 127) / 128);
+// Rows of a pass: one column tile of 8, or the most there is room for -- fewer passes, each with more to do. That
+// pays from 32 rows on (8 heads x 4 x 128, 20,000 tokens: 24 rows 28.4 us in tiles of 8, 31.5 of 16; 32 rows
+// 33.4 and 31.7; 128 rows 97.8 and 76.0) and where the GPU is still full (2 heads x 8 x 128, 1,000 tokens, 128
+// rows: 9.0 and 10.1).
+int chunk_columns(const pkv_cache_desc* d, int n_seqs, int max_query, int max_blocks) {
+    const int group = group_of(d), wide = wide_columns(d), per_pass = wide / group;
+    if ((long long)max_query * group < 32) return 8;
+    const double passes = (double)n_seqs * ((max_query + per_pass - 1) / per_pass);
+    return passes * d->n_kv_heads * max_blocks >= 6000 ? wide : 8;
+}
+
+// Whether a chunk is attended to in passes of `columns` rows, each reading the codes again, or widened first and
+// handed to the tensor-memory kernel of 16-bit pools. Nanoseconds, for contexts as long as the table is wide:
+//   passes  6.5 us (10.5 wide), the context once at 6.5 TB/s, and a pass's work on each token (measured: 3.8, 6.7
+//           and 8.5 TB/s of codes at head_dim 64, 128 and 256 in tiles of 8; 2.1 and 5.5 in passes of 32 and 16)
+//   widen   8 us, that kernel's waves of 128-key tiles (0.93 us, 1.28 at 256; one CTA of 128 rows an SM) and
+//           three bytes a code
+// 20,000 tokens, 8 heads x 4 x 128: chunks of 1, 8, 32 and 64 tokens take 19, 32, 76 and 136 us in passes, 168 us
+// the other way; 4 x 1,900 tokens, 8 heads x 4 x 64: 2, 16, 32 and 70 tokens 9.5, 22.5, 28.4, 45 against 23.
+bool by_passes(const pkv_cache_desc* d, int n_seqs, int n_tokens, int max_query, int max_blocks, int columns, int sms) {
+    const double per_pass = columns / group_of(d), row = 2.0 * d->head_dim * d->n_kv_heads;
+    const double most = n_seqs * ceil(max_query / per_pass), mean = n_tokens / per_pass + n_seqs * (1 - 1 / per_pass);
+    const double passes = most < mean ? most : mean, context = (double)max_blocks * pkv::kBlock;
+    const long long ctas = (long long)n_seqs * d->n_kv_heads * (((long long)max_query * group_of(d) + 127) / 128);
     const double waves = (double)((ctas + sms - 1) / sms);
-    const double rate = d->head_dim == 64 ? 3800 : d->head_dim == 128 ? 6700 : 8500;  // bytes a ns
-    return groups * row / rate < waves * (d->head_dim == 256 ? 1280.0 : 1000.0) / 128 + n_seqs * row * 3 / 6000.0;
+    const bool wide = columns > 8;
+    const double rate = d->head_dim == 64 ? (wide ? 2100 : 3800) : d->head_dim == 128 ? (wide ? 5500 : 6700) : 8500;
+    return (wide ? 10500 : 6500) + (passes * row / rate + n_seqs * row / 6500) * context <
+           8000 + (waves * (d->head_dim == 256 ? 10.0 : 7.3) + n_seqs * row * 3 / 6000.0) * context;
 }
 
 }  // namespace
@@ -367,14 +390,15 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     k_scales += layer_scales(d) * layer;
     v_scales += layer_scales(d) * layer;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int group = group_of(d), per_group = 8 / group, groups = (max_query_len + per_group - 1) / per_group;
+    const int group = group_of(d), columns = chunk_columns(d, n_seqs, max_query_len, max_blocks_per_seq);
+    const int per_group = columns / group, groups = (max_query_len + per_group - 1) / per_group;
     unsigned int* status = nullptr;
     int sms = 0;
     if (pkv::device_status_word(&status) != cudaSuccess || pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
 
-    if ((long long)n_seqs * groups <= 65535 && by_groups(d, n_seqs, n_tokens, max_query_len, sms)) {
+    if ((long long)n_seqs * groups <= 65535 && by_passes(d, n_seqs, n_tokens, max_query_len, max_blocks_per_seq, columns, sms)) {
         int per_sm = 0;
-        if (pkv::frag_multi_ctas_per_sm(d->dtype, d->head_dim, &per_sm) != cudaSuccess) return PKV_ERR_CUDA;
+        if (pkv::frag_multi_ctas_per_sm(d->dtype, d->head_dim, columns, &per_sm) != cudaSuccess) return PKV_ERR_CUDA;
         const FragGeometry geo =
             geometry_of((long long)n_seqs * groups * d->n_kv_heads, max_blocks_per_seq, sms, per_sm, pkv::kChunkRuns);
         pkv::FragArgs a;
@@ -403,7 +427,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
         a.groups = groups;
         a.shift = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
         a.partition = geo.partition;
-        const cudaError_t err = pkv::launch_frag_multi(d->dtype, d->head_dim, a, st);
+        const cudaError_t err = pkv::launch_frag_multi(d->dtype, d->head_dim, columns, a, st);
         if (err != cudaSuccess) return pkv::launch_status(err);
         pkv::count_launches(1);
         return PKV_OK;

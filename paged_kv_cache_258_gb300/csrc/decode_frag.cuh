@@ -20,9 +20,12 @@
 // Bound by memory: 10 x 30,000 tokens read at 6.4 TB/s (d = 256) and 6.5 (d = 128), 94 % of the copy
 // rate; the GPT-style batch at 6.0, its many short pairs' ends not wholly hidden.
 //
-// Short prompt chunks over an 8-bit pool run here too (MULTI): the eight query columns of an instruction
-// hold 8 / G tokens x G heads, a "sequence" of the list is such a group of tokens, and each column has
-// its own causal limit. Every group reads the context again, mostly from L2.
+// Short prompt chunks over an 8-bit pool run here too (MULTI): the query columns (8, or 16 and 32 as two and
+// four column tiles at D = 128 and 64) hold tokens x G heads, a "sequence" of the list is such a group of
+// tokens, and each column has its own causal limit. Every group reads the context again, mostly from L2; wide
+// ones do so less often and convert each code once for all tiles. Bound by issue and the tensor pipe: a block of
+// 16 tokens x 16 columns at D = 128 costs a scheduler 460 cycles. A second stage in flight is no faster, one
+// block an iteration (3 stages or 3 CTAs an SM) 30 % slower.
 //
 // Per-warp rings of TMA copies feed the warps as in decode_mma.cuh. What differs is how a 16-token tile
 // gets from shared memory into fragments:
@@ -39,9 +42,10 @@
 //    a query element keeps at least 11 bits unless it is 2^-29 of its row's largest, where what is
 //    lost is below fp32's own rounding of the dot product.
 //  * Weights for the PV product are fp16 too (11 bits; over 16-bit pools they have the pool's type, times
-//    2^15 for fp16: its subnormals begin at 2^-14, and many small weights may make up a large sum): w_j = 2^(z_j + log2 S_V(b) + 15 - m'), m' the running maximum of z + log2 S_V. So the
-//    largest w is 2^15 whatever the blocks' scales, and one keeps 11 bits down to 2^-29 of it. The
-//    sum of weights runs in fp32 beside it with its own maximum m.
+//    2^15 for fp16: its subnormals begin at 2^-14, and many small weights may make up a large sum):
+//    w_j = 2^(z_j + log2 S_V(b) + 15 - m'), m' the running maximum of z + log2 S_V. So the largest w is
+//    2^15 whatever the blocks' scales, and one keeps 11 bits down to 2^-29 of it (below 2^-40 it is 0:
+//    2^28 tokens of those make up 2^-12). The sum of weights runs in fp32 beside it with its own maximum m.
 //  * Positions past the length are removed by selection (logits) and by zeroing V's words, so NaN in
 //    unused rows cannot reach the result.
 // With `z` set every logit is also written out (fp32, G per position, 64 G contiguous bytes a block);
@@ -91,17 +95,18 @@ struct FragGeom {
     static constexpr uint32_t TILE = kBlock * ROWB;
     static constexpr uint32_t STAGE = 2 * BPI * TILE;
     static constexpr int KCH = ROWB / 64;                    // 16-byte chunks of a K row per lane
-    static constexpr size_t STAGES = (size_t)NW * ST * STAGE;
+    static constexpr int COLS = (G + 7) / 8 * 8;             // query columns of the instructions
+    static constexpr size_t MERGE = (size_t)NW * G * D * 4;  // join scratch, after the combine buffer
+    static constexpr size_t RINGS = (size_t)NW * ST * STAGE;
+    static constexpr size_t AFTER = MERGE + (JoinScratch<G>::BYTES > G * (D + 2) * 4 ? JoinScratch<G>::BYTES : G * (D + 2) * 4);
+    static constexpr size_t STAGES = RINGS > AFTER ? RINGS : (AFTER + 15) / 16 * 16;  // rings, then the join
     static constexpr size_t BARS = STAGES;                            // uint64 [NW][ST][K, V]
-    static constexpr size_t ML = BARS + (size_t)NW * ST * 16;         // float2 [NW][8]: (max, sum) of a warp's rows
-    static constexpr size_t JOIN = ML + (size_t)NW * 8 * 8;           // float [8][NW] weights, [8] maxima, [8] sums
-    static constexpr size_t FIND = JOIN + (size_t)8 * (NW + 2) * 4;   // long long [NW + 2]
+    static constexpr size_t ML = BARS + (size_t)NW * ST * 16;            // float2 [NW][COLS]: (max, sum) of a warp's rows
+    static constexpr size_t JOIN = ML + (size_t)NW * COLS * 8;           // float [COLS][NW] weights, [COLS] maxima, [COLS] sums
+    static constexpr size_t FIND = JOIN + (size_t)COLS * (NW + 2) * 4;   // long long [NW + 2]
     static constexpr size_t TOTAL = (FIND + (size_t)(NW + 2) * 8 + 15) / 16 * 16;
     static constexpr size_t ALLOC = TOTAL + 1024;             // room to align the base
     static_assert(TOTAL % 16 == 0, "the logits of a partition follow");
-    static constexpr size_t MERGE = (size_t)NW * G * D * 4;  // join scratch, after the combine buffer
-    static_assert(MERGE + JoinScratch<G>::BYTES <= STAGES && MERGE + G * (D + 2) * 4 <= STAGES,
-                  "combine buffer and join scratch must fit");
     // byte of 16-byte chunk `c` of row `r`: the copy's swizzle XORs the chunk with the 128-byte line's
     // number modulo the pattern (8 rows of 128 bytes, or 4 lines of two 64-byte rows)
     __device__ __forceinline__ static uint32_t at(int r, int c) {
@@ -365,13 +370,14 @@ template <typename T, bool Q8, int D, int G, int NW, int ST, int BPI, int CTAS, 
 __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragArgs fa,
                                                                     const __grid_constant__ CUtensorMap tm_k,
                                                                     const __grid_constant__ CUtensorMap tm_v) {
-    static_assert(G <= 8 && (!MULTI || (Q8 && G == 8)), "at most 8 query rows per KV head");
+    static_assert(MULTI ? Q8 && G % 8 == 0 && G <= 32 : G <= 8, "one column tile, or whole ones over codes");
     static_assert(BPI == 1 || BPI == 2 || BPI == 4, "blocks per iteration");
     using S = FragGeom<Q8, D, G, NW, ST, BPI>;
     using MT = typename std::conditional<Q8, __half, T>::type;  // type of the matrix instructions' operands
     using M = MmaType<MT>;
     constexpr int KSTEPS = D / 16;  // QK k-steps = PV m-tiles
     constexpr uint32_t TILE = S::TILE;
+    constexpr int NT = S::COLS / 8;  // column tiles: query rows 8 nt + 2 tig, + 1 are this lane's
     // what weights over 16-bit pools are multiplied with before their rounding; bf16 has fp32's range
     constexpr float kUp = std::is_same<T, __half>::value ? 32768.f : 1.f;
     static_assert(kWeightExp == 15.f, "both kinds of pools use the same room");
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int gid = lane >> 2;  // token row of S, chunk of V
-    const int tig = lane & 3;   // owns query rows 2 tig, 2 tig + 1
+    const int tig = lane & 3;   // owns query rows 2 tig, 2 tig + 1 of every column tile
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -508,8 +514,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         }
     }
 
-    float* s_join = reinterpret_cast<float*>(smem + S::JOIN);  // [8][NW] weights, [8] maxima, [8] sums
-    float2* s_ml = reinterpret_cast<float2*>(smem + S::ML);    // [NW][8]
+    float* s_join = reinterpret_cast<float*>(smem + S::JOIN);  // [COLS][NW] weights, [COLS] maxima, [COLS] sums
+    float2* s_ml = reinterpret_cast<float2*>(smem + S::ML);    // [NW][COLS]
     int t_next = 0;     // this warp's first chunk of the next pair's table, read ahead
     bool ahead = false; // and whether it has been
     bool lost = false;  // a wait gave up
@@ -536,14 +542,16 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         int t1 = nblk > 32 * NW ? load_chunk(1) : -1;
         int t2 = nblk > 64 * NW ? load_chunk(2) : -1;
         constexpr int PER = KSTEPS / S::KCH;  // k-steps per chunk of a K row
-        uint2 qraw[KSTEPS];                   // the query row's words, on their way while the first tiles are
-        {
-            const T* qrow = q_rows.row(gid);
+        uint2 qraw[NT][KSTEPS];               // the query rows' words, on their way while the first tiles are
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + gid;
+            const T* qrow = q_rows.row(r);
 #pragma unroll
             for (int i = 0; i < KSTEPS; ++i) {
-                qraw[i] = make_uint2(0u, 0u);
-                if (gid < G && q_rows.has(gid))
-                    qraw[i] = *reinterpret_cast<const uint2*>(qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) +
+                qraw[nt][i] = make_uint2(0u, 0u);
+                if (r < G && q_rows.has(r))
+                    qraw[nt][i] = *reinterpret_cast<const uint2*>(qrow + S::k_chunk(tig, i / PER) * (Q8 ? 16 : 8) +
                                                               (i % PER) * 4);
             }
         }
@@ -638,47 +646,55 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
 
         // Q^T fragments: k-step `ks` of row gid takes four dims of one of the lane's K chunks (one 32-bit
         // word of codes, two words of halves); rows >= G are 0.
-        uint32_t qb[KSTEPS][2];
-        float zf[2];  // factor of the logits of query rows 2 tig, 2 tig + 1
-        if constexpr (Q8) {
-            float amax = 0.f;
+        uint32_t qb[NT][KSTEPS][2];
+        float zf[NT][2];  // factor of the logits of the lane's query rows
 #pragma unroll
-            for (int i = 0; i < KSTEPS; ++i) {
-                const float2 lo = MmaType<T>::unpack(qraw[i].x), hi = MmaType<T>::unpack(qraw[i].y);
-                const float f[4] = {fabsf(lo.x), fabsf(lo.y), fabsf(hi.x), fabsf(hi.y)};
+        for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (Q8) {
+                float amax = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (f[e] <= 3.4028234e38f) amax = fmaxf(amax, f[e]);
+                for (int i = 0; i < KSTEPS; ++i) {
+                    const float2 lo = MmaType<T>::unpack(qraw[nt][i].x), hi = MmaType<T>::unpack(qraw[nt][i].y);
+                    const float f[4] = {fabsf(lo.x), fabsf(lo.y), fabsf(hi.x), fabsf(hi.y)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (f[e] <= 3.4028234e38f) amax = fmaxf(amax, f[e]);
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^-eq brings the row's largest element into [2^14, 2^15)
+                const int eq = max(amax > 0.f ? ilogbf(amax) - 14 : 0, -126);
+                const float down = pow2(-eq);
+#pragma unroll
+                for (int i = 0; i < KSTEPS; ++i) {
+                    const float2 lo = MmaType<T>::unpack(qraw[nt][i].x), hi = MmaType<T>::unpack(qraw[nt][i].y);
+                    qb[nt][i][0] = M::pack(lo.x * down, lo.y * down);
+                    qb[nt][i][1] = M::pack(hi.x * down, hi.y * down);
+                }
+                const float f = a.scale_log2 * pow2(eq);
+                zf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
+                zf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KSTEPS; ++i) {
+                    qb[nt][i][0] = qraw[nt][i].x;
+                    qb[nt][i][1] = qraw[nt][i].y;
+                }
+                zf[nt][0] = zf[nt][1] = a.scale_log2;
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^-eq brings the row's largest element into [2^14, 2^15)
-            const int eq = max(amax > 0.f ? ilogbf(amax) - 14 : 0, -126);
-            const float down = pow2(-eq);
-#pragma unroll
-            for (int i = 0; i < KSTEPS; ++i) {
-                const float2 lo = MmaType<T>::unpack(qraw[i].x), hi = MmaType<T>::unpack(qraw[i].y);
-                qb[i][0] = M::pack(lo.x * down, lo.y * down);
-                qb[i][1] = M::pack(hi.x * down, hi.y * down);
-            }
-            const float f = a.scale_log2 * pow2(eq);
-            zf[0] = __shfl_sync(0xffffffffu, f, 8 * tig);
-            zf[1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KSTEPS; ++i) {
-                qb[i][0] = qraw[i].x;
-                qb[i][1] = qraw[i].y;
-            }
-            zf[0] = zf[1] = a.scale_log2;
         }
 
-        float acc[KSTEPS][4];  // m-tile mt: (dims dA, dA + 1) x (row 2tig | 2tig+1)
+        float acc[NT][KSTEPS][4];  // m-tile mt: (dims dA, dA + 1) x (row 2tig | 2tig+1)
+        float m_run[NT][2];        // of z
+        float m_out[NT][2];        // of z + log2 S_V (8-bit pools)
+        float l_run[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < KSTEPS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-        float m_run[2] = {-INFINITY, -INFINITY};  // of z
-        float m_out[2] = {-INFINITY, -INFINITY};  // of z + log2 S_V (8-bit pools)
-        float l_run[2] = {0.f, 0.f};
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int mt = 0; mt < KSTEPS; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
+            m_run[nt][0] = m_run[nt][1] = m_out[nt][0] = m_out[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = 0.f;
+        }
 
         // where logits go: memory, or behind the rings in a grid of partitions
         float* zrow = nullptr;
@@ -727,13 +743,16 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
             int nvalid[BPI];
 #pragma unroll
             for (int u = 0; u < BPI; ++u) nvalid[u] = (have >> u) & 1 ? min(kBlock, ctx - jb - u * kBlock) : 0;
-            uint32_t b0f[BPI], b1f[BPI];
+            uint32_t b0f[NT][BPI], b1f[NT][BPI];
             if (have) {
-                // ---- S = K Q^T (16 tokens x 8 rows a block), fp32; two chains hide the instruction's latency ----
-                float z[BPI][4];  // tokens gid (0, 1) and gid + 8 (2, 3) x rows 2tig, 2tig+1
+                // ---- S = K Q^T (16 tokens x 8 rows a block and column tile), fp32; two chains hide the
+                // instruction's latency where there is one tile ----
+                float z[NT][BPI][4];  // tokens gid (0, 1) and gid + 8 (2, 3) x the lane's rows
 #pragma unroll
                 for (int u = 0; u < BPI; ++u) {
-                    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+                    float sa[NT][4], sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) sa[nt][0] = sa[nt][1] = sa[nt][2] = sa[nt][3] = 0.f;
 #pragma unroll
                     for (int i = 0; i < S::KCH; ++i) {
                         const int c = S::k_chunk(tig, i);
@@ -745,125 +764,126 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                             for (int w = 0; w < 4; ++w) {
                                 const uint32_t af[4] = {e4m3x2_to_half2(wl[w]), e4m3x2_to_half2(wh[w]),
                                                         e4m3x2_to_half2(wl[w] >> 16), e4m3x2_to_half2(wh[w] >> 16)};
-                                M::mma((w & 1) ? sb : sa, af, qb[i * 4 + w][0], qb[i * 4 + w][1]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    M::mma(NT == 1 && (w & 1) ? sb : sa[nt], af, qb[nt][i * 4 + w][0], qb[nt][i * 4 + w][1]);
                             }
                         } else {
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
                                 const uint32_t af[4] = {wl[2 * w], wh[2 * w], wl[2 * w + 1], wh[2 * w + 1]};
-                                M::mma(w ? sb : sa, af, qb[i * 2 + w][0], qb[i * 2 + w][1]);
+                                M::mma(w ? sb : sa[0], af, qb[0][i * 2 + w][0], qb[0][i * 2 + w][1]);
                             }
                         }
                     }
                     const bool v0 = gid < nvalid[u], v1 = gid + 8 < nvalid[u];
-                    const float f0 = zf[0] * sc2[u].x, f1 = zf[1] * sc2[u].x;
-                    z[u][0] = v0 ? (sa[0] + sb[0]) * f0 : -INFINITY;
-                    z[u][1] = v0 ? (sa[1] + sb[1]) * f1 : -INFINITY;
-                    z[u][2] = v1 ? (sa[2] + sb[2]) * f0 : -INFINITY;
-                    z[u][3] = v1 ? (sa[3] + sb[3]) * f1 : -INFINITY;
-                    if constexpr (MULTI) {  // each column's token sees the positions up to its own
-                        const int pos = jb + u * kBlock + gid;
-                        const int e0 = seq.first + (2 * tig >> fa.shift), e1 = seq.first + (2 * tig + 1 >> fa.shift);
-                        if (pos >= e0) z[u][0] = -INFINITY;
-                        if (pos >= e1) z[u][1] = -INFINITY;
-                        if (pos + 8 >= e0) z[u][2] = -INFINITY;
-                        if (pos + 8 >= e1) z[u][3] = -INFINITY;
-                    }
-                }
-                // ---- online softmax ----
-                float mx0 = -INFINITY, mx1 = -INFINITY;
-                float ev[BPI], mo0 = m_out[0], mo1 = m_out[1];
-                if constexpr (Q8) {
-                    // the largest z + log2 S_V of the iteration needs each block's own maximum
 #pragma unroll
-                    for (int u = 0; u < BPI; ++u) {
-                        float a0 = fmaxf(z[u][0], z[u][2]), a1 = fmaxf(z[u][1], z[u][3]);
-                        mx0 = fmaxf(mx0, a0);
-                        mx1 = fmaxf(mx1, a1);
-                        ev[u] = nvalid[u] > 0 ? __log2f(sc2[u].y) : 0.f;  // of a power of two; -inf for 0
-                        mo0 = fmaxf(mo0, a0 + ev[u]);
-                        mo1 = fmaxf(mo1, a1 + ev[u]);
-                    }
-#pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) {
-                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                        mo0 = fmaxf(mo0, __shfl_xor_sync(0xffffffffu, mo0, o));
-                        mo1 = fmaxf(mo1, __shfl_xor_sync(0xffffffffu, mo1, o));
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < BPI; ++u) {
-                        mx0 = fmaxf(mx0, fmaxf(z[u][0], z[u][2]));
-                        mx1 = fmaxf(mx1, fmaxf(z[u][1], z[u][3]));
-                    }
-#pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) {
-                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                    }
-                }
-                if (zrow != nullptr && 2 * tig < G) {
-#pragma unroll
-                    for (int u = 0; u < BPI; ++u) {
-                        float* zt = zrow + (size_t)(jb - z0 + u * kBlock + gid) * G + 2 * tig;
-                        const bool v0 = jb + u * kBlock + gid < z_end, v1 = jb + u * kBlock + gid + 8 < z_end;
-                        if constexpr (G == 1) {
-                            if (v0) zt[0] = z[u][0];
-                            if (v1) zt[8] = z[u][2];
-                        } else {
-                            if (v0) *reinterpret_cast<float2*>(zt) = make_float2(z[u][0], z[u][1]);
-                            if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(z[u][2], z[u][3]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* x = z[nt][u];
+                        const float f0 = zf[nt][0] * sc2[u].x, f1 = zf[nt][1] * sc2[u].x;
+                        x[0] = v0 ? (NT == 1 ? sa[nt][0] + sb[0] : sa[nt][0]) * f0 : -INFINITY;
+                        x[1] = v0 ? (NT == 1 ? sa[nt][1] + sb[1] : sa[nt][1]) * f1 : -INFINITY;
+                        x[2] = v1 ? (NT == 1 ? sa[nt][2] + sb[2] : sa[nt][2]) * f0 : -INFINITY;
+                        x[3] = v1 ? (NT == 1 ? sa[nt][3] + sb[3] : sa[nt][3]) * f1 : -INFINITY;
+                        if constexpr (MULTI) {  // each column's token sees the positions up to its own
+                            const int pos = jb + u * kBlock + gid, r = nt * 8 + 2 * tig;
+                            const int e0 = seq.first + (r >> fa.shift), e1 = seq.first + (r + 1 >> fa.shift);
+                            if (pos >= e0) x[0] = -INFINITY;
+                            if (pos >= e1) x[1] = -INFINITY;
+                            if (pos + 8 >= e0) x[2] = -INFINITY;
+                            if (pos + 8 >= e1) x[3] = -INFINITY;
                         }
                     }
                 }
-                // A maximum of -inf (nothing but -inf or NaN logits so far) stands for 0: 2^(-inf - 0) is 0.
-                const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
-                const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;
-                float al0 = ex2(m_run[0] - ms0), al1 = ex2(m_run[1] - ms1);
-                m_run[0] = mn0;
-                m_run[1] = mn1;
-                float sum0 = 0.f, sum1 = 0.f;
-                float c0 = 0.f, c1 = 0.f, be0 = 1.f, be1 = 1.f;
-                if constexpr (Q8) {
-                    const float os0 = mo0 == -INFINITY ? 0.f : mo0, os1 = mo1 == -INFINITY ? 0.f : mo1;
-                    be0 = ex2(m_out[0] - os0);
-                    be1 = ex2(m_out[1] - os1);
-                    m_out[0] = mo0;
-                    m_out[1] = mo1;
-                    c0 = kWeightExp - os0;
-                    c1 = kWeightExp - os1;
-                } else {
-                    be0 = al0;
-                    be1 = al1;
-                }
+                float ev[BPI];  // log2 S_V of the blocks (of a power of two; -inf for 0)
 #pragma unroll
-                for (int u = 0; u < BPI; ++u) {
-                    // the sum is of the weights before rounding: the scores divide by it in fp32
-                    const float p0 = ex2(z[u][0] - ms0), p1 = ex2(z[u][1] - ms1), p2 = ex2(z[u][2] - ms0), p3 = ex2(z[u][3] - ms1);
-                    sum0 += p0 + p2;
-                    sum1 += p1 + p3;
-                    uint32_t pa, pb;  // tokens gid, gid + 8: rows 2tig, 2tig+1
-                    if constexpr (Q8) {
-                        const float e0 = ev[u] + c0, e1 = ev[u] + c1;
-                        pa = M::pack(ex2(z[u][0] + e0), ex2(z[u][1] + e1));
-                        pb = M::pack(ex2(z[u][2] + e0), ex2(z[u][3] + e1));
-                    } else {
-                        pa = M::pack(p0 * kUp, p1 * kUp);
-                        pb = M::pack(p2 * kUp, p3 * kUp);
+                for (int u = 0; u < BPI; ++u) ev[u] = Q8 && nvalid[u] > 0 ? __log2f(sc2[u].y) : 0.f;
+                if constexpr (!MULTI) {
+                    if (zrow != nullptr && 2 * tig < G) {
+#pragma unroll
+                        for (int u = 0; u < BPI; ++u) {
+                            const float* x = z[0][u];
+                            float* zt = zrow + (size_t)(jb - z0 + u * kBlock + gid) * G + 2 * tig;
+                            const bool v0 = jb + u * kBlock + gid < z_end, v1 = jb + u * kBlock + gid + 8 < z_end;
+                            if constexpr (G == 1) {
+                                if (v0) zt[0] = x[0];
+                                if (v1) zt[8] = x[2];
+                            } else {
+                                if (v0) *reinterpret_cast<float2*>(zt) = make_float2(x[0], x[1]);
+                                if (v1) *reinterpret_cast<float2*>(zt + 8 * G) = make_float2(x[2], x[3]);
+                            }
+                        }
                     }
-                    b0f[u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
-                    b1f[u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
                 }
-                l_run[0] = fmaf(l_run[0], al0, sum0);
-                l_run[1] = fmaf(l_run[1], al1, sum1);
-                if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {
+                // ---- online softmax ----
 #pragma unroll
-                    for (int mt = 0; mt < KSTEPS; ++mt) {
-                        acc[mt][0] *= be0;
-                        acc[mt][1] *= be1;
-                        acc[mt][2] *= be0;
-                        acc[mt][3] *= be1;
+                for (int nt = 0; nt < NT; ++nt) {
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mo0 = m_out[nt][0], mo1 = m_out[nt][1];
+#pragma unroll
+                    for (int u = 0; u < BPI; ++u) {
+                        const float a0 = fmaxf(z[nt][u][0], z[nt][u][2]), a1 = fmaxf(z[nt][u][1], z[nt][u][3]);
+                        mx0 = fmaxf(mx0, a0);
+                        mx1 = fmaxf(mx1, a1);
+                        if constexpr (Q8) {  // the largest z + log2 S_V of the iteration needs each block's own maximum
+                            mo0 = fmaxf(mo0, a0 + ev[u]);
+                            mo1 = fmaxf(mo1, a1 + ev[u]);
+                        }
+                    }
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                        if constexpr (Q8) {
+                            mo0 = fmaxf(mo0, __shfl_xor_sync(0xffffffffu, mo0, o));
+                            mo1 = fmaxf(mo1, __shfl_xor_sync(0xffffffffu, mo1, o));
+                        }
+                    }
+                    // A maximum of -inf (nothing but -inf or NaN logits so far) stands for 0: 2^(-inf - 0) is 0.
+                    const float mn0 = fmaxf(m_run[nt][0], mx0), mn1 = fmaxf(m_run[nt][1], mx1);
+                    const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;
+                    const float al0 = ex2(m_run[nt][0] - ms0), al1 = ex2(m_run[nt][1] - ms1);
+                    m_run[nt][0] = mn0;
+                    m_run[nt][1] = mn1;
+                    float sum0 = 0.f, sum1 = 0.f;
+                    float c0 = 0.f, c1 = 0.f, be0 = al0, be1 = al1;
+                    if constexpr (Q8) {
+                        const float os0 = mo0 == -INFINITY ? 0.f : mo0, os1 = mo1 == -INFINITY ? 0.f : mo1;
+                        be0 = ex2(m_out[nt][0] - os0);
+                        be1 = ex2(m_out[nt][1] - os1);
+                        m_out[nt][0] = mo0;
+                        m_out[nt][1] = mo1;
+                        c0 = kWeightExp - os0;
+                        c1 = kWeightExp - os1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < BPI; ++u) {
+                        // the sum is of the weights before rounding: the scores divide by it in fp32
+                        const float* x = z[nt][u];
+                        const float p0 = ex2(x[0] - ms0), p1 = ex2(x[1] - ms1), p2 = ex2(x[2] - ms0), p3 = ex2(x[3] - ms1);
+                        sum0 += p0 + p2;
+                        sum1 += p1 + p3;
+                        uint32_t pa, pb;  // tokens gid, gid + 8: the lane's rows
+                        if constexpr (Q8) {
+                            const float e0 = ev[u] + c0, e1 = ev[u] + c1;
+                            pa = M::pack(ex2(x[0] + e0), ex2(x[1] + e1));
+                            pb = M::pack(ex2(x[2] + e0), ex2(x[3] + e1));
+                        } else {
+                            pa = M::pack(p0 * kUp, p1 * kUp);
+                            pb = M::pack(p2 * kUp, p3 * kUp);
+                        }
+                        b0f[nt][u] = movmatrix_trans(pa);  // P^T: tokens 2tig, 2tig+1 of row gid
+                        b1f[nt][u] = movmatrix_trans(pb);  // tokens 8+2tig, 9+2tig of row gid
+                    }
+                    l_run[nt][0] = fmaf(l_run[nt][0], al0, sum0);
+                    l_run[nt][1] = fmaf(l_run[nt][1], al1, sum1);
+                    if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {
+#pragma unroll
+                        for (int mt = 0; mt < KSTEPS; ++mt) {
+                            acc[nt][mt][0] *= be0;
+                            acc[nt][mt][1] *= be1;
+                            acc[nt][mt][2] *= be0;
+                            acc[nt][mt][3] *= be1;
+                        }
                     }
                 }
             } else if (zrow != nullptr) {  // blocks outside the pool: their positions weigh nothing
@@ -927,7 +947,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                         if (__any_sync(0xffffffffu, nan)) {
                             for (int i = 0; i < seq.tokens; ++i) {
                                 const int seen = seq.first + i - (jb + u * kBlock);  // rows of the block that token i sees
-                                const bool c0 = 2 * tig >> fa.shift == i, c1 = (2 * tig + 1) >> fa.shift == i;
 #pragma unroll
                                 for (int x = 0; x < WORDS; ++x) {
                                     uint32_t v[4];
@@ -939,16 +958,20 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                                         const uint32_t x01 = __byte_perm(v[0], v[1], sel), x23 = __byte_perm(v[2], v[3], sel);
                                         const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
                                                                 e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
-                                        float part[4] = {0.f, 0.f, 0.f, 0.f};
-                                        M::mma(part, af, b0f[u], b1f[u]);
-                                        float* to = acc[(pn * WORDS + x) * 2 + h];
-                                        if (c0) {
-                                            to[0] += part[0];
-                                            to[2] += part[2];
-                                        }
-                                        if (c1) {
-                                            to[1] += part[1];
-                                            to[3] += part[3];
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt) {
+                                            const int r = nt * 8 + 2 * tig;
+                                            float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                            M::mma(part, af, b0f[nt][u], b1f[nt][u]);
+                                            float* to = acc[nt][(pn * WORDS + x) * 2 + h];
+                                            if (r >> fa.shift == i) {
+                                                to[0] += part[0];
+                                                to[2] += part[2];
+                                            }
+                                            if (r + 1 >> fa.shift == i) {
+                                                to[1] += part[1];
+                                                to[3] += part[3];
+                                            }
                                         }
                                     }
                                 }
@@ -966,12 +989,14 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
                                 const uint32_t x23 = __byte_perm(w[2][x], w[3][x], sel);
                                 const uint32_t af[4] = {e4m3x2_to_half2(x01), e4m3x2_to_half2(x01 >> 16),
                                                         e4m3x2_to_half2(x23), e4m3x2_to_half2(x23 >> 16)};
-                                M::mma(acc[(pn * WORDS + x) * 2 + h], af, b0f[u], b1f[u]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    M::mma(acc[nt][(pn * WORDS + x) * 2 + h], af, b0f[nt][u], b1f[nt][u]);
                             }
                         } else {
                             const uint32_t af[4] = {__byte_perm(w[0][x], w[1][x], 0x5410u), __byte_perm(w[0][x], w[1][x], 0x7632u),
                                                     __byte_perm(w[2][x], w[3][x], 0x5410u), __byte_perm(w[2][x], w[3][x], 0x7632u)};
-                            M::mma(acc[pn * WORDS + x], af, b0f[u], b1f[u]);
+                            M::mma(acc[0][pn * WORDS + x], af, b0f[0][u], b1f[0][u]);
                         }
                     }
                 }
@@ -984,48 +1009,54 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
         }
 
         // ---- row sums over the 8 lanes sharing a row; the accumulator in units of 2^m_run ----
+        float fo[NT][2];
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) {
-            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
-            l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
-        }
-        float fo[2] = {1.f / kUp, 1.f / kUp};
-        if constexpr (Q8) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) fo[r] = m_out[r] == -INFINITY ? 0.f : exp2f(m_out[r] - kWeightExp - m_run[r]);
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) l_run[nt][r] += __shfl_xor_sync(0xffffffffu, l_run[nt][r], o);
+                fo[nt][r] = 1.f / kUp;
+                if constexpr (Q8)
+                    fo[nt][r] = m_out[nt][r] == -INFINITY ? 0.f : exp2f(m_out[nt][r] - kWeightExp - m_run[nt][r]);
+            }
         }
 
         // ---- join the warps ----
         __syncthreads();  // the rings have been read
         float* s_acc = reinterpret_cast<float*>(smem);  // [NW][G][D]
 #pragma unroll
-        for (int mt = 0; mt < KSTEPS; ++mt) {
-            constexpr int WORDS = S::PANB / 32;
-            constexpr int PER_PANEL = Q8 ? 2 * WORDS : WORDS;       // m-tiles per panel
-            constexpr int PAN_D = S::PANB / (Q8 ? 1 : 2);           // dims per panel
-            const int d0 = (mt / PER_PANEL) * PAN_D + gid * (2 * PER_PANEL) + 2 * (mt % PER_PANEL);
-            const int r0 = 2 * tig;
-            float* base = s_acc + (size_t)warp * G * D;
-            if (r0 < G) *reinterpret_cast<float2*>(base + r0 * D + d0) = make_float2(acc[mt][0] * fo[0], acc[mt][2] * fo[0]);
-            if (r0 + 1 < G)
-                *reinterpret_cast<float2*>(base + (r0 + 1) * D + d0) = make_float2(acc[mt][1] * fo[1], acc[mt][3] * fo[1]);
-        }
-        if (gid == 0) {
-            s_ml[warp * 8 + 2 * tig] = make_float2(m_run[0], l_run[0]);
-            s_ml[warp * 8 + 2 * tig + 1] = make_float2(m_run[1], l_run[1]);
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r0 = nt * 8 + 2 * tig;
+#pragma unroll
+            for (int mt = 0; mt < KSTEPS; ++mt) {
+                constexpr int WORDS = S::PANB / 32;
+                constexpr int PER_PANEL = Q8 ? 2 * WORDS : WORDS;       // m-tiles per panel
+                constexpr int PAN_D = S::PANB / (Q8 ? 1 : 2);           // dims per panel
+                const int d0 = (mt / PER_PANEL) * PAN_D + gid * (2 * PER_PANEL) + 2 * (mt % PER_PANEL);
+                const float* x = acc[nt][mt];
+                float* base = s_acc + (size_t)warp * G * D;
+                if (r0 < G) *reinterpret_cast<float2*>(base + r0 * D + d0) = make_float2(x[0] * fo[nt][0], x[2] * fo[nt][0]);
+                if (r0 + 1 < G)
+                    *reinterpret_cast<float2*>(base + (r0 + 1) * D + d0) = make_float2(x[1] * fo[nt][1], x[3] * fo[nt][1]);
+            }
+            if (gid == 0) {
+                s_ml[warp * S::COLS + r0] = make_float2(m_run[nt][0], l_run[nt][0]);
+                s_ml[warp * S::COLS + r0 + 1] = make_float2(m_run[nt][1], l_run[nt][1]);
+            }
         }
         __syncthreads();
-        float* s_max = s_join + 8 * NW;
-        float* s_sum = s_max + 8;
+        float* s_max = s_join + S::COLS * NW;
+        float* s_sum = s_max + S::COLS;
         if (threadIdx.x < G) {
             const int r = threadIdx.x;
             float Mx = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) Mx = fmaxf(Mx, s_ml[w * 8 + r].x);
+            for (int w = 0; w < NW; ++w) Mx = fmaxf(Mx, s_ml[w * S::COLS + r].x);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 // a warp without a finite maximum adds its sum times zero: nothing, or the NaN of its logits
-                const float2 u = s_ml[w * 8 + r];
+                const float2 u = s_ml[w * S::COLS + r];
                 const float f = u.x == -INFINITY ? 0.f : ex2(u.x - Mx);
                 s_join[r * NW + w] = f;
                 L = fmaf(u.y, f, L);
@@ -1117,8 +1148,8 @@ struct FragKernel {
     // codes, 10 x 30,000 tokens, 8 x 4 heads: 64 KiB 105 us, 96 KiB 99, 128 KiB 103, 192 KiB 115).
     static constexpr int NW = 4;
     static constexpr int ST = 1;
-    static constexpr int BPI = Q8 && D == 64 ? 4 : !Q8 && D == 256 ? 1 : 2;
-    static constexpr int CTAS = D == 256 ? 2 : !Q8 || D == 128 ? 3 : 4;
+    static constexpr int BPI = Q8 && D == 64 && G <= 8 ? 4 : !Q8 && D == 256 ? 1 : 2;
+    static constexpr int CTAS = D == 256 || G > 8 ? 2 : !Q8 || D == 128 ? 3 : 4;
     static constexpr size_t smem = FragGeom<Q8, D, G, NW, ST, BPI>::ALLOC;
     static unsigned long long attr_done;
     static int resident[64];
@@ -1178,26 +1209,30 @@ cudaError_t launch_frag_of(int head_dim, int group, const FragArgs& a, const CUt
     return cudaErrorInvalidValue;
 }
 
-// Prompt chunks (MULTI): eight columns whatever the group is.
+// Prompt chunks (MULTI): `columns` query rows (tokens x heads of the group) a pair, 8 or 2,048 / D.
 template <typename T>
-cudaError_t frag_multi_ctas_per_sm_of(int head_dim, int* out) {
-    switch (head_dim) {
-    case 64: return FragKernel<T, true, 64, 8, true>::ctas_per_sm(out);
-    case 128: return FragKernel<T, true, 128, 8, true>::ctas_per_sm(out);
-    case 256: return FragKernel<T, true, 256, 8, true>::ctas_per_sm(out);
-    default: return cudaErrorInvalidValue;
-    }
+cudaError_t frag_multi_ctas_per_sm_of(int head_dim, int columns, int* out) {
+    if (columns == 8) switch (head_dim) {
+        case 64: return FragKernel<T, true, 64, 8, true>::ctas_per_sm(out);
+        case 128: return FragKernel<T, true, 128, 8, true>::ctas_per_sm(out);
+        case 256: return FragKernel<T, true, 256, 8, true>::ctas_per_sm(out);
+        }
+    if (head_dim == 64 && columns == 32) return FragKernel<T, true, 64, 32, true>::ctas_per_sm(out);
+    if (head_dim == 128 && columns == 16) return FragKernel<T, true, 128, 16, true>::ctas_per_sm(out);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t launch_frag_multi_of(int head_dim, const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 cudaStream_t stream) {
-    switch (head_dim) {
-    case 64: return FragKernel<T, true, 64, 8, true>::launch(a, tk, tv, stream);
-    case 128: return FragKernel<T, true, 128, 8, true>::launch(a, tk, tv, stream);
-    case 256: return FragKernel<T, true, 256, 8, true>::launch(a, tk, tv, stream);
-    default: return cudaErrorInvalidValue;
-    }
+cudaError_t launch_frag_multi_of(int head_dim, int columns, const FragArgs& a, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, cudaStream_t stream) {
+    if (columns == 8) switch (head_dim) {
+        case 64: return FragKernel<T, true, 64, 8, true>::launch(a, tk, tv, stream);
+        case 128: return FragKernel<T, true, 128, 8, true>::launch(a, tk, tv, stream);
+        case 256: return FragKernel<T, true, 256, 8, true>::launch(a, tk, tv, stream);
+        }
+    if (head_dim == 64 && columns == 32) return FragKernel<T, true, 64, 32, true>::launch(a, tk, tv, stream);
+    if (head_dim == 128 && columns == 16) return FragKernel<T, true, 128, 16, true>::launch(a, tk, tv, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace pkv

@@ -12,11 +12,13 @@ cudaError_t frag_ctas_per_sm_q8_f16(int head_dim, int group, int* out) {
     return frag_ctas_per_sm_of<__half, true>(head_dim, group, out);
 }
 
-cudaError_t launch_frag_multi_f16(int head_dim, const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_frag_multi_f16(int head_dim, int columns, const FragArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t stream) {
-    return launch_frag_multi_of<__half>(head_dim, a, tk, tv, stream);
+    return launch_frag_multi_of<__half>(head_dim, columns, a, tk, tv, stream);
 }
 
-cudaError_t frag_multi_ctas_per_sm_f16(int head_dim, int* out) { return frag_multi_ctas_per_sm_of<__half>(head_dim, out); }
+cudaError_t frag_multi_ctas_per_sm_f16(int head_dim, int columns, int* out) {
+    return frag_multi_ctas_per_sm_of<__half>(head_dim, columns, out);
+}
 
 }  // namespace pkv

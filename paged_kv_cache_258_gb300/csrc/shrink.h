@@ -40,10 +40,10 @@ struct FragArgs {
     float* z = nullptr;               // [n_seqs][n_kv][max_blocks*16][G] base-2 logits, or null
     float* scores = nullptr;          // partitions: [n_seqs][n_kv][score_stride], or null
     long long score_stride = 0;
-    // Prompt chunks (8 columns of 8 / G tokens x G heads): d.n_seqs = sequences x groups of tokens.
+    // Prompt chunks (C columns of C / G tokens x G heads): d.n_seqs = sequences x groups of tokens.
     const int32_t* q_start = nullptr; // [sequences + 1]
     int n_tokens = 0, max_query = 0;
-    int groups = 0;                   // groups of a sequence: ceil(max_query / (8 / G))
+    int groups = 0;                   // groups of a sequence: ceil(max_query / (C / G))
     int shift = 0;                    // log2 G
     int partition = 0;                // > 0: a grid of partitions of so many blocks, n_parts a cluster; 0: runs
 };
@@ -143,8 +143,8 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 
 cudaError_t frag_ctas_per_sm(int dtype, bool q8, int head_dim, int group, int* out);
 cudaError_t launch_frag_decode(int dtype, bool q8, int head_dim, int group, const FragArgs& a, cudaStream_t stream);
-cudaError_t frag_multi_ctas_per_sm(int dtype, int head_dim, int* out);
-cudaError_t launch_frag_multi(int dtype, int head_dim, const FragArgs& a, cudaStream_t stream);
+cudaError_t frag_multi_ctas_per_sm(int dtype, int head_dim, int columns, int* out);
+cudaError_t launch_frag_multi(int dtype, int head_dim, int columns, const FragArgs& a, cudaStream_t stream);
 cudaError_t launch_scores(const ScoreArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_append(int dtype, int head_dim, const Q8AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_copy(const Q8CopyArgs& a, cudaStream_t stream);

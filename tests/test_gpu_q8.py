@@ -419,7 +419,7 @@ def prefill(desc, t, q, lens, counts, scale, dtype, extra_rows=0):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
 def test_short_chunks_over_long_contexts(dtype, d, G):
-    """Chunks that go by groups of 8 / G tokens (one launch): counts around the group's size, an empty
+    """Chunks that go by passes of 8 rows or more (one launch): counts around the group's size, an empty
     chunk, contexts in runs and in partitions."""
     n_kv = 2
     for lens, counts in (([3000, 40, 9, 700], [11, 1, 9, 0]), ([130], [3])):
@@ -436,6 +436,50 @@ def test_short_chunks_over_long_contexts(dtype, d, G):
                                            np.array([lens[s] - n + i + 1]), scale, dtype, 2.0 ** -11)
                 assert np.all(np.abs(got[row] - want[0]) <= tol[0]), (s, i)
                 row += 1
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_chunks_in_wide_passes(dtype, d, G):
+    """Chunks of more rows than a column tile, tables wide enough that the passes take several tiles: chunks
+    that end inside a pass, inside a tile, one token, none, and a whole context."""
+    n_kv = 2
+    tokens = 80 // G                                   # 80 rows: 2.5 passes of 32, 5 of 16
+    lens, counts = [900, 300, tokens, 33, 17], [tokens, tokens - 3, tokens, 1, 0]
+    desc, t, _, kf, vf, tables, lens = q8_case(dtype, lens, G * n_kv, n_kv, d, seed=5 * d + G, max_blocks=700)
+    q, qf = values(np.random.default_rng(16), (sum(counts) + 2, G * n_kv, d), dtype)
+    scale = 1 / np.sqrt(d) / 16
+    got, launches = prefill(desc, t, q, lens, counts, scale, dtype, extra_rows=2)
+    assert launches == 1 and pkv.pkv_get_device_status() == 0
+    assert np.all(got[sum(counts):] == 7.0)
+    row = 0
+    for s, n in enumerate(counts):
+        for i in range(n):
+            want, tol, _, _ = R.decode(qf[row:row + 1], np.nan_to_num(kf), np.nan_to_num(vf), tables[s:s + 1],
+                                       np.array([lens[s] - n + i + 1]), scale, dtype, 2.0 ** -11)
+            assert np.all(np.abs(got[row] - want[0]) <= tol[0]), (s, i)
+            row += 1
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 2), (128, 8)])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_wide_passes_are_causal_about_nan(d, G, where):
+    """A NaN in the row of a new token, in the middle of a pass, reaches that token and the later ones only."""
+    n_kv, length, tokens = 1, 2000, 48 // G
+    desc, t, _, kf, vf, tables, lens = q8_case("bf16", [length], G, n_kv, d, seed=24, max_blocks=9000)
+    at = tokens // 2 + 1
+    bad = length - tokens + at
+    t[where].view(torch.uint8)[0, int(tables[0, bad // 16]), 0, bad % 16, 41] = 0x7F
+    q, _ = values(np.random.default_rng(17), (tokens, G, d), "bf16")
+    got, launches = prefill(desc, t, q, lens, [tokens], 0.01, "bf16")
+    assert launches == 1
+    nan = np.isnan(got)
+    assert not nan[:at].any()
+    if where == "k":
+        assert nan[at:].all()
+    else:
+        assert nan[at:, :, 41].all() and not np.delete(nan, 41, axis=2).any()
 
 
 @pytest.mark.parametrize("G", [1, 4])
