@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     const int rounds = min(kKeys, (c + NT - 1) / NT);
     const int piece = NT * rounds;
     const int pieces = c > 0 ? (c + piece - 1) / piece : 0;
-    uint32_t key[kKeys];
+    uint32_t key[kKeys] = {};
     auto at = [&](int p, int r) -> int { return p * piece + (warp * rounds + r) * 32 + lane; };
     auto load = [&](int p) {
         float x[kKeys];
@@ -98,6 +98,11 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
 #pragma unroll
         for (int r = 0; r < kKeys; ++r)
             if (r < rounds) key[r] = order_key(x[r]);
+    };
+    // bit r: this thread's r-th position of piece p lies before `end`
+    auto before = [&](int p, int end) -> uint32_t {
+        const int n = (end - at(p, 0) + 31) / 32;
+        return n <= 0 ? 0u : (1u << min(n, rounds)) - 1;
     };
     // 8-bit pools: the old scales are on their way while the selection runs
     const int nb = (c + kBlock - 1) / kBlock;
@@ -117,8 +122,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     // threshold: positions above it are kept, of those equal to it the first `ties`
     uint32_t threshold = 0xffffffffu, ties = 0;
     if (pick == older) {
-        threshold = 0;
-        ties = (uint32_t)older;
+        threshold = 0;  // (no score has key 0)
     } else if (pick > 0) {
         uint32_t prefix = 0, mask = 0, left = (uint32_t)pick;
 #pragma unroll 1
@@ -129,9 +133,10 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             __syncthreads();
             for (int p = 0; p < pieces; ++p) {
                 if (pieces > 1) load(p);
+                const uint32_t old = before(p, older);
 #pragma unroll
                 for (int r = 0; r < kKeys; ++r)
-                    if (r < rounds && at(p, r) < older && (key[r] & mask) == prefix)
+                    if ((old >> r) & 1u && (key[r] & mask) == prefix)
                         atomicAdd(&s_hist[(key[r] >> shift) & ((1u << bits) - 1)], 1u);
             }
             __syncthreads();
@@ -172,24 +177,24 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         }
         // keys from the bin's first on; or, where not all of it is kept, the first `left` of one value
         const bool whole = left == s_pick[2];
-        threshold = whole && prefix > 0 ? prefix - 1 : prefix;  // (no score has key 0)
+        threshold = whole && prefix > 0 ? prefix - 1 : prefix;
         ties = whole ? 0u : left;
     }
 
     uint32_t n_above = 0, n_equal = 0;  // positions above the threshold and equal to it, in earlier pieces
     for (int p = 0; p < pieces; ++p) {
         if (pieces > 1) load(p);
-        // positions of the recent window count as above
-        auto above_of = [&](int r) -> bool { return r < rounds && at(p, r) < c && (at(p, r) >= older || key[r] > threshold); };
-        auto equal_of = [&](int r) -> bool { return r < rounds && at(p, r) < older && key[r] == threshold; };
-        uint32_t above = 0, equal = 0;
+        uint32_t is_above = 0, is_equal = 0;  // bit r: the thread's r-th position
 #pragma unroll
         for (int r = 0; r < kKeys; ++r) {
-            if (r < rounds) {
-                above += __popc(__ballot_sync(0xffffffffu, above_of(r)));
-                equal += __popc(__ballot_sync(0xffffffffu, equal_of(r)));
-            }
+            is_above |= (key[r] > threshold ? 1u : 0u) << r;
+            is_equal |= (key[r] == threshold ? 1u : 0u) << r;
         }
+        const uint32_t old = before(p, older);
+        is_above = (is_above & old) | (before(p, c) & ~old);  // the recent window counts as above
+        is_equal &= old;
+        const uint32_t above = __reduce_add_sync(0xffffffffu, __popc(is_above));
+        const uint32_t equal = __reduce_add_sync(0xffffffffu, __popc(is_equal));
         __syncthreads();  // the piece's scores are read by all; the counts of the last piece are consumed
         if (lane == 0) {
             s_warp[warp] = above;
@@ -213,19 +218,34 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         n_above += s_pick[0];
         n_equal += s_pick[1];
         const uint32_t below = (1u << lane) - 1;
+        if (ties == 0) {
 #pragma unroll
-        for (int r = 0; r < kKeys; ++r) {
-            if (r < rounds) {
-                const bool is_above = above_of(r), is_equal = equal_of(r);
-                const uint32_t ba = __ballot_sync(0xffffffffu, is_above), be = __ballot_sync(0xffffffffu, is_equal);
-                const uint32_t eq_before = eq + __popc(be & below);
-                if (is_above || (is_equal && eq_before < ties)) {
-                    const uint32_t i = ab + __popc(ba & below) + min(eq_before, ties);
-                    kept[i] = at(p, r);
-                    out[i] = key_score(key[r]);
+            for (int r = 0; r < kKeys; ++r) {
+                if (r < rounds) {
+                    const uint32_t ba = __ballot_sync(0xffffffffu, (is_above >> r) & 1u);
+                    if ((is_above >> r) & 1u) {
+                        const uint32_t i = ab + __popc(ba & below);
+                        kept[i] = at(p, r);
+                        out[i] = key_score(key[r]);
+                    }
+                    ab += __popc(ba);
                 }
-                ab += __popc(ba);
-                eq += __popc(be);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < kKeys; ++r) {
+                if (r < rounds) {
+                    const uint32_t ba = __ballot_sync(0xffffffffu, (is_above >> r) & 1u);
+                    const uint32_t be = __ballot_sync(0xffffffffu, (is_equal >> r) & 1u);
+                    const uint32_t eq_before = eq + __popc(be & below);
+                    if ((is_above >> r) & 1u || ((is_equal >> r) & 1u && eq_before < ties)) {
+                        const uint32_t i = ab + __popc(ba & below) + min(eq_before, ties);
+                        kept[i] = at(p, r);
+                        out[i] = key_score(key[r]);
+                    }
+                    ab += __popc(ba);
+                    eq += __popc(be);
+                }
             }
         }
     }
