@@ -348,10 +348,9 @@ class DecodeBatch:
         apart = c.q8 or self.scores is not None  # append and attention in launches of their own
         if self.fused or apart:  # the step's tensors checked once (and again only when they change);
             # each layer is then one C call, or two
-            key = (q, k_new, v_new, out, float(scale))
+            key = (q, k_new, v_new, out, self.scores, float(scale))
             hit = self._launchers[st["buf"]]
-            if hit is not None and len(hit[0]) == len(key) and all(a is b for a, b in zip(hit[0][:4], key[:4])) \
-                    and hit[0][4] == key[4]:
+            if hit is not None and all(a is b for a, b in zip(hit[0][:-1], key[:-1])) and hit[0][-1] == key[-1]:
                 launch = hit[1]
             else:
                 if apart:

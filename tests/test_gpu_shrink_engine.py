@@ -313,3 +313,32 @@ def test_launchers_equal_the_calls(dtype, q8, scored):
     if not q8:
         with pytest.raises(ValueError, match="scores"):
             cache.decode_launcher(q, tables, lens, 0.1, out, ws)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_steps_reuse_their_buffers(q8):
+    """Steps into the same tensors (checked once) equal steps into new ones, also behind a change of scores."""
+    L, n, n_q, n_kv, d = 2, 3, 4, 2, 64
+    desc = pkv.make_desc("bf16", L, 60, n_q, n_kv, d)
+    got = []
+    for reuse in (True, False):
+        rng = np.random.default_rng(31)
+        cache = PagedKVCache(desc, storage="q8" if q8 else None)
+        for i in range(n):
+            cache.add_sequence(i, 20 + i)
+        batch = DecodeBatch(cache, range(n), max_blocks=8, scored=True)
+        keep = [to_torch(x, "bf16") for x in io(rng, L, n, n_q, n_kv, d, "bf16")[:3]]
+        out = torch.zeros_like(keep[0])
+        outs = []
+        for step in range(7):
+            fresh = [to_torch(x, "bf16") for x in io(rng, L, n, n_q, n_kv, d, "bf16")[:3]]
+            if reuse:
+                for a, b in zip(keep, fresh):
+                    a.copy_(b)
+            if step == 4:
+                batch.scores = batch.scores.clone()
+            batch.step(*(keep if reuse else fresh), out if reuse else (out := torch.zeros_like(out)), 0.125)
+            outs.append(out.clone())
+        got.append(outs + [batch.scores, *cache._arrays()])
+    assert all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(*got))
+    assert pkv.pkv_get_device_status() == 0
