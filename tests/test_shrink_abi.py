@@ -20,8 +20,10 @@ def test_sizes():
     d = desc_of()
     assert pkv.pkv_q8_pool_bytes(d) == 2 * 16 * 2 * 16 * 64 == pkv.pkv_pool_bytes(d) // 2
     assert pkv.pkv_q8_scale_bytes(d) == 2 * 16 * 2 * 4
-    # counters, the partial results of 640 runs (2 x 8 rows of d + 2 floats), one layer of K and V in 16 bits
-    assert pkv.pkv_q8_prefill_workspace_bytes(d) == 8192 + 640 * 2 * 8 * (64 + 2) * 4 + 2 * pkv.pkv_pool_bytes(d) // 2
+    # counters, the partial results of 640 runs (2 x 32, 16 or 8 rows of d + 2 floats), one layer of K and V in 16 bits
+    for dim, rows in ((64, 32), (128, 16), (256, 8)):
+        x = pkv.make_desc("f16", 2, 16, 4, 2, dim)
+        assert pkv.pkv_q8_prefill_workspace_bytes(x) == 8192 + 640 * 2 * rows * (dim + 2) * 4 + 2 * pkv.pkv_pool_bytes(x) // 2
     assert pkv.pkv_evict_workspace_bytes(d, 3, 7, True) == 2 * 2 * 3 * 2 * 7 * 4
     assert pkv.pkv_evict_workspace_bytes(d, 3, 7, False) == 0
     f32 = desc_of("f32")
