@@ -415,9 +415,11 @@ class DecodeBatch:
         keep = np.minimum(keep, lens).astype(np.int32)
         words = 2 * n * mb + 2 * n
         if self._evict_stage is None:
-            self._evict_stage = dict(host=torch.empty(words, dtype=torch.int32).pin_memory(),
-                                     dev=torch.empty(words, dtype=torch.int32, device=c.device), done=torch.cuda.Event(),
-                                     ws=pkv.alloc_evict_workspace(c.desc, n, mb, device=c.device) if c.q8 else None)
+            with torch.cuda.stream(self.stream):  # memory of the batch's stream: nothing queued elsewhere still uses it
+                self._evict_stage = dict(host=torch.empty(words, dtype=torch.int32).pin_memory(),
+                                         dev=torch.empty(words, dtype=torch.int32, device=c.device),
+                                         done=torch.cuda.Event(),
+                                         ws=pkv.alloc_evict_workspace(c.desc, n, mb, device=c.device) if c.q8 else None)
         stage = self._evict_stage
         stage["done"].synchronize()  # the last eviction has read its image
         with torch.cuda.stream(self.stream):

@@ -641,12 +641,14 @@ def _table_width(block_tables) -> int:
     return int(block_tables.shape[1])
 
 
-def _bytes_tensor(n: int, device):
+def _bytes_tensor(n: int, device, counters: bool = True):
+    """A buffer of n bytes, its arrival counters zeroed on the current stream if it holds any."""
     t = _torch()
     if not n:
         return None
     buf = t.empty(-(-n // 16) * 4, dtype=t.float32, device=device)
-    buf[:PKV_ARRIVAL_BYTES // 4].zero_()
+    if counters:
+        buf[:PKV_ARRIVAL_BYTES // 4].zero_()
     return buf
 
 
@@ -690,8 +692,8 @@ def alloc_q8_prefill_workspace(desc: CacheDesc, device="cuda"):
 
 
 def alloc_evict_workspace(desc: CacheDesc, n_seqs: int, max_blocks_per_seq: int, device="cuda"):
-    """A device buffer for pkv_evict_tokens over 8-bit pools."""
-    return _bytes_tensor(pkv_evict_workspace_bytes(desc, n_seqs, max_blocks_per_seq, True), device)
+    """A device buffer for pkv_evict_tokens over 8-bit pools; it needs no initialisation."""
+    return _bytes_tensor(pkv_evict_workspace_bytes(desc, n_seqs, max_blocks_per_seq, True), device, counters=False)
 
 
 def pkv_q8_append(desc: CacheDesc, layer: int, k, v, slot_mapping, k_codes, v_codes, k_scales, v_scales,

@@ -342,3 +342,48 @@ def test_steps_reuse_their_buffers(q8):
         got.append(outs + [batch.scores, *cache._arrays()])
     assert all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(*got))
     assert pkv.pkv_get_device_status() == 0
+
+
+def test_evict_on_a_stream_of_its_own(monkeypatch):
+    """A batch on a side stream whose first eviction comes while the current stream is busy: what the eviction
+    needs is allocated on the batch's stream, and its codes and scores are those of the restatement."""
+    dtype, L, n, n_q, n_kv, d, nb, mb = "bf16", 2, 3, 4, 2, 64, 64, 16
+    rng = np.random.default_rng(41)
+    desc = pkv.make_desc(dtype, L, nb, n_q, n_kv, d)
+    cache = PagedKVCache(desc, storage="q8")
+    mirror = Mirror(desc, dtype, True)
+    slots = np.concatenate([cache.add_sequence(i, c) for i, c in enumerate((200, 77, 31))])
+    _, k, v, _ = io(rng, L, len(slots), n_q, n_kv, d, dtype)
+    for layer in range(L):
+        cache.append(layer, to_torch(k[layer], dtype), to_torch(v[layer], dtype), torch.from_numpy(slots).cuda())
+    mirror.append((k, v), slots)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    batch = DecodeBatch(cache, range(n), max_blocks=mb, scored=True, stream=side)
+    q, k, v, out = io(rng, L, n, n_q, n_kv, d, dtype)
+    torch.cuda.synchronize()
+    st = batch.step(to_torch(q, dtype), to_torch(k, dtype), to_torch(v, dtype), out, 0.125)
+    torch.cuda.synchronize()
+    mirror.append((k, v), st["slots"].numpy())
+    scores = batch.scores.cpu().numpy()
+    _, src, lens = cache.mgr.pack_tables(batch.seq_ids, mb)
+    seen, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        if "cuda" in str(kw.get("device")):
+            seen.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    torch.cuda._sleep(100_000_000)                     # some 50 ms of the current stream
+    monkeypatch.setattr(torch, "empty", recorded)
+    kept = batch.evict([50, 20, 31], 4)
+    monkeypatch.undo()
+    assert len(seen) == 2 and all(s == side for s in seen)
+    torch.cuda.synchronize()
+    _, dst, new_lens = cache.mgr.pack_tables(batch.seq_ids, mb)
+    want_kept = np.full(tuple(kept.shape), -1, dtype=np.int32)
+    new = scores.copy()
+    R.evict(mirror.pools, mirror.scales, src, dst, lens, np.array([50, 20, 31]), 4, scores, new, want_kept)
+    assert np.array_equal(kept.cpu().numpy(), want_kept) and np.array_equal(batch.scores.cpu().numpy(), new)
+    mirror.check(cache, dst, new_lens)
+    assert pkv.pkv_get_device_status() == 0

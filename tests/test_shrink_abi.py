@@ -267,3 +267,13 @@ def test_scales_are_the_least_that_fit(dtype):
     for amax in (0.0, 1e-9, 447.9, 448.0, 448.1, 896.0, 65504.0, 2.0 ** -24):
         s = R.least_scale(amax, dtype)
         assert amax <= 448 * s and (s == 2.0 ** R.MIN_EXP[dtype] or amax > 448 * s / 2)
+
+
+def test_an_eviction_workspace_is_not_written_when_it_is_allocated(monkeypatch):
+    """It holds saved scales, not counters: a fill queued behind the eviction's first launch would wipe them."""
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **k).fill_(5.0))
+    assert torch.all(pkv.alloc_evict_workspace(desc_of(), 3, 700, device="cpu") == 5.0)
+    counted = pkv.alloc_q8_prefill_workspace(desc_of(), device="cpu")      # this one holds counters
+    words = pkv.PKV_ARRIVAL_BYTES // 4
+    assert not counted[:words].any() and torch.all(counted[words:] == 5.0)
