@@ -397,10 +397,12 @@ class DecodeBatch:
         """Between two steps of a scored batch: shorten each sequence to keep_lens[s] positions (an int: the
         same for all), its `recent` last ones and those with the largest scores, by (layer, KV head).
 
-        The block manager shortens the tables first (blocks that other sequences hold too are replaced, so
-        those keep their rows; PkvError with nothing changed if there are not enough free blocks), then one
-        call moves rows and scores. Returns the positions kept, int32 [L, n, n_kv, max kept] (-1 behind a
-        sequence's last).
+        Every argument is checked first. Then the block manager shortens the tables (blocks that other
+        sequences hold too are replaced, so those keep their rows), and one call moves rows and scores. An
+        argument that is refused, or PkvError because there are not enough free blocks, leaves everything as
+        it was. If CUDA refuses a launch behind that (PkvError CUDA), the tables are short and the rows have not
+        moved: free the batch's sequences. Returns the positions kept, int32 [L, n, n_kv, max kept] (-1 behind
+        a sequence's last).
         """
         import torch
         if self.scores is None:
@@ -423,8 +425,13 @@ class DecodeBatch:
         stage = self._evict_stage
         stage["done"].synchronize()  # the last eviction has read its image
         with torch.cuda.stream(self.stream):
-            kept = torch.full((*self.scores.shape[:3], max(1, int(keep.max(initial=0)))), -1, dtype=torch.int32,
-                              device=c.device)
+            kept = torch.full((c.desc.n_layers, n, c.desc.n_kv_heads, max(1, int(keep.max(initial=0)))), -1,
+                              dtype=torch.int32, device=c.device)
+        m = stage["dev"]
+        launch = pkv.evict_launcher(c.desc, c.k_pool, c.v_pool, m[:n * mb].view(n, mb), m[n * mb:2 * n * mb].view(n, mb),
+                                    m[2 * n * mb:2 * n * mb + n], m[2 * n * mb + n:], recent, self.scores, self.scores,
+                                    kept, stream=self.stream, k_scales=c.k_scales, v_scales=c.v_scales,
+                                    workspace=stage["ws"])
         rc = c.mgr.compact(self.seq_ids, keep)
         if rc != pkv.PKV_OK:
             raise pkv.PkvError(rc, "compact")
@@ -432,12 +439,9 @@ class DecodeBatch:
         if rc != pkv.PKV_OK:
             raise pkv.PkvError(rc, "pack_tables")
         stage["host"].numpy()[:] = np.concatenate([src.reshape(-1), dst.reshape(-1), lens, keep])
-        pkv.upload_metadata_ptr(stage["dev"].data_ptr(), stage["host"].data_ptr(), 4 * words, self.stream.cuda_stream)
+        pkv.upload_metadata_ptr(m.data_ptr(), stage["host"].data_ptr(), 4 * words, self.stream.cuda_stream)
         stage["done"].record(self.stream)
-        m = stage["dev"]
-        pkv.pkv_evict_tokens(c.desc, c.k_pool, c.v_pool, m[:n * mb].view(n, mb), m[n * mb:2 * n * mb].view(n, mb),
-                             m[2 * n * mb:2 * n * mb + n], m[2 * n * mb + n:], recent, self.scores, self.scores, kept,
-                             stream=self.stream, k_scales=c.k_scales, v_scales=c.v_scales, workspace=stage["ws"])
+        launch()
         return kept
 
     def kv_bytes_last_step(self) -> int:

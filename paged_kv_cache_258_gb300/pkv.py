@@ -857,17 +857,13 @@ def q8_prefill_launcher(desc: CacheDesc, q, k_codes, v_codes, k_scales, v_scales
     return launch
 
 
-def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent: int,
-                     scores, new_scores, kept, stream=None, k_scales=None, v_scales=None, workspace=None) -> None:
-    """Shorten each sequence to its `recent` last and its highest-scored positions, keep_lens[s] in all.
-
-    scores, new_scores float32 [n_layers, n_seqs, n_kv, S] (the same tensor, or two disjoint ones);
-    kept int32 [n_layers, n_seqs, n_kv, max_keep]. For 8-bit pools k_pool / v_pool are the codes, with
-    k_scales, v_scales and a workspace from alloc_evict_workspace.
-    """
+def evict_launcher(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent: int,
+                   scores, new_scores, kept, stream=None, k_scales=None, v_scales=None, workspace=None):
+    """launch(): pkv_evict_tokens with its arguments checked here, before a caller shortens any table."""
     t, f, cur = _call(desc)
     n_seqs, max_blocks = src_tables.shape[0], _table_width(src_tables)
-    if k_scales is not None or v_scales is not None:
+    q8 = k_scales is not None or v_scales is not None
+    if q8:
         if k_scales is None or v_scales is None:
             raise ValueError("8-bit pools need k_scales and v_scales")
         kp, vp, ks, vs = _q8_pools(t, f, k_pool, v_pool, k_scales, v_scales, cur)
@@ -885,14 +881,35 @@ def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, co
         raise ValueError("kept must be [n_layers, n_seqs, n_kv, max_keep]")
     max_keep = kept.shape[3]
     ws, ws_bytes = _workspace(workspace, cur)
+    # what the library would refuse at the launch: sizes, a short workspace, more than one CTA for each (layer,
+    # sequence, head) of K and of V can count
+    if recent < 0 or n_seqs and (max_blocks < 1 or max_keep < 1 or
+                                 q8 and ws_bytes < pkv_evict_workspace_bytes(desc, n_seqs, max_blocks, True)):
+        raise PkvError(PKV_ERR_INVALID_ARG, "pkv_evict_tokens")
+    if n_seqs > 65535 or f.n_layers > 65535 or 2 * n_seqs * f.n_kv * f.n_layers >= 2 ** 31:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "pkv_evict_tokens")
     tables = (n_seqs, max_blocks)
-    rc = lib().pkv_evict_tokens(
-        ctypes.byref(desc), kp, vp, ks, vs, _ptr(src_tables, "src_tables", t.int32, tables, cur),
-        _ptr(dst_tables, "dst_tables", t.int32, tables, cur), max_blocks,
-        _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur),
-        _ptr(keep_lens, "keep_lens", t.int32, (n_seqs,), cur), n_seqs, min(int(recent), 2 ** 31 - 1), sp, new, stride,
-        _ptr(kept, "kept", t.int32, (*lead, max_keep), cur), max_keep, ws, ws_bytes, _raw(stream, cur))
-    _check(rc, "pkv_evict_tokens")
+    args = (ctypes.byref(desc), kp, vp, ks, vs, _ptr(src_tables, "src_tables", t.int32, tables, cur),
+            _ptr(dst_tables, "dst_tables", t.int32, tables, cur), max_blocks,
+            _ptr(context_lens, "context_lens", t.int32, (n_seqs,), cur),
+            _ptr(keep_lens, "keep_lens", t.int32, (n_seqs,), cur), n_seqs, min(int(recent), 2 ** 31 - 1), sp, new, stride,
+            _ptr(kept, "kept", t.int32, (*lead, max_keep), cur), max_keep, ws, ws_bytes, _raw(stream, cur))
+
+    def launch() -> None:
+        _check(lib().pkv_evict_tokens(*args), "pkv_evict_tokens")
+    return launch
+
+
+def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent: int,
+                     scores, new_scores, kept, stream=None, k_scales=None, v_scales=None, workspace=None) -> None:
+    """Shorten each sequence to its `recent` last and its highest-scored positions, keep_lens[s] in all.
+
+    scores, new_scores float32 [n_layers, n_seqs, n_kv, S] (the same tensor, or two disjoint ones);
+    kept int32 [n_layers, n_seqs, n_kv, max_keep]. For 8-bit pools k_pool / v_pool are the codes, with
+    k_scales, v_scales and a workspace from alloc_evict_workspace.
+    """
+    evict_launcher(desc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent, scores, new_scores, kept,
+                   stream, k_scales, v_scales, workspace)()
 
 
 def pkv_get_device_status(stream=None) -> int:

@@ -387,3 +387,26 @@ def test_evict_on_a_stream_of_its_own(monkeypatch):
     assert np.array_equal(kept.cpu().numpy(), want_kept) and np.array_equal(batch.scores.cpu().numpy(), new)
     mirror.check(cache, dst, new_lens)
     assert pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("scores", ["half", "narrow", "host", "layers"])
+def test_a_refused_eviction_changes_nothing(q8, scores):
+    """Scores that the call cannot take are refused before any table is shortened or block released."""
+    desc = pkv.make_desc("bf16", 2, 12, 4, 2, 64)
+    cache = PagedKVCache(desc, storage="q8" if q8 else None)
+    cache.add_sequence(1, 60)
+    cache.add_sequence(2, 33)
+    cache.fork(1, 3)
+    batch = DecodeBatch(cache, [1, 2], max_blocks=4, scored=True)
+    good = batch.scores
+    batch.scores = {"half": good.half(), "narrow": good[..., :-1].contiguous(), "host": good.cpu(), "layers": good[:1]}[scores]
+    before = cache.mgr.save()
+    launches = pkv.pkv_launch_count()
+    with pytest.raises(ValueError):
+        batch.evict(10, 2)
+    assert cache.mgr.save() == before and pkv.pkv_launch_count() == launches
+    batch.scores = good
+    batch.evict(10, 2)                                  # and the batch is still good
+    assert [cache.mgr.block_table(i)[2] for i in (1, 2, 3)] == [10, 10, 60]
+    assert pkv.pkv_get_device_status() == 0
