@@ -476,7 +476,8 @@ size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
  * Short chunks are attended to straight from the codes, 8 to 32 rows (tokens x G heads) at a time. Longer
  * ones take two launches: the blocks of the listed sequences are widened into the workspace, which is indexed by
  * physical block like one layer of a 16-bit pool, and attended to from there by the kernel of 16-bit
- * pools. The choice goes by the counts that are known on the host. Arguments, bad device values, limits and errors
+ * pools. The choice goes by the counts that are known on the host; with scale <= 0 every chunk goes the first way
+ * (PKV_ERR_UNSUPPORTED past 2^30 groups of rows). Arguments, bad device values, limits and errors
  * as pkv_paged_prefill_attention.
  *   workspace     device, >= pkv_q8_prefill_workspace_bytes(desc) bytes, 16-byte aligned, memory of
  *                 the current device, its first PKV_ARRIVAL_BYTES as in pkv_q8_decode_attention; calls

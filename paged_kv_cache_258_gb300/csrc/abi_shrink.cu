@@ -396,11 +396,16 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     int sms = 0;
     if (pkv::device_status_word(&status) != cudaSuccess || pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
 
-    if ((long long)n_seqs * groups <= 65535 && by_passes(d, n_seqs, n_tokens, max_query_len, max_blocks_per_seq, columns, sms)) {
+    // The widened rows' kernel takes the largest product for the largest logit and masks before it scales, so a
+    // scale of zero or less (or NaN) goes by passes whatever they cost.
+    const long long passes = (long long)n_seqs * groups;
+    if (!(scale > 0.f) && passes > (1 << 30)) return PKV_ERR_UNSUPPORTED;  // 32-bit places of the list
+    if (!(scale > 0.f) ||
+        (passes <= 65535 && by_passes(d, n_seqs, n_tokens, max_query_len, max_blocks_per_seq, columns, sms))) {
         int per_sm = 0;
         if (pkv::frag_multi_ctas_per_sm(d->dtype, d->head_dim, columns, &per_sm) != cudaSuccess) return PKV_ERR_CUDA;
         const FragGeometry geo =
-            geometry_of((long long)n_seqs * groups * d->n_kv_heads, max_blocks_per_seq, sms, per_sm, pkv::kChunkRuns);
+            geometry_of(passes * d->n_kv_heads, max_blocks_per_seq, sms, per_sm, pkv::kChunkRuns);
         pkv::FragArgs a;
         a.d.q = q;
         a.d.k_layer = k_layer;
@@ -411,7 +416,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
         a.d.part_o = reinterpret_cast<float*>(ws + l.o);
         a.d.part_ml = reinterpret_cast<float*>(ws + l.ml);
         a.d.status = status;
-        a.d.n_seqs = n_seqs * groups;
+        a.d.n_seqs = (int)passes;
         a.d.n_q = d->n_q_heads;
         a.d.n_kv = d->n_kv_heads;
         a.d.num_blocks = d->num_blocks;

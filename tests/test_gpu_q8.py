@@ -612,3 +612,34 @@ def test_offsets_past_32_bits():
         torch.cuda.empty_cache()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def long_chunk(dtype, seed, spread=3, d=128, G=8, n_kv=2, length=600, tokens=500):
+    """A chunk that is widened (two launches), its queries and the pools: (call(scale, n), case, qf). call
+    attends to the last n tokens."""
+    desc, t, _, kf, vf, tables, lens = q8_case(dtype, [length], G * n_kv, n_kv, d, seed=seed, spread=spread)
+    q, qf = values(np.random.default_rng(seed), (tokens, G * n_kv, d), dtype)
+
+    def call(scale, n=tokens):
+        return prefill(desc, t, q[-n:], lens, [n], scale, dtype)
+    return call, (desc, t, kf, vf, tables, lens), qf
+
+
+def check_chunk(got, qf, k, v, tables, length, scale, dtype, step, factor=1, more=0.0, every=7):
+    """Every `every`-th token of a chunk at the end of one sequence against the restatement."""
+    n = len(got)
+    for i in sorted({0, 1, n - 2, n - 1} | set(range(0, n, every))):
+        want, tol, _, _ = R.decode(qf[i - n:i - n + 1 or None], k, v, tables, np.array([length - n + i + 1]), scale, dtype, step)
+        assert np.all(np.abs(got[i] - want[0]) <= factor * tol[0] + more), i
+
+
+@pytest.mark.parametrize("scale", [-0.02, 0.0, -0.0])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_chunks_of_any_scale(dtype, scale):
+    """A softmax scale of zero (equal weights) or below, over a long chunk and a short one."""
+    call, (desc, t, kf, vf, tables, lens), qf = long_chunk(dtype, seed=31)
+    assert call(0.02)[1] == 2                              # with a positive scale the long chunk is widened
+    for n in (500, 3):
+        got, launches = call(scale, n)
+        assert launches == 1 and pkv.pkv_get_device_status() == 0
+        check_chunk(got, qf, np.nan_to_num(kf), np.nan_to_num(vf), tables, 600, scale, dtype, 2.0 ** -11)
