@@ -218,7 +218,13 @@ struct UmmaSmem {
 // still meets the other at the cluster barrier before it leaves. Remote arrivals carry the
 // instruction's default (CTA-scope) semantics: a cluster-scope release put microseconds on every
 // hand-off.
-template <typename T, int D, int G>
+//
+// WIDENED: the rows were 8-bit codes a launch before (q8_pool.cu), and what a chunk gives must not depend on
+// which of the two kernels it goes through. fp16 weights then carry 2^11 and the running maximum lags by 4 at
+// most, so that the largest weight is 2^15: one keeps its 11 bits down to 2^-25 of the row's largest and counts
+// down to 2^-36 (40,000 weights of 2^-23.4 came out 16 % low without). 2,432 tokens over 30,000, 4 x 4 heads x
+// 256: lag 8 with 2^7 617 us, 4 with 2^11 618, 2 with 2^13 709, 0 with 2^15 857.
+template <typename T, int D, int G, bool WIDENED = false>
 __global__ void __launch_bounds__(256, 1)
     paged_prefill_umma_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v) {
@@ -245,6 +251,8 @@ __global__ void __launch_bounds__(256, 1)
     static_assert(BPT % VB == 0, "whole V stages per tile");
     static_assert(Tu::PT ? VPT == 1 : (VB * kBlock) % 64 == 0, "a P part is whole 64-key panels");
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float LAG = WIDENED && !BF ? 4.f : 8.f;   // how far the running maximum may lag behind
+    constexpr float UP = WIDENED && !BF ? 11.f : 0.f;   // exponent of a weight at the running maximum
     constexpr uint32_t IDESC_S = umma_idesc_f16(BF, PAIR ? 256 : 128, BN, false);
     constexpr uint32_t IDESC_PV = umma_idesc_f16(BF, PAIR ? 256 : 128, D, true);
     constexpr uint32_t S_COL = Tu::S_COL, O_COL = Tu::O_COL, Q_COL = Tu::Q_COL;
@@ -674,8 +682,8 @@ __global__ void __launch_bounds__(256, 1)
             for (int c = 0; c < BN / 2; ++c) mx4[c & 3] = fmax3(mx4[c & 3], sc[2 * c], sc[2 * c + 1]);
             const float smax = fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
             const float mt = smax * sl;  // the tile's row maximum in base 2 (scale > 0)
-            // running maximum: move it (and rescale O, l) only when it grows by more than 8
-            const bool grow = mt > m_used + 8.f;
+            // running maximum: move it (and rescale O, l) only when it grows by more than LAG
+            const bool grow = mt > m_used + LAG;
             const float m_new = grow ? mt : m_used;
             const float alpha = grow ? exp2f(m_used - m_new) : 1.f;  // 0 when m_used is -inf
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(256, 1)
             // p = 2^(s * scale_log2 - m): one (packed) FFMA and one ex2 per score; a masked score
             // (-inf) gives exactly 0. While every score so far is masked m_used is -inf: subtract 0
             // instead.
-            const float msub = m_used == -INFINITY ? 0.f : m_used;
+            const float msub = (m_used == -INFINITY ? 0.f : m_used) - UP;
             uint32_t pw[BN / 2];
             float lsf[8];
             softmax_weights<M>(sc, sl, msub, pw, lsf);
@@ -801,13 +809,13 @@ __global__ void __launch_bounds__(256, 1)
     }
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool WIDENED>
 cudaError_t launch_prefill_umma_tpl(const PrefillArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                     cudaStream_t stream) {
     using Tu = UmmaTuning<D>;
     constexpr size_t smem = UmmaSmem<D>::ALLOC;
     static_assert(smem <= 227 * 1024, "shared memory per CTA");
-    auto kern = paged_prefill_umma_kernel<T, D, G>;
+    auto kern = paged_prefill_umma_kernel<T, D, G, WIDENED>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -893,11 +901,11 @@ cudaError_t prefill_umma_wave_ctas_dtype(int head_dim, int group, int sms, int* 
     return cudaErrorInvalidValue;
 }
 
-template <typename T>
+template <typename T, bool WIDENED = false>
 cudaError_t launch_prefill_umma_dtype(int head_dim, int group, const PrefillArgs& a, const CUtensorMap& tk,
                                       const CUtensorMap& tv, cudaStream_t stream) {
 #define PKV_CASE(DD, GG) \
-    if (head_dim == DD && group == GG) return launch_prefill_umma_tpl<T, DD, GG>(a, tk, tv, stream);
+    if (head_dim == DD && group == GG) return launch_prefill_umma_tpl<T, DD, GG, WIDENED>(a, tk, tv, stream);
     PKV_CASE(64, 1) PKV_CASE(64, 2) PKV_CASE(64, 4) PKV_CASE(64, 8)
     PKV_CASE(128, 1) PKV_CASE(128, 2) PKV_CASE(128, 4) PKV_CASE(128, 8)
     PKV_CASE(256, 1) PKV_CASE(256, 2) PKV_CASE(256, 4) PKV_CASE(256, 8)

@@ -643,3 +643,27 @@ def test_chunks_of_any_scale(dtype, scale):
         got, launches = call(scale, n)
         assert launches == 1 and pkv.pkv_get_device_status() == 0
         check_chunk(got, qf, np.nan_to_num(kf), np.nan_to_num(vf), tables, 600, scale, dtype, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("dtype,d,G,n_kv", [("f16", 64, 8, 1), ("f16", 128, 8, 1), ("f16", 256, 8, 1), ("bf16", 64, 8, 1)])
+def test_chunks_of_many_small_weights(dtype, d, G, n_kv):
+    """One key outweighs each of 40,000 others by 2^23.4 and only the others have values: a long chunk (widened)
+    and a short one give their sum, each weight rounded by half a step of its own."""
+    c, tokens = 40000, 600
+    nb = c // BLOCK
+    desc = pkv.make_desc(dtype, 1, nb, G * n_kv, n_kv, d)
+    kc, vc = np.zeros((1, nb, n_kv, BLOCK, d), dtype=np.uint8), np.full((1, nb, n_kv, BLOCK, d), 0x50, dtype=np.uint8)
+    kc[0, nb // 2, :, 3], vc[0, nb // 2, :, 3] = 0x41, 0                # 2.25 and 0; the other values are 8
+    ks, vs = np.ones((2, 1, nb, n_kv), dtype=np.float32)
+    scale = 16.25 / (2.25 * d)                                          # a logit of 16.25 = 23.44 ln 2
+    t = dict(k=codes_to_torch(kc), v=codes_to_torch(vc), ks=torch.from_numpy(ks).cuda(), vs=torch.from_numpy(vs).cuda(),
+             tables=torch.arange(nb, dtype=torch.int32, device="cuda")[None])
+    ones = torch.ones((tokens, G * n_kv, d), dtype=pkv.torch_dtype(dtype))
+    want, tol, _, _ = R.decode(np.ones((1, G * n_kv, d)), R.widen(kc[0], ks[0]), R.widen(vc[0], vs[0]),
+                               np.arange(nb, dtype=np.int32)[None], np.array([c]), scale, dtype,
+                               max(2.0 ** -11, R.HALF_STEP[dtype]))
+    assert np.all(tol < 0.02 * want)
+    for n, launches in ((tokens, 2), (1, 1)):
+        got, count = prefill(desc, t, to_host(ones[:n], dtype), [c], [n], scale, dtype)
+        assert count == launches
+        assert np.all(np.abs(got[-1] - want[0]) <= 2 * tol[0])
