@@ -80,7 +80,8 @@ enum {
     PKV_DEV_BAD_PAIR = 8u,        /* copy pair id outside [0, num_blocks)                    */
     PKV_DEV_WAIT_TIMEOUT = 16u,   /* a bounded wait on an asynchronous copy gave up          */
     PKV_DEV_BAD_QUERY_RANGE = 32u,/* prefill: query_start / chunk length inconsistent         */
-    PKV_DEV_BAD_KEEP = 64u        /* eviction: kept length < 0 or > max_keep                 */
+    PKV_DEV_BAD_KEEP = 64u,       /* eviction: kept length < 0 or > max_keep                 */
+    PKV_DEV_BAD_SCALE = 128u      /* 8-bit prefill: code * scale beyond the activations' type */
 };
 
 /*
@@ -406,10 +407,12 @@ int pkv_upload_metadata(void* dst, const void* src_host, size_t bytes, void* str
  * bf16; fp32 returns PKV_ERR_UNSUPPORTED. Zero-fill the scales before first use.
  *
  * pkv_q8_append writes powers of two: the least 2^e (e >= -15 for fp16 rows, -117 for bf16) that lets
- * the block's largest finite element in, |x| <= 448 * 2^e. The attention calls take any scale >= 0.
+ * the block's largest finite element in, |x| <= 448 * 2^e. The attention calls take any finite scale >= 0
+ * (pkv_q8_prefill_attention with the limits given there).
  * Values within a factor 2^14 of the block's largest keep e4m3's relative precision (2^-4); smaller
  * ones lose bits, below 2^-10 * 2^e they round to zero. fp16 elements above 63,488 are held as 65,536; the
- * attention calls return no fp16 output beyond 65,504 for it.
+ * attention calls return no fp16 output beyond 65,504 for it. bf16 elements above 3.35e38 are held as 2^128,
+ * infinite.
  */
 
 /* Bytes of one pool of codes (K or V), and of one array of scales, over all layers; 0 if unsupported. */
@@ -479,6 +482,10 @@ size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
  * pools. The choice goes by the counts that are known on the host; with scale <= 0 every chunk goes the first way
  * (PKV_ERR_UNSUPPORTED past 2^30 groups of rows). Arguments, bad device values, limits and errors
  * as pkv_paged_prefill_attention.
+ * Widened rows are code * scale in the activations' type. That is exact for the scales that pkv_q8_append writes
+ * (powers of two, from 2^-15 for fp16 and 2^-117 for bf16). With others the long chunks read it rounded to that
+ * type, and what lies beyond the type's largest number as that number; more than a rounding beyond (2^16 for
+ * fp16, 2^128 for bf16) also sets PKV_DEV_BAD_SCALE. Short chunks and decode have neither limit.
  *   workspace     device, >= pkv_q8_prefill_workspace_bytes(desc) bytes, 16-byte aligned, memory of
  *                 the current device, its first PKV_ARRIVAL_BYTES as in pkv_q8_decode_attention; calls
  *                 that overlap on the GPU must not share one

@@ -17,6 +17,8 @@
 // Bound by latency in a decode step (three dependent trips to memory), by bytes in a long chunk.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "shrink.h"
 
@@ -247,24 +249,31 @@ __global__ void __launch_bounds__(256) q8_copy_kernel(const Q8CopyArgs a) {
         scales[(size_t)dst * a.n_kv + h] = scales[(size_t)src * a.n_kv + h];
 }
 
-// code * S in the activations' type. fp16 has no room for the 65,536 that rows near 65,504 round to:
-// it is read as the largest half.
+// x in the activations' type, beyond its largest number as that number. Codes that the append wrote reach the
+// next power of two at most: fp16 rows near 65,504 round to 65,536 (bf16 ones above 3.35e38 to 2^128).
 template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t codes, float s);
+__device__ __forceinline__ uint32_t narrow2(float x, float y);
 template <>
-__device__ __forceinline__ uint32_t widen2<__nv_bfloat16>(uint32_t codes, float s) {
-    const float2 f = from_e4m3x2(codes);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * s, f.y * s);
+__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float x, float y) {
+    constexpr float kMax = 3.38953139e38f;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(fabsf(x) > kMax ? copysignf(kMax, x) : x,
+                                                   fabsf(y) > kMax ? copysignf(kMax, y) : y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ uint32_t widen2<__half>(uint32_t codes, float s) {
-    const float2 f = from_e4m3x2(codes);
-    float x = f.x * s, y = f.y * s;
-    if (fabsf(x) == 65536.f) x = copysignf(65504.f, x);
-    if (fabsf(y) == 65536.f) y = copysignf(65504.f, y);
-    const __half2 h = __floats2half2_rn(x, y);
+__device__ __forceinline__ uint32_t narrow2<__half>(float x, float y) {
+    const __half2 h = __floats2half2_rn(fabsf(x) > 65504.f ? copysignf(65504.f, x) : x,
+                                        fabsf(y) > 65504.f ? copysignf(65504.f, y) : y);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two codes * S. `over` is raised for what lies beyond that power of two.
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, float s, bool& over) {
+    constexpr float kHalf = std::is_same<T, __half>::value ? 32768.f : 1.70141183e38f;  // of it, to stay finite
+    const float2 f = from_e4m3x2(codes);
+    over = over || fmaxf(fabsf(f.x), fabsf(f.y)) * (0.5f * s) > kHalf;
+    return narrow2<T>(f.x * s, f.y * s);
 }
 
 constexpr int kWidenWarps = 8;
@@ -295,6 +304,7 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
         for (int i = 0; i < STEPS; ++i) x[v][i] = __ldcs(src + i * 32 + lane);
         sc[v] = __ldg((v ? a.v_scales : a.k_scales) + cell);
     }
+    bool over = false;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<T*>(v ? a.v_out : a.k_out) + cell * kBlock * D);
@@ -302,15 +312,19 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
         for (int i = 0; i < STEPS; ++i) {
             const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
             uint32_t o[8];
+            bool past = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                o[2 * e] = widen2<T>(w[e], sc[v]);
-                o[2 * e + 1] = widen2<T>(w[e] >> 16, sc[v]);
+                o[2 * e] = widen2<T>(w[e], sc[v], past);
+                o[2 * e + 1] = widen2<T>(w[e] >> 16, sc[v], past);
             }
+            // (rows past the context may hold anything)
+            over = over || (past && b * kBlock + (i * 32 + lane) * 16 / D < ctx);
             out[2 * (i * 32 + lane)] = make_uint4(o[0], o[1], o[2], o[3]);
             out[2 * (i * 32 + lane) + 1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
     }
+    if (__any_sync(0xffffffffu, over) && lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_SCALE);
 }
 
 template <typename T>

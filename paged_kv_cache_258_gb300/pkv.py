@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "ok", 1: "invalid", 2: "unsupported", 3: "no_blocks", 4: "bad
 PKV_DEV_BAD_BLOCK_ID, PKV_DEV_BAD_CONTEXT_LEN, PKV_DEV_BAD_SLOT, PKV_DEV_BAD_PAIR, PKV_DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 PKV_DEV_BAD_QUERY_RANGE = 32
 PKV_DEV_BAD_KEEP = 64
+PKV_DEV_BAD_SCALE = 128
 PKV_ARRIVAL_BYTES = 8192
 PKV_DECODE_OVERLAP_PREVIOUS = 1
 PKV_PREFILL_OVERLAP_PREVIOUS = 1

@@ -667,3 +667,74 @@ def test_chunks_of_many_small_weights(dtype, d, G, n_kv):
         got, count = prefill(desc, t, to_host(ones[:n], dtype), [c], [n], scale, dtype)
         assert count == launches
         assert np.all(np.abs(got[-1] - want[0]) <= 2 * tol[0])
+
+
+def odd_scales(t, tables, names=("ks", "vs")):
+    """Scales in (0, 1/32) that are no powers of two, in place; returns both pools widened in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for n in names:
+        t[n].copy_((torch.rand(t[n].shape, device="cuda", generator=g) + 0.01) / 32.5)
+    return [np.nan_to_num(R.widen(codes_to_host(t[a])[0], t[b][0].double().cpu().numpy())) for a, b in (("k", "ks"), ("v", "vs"))]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_chunks_of_any_block_scale(dtype):
+    """Block scales that are no powers of two: exact in a short chunk; in a long one K and V are rounded to the
+    activations' type first, by half a step h of each element. A logit is then off by at most dz = h |scale|
+    sum|q||k|, a weight by a factor exp(+-2 dz), the output by that and h, relative to sum w|v|."""
+    scale = 0.01
+    call, (desc, t, _, _, tables, lens), qf = long_chunk(dtype, seed=33)
+    k, v = odd_scales(t, tables)
+    h = R.HALF_STEP[dtype]
+    for n, launches in ((500, 2), (3, 1)):
+        got, count = call(scale, n)
+        assert count == launches and pkv.pkv_get_device_status() == 0
+        for i in sorted({0, n - 1} | set(range(0, n, 31))):
+            q, c = qf[i - n:i - n + 1 or None], 600 - n + i + 1
+            want, tol, _, _ = R.decode(q, k, v, tables, np.array([c]), scale, dtype, 2.0 ** -11 if n == 3 else h)
+            more = np.zeros_like(tol[0])
+            for head in range(q.shape[1] if launches == 2 else 0):
+                kg, vg = R.rows_of(k, tables[0], c, head // 8), R.rows_of(v, tables[0], c, head // 8)
+                _, w = R.attend(q[0, head], kg, vg, scale)
+                dz = h * scale * (np.abs(kg) @ np.abs(q[0, head])).max()
+                more[head] = (np.expm1(2 * dz) + h * np.exp(2 * dz)) * (w @ np.abs(vg))
+            assert np.all(np.abs(got[i] - want[0]) <= 2 * tol[0] + more), i
+
+
+@pytest.mark.parametrize("dtype,size,top", [("f16", 200.0, 65504.0)])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_chunks_of_block_scales_out_of_range(dtype, size, top, which):
+    """Codes times scale beyond the activations' type: a short chunk takes them as they are, a long one reads
+    the type's largest number and says so. Rows and blocks that no sequence uses are not judged. (Rows near
+    bf16's largest number overflow the fp32 sums of any order, so there is nothing to compare for bf16.)"""
+    call, (desc, t, kf, vf, tables, lens), qf = long_chunk(dtype, seed=34, spread=0)
+    name = which[0]
+    codes = t[name].view(torch.uint8)
+    codes[(codes & 127) >= 0x78] = 0x76                    # up to 224 (size * 224 < top), stale NaN rows too
+    t[which].fill_(size)
+    last, used = int(tables[0, 599 // 16]), 600 % 16
+    codes[0, last, :, used:] = 0x7E                        # 448 behind the context
+    spare = next(b for b in range(desc.num_blocks) if b not in tables[0])
+    codes[0, spare] = 0x7E
+    scale = 0.01 if which == "vs" else 0.01 / size / 64    # logits of some size
+    pools = {"ks": np.nan_to_num(kf), "vs": np.nan_to_num(vf)}
+
+    def true_pool():
+        c = codes_to_host(t[name])[0].copy()
+        c[last, :, used:] = 0
+        return R.VALUES[c] * size
+    pools[which] = true_pool()
+    for n, launches in ((500, 2), (3, 1)):
+        got, count = call(scale, n)
+        assert count == launches and pkv.pkv_get_device_status() == 0
+        check_chunk(got, qf, pools["ks"], pools["vs"], tables, 600, scale, dtype, max(2.0 ** -11, R.HALF_STEP[dtype]), 2, every=61)
+    codes[0, int(tables[0, 3]), 0, 2, 7] = 0x7E            # one element of 448 * size
+    codes[0, int(tables[0, 3]), 1, 2, 9] = 0xFE
+    pools[which] = true_pool()
+    got, count = call(scale, 3)
+    assert count == 1 and pkv.pkv_get_device_status() == 0
+    check_chunk(got, qf, pools["ks"], pools["vs"], tables, 600, scale, dtype, max(2.0 ** -11, R.HALF_STEP[dtype]), 2)
+    got, count = call(scale)
+    assert count == 2 and pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_SCALE
+    pools[which] = np.clip(pools[which], -top, top)
+    check_chunk(got, qf, pools["ks"], pools["vs"], tables, 600, scale, dtype, max(2.0 ** -11, R.HALF_STEP[dtype]), 2, every=61)
