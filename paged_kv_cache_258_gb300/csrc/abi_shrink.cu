@@ -13,6 +13,7 @@ cudaError_t launch_frag_scored_bf16(int, int, const FragArgs&, const CUtensorMap
 cudaError_t launch_frag_multi_f16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_frag_multi_bf16(int, int, const FragArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t launch_prefill_widened_f16(int, int, const PrefillArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+cudaError_t launch_prefill_widened_bf16(int, int, const PrefillArgs&, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
 cudaError_t frag_multi_ctas_per_sm_f16(int, int, int*);
 cudaError_t frag_multi_ctas_per_sm_bf16(int, int, int*);
 cudaError_t frag_ctas_per_sm_q8_f16(int, int, int*);
@@ -58,14 +59,14 @@ cudaError_t launch_frag_multi(int dtype, int head_dim, int columns, const FragAr
 }
 
 cudaError_t launch_prefill_widened(int dtype, int head_dim, int group, const PrefillArgs& a, cudaStream_t stream) {
-    if (dtype == PKV_BF16) return launch_prefill(dtype, head_dim, group, a, stream);
     const long long rows = (long long)a.num_blocks * a.n_kv * kBlock;
     CUtensorMap tk, tv;
     cudaError_t err = kv_tensor_map(a.k_layer, rows, head_dim, dtype, PKV_BOX_PANEL, &tk);
     if (err == cudaSuccess)  // (at head_dim 256 each CTA of a pair copies half of a V block's columns)
         err = kv_tensor_map(a.v_layer, rows, head_dim, dtype, head_dim == 256 ? PKV_BOX_BLOCK_HALF : PKV_BOX_BLOCK, &tv);
     if (err != cudaSuccess) return err;
-    return launch_prefill_widened_f16(head_dim, group, a, tk, tv, stream);
+    return dtype == PKV_F16 ? launch_prefill_widened_f16(head_dim, group, a, tk, tv, stream)
+                            : launch_prefill_widened_bf16(head_dim, group, a, tk, tv, stream);
 }
 
 }  // namespace pkv
@@ -464,6 +465,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     w.num_blocks = d->num_blocks;
     w.max_blocks = max_blocks_per_seq;
     w.status = status;
+    w.v_nan = reinterpret_cast<unsigned int*>(ws);  // (the arrival counters are not used this way)
     // the attention of 16-bit pools over the widened layer, a pool of one layer with the same blocks
     const int per_cta = pkv::prefill_tokens_per_cta(d->dtype, d->head_dim, group);
     pkv::PrefillArgs a;
@@ -482,6 +484,8 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     a.max_blocks = max_blocks_per_seq;
     a.n_tokens = n_tokens;
     a.q_tiles = (max_query_len + per_cta - 1) / per_cta;
+    a.v_codes = v_layer;
+    a.v_nan = w.v_nan;
     a.scale_log2 = scale * 1.4426950408889634f;
     if (pkv::launch_q8_widen(d->dtype, d->head_dim, w, st) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::count_launches(1);

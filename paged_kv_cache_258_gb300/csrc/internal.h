@@ -55,6 +55,10 @@ struct PrefillArgs {
     int q_tiles;            // CTAs along the chunk: ceil(max query length / tokens per CTA)
     float scale_log2;       // scale * log2(e)
     bool overlap_previous = false;  // launch as a programmatic dependent of the previous kernel
+    // Rows widened from 8-bit codes (k_layer, v_layer hold them, NaN codes of V as 0): this layer's codes of V,
+    // and two words, [0] not 0 if NaN codes were found, [1] the CTAs that know it; both 0 between calls.
+    const uint8_t* v_codes = nullptr;
+    unsigned int* v_nan = nullptr;
 };
 
 // Query rows (token x head-in-group) one prefill CTA covers; tokens per CTA = rows / group.

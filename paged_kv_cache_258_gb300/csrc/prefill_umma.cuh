@@ -224,6 +224,9 @@ struct UmmaSmem {
 // most, so that the largest weight is 2^15: one keeps its 11 bits down to 2^-25 of the row's largest and counts
 // down to 2^-36 (40,000 weights of 2^-23.4 came out 16 % low without). 2,432 tokens over 30,000, 4 x 4 heads x
 // 256: lag 8 with 2^7 617 us, 4 with 2^11 618, 2 with 2^13 709, 0 with 2^15 857.
+// NaN codes of V were widened as 0 and reported in v_nan. If there are any, the CTA goes through V's codes up to
+// its last position when its rows are out, and puts NaN where a token sees one: in that dim of its rows,
+// whatever the weight, and in no earlier token's (0 x NaN in a product would reach those).
 template <typename T, int D, int G, bool WIDENED = false>
 __global__ void __launch_bounds__(256, 1)
     paged_prefill_umma_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tm_k,
@@ -303,6 +306,12 @@ __global__ void __launch_bounds__(256, 1)
     // (the lighter tile's causal mask zeroes the keys it does not see). Both compute the same count.
     int n_tiles = key_tiles(tile);
     if constexpr (PAIR) n_tiles = max(n_tiles, key_tiles(a.q_tiles - 1 - (int)(blockIdx.x ^ 1u)));
+    // whether V held NaN codes; the last CTA that knows clears the words for the next call
+    auto know_nan = [&](unsigned found) {
+        const unsigned last = gridDim.x * gridDim.y * gridDim.z - 1;
+        if (found != 0 && atomicInc(a.v_nan + 1, last) == last) a.v_nan[0] = 0;
+    };
+    if (WIDENED && n_tiles == 0 && threadIdx.x == 0) know_nan(a.v_nan[0]);
     if (n_tiles == 0) return;  // both CTAs of a pair leave here together, before any cluster barrier
     const int t0 = tile * QT;
     const int pos0 = ctx - n_new + t0;
@@ -798,8 +807,36 @@ __global__ void __launch_bounds__(256, 1)
             }
         }
     }
+    if (WIDENED && threadIdx.x == 4 * 32) {
+        taddr_s[1] = a.v_nan[0];
+        know_nan(taddr_s[1]);
+    }
     tcgen05_before_sync();
     __syncthreads();
+    if constexpr (WIDENED) {
+        if (taddr_s[1] != 0u) {
+            constexpr int LPV = D / 16, RPV = 32 / LPV;  // lanes of a row of codes, rows of a load
+            const int32_t* table = a.tables + (size_t)s * a.max_blocks;
+            const int rows = min(QT, n_new - t0) * G;     // live ones (none in a pair's lighter tile past the chunk)
+            const int end = pos0 + rows / G;
+            const uint8_t* codes = a.v_codes + (size_t)g * kBlock * D + (lane % LPV) * 16;
+#pragma unroll 2
+            for (int p = warp * RPV + lane / LPV; rows > 0 && p < end; p += 8 * RPV) {
+                const int phys = table[p / kBlock];
+                if ((unsigned)phys >= (unsigned)a.num_blocks) continue;
+                const uint4 c = *reinterpret_cast<const uint4*>(codes + ((size_t)phys * a.n_kv * kBlock + p % kBlock) * D);
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t word = e < 8 ? (e < 4 ? w[0] : w[1]) : (e < 12 ? w[2] : w[3]);
+                    if (((word >> (8 * (e & 3))) & 0x7fu) != 0x7fu) continue;
+                    for (int r = max(0, (p - pos0) * G); r < rows; ++r)
+                        reinterpret_cast<uint16_t*>(a.out)[((size_t)(q0 + t0 + r / G) * a.n_q + (size_t)g * G + r % G) * D +
+                                                           (lane % LPV) * 16 + e] = 0x7fffu;  // NaN in both types
+                }
+            }
+        }
+    }
     // no CTA of a pair leaves (or releases its tensor memory) while the other may still arrive on
     // its barriers or the pair's products may still write its tensor memory
     if constexpr (PAIR) cluster_sync_all();

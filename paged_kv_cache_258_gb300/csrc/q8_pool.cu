@@ -279,7 +279,9 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes, float s, bool& over) 
 constexpr int kWidenWarps = 8;
 
 // One warp per (sequence, logical block, KV head): K and V chunk, 16 codes a lane and step. Sequences
-// that share blocks write the same values to the same places.
+// that share blocks write the same values to the same places. NaN codes of V become 0 and are reported: the
+// attention kernel multiplies every row of a tile with weights, 0 for tokens that do not see it, and 0 x NaN
+// would reach those too.
 template <typename T, int D>
 __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8WidenArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,27 +306,36 @@ __global__ void __launch_bounds__(kWidenWarps * 32) q8_widen_kernel(const Q8Wide
         for (int i = 0; i < STEPS; ++i) x[v][i] = __ldcs(src + i * 32 + lane);
         sc[v] = __ldg((v ? a.v_scales : a.k_scales) + cell);
     }
-    bool over = false;
+    bool over = false, nan = false;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<T*>(v ? a.v_out : a.k_out) + cell * kBlock * D);
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
+            uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
             uint32_t o[8];
+            const bool inside = b * kBlock + (i * 32 + lane) * 16 / D < ctx;  // rows past the context may hold anything
+            if (v == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t m = __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    nan = nan || (m != 0u && inside);
+                    w[e] &= ~m;
+                }
+            }
             bool past = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 o[2 * e] = widen2<T>(w[e], sc[v], past);
                 o[2 * e + 1] = widen2<T>(w[e] >> 16, sc[v], past);
             }
-            // (rows past the context may hold anything)
-            over = over || (past && b * kBlock + (i * 32 + lane) * 16 / D < ctx);
+            over = over || (past && inside);
             out[2 * (i * 32 + lane)] = make_uint4(o[0], o[1], o[2], o[3]);
             out[2 * (i * 32 + lane) + 1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
     }
     if (__any_sync(0xffffffffu, over) && lane == 0) atomicOr(a.status, (unsigned)PKV_DEV_BAD_SCALE);
+    if (__any_sync(0xffffffffu, nan) && lane == 0) *a.v_nan = 1u;
 }
 
 template <typename T>

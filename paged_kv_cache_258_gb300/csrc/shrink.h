@@ -93,6 +93,7 @@ struct Q8WidenArgs {
     void* k_out;
     void* v_out;
     unsigned int* status;
+    unsigned int* v_nan;   // set to 1 if a row of V in a context holds a NaN code
     int n_seqs, n_kv, num_blocks, max_blocks;
 };
 
