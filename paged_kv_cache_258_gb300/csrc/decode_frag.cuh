@@ -392,7 +392,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     const int lane = threadIdx.x & 31;
     const int gid = lane >> 2;  // token row of S, chunk of V
     const int tig = lane & 3;   // owns query rows 2 tig, 2 tig + 1 of every column tile
-    grid_launch_dependents();
     if (threadIdx.x == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
@@ -403,6 +402,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS) frag_decode_kernel(const FragAr
     // Nothing in global memory has been touched so far. Loads behind the wait are plain ones: the read-only
     // path is for data that nobody writes while this grid lives, and the grid before may still be writing.
     grid_dependency_wait();
+    grid_launch_dependents();
 
     const int cap = a.max_blocks * kBlock;
     uint64_t* wbars = bars + warp * ST * 2;  // [ST][K, V]

@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     const int s = (int)(pair / a.n_kv), g = (int)(pair % a.n_kv), layer = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cap = a.max_blocks * kBlock;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();
     const int c = a.lens[s], want = a.keep[s];
     if (c < 0 || c > cap || want < 0 || min(want, c) > a.max_keep) {
         if (threadIdx.x == 0 && g == 0 && layer == 0)
@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     const int layer = (int)(rest % a.n_layers);
     int s = (int)(rest / a.n_layers);
     const int cap = a.max_blocks * kBlock;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();
     if (a.n_seqs > 1 && a.n_seqs <= kRanked) {
         int* rank_k = reinterpret_cast<int*>(s_from);
         int* by_rank = rank_k + kRanked;

@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8Ap
     const bool is_v = part >= a.n_kv;
     const int g = is_v ? part - a.n_kv : part;
     const long long first = window * kWindow;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();
     if (threadIdx.x < kReach + kSeen) {
         const long long t = first - kReach + threadIdx.x;
         long long slot = t >= 0 && t < a.n_tok ? a.slots[t] : -1;
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) q8_append_kernel(const Q8Ap
 // grid (pair, layer, K/V): each CTA copies one block of one layer, codes and scales.
 __global__ void __launch_bounds__(256) q8_copy_kernel(const Q8CopyArgs a) {
     const int layer = blockIdx.y;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();
     const int src = a.pairs[2 * blockIdx.x];
     const int dst = a.pairs[2 * blockIdx.x + 1];
     if ((unsigned)src >= (unsigned)a.num_blocks || (unsigned)dst >= (unsigned)a.num_blocks) {

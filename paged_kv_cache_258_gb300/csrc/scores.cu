@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads) add_scores_kernel(const ScoreArgs a)
     __shared__ float s_m[8], s_inv[8];
     const int s = blockIdx.z, g = blockIdx.y;
     const int cap = a.max_blocks * kBlock;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();
     const int ctx = min(max(a.lens[s], 0), cap);
     const int j0 = blockIdx.x * kThreads * kPerThread;
     if (j0 >= ctx) return;

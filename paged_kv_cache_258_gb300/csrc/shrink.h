@@ -10,7 +10,11 @@ namespace pkv {
 constexpr int kCodesE4M3 = 3;
 
 #ifdef __CUDACC__
-// Lets the next launch on the stream, if it is a programmatic dependent, be placed from here on.
+// Lets the next launch on the stream, if it is a programmatic dependent, be placed from here on. Called behind
+// the wait for the launch before: a next launch with an OVERLAP_PREVIOUS flag reads its inputs at once, trusting
+// this kernel not to write them, and must not do so while the launch before this one still may. Ahead of
+// the wait it was no faster either: a step's append and decode over 24 layers, 4 x 300 tokens in 8 bits, 206.6 us
+// against 203.4.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 #endif
 

@@ -410,3 +410,37 @@ def test_a_refused_eviction_changes_nothing(q8, scores):
     batch.evict(10, 2)                                  # and the batch is still good
     assert [cache.mgr.block_table(i)[2] for i in (1, 2, 3)] == [10, 10, 60]
     assert pkv.pkv_get_device_status() == 0
+
+
+def test_overlapped_decode_behind_an_eviction_and_a_scored_layer():
+    """A layer's append + decode that may overlap the scored decode of the layer before it, right behind an
+    eviction of both layers: it reads its pool at once, which the eviction must have left by then."""
+    dtype, L, n, n_q, n_kv, d, c, k = "bf16", 2, 8, 16, 8, 128, 6000, 2900
+    mb = -(-c // 16)
+    nb = n * mb
+    desc = pkv.make_desc(dtype, L, nb, n_q, n_kv, d)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pools = [torch.randn(pkv.pool_shape(desc), device="cuda", generator=g).bfloat16() for _ in range(2)]
+    tables = torch.randperm(nb, device="cuda", generator=g).int().view(n, mb).contiguous()
+    lens, keep, grown = (torch.full((n,), x, dtype=torch.int32, device="cuda") for x in (c, k, k + 1))
+    scores = torch.rand((L, n, n_kv, mb * 16), device="cuda", generator=g)
+    q, knew, vnew = (torch.randn((L, n, h, d), device="cuda", generator=g).bfloat16() for h in (n_q, n_kv, n_kv))
+    ws, sws = pkv.alloc_workspace(desc, n, mb), pkv.alloc_scored_workspace(desc, n, mb)
+    kept = torch.empty((L, n, n_kv, k), dtype=torch.int32, device="cuda")
+    want = None
+    for overlap in [False] + [True] * 12:
+        work, sums = [p.clone() for p in pools], scores.clone()
+        out = torch.zeros_like(q)
+        evict = pkv.evict_launcher(desc, *work, tables, tables, lens, keep, 64, sums, sums, kept)
+        first = pkv.scored_decode_launcher(desc, q, *work, tables, keep, 0.09, out, sums, sws)
+        second = pkv.decode_append_launcher(desc, q, knew, vnew, *work, tables, grown, 0.09, out, ws)
+        torch.cuda.synchronize()
+        evict()
+        first(0)
+        second(1, overlap)
+        torch.cuda.synchronize()
+        got = [out, sums, *work]
+        if want is None:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert pkv.pkv_get_device_status() == 0
