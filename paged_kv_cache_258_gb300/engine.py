@@ -254,6 +254,7 @@ class DecodeBatch:
         self.total_cow = 0
         self.manager_s = 0.0       # host time in the block manager (append + pack), waits excluded
         self.steps_planned = 0
+        self._planned = None       # the newest step planned, until it is launched
         # validated per-layer launchers, one per device metadata image, for the step tensors they
         # were built for (kept alive here, so an identity match means the same tensors)
         self._launchers = [None, None]
@@ -283,6 +284,7 @@ class DecodeBatch:
         if len(ids) != self.n:
             raise ValueError("batch size is fixed")
         if self.scores is not None and not np.array_equal(ids, self.seq_ids):
+            self._no_step_planned("set_sequences")
             # a sequence keeps its sums in its new row; one that was not in the batch starts from zero
             import torch
             row = {int(x): i for i, x in enumerate(self.seq_ids)}
@@ -295,6 +297,11 @@ class DecodeBatch:
                 self.scores.copy_(new)
         self.seq_ids = ids
         self._p_ids = ids.ctypes.data_as(ctypes.POINTER(ctypes.c_int64))
+
+    def _no_step_planned(self, what: str) -> None:
+        """A planned step's tables, and the rows it adds its weights to, are those of the time of its plan."""
+        if self._planned is not None:
+            raise ValueError(f"{what}: a step is planned and has not been launched")
 
     def plan(self) -> dict:
         """Host part of a step: reserve slots, collect CoW pairs, pack tables (pinned)."""
@@ -321,6 +328,7 @@ class DecodeBatch:
             validate_step_metadata(self.cache.desc.num_blocks, self.cache.desc.block_size, st["tables"].numpy(),
                                    st["np_lens"], st["slots"].numpy(), st["pairs"].numpy()[:npairs])
         self.steps_planned += 1
+        self._planned = st
         self.last_lens = st["np_lens"].copy()
         self.last_n_pairs = npairs
         self.total_cow += npairs
@@ -386,6 +394,8 @@ class DecodeBatch:
                 on_decode(layer, "end")
         dv["read"].record(self.stream)
         dv["used"] = True
+        if self._planned is st:
+            self._planned = None
 
     def step(self, q, k_new, v_new, out, scale: float, on_decode=None) -> dict:
         st = self.plan()
@@ -394,7 +404,7 @@ class DecodeBatch:
         return st
 
     def evict(self, keep_lens, recent: int):
-        """Between two steps of a scored batch: shorten each sequence to keep_lens[s] positions (an int: the
+        """Between two steps of a scored batch (none planned ahead): shorten each sequence to keep_lens[s] positions (an int: the
         same for all), its `recent` last ones and those with the largest scores, by (layer, KV head).
 
         Every argument is checked first. Then the block manager shortens the tables (blocks that other
@@ -407,6 +417,7 @@ class DecodeBatch:
         import torch
         if self.scores is None:
             raise ValueError("evict needs a batch with scored=True")
+        self._no_step_planned("evict")
         c, n, mb = self.cache, self.n, self.max_blocks
         rc, src, lens = c.mgr.pack_tables(self.seq_ids, mb)
         if rc != pkv.PKV_OK:

@@ -444,3 +444,31 @@ def test_overlapped_decode_behind_an_eviction_and_a_scored_layer():
             want = got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert pkv.pkv_get_device_status() == 0
+
+
+def test_a_planned_step_is_launched_before_sequences_change():
+    """Between a step's plan and its launch a scored batch refuses to shorten or reorder its sequences: the
+    step's slots and tables are of the plan's time."""
+    desc = pkv.make_desc("bf16", 1, 16, 4, 2, 64)
+    cache = PagedKVCache(desc, storage="q8")
+    for i in range(2):
+        cache.add_sequence(i, 40 + i)
+    batch = DecodeBatch(cache, [0, 1], max_blocks=4, scored=True)
+    q, k, v, out = (torch.zeros((1, 2, h, 64), device="cuda", dtype=torch.bfloat16) for h in (4, 2, 2, 4))
+    st = batch.plan()
+    before = cache.mgr.save()
+    with pytest.raises(ValueError, match="planned"):
+        batch.evict(10, 2)
+    with pytest.raises(ValueError, match="planned"):
+        batch.set_sequences([1, 0])
+    batch.set_sequences([0, 1])                         # no change
+    assert cache.mgr.save() == before
+    batch.upload(st)
+    batch.run_device(st, q, k, v, out, 0.1)
+    batch.set_sequences([1, 0])
+    batch.evict(10, 2)
+    assert [cache.mgr.block_table(i)[2] for i in (0, 1)] == [10, 10]
+    plain = DecodeBatch(cache, [0, 1], max_blocks=4)   # without scores its rows may be reordered at any time
+    plain.plan()
+    plain.set_sequences([1, 0])
+    assert pkv.pkv_get_device_status() == 0
