@@ -409,8 +409,8 @@ int pkv_upload_metadata(void* dst, const void* src_host, size_t bytes, void* str
  * pkv_q8_append writes powers of two: the least 2^e (e >= -15 for fp16 rows, -117 for bf16) that lets
  * the block's largest finite element in, |x| <= 448 * 2^e. The attention calls take any finite scale >= 0
  * (pkv_q8_prefill_attention with the limits given there).
- * Values within a factor 2^14 of the block's largest keep e4m3's relative precision (2^-4); smaller
- * ones lose bits, below 2^-10 * 2^e they round to zero. fp16 elements above 63,488 are held as 65,536; the
+ * Values within a factor 14,336 (just under 2^14) of the block's largest keep e4m3's relative precision (2^-4)
+ * unless 2^e is at its least; smaller ones lose bits, from 2^-10 * 2^e down they round to zero. fp16 elements above 63,488 are held as 65,536; the
  * attention calls return no fp16 output beyond 65,504 for it. bf16 elements above 3.35e38 are held as 2^128,
  * infinite.
  */

@@ -1,6 +1,7 @@
 """8-bit pools, summed weights and eviction without a GPU: sizes, refusals before any launch, the shortening
 of sequences in the block manager."""
 import ctypes
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -277,3 +278,20 @@ def test_an_eviction_workspace_is_not_written_when_it_is_allocated(monkeypatch):
     counted = pkv.alloc_q8_prefill_workspace(desc_of(), device="cpu")      # this one holds counters
     words = pkv.PKV_ARRIVAL_BYTES // 4
     assert not counted[:words].any() and torch.all(counted[words:] == 5.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_the_range_that_keeps_full_precision(dtype):
+    """Elements down to 1 / 14,336 of a block's largest are held within 2^-4 of themselves: the least scale S has
+    224 S < largest <= 448 S, and codes are normal from 2^-6 S on. A factor of 2^14 would be too much."""
+    rng = np.random.default_rng(0)
+    worst = {14336.0: 0.0, 2.0 ** 14: 0.0}
+    for amax in np.concatenate([[224.001, 225.0, 256.0, 300.0, 447.9, 448.0], rng.uniform(224.1, 448, 200)]) * 2.0 ** 3:
+        s = R.least_scale(amax, dtype)
+        assert 224 * s < amax <= 448 * s
+        for factor in worst:
+            x = amax / np.exp(rng.uniform(0, np.log(factor), 4000))
+            x = np.append(x, amax / factor)
+            worst[factor] = max(worst[factor], np.max(np.abs(R.VALUES[R.to_codes(x / s)] * s / x - 1)))
+    assert worst[14336.0] <= 2.0 ** -4 < worst[2.0 ** 14]
+    assert "factor 14,336" in (Path(__file__).resolve().parents[1] / "include" / "pkv.h").read_text()
