@@ -280,3 +280,14 @@ def test_evict_offsets_past_32_bits(q8):
             assert torch.equal(moved, r.gather(1, at[..., None].expand(-1, -1, d)))
         del pools, calls
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n", [100, 256, 257, 400])
+def test_evict_of_many_sequences(n):
+    """As many sequences as the move ranks by what they keep, and more; some equal, some empty."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 90, size=n)
+    keep = np.minimum(rng.integers(0, 70, size=n), rng.integers(0, 70, size=n))
+    case = evict_case("bf16", lens, keep, 1, 64, 1, seed=10, in_place="mixed", q8=True)
+    check_evict(case, 3, "bf16", same_scores=False)
+    assert pkv.pkv_get_device_status() == 0
