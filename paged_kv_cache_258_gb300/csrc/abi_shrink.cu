@@ -93,8 +93,6 @@ int validate16(const pkv_cache_desc* d) {
 // kMaxPartition blocks with no more than one CTA per SM: small calls, where latency counts (8 heads of
 // 4,000 tokens: partitions 9.4 us, runs 13.8; at 64 blocks a partition four such sequences take 17.5 us
 // against 14.7).
-constexpr int kMaxCluster = 8;
-
 static_assert(pkv::kMaxRuns * sizeof(unsigned int) == PKV_ARRIVAL_BYTES, "one counter a run");
 
 struct FragGeometry {
@@ -103,7 +101,7 @@ struct FragGeometry {
 
 FragGeometry geometry_of(long long pairs, int max_blocks, int sms, int per_sm, int max_runs) {
     FragGeometry geo;
-    const long long parts = pairs >= sms ? 1 : sms / pairs < kMaxCluster ? sms / pairs : kMaxCluster;
+    const long long parts = pairs >= sms ? 1 : sms / pairs < pkv::kMaxCluster ? sms / pairs : pkv::kMaxCluster;
     const int partition = (int)((max_blocks + parts - 1) / parts);
     if (pairs <= sms && partition <= pkv::kMaxPartition) {
         geo.partition = partition < pkv::kMinPartition ? pkv::kMinPartition : partition;

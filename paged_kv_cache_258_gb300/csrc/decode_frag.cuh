@@ -41,8 +41,9 @@
 //    NaN). q is brought to fp16 with a power of two of its own row, so bf16's range cannot overflow:
 //    a query element keeps at least 11 bits unless it is 2^-29 of its row's largest, where what is
 //    lost is below fp32's own rounding of the dot product.
-//  * Weights for the PV product are fp16 too (11 bits; over 16-bit pools they have the pool's type, times
-//    2^15 for fp16: its subnormals begin at 2^-14, and many small weights may make up a large sum):
+//  * Weights for the PV product are fp16 too (11 bits; over 16-bit pools they have the pool's type, because both
+//    operands of an instruction have one type and V's range is bf16's: 8 bits there, each weight off by at most 2^-8 of
+//    itself; fp16 ones times 2^15: its subnormals begin at 2^-14, and many small weights may make up a large sum):
 //    w_j = 2^(z_j + log2 S_V(b) + 15 - m'), m' the running maximum of z + log2 S_V. So the largest w is
 //    2^15 whatever the blocks' scales, and one keeps 11 bits down to 2^-29 of it (below 2^-40 it is 0:
 //    2^28 tokens of those make up 2^-12). The sum of weights runs in fp32 beside it with its own maximum m.
@@ -68,8 +69,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
 }
-
-constexpr int kMaxCluster = 8;  // the portable limit
 
 // What a pair costs a CTA beside its blocks, in blocks: 4.7 us (loads of the table, the query and the
 // first tiles, the warps' join, the output) against 0.19 us a block of codes. Without it a CTA whose run

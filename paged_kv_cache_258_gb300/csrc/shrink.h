@@ -29,6 +29,8 @@ constexpr int kMinPartition = 8;
 constexpr int kMaxRuns = 2048;
 // Runs of a prompt chunk's launch, whose workspace is sized without asking a device.
 constexpr int kChunkRuns = 640;
+// Most partitions of a context in a grid of partitions: they are one cluster, and 8 is the portable limit.
+constexpr int kMaxCluster = 8;
 // Most blocks of a partition in a grid of partitions (its logits stay in shared memory).
 constexpr int kMaxPartition = 32;
 
