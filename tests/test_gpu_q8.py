@@ -822,3 +822,27 @@ def test_a_nan_does_not_outlive_its_call():
     for o in (outs[0], outs[2]):
         assert torch.equal(o.view(torch.int16), first.view(torch.int16))
     assert not ws[:COUNTERS].view(torch.int32).any() and pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,max_blocks", [([301], 19), ([9000, 40, 2500], 700), ([700, 1300, 64, 2048] * 6, 128)])
+@pytest.mark.parametrize("d,G", [(64, 8), (128, 1), (256, 4)])
+def test_results_repeat_bit_for_bit(lens, max_blocks, d, G):
+    """Outputs and sums of decode and of chunks do not depend on the order in which CTAs end: repeated beside
+    another stream's work that takes SMs away at other times."""
+    n_kv = 4
+    desc, t, qf, kf, vf, tables, ln = q8_case("bf16", lens, G * n_kv, n_kv, d, seed=51, max_blocks=max_blocks)
+    counts = [min(c, 3) for c in lens]
+    q, _ = values(np.random.default_rng(51), (sum(counts), G * n_kv, d), "bf16")
+    other, busy = torch.cuda.Stream(), torch.randn((2048, 2048), device="cuda")
+    torch.cuda.synchronize()
+    want = None
+    for i in range(12):
+        if i:
+            with torch.cuda.stream(other):
+                for _ in range(i % 4 * 8):
+                    busy = busy @ busy * 1e-3
+        scores = torch.zeros((len(lens), n_kv, max_blocks * BLOCK), device="cuda")
+        got = [run_decode(desc, t, 0.02, scores), scores, torch.from_numpy(prefill(desc, t, q, ln, counts, 0.02, "bf16")[0])]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+    assert pkv.pkv_get_device_status() == 0
