@@ -58,13 +58,20 @@ cudaError_t launch_frag_multi(int dtype, int head_dim, int columns, const FragAr
                             : launch_frag_multi_bf16(head_dim, columns, a, tk, tv, stream);
 }
 
-cudaError_t launch_prefill_widened(int dtype, int head_dim, int group, const PrefillArgs& a, cudaStream_t stream) {
-    const long long rows = (long long)a.num_blocks * a.n_kv * kBlock;
-    CUtensorMap tk, tv;
-    cudaError_t err = kv_tensor_map(a.k_layer, rows, head_dim, dtype, PKV_BOX_PANEL, &tk);
-    if (err == cudaSuccess)  // (at head_dim 256 each CTA of a pair copies half of a V block's columns)
-        err = kv_tensor_map(a.v_layer, rows, head_dim, dtype, head_dim == 256 ? PKV_BOX_BLOCK_HALF : PKV_BOX_BLOCK, &tv);
-    if (err != cudaSuccess) return err;
+cudaError_t widened_maps(int dtype, int head_dim, const Q8WidenArgs& w, CUtensorMap* tk, CUtensorMap* tv) {
+    const long long rows = (long long)w.num_blocks * w.n_kv * kBlock;
+    CUtensorMap codes;  // (only asked for: the widening takes plain addresses)
+    cudaError_t err = kv_tensor_map(w.k_codes, rows, head_dim, kCodesE4M3, PKV_BOX_PANEL, &codes);
+    if (err == cudaSuccess) err = kv_tensor_map(w.v_codes, rows, head_dim, kCodesE4M3, PKV_BOX_PANEL, &codes);
+    if (err == cudaSuccess) err = kv_tensor_map(w.k_out, rows, head_dim, dtype, PKV_BOX_PANEL, tk);
+    // (at head_dim 256 each CTA of a pair copies half of a V block's columns)
+    return err != cudaSuccess ? err
+                              : kv_tensor_map(w.v_out, rows, head_dim, dtype,
+                                              head_dim == 256 ? PKV_BOX_BLOCK_HALF : PKV_BOX_BLOCK, tv);
+}
+
+cudaError_t launch_prefill_widened(int dtype, int head_dim, int group, const PrefillArgs& a, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, cudaStream_t stream) {
     return dtype == PKV_F16 ? launch_prefill_widened_f16(head_dim, group, a, tk, tv, stream)
                             : launch_prefill_widened_bf16(head_dim, group, a, tk, tv, stream);
 }
@@ -485,10 +492,12 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
     a.v_codes = v_layer;
     a.v_nan = w.v_nan;
     a.scale_log2 = scale * 1.4426950408889634f;
+    CUtensorMap tk, tv;
+    const cudaError_t err = pkv::widened_maps(d->dtype, d->head_dim, w, &tk, &tv);
+    if (err != cudaSuccess) return pkv::launch_status(err);
     if (pkv::launch_q8_widen(d->dtype, d->head_dim, w, st) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::count_launches(1);
-    const cudaError_t err = pkv::launch_prefill_widened(d->dtype, d->head_dim, group, a, st);
-    if (err != cudaSuccess) return pkv::launch_status(err);
+    if (pkv::launch_prefill_widened(d->dtype, d->head_dim, group, a, tk, tv, st) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::count_launches(1);
     return PKV_OK;
 }

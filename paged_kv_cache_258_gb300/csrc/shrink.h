@@ -155,8 +155,11 @@ cudaError_t launch_frag_multi(int dtype, int head_dim, int columns, const FragAr
 cudaError_t launch_scores(const ScoreArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_append(int dtype, int head_dim, const Q8AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_copy(const Q8CopyArgs& a, cudaStream_t stream);
-// Prefill attention over the layer that launch_q8_widen filled.
-cudaError_t launch_prefill_widened(int dtype, int head_dim, int group, const PrefillArgs& a, cudaStream_t stream);
+// Prefill attention over the layer that launch_q8_widen filled, and before either its tensor maps: they refuse
+// (cudaErrorInvalidDevicePointer) codes or a workspace that are not memory of the current device.
+cudaError_t widened_maps(int dtype, int head_dim, const Q8WidenArgs& w, CUtensorMap* tk, CUtensorMap* tv);
+cudaError_t launch_prefill_widened(int dtype, int head_dim, int group, const PrefillArgs& a, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_q8_widen(int dtype, int head_dim, const Q8WidenArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 

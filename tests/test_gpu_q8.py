@@ -846,3 +846,39 @@ def test_results_repeat_bit_for_bit(lens, max_blocks, d, G):
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
     assert pkv.pkv_get_device_status() == 0
+
+
+def test_codes_and_workspaces_on_the_host_are_refused_before_launch():
+    """Page-locked host memory in the place of codes (decode, short and long chunks) or of a long chunk's
+    workspace: PKV_ERR_INVALID_ARG, nothing launched. Through the C entry points; the binding takes no such tensor."""
+    import ctypes
+    desc, t, _, kf, vf, tables, lens = q8_case("f16", [600], 16, 2, 128, seed=37)
+    host = t["k"].view(torch.uint8).cpu().pin_memory()
+    q = torch.zeros((500, 16, 128), dtype=torch.float16, device="cuda")
+    out, ws = torch.full_like(q, 3.0), pkv.alloc_q8_prefill_workspace(desc)
+    host_ws = torch.zeros(ws.numel(), dtype=torch.float32).pin_memory()
+    dws = pkv.alloc_q8_workspace(desc, 1, tables.shape[1])
+    codes = [t["k"].data_ptr(), t["v"].data_ptr()]
+    scales = [t["ks"].data_ptr(), t["vs"].data_ptr()]
+    L, d = pkv.lib(), ctypes.byref(desc)
+    before = pkv.pkv_launch_count()
+
+    def chunk(n, codes, w):
+        starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        return L.pkv_q8_prefill_attention(d, 0, q.data_ptr(), *codes, *scales, t["tables"].data_ptr(), tables.shape[1],
+                                          t["lens"].data_ptr(), starts.data_ptr(), 1, n, n, 0.1, out.data_ptr(), w.data_ptr(),
+                                          ws.nbytes, None)
+    for i in range(2):
+        bad = list(codes)
+        bad[i] = host.data_ptr()
+        assert chunk(3, bad, ws) == chunk(500, bad, ws) == pkv.PKV_ERR_INVALID_ARG
+        assert L.pkv_q8_decode_attention(d, 0, q.data_ptr(), *bad, *scales, t["tables"].data_ptr(), tables.shape[1],
+                                         t["lens"].data_ptr(), 1, 0.1, out.data_ptr(), None, 0,
+                                         None if dws is None else dws.data_ptr(), 0 if dws is None else dws.nbytes,
+                                         None) == pkv.PKV_ERR_INVALID_ARG
+    assert chunk(500, codes, host_ws) == pkv.PKV_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert pkv.pkv_launch_count() == before and torch.all(out == 3.0)
+    assert chunk(500, codes, ws) == pkv.PKV_OK and pkv.pkv_launch_count() == before + 2
+    assert chunk(3, codes, ws) == pkv.PKV_OK and pkv.pkv_launch_count() == before + 3
+    assert pkv.pkv_get_device_status() == 0
