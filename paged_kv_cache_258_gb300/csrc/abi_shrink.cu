@@ -306,7 +306,8 @@ int pkv_q8_append(const pkv_cache_desc* d, int32_t layer, const void* k, const v
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||
         !aligned4(v_scales))
         return PKV_ERR_INVALID_ARG;
-    if ((long long)n_tokens * d->n_kv_heads >= (1LL << 33)) return PKV_ERR_UNSUPPORTED;  // a CTA per 16 tokens, head, K / V
+    // a CTA for every 16 tokens, head, K and V
+    if (((long long)n_tokens + 15) / 16 * 2 * d->n_kv_heads >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
     pkv::Q8AppendArgs a;
     a.k = k;
     a.v = v;
@@ -393,7 +394,7 @@ int pkv_q8_prefill_attention(const pkv_cache_desc* d, int32_t layer, const void*
         return PKV_ERR_INVALID_ARG;
     if (n_seqs == 0 || max_query_len == 0) return PKV_OK;
     if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24)) return PKV_ERR_INVALID_ARG;
-    if (n_seqs > 65535 || pool_rows(d) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    if (n_seqs > 65535 || d->n_kv_heads > 65535 || pool_rows(d) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
     if ((long long)max_blocks_per_seq * d->n_kv_heads >= (1LL << 33)) return PKV_ERR_UNSUPPORTED;  // one warp per block and head
     if (!q || !k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !context_lens || !query_start || !out)
         return PKV_ERR_INVALID_ARG;

@@ -295,3 +295,11 @@ def test_the_range_that_keeps_full_precision(dtype):
             worst[factor] = max(worst[factor], np.max(np.abs(R.VALUES[R.to_codes(x / s)] * s / x - 1)))
     assert worst[14336.0] <= 2.0 ** -4 < worst[2.0 ** 14]
     assert "factor 14,336" in (Path(__file__).resolve().parents[1] / "include" / "pkv.h").read_text()
+
+
+def test_more_heads_than_a_grid_holds_are_refused():
+    many = desc_of(nb=1, n_q=65536, n_kv=65536)
+    assert decode(many) == scored(many) == prefill(many) == pkv.PKV_ERR_UNSUPPORTED
+    # the append has a CTA for every 16 tokens, head, K and V: 2^31 - 1 at most
+    assert append(desc_of(nb=1, n_q=1 << 30, n_kv=1 << 30), n=1) == pkv.PKV_ERR_UNSUPPORTED
+    assert append(desc_of(nb=1, n_q=1 << 27, n_kv=1 << 27), n=8 * 16) == pkv.PKV_ERR_UNSUPPORTED
