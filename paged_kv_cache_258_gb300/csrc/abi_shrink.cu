@@ -268,8 +268,8 @@ int chunk_columns(const pkv_cache_desc* d, int n_seqs, int max_query, int max_bl
 // handed to the tensor-memory kernel of 16-bit pools. Nanoseconds, for contexts as long as the table is wide:
 //   passes  6.5 us (10.5 wide), the context once at 6.5 TB/s, and a pass's work on each token (measured: 3.8, 6.7
 //           and 8.5 TB/s of codes at head_dim 64, 128 and 256 in tiles of 8; 2.1 and 5.5 in passes of 32 and 16)
-//   widen   8 us, that kernel's waves of 128-key tiles (0.93 us, 1.28 at 256; one CTA of 128 rows an SM) and
-//           three bytes a code
+//   widen   8 us, that kernel's waves of 128-key tiles (0.93 us, 1.28 at 256; one CTA of 128 rows an SM, the two of
+//           a pair at 256 counted singly) and three bytes a code
 // 20,000 tokens, 8 heads x 4 x 128: chunks of 1, 8, 32 and 64 tokens take 19, 32, 76 and 136 us in passes, 168 us
 // the other way; 4 x 1,900 tokens, 8 heads x 4 x 64: 2, 16, 32 and 70 tokens 9.5, 22.5, 28.4, 45 against 23.
 bool by_passes(const pkv_cache_desc* d, int n_seqs, int n_tokens, int max_query, int max_blocks, int columns, int sms) {
