@@ -882,3 +882,45 @@ def test_codes_and_workspaces_on_the_host_are_refused_before_launch():
     assert chunk(500, codes, ws) == pkv.PKV_OK and pkv.pkv_launch_count() == before + 2
     assert chunk(3, codes, ws) == pkv.PKV_OK and pkv.pkv_launch_count() == before + 3
     assert pkv.pkv_get_device_status() == 0
+
+
+def test_calls_at_once_on_two_streams():
+    """Appends, decode with summed weights, short and long chunks of two caches on two streams, each with its own
+    workspaces, give what they give one after the other."""
+    dtype, d, G, n_kv = "bf16", 128, 8, 2
+    cases = []
+    for i, lens in enumerate(([4000, 600, 33], [900, 5200])):
+        desc, t, _, kf, vf, tables, ln = q8_case(dtype, lens, G * n_kv, n_kv, d, seed=60 + i, max_blocks=400)
+        n = len(lens)
+        long = min(lens[0], 500)
+        starts = [torch.tensor([0, m] + [m] * (n - 1), dtype=torch.int32, device="cuda") for m in (3, long)]
+        rows = torch.randn((4, n_kv, d), device="cuda").bfloat16()
+        slots = torch.tensor([int(tables[1, 0]) * 16 + j for j in range(4)], device="cuda")
+        qs = [torch.randn((m, G * n_kv, d), device="cuda").bfloat16() for m in (3, long)]
+        cases.append((desc, t, n, starts, rows, slots, qs, pkv.alloc_q8_workspace(desc, n, 400, scored=True),
+                      pkv.alloc_q8_prefill_workspace(desc)))
+    torch.cuda.synchronize()
+
+    def queue(case, times):
+        desc, t, n, starts, rows, slots, qs, ws, pws = case
+        out, scores = torch.empty_like(t["q"]), torch.zeros((n, n_kv, 6400), device="cuda")
+        outs = [torch.empty_like(x) for x in qs]
+        for _ in range(times):
+            pkv.pkv_q8_append(desc, 0, rows, rows, slots, t["k"], t["v"], t["ks"], t["vs"])
+            pkv.pkv_q8_decode_attention(desc, 0, t["q"], t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"], 0.02, out, ws,
+                                        scores=scores)
+            for x, o, s in zip(qs, outs, starts):
+                pkv.pkv_q8_prefill_attention(desc, 0, x, t["k"], t["v"], t["ks"], t["vs"], t["tables"], t["lens"], s,
+                                             x.shape[0], 0.02, o, pws)
+        return [out, scores, *outs]
+    want = [queue(c, 5) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            got.append(queue(c, 5))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    assert pkv.pkv_get_device_status() == 0
