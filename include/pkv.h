@@ -21,7 +21,8 @@
  * Two halves:
  *   - device calls (kv append, paged decode attention -- optionally with the step's append
  *     fused in --, chunked-prefill attention, block copy, the upload of a step's metadata; the
- *     same over 8-bit pools; decode that sums its attention weights, and eviction by them):
+ *     same over 8-bit pools; decode that sums its attention weights, and eviction by them; linear
+ *     attention over a pool of states; a step's tables and slots from request lengths):
  *     asynchronous on the caller's CUDA stream, no host synchronisation, no allocation; every
  *     device pointer is owned by the caller;
  *   - a host block manager (pure C, no CUDA): free list, block tables, reference counts,
@@ -81,7 +82,9 @@ enum {
     PKV_DEV_WAIT_TIMEOUT = 16u,   /* a bounded wait on an asynchronous copy gave up          */
     PKV_DEV_BAD_QUERY_RANGE = 32u,/* prefill: query_start / chunk length inconsistent         */
     PKV_DEV_BAD_KEEP = 64u,       /* eviction: kept length < 0 or > max_keep                 */
-    PKV_DEV_BAD_SCALE = 128u      /* 8-bit prefill: code * scale beyond the activations' type */
+    PKV_DEV_BAD_SCALE = 128u,     /* 8-bit prefill: code * scale beyond the activations' type */
+    PKV_DEV_BAD_STATE_SLOT = 256u,/* linear attention: state slot >= n_slots                  */
+    PKV_DEV_BAD_FREE_LIST = 512u  /* tables: free block outside [0, num_blocks), bad `used`   */
 };
 
 /*
@@ -551,6 +554,104 @@ int pkv_evict_tokens(const pkv_cache_desc* desc, void* k_pool, void* v_pool, flo
                      const int32_t* context_lens, const int32_t* keep_lens, int32_t n_seqs, int32_t recent,
                      const float* scores, float* new_scores, int64_t score_stride, int32_t* kept, int32_t max_keep,
                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- linear attention over a pool of states --------------------------------------------- */
+
+/*
+ * The other layers of a hybrid model: the pages put 16 attention layers beside 48 whose memory of a sequence has
+ * a fixed size ("PagedAttention e continuous batching", "01 - Conceito", paragraph 2). For head h of v, which reads
+ * head h / (n_v_heads / n_qk_heads) of q and k, and a log decay g:
+ *   S_t = exp(g_t) S_{t-1} + k_t^T v_t        (S: dim_k x dim_v, fp32)
+ *   out_t = scale * q_t S_t
+ *   q, k    [n_tokens][n_qk_heads][dim_k];  v, out  [n_tokens][n_v_heads][dim_v], of desc->dtype
+ *   state   float [n_layers][n_slots][n_v_heads][dim_k][dim_v]: a slot is one sequence's memory in every layer
+ * Supported: dtype in pkv_dtype; dim_k and dim_v in {64, 128}; n_v_heads a multiple of n_qk_heads, at most 65,535.
+ */
+typedef struct {
+    int32_t dtype;      /* pkv_dtype of q, k, v and out */
+    int32_t n_layers;
+    int32_t n_slots;    /* states in the pool (every layer) */
+    int32_t n_qk_heads;
+    int32_t n_v_heads;
+    int32_t dim_k;
+    int32_t dim_v;
+} pkv_linear_desc;
+
+/* PKV_OK if the descriptor is supported, else the error code the calls would return. */
+int pkv_linear_validate_desc(const pkv_linear_desc* desc);
+
+/* Bytes of the state pool over all layers; 0 if desc is invalid. */
+uint64_t pkv_linear_state_bytes(const pkv_linear_desc* desc);
+
+/*
+ * One token for each of n_seqs sequences, one layer; sequence s owns row s of q, k, v and out.
+ *   log_decay     NULL (no decay), or device float: g of token t and head h is log_decay[t * decay_stride + h];
+ *                 decay_stride 0 gives each head one decay, otherwise it is >= n_v_heads. g <= 0 decays; -infinity
+ *                 forgets; a positive g grows, as far as fp32 reaches
+ *   state         device, whole pool (all layers), 16-byte aligned
+ *   src_slots     device int32 [n_seqs]: the slot sequence s reads its state from; negative: it starts from zeros
+ *   dst_slots     device int32 [n_seqs]: the slot its state after the call goes to; negative: it is not kept. May
+ *                 be its src slot. No two sequences write one slot and none reads a slot that another one writes
+ *                 (else those states are unspecified); any number may read one slot, as forks of a prefix do
+ *   q, k, v, out  16-byte aligned
+ * A sequence with a slot >= n_slots is skipped whole, its row of out left unwritten, and sets
+ * PKV_DEV_BAD_STATE_SLOT. Sums and the state are fp32; out is rounded to desc->dtype. n_seqs at most 65,535.
+ */
+int pkv_linear_decode(const pkv_linear_desc* desc, int32_t layer, const void* q, const void* k, const void* v,
+                      const float* log_decay, int64_t decay_stride, float* state, const int32_t* src_slots,
+                      const int32_t* dst_slots, int32_t n_seqs, float scale, void* out, void* stream);
+
+/* Scratch bytes of pkv_linear_prefill for up to these counts on the current device; 0 when it needs none, and also
+ * for an unsupported descriptor, a bad count or no usable device. */
+size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* desc, int32_t n_seqs, int32_t n_tokens,
+                                          int32_t max_query_len);
+
+/*
+ * The same for a chunk of tokens of each sequence, packed as for pkv_paged_prefill_attention.
+ *   query_start   device int32 [n_seqs + 1]: sequence s owns rows query_start[s] .. query_start[s+1]-1; rows that
+ *                 no sequence owns are neither read for a result nor written
+ *   max_query_len host: the longest chunk, 0 <= max_query_len <= n_tokens
+ *   workspace     device, >= pkv_linear_prefill_workspace_bytes(...), 16-byte aligned, no initialisation; calls
+ *                 that overlap on the GPU must not share one
+ * Other arguments as pkv_linear_decode. An empty chunk leaves its sequence's state in dst_slots as it was. A
+ * sequence whose range is outside [0, n_tokens], negative or longer than max_query_len is skipped whole and sets
+ * PKV_DEV_BAD_QUERY_RANGE; one with a bad slot, PKV_DEV_BAD_STATE_SLOT.
+ */
+int pkv_linear_prefill(const pkv_linear_desc* desc, int32_t layer, const void* q, const void* k, const void* v,
+                       const float* log_decay, int64_t decay_stride, float* state, const int32_t* src_slots,
+                       const int32_t* dst_slots, const int32_t* query_start, int32_t n_seqs, int32_t n_tokens,
+                       int32_t max_query_len, float scale, void* out, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* ---- tables and slots from request lengths ---------------------------------------------- */
+
+/*
+ * What the block manager and an upload do for a step, on the device: extend every row's block table by its new
+ * tokens and work out their slots ("La idea de PagedAttention", steps 2 and 3), so that a captured graph of steps
+ * can be replayed without the host. Rows take free blocks in row order, each row all or nothing as pkv_mgr_extend
+ * does. Rows are served up to the first that does not fit (too few free blocks, more than max_blocks_per_seq
+ * entries, more than max_tokens tokens in all); that row and all behind it get no tokens in this call. With the
+ * manager's free list (pkv_mgr_free_list) as free_blocks, the same pkv_mgr_extend calls give the same tables.
+ *   free_blocks   device int32 [n_free]: ids in the order they are taken
+ *   used          device int32: how many of them are taken already
+ *   block_tables  device int32 [n_seqs][max_blocks_per_seq], extended in place; no other entries are written.
+ *                 A partly filled last block must be its row's own: copy-on-write stays the manager's
+ *   context_lens  device int32 [n_seqs]: tokens each row holds before the call
+ *   new_tokens    device int32 [n_seqs], or NULL: one for each row
+ *   slot_mapping  device int64 [max_tokens]: the new tokens' slots packed by rows, then -1, which pkv_kv_append
+ *                 skips; also -1 for a token whose block id is outside [0, num_blocks)
+ *   query_start   device int32 [n_seqs + 1]: as the prefill calls take it
+ *   new_lens      device int32 [n_seqs]: lengths after the call; may be context_lens itself
+ *   totals        device int32 [3]: free blocks taken in all, rows served, new tokens. Its first may be `used`
+ * A length outside [0, max_blocks_per_seq*16] sets PKV_DEV_BAD_CONTEXT_LEN, a negative count PKV_DEV_BAD_QUERY_RANGE:
+ * such a row gets no tokens and counts as served. `used` outside [0, n_free] counts as nothing left and sets
+ * PKV_DEV_BAD_FREE_LIST, as does a fresh id outside [0, num_blocks); an old one sets PKV_DEV_BAD_BLOCK_ID.
+ * One launch. n_seqs at most 65,535. Arrays other than those named do not overlap.
+ */
+int pkv_extend_tables(int32_t num_blocks, const int32_t* free_blocks, int32_t n_free, const int32_t* used,
+                      int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      const int32_t* new_tokens, int32_t n_seqs, int64_t* slot_mapping, int32_t max_tokens,
+                      int32_t* query_start, int32_t* new_lens, int32_t* totals, void* stream);
 
 /*
  * Synchronise `stream`, then read and clear this library's device status word on the

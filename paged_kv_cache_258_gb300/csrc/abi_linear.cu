@@ -1,0 +1,149 @@
+// abi_linear.cu -- the C ABI of linear attention and of tables built on the GPU: argument validation, dispatch.
+#include "linear.h"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t layer_floats(const pkv_linear_desc* d) {
+    return (size_t)d->n_slots * d->n_v_heads * d->dim_k * d->dim_v;
+}
+
+// What decode and prefill check alike; layer's arguments into a.
+int linear_args(const pkv_linear_desc* d, int32_t layer, const void* q, const void* k, const void* v,
+                const float* log_decay, int64_t decay_stride, float* state, const int32_t* src, const int32_t* dst,
+                int32_t n_seqs, float scale, void* out, pkv::LinearArgs* a) {
+    if (!q || !k || !v || !state || !src || !dst || !out) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state) || !aligned4(src) ||
+        !aligned4(dst))
+        return PKV_ERR_INVALID_ARG;
+    if (log_decay && (!aligned4(log_decay) || (decay_stride != 0 && decay_stride < d->n_v_heads)))
+        return PKV_ERR_INVALID_ARG;
+    // a CTA for every sequence, head and 32 columns
+    if (n_seqs > 65535 || (long long)n_seqs * d->n_v_heads * (d->dim_v / 32) >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->out = out;
+    a->log_decay = log_decay;
+    a->decay_stride = decay_stride;
+    a->state = state + layer_floats(d) * layer;
+    a->src = src;
+    a->dst = dst;
+    a->n_seqs = n_seqs;
+    a->n_qk = d->n_qk_heads;
+    a->n_v = d->n_v_heads;
+    a->n_slots = d->n_slots;
+    a->scale = scale;
+    return pkv::device_status_word(&a->status) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_linear_validate_desc(const pkv_linear_desc* d) {
+    if (!d || d->n_layers <= 0 || d->n_slots <= 0 || d->n_qk_heads <= 0 || d->n_v_heads <= 0 || d->dim_k <= 0 ||
+        d->dim_v <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (d->dtype != PKV_F32 && d->dtype != PKV_F16 && d->dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if ((d->dim_k != 64 && d->dim_k != 128) || (d->dim_v != 64 && d->dim_v != 128)) return PKV_ERR_UNSUPPORTED;
+    if (d->n_v_heads % d->n_qk_heads != 0 || d->n_v_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+uint64_t pkv_linear_state_bytes(const pkv_linear_desc* d) {
+    return pkv_linear_validate_desc(d) == PKV_OK ? (uint64_t)d->n_layers * layer_floats(d) * sizeof(float) : 0;
+}
+
+int pkv_linear_decode(const pkv_linear_desc* d, int32_t layer, const void* q, const void* k, const void* v,
+                      const float* log_decay, int64_t decay_stride, float* state, const int32_t* src_slots,
+                      const int32_t* dst_slots, int32_t n_seqs, float scale, void* out, void* stream) {
+    int rc = pkv_linear_validate_desc(d);
+    if (rc != PKV_OK) return rc;
+    if (layer < 0 || layer >= d->n_layers || n_seqs < 0) return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0) return PKV_OK;
+    pkv::LinearArgs a;
+    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, &a);
+    if (rc != PKV_OK) return rc;
+    a.q_start = nullptr;
+    a.n_tokens = n_seqs;
+    a.max_query = 1;
+    int sms = 0;
+    if (pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_linear_step(d->dtype, d->dim_k, d->dim_v, sms, a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* d, int32_t n_seqs, int32_t n_tokens,
+                                          int32_t max_query_len) {
+    if (pkv_linear_validate_desc(d) != PKV_OK || n_seqs <= 0 || n_tokens <= 0 || max_query_len <= 0) return 0;
+    return 0;
+}
+
+int pkv_linear_prefill(const pkv_linear_desc* d, int32_t layer, const void* q, const void* k, const void* v,
+                       const float* log_decay, int64_t decay_stride, float* state, const int32_t* src_slots,
+                       const int32_t* dst_slots, const int32_t* query_start, int32_t n_seqs, int32_t n_tokens,
+                       int32_t max_query_len, float scale, void* out, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+    int rc = pkv_linear_validate_desc(d);
+    if (rc != PKV_OK) return rc;
+    if (layer < 0 || layer >= d->n_layers || n_seqs < 0 || n_tokens < 0 || max_query_len < 0 || max_query_len > n_tokens)
+        return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0) return PKV_OK;
+    if (!query_start || !aligned4(query_start)) return PKV_ERR_INVALID_ARG;
+    pkv::LinearArgs a;
+    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, &a);
+    if (rc != PKV_OK) return rc;
+    a.q_start = query_start;
+    a.n_tokens = n_tokens;
+    a.max_query = max_query_len;
+    int sms = 0;
+    if (pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+    (void)workspace;
+    (void)workspace_bytes;
+    if (pkv::launch_linear_step(d->dtype, d->dim_k, d->dim_v, sms, a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+int pkv_extend_tables(int32_t num_blocks, const int32_t* free_blocks, int32_t n_free, const int32_t* used,
+                      int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      const int32_t* new_tokens, int32_t n_seqs, int64_t* slot_mapping, int32_t max_tokens,
+                      int32_t* query_start, int32_t* new_lens, int32_t* totals, void* stream) {
+    if (num_blocks <= 0 || n_free < 0 || n_seqs < 0 || max_tokens < 0) return PKV_ERR_INVALID_ARG;
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24)) return PKV_ERR_INVALID_ARG;
+    if (n_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if ((n_free > 0 && !free_blocks) || !used || !query_start || !totals || (max_tokens > 0 && !slot_mapping))
+        return PKV_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!block_tables || !context_lens || !new_lens)) return PKV_ERR_INVALID_ARG;
+    if (!aligned4(free_blocks) || !aligned4(used) || !aligned4(block_tables) || !aligned4(context_lens) ||
+        !aligned4(new_tokens) || !aligned4(query_start) || !aligned4(new_lens) || !aligned4(totals) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+        return PKV_ERR_INVALID_ARG;
+    pkv::ExtendArgs a;
+    a.free_blocks = free_blocks;
+    a.used = used;
+    a.tables = block_tables;
+    a.lens = context_lens;
+    a.new_tokens = new_tokens;
+    a.slots = slot_mapping;
+    a.query_start = query_start;
+    a.new_lens = new_lens;
+    a.totals = totals;
+    a.num_blocks = num_blocks;
+    a.n_free = n_free;
+    a.max_blocks = max_blocks_per_seq;
+    a.n_seqs = n_seqs;
+    a.max_tokens = max_tokens;
+    if (pkv::device_status_word(&a.status) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_extend_tables(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::count_launches(1);
+    return PKV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,44 @@
+// linear.h -- arguments and launchers of linear attention and of tables built on the GPU (not installed).
+#pragma once
+
+#include "internal.h"
+
+namespace pkv {
+
+struct ExtendArgs {
+    const int32_t* free_blocks;  // [n_free]
+    const int32_t* used;
+    int32_t* tables;             // [n_seqs][max_blocks]
+    const int32_t* lens;         // [n_seqs]
+    const int32_t* new_tokens;   // [n_seqs], or nullptr: one each
+    int64_t* slots;              // [max_tokens]
+    int32_t* query_start;        // [n_seqs + 1]
+    int32_t* new_lens;           // [n_seqs], lens itself or apart
+    int32_t* totals;             // [3], its first may be used
+    unsigned int* status;
+    int num_blocks, n_free, max_blocks, n_seqs, max_tokens;
+};
+
+// One layer of linear attention. Sequence s owns rows q_start[s] .. q_start[s+1]-1 of the packed tokens, or row s
+// where q_start is nullptr.
+struct LinearArgs {
+    const void* q;               // [n_tokens][n_qk][DK]
+    const void* k;
+    const void* v;               // [n_tokens][n_v][DV]
+    void* out;                   // [n_tokens][n_v][DV]
+    const float* log_decay;      // nullptr: none
+    long long decay_stride;      // floats from token to token, 0: one for each head
+    float* state;                // this layer: [n_slots][n_v][DK][DV]
+    const int32_t* src;          // [n_seqs], negative: zeros
+    const int32_t* dst;          // [n_seqs], negative: not kept
+    const int32_t* q_start;
+    unsigned int* status;
+    int n_seqs, n_qk, n_v, n_slots, n_tokens, max_query;
+    float scale;
+};
+
+cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream);
+// Token after token with the state in registers (linear_step.cu).
+cudaError_t launch_linear_step(int dtype, int dk, int dv, int sms, const LinearArgs& a, cudaStream_t stream);
+
+}  // namespace pkv

@@ -21,6 +21,8 @@ PKV_DEV_BAD_BLOCK_ID, PKV_DEV_BAD_CONTEXT_LEN, PKV_DEV_BAD_SLOT, PKV_DEV_BAD_PAI
 PKV_DEV_BAD_QUERY_RANGE = 32
 PKV_DEV_BAD_KEEP = 64
 PKV_DEV_BAD_SCALE = 128
+PKV_DEV_BAD_STATE_SLOT = 256
+PKV_DEV_BAD_FREE_LIST = 512
 PKV_ARRIVAL_BYTES = 8192
 PKV_DECODE_OVERLAP_PREVIOUS = 1
 PKV_PREFILL_OVERLAP_PREVIOUS = 1
@@ -38,6 +40,15 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("n_layers", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("block_size", ctypes.c_int32)]
+
+    @property
+    def dtype_name(self) -> str:
+        return {v: k for k, v in DTYPE_CODES.items()}[self.dtype]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "n_layers", "n_slots", "n_qk_heads", "n_v_heads", "dim_k",
+                                              "dim_v")]
 
     @property
     def dtype_name(self) -> str:
@@ -65,7 +76,7 @@ def lib():
     L = ctypes.CDLL(str(LIB_PATH))
     c_i32, c_i64, c_u32, c_u64, c_sz, vp = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64,
                                             ctypes.c_size_t, ctypes.c_void_p)
-    dp = ctypes.POINTER(CacheDesc)
+    dp, lp = ctypes.POINTER(CacheDesc), ctypes.POINTER(LinearDesc)
     sigs = {
         "pkv_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "pkv_validate_desc": (ctypes.c_int, [dp]),
@@ -113,6 +124,15 @@ def lib():
         "pkv_evict_workspace_bytes": (c_sz, [dp, c_i32, c_i32, c_i32]),
         "pkv_evict_tokens": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, c_i32, vp, vp, c_i32, c_i32, vp, vp, c_i64,
                                             vp, c_i32, vp, c_sz, vp]),
+        "pkv_linear_validate_desc": (ctypes.c_int, [lp]),
+        "pkv_linear_state_bytes": (c_u64, [lp]),
+        "pkv_linear_decode": (ctypes.c_int, [lp, c_i32, vp, vp, vp, vp, c_i64, vp, vp, vp, c_i32, ctypes.c_float, vp,
+                                             vp]),
+        "pkv_linear_prefill_workspace_bytes": (c_sz, [lp, c_i32, c_i32, c_i32]),
+        "pkv_linear_prefill": (ctypes.c_int, [lp, c_i32, vp, vp, vp, vp, c_i64, vp, vp, vp, vp, c_i32, c_i32, c_i32,
+                                              ctypes.c_float, vp, vp, c_sz, vp]),
+        "pkv_extend_tables": (ctypes.c_int, [c_i32, vp, c_i32, vp, vp, c_i32, vp, vp, c_i32, vp, c_i32, vp, vp, vp,
+                                             vp]),
         "pkv_mgr_compact": (ctypes.c_int, [vp, vp, c_i32, vp]),
         "pkv_mgr_create": (vp, [c_i32, c_i32, vp]),
         "pkv_mgr_clone": (vp, [vp]),
@@ -573,23 +593,28 @@ _facts_by_value: dict = {}
 _t = None  # torch, once a call has needed it
 
 
-def _call(desc):
-    """(torch, facts of the descriptor, index of the current device) for a call's checks. Without a CUDA
-    device the index is -2, which no tensor's device equals."""
+def _torch_and_device():
+    """(torch, index of the current device); -2, which no tensor's device equals, without a CUDA device."""
     global _t
     if _t is None:
         _t = _torch()
     try:
-        cur = _t.cuda.current_device()
+        return _t, _t.cuda.current_device()
     except (RuntimeError, AssertionError):
-        cur = -2
-    key = bytes(desc)
+        return _t, -2
+
+
+def _call(desc):
+    """(torch, facts of the descriptor, index of the current device) for a call's checks. Without a CUDA
+    device the index is -2, which no tensor's device equals."""
+    t, cur = _torch_and_device()
+    key = bytes(desc) if type(desc) is CacheDesc else (type(desc), bytes(desc))
     f = _facts_by_value.get(key)
     if f is None:
         if len(_facts_by_value) >= 256:
             _facts_by_value.clear()
-        f = _facts_by_value[key] = _Facts(desc)
-    return _t, f, cur
+        f = _facts_by_value[key] = (_LinearFacts if isinstance(desc, LinearDesc) else _Facts)(desc)
+    return t, f, cur
 
 
 def _ptr(x, name, dtype, shape, cur) -> int:
@@ -911,6 +936,188 @@ def pkv_evict_tokens(desc: CacheDesc, k_pool, v_pool, src_tables, dst_tables, co
     """
     evict_launcher(desc, k_pool, v_pool, src_tables, dst_tables, context_lens, keep_lens, recent, scores, new_scores, kept,
                    stream, k_scales, v_scales, workspace)()
+
+
+# ---- linear attention over a pool of states -----------------------------------------------------
+
+class _LinearFacts:
+    """What the checks of a call need of a linear descriptor, as _Facts."""
+    __slots__ = ("dtype", "state", "n_layers", "n_qk", "n_v", "dk", "dv")
+
+    def __init__(self, desc: LinearDesc):
+        self.dtype = torch_dtype(desc.dtype_name) if desc.dtype in DTYPE_CODES.values() else None
+        self.state = linear_state_shape(desc)
+        self.n_layers, self.n_qk, self.n_v, self.dk, self.dv = (desc.n_layers, desc.n_qk_heads, desc.n_v_heads, desc.dim_k,
+                                                                desc.dim_v)
+
+
+def make_linear_desc(dtype: str, n_layers: int, n_slots: int, n_qk_heads: int, n_v_heads: int, dim_k: int,
+                     dim_v: int) -> LinearDesc:
+    return LinearDesc(DTYPE_CODES[dtype], n_layers, n_slots, n_qk_heads, n_v_heads, dim_k, dim_v)
+
+
+def linear_state_shape(desc: LinearDesc):
+    """[n_layers, n_slots, n_v, dim_k, dim_v]: float32, a slot is one sequence's memory in every layer."""
+    return (desc.n_layers, desc.n_slots, desc.n_v_heads, desc.dim_k, desc.dim_v)
+
+
+def pkv_linear_validate_desc(desc: LinearDesc) -> int:
+    return int(lib().pkv_linear_validate_desc(ctypes.byref(desc)))
+
+
+def pkv_linear_state_bytes(desc: LinearDesc) -> int:
+    return int(lib().pkv_linear_state_bytes(ctypes.byref(desc)))
+
+
+def pkv_linear_prefill_workspace_bytes(desc: LinearDesc, n_seqs: int, n_tokens: int, max_query_len: int) -> int:
+    return int(lib().pkv_linear_prefill_workspace_bytes(ctypes.byref(desc), int(n_seqs), int(n_tokens),
+                                                        int(max_query_len)))
+
+
+def alloc_linear_prefill_workspace(desc: LinearDesc, n_seqs: int, n_tokens: int, max_query_len: int, device="cuda"):
+    """A device buffer for pkv_linear_prefill calls of up to these counts (None where they need none)."""
+    return _bytes_tensor(pkv_linear_prefill_workspace_bytes(desc, n_seqs, n_tokens, max_query_len), device, counters=False)
+
+
+def _linear_rows(t, f, q, k, v, out, cur):
+    """Addresses of one layer's q, k, v, out."""
+    n = q.shape[0]
+    return (_ptr(q, "q", f.dtype, (n, f.n_qk, f.dk), cur), _ptr(k, "k", f.dtype, (n, f.n_qk, f.dk), cur),
+            _ptr(v, "v", f.dtype, (n, f.n_v, f.dv), cur), _ptr(out, "out", f.dtype, (n, f.n_v, f.dv), cur))
+
+
+def _log_decay(t, f, log_decay, n: int, cur):
+    """(address, floats between tokens) of log decays [n, n_v], [n_v] or None."""
+    if log_decay is None:
+        return None, 0
+    if log_decay.dim() == 1:
+        return _ptr(log_decay, "log_decay", t.float32, (f.n_v,), cur), 0
+    return _ptr(log_decay, "log_decay", t.float32, (n, f.n_v), cur), f.n_v
+
+
+def pkv_linear_decode(desc: LinearDesc, layer: int, q, k, v, log_decay, state, src_slots, dst_slots, scale: float, out,
+                      stream=None) -> None:
+    """Linear attention of one token a sequence (one layer): q, k [n, n_qk, dim_k]; v, out [n, n_v, dim_v];
+    log_decay float32 [n, n_v], [n_v] (the same for every token) or None; state float32 linear_state_shape(desc),
+    read at src_slots (negative: zeros) and written at dst_slots (negative: not kept), both int32 [n]."""
+    t, f, cur = _call(desc)
+    n = q.shape[0]
+    rows = _linear_rows(t, f, q, k, v, out, cur)
+    g, stride = _log_decay(t, f, log_decay, n, cur)
+    rc = lib().pkv_linear_decode(
+        ctypes.byref(desc), int(layer), rows[0], rows[1], rows[2], g, stride, _ptr(state, "state", t.float32, f.state, cur),
+        _ptr(src_slots, "src_slots", t.int32, (n,), cur), _ptr(dst_slots, "dst_slots", t.int32, (n,), cur), n, scale,
+        rows[3], _raw(stream, cur))
+    _check(rc, "pkv_linear_decode")
+
+
+def pkv_linear_prefill(desc: LinearDesc, layer: int, q, k, v, log_decay, state, src_slots, dst_slots, query_start,
+                       max_query_len: int, scale: float, out, workspace=None, stream=None) -> None:
+    """pkv_linear_decode for a chunk of tokens of each sequence, packed: query_start int32 [n_seqs + 1] (device),
+    max_query_len the longest chunk; workspace from alloc_linear_prefill_workspace."""
+    t, f, cur = _call(desc)
+    n_tokens, n_seqs = q.shape[0], src_slots.shape[0]
+    rows = _linear_rows(t, f, q, k, v, out, cur)
+    g, stride = _log_decay(t, f, log_decay, n_tokens, cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    rc = lib().pkv_linear_prefill(
+        ctypes.byref(desc), int(layer), rows[0], rows[1], rows[2], g, stride, _ptr(state, "state", t.float32, f.state, cur),
+        _ptr(src_slots, "src_slots", t.int32, (n_seqs,), cur), _ptr(dst_slots, "dst_slots", t.int32, (n_seqs,), cur),
+        _ptr(query_start, "query_start", t.int32, (n_seqs + 1,), cur), n_seqs, n_tokens, int(max_query_len), scale, rows[3],
+        ws, ws_bytes, _raw(stream, cur))
+    _check(rc, "pkv_linear_prefill")
+
+
+def _linear_layers(t, f, q, k, v, log_decay, out, cur):
+    """([address of layer 0, bytes between layers] of q, k, v, decay and out, floats between tokens) of a step's
+    [L, n, ...] tensors."""
+    L, n = f.n_layers, int(q.shape[1])
+    at = [_layered(q, "q", f.dtype, L, (n, f.n_qk, f.dk), cur=cur), _layered(k, "k", f.dtype, L, (n, f.n_qk, f.dk), cur=cur),
+          _layered(v, "v", f.dtype, L, (n, f.n_v, f.dv), cur=cur), (0, 0),
+          _layered(out, "out", f.dtype, L, (n, f.n_v, f.dv), cur=cur)]
+    stride = 0
+    if log_decay is not None:
+        per_token = log_decay.dim() == 3
+        at[3] = _layered(log_decay, "log_decay", t.float32, L, (n, f.n_v) if per_token else (f.n_v,), cur=cur)
+        stride = f.n_v if per_token else 0
+    return at, stride
+
+
+def linear_decode_launcher(desc: LinearDesc, q, k, v, log_decay, state, src_slots, dst_slots, scale: float, out,
+                           stream=None):
+    """launch(layer): pkv_linear_decode of one layer, with q, k, v, out [L, n, ...] and log_decay [L, n, n_v],
+    [L, n_v] or None checked here once."""
+    t, f, cur = _call(desc)
+    n = int(q.shape[1])
+    ((q0, qs), (k0, ks), (v0, vs), (g0, gs), (o0, os_)), stride = _linear_layers(t, f, q, k, v, log_decay, out, cur)
+    st = _ptr(state, "state", t.float32, f.state, cur)
+    src, dst = (_ptr(x, name, t.int32, (n,), cur) for x, name in ((src_slots, "src_slots"), (dst_slots, "dst_slots")))
+    fn, dref, scale, sh = lib().pkv_linear_decode, ctypes.byref(desc), float(scale), _raw(stream, cur)
+
+    def launch(layer: int) -> None:
+        rc = fn(dref, layer, q0 + layer * qs, k0 + layer * ks, v0 + layer * vs, g0 + layer * gs, stride, st, src, dst, n,
+                scale, o0 + layer * os_, sh)  # (no decay: 0, a null pointer)
+        if rc:
+            raise PkvError(rc, "pkv_linear_decode")
+    return launch
+
+
+def linear_prefill_launcher(desc: LinearDesc, q, k, v, log_decay, state, src_slots, dst_slots, query_start,
+                            max_query_len: int, scale: float, out, workspace=None, stream=None):
+    """launch(layer): pkv_linear_prefill of one layer, as linear_decode_launcher."""
+    t, f, cur = _call(desc)
+    n_tok, n_seqs, mq = int(q.shape[1]), int(src_slots.shape[0]), int(max_query_len)
+    ((q0, qs), (k0, ks), (v0, vs), (g0, gs), (o0, os_)), stride = _linear_layers(t, f, q, k, v, log_decay, out, cur)
+    st = _ptr(state, "state", t.float32, f.state, cur)
+    src, dst = (_ptr(x, name, t.int32, (n_seqs,), cur) for x, name in ((src_slots, "src_slots"), (dst_slots, "dst_slots")))
+    start = _ptr(query_start, "query_start", t.int32, (n_seqs + 1,), cur)
+    ws, ws_bytes = _workspace(workspace, cur)
+    fn, dref, scale, sh = lib().pkv_linear_prefill, ctypes.byref(desc), float(scale), _raw(stream, cur)
+
+    def launch(layer: int) -> None:
+        rc = fn(dref, layer, q0 + layer * qs, k0 + layer * ks, v0 + layer * vs, g0 + layer * gs, stride, st, src, dst, start,
+                n_seqs, n_tok, mq, scale, o0 + layer * os_, ws, ws_bytes, sh)
+        if rc:
+            raise PkvError(rc, "pkv_linear_prefill")
+    return launch
+
+
+# ---- tables and slots from request lengths ------------------------------------------------------
+
+def extend_tables_launcher(num_blocks: int, free_blocks, used, block_tables, context_lens, new_tokens, slot_mapping,
+                           query_start, new_lens, totals, stream=None):
+    """launch(): pkv_extend_tables with its arguments checked here once.
+
+    free_blocks int32 [n_free], used int32 [1], block_tables int32 [n, max_blocks], context_lens int32 [n], new_tokens
+    int32 [n] or None (one each), slot_mapping int64 [max_tokens], query_start int32 [n + 1], new_lens int32 [n]
+    (context_lens itself, or apart), totals int32 [3] (used may be totals[:1])."""
+    t, cur = _torch_and_device()
+    n, mb = int(block_tables.shape[0]), _table_width(block_tables)
+    if context_lens.data_ptr() != new_lens.data_ptr() and n and abs(context_lens.data_ptr() - new_lens.data_ptr()) < 4 * n:
+        raise ValueError("new_lens must be context_lens itself or not overlap it")
+    if free_blocks.dim() != 1 or slot_mapping.dim() != 1:
+        raise ValueError("free_blocks and slot_mapping must have one dimension")
+    args = (int(num_blocks), _ptr(free_blocks, "free_blocks", t.int32, free_blocks.shape, cur), free_blocks.shape[0],
+            _ptr(used, "used", t.int32, (1,), cur), _ptr(block_tables, "block_tables", t.int32, (n, mb), cur), mb,
+            _ptr(context_lens, "context_lens", t.int32, (n,), cur),
+            None if new_tokens is None else _ptr(new_tokens, "new_tokens", t.int32, (n,), cur), n,
+            _ptr(slot_mapping, "slot_mapping", t.int64, slot_mapping.shape, cur), slot_mapping.shape[0],
+            _ptr(query_start, "query_start", t.int32, (n + 1,), cur), _ptr(new_lens, "new_lens", t.int32, (n,), cur),
+            _ptr(totals, "totals", t.int32, (3,), cur), _raw(stream, cur))
+    fn = lib().pkv_extend_tables
+
+    def launch() -> None:
+        rc = fn(*args)
+        if rc:
+            raise PkvError(rc, "pkv_extend_tables")
+    return launch
+
+
+def pkv_extend_tables(num_blocks: int, free_blocks, used, block_tables, context_lens, new_tokens, slot_mapping,
+                      query_start, new_lens, totals, stream=None) -> None:
+    """Extend every row's block table by its new tokens, on the device (arguments as extend_tables_launcher)."""
+    extend_tables_launcher(num_blocks, free_blocks, used, block_tables, context_lens, new_tokens, slot_mapping, query_start,
+                           new_lens, totals, stream)()
 
 
 def pkv_get_device_status(stream=None) -> int:
