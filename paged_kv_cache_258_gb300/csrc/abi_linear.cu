@@ -39,6 +39,37 @@ int linear_args(const pkv_linear_desc* d, int32_t layer, const void* q, const vo
     return pkv::device_status_word(&a->status) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+constexpr int kPiece = 128;          // tokens the tensor-core kernel takes at once
+constexpr int kMinChunk = 33;        // longest chunk from which it is used
+constexpr int kMinSegment = 4 * kPiece;
+
+bool by_pieces(const pkv_linear_desc* d, int max_query) { return d->dtype != PKV_F32 && max_query >= kMinChunk; }
+
+// How a call's sequences are shared out along their length: while the (sequence, head, 64 columns) units fill less
+// than half the GPU, in as many segments as it holds CTAs.
+struct Segments {
+    int n, tokens;
+};
+Segments segments_of(const pkv_linear_desc* d, int n_seqs, int max_query, int sms) {
+    const long long units = (long long)n_seqs * d->n_v_heads * (d->dim_v / 64);
+    long long n = units * 2 <= sms ? sms / units : 1;
+    if (n > max_query / kMinSegment) n = max_query / kMinSegment;
+    if (n < 2) return {1, (max_query + kPiece - 1) / kPiece * kPiece};
+    const int pieces = (max_query + kPiece - 1) / kPiece;
+    const int tokens = (int)((pieces + n - 1) / n) * kPiece;
+    return {(max_query + tokens - 1) / tokens, tokens};
+}
+
+// Workspace of a shared-out call, in floats: units of 64 columns are at most sms / segments, so sms of them hold all
+// that the segments leave, and as many the starts.
+struct PrefillLayout {
+    size_t start, added, sums, bytes;
+};
+PrefillLayout prefill_layout(const pkv_linear_desc* d, int sms) {
+    const size_t unit = (size_t)d->dim_k * 64, all = unit * (size_t)sms;
+    return {0, all, 2 * all, (2 * all + (size_t)sms) * sizeof(float)};
+}
+
 }  // namespace
 
 extern "C" {
@@ -81,7 +112,13 @@ int pkv_linear_decode(const pkv_linear_desc* d, int32_t layer, const void* q, co
 size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* d, int32_t n_seqs, int32_t n_tokens,
                                           int32_t max_query_len) {
     if (pkv_linear_validate_desc(d) != PKV_OK || n_seqs <= 0 || n_tokens <= 0 || max_query_len <= 0) return 0;
-    return 0;
+    if (!by_pieces(d, max_query_len) || max_query_len < 2 * kMinSegment) return 0;
+    int sms = 0;
+    if (pkv::current_sm_count(&sms) != cudaSuccess) {
+        cudaGetLastError();  // no usable device: report nothing rather than a guess
+        return 0;
+    }
+    return prefill_layout(d, sms).bytes;
 }
 
 int pkv_linear_prefill(const pkv_linear_desc* d, int32_t layer, const void* q, const void* k, const void* v,
@@ -103,8 +140,33 @@ int pkv_linear_prefill(const pkv_linear_desc* d, int32_t layer, const void* q, c
     a.max_query = max_query_len;
     int sms = 0;
     if (pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
-    (void)workspace;
-    (void)workspace_bytes;
+    if (by_pieces(d, max_query_len)) {
+        pkv::ChunkArgs c;
+        c.l = a;
+        c.dv = d->dim_v;
+        c.slices = d->dim_v / 64;
+        const Segments seg = segments_of(d, n_seqs, max_query_len, sms);
+        c.n_segs = seg.n;
+        c.seg_tokens = seg.tokens;
+        if (seg.n > 1) {
+            const PrefillLayout lay = prefill_layout(d, sms);
+            if (!workspace || !aligned16(workspace) || workspace_bytes < lay.bytes) return PKV_ERR_INVALID_ARG;
+            float* ws = static_cast<float*>(workspace);
+            c.start = ws + lay.start;
+            c.added = ws + lay.added;
+            c.sums = ws + lay.sums;
+        }
+        CUtensorMap tq, tk, tv;
+        cudaError_t err = pkv::rows_tensor_map(q, n_tokens, d->n_qk_heads * d->dim_k, d->dtype, kPiece, &tq);
+        if (err == cudaSuccess) err = pkv::rows_tensor_map(k, n_tokens, d->n_qk_heads * d->dim_k, d->dtype, kPiece, &tk);
+        if (err == cudaSuccess) err = pkv::rows_tensor_map(v, n_tokens, d->n_v_heads * d->dim_v, d->dtype, kPiece, &tv);
+        if (err != cudaSuccess) return pkv::launch_status(err);
+        const auto launch = d->dtype == PKV_F16 ? pkv::launch_linear_chunk_f16 : pkv::launch_linear_chunk_bf16;
+        err = launch(d->dim_k, c, tq, tk, tv, static_cast<cudaStream_t>(stream));
+        if (err != cudaSuccess) return PKV_ERR_CUDA;
+        pkv::count_launches(seg.n > 1 ? 2 : 1);
+        return PKV_OK;
+    }
     if (pkv::launch_linear_step(d->dtype, d->dim_k, d->dim_v, sms, a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PKV_ERR_CUDA;
     pkv::count_launches(1);

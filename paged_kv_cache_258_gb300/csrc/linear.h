@@ -41,4 +41,23 @@ cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream);
 // Token after token with the state in registers (linear_step.cu).
 cudaError_t launch_linear_step(int dtype, int dk, int dv, int sms, const LinearArgs& a, cudaStream_t stream);
 
+// Long chunks of 16-bit types on the tensor cores (linear_chunk.cuh). A sequence may be shared out in segments along
+// its length: a first launch leaves what each segment but the last adds to the state, the second starts each from
+// the sum of those before.
+struct ChunkArgs {
+    LinearArgs l;
+    int dv, slices;         // dim_v, and its slices of 64
+    int n_segs, seg_tokens; // segments of a sequence (1: whole), tokens of each: a multiple of 128
+    float* start = nullptr; // [n_seqs][n_v][DK][DV]: the states the sequences start from
+    float* added = nullptr; // [n_seqs][n_segs - 1][n_v][DK][DV]: what a segment leaves (the first: with the start)
+    float* sums = nullptr;  // [n_seqs][n_segs - 1][n_v]: log2 of the decay over a segment
+};
+cudaError_t launch_linear_chunk_f16(int dk, const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                                    const CUtensorMap& v, cudaStream_t stream);
+cudaError_t launch_linear_chunk_bf16(int dk, const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                                     const CUtensorMap& v, cudaStream_t stream);
+
+// Tensor map of packed rows of `width` 16-bit elements, in boxes of 64 columns x box_rows rows (tmap.cu).
+cudaError_t rows_tensor_map(const void* base, long long rows, int width, int dtype, int box_rows, CUtensorMap* out);
+
 }  // namespace pkv

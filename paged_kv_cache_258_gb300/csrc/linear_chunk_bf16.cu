@@ -1,0 +1,9 @@
+// linear_chunk_bf16.cu -- the tensor-core kernel of linear attention for bf16.
+#include "linear_chunk.cuh"
+
+namespace pkv {
+cudaError_t launch_linear_chunk_bf16(int dk, const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                                     const CUtensorMap& v, cudaStream_t stream) {
+    return launch_linear_chunk_dtype<__nv_bfloat16>(dk, a, q, k, v, stream);
+}
+}  // namespace pkv

@@ -19,6 +19,8 @@
 // so an entry stays valid even if its pool is freed and another one reuses the address. A new
 // address is accepted only if it is device memory of the current device
 // (cudaErrorInvalidDevicePointer otherwise, which the C ABI reports as PKV_ERR_INVALID_ARG).
+// A call's own packed rows (rows_tensor_map: 64 columns x box_rows) have another address every time; their maps
+// are encoded for each call.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -133,6 +135,35 @@ cudaError_t kv_tensor_map(const void* layer_base, long long rows, int head_dim, 
     g_maps->emplace(key, map);
     *out = map;
     return cudaSuccess;
+}
+
+cudaError_t rows_tensor_map(const void* base, long long rows, int width, int dtype, int box_rows, CUtensorMap* out) {
+    if ((dtype != PKV_F16 && dtype != PKV_BF16) || rows <= 0 || rows >= (1LL << 31) || width <= 0 || width % 64 != 0)
+        return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    cudaPointerAttributes pa{};
+    if (cudaPointerGetAttributes(&pa, base) != cudaSuccess) {
+        cudaGetLastError();
+        return cudaErrorInvalidDevicePointer;
+    }
+    if (pa.type != cudaMemoryTypeDevice || pa.device != dev) return cudaErrorInvalidDevicePointer;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_map_mu);
+        err = encoder(&encode);
+    }
+    if (err != cudaSuccess) return err;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)width * 2};
+    const cuuint32_t boxdim[2] = {64u, (cuuint32_t)box_rows};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    const CUresult r = encode(out, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                              const_cast<void*>(base), dims, strides, boxdim, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace pkv
