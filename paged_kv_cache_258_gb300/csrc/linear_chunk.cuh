@@ -9,19 +9,19 @@
 // A CTA takes one sequence, one head and 64 columns of v (the columns of S do not depend on one another; a head of
 // 128 has two CTAs, which both compute P), and walks its pieces with the roles below working on different
 // ones: the state is the only thing that passes from piece to piece.
-//   warps 0-3    P: tensor memory -> weights -> P' (16 bits, the A operand of OA, in tensor memory). Row i against 32
+//   warps 0-7    P: tensor memory -> weights -> P' (16 bits, the A operand of OA, in tensor memory). Row i against
 //                columns of an earlier block of 32: exp(G_i - R) times exp(R - G_j), R the sum up to the block's end:
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
-//                one for each pair
-//   warps 4-7    V~, in quarters of 32 rows through a ring: split into numbers of the type that add up to it (two of
-//                fp16, three of bf16: 2^-22 is left), beside one another along N, so that one product of N = 128 or 192
-//                gives their sums and the state keeps fp32's precision
-//   warps 8-11   the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
+//                one for each pair. A thread takes a row's even or odd halves of 32 columns
+//   warps 8-11   V~, in quarters of 32 rows through a ring: split into numbers of the type that add up to it (two of
+//                fp16: 2^-22 is left; three of bf16: exact), beside one another along N, so that one product of N = 128
+//                or 192 gives their sums and the state keeps fp32's precision
+//   warps 12-15  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
-//   warps 12-15  results: exp(G_i) OI + OA, through shared memory to whole rows
-//   warp 16      tensor copies of Q, K and V, two pieces ahead
-//   warp 17      issues the products
-//   warp 18      sums of decays (in 64 bits: differences of far sums; held as two fp32 where pairs need them)
+//   warps 16-19  results: exp(G_i) OI + OA, through shared memory to whole rows
+//   warp 20      tensor copies of Q, K and V, two pieces ahead
+//   warp 21      issues the products
+//   warp 22      sums of decays (in 64 bits: differences of far sums; held as two fp32 where pairs need them)
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
 // fp16 cannot hold their range: rows of P', the copy of S and V~ are then brought to 2^14 by a power of two each, which
@@ -35,7 +35,6 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "decode_mma.cuh"
 #include "linear.h"
 #include "umma.cuh"
 
@@ -43,18 +42,48 @@ namespace pkv {
 
 constexpr int kPiece = 128;   // tokens of a piece: the M of a product
 constexpr int kSlice = 64;    // columns of v of a CTA
-constexpr int kChunkThreads = 19 * 32;
+constexpr int kChunkThreads = 6 * 128;
+
+// Pairs of 16-bit numbers in a word.
+template <typename T>
+struct Pair16;
+template <>
+struct Pair16<__half> {
+    __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+    __device__ __forceinline__ static uint32_t zero_times(uint32_t w, uint32_t sum) {
+        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(0.f), *reinterpret_cast<const __half2*>(&sum));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
+struct Pair16<__nv_bfloat16> {
+    __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ static uint32_t zero_times(uint32_t w, uint32_t sum) {
+        const __nv_bfloat162 h = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.f),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&sum));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
 
 // Pieces of a piece's 128 gates, as the roles need them.
 struct __align__(16) PieceGates {
-    float hi[kPiece], lo[kPiece];  // sum of the log decays from the start of token's block of 32 to it, base 2
+    float hi[kPiece], lo[kPiece];  // minus the sum of the log decays from the start of token's block of 32 to it, base 2
     float col[kPiece];             // 2^(sum to the block's end - sum to the token)
     float block[4];                // sum over each block
     float after[4];                // 2^(sum over the blocks behind it)
-    float keep;                    // 2^(sum over all)
-    float keep_less1;              // that - 1, exact where the sum is small
-    int small;                     // whether it is
-    float grow;                    // sum of the positive ones
+    float keep, once;              // S' = S + (U + S * keep) with 2^(sum over all) - 1 where that is small, once = 1,
+    float grow;                    // else S * keep + U, once = 0; sum of the positive ones
+    int pad;
 };
 
 template <typename T, int DK>
@@ -103,10 +132,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Every thread of the four warps: registers a thread from here on. The kernel's 80 a thread are shared out anew:
+// 72 + 72 + 72 + 136 + 72 + 56 = 6 * 80.
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+
+__device__ __forceinline__ float2 f2_get(uint64_t v) {
+    float2 r;
+    f2_unpack(v, r.x, r.y);
+    return r;
 }
 
 // 2^e, e clamped to what a normal number holds
@@ -131,7 +177,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     using L = ChunkSmem<T, DK>;
-    using M = MmaType<T>;
+    using M = Pair16<T>;
     constexpr bool BF = L::BF;
     constexpr int NT = L::NT, NR = L::NR;
     constexpr uint32_t PANEL = L::PANEL;
@@ -140,7 +186,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr uint32_t IDESC_P = umma_idesc_f16(BF, 128, kPiece, false);
     constexpr uint32_t IDESC_O = umma_idesc_f16(BF, 128, kSlice, true);
     constexpr uint32_t IDESC_U = umma_idesc_f16(BF, 128, kSlice * NT, true) | (1u << 15);  // A = K^T: M-major
-    constexpr uint32_t GATE_READERS = STATES ? 8 : 16;  // warps
+    constexpr uint32_t GATE_READERS = STATES ? 8 : 20;  // warps
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -216,7 +262,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(s_full, 4);
         mbar_init(s_free, 1);
         mbar_init(p_full, 1);
-        mbar_init(w_full, 4);
+        mbar_init(w_full, 8);
         mbar_init(o_free, 4);
         for (int i = 0; i < 3; ++i) mbar_init(&role[i], 4);
         mbar_init(all_done, 1);
@@ -224,7 +270,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = threadIdx.x; i < 4 * 64; i += kChunkThreads) bad[i] = kPiece;
     if (threadIdx.x < 4) any_bad[threadIdx.x] = 0;
-    if (warp == 17) tmem_alloc_cg<1>(taddr_s, 512);
+    if (warp == 21) tmem_alloc_cg<1>(taddr_s, 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -245,100 +291,119 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     };
     bool ok = true;
 
-    if (warp < 4) {
-        // ===================== weights of the pairs inside a piece: thread = row =====================
+    if (warp < 8) {
+        // ===================== weights of the pairs inside a piece: thread = row, half of its columns =====================
+        registers_down<72>();
         if constexpr (!STATES) {
-            const int row = threadIdx.x;
-            const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+            const int w4 = warp & 3, side = (warp >> 2) * 16;
+            const int row = w4 * 32 + lane;
+            const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+            const uint32_t from_col = lanes + P_COL + side, to_col = lanes + PW_COL + side / 2;
+            uint32_t seen[8];  // of the block on the diagonal: the pairs of columns up to the row
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                seen[j] = (lane >= side + 2 * j ? 0xffffu : 0u) | (lane > side + 2 * j ? 0xffff0000u : 0u);
+            auto put = [&](int b, const uint32_t (&w)[8]) {
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(to_col + b * 16),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                             : "memory");
+            };
+            {  // the blocks behind the row's own stay 0
+                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                for (int b = w4 + 1; b < 4; ++b) put(b, zero);
+            }
             for (int c = 0; c < pieces; ++c) {
                 const PieceGates& g = gates[c & 1];
-                if (!wait(&g_full[c & 1], c >> 1) || !wait(p_full, c)) { ok = false; break; }
+                if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
+                const float mine = -g.hi[row];
+                float mine_lo = -g.lo[row];
+                if (!wait(p_full, c)) { ok = false; break; }
                 tcgen05_after_sync();
-                const float mine = g.hi[row], mine_lo = g.lo[row];
                 float shift = 0.f;  // log2 of what the row is multiplied by
                 if constexpr (!BF) {
                     float m0 = 0.f, m1 = 0.f;
 #pragma unroll 1
-                    for (int b = 0; b <= warp; ++b) {
+                    for (int h16 = 0; h16 < 2 * w4 + 2; ++h16) {
+                        float p[16];
+                        tmem_ld16(lanes + P_COL + h16 * 16, p);
+                        tmem_wait_ld();
+                        if (h16 < 2 * w4) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float p[16];
-                            tmem_ld16(lanes + P_COL + b * 32 + half * 16, p);
-                            tmem_wait_ld();
+                            for (int j = 0; j < 16; j += 2) m0 = fmaxf(m0, fabsf(p[j])), m1 = fmaxf(m1, fabsf(p[j + 1]));
+                        } else {
+                            const int last = lane - (h16 & 1) * 16;
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                const bool in0 = b < warp || half * 16 + j <= lane, in1 = b < warp || half * 16 + j + 1 <= lane;
-                                m0 = fmaxf(m0, in0 ? fabsf(p[j]) : 0.f);
-                                m1 = fmaxf(m1, in1 ? fabsf(p[j + 1]) : 0.f);
-                            }
+                            for (int j = 0; j < 16; ++j) m0 = fmaxf(m0, j <= last ? fabsf(p[j]) : 0.f);
                         }
                     }
                     const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
                     shift = (float)(14 - e);
-                    row_unit[(c & 1) * kPiece + row] = ex2(-shift);
+                    if (side == 0) row_unit[(c & 1) * kPiece + row] = ex2_approx(-shift);
+                    mine_lo += shift;
                 }
+                uint32_t p[16], w[8];
+                float* pf = reinterpret_cast<float*>(p);
+                tmem_ld16(from_col + w4 * 32, *reinterpret_cast<float(*)[16]>(pf));
                 // P' of the piece before has been read
                 if (c > 0 && !wait(&done[(c - 1) & 1], (c - 1) >> 1)) { ok = false; break; }
                 tcgen05_after_sync();
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    float from = shift + mine;  // to the row from the end of block b
-                    for (int i = b + 1; i < warp; ++i) from += g.block[i];
-                    const float f = ex2(from);
+                {  // the block on the diagonal: an exponential for each pair
+                    const uint64_t hi2 = f2_pack(mine, mine), lo2 = f2_pack(mine_lo, mine_lo);
+                    const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
+                    const ulonglong2* gl = reinterpret_cast<const ulonglong2*>(&g.lo[w4 * 32 + side]);
+                    float x[16];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int j0 = b * 32 + half * 16;
-                        uint32_t w[8];
-                        if (b > warp) {
+                    for (int j = 0; j < 4; ++j) {
+                        const ulonglong2 y = gh[j], z = gl[j];
+                        const float2 d0 = f2_get(f2_add(f2_add(hi2, y.x), f2_add(lo2, z.x)));
+                        const float2 d1 = f2_get(f2_add(f2_add(hi2, y.y), f2_add(lo2, z.y)));
+                        x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
+                        x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
+                    }
+                    tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = 0u;
-                        } else {
-                            float p[16], x[16];
-                            tmem_ld16(lanes + P_COL + j0, p);
-                            if (b < warp) {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 y = *reinterpret_cast<const float4*>(&g.col[j0 + j]);
-                                    x[j] = y.x * f, x[j + 1] = y.y * f, x[j + 2] = y.z * f, x[j + 3] = y.w * f;
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 y = *reinterpret_cast<const float4*>(&g.hi[j0 + j]);
-                                    const float4 z = *reinterpret_cast<const float4*>(&g.lo[j0 + j]);
-                                    x[j] = ex2((mine - y.x) + (mine_lo - z.x) + shift);
-                                    x[j + 1] = ex2((mine - y.y) + (mine_lo - z.y) + shift);
-                                    x[j + 2] = ex2((mine - y.z) + (mine_lo - z.z) + shift);
-                                    x[j + 3] = ex2((mine - y.w) + (mine_lo - z.w) + shift);
-                                }
-                            }
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                x[j] *= p[j];
-                                if (b == warp && half * 16 + j > lane) x[j] = 0.f;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = M::pack(x[2 * j], x[2 * j + 1]);
-                        }
-                        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                                         lanes + PW_COL + j0 / 2),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                     : "memory");
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 y = f2_get(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), f2_pack(pf[2 * j], pf[2 * j + 1])));
+                        w[j] = M::pack(y.x, y.y) & seen[j];
                     }
                 }
+                float from = mine + shift;  // the sum from the end of block b to the row
+#pragma unroll 1
+                for (int b = w4 - 1; b >= 0; --b) {
+                    tmem_ld16(from_col + b * 32, *reinterpret_cast<float(*)[16]>(pf));
+                    put(b + 1, w);
+                    const float f = ex2_approx(from);
+                    from += g.block[b];
+                    const uint64_t f2 = f2_pack(f, f);
+                    const ulonglong2* gc = reinterpret_cast<const ulonglong2*>(&g.col[b * 32 + side]);
+                    uint64_t x[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const ulonglong2 y = gc[j];
+                        x[2 * j] = f2_mul(y.x, f2), x[2 * j + 1] = f2_mul(y.y, f2);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 y = f2_get(f2_mul(x[j], f2_pack(pf[2 * j], pf[2 * j + 1])));
+                        w[j] = M::pack(y.x, y.y);
+                    }
+                }
+                put(0, w);
                 tmem_wait_st();
                 tcgen05_before_sync();
                 arrive_warp(w_full);
-                arrive_warp(&g_free[c & 1]);
+                if (lane == 0) mbar_arrive(&g_free[c & 1]);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ===================== V~: 32 rows at a time, four threads a row =====================
-        const int tid = threadIdx.x - 128;
+        registers_down<72>();
+        const int tid = threadIdx.x - 256;
         const int r = tid >> 2;
         // which four 16-byte units of its row: two threads' rows share the banks of half a row otherwise
-        const int u0 = (tid & 3) + 4 * (r & 1), u1 = u0 ^ 4;
+        const int u0 = (tid & 3) + 4 * (r & 1);
+        const uint32_t at[2] = {(uint32_t)((u0 ^ (r & 7)) << 4), (uint32_t)((u0 ^ 4 ^ (r & 7)) << 4)};
         for (int c = 0; c < pieces; ++c) {
             const int st = c & 1;
             const int n = min(kPiece, tokens - c * kPiece);
@@ -362,19 +427,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 float most = 0.f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float f = g.col[q * 32 + r] * g.after[q];
+                    __half2 m = __float2half2_rn(0.f);
+                    uint4 x[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(v + (q * 32 + r) * 128 + (((k ? u1 : u0) ^ (r & 7)) << 4));
-                        float y[8];
-                        Vec16<T>::to_float(x, y);
+                        x[k] = *reinterpret_cast<const uint4*>(v + (q * 32 + r) * 128 + at[k]);
+                        const __half2* y = reinterpret_cast<const __half2*>(&x[k]);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(y[j]) <= 65504.f ? fabsf(y[j] * f) : 0.f);
+                        for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(y[j]));
                     }
+                    float top = fmaxf(__low2float(m), __high2float(m));
+                    if (top > 65504.f) {  // an infinity: the largest of the others
+                        top = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float y[8];
+                            Vec16<T>::to_float(x[k], y);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]) <= 65504.f ? fabsf(y[j]) : 0.f);
+                        }
+                    }
+                    most = fmaxf(most, top * (g.col[q * 32 + r] * g.after[q]));
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                if (lane == 0) part[warp - 4] = most;
+                if (lane == 0) part[warp - 8] = most;
                 if (!meet(0)) { ok = false; break; }
                 const int e = exponent14(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
                 unit = pow2i(14 - e);
@@ -382,96 +459,96 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (tid == 0) u_unit[st] = pow2i(e - 14);
                 if (!meet(0)) { ok = false; break; }  // part may be written again
             }
+            int slot = c * 4 % NR, turn = c * 4 / NR;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
-                const int p = c * 4 + q, slot = p % NR;
                 const int row = q * 32 + r;
+                unsigned char* from = v + row * 128;
                 uint4 x[2];
-                unsigned char* from[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    from[k] = v + row * 128 + (((k ? u1 : u0) ^ (r & 7)) << 4);
-                    x[k] = *reinterpret_cast<const uint4*>(from[k]);
-                }
+                for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
                 const float f = g.col[row] * g.after[q] * unit;
-                if (p >= NR && !wait(&vt_free[slot], p / NR - 1)) { ok = false; break; }
+                const uint64_t f2 = f2_pack(f, f);
+                if (turn > 0 && !wait(&vt_free[slot], turn - 1)) { ok = false; break; }
                 unsigned char* to = smem + L::VT + slot * L::QUARTER + r * 128;
-                bool non_finite = false;
+                uint32_t probe = 0;  // 0 x v, summed: not 0 if one is not finite
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float y[8], probe = 0.f;
-                    Vec16<T>::to_float(x[k], y);
+                    const uint32_t xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                    uint32_t w[NT][4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) probe = fmaf(y[j], 0.f, probe);
-                    non_finite |= !(probe == 0.f);
-                    const uint32_t at = (((k ? u1 : u0) ^ (r & 7)) << 4);
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (!STATES) probe = M::zero_times(xw[j], probe);
+                        const float2 a2 = M::unpack(xw[j]);
+                        uint64_t y2 = f2_mul(f2_pack(a2.x, a2.y), f2);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = row < n ? y[j] * f : 0.f;
-#pragma unroll
-                    for (int term = 0; term < NT; ++term) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            w[j] = M::pack(y[2 * j], y[2 * j + 1]);
-                            if (term + 1 < NT) {
-                                const float2 z = M::unpack(w[j]);
-                                y[2 * j] -= z.x;
-                                y[2 * j + 1] -= z.y;
+                        for (int term = 0; term < NT; ++term) {
+                            const float2 y = f2_get(y2);
+                            if constexpr (BF) {  // the 24 bits of a number cut into three of 8
+                                const uint32_t b0 = __float_as_uint(y.x), b1 = __float_as_uint(y.y);
+                                w[term][j] = __byte_perm(b0, b1, 0x7632);
+                                if (term + 1 < NT)
+                                    y2 = f2_add(y2, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u)));
+                            } else {
+                                w[term][j] = M::pack(y.x, y.y);
+                                const float2 z = M::unpack(w[term][j]);
+                                if (term + 1 < NT) y2 = f2_add(y2, f2_pack(-z.x, -z.y));
                             }
                         }
-                        *reinterpret_cast<uint4*>(to + term * 4096 + at) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+#pragma unroll
+                    for (int term = 0; term < NT; ++term)
+                        *reinterpret_cast<uint4*>(to + term * 4096 + at[k]) =
+                            make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]);
                 }
-                if (!STATES && non_finite) {  // out of V, and noted for the results
-#pragma unroll
+                if (!STATES && (probe & 0x7fff7fffu) != 0) {  // out of V, and noted for the results
+#pragma unroll 1
                     for (int k = 0; k < 2; ++k) {
-                        float y[8];
-                        Vec16<T>::to_float(x[k], y);
-                        uint32_t w[4];
-#pragma unroll
+                        T* y = reinterpret_cast<T*>(from + at[k]);
                         for (int j = 0; j < 8; ++j)
-                            if (!(fabsf(y[j]) <= 3.4028234e38f)) {
-                                y[j] = 0.f;
-                                atomicMin(&bad[(c & 3) * 64 + (k ? u1 : u0) * 8 + j], row);
+                            if (!(fabsf(static_cast<float>(y[j])) <= 3.4028234e38f)) {
+                                y[j] = from_float<T>(0.f);
+                                atomicMin(&bad[(c & 3) * 64 + (u0 ^ (k * 4)) * 8 + j], row);
                                 any_bad[c & 3] = 1;
                             }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = M::pack(y[2 * j], y[2 * j + 1]);
-                        *reinterpret_cast<uint4*>(from[k]) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 fence_proxy_async_smem();
                 arrive_warp(&vt_full[slot]);
+                if (++slot == NR) slot = 0, ++turn;
             }
             if (!ok) break;
-            arrive_warp(&g_free[st]);
+            if (lane == 0) mbar_arrive(&g_free[st]);
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ===================== the state: thread = row of dim_k (half a row at dim_k = 64) =====================
+        registers_up<136>();
         constexpr int NC = DK == 128 ? 64 : 32;
-        const int tid = threadIdx.x - 256;
+        const int tid = threadIdx.x - 384;
         const int row = tid & (DK - 1);
         const int c0 = DK == 128 ? 0 : (tid >> 6) * 32;
-        const uint32_t lanes = tmem + ((uint32_t)((warp - 8) * 32) << 16);
+        const uint32_t lanes = tmem + ((uint32_t)((warp - 12) * 32) << 16);
         const size_t at = (size_t)row * a.dv + slice * kSlice + c0;  // in a head's state
-        float x[NC];
+        uint64_t x[NC / 2];  // pairs of columns
         auto load = [&](const float* from, bool add, float keep) {
+            const uint64_t k2 = f2_pack(keep, keep);
 #pragma unroll
-            for (int i = 0; i < NC; i += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(from + at + i);
-                x[i] = add ? fmaf(x[i], keep, y.x) : y.x;
-                x[i + 1] = add ? fmaf(x[i + 1], keep, y.y) : y.y;
-                x[i + 2] = add ? fmaf(x[i + 2], keep, y.z) : y.z;
-                x[i + 3] = add ? fmaf(x[i + 3], keep, y.w) : y.w;
+            for (int i = 0; i < NC / 2; i += 2) {
+                const float4 y = *reinterpret_cast<const float4*>(from + at + 2 * i);
+                const uint64_t y0 = f2_pack(y.x, y.y), y1 = f2_pack(y.z, y.w);
+                x[i] = add ? f2_fma(x[i], k2, y0) : y0;
+                x[i + 1] = add ? f2_fma(x[i + 1], k2, y1) : y1;
             }
         };
         auto save = [&](float* to) {
 #pragma unroll
-            for (int i = 0; i < NC; i += 4)
-                *reinterpret_cast<float4*>(to + at + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            for (int i = 0; i < NC / 2; i += 2) {
+                const float2 y = f2_get(x[i]), z = f2_get(x[i + 1]);
+                *reinterpret_cast<float4*>(to + at + 2 * i) = make_float4(y.x, y.y, z.x, z.y);
+            }
         };
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] = 0.f;
+        for (int i = 0; i < NC / 2; ++i) x[i] = 0;
         if (seg == 0) {
             // shared out, the second pass reads the start from where the first left it: its last segment writes dst
             if (!STATES && used_segs > 1)
@@ -487,17 +564,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         for (int c = 0; c < pieces; ++c) {
             if constexpr (!STATES) {  // the copy that Q meets
-                float unit = 1.f, back_s = 1.f;
+                uint64_t unit2 = 0;
+                float back_s = 1.f;
                 if constexpr (!BF) {
-                    float most = 0.f;
+                    float most = 0.f, other = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) most = fmaxf(most, fabsf(x[i]));
+                    for (int i = 0; i < NC / 2; ++i) {
+                        const float2 y = f2_get(x[i]);
+                        most = fmaxf(most, fabsf(y.x)), other = fmaxf(other, fabsf(y.y));
+                    }
+                    most = fmaxf(most, other);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    if (lane == 0) part[4 + warp - 8] = most;
+                    if (lane == 0) part[4 + warp - 12] = most;
                     if (!meet(1)) { ok = false; break; }
                     const int e = exponent14(fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
-                    unit = pow2i(14 - e);
+                    unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
                     back_s = pow2i(e - 14);
                     if (!meet(1)) { ok = false; break; }  // part may be written again
                 }
@@ -506,50 +588,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!BF && tid == 0) s_unit[c & 1] = back_s;
                 unsigned char* to = smem + L::S + row * 128;
 #pragma unroll
-                for (int i = 0; i < NC; i += 8) {
+                for (int i = 0; i < NC / 2; i += 4) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = M::pack(x[i + 2 * j] * unit, x[i + 2 * j + 1] * unit);
-                    *reinterpret_cast<uint4*>(to + ((((c0 + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = f2_get(BF ? x[i + j] : f2_mul(x[i + j], unit2));
+                        w[j] = M::pack(y.x, y.y);
+                    }
+                    *reinterpret_cast<uint4*>(to + ((((c0 + 2 * i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_proxy_async_smem();
                 arrive_warp(s_full);
             }
             const PieceGates& g = gates[c & 1];
             if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-            const float keep = g.keep, less1 = g.keep_less1;
-            const bool small = g.small != 0;
+            const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
             if (!wait(u_full, c)) { ok = false; break; }
             tcgen05_after_sync();
             const float back = BF ? 1.f : u_unit[c & 1];
 #pragma unroll
-            for (int i = 0; i < NC; i += 16) {
-                float u[16];
-                tmem_ld16(lanes + U_COL + c0 + i, u);
+            for (int i = 0; i < NC / 2; i += 8) {
+                float u[NT][16];
+#pragma unroll
+                for (int term = 0; term < NT; ++term) tmem_ld16(lanes + U_COL + 64 * term + c0 + 2 * i, u[term]);
                 tmem_wait_ld();
-                if (!BF) {
-                    float y[16];
-                    tmem_ld16(lanes + U_COL + 64 + c0 + i, y);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) u[j] = (u[j] + y[j]) * back;
-                }
+                for (int j = 0; j < 8; ++j) {
+                    uint64_t y = f2_pack(u[NT - 1][2 * j], u[NT - 1][2 * j + 1]);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[i + j] = small ? fmaf(x[i + j], less1, x[i + j] + u[j]) : fmaf(x[i + j], keep, u[j]);
-                if (BF) {
-#pragma unroll
-                    for (int term = 1; term < NT; ++term) {
-                        tmem_ld16(lanes + U_COL + 64 * term + c0 + i, u);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) x[i + j] += u[j];
-                    }
+                    for (int term = NT - 2; term >= 0; --term) y = f2_add(y, f2_pack(u[term][2 * j], u[term][2 * j + 1]));
+                    if (!BF) y = f2_mul(y, f2_pack(back, back));
+                    x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
                 }
             }
             tcgen05_before_sync();
             arrive_warp(u_free);
-            arrive_warp(&g_free[c & 1]);
+            if (lane == 0) mbar_arrive(&g_free[c & 1]);
         }
         if (ok) {
             if (STATES)
@@ -557,10 +631,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             else if (seg == used_segs - 1 && dst >= 0)
                 save(l.state + ((size_t)dst * l.n_v + h) * head);
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ===================== results: thread = row =====================
+        registers_down<72>();
         if constexpr (!STATES) {
-            const int w4 = warp - 12;
+            const int w4 = warp - 16;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
             unsigned char* stage = smem + L::O + w4 * 2048;
@@ -568,16 +643,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const int n = min(kPiece, tokens - c * kPiece);
                 const PieceGates& g = gates[c & 1];
                 if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-                float sum = g.hi[row];
+                float sum = -g.hi[row];
                 for (int i = 0; i < w4; ++i) sum += g.block[i];
                 arrive_warp(&g_free[c & 1]);
-                float fi = ex2(sum) * l.scale, fa = l.scale;
+                float fi = ex2_approx(sum) * l.scale, fa = l.scale;
                 if (!wait(&done[c & 1], c >> 1)) { ok = false; break; }
                 tcgen05_after_sync();
                 if constexpr (!BF) {
                     fi *= s_unit[c & 1];
                     fa *= row_unit[(c & 1) * kPiece + row];
                 }
+                const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
                 const bool poisoned = any_bad[c & 3] != 0;
 #pragma unroll
                 for (int c0 = 0; c0 < kSlice; c0 += 32) {
@@ -589,7 +665,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         tmem_ld16(lanes + OA_COL + c0 + half, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = fmaf(x[j], fi, y[j] * fa);
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
+                            x[j] = z.x, x[j + 1] = z.y;
+                        }
                         if (poisoned) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
@@ -628,178 +707,182 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
             }
         }
-    } else if (warp == 16) {
-        // ===================== tensor copies =====================
-        if (lane == 0) {
-            int issued = 0;
-            for (int c = 0; c < pieces; ++c) {
-                const int st = c & 1;
-                if (c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
-                const int y = t0 + c * kPiece;
-                mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
-#pragma unroll
-                for (int p = 0; p < DK / 64; ++p) {
-                    if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
-                    tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
-                }
-                mbar_arrive_expect_tx(&v_full[st], PANEL);
-                tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
-                issued = c + 1;
-            }
-            // no copy is in flight when the CTA leaves
-            for (int c = max(issued - 2, 0); c < issued; ++c) {
-                ok = wait1(&qk_full[c & 1], c >> 1) && ok;
-                ok = wait1(&v_full[c & 1], c >> 1) && ok;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 17) {
-        // ===================== products =====================
-        if (lane == 0) {
-            const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
-            const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
-            // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
-            const uint64_t dkt = umma_desc_sw128(sbase + L::K, DK == 128 ? PANEL : 0, 1024);
-            const uint64_t dv = umma_desc_sw128(sbase + L::V, PANEL, 1024);
-            const uint64_t ds = umma_desc_sw128(sbase + L::S, DK * 128, 1024);
-            const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
-            auto pairs = [&](int c) {  // P = Q K^T
-                const uint32_t st = (uint32_t)(c & 1) * L::QK;
-                tcgen05_after_sync();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint64_t off = (st + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4;
-                    umma_f16_cg<1>(tmem + P_COL, dq + off, dk + off, IDESC_P, k > 0);
-                }
-                umma_commit_cg<1>(p_full);
-            };
-            if (!STATES && pieces > 0) {
-                ok = wait1(&qk_full[0], 0);
-                if (ok) pairs(0);
-            }
-            for (int c = 0; c < pieces && ok; ++c) {
-                const uint32_t st = (uint32_t)(c & 1);
-                // U = K^T V~
-                if (!wait1(&qk_full[st], c >> 1) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
-                for (int q = 0; q < 4; ++q) {
-                    const int p = c * 4 + q, slot = p % NR;
-                    if (!wait1(&vt_full[slot], p / NR)) { ok = false; break; }
-                    tcgen05_after_sync();
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        umma_f16_cg<1>(tmem + U_COL, dkt + (uint64_t)((st * L::QK + (uint32_t)(q * 2 + k) * 2048) >> 4),
-                                       dvt + (uint64_t)(((uint32_t)slot * L::QUARTER + (uint32_t)k * 2048) >> 4), IDESC_U,
-                                       q > 0 || k > 0);
-                    umma_commit_cg<1>(&vt_free[slot]);
-                }
-                if (!ok) break;
-                umma_commit_cg<1>(u_full);
-                if constexpr (STATES) {
-                    umma_commit_cg<1>(&done[st]);
-                } else {
-                    // OI = Q S
-                    if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
-                    tcgen05_after_sync();
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        umma_f16_cg<1>(tmem + OI_COL,
-                                       dq + (uint64_t)((st * L::QK + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4),
-                                       ds + (uint64_t)(((uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
-                    umma_commit_cg<1>(s_free);
-                    if (!wait1(w_full, c)) { ok = false; break; }
-                    if (c + 1 < pieces) {
-                        if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
-                        pairs(c + 1);
-                    }
-                    // OA = P' V
-                    if (!wait1(&v_full[st], c >> 1)) { ok = false; break; }
-                    tcgen05_after_sync();
-#pragma unroll
-                    for (int k = 0; k < kPiece / 16; ++k)
-                        umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + k * 8,
-                                              dv + (uint64_t)((st * PANEL + (uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
-                    umma_commit_cg<1>(&done[st]);
-                }
-            }
-            // every product is done before tensor memory is given back
-            umma_commit_cg<1>(all_done);
-            ok = wait1(all_done, 0) && ok;
-        }
-        __syncwarp();
-    } else if (warp == 18) {
-        // ===================== sums of the log decays: lane = 4 tokens =====================
-        float raw[4];
-        auto fetch = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = c * kPiece + lane * 4 + i;
-                raw[i] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
-            }
-        };
-        if (pieces > 0) fetch(0);
-        double total = 0.0;
-        for (int c = 0; c < pieces; ++c) {
-            double x[4], grow = 0.0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // 2^-150 is 0 in fp32: a token that forgets (-infinity) then takes part in sums
-                const float y = raw[i] < -104.f ? -104.f : raw[i];
-                x[i] = (double)y * 1.4426950408889634;
-                if (x[i] > 0.0) grow += x[i];
-            }
-            if (c + 1 < pieces) fetch(c + 1);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
-            double before = x[3];  // over the lanes of a block of 32 tokens (eight)
-#pragma unroll
-            for (int o = 1; o < 8; o *= 2) {
-                const double y = __shfl_up_sync(0xffffffffu, before, o);
-                if ((lane & 7) >= o) before += y;
-            }
-            const double block = __shfl_sync(0xffffffffu, before, lane | 7);
-            before -= x[3];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
-            double blocks[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) blocks[b] = __shfl_sync(0xffffffffu, block, b * 8);
-            if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
-            PieceGates& g = gates[c & 1];
-            float hi[4], lo[4], col[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const double y = before + x[i];
-                hi[i] = (float)y;
-                lo[i] = (float)(y - (double)hi[i]);
-                col[i] = exp2f((float)(block - y));
-            }
-            *reinterpret_cast<float4*>(&g.hi[lane * 4]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<float4*>(&g.lo[lane * 4]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-            *reinterpret_cast<float4*>(&g.col[lane * 4]) = make_float4(col[0], col[1], col[2], col[3]);
-            const double all = (blocks[0] + blocks[1]) + (blocks[2] + blocks[3]);
-            total += all;
+    } else {
+        registers_down<56>();  // (one instruction for the four warps)
+        if (warp == 20) {
+            // ===================== tensor copies =====================
             if (lane == 0) {
-                double behind = 0.0;
+                int issued = 0;
+                for (int c = 0; c < pieces; ++c) {
+                    const int st = c & 1;
+                    if (c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
+                    const int y = t0 + c * kPiece;
+                    mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
 #pragma unroll
-                for (int b = 3; b >= 0; --b) {
-                    g.block[b] = (float)blocks[b];
-                    g.after[b] = exp2f((float)behind);
-                    behind += blocks[b];
+                    for (int p = 0; p < DK / 64; ++p) {
+                        if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
+                        tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
+                    }
+                    mbar_arrive_expect_tx(&v_full[st], PANEL);
+                    tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
+                    issued = c + 1;
                 }
-                g.keep = exp2f((float)all);
-                g.keep_less1 = expm1f((float)(all * 0.6931471805599453));
-                g.small = all > -0.7 && all < 0.7;
-                g.grow = (float)grow;
+                // no copy is in flight when the CTA leaves
+                for (int c = max(issued - 2, 0); c < issued; ++c) {
+                    ok = wait1(&qk_full[c & 1], c >> 1) && ok;
+                    ok = wait1(&v_full[c & 1], c >> 1) && ok;
+                }
             }
-            arrive_warp(&g_full[c & 1]);
+            __syncwarp();
+        } else if (warp == 21) {
+            // ===================== products: the warp goes along, one thread issues =====================
+            {
+                const bool lead = elect_one() != 0;
+                const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
+                const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
+                // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
+                const uint64_t dkt = umma_desc_sw128(sbase + L::K, DK == 128 ? PANEL : 0, 1024);
+                const uint64_t dv = umma_desc_sw128(sbase + L::V, PANEL, 1024);
+                const uint64_t ds = umma_desc_sw128(sbase + L::S, DK * 128, 1024);
+                const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
+                auto pairs = [&](int c) {  // P = Q K^T
+                    const uint32_t st = (uint32_t)(c & 1) * L::QK;
+                    tcgen05_after_sync();
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k) {
+                        const uint64_t off = (st + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4;
+                        if (lead) umma_f16_cg<1>(tmem + P_COL, dq + off, dk + off, IDESC_P, k > 0);
+                    }
+                    if (lead) umma_commit_cg<1>(p_full);
+                };
+                if (!STATES && pieces > 0) {
+                    ok = wait(&qk_full[0], 0);
+                    if (ok) pairs(0);
+                }
+                for (int c = 0; c < pieces && ok; ++c) {
+                    const uint32_t st = (uint32_t)(c & 1);
+                    // U = K^T V~
+                    if (!wait(&qk_full[st], c >> 1) || (c > 0 && !wait(u_free, c - 1))) { ok = false; break; }
+                    for (int q = 0; q < 4; ++q) {
+                        const int p = c * 4 + q, slot = p % NR;
+                        if (!wait(&vt_full[slot], p / NR)) { ok = false; break; }
+                        tcgen05_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (lead) umma_f16_cg<1>(tmem + U_COL, dkt + (uint64_t)((st * L::QK + (uint32_t)(q * 2 + k) * 2048) >> 4),
+                                           dvt + (uint64_t)(((uint32_t)slot * L::QUARTER + (uint32_t)k * 2048) >> 4), IDESC_U,
+                                           q > 0 || k > 0);
+                        if (lead) umma_commit_cg<1>(&vt_free[slot]);
+                    }
+                    if (!ok) break;
+                    if (lead) umma_commit_cg<1>(u_full);
+                    if constexpr (STATES) {
+                        if (lead) umma_commit_cg<1>(&done[st]);
+                    } else {
+                        // OI = Q S
+                        if (!wait(s_full, c) || (c > 0 && !wait(o_free, c - 1))) { ok = false; break; }
+                        tcgen05_after_sync();
+#pragma unroll
+                        for (int k = 0; k < DK / 16; ++k)
+                            if (lead) umma_f16_cg<1>(tmem + OI_COL,
+                                           dq + (uint64_t)((st * L::QK + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4),
+                                           ds + (uint64_t)(((uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
+                        if (lead) umma_commit_cg<1>(s_free);
+                        if (!wait(w_full, c)) { ok = false; break; }
+                        if (c + 1 < pieces) {
+                            if (!wait(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
+                            pairs(c + 1);
+                        }
+                        // OA = P' V
+                        if (!wait(&v_full[st], c >> 1)) { ok = false; break; }
+                        tcgen05_after_sync();
+#pragma unroll
+                        for (int k = 0; k < kPiece / 16; ++k)
+                            if (lead) umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + k * 8,
+                                                  dv + (uint64_t)((st * PANEL + (uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
+                        if (lead) umma_commit_cg<1>(&done[st]);
+                    }
+                }
+                // every product is done before tensor memory is given back
+                if (lead) umma_commit_cg<1>(all_done);
+                ok = wait(all_done, 0) && ok;
+            }
+            __syncwarp();
+        } else if (warp == 22) {
+            // ===================== sums of the log decays: lane = 4 tokens =====================
+            float raw[4];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = c * kPiece + lane * 4 + i;
+                    raw[i] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
+                }
+            };
+            if (pieces > 0) fetch(0);
+            double total = 0.0;
+            for (int c = 0; c < pieces; ++c) {
+                double x[4], grow = 0.0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // 2^-150 is 0 in fp32: a token that forgets (-infinity) then takes part in sums
+                    const float y = raw[i] < -104.f ? -104.f : raw[i];
+                    x[i] = (double)y * 1.4426950408889634;
+                    if (x[i] > 0.0) grow += x[i];
+                }
+                if (c + 1 < pieces) fetch(c + 1);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
+                double before = x[3];  // over the lanes of a block of 32 tokens (eight)
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2) {
+                    const double y = __shfl_up_sync(0xffffffffu, before, o);
+                    if ((lane & 7) >= o) before += y;
+                }
+                const double block = __shfl_sync(0xffffffffu, before, lane | 7);
+                before -= x[3];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
+                double blocks[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) blocks[b] = __shfl_sync(0xffffffffu, block, b * 8);
+                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                PieceGates& g = gates[c & 1];
+                float hi[4], lo[4], col[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double y = before + x[i];
+                    hi[i] = -(float)y;
+                    lo[i] = -(float)(y + (double)hi[i]);
+                    col[i] = exp2f((float)(block - y));
+                }
+                *reinterpret_cast<float4*>(&g.hi[lane * 4]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<float4*>(&g.lo[lane * 4]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<float4*>(&g.col[lane * 4]) = make_float4(col[0], col[1], col[2], col[3]);
+                const double all = (blocks[0] + blocks[1]) + (blocks[2] + blocks[3]);
+                total += all;
+                if (lane == 0) {
+                    double behind = 0.0;
+#pragma unroll
+                    for (int b = 3; b >= 0; --b) {
+                        g.block[b] = (float)blocks[b];
+                        g.after[b] = exp2f((float)behind);
+                        behind += blocks[b];
+                    }
+                    const bool small = all > -0.7 && all < 0.7;
+                    g.keep = small ? expm1f((float)(all * 0.6931471805599453)) : exp2f((float)all);
+                    g.once = small ? 1.f : 0.f;
+                    g.grow = (float)grow;
+                }
+                arrive_warp(&g_full[c & 1]);
+            }
+            if (STATES && ok && lane == 0 && slice == 0) a.sums[((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h] = (float)total;
         }
-        if (STATES && ok && lane == 0 && slice == 0) a.sums[((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h] = (float)total;
     }
     if (!ok && lane == 0) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 17) tmem_dealloc_cg<1>(tmem, 512);
+    if (warp == 21) tmem_dealloc_cg<1>(tmem, 512);
 }
 
 template <typename T, int DK, bool STATES>
