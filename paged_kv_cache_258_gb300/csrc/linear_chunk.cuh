@@ -13,15 +13,15 @@
 //                columns of an earlier block of 32: exp(G_i - R) times exp(R - G_j), R the sum up to the block's end:
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
 //                one for each pair. A thread takes a row's even or odd halves of 32 columns
-//   warps 8-11   V~, in quarters of 32 rows through a ring: split into numbers of the type that add up to it (two of
+//   warps 8-15   V~, in quarters of 32 rows through a ring, four warps on every other one: split into numbers of the type that add up to it (two of
 //                fp16: 2^-22 is left; three of bf16: exact), beside one another along N, so that one product of N = 128
 //                or 192 gives their sums and the state keeps fp32's precision
-//   warps 12-15  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
+//   warps 16-19  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
-//   warps 16-19  results: exp(G_i) OI + OA, through shared memory to whole rows
-//   warp 20      tensor copies of Q, K and V, two pieces ahead
-//   warp 21      issues the products
-//   warp 22      sums of decays (in 64 bits: differences of far sums; held as two fp32 where pairs need them)
+//   warps 20-23  results: exp(G_i) OI + OA, through shared memory to whole rows
+//   warp 24      tensor copies of Q, K and V, two pieces ahead
+//   warp 25      issues the products
+//   warps 26, 27 sums of decays (in 64 bits: differences of far sums; held as two fp32 where pairs need them)
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
 // fp16 cannot hold their range: rows of P', the copy of S and V~ are then brought to 2^14 by a power of two each, which
@@ -42,7 +42,7 @@ namespace pkv {
 
 constexpr int kPiece = 128;   // tokens of a piece: the M of a product
 constexpr int kSlice = 64;    // columns of v of a CTA
-constexpr int kChunkThreads = 6 * 128;
+constexpr int kChunkThreads = 7 * 128;
 
 // Pairs of 16-bit numbers in a word.
 template <typename T>
@@ -83,7 +83,7 @@ struct __align__(16) PieceGates {
     float after[4];                // 2^(sum over the blocks behind it)
     float keep, once;              // S' = S + (U + S * keep) with 2^(sum over all) - 1 where that is small, once = 1,
     float grow;                    // else S * keep + U, once = 0; sum of the positive ones
-    int pad;
+    float sum;                     // over all
 };
 
 template <typename T, int DK>
@@ -103,8 +103,8 @@ struct ChunkSmem {
     static constexpr uint32_t GATES = O + 4 * 2048;        // [2]
     static constexpr uint32_t BAD = GATES + 2 * sizeof(PieceGates);  // int [4][64]: first non-finite v of a column
     static constexpr uint32_t ROW = BAD + 4 * 64 * 4;      // fp16: float [2][128], 2^-e of P's rows
-    static constexpr uint32_t MISC = ROW + (BF ? 0 : 2 * 128 * 4);  // any_bad[4] s_unit[2] u_unit[2] part[2][4]
-    static constexpr uint32_t BARS = MISC + 64;
+    static constexpr uint32_t MISC = ROW + (BF ? 0 : 2 * 128 * 4);  // any_bad[4] s_unit[2] u_unit[2] part[8 + 4]
+    static constexpr uint32_t BARS = MISC + 96;
     static constexpr int NBARS = 2 + 2 + 2 + 2 + 2 + 2 * NR + 7 + 4;
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
@@ -132,8 +132,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// Every thread of the four warps: registers a thread from here on. The kernel's 80 a thread are shared out anew:
-// 72 + 72 + 72 + 136 + 72 + 56 = 6 * 80.
+// Every thread of the four warps: registers a thread from here on. The kernel's 72 a thread are shared out anew, as
+// 64 + 64 + 64 + 64 + 136 + 64 + 48 = 7 * 72.
 template <int N>
 __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -153,6 +153,17 @@ __device__ __forceinline__ float2 f2_get(uint64_t v) {
     float2 r;
     f2_unpack(v, r.x, r.y);
     return r;
+}
+
+// mbar_wait_bounded in few instructions: the roles' loops compete for the instruction caches.
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
+    uint64_t begin = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        const uint64_t now = global_timer_ns();
+        if (begin == 0) begin = now;
+        if (now - begin > kWaitLimitNs) return false;
+    }
+    return true;
 }
 
 // 2^e, e clamped to what a normal number holds
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr uint32_t IDESC_P = umma_idesc_f16(BF, 128, kPiece, false);
     constexpr uint32_t IDESC_O = umma_idesc_f16(BF, 128, kSlice, true);
     constexpr uint32_t IDESC_U = umma_idesc_f16(BF, 128, kSlice * NT, true) | (1u << 15);  // A = K^T: M-major
-    constexpr uint32_t GATE_READERS = STATES ? 8 : 20;  // warps
+    constexpr uint32_t GATE_READERS = STATES ? 12 : 24;  // warps
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -198,7 +209,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     int* any_bad = reinterpret_cast<int*>(smem + L::MISC);
     float* s_unit = reinterpret_cast<float*>(smem + L::MISC + 16);
     float* u_unit = reinterpret_cast<float*>(smem + L::MISC + 24);
-    float* part = reinterpret_cast<float*>(smem + L::MISC + 32);  // [2 roles][4 warps]
+    float* part = reinterpret_cast<float*>(smem + L::MISC + 32);  // of V~'s warps, then the state's
     uint64_t* qk_full = reinterpret_cast<uint64_t*>(smem + L::BARS);  // [2] Q and K of a piece have landed
     uint64_t* v_full = qk_full + 2;                                   // [2]
     uint64_t* done = v_full + 2;       // [2] every product of a piece is done: its buffers and results
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* p_full = s_free + 1;     // P is done
     uint64_t* w_full = p_full + 1;     // P' is written (and P read)
     uint64_t* o_free = w_full + 1;     // OI and OA are read
-    uint64_t* role = o_free + 1;       // [3] the four warps of a role meet
+    uint64_t* role = o_free + 1;       // [3] the warps of a role meet
     uint64_t* all_done = role + 3;     // every product issued is done
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
@@ -264,28 +275,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(p_full, 1);
         mbar_init(w_full, 8);
         mbar_init(o_free, 4);
-        for (int i = 0; i < 3; ++i) mbar_init(&role[i], 4);
+        for (int i = 0; i < 3; ++i) mbar_init(&role[i], i == 0 ? 8 : 4);
         mbar_init(all_done, 1);
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 4 * 64; i += kChunkThreads) bad[i] = kPiece;
     if (threadIdx.x < 4) any_bad[threadIdx.x] = 0;
-    if (warp == 21) tmem_alloc_cg<1>(taddr_s, 512);
+    if (warp == 25) tmem_alloc_cg<1>(taddr_s, 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = *taddr_s;
     // The n-th phase of a barrier, for one thread, or for a whole warp, which goes on or gives up together.
-    auto wait1 = [](uint64_t* bar, int n) -> bool { return mbar_wait_bounded(bar, (uint32_t)n & 1u); };
-    auto wait = [](uint64_t* bar, int n) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)n & 1u));
-    };
+    auto wait1 = [](uint64_t* bar, int n) -> bool { return wait_short(bar, (uint32_t)n & 1u); };
+    auto wait = [](uint64_t* bar, int n) -> bool { return __all_sync(0xffffffffu, wait_short(bar, (uint32_t)n & 1u)); };
     auto arrive_warp = [&](uint64_t* bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
     int met = 0;
-    auto meet = [&](int id) -> bool {  // the four warps of a role
+    auto meet = [&](int id) -> bool {  // the warps of a role
         arrive_warp(&role[id]);
         return wait(&role[id], met++);
     };
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
     if (warp < 8) {
         // ===================== weights of the pairs inside a piece: thread = row, half of its columns =====================
-        registers_down<72>();
+        registers_down<64>();
         if constexpr (!STATES) {
             const int w4 = warp & 3, side = (warp >> 2) * 16;
             const int row = w4 * 32 + lane;
@@ -396,11 +405,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (lane == 0) mbar_arrive(&g_free[c & 1]);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ===================== V~: 32 rows at a time, four threads a row =====================
-        registers_down<72>();
+        registers_down<64>();
         const int tid = threadIdx.x - 256;
-        const int r = tid >> 2;
+        const int half = tid >> 7;  // quarters 0 and 2, or 1 and 3
+        const int r = (tid & 127) >> 2;
         // which four 16-byte units of its row: two threads' rows share the banks of half a row otherwise
         const int u0 = (tid & 3) + 4 * (r & 1);
         const uint32_t at[2] = {(uint32_t)((u0 ^ (r & 7)) << 4), (uint32_t)((u0 ^ 4 ^ (r & 7)) << 4)};
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (n < kPiece) {  // rows behind the sequence's end
                 if (!wait(&qk_full[st], c >> 1)) { ok = false; break; }
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = n * 8 + tid; i < kPiece * 8; i += 128) {
+                for (int i = n * 8 + tid; i < kPiece * 8; i += 256) {
                     *reinterpret_cast<uint4*>(v + i * 16) = zero;
 #pragma unroll
                     for (int p = 0; p < DK / 64; ++p)
@@ -425,8 +435,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             float unit = 1.f;
             if constexpr (!BF) {  // the largest of V~, to bring it to 2^14
                 float most = 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
+#pragma unroll 1
+                for (int q = half; q < 4; q += 2) {
                     __half2 m = __float2half2_rn(0.f);
                     uint4 x[2];
 #pragma unroll
@@ -453,15 +463,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
                 if (lane == 0) part[warp - 8] = most;
                 if (!meet(0)) { ok = false; break; }
-                const int e = exponent14(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+                const float4 p0 = *reinterpret_cast<const float4*>(part), p1 = *reinterpret_cast<const float4*>(part + 4);
+                const int e = exponent14(fmaxf(fmaxf(fmaxf(p0.x, p0.y), fmaxf(p0.z, p0.w)), fmaxf(fmaxf(p1.x, p1.y), fmaxf(p1.z, p1.w))));
                 unit = pow2i(14 - e);
                 // (read for the piece before the last one: that piece's gates have been released by the state's warps)
                 if (tid == 0) u_unit[st] = pow2i(e - 14);
                 if (!meet(0)) { ok = false; break; }  // part may be written again
             }
-            int slot = c * 4 % NR, turn = c * 4 / NR;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = half; q < 4; q += 2) {
+                const int turn = (c * 4 + q) / NR, slot = c * 4 + q - turn * NR;
                 const int row = q * 32 + r;
                 unsigned char* from = v + row * 128;
                 uint4 x[2];
@@ -515,19 +526,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 fence_proxy_async_smem();
                 arrive_warp(&vt_full[slot]);
-                if (++slot == NR) slot = 0, ++turn;
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&g_free[st]);
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ===================== the state: thread = row of dim_k (half a row at dim_k = 64) =====================
         registers_up<136>();
         constexpr int NC = DK == 128 ? 64 : 32;
-        const int tid = threadIdx.x - 384;
+        const int tid = threadIdx.x - 512;
         const int row = tid & (DK - 1);
         const int c0 = DK == 128 ? 0 : (tid >> 6) * 32;
-        const uint32_t lanes = tmem + ((uint32_t)((warp - 12) * 32) << 16);
+        const uint32_t lanes = tmem + ((uint32_t)((warp - 16) * 32) << 16);
         const size_t at = (size_t)row * a.dv + slice * kSlice + c0;  // in a head's state
         uint64_t x[NC / 2];  // pairs of columns
         auto load = [&](const float* from, bool add, float keep) {
@@ -562,6 +572,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 load(a.added + to * head, i > 0, i > 0 ? exp2f(a.sums[to]) : 0.f);
             }
         }
+        float sum = 0.f;
         for (int c = 0; c < pieces; ++c) {
             if constexpr (!STATES) {  // the copy that Q meets
                 uint64_t unit2 = 0;
@@ -576,9 +587,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     most = fmaxf(most, other);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    if (lane == 0) part[4 + warp - 12] = most;
+                    if (lane == 0) part[8 + warp - 16] = most;
                     if (!meet(1)) { ok = false; break; }
-                    const int e = exponent14(fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
+                    const int e = exponent14(fmaxf(fmaxf(part[8], part[9]), fmaxf(part[10], part[11])));
                     unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
                     back_s = pow2i(e - 14);
                     if (!meet(1)) { ok = false; break; }  // part may be written again
@@ -603,6 +614,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const PieceGates& g = gates[c & 1];
             if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
             const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
+            if (STATES) sum += g.sum;
             if (!wait(u_full, c)) { ok = false; break; }
             tcgen05_after_sync();
             const float back = BF ? 1.f : u_unit[c & 1];
@@ -626,19 +638,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (lane == 0) mbar_arrive(&g_free[c & 1]);
         }
         if (ok) {
-            if (STATES)
-                save(a.added + (((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h) * head);
-            else if (seg == used_segs - 1 && dst >= 0)
+            if (STATES) {
+                const size_t to = ((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h;
+                save(a.added + to * head);
+                if (tid == 0 && slice == 0) a.sums[to] = sum;
+            } else if (seg == used_segs - 1 && dst >= 0)
                 save(l.state + ((size_t)dst * l.n_v + h) * head);
         }
-    } else if (warp < 20) {
+    } else if (warp < 24) {
         // ===================== results: thread = row =====================
-        registers_down<72>();
+        registers_down<64>();
         if constexpr (!STATES) {
-            const int w4 = warp - 16;
+            const int w4 = warp - 20;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+            // 64 bytes of each of the warp's 32 rows are staged at a time: unit u of row r at u ^ (r / 2 & 3), so that
+            // eight rows' units lie in different banks; a store then takes eight rows, four lanes a row
             unsigned char* stage = smem + L::O + w4 * 2048;
+            const uint32_t swz = (lane >> 1) & 3;
+            const int out_row = w4 * 32 + (lane >> 2);
+            const uint32_t from = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+            const size_t pitch = (size_t)l.n_v * a.dv * sizeof(T);
+            char* out = static_cast<char*>(l.out) + (size_t)(t0 + out_row) * pitch +
+                        ((size_t)h * a.dv + slice * kSlice + (lane & 3) * 8) * sizeof(T);
             for (int c = 0; c < pieces; ++c) {
                 const int n = min(kPiece, tokens - c * kPiece);
                 const PieceGates& g = gates[c & 1];
@@ -655,51 +677,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
                 const bool poisoned = any_bad[c & 3] != 0;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kSlice; c0 += 16) {
+                    float x[16], y[16];
+                    tmem_ld16(lanes + OI_COL + c0, x);
+                    tmem_ld16(lanes + OA_COL + c0, y);
+                    tmem_wait_ld();
+                    uint32_t w[8];
 #pragma unroll
-                for (int c0 = 0; c0 < kSlice; c0 += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int half = 0; half < 32; half += 16) {
-                        float x[16], y[16];
-                        tmem_ld16(lanes + OI_COL + c0 + half, x);
-                        tmem_ld16(lanes + OA_COL + c0 + half, y);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
-                            x[j] = z.x, x[j + 1] = z.y;
-                        }
-                        if (poisoned) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (bad[(c & 3) * 64 + c0 + half + j] <= row) x[j] = __int_as_float(0x7fffffff);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) w[half / 2 + j] = M::pack(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 16; j += 2) {
+                        float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
+                        w[j / 2] = M::pack(z.x, z.y);
                     }
-                    if (c0 + 32 == kSlice) {
-                        tcgen05_before_sync();
-                        arrive_warp(o_free);
+                    if (poisoned) {
+                        const int* mark = &bad[(c & 3) * 64 + c0];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (mark[j] <= row) w[j / 2] |= 0x7fffu << (16 * (j & 1));
                     }
-                    // 64 bytes of each of the warp's 32 rows: unit u of row r at u ^ (r / 2 & 3), so that eight
-                    // rows' units lie in different banks
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int rr = k * 8 + (lane >> 2), u = lane & 3, in = w4 * 32 + rr;
-                        if (in < n) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
-                            T* out = static_cast<T*>(l.out) + ((size_t)(t0 + c * kPiece + in) * l.n_v + h) * a.dv +
-                                     slice * kSlice + c0 + u * 8;
-                            *reinterpret_cast<uint4*>(out) = y;
+                    const int u = (c0 >> 3) & 2;
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + (((u + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    if (c0 & 16) {
+                        if (c0 + 16 == kSlice) {
+                            tcgen05_before_sync();
+                            arrive_warp(o_free);
+                        } else {
+                            __syncwarp();
                         }
+                        char* to = out + (size_t)(c0 - 16) * sizeof(T);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k, to += 8 * pitch)
+                            if (out_row + k * 8 < n) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(stage + from + k * 512);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                out += kPiece * pitch;
                 if (poisoned) {  // the columns' marks are used again four pieces on
                     if (!meet(2)) { ok = false; break; }
                     if (row < 64) bad[(c & 3) * 64 + row] = kPiece;
@@ -708,8 +721,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         }
     } else {
-        registers_down<56>();  // (one instruction for the four warps)
-        if (warp == 20) {
+        registers_down<48>();  // (one instruction for the four warps)
+        if (warp == 24) {
             // ===================== tensor copies =====================
             if (lane == 0) {
                 int issued = 0;
@@ -734,10 +747,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == 21) {
-            // ===================== products: the warp goes along, one thread issues =====================
-            {
-                const bool lead = elect_one() != 0;
+        } else if (warp == 25) {
+            // ===================== products: one thread =====================
+            if (elect_one()) {
                 const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
                 const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
                 // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
@@ -745,71 +757,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const uint64_t dv = umma_desc_sw128(sbase + L::V, PANEL, 1024);
                 const uint64_t ds = umma_desc_sw128(sbase + L::S, DK * 128, 1024);
                 const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
-                auto pairs = [&](int c) {  // P = Q K^T
-                    const uint32_t st = (uint32_t)(c & 1) * L::QK;
+                auto pairs = [&](uint32_t st) {  // P = Q K^T
+                    const uint64_t q = dq + ((st * L::QK) >> 4), k = dk + ((st * L::QK) >> 4);
                     tcgen05_after_sync();
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k) {
-                        const uint64_t off = (st + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4;
-                        if (lead) umma_f16_cg<1>(tmem + P_COL, dq + off, dk + off, IDESC_P, k > 0);
+                    for (int i = 0; i < DK / 16; ++i) {
+                        const uint32_t off = (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4);
+                        umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
                     }
-                    if (lead) umma_commit_cg<1>(p_full);
+                    umma_commit_cg<1>(p_full);
                 };
                 if (!STATES && pieces > 0) {
-                    ok = wait(&qk_full[0], 0);
+                    ok = wait1(&qk_full[0], 0);
                     if (ok) pairs(0);
                 }
+                int slot = 0, turn = 0;  // of V~'s ring
                 for (int c = 0; c < pieces && ok; ++c) {
                     const uint32_t st = (uint32_t)(c & 1);
-                    // U = K^T V~
-                    if (!wait(&qk_full[st], c >> 1) || (c > 0 && !wait(u_free, c - 1))) { ok = false; break; }
+                    // U = K^T V~ (V~'s warps have seen V land; K has landed where P was computed)
+                    if ((STATES && !wait1(&qk_full[st], c >> 1)) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
+                    const uint64_t kt = dkt + ((st * L::QK) >> 4);
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        const int p = c * 4 + q, slot = p % NR;
-                        if (!wait(&vt_full[slot], p / NR)) { ok = false; break; }
+                        if (!wait1(&vt_full[slot], turn)) { ok = false; break; }
                         tcgen05_after_sync();
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (lead) umma_f16_cg<1>(tmem + U_COL, dkt + (uint64_t)((st * L::QK + (uint32_t)(q * 2 + k) * 2048) >> 4),
-                                           dvt + (uint64_t)(((uint32_t)slot * L::QUARTER + (uint32_t)k * 2048) >> 4), IDESC_U,
-                                           q > 0 || k > 0);
-                        if (lead) umma_commit_cg<1>(&vt_free[slot]);
+                        const uint64_t vt = dvt + (((uint32_t)slot * L::QUARTER) >> 4), k0 = kt + (uint32_t)q * (4096 >> 4);
+                        umma_f16_cg<1>(tmem + U_COL, k0, vt, IDESC_U, q > 0);
+                        umma_f16_cg<1>(tmem + U_COL, k0 + (2048 >> 4), vt + (2048 >> 4), IDESC_U, true);
+                        umma_commit_cg<1>(&vt_free[slot]);
+                        if (++slot == NR) slot = 0, ++turn;
                     }
                     if (!ok) break;
-                    if (lead) umma_commit_cg<1>(u_full);
+                    umma_commit_cg<1>(u_full);
                     if constexpr (STATES) {
-                        if (lead) umma_commit_cg<1>(&done[st]);
+                        umma_commit_cg<1>(&done[st]);
                     } else {
                         // OI = Q S
-                        if (!wait(s_full, c) || (c > 0 && !wait(o_free, c - 1))) { ok = false; break; }
+                        if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
                         tcgen05_after_sync();
+                        const uint64_t q = dq + ((st * L::QK) >> 4);
 #pragma unroll
-                        for (int k = 0; k < DK / 16; ++k)
-                            if (lead) umma_f16_cg<1>(tmem + OI_COL,
-                                           dq + (uint64_t)((st * L::QK + (uint32_t)(k >> 2) * PANEL + (uint32_t)(k & 3) * 32) >> 4),
-                                           ds + (uint64_t)(((uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
-                        if (lead) umma_commit_cg<1>(s_free);
-                        if (!wait(w_full, c)) { ok = false; break; }
+                        for (int i = 0; i < DK / 16; ++i)
+                            umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
+                                           ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
+                        umma_commit_cg<1>(s_free);
+                        if (!wait1(w_full, c)) { ok = false; break; }
                         if (c + 1 < pieces) {
-                            if (!wait(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
-                            pairs(c + 1);
+                            if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
+                            pairs(st ^ 1);
                         }
                         // OA = P' V
-                        if (!wait(&v_full[st], c >> 1)) { ok = false; break; }
                         tcgen05_after_sync();
+                        const uint64_t v = dv + ((st * PANEL) >> 4);
 #pragma unroll
-                        for (int k = 0; k < kPiece / 16; ++k)
-                            if (lead) umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + k * 8,
-                                                  dv + (uint64_t)((st * PANEL + (uint32_t)k * 2048) >> 4), IDESC_O, k > 0);
-                        if (lead) umma_commit_cg<1>(&done[st]);
+                        for (int i = 0; i < kPiece / 16; ++i)
+                            umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + i * 8, v + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
+                        umma_commit_cg<1>(&done[st]);
                     }
                 }
                 // every product is done before tensor memory is given back
-                if (lead) umma_commit_cg<1>(all_done);
-                ok = wait(all_done, 0) && ok;
+                umma_commit_cg<1>(all_done);
+                ok = wait1(all_done, 0) && ok;
+                if (!ok) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
             }
             __syncwarp();
-        } else if (warp == 22) {
-            // ===================== sums of the log decays: lane = 4 tokens =====================
+        } else {
+            // ===================== sums of the log decays: lane = 4 tokens, a warp for every other piece =====================
+            // Whole numbers of 2^-40 (in 64 bits): sums and differences are exact, and 64-bit floats too slow here.
+            constexpr float UNIT = 1.0f / 1099511627776.0f;
             float raw[4];
             auto fetch = [&](int c) {
 #pragma unroll
@@ -818,71 +833,99 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     raw[i] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
                 }
             };
-            if (pieces > 0) fetch(0);
-            double total = 0.0;
-            for (int c = 0; c < pieces; ++c) {
-                double x[4], grow = 0.0;
+            const int odd = warp - 26;
+            if (odd < pieces) fetch(odd);
+            for (int c = odd; c < pieces; c += 2) {
+                long long x[4];
+                float poison[4], grow = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // 2^-150 is 0 in fp32: a token that forgets (-infinity) then takes part in sums
-                    const float y = raw[i] < -104.f ? -104.f : raw[i];
-                    x[i] = (double)y * 1.4426950408889634;
-                    if (x[i] > 0.0) grow += x[i];
+                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums
+                    const float y = fminf(fmaxf(raw[i], -104.f), 1e4f);
+                    const float hi = y * 1.44269504f;
+                    const float lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
+                    x[i] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
+                    grow += fmaxf(hi, 0.f);
+                    poison[i] = raw[i] != raw[i] ? raw[i] : 0.f;  // a NaN is kept apart
                 }
-                if (c + 1 < pieces) fetch(c + 1);
+                const bool nan = __any_sync(0xffffffffu, (poison[0] + poison[1]) + (poison[2] + poison[3]) != 0.f);
+                if (c + 2 < pieces) fetch(c + 2);
 #pragma unroll
                 for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
-                double before = x[3];  // over the lanes of a block of 32 tokens (eight)
+                long long before = x[3];  // over the lanes of a block of 32 tokens (eight)
 #pragma unroll
                 for (int o = 1; o < 8; o *= 2) {
-                    const double y = __shfl_up_sync(0xffffffffu, before, o);
+                    const long long y = __shfl_up_sync(0xffffffffu, before, o);
                     if ((lane & 7) >= o) before += y;
                 }
-                const double block = __shfl_sync(0xffffffffu, before, lane | 7);
+                const long long block = __shfl_sync(0xffffffffu, before, lane | 7);
                 before -= x[3];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
-                double blocks[4];
+                long long blocks[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) blocks[b] = __shfl_sync(0xffffffffu, block, b * 8);
-                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
-                PieceGates& g = gates[c & 1];
                 float hi[4], lo[4], col[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const double y = before + x[i];
-                    hi[i] = -(float)y;
-                    lo[i] = -(float)(y + (double)hi[i]);
-                    col[i] = exp2f((float)(block - y));
+                    const long long y = -(before + x[i]);
+                    hi[i] = __ll2float_rn(y);
+                    lo[i] = __ll2float_rn(y - __float2ll_rn(hi[i])) * UNIT;
+                    hi[i] *= UNIT;
+                    col[i] = exp2f(__ll2float_rn(block + y) * UNIT);
                 }
+                float block_nan = 0.f, any_nan = 0.f, blocks_nan[4] = {0.f, 0.f, 0.f, 0.f};
+                if (nan) {  // from its token on, and wherever a sum has it
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) poison[i] += poison[i - 1];
+                    float p = poison[3];
+#pragma unroll
+                    for (int o = 1; o < 8; o *= 2) {
+                        const float y = __shfl_up_sync(0xffffffffu, p, o);
+                        if ((lane & 7) >= o) p += y;
+                    }
+                    block_nan = __shfl_sync(0xffffffffu, p, lane | 7);
+                    p = __shfl_up_sync(0xffffffffu, p, 1);
+                    if ((lane & 7) == 0) p = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) hi[i] += p + poison[i], col[i] += block_nan;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) any_nan += blocks_nan[b] = __shfl_sync(0xffffffffu, block_nan, b * 8);
+                }
+                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                PieceGates& g = gates[c & 1];
                 *reinterpret_cast<float4*>(&g.hi[lane * 4]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<float4*>(&g.lo[lane * 4]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
                 *reinterpret_cast<float4*>(&g.col[lane * 4]) = make_float4(col[0], col[1], col[2], col[3]);
-                const double all = (blocks[0] + blocks[1]) + (blocks[2] + blocks[3]);
-                total += all;
-                if (lane == 0) {
-                    double behind = 0.0;
-#pragma unroll
-                    for (int b = 3; b >= 0; --b) {
-                        g.block[b] = (float)blocks[b];
-                        g.after[b] = exp2f((float)behind);
-                        behind += blocks[b];
-                    }
-                    const bool small = all > -0.7 && all < 0.7;
-                    g.keep = small ? expm1f((float)(all * 0.6931471805599453)) : exp2f((float)all);
+                const long long all = (blocks[0] + blocks[1]) + (blocks[2] + blocks[3]);
+                if (lane < 4) {
+                    const long long behind = (lane < 1 ? blocks[1] : 0) + (lane < 2 ? blocks[2] : 0) + (lane < 3 ? blocks[3] : 0);
+                    const float behind_nan = (lane < 1 ? blocks_nan[1] : 0.f) + (lane < 2 ? blocks_nan[2] : 0.f) +
+                                             (lane < 3 ? blocks_nan[3] : 0.f);
+                    const long long mine = lane == 0 ? blocks[0] : lane == 1 ? blocks[1] : lane == 2 ? blocks[2] : blocks[3];
+                    const float mine_nan = lane == 0   ? blocks_nan[0]
+                                           : lane == 1 ? blocks_nan[1]
+                                           : lane == 2 ? blocks_nan[2]
+                                                       : blocks_nan[3];
+                    g.block[lane] = __ll2float_rn(mine) * UNIT + mine_nan;
+                    g.after[lane] = exp2f(__ll2float_rn(behind) * UNIT) + behind_nan;
+                } else if (lane == 4) {
+                    const float sum = __ll2float_rn(all) * UNIT;
+                    const bool small = sum > -0.7f && sum < 0.7f;
+                    g.keep = (small ? expm1f(sum * 0.693147181f) : exp2f(sum)) + any_nan;
                     g.once = small ? 1.f : 0.f;
-                    g.grow = (float)grow;
+                    g.grow = grow;
+                    g.sum = sum;
                 }
                 arrive_warp(&g_full[c & 1]);
             }
-            if (STATES && ok && lane == 0 && slice == 0) a.sums[((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h] = (float)total;
         }
     }
     if (!ok && lane == 0) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 21) tmem_dealloc_cg<1>(tmem, 512);
+    if (warp == 25) tmem_dealloc_cg<1>(tmem, 512);
 }
 
 template <typename T, int DK, bool STATES>
