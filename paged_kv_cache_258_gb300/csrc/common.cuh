@@ -190,6 +190,13 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return d;
 }
 
+// max(a, b, c) in one instruction
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // ---- warp reductions -------------------------------------------------------------------------
 // Sum N values per lane across aligned groups of 2*O lanes, halving the values kept per lane at
 // each step (a transpose-reduce): after the call, lane L of its group holds the complete sums of

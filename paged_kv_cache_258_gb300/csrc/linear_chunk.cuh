@@ -13,19 +13,19 @@
 //                columns of an earlier block of 32: exp(G_i - R) times exp(R - G_j), R the sum up to the block's end:
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
 //                one for each pair. A thread takes a row's even or odd halves of 32 columns
-//   warps 8-15   V~, in quarters of 32 rows through a ring, four warps on every other one: split into numbers of the type that add up to it (two of
+//   warps 8-15   V~, in quarters of 32 rows one after the other, four warps on every other one: split into numbers of the type that add up to it (two of
 //                fp16: 2^-22 is left; three of bf16: exact), beside one another along N, so that one product of N = 128
 //                or 192 gives their sums and the state keeps fp32's precision
 //   warps 16-19  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
-//   warps 20-23  results: exp(G_i) OI + OA, through shared memory to whole rows
+//   warps 20-23  results: exp(G_i) OI + OA, whole 32-byte sectors of a row from its thread
 //   warp 24      tensor copies of Q, K and V, two pieces ahead
 //   warp 25      issues the products
-//   warps 26, 27 sums of decays (in 64 bits: differences of far sums; held as two fp32 where pairs need them)
+//   warps 26, 27 sums of decays (whole numbers of 64 bits: differences of far sums)
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
-// fp16 cannot hold their range: rows of P', the copy of S and V~ are then brought to 2^14 by a power of two each, which
-// the sums undo in fp32.
+// fp16 cannot hold their range: rows of P' and the copy of S are then brought to 2^14 by a power of two each, which the
+// sums undo in fp32.
 //
 // A piece past the sequence's end: rows of K and V behind it are zeroed in shared memory (another sequence's rows, or
 // nobody's, NaN perhaps). A non-finite v would reach earlier tokens of its piece through 0 x NaN: it is taken
@@ -42,6 +42,9 @@ namespace pkv {
 
 constexpr int kPiece = 128;   // tokens of a piece: the M of a product
 constexpr int kSlice = 64;    // columns of v of a CTA
+// fp16: the second number of a value of V~ is this times what the first lacks of it: at most the value, so it fits, and
+// the two are within 2^-22 of a value, or within 2^-36 where that is more.
+constexpr float kSecond = 2048.f;
 constexpr int kChunkThreads = 7 * 128;
 
 // Pairs of 16-bit numbers in a word.
@@ -75,10 +78,13 @@ struct Pair16<__nv_bfloat16> {
     }
 };
 
-// Pieces of a piece's 128 gates, as the roles need them.
+// A piece's 128 log decays, as the roles need them.
+template <bool LO>
 struct __align__(16) PieceGates {
-    float hi[kPiece], lo[kPiece];  // minus the sum of the log decays from the start of token's block of 32 to it, base 2
-    float col[kPiece];             // 2^(sum to the block's end - sum to the token)
+    float hi[kPiece];              // minus the sum from the start of a token's block of 32 to it, base 2
+    float lo[LO ? kPiece : 4];     // what hi lacks of it (fp16; bf16 weights are coarser than what it changes: with every
+                                   // token of a block forgetting all, 2^-12)
+    float col[kPiece];             // 2^(sum from the token to its block's end)
     float block[4];                // sum over each block
     float after[4];                // 2^(sum over the blocks behind it)
     float keep, once;              // S' = S + (U + S * keep) with 2^(sum over all) - 1 where that is small, once = 1,
@@ -90,7 +96,6 @@ template <typename T, int DK>
 struct ChunkSmem {
     static constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int NT = BF ? 3 : 2;                  // numbers a value of V~ is split into
-    static constexpr int NR = BF ? 3 : 4;                  // quarters of V~ in the ring
     static constexpr uint32_t PANEL = kPiece * 128;        // 64 columns of 128 rows
     static constexpr uint32_t QK = PANEL * (DK / 64);
     static constexpr uint32_t QUARTER = 32 * 128 * NT;     // [NT][32 rows][128 B]
@@ -98,17 +103,17 @@ struct ChunkSmem {
     static constexpr uint32_t K = Q + 2 * QK;
     static constexpr uint32_t V = K + 2 * QK;
     static constexpr uint32_t VT = V + 2 * PANEL;
-    static constexpr uint32_t S = VT + NR * QUARTER;       // [DK rows][128 B]
-    static constexpr uint32_t O = S + DK * 128;            // [4 warps][32 rows][64 B]
-    static constexpr uint32_t GATES = O + 4 * 2048;        // [2]
-    static constexpr uint32_t BAD = GATES + 2 * sizeof(PieceGates);  // int [4][64]: first non-finite v of a column
-    static constexpr uint32_t ROW = BAD + 4 * 64 * 4;      // fp16: float [2][128], 2^-e of P's rows
-    static constexpr uint32_t MISC = ROW + (BF ? 0 : 2 * 128 * 4);  // any_bad[4] s_unit[2] u_unit[2] part[8 + 4]
-    static constexpr uint32_t BARS = MISC + 96;
-    static constexpr int NBARS = 2 + 2 + 2 + 2 + 2 + 2 * NR + 7 + 4;
+    static constexpr uint32_t S = VT + 4 * QUARTER;        // [DK rows][128 B]
+    using Gates = PieceGates<!BF>;
+    static constexpr uint32_t GATES = S + DK * 128;        // [2]
+    static constexpr uint32_t BAD = GATES + 2 * sizeof(Gates);  // bytes [4][64]: first token whose v is not finite
+    static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [2][128], 2^-e of P's rows
+    static constexpr uint32_t MISC = ROW + (BF ? 0 : 2 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
+    static constexpr uint32_t BARS = MISC + 64;
+    static constexpr int NBARS = 5 * 2 + 2 * 4 + 7 + 4;
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
-    static constexpr uint32_t ALLOC = TOTAL + 1024;
+    static constexpr uint32_t ALLOC = TOTAL;               // (on a 1,024-byte boundary: the array is declared so)
     static_assert(ALLOC <= 232448, "shared memory");
     static_assert((VT % 1024) == 0 && (S % 1024) == 0 && (QUARTER % 1024) == 0 && (BARS % 8) == 0, "alignment");
 };
@@ -155,16 +160,39 @@ __device__ __forceinline__ float2 f2_get(uint64_t v) {
     return r;
 }
 
-// mbar_wait_bounded in few instructions: the roles' loops compete for the instruction caches.
+// mbar_wait_bounded in few instructions (28 warps of seven roles share the instruction caches): a thread sleeps up to a
+// microsecond in each try, and gives up after as many as make about a second.
 __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
-    uint64_t begin = 0;
-    while (!mbar_try_wait(bar, parity)) {
-        const uint64_t now = global_timer_ns();
-        if (begin == 0) begin = now;
-        if (now - begin > kWaitLimitNs) return false;
+    const uint32_t addr = smem_addr(bar);
+#pragma unroll 1
+    for (int tries = 1 << 20; tries > 0; --tries) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
     }
-    return true;
+    return false;
 }
+
+// *p = min(*p, x), of bytes in shared memory
+__device__ __forceinline__ void byte_min(uint8_t* p, int x) {
+    uint32_t* word = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+    const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 3) * 8;
+    uint32_t old = *word;
+    while ((int)((old >> shift) & 255u) > x) {
+        const uint32_t seen = atomicCAS(word, old, (old & ~(255u << shift)) | ((uint32_t)x << shift));
+        if (seen == old) break;
+        old = seen;
+    }
+}
+
+// What keeps values of fp16 that gates with sums of positive parts `grow` weigh within fp16: a power of two.
+__device__ __forceinline__ float down_by(float grow) { return ex2_approx(-ceilf(fminf(grow, 100.f))); }
 
 // 2^e, e clamped to what a normal number holds
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
@@ -190,7 +218,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     using L = ChunkSmem<T, DK>;
     using M = Pair16<T>;
     constexpr bool BF = L::BF;
-    constexpr int NT = L::NT, NR = L::NR;
+    constexpr int NT = L::NT;
     constexpr uint32_t PANEL = L::PANEL;
     constexpr uint32_t P_COL = 0, PW_COL = 128, OI_COL = 192, OA_COL = 256, U_COL = 320;
     static_assert(U_COL + 64 * NT <= 512, "tensor memory");
@@ -199,25 +227,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr uint32_t IDESC_U = umma_idesc_f16(BF, 128, kSlice * NT, true) | (1u << 15);  // A = K^T: M-major
     constexpr uint32_t GATE_READERS = STATES ? 12 : 24;  // warps
 
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                           ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_addr(smem);
-    PieceGates* gates = reinterpret_cast<PieceGates*>(smem + L::GATES);
-    int* bad = reinterpret_cast<int*>(smem + L::BAD);
+    using Gates = typename L::Gates;
+    Gates* gates = reinterpret_cast<Gates*>(smem + L::GATES);
+    uint8_t* bad = smem + L::BAD;
     float* row_unit = reinterpret_cast<float*>(smem + L::ROW);
     int* any_bad = reinterpret_cast<int*>(smem + L::MISC);
     float* s_unit = reinterpret_cast<float*>(smem + L::MISC + 16);
-    float* u_unit = reinterpret_cast<float*>(smem + L::MISC + 24);
-    float* part = reinterpret_cast<float*>(smem + L::MISC + 32);  // of V~'s warps, then the state's
+    float* part = reinterpret_cast<float*>(smem + L::MISC + 32);
     uint64_t* qk_full = reinterpret_cast<uint64_t*>(smem + L::BARS);  // [2] Q and K of a piece have landed
     uint64_t* v_full = qk_full + 2;                                   // [2]
     uint64_t* done = v_full + 2;       // [2] every product of a piece is done: its buffers and results
     uint64_t* g_full = done + 2;       // [2] gates
     uint64_t* g_free = g_full + 2;     // [2]
-    uint64_t* vt_full = g_free + 2;    // [NR] a quarter of V~ is written
-    uint64_t* vt_free = vt_full + NR;  // [NR] and read
-    uint64_t* u_full = vt_free + NR;   // U is done
+    uint64_t* vt_full = g_free + 2;    // [4] a quarter of V~ is written
+    uint64_t* vt_free = vt_full + 4;   // [4] and read
+    uint64_t* u_full = vt_free + 4;    // U is done
     uint64_t* u_free = u_full + 1;     // and read
     uint64_t* s_full = u_free + 1;     // the copy of S is written
     uint64_t* s_free = s_full + 1;     // and read
@@ -241,6 +267,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int src = l.src[s], dst = l.dst[s];
     const bool bad_range = q0 < 0 || q1 < q0 || q1 > l.n_tokens || q1 - q0 > l.max_query;
     const bool bad_slot = src >= l.n_slots || dst >= l.n_slots;
+    if ((sbase & 1023u) != 0) {  // (the swizzled tiles need it; never seen)
+        if (threadIdx.x == 0) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
+        return;
+    }
     if (bad_range || bad_slot) {
         if (!STATES && h == 0 && slice == 0 && seg == 0 && threadIdx.x == 0)
             atomicOr(l.status, (bad_range ? (unsigned)PKV_DEV_BAD_QUERY_RANGE : 0u) |
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(&g_full[i], 1);
             mbar_init(&g_free[i], GATE_READERS);
         }
-        for (int i = 0; i < NR; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&vt_full[i], 4);
             mbar_init(&vt_free[i], 1);
         }
@@ -279,7 +309,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(all_done, 1);
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 4 * 64; i += kChunkThreads) bad[i] = kPiece;
+    if (threadIdx.x < 4 * 64) bad[threadIdx.x] = kPiece;
     if (threadIdx.x < 4) any_bad[threadIdx.x] = 0;
     if (warp == 25) tmem_alloc_cg<1>(taddr_s, 512);
     tcgen05_before_sync();
@@ -319,30 +349,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             };
             {  // the blocks behind the row's own stay 0
                 const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll 1
                 for (int b = w4 + 1; b < 4; ++b) put(b, zero);
             }
+#pragma unroll 1
             for (int c = 0; c < pieces; ++c) {
-                const PieceGates& g = gates[c & 1];
+                const Gates& g = gates[c & 1];
                 if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
                 const float mine = -g.hi[row];
-                float mine_lo = -g.lo[row];
+                float mine_lo = BF ? 0.f : -g.lo[row];
                 if (!wait(p_full, c)) { ok = false; break; }
                 tcgen05_after_sync();
                 float shift = 0.f;  // log2 of what the row is multiplied by
                 if constexpr (!BF) {
                     float m0 = 0.f, m1 = 0.f;
 #pragma unroll 1
-                    for (int h16 = 0; h16 < 2 * w4 + 2; ++h16) {
-                        float p[16];
-                        tmem_ld16(lanes + P_COL + h16 * 16, p);
+                    for (int b = 0; b <= w4; ++b) {
+                        uint32_t x[32];
+                        tmem_ld32(lanes + P_COL + b * 32, x);
                         tmem_wait_ld();
-                        if (h16 < 2 * w4) {
+                        const int last = b < w4 ? 31 : lane;
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) m0 = fmaxf(m0, fabsf(p[j])), m1 = fmaxf(m1, fabsf(p[j + 1]));
-                        } else {
-                            const int last = lane - (h16 & 1) * 16;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) m0 = fmaxf(m0, j <= last ? fabsf(p[j]) : 0.f);
+                        for (int j = 0; j < 32; j += 4) {
+                            const float y0 = __uint_as_float(x[j]), y1 = __uint_as_float(x[j + 1]), y2 = __uint_as_float(x[j + 2]),
+                                        y3 = __uint_as_float(x[j + 3]);
+                            m0 = fmax3(m0, j <= last ? fabsf(y0) : 0.f, j + 1 <= last ? fabsf(y1) : 0.f);
+                            m1 = fmax3(m1, j + 2 <= last ? fabsf(y2) : 0.f, j + 3 <= last ? fabsf(y3) : 0.f);
                         }
                     }
                     const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
@@ -359,13 +391,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 {  // the block on the diagonal: an exponential for each pair
                     const uint64_t hi2 = f2_pack(mine, mine), lo2 = f2_pack(mine_lo, mine_lo);
                     const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
-                    const ulonglong2* gl = reinterpret_cast<const ulonglong2*>(&g.lo[w4 * 32 + side]);
+                    const ulonglong2* gl = reinterpret_cast<const ulonglong2*>(BF ? g.lo : &g.lo[w4 * 32 + side]);
                     float x[16];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 y = gh[j], z = gl[j];
-                        const float2 d0 = f2_get(f2_add(f2_add(hi2, y.x), f2_add(lo2, z.x)));
-                        const float2 d1 = f2_get(f2_add(f2_add(hi2, y.y), f2_add(lo2, z.y)));
+                        const ulonglong2 y = gh[j];
+                        uint64_t e0 = f2_add(hi2, y.x), e1 = f2_add(hi2, y.y);
+                        if constexpr (!BF) {
+                            const ulonglong2 z = gl[j];
+                            e0 = f2_add(e0, f2_add(lo2, z.x)), e1 = f2_add(e1, f2_add(lo2, z.y));
+                        }
+                        const float2 d0 = f2_get(e0), d1 = f2_get(e1);
                         x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
                         x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
                     }
@@ -414,15 +450,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // which four 16-byte units of its row: two threads' rows share the banks of half a row otherwise
         const int u0 = (tid & 3) + 4 * (r & 1);
         const uint32_t at[2] = {(uint32_t)((u0 ^ (r & 7)) << 4), (uint32_t)((u0 ^ 4 ^ (r & 7)) << 4)};
+#pragma unroll 1
         for (int c = 0; c < pieces; ++c) {
             const int st = c & 1;
             const int n = min(kPiece, tokens - c * kPiece);
             unsigned char* v = smem + L::V + st * PANEL;
-            const PieceGates& g = gates[st];
+            const Gates& g = gates[st];
             if (!wait(&g_full[st], c >> 1) || !wait(&v_full[st], c >> 1)) { ok = false; break; }
             if (n < kPiece) {  // rows behind the sequence's end
                 if (!wait(&qk_full[st], c >> 1)) { ok = false; break; }
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
                 for (int i = n * 8 + tid; i < kPiece * 8; i += 256) {
                     *reinterpret_cast<uint4*>(v + i * 16) = zero;
 #pragma unroll
@@ -432,47 +470,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fence_proxy_async_smem();
                 if (!meet(0)) { ok = false; break; }
             }
-            float unit = 1.f;
-            if constexpr (!BF) {  // the largest of V~, to bring it to 2^14
-                float most = 0.f;
-#pragma unroll 1
-                for (int q = half; q < 4; q += 2) {
-                    __half2 m = __float2half2_rn(0.f);
-                    uint4 x[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        x[k] = *reinterpret_cast<const uint4*>(v + (q * 32 + r) * 128 + at[k]);
-                        const __half2* y = reinterpret_cast<const __half2*>(&x[k]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(y[j]));
-                    }
-                    float top = fmaxf(__low2float(m), __high2float(m));
-                    if (top > 65504.f) {  // an infinity: the largest of the others
-                        top = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float y[8];
-                            Vec16<T>::to_float(x[k], y);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]) <= 65504.f ? fabsf(y[j]) : 0.f);
-                        }
-                    }
-                    most = fmaxf(most, top * (g.col[q * 32 + r] * g.after[q]));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                if (lane == 0) part[warp - 8] = most;
-                if (!meet(0)) { ok = false; break; }
-                const float4 p0 = *reinterpret_cast<const float4*>(part), p1 = *reinterpret_cast<const float4*>(part + 4);
-                const int e = exponent14(fmaxf(fmaxf(fmaxf(p0.x, p0.y), fmaxf(p0.z, p0.w)), fmaxf(fmaxf(p1.x, p1.y), fmaxf(p1.z, p1.w))));
-                unit = pow2i(14 - e);
-                // (read for the piece before the last one: that piece's gates have been released by the state's warps)
-                if (tid == 0) u_unit[st] = pow2i(e - 14);
-                if (!meet(0)) { ok = false; break; }  // part may be written again
-            }
+            const float unit = BF ? 1.f : down_by(g.grow);
 #pragma unroll 1
             for (int q = half; q < 4; q += 2) {
-                const int turn = (c * 4 + q) / NR, slot = c * 4 + q - turn * NR;
                 const int row = q * 32 + r;
                 unsigned char* from = v + row * 128;
                 uint4 x[2];
@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
                 const float f = g.col[row] * g.after[q] * unit;
                 const uint64_t f2 = f2_pack(f, f);
-                if (turn > 0 && !wait(&vt_free[slot], turn - 1)) { ok = false; break; }
-                unsigned char* to = smem + L::VT + slot * L::QUARTER + r * 128;
+                if (c > 0 && !wait(&vt_free[q], c - 1)) { ok = false; break; }
+                unsigned char* to = smem + L::VT + q * L::QUARTER + r * 128;
                 uint32_t probe = 0;  // 0 x v, summed: not 0 if one is not finite
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             } else {
                                 w[term][j] = M::pack(y.x, y.y);
                                 const float2 z = M::unpack(w[term][j]);
-                                if (term + 1 < NT) y2 = f2_add(y2, f2_pack(-z.x, -z.y));
+                                if (term + 1 < NT) y2 = f2_mul(f2_add(y2, f2_pack(-z.x, -z.y)), f2_pack(kSecond, kSecond));
                             }
                         }
                     }
@@ -516,16 +516,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
                     for (int k = 0; k < 2; ++k) {
                         T* y = reinterpret_cast<T*>(from + at[k]);
+#pragma unroll 1
                         for (int j = 0; j < 8; ++j)
                             if (!(fabsf(static_cast<float>(y[j])) <= 3.4028234e38f)) {
                                 y[j] = from_float<T>(0.f);
-                                atomicMin(&bad[(c & 3) * 64 + (u0 ^ (k * 4)) * 8 + j], row);
+                                byte_min(&bad[(c & 3) * 64 + (u0 ^ (k * 4)) * 8 + j], row);
                                 any_bad[c & 3] = 1;
                             }
                     }
                 }
                 fence_proxy_async_smem();
-                arrive_warp(&vt_full[slot]);
+                arrive_warp(&vt_full[q]);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&g_free[st]);
@@ -540,14 +541,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)((warp - 16) * 32) << 16);
         const size_t at = (size_t)row * a.dv + slice * kSlice + c0;  // in a head's state
         uint64_t x[NC / 2];  // pairs of columns
-        auto load = [&](const float* from, bool add, float keep) {
+        auto load = [&](const float* from, float keep) {
             const uint64_t k2 = f2_pack(keep, keep);
 #pragma unroll
             for (int i = 0; i < NC / 2; i += 2) {
                 const float4 y = *reinterpret_cast<const float4*>(from + at + 2 * i);
-                const uint64_t y0 = f2_pack(y.x, y.y), y1 = f2_pack(y.z, y.w);
-                x[i] = add ? f2_fma(x[i], k2, y0) : y0;
-                x[i + 1] = add ? f2_fma(x[i + 1], k2, y1) : y1;
+                x[i] = f2_fma(x[i], k2, f2_pack(y.x, y.y));
+                x[i + 1] = f2_fma(x[i + 1], k2, f2_pack(y.z, y.w));
             }
         };
         auto save = [&](float* to) {
@@ -559,40 +559,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         };
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i) x[i] = 0;
-        if (seg == 0) {
-            // shared out, the second pass reads the start from where the first left it: its last segment writes dst
-            if (!STATES && used_segs > 1)
-                load(a.start + ((size_t)s * l.n_v + h) * head, false, 0.f);
-            else if (src >= 0)
-                load(l.state + ((size_t)src * l.n_v + h) * head, false, 0.f);
-            if (STATES) save(a.start + ((size_t)s * l.n_v + h) * head);
-        } else if (!STATES) {
-            for (int i = 0; i < seg; ++i) {
+        {
+            // shared out, the second pass reads the start from where the first left it (its last segment writes dst), or
+            // adds up what the segments before leave
+            const size_t mine = (size_t)s * l.n_v + h;
+            const bool from_state = STATES || used_segs == 1;
+            const int n = seg > 0 ? (STATES ? 0 : seg) : !from_state || src >= 0;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
                 const size_t to = ((size_t)s * (a.n_segs - 1) + i) * l.n_v + h;
-                load(a.added + to * head, i > 0, i > 0 ? exp2f(a.sums[to]) : 0.f);
+                load(seg > 0      ? a.added + to * head
+                     : from_state ? l.state + ((size_t)src * l.n_v + h) * head
+                                  : a.start + mine * head,
+                     i > 0 ? exp2f(a.sums[to]) : 0.f);
             }
+            if (STATES && seg == 0) save(a.start + mine * head);
         }
         float sum = 0.f;
+#pragma unroll 1
         for (int c = 0; c < pieces; ++c) {
             if constexpr (!STATES) {  // the copy that Q meets
                 uint64_t unit2 = 0;
                 float back_s = 1.f;
                 if constexpr (!BF) {
-                    float most = 0.f, other = 0.f;
+                    float most = 0.f;
 #pragma unroll
                     for (int i = 0; i < NC / 2; ++i) {
                         const float2 y = f2_get(x[i]);
-                        most = fmaxf(most, fabsf(y.x)), other = fmaxf(other, fabsf(y.y));
+                        most = fmax3(most, fabsf(y.x), fabsf(y.y));
                     }
-                    most = fmaxf(most, other);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    if (lane == 0) part[8 + warp - 16] = most;
+                    float* mine = part + (c & 1) * 4;  // (read for piece c by all before any of them meets for c + 1)
+                    if (lane == 0) mine[warp - 16] = most;
                     if (!meet(1)) { ok = false; break; }
-                    const int e = exponent14(fmaxf(fmaxf(part[8], part[9]), fmaxf(part[10], part[11])));
+                    const int e = exponent14(fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3])));
                     unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
                     back_s = pow2i(e - 14);
-                    if (!meet(1)) { ok = false; break; }  // part may be written again
                 }
                 if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
                 // (Q S of the piece before is done: it began when the results of the one before that had been read)
@@ -611,13 +614,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fence_proxy_async_smem();
                 arrive_warp(s_full);
             }
-            const PieceGates& g = gates[c & 1];
+            const Gates& g = gates[c & 1];
             if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
+            const float unit_v = BF ? 1.f : down_by(g.grow);
             const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
             if (STATES) sum += g.sum;
             if (!wait(u_full, c)) { ok = false; break; }
             tcgen05_after_sync();
-            const float back = BF ? 1.f : u_unit[c & 1];
+            const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
 #pragma unroll
             for (int i = 0; i < NC / 2; i += 8) {
                 float u[NT][16];
@@ -627,9 +631,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint64_t y = f2_pack(u[NT - 1][2 * j], u[NT - 1][2 * j + 1]);
+                    if constexpr (BF) {
 #pragma unroll
-                    for (int term = NT - 2; term >= 0; --term) y = f2_add(y, f2_pack(u[term][2 * j], u[term][2 * j + 1]));
-                    if (!BF) y = f2_mul(y, f2_pack(back, back));
+                        for (int term = NT - 2; term >= 0; --term) y = f2_add(y, f2_pack(u[term][2 * j], u[term][2 * j + 1]));
+                    } else {
+                        y = f2_fma(f2_pack(u[0][2 * j], u[0][2 * j + 1]), f2_pack(back, back), f2_mul(y, f2_pack(back2, back2)));
+                    }
                     x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
                 }
             }
@@ -652,20 +659,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int w4 = warp - 20;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-            // 64 bytes of each of the warp's 32 rows are staged at a time: unit u of row r at u ^ (r / 2 & 3), so that
-            // eight rows' units lie in different banks; a store then takes eight rows, four lanes a row
-            unsigned char* stage = smem + L::O + w4 * 2048;
-            const uint32_t swz = (lane >> 1) & 3;
-            const int out_row = w4 * 32 + (lane >> 2);
-            const uint32_t from = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
             const size_t pitch = (size_t)l.n_v * a.dv * sizeof(T);
-            char* out = static_cast<char*>(l.out) + (size_t)(t0 + out_row) * pitch +
-                        ((size_t)h * a.dv + slice * kSlice + (lane & 3) * 8) * sizeof(T);
+            char* out = static_cast<char*>(l.out) + (size_t)(t0 + row) * pitch + ((size_t)h * a.dv + slice * kSlice) * sizeof(T);
+            const bool sectors = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0;
+#pragma unroll 1
             for (int c = 0; c < pieces; ++c) {
                 const int n = min(kPiece, tokens - c * kPiece);
-                const PieceGates& g = gates[c & 1];
+                const Gates& g = gates[c & 1];
                 if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
                 float sum = -g.hi[row];
+#pragma unroll 1
                 for (int i = 0; i < w4; ++i) sum += g.block[i];
                 arrive_warp(&g_free[c & 1]);
                 float fi = ex2_approx(sum) * l.scale, fa = l.scale;
@@ -690,26 +693,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         w[j / 2] = M::pack(z.x, z.y);
                     }
                     if (poisoned) {
-                        const int* mark = &bad[(c & 3) * 64 + c0];
+                        const uint8_t* mark = &bad[(c & 3) * 64 + c0];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             if (mark[j] <= row) w[j / 2] |= 0x7fffu << (16 * (j & 1));
                     }
-                    const int u = (c0 >> 3) & 2;
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + (((u + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-                    if (c0 & 16) {
-                        if (c0 + 16 == kSlice) {
-                            tcgen05_before_sync();
-                            arrive_warp(o_free);
+                    if (c0 + 16 == kSlice) {
+                        tcgen05_before_sync();
+                        arrive_warp(o_free);
+                    }
+                    if (row < n) {
+                        char* to = out + c0 * sizeof(T);
+                        if (sectors) {
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
+                                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                         : "memory");
                         } else {
-                            __syncwarp();
+                            reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
-                        char* to = out + (size_t)(c0 - 16) * sizeof(T);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k, to += 8 * pitch)
-                            if (out_row + k * 8 < n) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(stage + from + k * 512);
-                        __syncwarp();
                     }
                 }
                 out += kPiece * pitch;
@@ -726,18 +728,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // ===================== tensor copies =====================
             if (lane == 0) {
                 int issued = 0;
+#pragma unroll 1
                 for (int c = 0; c < pieces; ++c) {
                     const int st = c & 1;
                     if (c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
                     const int y = t0 + c * kPiece;
+                    // (V first: its warps are the furthest ahead)
+                    mbar_arrive_expect_tx(&v_full[st], PANEL);
+                    tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
                     mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
 #pragma unroll
                     for (int p = 0; p < DK / 64; ++p) {
                         if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
                         tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
                     }
-                    mbar_arrive_expect_tx(&v_full[st], PANEL);
-                    tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
                     issued = c + 1;
                 }
                 // no copy is in flight when the CTA leaves
@@ -748,7 +752,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
         } else if (warp == 25) {
-            // ===================== products: one thread =====================
+            // ===================== products: one thread (an instruction takes the tensor core 50 to 100 cycles: short
+            // code counts more than unrolled loops) =====================
             if (elect_one()) {
                 const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
                 const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
@@ -760,9 +765,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 auto pairs = [&](uint32_t st) {  // P = Q K^T
                     const uint64_t q = dq + ((st * L::QK) >> 4), k = dk + ((st * L::QK) >> 4);
                     tcgen05_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < DK / 16; ++i) {
-                        const uint32_t off = (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4);
+                        const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
                         umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
                     }
                     umma_commit_cg<1>(p_full);
@@ -771,7 +776,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     ok = wait1(&qk_full[0], 0);
                     if (ok) pairs(0);
                 }
-                int slot = 0, turn = 0;  // of V~'s ring
+#pragma unroll 1
                 for (int c = 0; c < pieces && ok; ++c) {
                     const uint32_t st = (uint32_t)(c & 1);
                     // U = K^T V~ (V~'s warps have seen V land; K has landed where P was computed)
@@ -779,13 +784,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const uint64_t kt = dkt + ((st * L::QK) >> 4);
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        if (!wait1(&vt_full[slot], turn)) { ok = false; break; }
+                        if (!wait1(&vt_full[q], c)) { ok = false; break; }
                         tcgen05_after_sync();
-                        const uint64_t vt = dvt + (((uint32_t)slot * L::QUARTER) >> 4), k0 = kt + (uint32_t)q * (4096 >> 4);
+                        const uint64_t vt = dvt + (((uint32_t)q * L::QUARTER) >> 4), k0 = kt + (uint32_t)q * (4096 >> 4);
                         umma_f16_cg<1>(tmem + U_COL, k0, vt, IDESC_U, q > 0);
                         umma_f16_cg<1>(tmem + U_COL, k0 + (2048 >> 4), vt + (2048 >> 4), IDESC_U, true);
-                        umma_commit_cg<1>(&vt_free[slot]);
-                        if (++slot == NR) slot = 0, ++turn;
+                        umma_commit_cg<1>(&vt_free[q]);
                     }
                     if (!ok) break;
                     umma_commit_cg<1>(u_full);
@@ -796,7 +800,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
                         tcgen05_after_sync();
                         const uint64_t q = dq + ((st * L::QK) >> 4);
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < DK / 16; ++i)
                             umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
                                            ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
@@ -809,7 +813,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         // OA = P' V
                         tcgen05_after_sync();
                         const uint64_t v = dv + ((st * PANEL) >> 4);
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < kPiece / 16; ++i)
                             umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + i * 8, v + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
                         umma_commit_cg<1>(&done[st]);
@@ -822,97 +826,69 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
         } else {
-            // ===================== sums of the log decays: lane = 4 tokens, a warp for every other piece =====================
+            // ===================== sums of the log decays: lane = token of a block, a warp for every other piece =====================
             // Whole numbers of 2^-40 (in 64 bits): sums and differences are exact, and 64-bit floats too slow here.
             constexpr float UNIT = 1.0f / 1099511627776.0f;
-            float raw[4];
-            auto fetch = [&](int c) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = c * kPiece + lane * 4 + i;
-                    raw[i] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
-                }
-            };
             const int odd = warp - 26;
-            if (odd < pieces) fetch(odd);
+            auto fetch = [&](int t) -> float {  // t: within the segment
+                return l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
+            };
+            float next = fetch(odd * kPiece + lane), next2 = fetch(odd * kPiece + 32 + lane);
+#pragma unroll 1
             for (int c = odd; c < pieces; c += 2) {
-                long long x[4];
-                float poison[4], grow = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums
-                    const float y = fminf(fmaxf(raw[i], -104.f), 1e4f);
-                    const float hi = y * 1.44269504f;
-                    const float lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
-                    x[i] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
-                    grow += fmaxf(hi, 0.f);
-                    poison[i] = raw[i] != raw[i] ? raw[i] : 0.f;  // a NaN is kept apart
-                }
-                const bool nan = __any_sync(0xffffffffu, (poison[0] + poison[1]) + (poison[2] + poison[3]) != 0.f);
-                if (c + 2 < pieces) fetch(c + 2);
-#pragma unroll
-                for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
-                long long before = x[3];  // over the lanes of a block of 32 tokens (eight)
-#pragma unroll
-                for (int o = 1; o < 8; o *= 2) {
-                    const long long y = __shfl_up_sync(0xffffffffu, before, o);
-                    if ((lane & 7) >= o) before += y;
-                }
-                const long long block = __shfl_sync(0xffffffffu, before, lane | 7);
-                before -= x[3];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
-                long long blocks[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) blocks[b] = __shfl_sync(0xffffffffu, block, b * 8);
-                float hi[4], lo[4], col[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long y = -(before + x[i]);
-                    hi[i] = __ll2float_rn(y);
-                    lo[i] = __ll2float_rn(y - __float2ll_rn(hi[i])) * UNIT;
-                    hi[i] *= UNIT;
-                    col[i] = exp2f(__ll2float_rn(block + y) * UNIT);
-                }
-                float block_nan = 0.f, any_nan = 0.f, blocks_nan[4] = {0.f, 0.f, 0.f, 0.f};
-                if (nan) {  // from its token on, and wherever a sum has it
-#pragma unroll
-                    for (int i = 1; i < 4; ++i) poison[i] += poison[i - 1];
-                    float p = poison[3];
-#pragma unroll
-                    for (int o = 1; o < 8; o *= 2) {
-                        const float y = __shfl_up_sync(0xffffffffu, p, o);
-                        if ((lane & 7) >= o) p += y;
-                    }
-                    block_nan = __shfl_sync(0xffffffffu, p, lane | 7);
-                    p = __shfl_up_sync(0xffffffffu, p, 1);
-                    if ((lane & 7) == 0) p = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) hi[i] += p + poison[i], col[i] += block_nan;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) any_nan += blocks_nan[b] = __shfl_sync(0xffffffffu, block_nan, b * 8);
-                }
                 if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
-                PieceGates& g = gates[c & 1];
-                *reinterpret_cast<float4*>(&g.hi[lane * 4]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<float4*>(&g.lo[lane * 4]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-                *reinterpret_cast<float4*>(&g.col[lane * 4]) = make_float4(col[0], col[1], col[2], col[3]);
-                const long long all = (blocks[0] + blocks[1]) + (blocks[2] + blocks[3]);
+                Gates& g = gates[c & 1];
+                long long total = 0;      // lane b: of block b
+                float grow = 0.f;
+                unsigned nans = 0;        // bit b: a NaN in block b
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    const float raw = next;
+                    next = next2;
+                    next2 = fetch(b < 2 ? c * kPiece + (b + 2) * 32 + lane : (c + 2) * kPiece + (b - 2) * 32 + lane);
+                    const unsigned nan = __ballot_sync(0xffffffffu, raw != raw);
+                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums
+                    const float y = fminf(fmaxf(raw, -104.f), 1e4f);
+                    const float yh = y * 1.44269504f;
+                    const float yl = fmaf(y, 1.44269504f, -yh) + y * 1.92596299e-8f;
+                    long long x = __float2ll_rn(yh * 1099511627776.0f) + __float2ll_rn(yl * 1099511627776.0f);
+                    grow += fmaxf(yh, 0.f);
+#pragma unroll 1
+                    for (int o = 1; o < 32; o *= 2) {
+                        const long long z = __shfl_up_sync(0xffffffffu, x, o);
+                        if (lane >= o) x += z;
+                    }
+                    const long long all = __shfl_sync(0xffffffffu, x, 31);
+                    if (lane == b) total = all;
+                    const float hi = __ll2float_rn(-x);
+                    float to_end = ex2_approx(__ll2float_rn(all - x) * UNIT);
+                    float hi_out = hi * UNIT;
+                    if (nan) {  // from its token on, and in every sum that has it
+                        nans |= 1u << b;
+                        to_end = __int_as_float(0x7fffffff);
+                        if (nan & (0xffffffffu >> (31 - lane))) hi_out = to_end;
+                    }
+                    g.hi[b * 32 + lane] = hi_out;
+                    if constexpr (!BF) g.lo[b * 32 + lane] = __ll2float_rn(-x - __float2ll_rn(hi)) * UNIT;
+                    g.col[b * 32 + lane] = to_end;
+                }
+                if (__any_sync(0xffffffffu, grow != 0.f)) {
+#pragma unroll 1
+                    for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
+                }
+                long long behind = total;  // lanes 0-3: over the lane's block and those behind it
+                if (lane > 3) behind = 0;
+#pragma unroll
+                for (int o = 1; o < 4; o *= 2) behind += __shfl_down_sync(0xffffffffu, behind, o);
+                const float nan_b = __int_as_float(0x7fffffff);
                 if (lane < 4) {
-                    const long long behind = (lane < 1 ? blocks[1] : 0) + (lane < 2 ? blocks[2] : 0) + (lane < 3 ? blocks[3] : 0);
-                    const float behind_nan = (lane < 1 ? blocks_nan[1] : 0.f) + (lane < 2 ? blocks_nan[2] : 0.f) +
-                                             (lane < 3 ? blocks_nan[3] : 0.f);
-                    const long long mine = lane == 0 ? blocks[0] : lane == 1 ? blocks[1] : lane == 2 ? blocks[2] : blocks[3];
-                    const float mine_nan = lane == 0   ? blocks_nan[0]
-                                           : lane == 1 ? blocks_nan[1]
-                                           : lane == 2 ? blocks_nan[2]
-                                                       : blocks_nan[3];
-                    g.block[lane] = __ll2float_rn(mine) * UNIT + mine_nan;
-                    g.after[lane] = exp2f(__ll2float_rn(behind) * UNIT) + behind_nan;
-                } else if (lane == 4) {
-                    const float sum = __ll2float_rn(all) * UNIT;
+                    g.block[lane] = nans >> lane & 1 ? nan_b : __ll2float_rn(total) * UNIT;
+                    g.after[lane] = nans >> lane >> 1 ? nan_b : ex2_approx(__ll2float_rn(behind - total) * UNIT);
+                }
+                if (lane == 0) {
+                    const float sum = __ll2float_rn(behind) * UNIT;
                     const bool small = sum > -0.7f && sum < 0.7f;
-                    g.keep = (small ? expm1f(sum * 0.693147181f) : exp2f(sum)) + any_nan;
+                    g.keep = nans ? nan_b : small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
                     g.once = small ? 1.f : 0.f;
                     g.grow = grow;
                     g.sum = sum;

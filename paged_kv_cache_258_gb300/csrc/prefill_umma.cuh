@@ -80,13 +80,6 @@ __device__ __forceinline__ void tma_load_3d_keep(uint32_t dst, const void* tmap,
         : "memory");
 }
 
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Weights of one row of a tile: p = 2^(s * sl - msub) (ex2.approx; a masked score, -inf, gives
 // exactly 0), packed to the storage type in pw, their fp32 sums accumulated in ls (8 partial sums).
 // The scale-and-subtract and the sums run as .f32x2 instructions: the softmax thread is bound by
