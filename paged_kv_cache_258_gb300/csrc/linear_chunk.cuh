@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const float unit_v = BF ? 1.f : down_by(g.grow);
             const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
             if (STATES) sum += g.sum;
+            arrive_warp(&g_free[c & 1]);
             if (!wait(u_full, c)) { ok = false; break; }
             tcgen05_after_sync();
             const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
@@ -642,7 +643,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             tcgen05_before_sync();
             arrive_warp(u_free);
-            if (lane == 0) mbar_arrive(&g_free[c & 1]);
         }
         if (ok) {
             if (STATES) {
@@ -661,19 +661,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
             const size_t pitch = (size_t)l.n_v * a.dv * sizeof(T);
             char* out = static_cast<char*>(l.out) + (size_t)(t0 + row) * pitch + ((size_t)h * a.dv + slice * kSlice) * sizeof(T);
-            const bool sectors = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0;
-#pragma unroll 1
-            for (int c = 0; c < pieces; ++c) {
-                const int n = min(kPiece, tokens - c * kPiece);
+            float sum = 0.f;  // of the log decays up to the row
+            auto decays = [&](int c) -> bool {
+                if (!wait(&g_full[c & 1], c >> 1)) return false;
                 const Gates& g = gates[c & 1];
-                if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-                float sum = -g.hi[row];
+                sum = -g.hi[row];
 #pragma unroll 1
                 for (int i = 0; i < w4; ++i) sum += g.block[i];
                 arrive_warp(&g_free[c & 1]);
-                float fi = ex2_approx(sum) * l.scale, fa = l.scale;
+                return true;
+            };
+            if (pieces > 0) ok = decays(0);
+            const bool sectors = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0;
+#pragma unroll 1
+            for (int c = 0; c < pieces && ok; ++c) {
+                const int n = min(kPiece, tokens - c * kPiece);
                 if (!wait(&done[c & 1], c >> 1)) { ok = false; break; }
                 tcgen05_after_sync();
+                float fi = ex2_approx(sum) * l.scale, fa = l.scale;
+                if (c + 1 < pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
                 if constexpr (!BF) {
                     fi *= s_unit[c & 1];
                     fa *= row_unit[(c & 1) * kPiece + row];
@@ -833,7 +839,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             auto fetch = [&](int t) -> float {  // t: within the segment
                 return l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
             };
-            float next = fetch(odd * kPiece + lane), next2 = fetch(odd * kPiece + 32 + lane);
+            // a whole piece's loads are in flight, the warp's next piece's
+            float n0 = fetch(odd * kPiece + lane), n1 = fetch(odd * kPiece + 32 + lane), n2 = fetch(odd * kPiece + 64 + lane),
+                  n3 = fetch(odd * kPiece + 96 + lane);
 #pragma unroll 1
             for (int c = odd; c < pieces; c += 2) {
                 if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
@@ -843,9 +851,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 unsigned nans = 0;        // bit b: a NaN in block b
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
-                    const float raw = next;
-                    next = next2;
-                    next2 = fetch(b < 2 ? c * kPiece + (b + 2) * 32 + lane : (c + 2) * kPiece + (b - 2) * 32 + lane);
+                    const float raw = n0;
+                    n0 = n1, n1 = n2, n2 = n3;
+                    n3 = fetch((c + 2) * kPiece + b * 32 + lane);
                     const unsigned nan = __ballot_sync(0xffffffffu, raw != raw);
                     // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums
                     const float y = fminf(fmaxf(raw, -104.f), 1e4f);
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const float yl = fmaf(y, 1.44269504f, -yh) + y * 1.92596299e-8f;
                     long long x = __float2ll_rn(yh * 1099511627776.0f) + __float2ll_rn(yl * 1099511627776.0f);
                     grow += fmaxf(yh, 0.f);
-#pragma unroll 1
+#pragma unroll
                     for (int o = 1; o < 32; o *= 2) {
                         const long long z = __shfl_up_sync(0xffffffffu, x, o);
                         if (lane >= o) x += z;
