@@ -14,14 +14,15 @@
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
 //                one for each pair. A thread takes a row's even or odd halves of 32 columns
 //   warps 8-15   V~, in quarters of 32 rows one after the other, four warps on every other one: split into numbers of the type that add up to it (two of
-//                fp16: 2^-22 is left; three of bf16: exact), beside one another along N, so that one product of N = 128
-//                or 192 gives their sums and the state keeps fp32's precision
+//                fp16: 2^-22 is left; three of bf16: exact), two beside one another along N, so that one product of
+//                N = 128 gives both sums (the third is added to the second's), and the state keeps fp32's precision
 //   warps 16-19  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
 //   warps 20-23  results: exp(G_i) OI + OA, whole 32-byte sectors of a row from its thread
 //   warp 24      tensor copies of Q, K and V, two pieces ahead
-//   warp 25      issues the products
-//   warps 26, 27 sums of decays (whole numbers of 64 bits: differences of far sums)
+//   warps 25, 26 issue the products: P, OI and OA, and U: a thread's waits (some 150 cycles each here, met or not) then
+//                leave the tensor cores to the other's products
+//   warp 27      sums of decays 
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
 // fp16 cannot hold their range: rows of P' and the copy of S are then brought to 2^14 by a power of two each, which the
@@ -79,12 +80,9 @@ struct Pair16<__nv_bfloat16> {
 };
 
 // A piece's 128 log decays, as the roles need them.
-template <bool LO>
 struct __align__(16) PieceGates {
     float hi[kPiece];              // minus the sum from the start of a token's block of 32 to it, base 2
-    float lo[LO ? kPiece : 4];     // what hi lacks of it (fp16; bf16 weights are coarser than what it changes: with every
-                                   // token of a block forgetting all, 2^-12)
-    float col[kPiece];             // 2^(sum from the token to its block's end)
+    float col[kPiece];             // 2^(sum from behind the token to its block's end)
     float block[4];                // sum over each block
     float after[4];                // 2^(sum over the blocks behind it)
     float keep, once;              // S' = S + (U + S * keep) with 2^(sum over all) - 1 where that is small, once = 1,
@@ -104,13 +102,13 @@ struct ChunkSmem {
     static constexpr uint32_t V = K + 2 * QK;
     static constexpr uint32_t VT = V + 2 * PANEL;
     static constexpr uint32_t S = VT + 4 * QUARTER;        // [DK rows][128 B]
-    using Gates = PieceGates<!BF>;
+    using Gates = PieceGates;
     static constexpr uint32_t GATES = S + DK * 128;        // [2]
     static constexpr uint32_t BAD = GATES + 2 * sizeof(Gates);  // bytes [4][64]: first token whose v is not finite
-    static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [2][128], 2^-e of P's rows
-    static constexpr uint32_t MISC = ROW + (BF ? 0 : 2 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
+    static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [4][128], 2^-e of P's rows
+    static constexpr uint32_t MISC = ROW + (BF ? 0 : 4 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
     static constexpr uint32_t BARS = MISC + 64;
-    static constexpr int NBARS = 5 * 2 + 2 * 4 + 7 + 4;
+    static constexpr int NBARS = 8 * 2 + 2 * 4 + 7 + 3 + 2;
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
     static constexpr uint32_t ALLOC = TOTAL;               // (on a 1,024-byte boundary: the array is declared so)
@@ -138,7 +136,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // Every thread of the four warps: registers a thread from here on. The kernel's 72 a thread are shared out anew, as
-// 64 + 64 + 64 + 64 + 136 + 64 + 48 = 7 * 72.
+// 64 + 64 + 56 + 56 + 112 + 96 + 56 = 7 * 72.
 template <int N>
 __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -220,11 +218,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr bool BF = L::BF;
     constexpr int NT = L::NT;
     constexpr uint32_t PANEL = L::PANEL;
-    constexpr uint32_t P_COL = 0, PW_COL = 128, OI_COL = 192, OA_COL = 256, U_COL = 320;
-    static_assert(U_COL + 64 * NT <= 512, "tensor memory");
+    constexpr uint32_t P_COL = 0, PW_COL = 128, OI_COL = 256, OA_COL = 320, U_COL = 384;  // (all 512 columns)
     constexpr uint32_t IDESC_P = umma_idesc_f16(BF, 128, kPiece, false);
     constexpr uint32_t IDESC_O = umma_idesc_f16(BF, 128, kSlice, true);
-    constexpr uint32_t IDESC_U = umma_idesc_f16(BF, 128, kSlice * NT, true) | (1u << 15);  // A = K^T: M-major
+    constexpr uint32_t IDESC_U = umma_idesc_f16(BF, 128, kSlice * 2, true) | (1u << 15);  // A = K^T: M-major
+    constexpr uint32_t IDESC_U3 = umma_idesc_f16(BF, 128, kSlice, true) | (1u << 15);     // bf16's third numbers
     constexpr uint32_t GATE_READERS = STATES ? 12 : 24;  // warps
 
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -238,8 +236,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float* part = reinterpret_cast<float*>(smem + L::MISC + 32);
     uint64_t* qk_full = reinterpret_cast<uint64_t*>(smem + L::BARS);  // [2] Q and K of a piece have landed
     uint64_t* v_full = qk_full + 2;                                   // [2]
-    uint64_t* done = v_full + 2;       // [2] every product of a piece is done: its buffers and results
-    uint64_t* g_full = done + 2;       // [2] gates
+    uint64_t* done = v_full + 2;       // [2] P, OI and OA of a piece are done: V, P' and results
+    uint64_t* q_free = done + 2;       // [2] P and OI are
+    uint64_t* k_free = q_free + 2;     // [2] U is
+    uint64_t* v_clean = k_free + 2;    // [2] V's warps are through with a piece of V
+    uint64_t* g_full = v_clean + 2;       // [2] gates
     uint64_t* g_free = g_full + 2;     // [2]
     uint64_t* vt_full = g_free + 2;    // [4] a quarter of V~ is written
     uint64_t* vt_free = vt_full + 4;   // [4] and read
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* w_full = p_full + 1;     // P' is written (and P read)
     uint64_t* o_free = w_full + 1;     // OI and OA are read
     uint64_t* role = o_free + 1;       // [3] the warps of a role meet
-    uint64_t* all_done = role + 3;     // every product issued is done
+    uint64_t* all_done = role + 3;     // [2] every product a thread issued is done
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
     const LinearArgs& l = a.l;
@@ -291,6 +292,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(&qk_full[i], 1);
             mbar_init(&v_full[i], 1);
             mbar_init(&done[i], 1);
+            mbar_init(&q_free[i], 1);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_clean[i], 8);
+            mbar_init(&all_done[i], 1);
             mbar_init(&g_full[i], 1);
             mbar_init(&g_free[i], GATE_READERS);
         }
@@ -306,7 +311,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(w_full, 8);
         mbar_init(o_free, 4);
         for (int i = 0; i < 3; ++i) mbar_init(&role[i], i == 0 ? 8 : 4);
-        mbar_init(all_done, 1);
         fence_mbar_init();
     }
     if (threadIdx.x < 4 * 64) bad[threadIdx.x] = kPiece;
@@ -337,7 +341,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int w4 = warp & 3, side = (warp >> 2) * 16;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-            const uint32_t from_col = lanes + P_COL + side, to_col = lanes + PW_COL + side / 2;
+            const uint32_t from_col = lanes + P_COL + side;
+            uint32_t to_col = lanes + PW_COL + side / 2;  // of two buffers
             uint32_t seen[8];  // of the block on the diagonal: the pairs of columns up to the row
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -350,14 +355,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             {  // the blocks behind the row's own stay 0
                 const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll 1
-                for (int b = w4 + 1; b < 4; ++b) put(b, zero);
+                for (int b = w4 + 1; b < 4; ++b) put(b, zero), put(b + 4, zero);
             }
 #pragma unroll 1
             for (int c = 0; c < pieces; ++c) {
                 const Gates& g = gates[c & 1];
                 if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
                 const float mine = -g.hi[row];
-                float mine_lo = BF ? 0.f : -g.lo[row];
                 if (!wait(p_full, c)) { ok = false; break; }
                 tcgen05_after_sync();
                 float shift = 0.f;  // log2 of what the row is multiplied by
@@ -379,28 +383,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
                     shift = (float)(14 - e);
-                    if (side == 0) row_unit[(c & 1) * kPiece + row] = ex2_approx(-shift);
-                    mine_lo += shift;
+                    if (side == 0) row_unit[(c & 3) * kPiece + row] = ex2_approx(-shift);
                 }
                 uint32_t p[16], w[8];
                 float* pf = reinterpret_cast<float*>(p);
                 tmem_ld16(from_col + w4 * 32, *reinterpret_cast<float(*)[16]>(pf));
-                // P' of the piece before has been read
-                if (c > 0 && !wait(&done[(c - 1) & 1], (c - 1) >> 1)) { ok = false; break; }
+                // P' of the piece before the last has been read
+                if (c > 1 && !wait(&done[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                to_col = lanes + PW_COL + (c & 1) * 64 + side / 2;
                 tcgen05_after_sync();
                 {  // the block on the diagonal: an exponential for each pair
-                    const uint64_t hi2 = f2_pack(mine, mine), lo2 = f2_pack(mine_lo, mine_lo);
+                    const uint64_t hi2 = f2_pack(mine, mine), shift2 = f2_pack(shift, shift);
                     const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
-                    const ulonglong2* gl = reinterpret_cast<const ulonglong2*>(BF ? g.lo : &g.lo[w4 * 32 + side]);
                     float x[16];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const ulonglong2 y = gh[j];
                         uint64_t e0 = f2_add(hi2, y.x), e1 = f2_add(hi2, y.y);
-                        if constexpr (!BF) {
-                            const ulonglong2 z = gl[j];
-                            e0 = f2_add(e0, f2_add(lo2, z.x)), e1 = f2_add(e1, f2_add(lo2, z.y));
-                        }
+                        if constexpr (!BF) e0 = f2_add(e0, shift2), e1 = f2_add(e1, shift2);
                         const float2 d0 = f2_get(e0), d1 = f2_get(e1);
                         x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
                         x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (warp < 16) {
         // ===================== V~: 32 rows at a time, four threads a row =====================
-        registers_down<64>();
+        registers_down<56>();
         const int tid = threadIdx.x - 256;
         const int half = tid >> 7;  // quarters 0 and 2, or 1 and 3
         const int r = (tid & 127) >> 2;
@@ -529,11 +529,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 arrive_warp(&vt_full[q]);
             }
             if (!ok) break;
-            if (lane == 0) mbar_arrive(&g_free[st]);
+            if (lane == 0) {
+                mbar_arrive(&v_clean[st]);
+                mbar_arrive(&g_free[st]);
+            }
         }
     } else if (warp < 20) {
         // ===================== the state: thread = row of dim_k (half a row at dim_k = 64) =====================
-        registers_up<136>();
+        registers_up<112>();
         constexpr int NC = DK == 128 ? 64 : 32;
         const int tid = threadIdx.x - 512;
         const int row = tid & (DK - 1);
@@ -625,19 +628,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
 #pragma unroll
             for (int i = 0; i < NC / 2; i += 8) {
-                float u[NT][16];
+                float u[2][16];  // the first numbers' product, and the others'
 #pragma unroll
-                for (int term = 0; term < NT; ++term) tmem_ld16(lanes + U_COL + 64 * term + c0 + 2 * i, u[term]);
+                for (int term = 0; term < 2; ++term) tmem_ld16(lanes + U_COL + 64 * term + c0 + 2 * i, u[term]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    uint64_t y = f2_pack(u[NT - 1][2 * j], u[NT - 1][2 * j + 1]);
-                    if constexpr (BF) {
-#pragma unroll
-                        for (int term = NT - 2; term >= 0; --term) y = f2_add(y, f2_pack(u[term][2 * j], u[term][2 * j + 1]));
-                    } else {
-                        y = f2_fma(f2_pack(u[0][2 * j], u[0][2 * j + 1]), f2_pack(back, back), f2_mul(y, f2_pack(back2, back2)));
-                    }
+                    const uint64_t first = f2_pack(u[0][2 * j], u[0][2 * j + 1]), other = f2_pack(u[1][2 * j], u[1][2 * j + 1]);
+                    const uint64_t y = BF ? f2_add(first, other)
+                                          : f2_fma(first, f2_pack(back, back), f2_mul(other, f2_pack(back2, back2)));
                     x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
                 }
             }
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (warp < 24) {
         // ===================== results: thread = row =====================
-        registers_down<64>();
+        registers_up<96>();
         if constexpr (!STATES) {
             const int w4 = warp - 20;
             const int row = w4 * 32 + lane;
@@ -682,42 +681,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (c + 1 < pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
                 if constexpr (!BF) {
                     fi *= s_unit[c & 1];
-                    fa *= row_unit[(c & 1) * kPiece + row];
+                    fa *= row_unit[(c & 3) * kPiece + row];
                 }
                 const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
                 const bool poisoned = any_bad[c & 3] != 0;
-#pragma unroll 1
+                uint32_t w[kSlice / 2];
+#pragma unroll
                 for (int c0 = 0; c0 < kSlice; c0 += 16) {
                     float x[16], y[16];
                     tmem_ld16(lanes + OI_COL + c0, x);
                     tmem_ld16(lanes + OA_COL + c0, y);
                     tmem_wait_ld();
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
-                        w[j / 2] = M::pack(z.x, z.y);
-                    }
-                    if (poisoned) {
-                        const uint8_t* mark = &bad[(c & 3) * 64 + c0];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (mark[j] <= row) w[j / 2] |= 0x7fffu << (16 * (j & 1));
-                    }
                     if (c0 + 16 == kSlice) {
                         tcgen05_before_sync();
                         arrive_warp(o_free);
                     }
-                    if (row < n) {
-                        char* to = out + c0 * sizeof(T);
-                        if (sectors) {
-                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
-                                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
+                        w[(c0 + j) / 2] = M::pack(z.x, z.y);
+                    }
+                }
+                if (poisoned) {
+                    const uint8_t* mark = &bad[(c & 3) * 64];
+#pragma unroll
+                    for (int j = 0; j < kSlice / 2; ++j) {
+                        if (mark[2 * j] <= row) w[j] |= 0x7fffu;
+                        if (mark[2 * j + 1] <= row) w[j] |= 0x7fffu << 16;
+                    }
+                }
+                if (row < n) {
+                    if (sectors) {
+#pragma unroll
+                        for (int j = 0; j < kSlice / 2; j += 8)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + j * 4), "r"(w[j]),
+                                         "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]),
+                                         "r"(w[j + 7])
                                          : "memory");
-                        } else {
-                            reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kSlice / 2; j += 4)
+                            *reinterpret_cast<uint4*>(out + j * 4) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
                     }
                 }
                 out += kPiece * pitch;
@@ -729,80 +733,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         }
     } else {
-        registers_down<48>();  // (one instruction for the four warps)
+        registers_down<56>();  // (one instruction for the four warps)
         if (warp == 24) {
             // ===================== tensor copies =====================
             if (lane == 0) {
-                int issued = 0;
+                int issued_qk = 0, issued = 0;
 #pragma unroll 1
                 for (int c = 0; c < pieces; ++c) {
                     const int st = c & 1;
-                    if (c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
                     const int y = t0 + c * kPiece;
-                    // (V first: its warps are the furthest ahead)
+                    if (c >= 2 && ((!STATES && !wait1(&q_free[st], (c >> 1) - 1)) || !wait1(&k_free[st], (c >> 1) - 1))) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
+#pragma unroll 1
+                    for (int p = 0; p < DK / 64; ++p) {
+                        tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
+                        if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
+                    }
+                    issued_qk = c + 1;
+                    if (!STATES && c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
                     mbar_arrive_expect_tx(&v_full[st], PANEL);
                     tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
-                    mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
-#pragma unroll
-                    for (int p = 0; p < DK / 64; ++p) {
-                        if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
-                        tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
-                    }
                     issued = c + 1;
                 }
                 // no copy is in flight when the CTA leaves
-                for (int c = max(issued - 2, 0); c < issued; ++c) {
+                for (int c = max(issued - 2, 0); c < issued_qk; ++c) {
                     ok = wait1(&qk_full[c & 1], c >> 1) && ok;
-                    ok = wait1(&v_full[c & 1], c >> 1) && ok;
+                    if (c < issued) ok = wait1(&v_full[c & 1], c >> 1) && ok;
                 }
             }
             __syncwarp();
         } else if (warp == 25) {
-            // ===================== products: one thread (an instruction takes the tensor core 50 to 100 cycles: short
-            // code counts more than unrolled loops) =====================
-            if (elect_one()) {
+            // ===================== products P, OI and OA: one thread (an instruction takes the tensor core 50 to 100
+            // cycles: short code counts more than unrolled loops) =====================
+            if (!STATES && elect_one()) {
                 const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
                 const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
-                // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
-                const uint64_t dkt = umma_desc_sw128(sbase + L::K, DK == 128 ? PANEL : 0, 1024);
                 const uint64_t dv = umma_desc_sw128(sbase + L::V, PANEL, 1024);
                 const uint64_t ds = umma_desc_sw128(sbase + L::S, DK * 128, 1024);
-                const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
-                auto pairs = [&](uint32_t st) {  // P = Q K^T
-                    const uint64_t q = dq + ((st * L::QK) >> 4), k = dk + ((st * L::QK) >> 4);
-                    tcgen05_after_sync();
-#pragma unroll 1
-                    for (int i = 0; i < DK / 16; ++i) {
-                        const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
-                        umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
-                    }
-                    umma_commit_cg<1>(p_full);
-                };
-                if (!STATES && pieces > 0) {
-                    ok = wait1(&qk_full[0], 0);
-                    if (ok) pairs(0);
-                }
-#pragma unroll 1
-                for (int c = 0; c < pieces && ok; ++c) {
+                for (int c = -1; c < pieces; ++c) {
                     const uint32_t st = (uint32_t)(c & 1);
-                    // U = K^T V~ (V~'s warps have seen V land; K has landed where P was computed)
-                    if ((STATES && !wait1(&qk_full[st], c >> 1)) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
-                    const uint64_t kt = dkt + ((st * L::QK) >> 4);
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        if (!wait1(&vt_full[q], c)) { ok = false; break; }
-                        tcgen05_after_sync();
-                        const uint64_t vt = dvt + (((uint32_t)q * L::QUARTER) >> 4), k0 = kt + (uint32_t)q * (4096 >> 4);
-                        umma_f16_cg<1>(tmem + U_COL, k0, vt, IDESC_U, q > 0);
-                        umma_f16_cg<1>(tmem + U_COL, k0 + (2048 >> 4), vt + (2048 >> 4), IDESC_U, true);
-                        umma_commit_cg<1>(&vt_free[q]);
-                    }
-                    if (!ok) break;
-                    umma_commit_cg<1>(u_full);
-                    if constexpr (STATES) {
-                        umma_commit_cg<1>(&done[st]);
-                    } else {
-                        // OI = Q S
+                    if (c >= 0) {  // OI = Q S
                         if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
                         tcgen05_after_sync();
                         const uint64_t q = dq + ((st * L::QK) >> 4);
@@ -811,92 +784,124 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
                                            ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
                         umma_commit_cg<1>(s_free);
+                        umma_commit_cg<1>(&q_free[st]);
                         if (!wait1(w_full, c)) { ok = false; break; }
-                        if (c + 1 < pieces) {
-                            if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
-                            pairs(st ^ 1);
+                    }
+                    if (c + 1 < pieces) {  // P = Q K^T of the next piece
+                        if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
+                        const uint64_t q = dq + (((st ^ 1) * L::QK) >> 4), k = dk + (((st ^ 1) * L::QK) >> 4);
+                        tcgen05_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < DK / 16; ++i) {
+                            const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
+                            umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
                         }
-                        // OA = P' V
+                        umma_commit_cg<1>(p_full);
+                    }
+                    if (c >= 0) {  // OA = P' V
+                        if (!wait1(&v_clean[st], c >> 1)) { ok = false; break; }
                         tcgen05_after_sync();
                         const uint64_t v = dv + ((st * PANEL) >> 4);
 #pragma unroll 1
                         for (int i = 0; i < kPiece / 16; ++i)
-                            umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + i * 8, v + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
+                            umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + st * 64 + i * 8, v + (uint32_t)i * (2048 >> 4),
+                                                  IDESC_O, i > 0);
                         umma_commit_cg<1>(&done[st]);
                     }
                 }
                 // every product is done before tensor memory is given back
-                umma_commit_cg<1>(all_done);
-                ok = wait1(all_done, 0) && ok;
+                umma_commit_cg<1>(&all_done[0]);
+                ok = wait1(&all_done[0], 0) && ok;
+                if (!ok) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
+            }
+            __syncwarp();
+        } else if (warp == 26) {
+            // ===================== product U = K^T V~: one thread =====================
+            if (elect_one()) {
+                // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
+                const uint64_t dkt = umma_desc_sw128(sbase + L::K, DK == 128 ? PANEL : 0, 1024);
+                const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
+                for (int c = 0; c < pieces && ok; ++c) {
+                    const uint32_t st = (uint32_t)(c & 1);
+                    if (!wait1(&qk_full[st], c >> 1) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
+                    uint64_t kt = dkt + ((st * L::QK) >> 4), vt = dvt;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        if (!wait1(&vt_full[q], c)) { ok = false; break; }
+                        tcgen05_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint64_t ka = kt + k * (2048 >> 4), vb = vt + k * (2048 >> 4);
+                            umma_f16_cg<1>(tmem + U_COL, ka, vb, IDESC_U, q > 0 || k > 0);
+                            if (NT == 3) umma_f16_cg<1>(tmem + U_COL + 64, ka, vb + (2 * 4096 >> 4), IDESC_U3, true);
+                        }
+                        umma_commit_cg<1>(&vt_free[q]);
+                        kt += 4096 >> 4, vt += L::QUARTER >> 4;
+                    }
+                    if (!ok) break;
+                    umma_commit_cg<1>(u_full);
+                    umma_commit_cg<1>(&k_free[st]);
+                }
+                umma_commit_cg<1>(&all_done[1]);
+                ok = wait1(&all_done[1], 0) && ok;
                 if (!ok) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
             }
             __syncwarp();
         } else {
-            // ===================== sums of the log decays: lane = token of a block, a warp for every other piece =====================
-            // Whole numbers of 2^-40 (in 64 bits): sums and differences are exact, and 64-bit floats too slow here.
-            constexpr float UNIT = 1.0f / 1099511627776.0f;
-            const int odd = warp - 26;
-            auto fetch = [&](int t) -> float {  // t: within the segment
-                return l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
-            };
-            // a whole piece's loads are in flight, the warp's next piece's
-            float n0 = fetch(odd * kPiece + lane), n1 = fetch(odd * kPiece + 32 + lane), n2 = fetch(odd * kPiece + 64 + lane),
-                  n3 = fetch(odd * kPiece + 96 + lane);
-#pragma unroll 1
-            for (int c = odd; c < pieces; c += 2) {
-                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
-                Gates& g = gates[c & 1];
-                long long total = 0;      // lane b: of block b
-                float grow = 0.f;
-                unsigned nans = 0;        // bit b: a NaN in block b
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    const float raw = n0;
-                    n0 = n1, n1 = n2, n2 = n3;
-                    n3 = fetch((c + 2) * kPiece + b * 32 + lane);
-                    const unsigned nan = __ballot_sync(0xffffffffu, raw != raw);
-                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums
-                    const float y = fminf(fmaxf(raw, -104.f), 1e4f);
-                    const float yh = y * 1.44269504f;
-                    const float yl = fmaf(y, 1.44269504f, -yh) + y * 1.92596299e-8f;
-                    long long x = __float2ll_rn(yh * 1099511627776.0f) + __float2ll_rn(yl * 1099511627776.0f);
-                    grow += fmaxf(yh, 0.f);
+            // ===================== sums of the log decays: lane = token of a block of 32 =====================
+            // Sums from a block's front and from its back are added up apart: a difference of two front sums would lose
+            // what comes behind a token that forgets.
+            float raw[4];
+            auto fetch = [&](int c) {
 #pragma unroll
-                    for (int o = 1; o < 32; o *= 2) {
-                        const long long z = __shfl_up_sync(0xffffffffu, x, o);
-                        if (lane >= o) x += z;
-                    }
-                    const long long all = __shfl_sync(0xffffffffu, x, 31);
-                    if (lane == b) total = all;
-                    const float hi = __ll2float_rn(-x);
-                    float to_end = ex2_approx(__ll2float_rn(all - x) * UNIT);
-                    float hi_out = hi * UNIT;
-                    if (nan) {  // from its token on, and in every sum that has it
-                        nans |= 1u << b;
-                        to_end = __int_as_float(0x7fffffff);
-                        if (nan & (0xffffffffu >> (31 - lane))) hi_out = to_end;
-                    }
-                    g.hi[b * 32 + lane] = hi_out;
-                    if constexpr (!BF) g.lo[b * 32 + lane] = __ll2float_rn(-x - __float2ll_rn(hi)) * UNIT;
-                    g.col[b * 32 + lane] = to_end;
+                for (int b = 0; b < 4; ++b) {
+                    const int t = c * kPiece + b * 32 + lane;
+                    raw[b] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
                 }
+            };
+            fetch(0);
+#pragma unroll 1
+            for (int c = 0; c < pieces; ++c) {
+                float front[4], back[4], all[4], grow = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums; NaN stays
+                    float y = raw[b] < -104.f ? -104.f : raw[b];
+                    y = (y > 1e4f ? 1e4f : y) * 1.44269504f;
+                    grow += fmaxf(y, 0.f);
+                    front[b] = y;
+                    back[b] = __shfl_down_sync(0xffffffffu, y, 1);
+                    if (lane == 31) back[b] = 0.f;
+                }
+                if (c + 1 < pieces) fetch(c + 1);
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float f = __shfl_up_sync(0xffffffffu, front[b], o), k = __shfl_down_sync(0xffffffffu, back[b], o);
+                        if (lane >= o) front[b] += f;
+                        if (lane + o < 32) back[b] += k;
+                    }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[b], 31);
                 if (__any_sync(0xffffffffu, grow != 0.f)) {
 #pragma unroll 1
                     for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
                 }
-                long long behind = total;  // lanes 0-3: over the lane's block and those behind it
-                if (lane > 3) behind = 0;
+                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                Gates& g = gates[c & 1];
 #pragma unroll
-                for (int o = 1; o < 4; o *= 2) behind += __shfl_down_sync(0xffffffffu, behind, o);
-                const float nan_b = __int_as_float(0x7fffffff);
-                if (lane < 4) {
-                    g.block[lane] = nans >> lane & 1 ? nan_b : __ll2float_rn(total) * UNIT;
-                    g.after[lane] = nans >> lane >> 1 ? nan_b : ex2_approx(__ll2float_rn(behind - total) * UNIT);
+                for (int b = 0; b < 4; ++b) {
+                    g.hi[b * 32 + lane] = -front[b];
+                    g.col[b * 32 + lane] = ex2_approx(back[b]);
                 }
-                if (lane == 0) {
-                    const float sum = __ll2float_rn(behind) * UNIT;
+                const float sum = (all[0] + all[1]) + (all[2] + all[3]);
+                if (lane < 4) {
+                    g.block[lane] = lane == 0 ? all[0] : lane == 1 ? all[1] : lane == 2 ? all[2] : all[3];
+                    g.after[lane] = ex2_approx(lane == 0 ? all[1] + (all[2] + all[3]) : lane == 1 ? all[2] + all[3] : lane == 2 ? all[3] : 0.f);
+                } else if (lane == 4) {
                     const bool small = sum > -0.7f && sum < 0.7f;
-                    g.keep = nans ? nan_b : small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
+                    g.keep = small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
                     g.once = small ? 1.f : 0.f;
                     g.grow = grow;
                     g.sum = sum;
