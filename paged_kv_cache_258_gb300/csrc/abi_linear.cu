@@ -40,20 +40,39 @@ int linear_args(const pkv_linear_desc* d, int32_t layer, const void* q, const vo
 }
 
 constexpr int kPiece = 128;          // tokens the tensor-core kernel takes at once
-constexpr int kMinChunk = 33;        // longest chunk from which it is used
-constexpr int kMinSegment = 4 * kPiece;
+constexpr int kMinSegment = 2 * kPiece;
+constexpr int kMinShared = 10 * kPiece;  // shortest chunk that is shared out along its length
 
-bool by_pieces(const pkv_linear_desc* d, int max_query) { return d->dtype != PKV_F32 && max_query >= kMinChunk; }
+// Whether a prefill goes by pieces of 128 tokens on the tensor cores or token after token, by what each is estimated to
+// take, in microseconds; fp32 has no choice. Measured over state elements (heads x dim_k x dim_v):
+//   tokens  a token 0.33 (dim_k 128) or 0.21 (64), and over all sequences 0.17 for each million state elements
+//   pieces  a CTA for each (sequence, head, 64 columns), 8.1 for one piece or less (dim_k 64: 6.7) and 2 (1.4) for each more
+// 48 heads x 128 x 128, bf16: 16, 24 and 64 tokens 7.4, 10.0 and 23.4 against 9.4; 8 sequences of 32, 48 and 64 tokens
+// 36, 52 and 67 against 49; 32 heads x 64 x 64, fp16: 16, 32 and 64 tokens 5.2, 8.6 and 15.3 against 7.8.
+bool by_pieces(const pkv_linear_desc* d, int n_seqs, int n_tokens, int max_query, int sms) {
+    if (d->dtype == PKV_F32 || max_query < 2) return false;
+    const double small = d->dim_k == 64, tokens = n_tokens < (double)n_seqs * max_query ? n_tokens : (double)n_seqs * max_query;
+    const double elements = (double)d->n_v_heads * d->dim_k * d->dim_v * 1e-6;
+    const double work = 0.17 * tokens * elements, longest = (small ? 0.21 : 0.33) * max_query;
+    const double units = (double)n_seqs * d->n_v_heads * (d->dim_v / 64), more = small ? 1.4 : 2.0;
+    const double each = (small ? 6.7 : 8.1) + more * (tokens / n_seqs / kPiece > 1 ? tokens / n_seqs / kPiece - 1 : 0);
+    const double waves = units <= sms ? 1 : units / sms + 0.5, most = (small ? 6.7 : 8.1) + more * ((max_query - 1) / kPiece);
+    return 1.3 + (each * waves > most ? each * waves : most) < 2.0 + (work > longest ? work : longest);
+}
 
-// How a call's sequences are shared out along their length: while the (sequence, head, 64 columns) units fill less
-// than half the GPU, in as many segments as it holds CTAs.
+// How a call's sequences are shared out along their length: while the (sequence, head, 64 columns) units fill no more
+// than half the GPU, in as many segments as it holds CTAs, but no more than kMaxSegments, each of which reads what all
+// before it leave. 8 heads x 128 x 64: 9,005 tokens 139 us whole, 32 in segments of two pieces or more, 34 of four, 44 of
+// eight; 1,024 tokens 22 whole and 24 in segments, 1,500 tokens 29 and 26.
+constexpr int kMaxSegments = 32;
 struct Segments {
     int n, tokens;
 };
 Segments segments_of(const pkv_linear_desc* d, int n_seqs, int max_query, int sms) {
     const long long units = (long long)n_seqs * d->n_v_heads * (d->dim_v / 64);
-    long long n = units * 2 <= sms ? sms / units : 1;
+    long long n = units * 2 <= sms && max_query >= kMinShared ? sms / units : 1;
     if (n > max_query / kMinSegment) n = max_query / kMinSegment;
+    if (n > kMaxSegments) n = kMaxSegments;
     if (n < 2) return {1, (max_query + kPiece - 1) / kPiece * kPiece};
     const int pieces = (max_query + kPiece - 1) / kPiece;
     const int tokens = (int)((pieces + n - 1) / n) * kPiece;
@@ -112,7 +131,7 @@ int pkv_linear_decode(const pkv_linear_desc* d, int32_t layer, const void* q, co
 size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* d, int32_t n_seqs, int32_t n_tokens,
                                           int32_t max_query_len) {
     if (pkv_linear_validate_desc(d) != PKV_OK || n_seqs <= 0 || n_tokens <= 0 || max_query_len <= 0) return 0;
-    if (!by_pieces(d, max_query_len) || max_query_len < 2 * kMinSegment) return 0;
+    if (d->dtype == PKV_F32 || max_query_len < kMinShared) return 0;
     int sms = 0;
     if (pkv::current_sm_count(&sms) != cudaSuccess) {
         cudaGetLastError();  // no usable device: report nothing rather than a guess
@@ -140,7 +159,7 @@ int pkv_linear_prefill(const pkv_linear_desc* d, int32_t layer, const void* q, c
     a.max_query = max_query_len;
     int sms = 0;
     if (pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
-    if (by_pieces(d, max_query_len)) {
+    if (by_pieces(d, n_seqs, n_tokens, max_query_len, sms)) {
         pkv::ChunkArgs c;
         c.l = a;
         c.dv = d->dim_v;

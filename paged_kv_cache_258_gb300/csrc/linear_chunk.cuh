@@ -108,11 +108,12 @@ struct ChunkSmem {
     static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [4][128], 2^-e of P's rows
     static constexpr uint32_t MISC = ROW + (BF ? 0 : 4 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
     static constexpr uint32_t BARS = MISC + 64;
-    static constexpr int NBARS = 8 * 2 + 2 * 4 + 7 + 3 + 2;
+    static constexpr int NBARS = 8 * 2 + 2 * 4 + 7 + 3 + 2 + 1;
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
     static constexpr uint32_t ALLOC = TOTAL;               // (on a 1,024-byte boundary: the array is declared so)
     static_assert(ALLOC <= 232448, "shared memory");
+    static_assert(4 * QUARTER >= DK * kSlice * 4, "a segment's first state fits where V~ goes");
     static_assert((VT % 1024) == 0 && (S % 1024) == 0 && (QUARTER % 1024) == 0 && (BARS % 8) == 0, "alignment");
 };
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // Every thread of the four warps: registers a thread from here on. The kernel's 72 a thread are shared out anew, as
-// 64 + 64 + 56 + 56 + 112 + 96 + 56 = 7 * 72.
+// 64 + 64 + 64 + 64 + 112 + 88 + 48 = 7 * 72.
 template <int N>
 __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* o_free = w_full + 1;     // OI and OA are read
     uint64_t* role = o_free + 1;       // [3] the warps of a role meet
     uint64_t* all_done = role + 3;     // [2] every product a thread issued is done
+    uint64_t* begun = all_done + 2;    // a segment's first state has been taken from V~'s place
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
     const LinearArgs& l = a.l;
@@ -310,12 +312,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(p_full, 1);
         mbar_init(w_full, 8);
         mbar_init(o_free, 4);
+        mbar_init(begun, 4);
         for (int i = 0; i < 3; ++i) mbar_init(&role[i], i == 0 ? 8 : 4);
         fence_mbar_init();
     }
     if (threadIdx.x < 4 * 64) bad[threadIdx.x] = kPiece;
     if (threadIdx.x < 4) any_bad[threadIdx.x] = 0;
     if (warp == 25) tmem_alloc_cg<1>(taddr_s, 512);
+    if (!STATES && seg > 0) {
+        // the state before a later segment: what those before leave, each decayed over the ones behind it. All threads
+        // add it up, many loads in flight (one role's 128 threads took a microsecond a segment)
+        float4* to = reinterpret_cast<float4*>(smem + L::VT);
+        const size_t step = (size_t)l.n_v * head, first = ((size_t)s * (a.n_segs - 1) * l.n_v + h);
+        for (int e = threadIdx.x; e < DK * kSlice / 4; e += kChunkThreads) {
+            const float* from = a.added + first * head + (size_t)(e / (kSlice / 4)) * a.dv + slice * kSlice + e % (kSlice / 4) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float since = 0.f;
+#pragma unroll 8
+            for (int i = seg - 1; i >= 0; --i) {
+                const float4 y = *reinterpret_cast<const float4*>(from + i * step);
+                const float w = ex2_approx(since);
+                since += a.sums[first + (size_t)i * l.n_v];
+                sum.x = fmaf(y.x, w, sum.x), sum.y = fmaf(y.y, w, sum.y), sum.z = fmaf(y.z, w, sum.z), sum.w = fmaf(y.w, w, sum.w);
+            }
+            to[e] = sum;
+        }
+    }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -367,20 +389,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 float shift = 0.f;  // log2 of what the row is multiplied by
                 if constexpr (!BF) {
                     float m0 = 0.f, m1 = 0.f;
+                    uint32_t x[32];
 #pragma unroll 1
-                    for (int b = 0; b <= w4; ++b) {
-                        uint32_t x[32];
+                    for (int b = 0; b < w4; ++b) {
                         tmem_ld32(lanes + P_COL + b * 32, x);
                         tmem_wait_ld();
-                        const int last = b < w4 ? 31 : lane;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
-                            const float y0 = __uint_as_float(x[j]), y1 = __uint_as_float(x[j + 1]), y2 = __uint_as_float(x[j + 2]),
-                                        y3 = __uint_as_float(x[j + 3]);
-                            m0 = fmax3(m0, j <= last ? fabsf(y0) : 0.f, j + 1 <= last ? fabsf(y1) : 0.f);
-                            m1 = fmax3(m1, j + 2 <= last ? fabsf(y2) : 0.f, j + 3 <= last ? fabsf(y3) : 0.f);
+                            m0 = fmax3(m0, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
+                            m1 = fmax3(m1, fabsf(__uint_as_float(x[j + 2])), fabsf(__uint_as_float(x[j + 3])));
                         }
                     }
+                    tmem_ld32(lanes + P_COL + w4 * 32, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) m0 = fmaxf(m0, j <= lane ? fabsf(__uint_as_float(x[j])) : 0.f);
                     const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
                     shift = (float)(14 - e);
                     if (side == 0) row_unit[(c & 3) * kPiece + row] = ex2_approx(-shift);
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (warp < 16) {
         // ===================== V~: 32 rows at a time, four threads a row =====================
-        registers_down<56>();
+        registers_down<64>();
         const int tid = threadIdx.x - 256;
         const int half = tid >> 7;  // quarters 0 and 2, or 1 and 3
         const int r = (tid & 127) >> 2;
@@ -480,7 +503,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
                 const float f = g.col[row] * g.after[q] * unit;
                 const uint64_t f2 = f2_pack(f, f);
-                if (c > 0 && !wait(&vt_free[q], c - 1)) { ok = false; break; }
+                if (c > 0 ? !wait(&vt_free[q], c - 1) : !STATES && seg > 0 && !wait(begun, 0)) { ok = false; break; }
                 unsigned char* to = smem + L::VT + q * L::QUARTER + r * 128;
                 uint32_t probe = 0;  // 0 x v, summed: not 0 if one is not finite
 #pragma unroll
@@ -544,13 +567,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)((warp - 16) * 32) << 16);
         const size_t at = (size_t)row * a.dv + slice * kSlice + c0;  // in a head's state
         uint64_t x[NC / 2];  // pairs of columns
-        auto load = [&](const float* from, float keep) {
-            const uint64_t k2 = f2_pack(keep, keep);
+        auto load = [&](const float* from) {
 #pragma unroll
             for (int i = 0; i < NC / 2; i += 2) {
-                const float4 y = *reinterpret_cast<const float4*>(from + at + 2 * i);
-                x[i] = f2_fma(x[i], k2, f2_pack(y.x, y.y));
-                x[i + 1] = f2_fma(x[i + 1], k2, f2_pack(y.z, y.w));
+                const float4 y = *reinterpret_cast<const float4*>(from + 2 * i);
+                x[i] = f2_pack(y.x, y.y);
+                x[i + 1] = f2_pack(y.z, y.w);
             }
         };
         auto save = [&](float* to) {
@@ -562,21 +584,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         };
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i) x[i] = 0;
-        {
-            // shared out, the second pass reads the start from where the first left it (its last segment writes dst), or
-            // adds up what the segments before leave
+        if (seg == 0) {
+            // shared out, the second pass reads the start from where the first left it: its last segment writes dst
             const size_t mine = (size_t)s * l.n_v + h;
             const bool from_state = STATES || used_segs == 1;
-            const int n = seg > 0 ? (STATES ? 0 : seg) : !from_state || src >= 0;
-#pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                const size_t to = ((size_t)s * (a.n_segs - 1) + i) * l.n_v + h;
-                load(seg > 0      ? a.added + to * head
-                     : from_state ? l.state + ((size_t)src * l.n_v + h) * head
-                                  : a.start + mine * head,
-                     i > 0 ? exp2f(a.sums[to]) : 0.f);
-            }
-            if (STATES && seg == 0) save(a.start + mine * head);
+            if (!from_state || src >= 0)
+                load((from_state ? l.state + ((size_t)src * l.n_v + h) * head : a.start + mine * head) + at);
+            if (STATES) save(a.start + mine * head);
+        } else if (!STATES) {
+            load(reinterpret_cast<const float*>(smem + L::VT) + row * kSlice + c0);
+            arrive_warp(begun);
         }
         float sum = 0.f;
 #pragma unroll 1
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
     } else if (warp < 24) {
         // ===================== results: thread = row =====================
-        registers_up<96>();
+        registers_up<88>();
         if constexpr (!STATES) {
             const int w4 = warp - 20;
             const int row = w4 * 32 + lane;
@@ -733,7 +750,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         }
     } else {
-        registers_down<56>();  // (one instruction for the four warps)
+        registers_down<48>();  // (one instruction for the four warps)
         if (warp == 24) {
             // ===================== tensor copies =====================
             if (lane == 0) {
@@ -766,8 +783,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
         } else if (warp == 25) {
-            // ===================== products P, OI and OA: one thread (an instruction takes the tensor core 50 to 100
-            // cycles: short code counts more than unrolled loops) =====================
+            // ===================== products P, OI and OA: one thread =====================
             if (!STATES && elect_one()) {
                 const uint64_t dq = umma_desc_sw128(sbase + L::Q, 16, 1024);
                 const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
@@ -779,7 +795,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
                         tcgen05_after_sync();
                         const uint64_t q = dq + ((st * L::QK) >> 4);
-#pragma unroll 1
+#pragma unroll
                         for (int i = 0; i < DK / 16; ++i)
                             umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
                                            ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
@@ -791,7 +807,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
                         const uint64_t q = dq + (((st ^ 1) * L::QK) >> 4), k = dk + (((st ^ 1) * L::QK) >> 4);
                         tcgen05_after_sync();
-#pragma unroll 1
+#pragma unroll
                         for (int i = 0; i < DK / 16; ++i) {
                             const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
                             umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
@@ -802,7 +818,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         if (!wait1(&v_clean[st], c >> 1)) { ok = false; break; }
                         tcgen05_after_sync();
                         const uint64_t v = dv + ((st * PANEL) >> 4);
-#pragma unroll 1
+#pragma unroll
                         for (int i = 0; i < kPiece / 16; ++i)
                             umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + st * 64 + i * 8, v + (uint32_t)i * (2048 >> 4),
                                                   IDESC_O, i > 0);
