@@ -613,7 +613,12 @@ size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* desc, int32_t n
  *   max_query_len host: the longest chunk, 0 <= max_query_len <= n_tokens
  *   workspace     device, >= pkv_linear_prefill_workspace_bytes(...), 16-byte aligned, no initialisation; calls
  *                 that overlap on the GPU must not share one
- * Other arguments as pkv_linear_decode. An empty chunk leaves its sequence's state in dst_slots as it was. A
+ * Other arguments as pkv_linear_decode. Short chunks and fp32 go token after token, longer ones of fp16 and bf16 in
+ * pieces of 128 tokens on the tensor cores, as the counts known on the host say; q, k and v are then device memory
+ * of the current device (else PKV_ERR_INVALID_ARG). In pieces the weight of a pair of tokens and the state as q reads
+ * it are rounded to the type once each, as attention weights are; the state itself stays fp32. An infinity in v counts
+ * as NaN there. What is not finite reaches its own and later tokens of its sequence only, v in its own columns.
+ * An empty chunk leaves its sequence's state in dst_slots as it was. A
  * sequence whose range is outside [0, n_tokens], negative or longer than max_query_len is skipped whole and sets
  * PKV_DEV_BAD_QUERY_RANGE; one with a bad slot, PKV_DEV_BAD_STATE_SLOT.
  */

@@ -21,6 +21,9 @@ A cache with ``storage="q8"`` holds its rows in 8 bits (half the bytes; pkv_q8_*
 with ``scored=True`` sums every cached position's attention weight, and its ``evict`` shortens the
 sequences to the positions used most (pkv_evict_tokens). Both work together.
 
+A hybrid model's linear layers keep a state of fixed size a sequence: ``LinearStates``. ``DeviceTables`` grows a
+batch's block tables on the device, so that a captured graph of whole steps can be replayed without the host.
+
 All device work is in libpkv's kernels; this module only moves arguments.
 """
 from __future__ import annotations
@@ -459,6 +462,130 @@ class DecodeBatch:
         """Algorithmic KV bytes the last step's attention read: sum(ctx) * 2 * n_kv * d * e * L."""
         return int(self.last_lens.astype(np.int64).sum()) * self.cache.kv_bytes_per_token_layer() * \
             self.cache.desc.n_layers
+
+
+class LinearStates:
+    """The states of a hybrid model's linear layers ("PagedAttention e continuous batching", "01 - Conceito", paragraph
+    2: beside the paged cache, a memory of fixed size for each sequence): a slot of ``state`` for each sequence, all
+    layers of it. ``slots`` gives what pkv_linear_prefill and pkv_linear_decode take; a sequence that has not been
+    listed there yet starts from zeros, whatever its slot held."""
+
+    def __init__(self, desc: pkv.LinearDesc, device=None, stream=None):
+        import torch
+        rc = pkv.pkv_linear_validate_desc(desc)
+        if rc != pkv.PKV_OK:
+            raise pkv.PkvError(rc, "LinearStates")
+        self.desc = desc
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(self.stream):
+            self.state = torch.zeros(pkv.linear_state_shape(desc), device=self.device)
+        self._slot: dict = {}
+        self._free = list(range(desc.n_slots))
+        self._begun: set = set()
+
+    def add(self, seq_id: int) -> int:
+        """A slot for a new sequence; PkvError (no blocks) if all are taken."""
+        if seq_id in self._slot:
+            raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"add({seq_id})")
+        if not self._free:
+            raise pkv.PkvError(pkv.PKV_ERR_NO_BLOCKS, f"add({seq_id}): no free state slot")
+        self._slot[seq_id] = self._free.pop(0)
+        return self._slot[seq_id]
+
+    def fork(self, parent: int, child: int) -> int:
+        """child starts with parent's state as it is behind what the stream holds so far (prefix sharing)."""
+        import torch
+        if parent not in self._slot:
+            raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"fork({parent}, {child})")
+        slot = self.add(child)
+        if parent in self._begun:
+            with torch.cuda.stream(self.stream):
+                self.state[:, slot].copy_(self.state[:, self._slot[parent]])
+            self._begun.add(child)
+        return slot
+
+    def free(self, seq_id: int) -> None:
+        if seq_id not in self._slot:
+            raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"free({seq_id})")
+        self._free.append(self._slot.pop(seq_id))
+        self._begun.discard(seq_id)
+
+    def slots(self, seq_ids):
+        """(src_slots, dst_slots), int32 [n] on the device, for one step over distinct sequences."""
+        import torch
+        ids = [int(x) for x in seq_ids]
+        if len(set(ids)) != len(ids) or any(x not in self._slot for x in ids):
+            raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, "slots: a sequence is unknown or listed twice")
+        dst = [self._slot[x] for x in ids]
+        src = [d if x in self._begun else -1 for x, d in zip(ids, dst)]
+        self._begun.update(ids)
+        with torch.cuda.stream(self.stream):
+            both = torch.tensor([src, dst], dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
+        return both[0], both[1]
+
+
+class DeviceTables:
+    """Block tables, lengths and slots of a batch that grow on the device (pkv_extend_tables), for steps that are
+    captured in a graph and replayed, or that are to run ahead of the host.
+
+    The batch takes blocks in the order of the manager's free list, row by row, as the manager itself would; ``follow``
+    then brings the manager to the same state. Until it has, nothing else may be done with the manager. A sequence whose
+    last block is partly filled and shared is refused: its copy on write is the manager's.
+    """
+
+    def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, max_tokens: int | None = None, stream=None):
+        import torch
+        self.cache = cache
+        self.seq_ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        self.n, self.max_blocks = len(self.seq_ids), int(max_blocks)
+        if len(set(self.seq_ids.tolist())) != self.n:
+            raise ValueError("a sequence is listed twice")
+        self.max_tokens = self.n if max_tokens is None else int(max_tokens)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(cache.device)
+        rc, tables, lens = cache.mgr.pack_tables(self.seq_ids, self.max_blocks)
+        if rc != pkv.PKV_OK:
+            raise pkv.PkvError(rc, "pack_tables (is max_blocks wide enough?)")
+        for i, c in enumerate(lens):
+            if c % pkv.BLOCK and cache.mgr.refcount(int(tables[i, c // pkv.BLOCK])) > 1:
+                raise ValueError(f"sequence {int(self.seq_ids[i])}: its last block is partly filled and shared")
+        free = np.asarray(cache.mgr.free_list(), dtype=np.int32)
+        dev = cache.device
+        with torch.cuda.stream(self.stream):
+            self.tables, self.lens, self.free = (torch.from_numpy(x.copy()).to(dev) for x in (tables, lens, free))
+            self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=dev)
+            self.query_start = torch.zeros(self.n + 1, dtype=torch.int32, device=dev)
+            self.totals = torch.zeros(3, dtype=torch.int32, device=dev)  # blocks taken, rows served, new tokens
+
+    def extend(self, new_tokens=None, stream=None) -> None:
+        """One step's new tokens: int32 [n] on the device, or one for each row. tables, lens, slots, query_start and
+        totals are those of the step when the launch has run. May be captured."""
+        pkv.pkv_extend_tables(self.cache.desc.num_blocks, self.free, self.totals[:1], self.tables, self.lens, new_tokens,
+                              self.slots, self.query_start, self.lens, self.totals,
+                              stream=self.stream if stream is None else stream)
+
+    def follow(self, new_tokens=None) -> int:
+        """The manager's part of one extend, with the same counts (host integers); returns the rows served."""
+        mgr = self.cache.mgr
+        counts = [1] * self.n if new_tokens is None else [int(x) for x in new_tokens]
+        if len(counts) != self.n:
+            raise ValueError("one count for each row")
+        total = 0
+        for i, m in enumerate(counts):
+            sid = int(self.seq_ids[i])
+            rc, table, ctx = mgr.block_table(sid)
+            if rc != pkv.PKV_OK:
+                raise pkv.PkvError(rc, f"block_table({sid})")
+            total += max(m, 0)
+            if m > 0:
+                if total > self.max_tokens or -(-(ctx + m) // pkv.BLOCK) > self.max_blocks:
+                    return i
+                rc = mgr.extend(sid, m)[0]
+                if rc == pkv.PKV_ERR_NO_BLOCKS:
+                    return i
+                if rc != pkv.PKV_OK:
+                    raise pkv.PkvError(rc, f"extend({sid}, {m})")
+        return self.n
 
 
 class PrefillStep:

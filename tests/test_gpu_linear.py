@@ -236,3 +236,118 @@ def test_repeats_bit_for_bit_on_another_stream(dtype):
         second = run(dtype, q, k, v, d, b, [0, 1, 2], [0, 1, 2], starts)
     side.synchronize()
     assert torch.equal(first[:849], second[:849]) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("length", [20, 200])
+def test_rows_on_sixteen_byte_boundaries(dtype, length):
+    """Every row array starts 16 bytes past a coarser boundary."""
+    q, k, v, d, state, starts = inputs(dtype, [length, 3], 1, 2, 64, 128, "head", seed=13)
+    want = run(dtype, q, k, v, d, state.clone(), [0, 1], [0, 1], starts)
+    step = 16 // q.element_size()
+
+    def shifted(x):
+        flat = torch.zeros(x.numel() + step, dtype=x.dtype, device="cuda")
+        y = flat[step:].view(x.shape)
+        y.copy_(x)
+        return y
+    desc = pkv.make_linear_desc(dtype, *state.shape[:2], 1, 2, 64, 128)
+    out = shifted(torch.full_like(v, 7.0))
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    pkv.pkv_linear_prefill(desc, 1, shifted(q), shifted(k), shifted(v), d, state, i32([0, 1]), i32([0, 1]), i32(starts), length,
+                           SCALE, out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_captured_and_replayed_with_other_inputs(dtype):
+    """Long (shared out), short, and single-token calls in one graph, replayed on other contents of the same buffers."""
+    lens = [2000, 40]
+    sets = [inputs(dtype, lens, 1, 2, 128, 64, "token", seed=s) for s in (20, 21)]
+    q, k, v, d, state, starts = [x.clone() if torch.is_tensor(x) else x for x in sets[0]]
+    desc = pkv.make_linear_desc(dtype, *state.shape[:2], 1, 2, 128, 64)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    src, dst, st = i32([0, 1]), i32([1, 0]), i32(starts)
+    ws = pkv.alloc_linear_prefill_workspace(desc, 2, q.shape[0], 2000)
+    outs = [torch.zeros_like(v) for _ in range(3)]
+
+    def calls():
+        pkv.pkv_linear_prefill(desc, 1, q, k, v, d, state, src, dst, st, 2000, SCALE, outs[0], ws)
+        pkv.pkv_linear_prefill(desc, 0, q[:6], k[:6], v[:6], d[:6], state, src, dst, i32_small, 3, SCALE, outs[1][:6])
+        pkv.pkv_linear_decode(desc, 0, q[:2], k[:2], v[:2], d[:2], state, dst, src, SCALE, outs[2][:2])
+    i32_small = i32([0, 3, 6])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    for x in (sets[1], sets[0]):
+        for to, frm in zip((q, k, v, d, state), x):
+            to.copy_(frm)
+        graph.replay()
+        got = [o.clone() for o in outs] + [state.clone()]
+        for to, frm in zip((q, k, v, d, state), x):
+            to.copy_(frm)
+        calls()
+        T = sum(lens)
+        for a, b in zip(got, outs + [state]):
+            assert torch.equal(a[:T], b[:T])
+    assert pkv.pkv_get_device_status() == 0
+
+
+def test_two_streams_at_once():
+    a, b = (inputs("bf16", [3000], 1, 2, 128, 64, "head", seed=s) for s in (30, 31))
+    want = [run("bf16", *x[:4], x[4].clone(), [0], [0], x[5]) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = []
+        for st, x in zip(streams, (a, b)):
+            with torch.cuda.stream(st):
+                got.append(run("bf16", *x[:4], x[4].clone(), [0], [0], x[5]))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[:3000], w[:3000])
+
+
+def test_a_missing_workspace_is_refused():
+    q, k, v, d, state, starts = inputs("bf16", [4000], 1, 1, 64, 64, "none", seed=14)
+    desc = pkv.make_linear_desc("bf16", *state.shape[:2], 1, 1, 64, 64)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    need = pkv.pkv_linear_prefill_workspace_bytes(desc, 1, 4000, 4000)
+    assert need > 0 and pkv.pkv_linear_prefill_workspace_bytes(desc, 1, 100, 100) == 0
+    for ws in (None, torch.empty(need - 16, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.pkv_linear_prefill(desc, 0, q, k, v, d, state, i32([0]), i32([0]), i32(starts), 4000, SCALE,
+                                   torch.empty_like(v), ws)
+        assert e.value.status == pkv.PKV_ERR_INVALID_ARG
+
+
+def test_other_strides_and_types_are_refused():
+    q, k, v, d, state, starts = inputs("bf16", [4], 2, 2, 64, 64, "token", seed=15, behind=0)
+    desc = pkv.make_linear_desc("bf16", *state.shape[:2], 2, 2, 64, 64)
+    slots = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ok = dict(q=q, k=k, v=v, g=d, state=state, src=slots, dst=slots, out=torch.empty_like(v))
+    for name, bad in (("q", torch.cat([q, q], 2)[..., :64]), ("k", k.float()), ("v", v[:3]), ("g", d.double()), ("g", d[:, :1]),
+                      ("state", state[:1]), ("src", slots.long()), ("dst", slots[:3]), ("out", torch.empty_like(v).transpose(0, 1))):
+        a = dict(ok, **{name: bad})
+        with pytest.raises(ValueError):
+            pkv.pkv_linear_decode(desc, 0, a["q"], a["k"], a["v"], a["g"], a["state"], a["src"], a["dst"], SCALE, a["out"])
+
+
+def test_offsets_past_32_bits():
+    """A slot whose first element lies past 2^31, and a layer past it."""
+    n_slots = 1030
+    state = torch.zeros((2, n_slots, 64, 128, 128), device="cuda")   # 2^30 elements a layer and more
+    q, k, v, d, small, starts = inputs("bf16", [150], 64, 64, 128, 128, "head", seed=16, behind=0)
+    first = torch.randn((64, 128, 128), device="cuda")
+    small[1, 0] = first
+    want = run("bf16", q, k, v, d, small, [0], [1], starts)
+    for layer, slot in ((1, n_slots - 1), (1, 1000), (0, n_slots - 1)):
+        state[layer, slot] = first
+        got = run("bf16", q, k, v, d, state, [slot], [slot], starts, layer=layer)
+        assert torch.equal(got, want) and torch.equal(state[layer, slot], small[1, 1])
+    one = run("bf16", q[:1], k[:1], v[:1], d, state, [n_slots - 1], [0], None, decode=True)
+    two = run("bf16", q[:1], k[:1], v[:1], d, small, [1], [0], None, decode=True)
+    assert torch.equal(one, two) and torch.equal(state[1, 0], small[1, 0])
