@@ -222,8 +222,10 @@ int pkv_extend_tables(int32_t num_blocks, const int32_t* free_blocks, int32_t n_
     a.n_seqs = n_seqs;
     a.max_tokens = max_tokens;
     if (pkv::device_status_word(&a.status) != cudaSuccess) return PKV_ERR_CUDA;
-    if (pkv::launch_extend_tables(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
-    pkv::count_launches(1);
+    int sms = 0, launches = 0;
+    if (pkv::current_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pkv::launch_extend_tables(a, static_cast<cudaStream_t>(stream), sms, &launches) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::count_launches(launches);
     return PKV_OK;
 }
 

@@ -37,7 +37,7 @@ struct LinearArgs {
     float scale;
 };
 
-cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream);
+cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream, int sms, int* n_launches);
 // Token after token with the state in registers (linear_step.cu).
 cudaError_t launch_linear_step(int dtype, int dk, int dv, int sms, const LinearArgs& a, cudaStream_t stream);
 

@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* begun = all_done + 2;    // a segment's first state has been taken from V~'s place
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
+    if (STATES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second pass may set itself up
     const LinearArgs& l = a.l;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = blockIdx.x % a.slices;
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (threadIdx.x < 4 * 64) bad[threadIdx.x] = kPiece;
     if (threadIdx.x < 4) any_bad[threadIdx.x] = 0;
     if (warp == 25) tmem_alloc_cg<1>(taddr_s, 512);
+    if (!STATES && a.n_segs > 1) grid_dependency_wait();  // the first pass is done
     if (!STATES && seg > 0) {
         // the state before a later segment: what those before leave, each decayed over the ones behind it. All threads
         // add it up, many loads in flight (one role's 128 threads took a microsecond a segment)
@@ -948,8 +950,17 @@ cudaError_t run_chunk(const ChunkArgs& a, const CUtensorMap& q, const CUtensorMa
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     const unsigned segs = STATES ? a.n_segs - 1 : a.n_segs;
-    kern<<<(unsigned)a.l.n_seqs * segs * a.l.n_v * a.slices, kChunkThreads, smem, stream>>>(a, q, k, v);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.l.n_seqs * segs * a.l.n_v * a.slices);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = !STATES && a.n_segs > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a, q, k, v);
 }
 
 template <typename T>

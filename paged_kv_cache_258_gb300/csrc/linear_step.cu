@@ -20,11 +20,15 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStep = 8;  // tokens staged in shared memory at a time
+// Tokens staged in shared memory at a time. 16 where a token's latency counts (columns of 32, 500 tokens of 8 heads x 64 x
+// 64 in fp32: 73 us, in steps of 8 83, of 4 106) and where a whole short chunk fits; 8 for many long fp32 rows (256 tokens of
+// 8 x 32 heads x 128 x 128: 172 us against 189).
+template <typename T, int NC>
+constexpr int kStep = sizeof(T) == 2 || NC == 32 ? 16 : 8;
 
 template <typename T, int DK, int DV, int NC, bool ONE>
 __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs a) {
-    constexpr int TB = ONE ? 1 : kStep;
+    constexpr int TB = ONE ? 1 : kStep<T, NC>;
     constexpr int SLICES = DV / NC;
     constexpr int LPR = NC / 4;                   // lanes of a row of S
     constexpr int GROUPS = kThreads / LPR;        // row groups of the CTA
@@ -34,7 +38,8 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
     __shared__ __align__(16) float s_q[TB][DK];
     __shared__ __align__(16) float s_k[TB][DK];
     __shared__ __align__(16) float s_v[TB][NC];
-    __shared__ float s_g[TB];
+    __shared__ float s_d[TB];       // what a token's decay multiplies the state by (exp(g)), or that less 1
+    __shared__ float s_once[TB];    // 0 for the first, 1 for the second
     __shared__ __align__(16) float s_o[TB][kThreads / 32][NC];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slice = blockIdx.x % SLICES;
@@ -114,45 +119,42 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
             const int e = (i * kThreads + tid) * N;
             if (e / NC < n) widen(rv[i], &s_v[0][0] + e);
         }
-        if (tid < n) s_g[tid] = rg;
+        if (tid < n) {
+            const bool slow = rg > -0.5f && rg < 0.5f;
+            s_d[tid] = slow ? expm1f(rg) : expf(rg);
+            s_once[tid] = slow ? 1.f : 0.f;
+        }
         __syncthreads();
         if (t0 + TB < q1) fetch(t0 + TB);
-#pragma unroll 1
-        for (int t = 0; t < n; ++t) {
-            const float g = s_g[t];
+        auto token = [&](auto slow, int t) {
+            const float d = s_d[t], once = s_once[t];
             const float4 vt = *reinterpret_cast<const float4*>(&s_v[t][col]);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto rows = [&](auto slow, float d) {
 #pragma unroll
-                for (int i = 0; i < R; i += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(&s_k[t][row0 + i]);
-                    const float4 q4 = *reinterpret_cast<const float4*>(&s_q[t][row0 + i]);
-                    const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+            for (int i = 0; i < R; i += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(&s_k[t][row0 + i]);
+                const float4 q4 = *reinterpret_cast<const float4*>(&s_q[t][row0 + i]);
+                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float4& y = x[i + j];
-                        if constexpr (decltype(slow)::value) {  // d = expm1(g)
-                            y.x = fmaf(y.x, d, fmaf(kk[j], vt.x, y.x));
-                            y.y = fmaf(y.y, d, fmaf(kk[j], vt.y, y.y));
-                            y.z = fmaf(y.z, d, fmaf(kk[j], vt.z, y.z));
-                            y.w = fmaf(y.w, d, fmaf(kk[j], vt.w, y.w));
-                        } else {                                // d = exp(g)
-                            y.x = fmaf(kk[j], vt.x, y.x * d);
-                            y.y = fmaf(kk[j], vt.y, y.y * d);
-                            y.z = fmaf(kk[j], vt.z, y.z * d);
-                            y.w = fmaf(kk[j], vt.w, y.w * d);
-                        }
-                        o.x = fmaf(qq[j], y.x, o.x);
-                        o.y = fmaf(qq[j], y.y, o.y);
-                        o.z = fmaf(qq[j], y.z, o.z);
-                        o.w = fmaf(qq[j], y.w, o.w);
+                for (int j = 0; j < 4; ++j) {
+                    float4& y = x[i + j];
+                    if constexpr (decltype(slow)::value) {  // d = expm1(g)
+                        y.x = fmaf(y.x, d, fmaf(kk[j], vt.x, y.x));
+                        y.y = fmaf(y.y, d, fmaf(kk[j], vt.y, y.y));
+                        y.z = fmaf(y.z, d, fmaf(kk[j], vt.z, y.z));
+                        y.w = fmaf(y.w, d, fmaf(kk[j], vt.w, y.w));
+                    } else {                                // either
+                        y.x = fmaf(y.x, d, fmaf(kk[j], vt.x, y.x * once));
+                        y.y = fmaf(y.y, d, fmaf(kk[j], vt.y, y.y * once));
+                        y.z = fmaf(y.z, d, fmaf(kk[j], vt.z, y.z * once));
+                        y.w = fmaf(y.w, d, fmaf(kk[j], vt.w, y.w * once));
                     }
+                    o.x = fmaf(qq[j], y.x, o.x);
+                    o.y = fmaf(qq[j], y.y, o.y);
+                    o.z = fmaf(qq[j], y.z, o.z);
+                    o.w = fmaf(qq[j], y.w, o.w);
                 }
-            };
-            if (g > -0.5f && g < 0.5f)
-                rows(std::true_type{}, expm1f(g));
-            else
-                rows(std::false_type{}, expf(g));
+            }
 #pragma unroll
             for (int m = LPR; m < 32; m *= 2) {
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
@@ -161,6 +163,19 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
                 o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
             }
             if (lane < LPR) *reinterpret_cast<float4*>(&s_o[t][warp][col]) = o;
+        };
+        // tokens follow one another without a branch: the loads, products and shuffles of one overlap those of the next,
+        // whose state needs only the products
+        bool any = false;
+#pragma unroll
+        for (int t = 0; t < TB; ++t) any |= t < n && s_once[t] == 0.f;
+        constexpr int AT_ONCE = !ONE && R <= 8 ? 4 : 1;
+        if (!any) {
+#pragma unroll AT_ONCE
+            for (int t = 0; t < n; ++t) token(std::true_type{}, t);
+        } else {
+#pragma unroll AT_ONCE
+            for (int t = 0; t < n; ++t) token(std::false_type{}, t);
         }
         __syncthreads();
         for (int e = tid; e < n * NC; e += kThreads) {
@@ -189,8 +204,8 @@ cudaError_t run(const LinearArgs& a, cudaStream_t stream) {
 
 template <typename T, int DK, int DV>
 cudaError_t pick(int sms, const LinearArgs& a, cudaStream_t stream) {
-    // whole rows of S while there are enough of them to fill the GPU, else columns of 32
-    return (long long)a.n_seqs * a.n_v >= 2LL * sms ? run<T, DK, DV, DV>(a, stream) : run<T, DK, DV, 32>(a, stream);
+    // columns of 64 while there are enough of them to fill the GPU, else of 32
+    return (long long)a.n_seqs * a.n_v * (DV / 64) >= 2LL * sms ? run<T, DK, DV, 64>(a, stream) : run<T, DK, DV, 32>(a, stream);
 }
 
 template <typename T>

@@ -9,11 +9,10 @@
 // rows at a time, and kept in shared memory; the tokens are then shared out by warps, 32 at a time, each finding its
 // row by bisection (once for the whole warp where the 32 lie in one row). A fresh block's table entry is written
 // with its first token, which this call always holds. Lengths and totals may be written over what they were read
-// from, so they are written when every CTA has read them: the CTAs are one cluster, and a cluster barrier says so.
+// from, so one CTA alone writes them: behind its tokens where it does the whole call, in a launch of its own behind the
+// CTAs that share many tokens.
 //
 // Bound by latency: the counts, the scan, free ids, stores one after the other.
-#include <cooperative_groups.h>
-
 #include "common.cuh"
 #include "linear.h"
 
@@ -22,6 +21,8 @@ namespace {
 
 constexpr int kRows = 1024;  // rows of a tile, one a thread
 constexpr unsigned kMost = 0x7fffffffu;
+constexpr int kShared = 8 * kRows;  // up to this many tokens one CTA does the whole call
+constexpr int kEach = 2 * kRows;    // tokens of a CTA beyond that
 
 __device__ __forceinline__ unsigned sat_add(unsigned a, unsigned b) { return min(a + b, kMost); }
 
@@ -48,6 +49,8 @@ __device__ __forceinline__ void block_scan(unsigned& x, unsigned& y, unsigned (*
     if (warp > 0) x = sat_add(x, part[0][warp - 1]), y = sat_add(y, part[1][warp - 1]);
 }
 
+// TOKENS: tables and slots of the new tokens, shared by the grid. ROWS (one CTA): starts, lengths, totals.
+template <bool TOKENS, bool ROWS>
 __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a) {
     __shared__ unsigned s_part[2][32];
     __shared__ int s_start[kRows + 1];  // first token of each row of the tile
@@ -62,6 +65,7 @@ __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a
     const bool bad_used = used < 0 || used > a.n_free;
     const unsigned avail = bad_used ? 0u : (unsigned)(a.n_free - used);
     unsigned flags = bad_used ? (unsigned)PKV_DEV_BAD_FREE_LIST : 0u;
+    constexpr unsigned row_flags = PKV_DEV_BAD_CONTEXT_LEN | PKV_DEV_BAD_QUERY_RANGE;  // which every CTA finds
     unsigned tok = 0, blk = 0;  // before this tile
     int served = 0;
     bool open = true;
@@ -103,12 +107,12 @@ __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a
         s_len[tid] = len;
         s_block[tid] = y - need;
         if (tid == 0) s_start[kRows] = (int)end;
-        if (cta == 0 && tid < rows) a.query_start[row] = s_start[tid];
+        if (ROWS && tid < rows) a.query_start[row] = s_start[tid];
         served += first;
         open = open && first == rows;
         __syncthreads();
         // tokens tok .. end - 1 lie in rows 0 .. first - 1 of the tile
-        for (unsigned t0 = tok + warp_of_all * 32; t0 < end; t0 += warps * 32) {
+        for (unsigned t0 = TOKENS ? tok + warp_of_all * 32 : end; t0 < end; t0 += warps * 32) {
             const unsigned t = t0 + lane;
             int lo = 0, hi = first;  // s_start[lo] <= t0, and t0 < s_start[hi] or hi == first
             while (hi - lo > 1) {
@@ -142,40 +146,39 @@ __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a
         blk = s_blk;
         __syncthreads();  // the tile's shared values have been read
     }
-    for (unsigned t = tok + warp_of_all * 32 + lane; t < (unsigned)a.max_tokens; t += warps * 32) a.slots[t] = -1;
-    if (flags) atomicOr(a.status, flags);
-    if (cta == 0 && tid == 0) a.query_start[a.n_seqs] = (int)tok;
-    // every CTA has read the lengths and `used`; query_start is written
-    if (ctas > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
-    if (a.n_seqs <= kRows) {
-        if (cta == 0 && tid < a.n_seqs) a.new_lens[tid] = my_len + my_new;
-    } else {
-        for (int row = cta * kRows + tid; row < a.n_seqs; row += ctas * kRows)
-            a.new_lens[row] = a.lens[row] + (a.query_start[row + 1] - a.query_start[row]);
-    }
-    if (cta == 0 && tid == 0) {
-        a.totals[0] = used + (int)blk;
-        a.totals[1] = served;
-        a.totals[2] = (int)tok;
+    if (TOKENS)
+        for (unsigned t = tok + warp_of_all * 32 + lane; t < (unsigned)a.max_tokens; t += warps * 32) a.slots[t] = -1;
+    if (flags && (cta == 0 || (flags & ~row_flags))) atomicOr(a.status, flags);
+    if constexpr (ROWS) {
+        if (tid == 0) a.query_start[a.n_seqs] = (int)tok;
+        __syncthreads();  // the lengths and `used` have been read, query_start is written
+        if (a.n_seqs <= kRows) {
+            if (tid < a.n_seqs) a.new_lens[tid] = my_len + my_new;
+        } else {
+            for (int row = tid; row < a.n_seqs; row += kRows)
+                a.new_lens[row] = a.lens[row] + (a.query_start[row + 1] - a.query_start[row]);
+        }
+        if (tid == 0) {
+            a.totals[0] = used + (int)blk;
+            a.totals[1] = served;
+            a.totals[2] = (int)tok;
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream) {
-    // one CTA places 1,024 tokens at a time; beyond a few rounds of that a cluster shares them
-    const int ctas = a.max_tokens <= 4 * kRows ? 1 : 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, extend_tables_kernel, a);
+cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream, int sms, int* n_launches) {
+    *n_launches = 1;
+    if (a.max_tokens <= kShared) {
+        extend_tables_kernel<true, true><<<1, kRows, 0, stream>>>(a);
+    } else {
+        const long long ctas = ((long long)a.max_tokens + kEach - 1) / kEach;
+        extend_tables_kernel<true, false><<<(unsigned)(ctas < sms ? ctas : sms), kRows, 0, stream>>>(a);
+        extend_tables_kernel<false, true><<<1, kRows, 0, stream>>>(a);
+        *n_launches = 2;
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace pkv
