@@ -48,6 +48,7 @@ struct ChunkArgs {
     LinearArgs l;
     int dv, slices;         // dim_v, and its slices of 64
     int n_segs, seg_tokens; // segments of a sequence (1: whole), tokens of each: a multiple of 128
+    bool take_more = false; // a CTA goes on with other CTAs' work (n_segs == 1, and more CTAs than the GPU holds)
     float* start = nullptr; // [n_seqs][n_v][DK][DV]: the states the sequences start from
     float* added = nullptr; // [n_seqs][n_segs - 1][n_v][DK][DV]: what a segment leaves (the first: with the start)
     float* sums = nullptr;  // [n_seqs][n_segs - 1][n_v]: log2 of the decay over a segment

@@ -13,20 +13,30 @@
 //                columns of an earlier block of 32: exp(G_i - R) times exp(R - G_j), R the sum up to the block's end:
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
 //                one for each pair. A thread takes a row's even or odd halves of 32 columns
-//   warps 8-15   V~, in quarters of 32 rows one after the other, four warps on every other one: split into numbers of the type that add up to it (two of
-//                fp16: 2^-22 is left; three of bf16: exact), two beside one another along N, so that one product of
-//                N = 128 gives both sums (the third is added to the second's), and the state keeps fp32's precision
+//   warps 8-15   V~, in quarters of 32 rows, four warps on every other one: split into numbers of the type that add up
+//                to it (two of fp16: 2^-22 is left; three of bf16: exact), two beside one another along N, so that one
+//                product of N = 128 gives both sums (the third is added to the second's), and the state keeps fp32's
+//                precision
 //   warps 16-19  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
 //   warps 20-23  results: exp(G_i) OI + OA, whole 32-byte sectors of a row from its thread
 //   warp 24      tensor copies of Q, K and V, two pieces ahead
 //   warps 25, 26 issue the products: P, OI and OA, and U: a thread's waits (some 150 cycles each here, met or not) then
 //                leave the tensor cores to the other's products
-//   warp 27      sums of decays 
+//   warp 27      sums of the log decays, for all the others
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
 // fp16 cannot hold their range: rows of P' and the copy of S are then brought to 2^14 by a power of two each, which the
 // sums undo in fp32.
+//
+// Fewer units than the GPU holds: a long sequence is shared out along its length in segments, a first pass leaving what
+// each adds to the state (STATES). More: a CTA goes on with others' work (MORE), its roles without a pause, so that a
+// second unit of one piece takes 4.5 us instead of 8.1 (a CTA's start, first copies and end, with nothing beside them).
+//
+// What bounds it: the walk along a sequence. A piece takes 1.8 us of a CTA, twice what its products take alone: U, the
+// state's sum and rounding, OI and the reading of results follow one another, and the roles' instructions share four
+// schedulers. 48 heads x 128 x 128, bf16, decays of a head and token: 8,192 tokens of one sequence 117 us (2.3 TB/s of
+// q, k, v and results, 0.77 PFLOP/s of products), 4 x 2,048 113 us, 8 x 64 tokens 31 us.
 //
 // A piece past the sequence's end: rows of K and V behind it are zeroed in shared memory (another sequence's rows, or
 // nobody's, NaN perhaps). A non-finite v would reach earlier tokens of its piece through 0 x NaN: it is taken
@@ -90,6 +100,12 @@ struct __align__(16) PieceGates {
     float sum;                     // over all
 };
 
+// The work of one CTA of the grid: a sequence (or a segment of it), a head, 64 columns of v.
+struct __align__(16) ChunkWork {
+    int valid, slice, h, s, seg, used_segs, src, dst;
+    int t0, tokens, pieces, pad;  // its first token and how many; pieces of 128
+};
+
 template <typename T, int DK>
 struct ChunkSmem {
     static constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
@@ -107,8 +123,10 @@ struct ChunkSmem {
     static constexpr uint32_t BAD = GATES + 2 * sizeof(Gates);  // bytes [4][64]: first token whose v is not finite
     static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [4][128], 2^-e of P's rows
     static constexpr uint32_t MISC = ROW + (BF ? 0 : 4 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
-    static constexpr uint32_t BARS = MISC + 64;
-    static constexpr int NBARS = 8 * 2 + 2 * 4 + 7 + 3 + 2 + 1;
+    static constexpr uint32_t NEXT = MISC + 64;            // 16 bytes: the answer to a request for another CTA's work
+    static constexpr uint32_t WORK = NEXT + 16;            // [2]
+    static constexpr uint32_t BARS = WORK + 2 * sizeof(ChunkWork);
+    static constexpr int NBARS = 10 * 2 + 2 * 4 + 7 + 3 + 2 + 2;
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
     static constexpr uint32_t ALLOC = TOTAL;               // (on a 1,024-byte boundary: the array is declared so)
@@ -137,7 +155,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // Every thread of the four warps: registers a thread from here on. The kernel's 72 a thread are shared out anew, as
-// 64 + 64 + 64 + 64 + 112 + 88 + 48 = 7 * 72.
+// 64 + 64 + 56 + 56 + 128 + 88 + 48 = 7 * 72, or where a CTA goes on with other work (results by 16 columns, which take
+// fewer) 64 + 64 + 64 + 64 + 128 + 72 + 48.
 template <int N>
 __device__ __forceinline__ void registers_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -210,7 +229,8 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 }
 
 // STATES: the first pass over a sequence's segments but the last, which keeps only what they add to the state.
-template <typename T, int DK, bool STATES>
+// MORE: the grid has more CTAs than the GPU holds, and a CTA goes on with others' work.
+template <typename T, int DK, bool STATES, bool MORE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
@@ -255,40 +275,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* role = o_free + 1;       // [3] the warps of a role meet
     uint64_t* all_done = role + 3;     // [2] every product a thread issued is done
     uint64_t* begun = all_done + 2;    // a segment's first state has been taken from V~'s place
+    uint64_t* next_full = begun + 1;   // an answer has come
+    uint64_t* work_full = next_full + 1;  // [2] work is written
+    uint64_t* work_free = work_full + 2;  // [2] and read
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
     if (STATES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second pass may set itself up
     const LinearArgs& l = a.l;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slice = blockIdx.x % a.slices;
-    long long unit = blockIdx.x / a.slices;
-    const int h = (int)(unit % l.n_v);
-    unit /= l.n_v;
-    const int segs = STATES ? a.n_segs - 1 : a.n_segs;
-    const int seg = (int)(unit % segs), s = (int)(unit / segs);
-    const int hq = h / (l.n_v / l.n_qk);
-    const int q0 = l.q_start[s], q1 = l.q_start[s + 1];
-    const int src = l.src[s], dst = l.dst[s];
-    const bool bad_range = q0 < 0 || q1 < q0 || q1 > l.n_tokens || q1 - q0 > l.max_query;
-    const bool bad_slot = src >= l.n_slots || dst >= l.n_slots;
+    const size_t head = (size_t)DK * a.dv;
     if ((sbase & 1023u) != 0) {  // (the swizzled tiles need it; never seen)
         if (threadIdx.x == 0) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
         return;
     }
-    if (bad_range || bad_slot) {
-        if (!STATES && h == 0 && slice == 0 && seg == 0 && threadIdx.x == 0)
+    ChunkWork* work = reinterpret_cast<ChunkWork*>(smem + L::WORK);
+    // What CTA `block` of the grid has to do; valid: anything at all.
+    auto work_of = [&](int block, bool report) -> ChunkWork {
+        ChunkWork w;
+        w.slice = block % a.slices;
+        int unit = block / a.slices;
+        w.h = unit % l.n_v;
+        unit /= l.n_v;
+        const int segs = STATES ? a.n_segs - 1 : a.n_segs;
+        w.seg = unit % segs, w.s = unit / segs;
+        const int q0 = l.q_start[w.s], q1 = l.q_start[w.s + 1];
+        w.src = l.src[w.s], w.dst = l.dst[w.s];
+        const bool bad_range = q0 < 0 || q1 < q0 || q1 > l.n_tokens || q1 - q0 > l.max_query;
+        const bool bad_slot = w.src >= l.n_slots || w.dst >= l.n_slots;
+        const bool bad_any = bad_range || bad_slot;
+        if (bad_any && report && !STATES && w.h == 0 && w.slice == 0 && w.seg == 0)
             atomicOr(l.status, (bad_range ? (unsigned)PKV_DEV_BAD_QUERY_RANGE : 0u) |
                                    (bad_slot ? (unsigned)PKV_DEV_BAD_STATE_SLOT : 0u));
-        return;
-    }
-    const int whole = q1 - q0;
-    // a sequence that fits fewer segments leaves the others nothing; its last keeps the state
-    const int used_segs = whole > 0 ? (whole + a.seg_tokens - 1) / a.seg_tokens : 1;
-    if (seg >= (STATES ? used_segs - 1 : used_segs)) return;
-    const int t0 = q0 + seg * a.seg_tokens;
-    const int tokens = min(a.seg_tokens, q1 - t0);
-    const int pieces = (tokens + kPiece - 1) / kPiece;
-    const size_t head = (size_t)DK * a.dv;
+        // a sequence that fits fewer segments leaves the others nothing; its last keeps the state
+        const int whole = bad_any ? 0 : q1 - q0;
+        w.used_segs = whole > 0 ? (whole + a.seg_tokens - 1) / a.seg_tokens : 1;
+        w.valid = !bad_any && w.seg < (STATES ? w.used_segs - 1 : w.used_segs);
+        w.t0 = q0 + w.seg * a.seg_tokens;
+        w.tokens = w.valid ? min(a.seg_tokens, q1 - w.t0) : 0;
+        w.pieces = (w.tokens + kPiece - 1) / kPiece;
+        if (!w.valid) w.src = w.dst = -1;  // (nothing read, nothing kept)
+        return w;
+    };
+    const ChunkWork first = work_of(blockIdx.x, threadIdx.x == 0);
+    if (!first.valid && !MORE) return;  // (otherwise the CTA may still take other work)
+    if (threadIdx.x == 0) work[0] = first;
+    const int seg = MORE ? 0 : first.seg;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -314,6 +345,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_init(w_full, 8);
         mbar_init(o_free, 4);
         mbar_init(begun, 4);
+        mbar_init(next_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&work_full[i], 1);
+            mbar_init(&work_free[i], 8 + 8 + 4 + 4 + 3);  // warps, or the one thread of a warp
+        }
         for (int i = 0; i < 3; ++i) mbar_init(&role[i], i == 0 ? 8 : 4);
         fence_mbar_init();
     }
@@ -325,16 +361,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // the state before a later segment: what those before leave, each decayed over the ones behind it. All threads
         // add it up, many loads in flight (one role's 128 threads took a microsecond a segment)
         float4* to = reinterpret_cast<float4*>(smem + L::VT);
-        const size_t step = (size_t)l.n_v * head, first = ((size_t)s * (a.n_segs - 1) * l.n_v + h);
+        const size_t step = (size_t)l.n_v * head, at0 = ((size_t)first.s * (a.n_segs - 1) * l.n_v + first.h);
         for (int e = threadIdx.x; e < DK * kSlice / 4; e += kChunkThreads) {
-            const float* from = a.added + first * head + (size_t)(e / (kSlice / 4)) * a.dv + slice * kSlice + e % (kSlice / 4) * 4;
+            const float* from = a.added + at0 * head + (size_t)(e / (kSlice / 4)) * a.dv + first.slice * kSlice + e % (kSlice / 4) * 4;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             float since = 0.f;
 #pragma unroll 8
             for (int i = seg - 1; i >= 0; --i) {
                 const float4 y = *reinterpret_cast<const float4*>(from + i * step);
                 const float w = ex2_approx(since);
-                since += a.sums[first + (size_t)i * l.n_v];
+                since += a.sums[at0 + (size_t)i * l.n_v];
                 sum.x = fmaf(y.x, w, sum.x), sum.y = fmaf(y.y, w, sum.y), sum.z = fmaf(y.z, w, sum.z), sum.w = fmaf(y.w, w, sum.w);
             }
             to[e] = sum;
@@ -357,11 +393,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         return wait(&role[id], met++);
     };
     bool ok = true;
+    // The roles run on from work to work without a pause: behind the CTA's own that of CTAs of the grid that have not
+    // started, whose launch the thread that issues the copies cancels for it. (Not where the GPU holds the whole grid at
+    // once, as it does where sequences are shared out.)
+    constexpr bool steal = MORE;
+    int slice, h, s, used_segs, src, dst, t0, tokens, pieces;
+    int base = 0;   // pieces of the work before: the phases go on
+    int taken = 0;  // works before
+    auto read = [&]() -> bool {
+        const ChunkWork& w = work[taken & 1];
+        slice = w.slice, h = w.h, s = w.s, used_segs = w.used_segs, src = w.src, dst = w.dst;
+        t0 = w.t0, tokens = w.tokens, pieces = w.pieces;
+        return w.valid || taken == 0;
+    };
+    auto begin = [&]() {
+        read();
+        if (steal) arrive_warp(&work_free[0]);
+    };
+    auto begin1 = [&]() {
+        read();
+        if (steal) mbar_arrive(&work_free[0]);
+    };
+    auto more = [&]() -> bool {  // whole warp
+        base += pieces;
+        if (!steal || !ok) return false;
+        ++taken;
+        if (!wait(&work_full[taken & 1], (taken - 1) >> 1)) { ok = false; return false; }
+        const bool yes = read();
+        arrive_warp(&work_free[taken & 1]);
+        return yes;
+    };
+    auto more1 = [&]() -> bool {  // one thread
+        base += pieces;
+        if (!steal || !ok) return false;
+        ++taken;
+        if (!wait1(&work_full[taken & 1], (taken - 1) >> 1)) { ok = false; return false; }
+        const bool yes = read();
+        mbar_arrive(&work_free[taken & 1]);
+        return yes;
+    };
 
     if (warp < 8) {
         // ===================== weights of the pairs inside a piece: thread = row, half of its columns =====================
         registers_down<64>();
         if constexpr (!STATES) {
+            begin();
             const int w4 = warp & 3, side = (warp >> 2) * 16;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
@@ -381,193 +457,199 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
                 for (int b = w4 + 1; b < 4; ++b) put(b, zero), put(b + 4, zero);
             }
+            do {
 #pragma unroll 1
-            for (int c = 0; c < pieces; ++c) {
-                const Gates& g = gates[c & 1];
-                if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-                const float mine = -g.hi[row];
-                if (!wait(p_full, c)) { ok = false; break; }
-                tcgen05_after_sync();
-                float shift = 0.f;  // log2 of what the row is multiplied by
-                if constexpr (!BF) {
-                    float m0 = 0.f, m1 = 0.f;
-                    uint32_t x[32];
+                for (int c = base; c < base + pieces; ++c) {
+                    const Gates& g = gates[c & 1];
+                    if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
+                    const float mine = -g.hi[row];
+                    if (!wait(p_full, c)) { ok = false; break; }
+                    tcgen05_after_sync();
+                    float shift = 0.f;  // log2 of what the row is multiplied by
+                    if constexpr (!BF) {
+                        float m0 = 0.f, m1 = 0.f;
+                        uint32_t x[32];
 #pragma unroll 1
-                    for (int b = 0; b < w4; ++b) {
-                        tmem_ld32(lanes + P_COL + b * 32, x);
+                        for (int b = 0; b < w4; ++b) {
+                            tmem_ld32(lanes + P_COL + b * 32, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                m0 = fmax3(m0, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
+                                m1 = fmax3(m1, fabsf(__uint_as_float(x[j + 2])), fabsf(__uint_as_float(x[j + 3])));
+                            }
+                        }
+                        tmem_ld32(lanes + P_COL + w4 * 32, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            m0 = fmax3(m0, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
-                            m1 = fmax3(m1, fabsf(__uint_as_float(x[j + 2])), fabsf(__uint_as_float(x[j + 3])));
+                        for (int j = 0; j < 32; ++j) m0 = fmaxf(m0, j <= lane ? fabsf(__uint_as_float(x[j])) : 0.f);
+                        const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
+                        shift = (float)(14 - e);
+                        if (side == 0) row_unit[(c & 3) * kPiece + row] = ex2_approx(-shift);
+                    }
+                    uint32_t p[16], w[8];
+                    float* pf = reinterpret_cast<float*>(p);
+                    tmem_ld16(from_col + w4 * 32, *reinterpret_cast<float(*)[16]>(pf));
+                    // P' of the piece before the last has been read
+                    if (c > 1 && !wait(&done[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                    to_col = lanes + PW_COL + (c & 1) * 64 + side / 2;
+                    tcgen05_after_sync();
+                    {  // the block on the diagonal: an exponential for each pair
+                        const uint64_t hi2 = f2_pack(mine, mine), shift2 = f2_pack(shift, shift);
+                        const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
+                        float x[16];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const ulonglong2 y = gh[j];
+                            uint64_t e0 = f2_add(hi2, y.x), e1 = f2_add(hi2, y.y);
+                            if constexpr (!BF) e0 = f2_add(e0, shift2), e1 = f2_add(e1, shift2);
+                            const float2 d0 = f2_get(e0), d1 = f2_get(e1);
+                            x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
+                            x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 y = f2_get(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), f2_pack(pf[2 * j], pf[2 * j + 1])));
+                            w[j] = M::pack(y.x, y.y) & seen[j];
                         }
                     }
-                    tmem_ld32(lanes + P_COL + w4 * 32, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) m0 = fmaxf(m0, j <= lane ? fabsf(__uint_as_float(x[j])) : 0.f);
-                    const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
-                    shift = (float)(14 - e);
-                    if (side == 0) row_unit[(c & 3) * kPiece + row] = ex2_approx(-shift);
-                }
-                uint32_t p[16], w[8];
-                float* pf = reinterpret_cast<float*>(p);
-                tmem_ld16(from_col + w4 * 32, *reinterpret_cast<float(*)[16]>(pf));
-                // P' of the piece before the last has been read
-                if (c > 1 && !wait(&done[c & 1], (c >> 1) - 1)) { ok = false; break; }
-                to_col = lanes + PW_COL + (c & 1) * 64 + side / 2;
-                tcgen05_after_sync();
-                {  // the block on the diagonal: an exponential for each pair
-                    const uint64_t hi2 = f2_pack(mine, mine), shift2 = f2_pack(shift, shift);
-                    const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
-                    float x[16];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 y = gh[j];
-                        uint64_t e0 = f2_add(hi2, y.x), e1 = f2_add(hi2, y.y);
-                        if constexpr (!BF) e0 = f2_add(e0, shift2), e1 = f2_add(e1, shift2);
-                        const float2 d0 = f2_get(e0), d1 = f2_get(e1);
-                        x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
-                        x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 y = f2_get(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), f2_pack(pf[2 * j], pf[2 * j + 1])));
-                        w[j] = M::pack(y.x, y.y) & seen[j];
-                    }
-                }
-                float from = mine + shift;  // the sum from the end of block b to the row
+                    float from = mine + shift;  // the sum from the end of block b to the row
 #pragma unroll 1
-                for (int b = w4 - 1; b >= 0; --b) {
-                    tmem_ld16(from_col + b * 32, *reinterpret_cast<float(*)[16]>(pf));
-                    put(b + 1, w);
-                    const float f = ex2_approx(from);
-                    from += g.block[b];
-                    const uint64_t f2 = f2_pack(f, f);
-                    const ulonglong2* gc = reinterpret_cast<const ulonglong2*>(&g.col[b * 32 + side]);
-                    uint64_t x[8];
+                    for (int b = w4 - 1; b >= 0; --b) {
+                        tmem_ld16(from_col + b * 32, *reinterpret_cast<float(*)[16]>(pf));
+                        put(b + 1, w);
+                        const float f = ex2_approx(from);
+                        from += g.block[b];
+                        const uint64_t f2 = f2_pack(f, f);
+                        const ulonglong2* gc = reinterpret_cast<const ulonglong2*>(&g.col[b * 32 + side]);
+                        uint64_t x[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 y = gc[j];
-                        x[2 * j] = f2_mul(y.x, f2), x[2 * j + 1] = f2_mul(y.y, f2);
-                    }
-                    tmem_wait_ld();
+                        for (int j = 0; j < 4; ++j) {
+                            const ulonglong2 y = gc[j];
+                            x[2 * j] = f2_mul(y.x, f2), x[2 * j + 1] = f2_mul(y.y, f2);
+                        }
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 y = f2_get(f2_mul(x[j], f2_pack(pf[2 * j], pf[2 * j + 1])));
-                        w[j] = M::pack(y.x, y.y);
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 y = f2_get(f2_mul(x[j], f2_pack(pf[2 * j], pf[2 * j + 1])));
+                            w[j] = M::pack(y.x, y.y);
+                        }
                     }
+                    put(0, w);
+                    tmem_wait_st();
+                    tcgen05_before_sync();
+                    arrive_warp(w_full);
+                    if (lane == 0) mbar_arrive(&g_free[c & 1]);
                 }
-                put(0, w);
-                tmem_wait_st();
-                tcgen05_before_sync();
-                arrive_warp(w_full);
-                if (lane == 0) mbar_arrive(&g_free[c & 1]);
-            }
+            } while (more());
         }
     } else if (warp < 16) {
         // ===================== V~: 32 rows at a time, four threads a row =====================
-        registers_down<64>();
+        registers_down<MORE ? 64 : 56>();
+        begin();
         const int tid = threadIdx.x - 256;
         const int half = tid >> 7;  // quarters 0 and 2, or 1 and 3
         const int r = (tid & 127) >> 2;
         // which four 16-byte units of its row: two threads' rows share the banks of half a row otherwise
         const int u0 = (tid & 3) + 4 * (r & 1);
         const uint32_t at[2] = {(uint32_t)((u0 ^ (r & 7)) << 4), (uint32_t)((u0 ^ 4 ^ (r & 7)) << 4)};
+        do {
 #pragma unroll 1
-        for (int c = 0; c < pieces; ++c) {
-            const int st = c & 1;
-            const int n = min(kPiece, tokens - c * kPiece);
-            unsigned char* v = smem + L::V + st * PANEL;
-            const Gates& g = gates[st];
-            if (!wait(&g_full[st], c >> 1) || !wait(&v_full[st], c >> 1)) { ok = false; break; }
-            if (n < kPiece) {  // rows behind the sequence's end
-                if (!wait(&qk_full[st], c >> 1)) { ok = false; break; }
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = base; c < base + pieces; ++c) {
+                const int st = c & 1;
+                const int n = min(kPiece, tokens - (c - base) * kPiece);
+                unsigned char* v = smem + L::V + st * PANEL;
+                const Gates& g = gates[st];
+                if (!wait(&g_full[st], c >> 1) || !wait(&v_full[st], c >> 1)) { ok = false; break; }
+                if (n < kPiece) {  // rows behind the sequence's end
+                    if (!wait(&qk_full[st], c >> 1)) { ok = false; break; }
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-                for (int i = n * 8 + tid; i < kPiece * 8; i += 256) {
-                    *reinterpret_cast<uint4*>(v + i * 16) = zero;
+                    for (int i = n * 8 + tid; i < kPiece * 8; i += 256) {
+                        *reinterpret_cast<uint4*>(v + i * 16) = zero;
 #pragma unroll
-                    for (int p = 0; p < DK / 64; ++p)
-                        *reinterpret_cast<uint4*>(smem + L::K + st * L::QK + p * PANEL + i * 16) = zero;
+                        for (int p = 0; p < DK / 64; ++p)
+                            *reinterpret_cast<uint4*>(smem + L::K + st * L::QK + p * PANEL + i * 16) = zero;
+                    }
+                    fence_proxy_async_smem();
+                    if (!meet(0)) { ok = false; break; }
                 }
-                fence_proxy_async_smem();
-                if (!meet(0)) { ok = false; break; }
-            }
-            const float unit = BF ? 1.f : down_by(g.grow);
+                const float unit = BF ? 1.f : down_by(g.grow);
 #pragma unroll 1
-            for (int q = half; q < 4; q += 2) {
-                const int row = q * 32 + r;
-                unsigned char* from = v + row * 128;
-                uint4 x[2];
+                for (int q = half; q < 4; q += 2) {
+                    const int row = q * 32 + r;
+                    unsigned char* from = v + row * 128;
+                    uint4 x[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
-                const float f = g.col[row] * g.after[q] * unit;
-                const uint64_t f2 = f2_pack(f, f);
-                if (c > 0 ? !wait(&vt_free[q], c - 1) : !STATES && seg > 0 && !wait(begun, 0)) { ok = false; break; }
-                unsigned char* to = smem + L::VT + q * L::QUARTER + r * 128;
-                uint32_t probe = 0;  // 0 x v, summed: not 0 if one is not finite
+                    for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+                    const float f = g.col[row] * g.after[q] * unit;
+                    const uint64_t f2 = f2_pack(f, f);
+                    if (c > 0 ? !wait(&vt_free[q], c - 1) : !STATES && seg > 0 && !wait(begun, 0)) { ok = false; break; }
+                    unsigned char* to = smem + L::VT + q * L::QUARTER + r * 128;
+                    uint32_t probe = 0;  // 0 x v, summed: not 0 if one is not finite
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                    uint32_t w[NT][4];
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t xw[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        uint32_t w[NT][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (!STATES) probe = M::zero_times(xw[j], probe);
-                        const float2 a2 = M::unpack(xw[j]);
-                        uint64_t y2 = f2_mul(f2_pack(a2.x, a2.y), f2);
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (!STATES) probe = M::zero_times(xw[j], probe);
+                            const float2 a2 = M::unpack(xw[j]);
+                            uint64_t y2 = f2_mul(f2_pack(a2.x, a2.y), f2);
 #pragma unroll
-                        for (int term = 0; term < NT; ++term) {
-                            const float2 y = f2_get(y2);
-                            if constexpr (BF) {  // the 24 bits of a number cut into three of 8
-                                const uint32_t b0 = __float_as_uint(y.x), b1 = __float_as_uint(y.y);
-                                w[term][j] = __byte_perm(b0, b1, 0x7632);
-                                if (term + 1 < NT)
-                                    y2 = f2_add(y2, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u)));
-                            } else {
-                                w[term][j] = M::pack(y.x, y.y);
-                                const float2 z = M::unpack(w[term][j]);
-                                if (term + 1 < NT) y2 = f2_mul(f2_add(y2, f2_pack(-z.x, -z.y)), f2_pack(kSecond, kSecond));
+                            for (int term = 0; term < NT; ++term) {
+                                const float2 y = f2_get(y2);
+                                if constexpr (BF) {  // the 24 bits of a number cut into three of 8
+                                    const uint32_t b0 = __float_as_uint(y.x), b1 = __float_as_uint(y.y);
+                                    w[term][j] = __byte_perm(b0, b1, 0x7632);
+                                    if (term + 1 < NT)
+                                        y2 = f2_add(y2, f2_pack(-__uint_as_float(b0 & 0xffff0000u), -__uint_as_float(b1 & 0xffff0000u)));
+                                } else {
+                                    w[term][j] = M::pack(y.x, y.y);
+                                    const float2 z = M::unpack(w[term][j]);
+                                    if (term + 1 < NT) y2 = f2_mul(f2_add(y2, f2_pack(-z.x, -z.y)), f2_pack(kSecond, kSecond));
+                                }
                             }
                         }
-                    }
 #pragma unroll
-                    for (int term = 0; term < NT; ++term)
-                        *reinterpret_cast<uint4*>(to + term * 4096 + at[k]) =
-                            make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]);
-                }
-                if (!STATES && (probe & 0x7fff7fffu) != 0) {  // out of V, and noted for the results
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        T* y = reinterpret_cast<T*>(from + at[k]);
-#pragma unroll 1
-                        for (int j = 0; j < 8; ++j)
-                            if (!(fabsf(static_cast<float>(y[j])) <= 3.4028234e38f)) {
-                                y[j] = from_float<T>(0.f);
-                                byte_min(&bad[(c & 3) * 64 + (u0 ^ (k * 4)) * 8 + j], row);
-                                any_bad[c & 3] = 1;
-                            }
+                        for (int term = 0; term < NT; ++term)
+                            *reinterpret_cast<uint4*>(to + term * 4096 + at[k]) =
+                                make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]);
                     }
+                    if (!STATES && (probe & 0x7fff7fffu) != 0) {  // out of V, and noted for the results
+#pragma unroll 1
+                        for (int k = 0; k < 2; ++k) {
+                            T* y = reinterpret_cast<T*>(from + at[k]);
+#pragma unroll 1
+                            for (int j = 0; j < 8; ++j)
+                                if (!(fabsf(static_cast<float>(y[j])) <= 3.4028234e38f)) {
+                                    y[j] = from_float<T>(0.f);
+                                    byte_min(&bad[(c & 3) * 64 + (u0 ^ (k * 4)) * 8 + j], row);
+                                    any_bad[c & 3] = 1;
+                                }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    arrive_warp(&vt_full[q]);
                 }
-                fence_proxy_async_smem();
-                arrive_warp(&vt_full[q]);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive(&v_clean[st]);
+                    mbar_arrive(&g_free[st]);
+                }
             }
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive(&v_clean[st]);
-                mbar_arrive(&g_free[st]);
-            }
-        }
+        } while (more());
     } else if (warp < 20) {
         // ===================== the state: thread = row of dim_k (half a row at dim_k = 64) =====================
-        registers_up<112>();
+        registers_up<128>();
+        begin();
         constexpr int NC = DK == 128 ? 64 : 32;
         const int tid = threadIdx.x - 512;
         const int row = tid & (DK - 1);
         const int c0 = DK == 128 ? 0 : (tid >> 6) * 32;
         const uint32_t lanes = tmem + ((uint32_t)((warp - 16) * 32) << 16);
-        const size_t at = (size_t)row * a.dv + slice * kSlice + c0;  // in a head's state
+        size_t at;  // in a head's state
         uint64_t x[NC / 2];  // pairs of columns
         auto load = [&](const float* from) {
 #pragma unroll
@@ -584,101 +666,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 *reinterpret_cast<float4*>(to + at + 2 * i) = make_float4(y.x, y.y, z.x, z.y);
             }
         };
+        do {
+            at = (size_t)row * a.dv + slice * kSlice + c0;
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) x[i] = 0;
-        if (seg == 0) {
-            // shared out, the second pass reads the start from where the first left it: its last segment writes dst
-            const size_t mine = (size_t)s * l.n_v + h;
-            const bool from_state = STATES || used_segs == 1;
-            if (!from_state || src >= 0)
-                load((from_state ? l.state + ((size_t)src * l.n_v + h) * head : a.start + mine * head) + at);
-            if (STATES) save(a.start + mine * head);
-        } else if (!STATES) {
-            load(reinterpret_cast<const float*>(smem + L::VT) + row * kSlice + c0);
-            arrive_warp(begun);
-        }
-        float sum = 0.f;
+            for (int i = 0; i < NC / 2; ++i) x[i] = 0;
+            if (seg == 0) {
+                // shared out, the second pass reads the start from where the first left it: its last segment writes dst
+                const size_t mine = (size_t)s * l.n_v + h;
+                const bool from_state = STATES || used_segs == 1;
+                if (!from_state || src >= 0)
+                    load((from_state ? l.state + ((size_t)src * l.n_v + h) * head : a.start + mine * head) + at);
+                if (STATES) save(a.start + mine * head);
+            } else if (!STATES) {
+                load(reinterpret_cast<const float*>(smem + L::VT) + row * kSlice + c0);
+                arrive_warp(begun);
+            }
+            float sum = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < pieces; ++c) {
-            if constexpr (!STATES) {  // the copy that Q meets
-                uint64_t unit2 = 0;
-                float back_s = 1.f;
-                if constexpr (!BF) {
-                    float most = 0.f;
+            for (int c = base; c < base + pieces; ++c) {
+                if constexpr (!STATES) {  // the copy that Q meets
+                    uint64_t unit2 = 0;
+                    float back_s = 1.f;
+                    if constexpr (!BF) {
+                        float most = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NC / 2; ++i) {
-                        const float2 y = f2_get(x[i]);
-                        most = fmax3(most, fabsf(y.x), fabsf(y.y));
+                        for (int i = 0; i < NC / 2; ++i) {
+                            const float2 y = f2_get(x[i]);
+                            most = fmax3(most, fabsf(y.x), fabsf(y.y));
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        float* mine = part + (c & 1) * 4;  // (read for piece c by all before any of them meets for c + 1)
+                        if (lane == 0) mine[warp - 16] = most;
+                        if (!meet(1)) { ok = false; break; }
+                        const int e = exponent14(fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3])));
+                        unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
+                        back_s = pow2i(e - 14);
                     }
+                    if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
+                    // (Q S of the piece before is done: it began when the results of the one before that had been read)
+                    if (!BF && tid == 0) s_unit[c & 1] = back_s;
+                    unsigned char* to = smem + L::S + row * 128;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    float* mine = part + (c & 1) * 4;  // (read for piece c by all before any of them meets for c + 1)
-                    if (lane == 0) mine[warp - 16] = most;
-                    if (!meet(1)) { ok = false; break; }
-                    const int e = exponent14(fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3])));
-                    unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
-                    back_s = pow2i(e - 14);
-                }
-                if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
-                // (Q S of the piece before is done: it began when the results of the one before that had been read)
-                if (!BF && tid == 0) s_unit[c & 1] = back_s;
-                unsigned char* to = smem + L::S + row * 128;
+                    for (int i = 0; i < NC / 2; i += 4) {
+                        uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < NC / 2; i += 4) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = f2_get(BF ? x[i + j] : f2_mul(x[i + j], unit2));
-                        w[j] = M::pack(y.x, y.y);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 y = f2_get(BF ? x[i + j] : f2_mul(x[i + j], unit2));
+                            w[j] = M::pack(y.x, y.y);
+                        }
+                        *reinterpret_cast<uint4*>(to + ((((c0 + 2 * i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(to + ((((c0 + 2 * i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    fence_proxy_async_smem();
+                    arrive_warp(s_full);
                 }
-                fence_proxy_async_smem();
-                arrive_warp(s_full);
-            }
-            const Gates& g = gates[c & 1];
-            if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-            const float unit_v = BF ? 1.f : down_by(g.grow);
-            const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
-            if (STATES) sum += g.sum;
-            arrive_warp(&g_free[c & 1]);
-            if (!wait(u_full, c)) { ok = false; break; }
-            tcgen05_after_sync();
-            const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
+                const Gates& g = gates[c & 1];
+                if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
+                const float unit_v = BF ? 1.f : down_by(g.grow);
+                const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
+                if (STATES) sum += g.sum;
+                arrive_warp(&g_free[c & 1]);
+                if (!wait(u_full, c)) { ok = false; break; }
+                tcgen05_after_sync();
+                const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
 #pragma unroll
-            for (int i = 0; i < NC / 2; i += 8) {
-                float u[2][16];  // the first numbers' product, and the others'
+                for (int i = 0; i < NC / 2; i += 8) {
+                    float u[2][16];  // the first numbers' product, and the others'
 #pragma unroll
-                for (int term = 0; term < 2; ++term) tmem_ld16(lanes + U_COL + 64 * term + c0 + 2 * i, u[term]);
-                tmem_wait_ld();
+                    for (int term = 0; term < 2; ++term) tmem_ld16(lanes + U_COL + 64 * term + c0 + 2 * i, u[term]);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint64_t first = f2_pack(u[0][2 * j], u[0][2 * j + 1]), other = f2_pack(u[1][2 * j], u[1][2 * j + 1]);
-                    const uint64_t y = BF ? f2_add(first, other)
-                                          : f2_fma(first, f2_pack(back, back), f2_mul(other, f2_pack(back2, back2)));
-                    x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
+                    for (int j = 0; j < 8; ++j) {
+                        const uint64_t first = f2_pack(u[0][2 * j], u[0][2 * j + 1]), other = f2_pack(u[1][2 * j], u[1][2 * j + 1]);
+                        const uint64_t y = BF ? f2_add(first, other)
+                                              : f2_fma(first, f2_pack(back, back), f2_mul(other, f2_pack(back2, back2)));
+                        x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
+                    }
                 }
+                tcgen05_before_sync();
+                arrive_warp(u_free);
             }
-            tcgen05_before_sync();
-            arrive_warp(u_free);
-        }
-        if (ok) {
-            if (STATES) {
-                const size_t to = ((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h;
-                save(a.added + to * head);
-                if (tid == 0 && slice == 0) a.sums[to] = sum;
-            } else if (seg == used_segs - 1 && dst >= 0)
-                save(l.state + ((size_t)dst * l.n_v + h) * head);
-        }
+            if (ok) {
+                if (STATES) {
+                    const size_t to = ((size_t)s * (a.n_segs - 1) + seg) * l.n_v + h;
+                    save(a.added + to * head);
+                    if (tid == 0 && slice == 0) a.sums[to] = sum;
+                } else if (seg == used_segs - 1 && dst >= 0)
+                    save(l.state + ((size_t)dst * l.n_v + h) * head);
+            }
+        } while (more());
     } else if (warp < 24) {
         // ===================== results: thread = row =====================
-        registers_up<88>();
+        if constexpr (!MORE) registers_up<88>();
         if constexpr (!STATES) {
+            begin();
             const int w4 = warp - 20;
             const int row = w4 * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
             const size_t pitch = (size_t)l.n_v * a.dv * sizeof(T);
-            char* out = static_cast<char*>(l.out) + (size_t)(t0 + row) * pitch + ((size_t)h * a.dv + slice * kSlice) * sizeof(T);
             float sum = 0.f;  // of the log decays up to the row
             auto decays = [&](int c) -> bool {
                 if (!wait(&g_full[c & 1], c >> 1)) return false;
@@ -689,67 +774,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 arrive_warp(&g_free[c & 1]);
                 return true;
             };
-            if (pieces > 0) ok = decays(0);
             const bool sectors = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0;
+            do {
+                char* out = static_cast<char*>(l.out) + (size_t)(t0 + row) * pitch + ((size_t)h * a.dv + slice * kSlice) * sizeof(T);
+                if (pieces > 0) ok = decays(base);
 #pragma unroll 1
-            for (int c = 0; c < pieces && ok; ++c) {
-                const int n = min(kPiece, tokens - c * kPiece);
-                if (!wait(&done[c & 1], c >> 1)) { ok = false; break; }
-                tcgen05_after_sync();
-                float fi = ex2_approx(sum) * l.scale, fa = l.scale;
-                if (c + 1 < pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
-                if constexpr (!BF) {
-                    fi *= s_unit[c & 1];
-                    fa *= row_unit[(c & 3) * kPiece + row];
-                }
-                const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
-                const bool poisoned = any_bad[c & 3] != 0;
-                uint32_t w[kSlice / 2];
-#pragma unroll
-                for (int c0 = 0; c0 < kSlice; c0 += 16) {
-                    float x[16], y[16];
-                    tmem_ld16(lanes + OI_COL + c0, x);
-                    tmem_ld16(lanes + OA_COL + c0, y);
-                    tmem_wait_ld();
-                    if (c0 + 16 == kSlice) {
-                        tcgen05_before_sync();
-                        arrive_warp(o_free);
+                for (int c = base; c < base + pieces && ok; ++c) {
+                    const int n = min(kPiece, tokens - (c - base) * kPiece);
+                    if (!wait(&done[c & 1], c >> 1)) { ok = false; break; }
+                    tcgen05_after_sync();
+                    float fi = ex2_approx(sum) * l.scale, fa = l.scale;
+                    if (c + 1 < base + pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
+                    if constexpr (!BF) {
+                        fi *= s_unit[c & 1];
+                        fa *= row_unit[(c & 3) * kPiece + row];
                     }
+                    const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
+                    const bool poisoned = any_bad[c & 3] != 0;
+                    // All of a row is read before any of it is stored, for the next product waits for that (117 us for 64 pieces,
+                    // in slices 142); where a CTA goes on with other work, whose loop wants registers too, in slices (packed
+                    // prompts 277 us, whole 317).
+                    constexpr int WORDS = MORE ? 8 : kSlice / 2;
+                    uint32_t w[WORDS];
+                    auto out_words = [&](char* to) {
+                        if (row < n) {
+                            if (sectors) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
-                        w[(c0 + j) / 2] = M::pack(z.x, z.y);
+                                for (int j = 0; j < WORDS; j += 8)
+                                    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + j * 4), "r"(w[j]),
+                                                 "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]),
+                                                 "r"(w[j + 6]), "r"(w[j + 7])
+                                                 : "memory");
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < WORDS; j += 4)
+                                    *reinterpret_cast<uint4*>(to + j * 4) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                            }
+                        }
+                    };
+                    constexpr int AT_ONCE = MORE ? 1 : kSlice / 16;
+#pragma unroll AT_ONCE
+                    for (int c0 = 0; c0 < kSlice; c0 += 16) {
+                        float x[16], y[16];
+                        tmem_ld16(lanes + OI_COL + c0, x);
+                        tmem_ld16(lanes + OA_COL + c0, y);
+                        tmem_wait_ld();
+                        if (c0 + 16 == kSlice) {
+                            tcgen05_before_sync();
+                            arrive_warp(o_free);
+                        }
+                        const int w0 = MORE ? 0 : c0 / 2;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
+                            w[w0 + j / 2] = M::pack(z.x, z.y);
+                        }
+                        if (poisoned) {
+                            const uint8_t* mark = &bad[(c & 3) * 64 + c0];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (mark[j] <= row) w[w0 + j / 2] |= 0x7fffu << (16 * (j & 1));
+                        }
+                        if (MORE) out_words(out + c0 * sizeof(T));
+                    }
+                    if (!MORE) out_words(out);
+                    out += kPiece * pitch;
+                    if (poisoned) {  // the columns' marks are used again four pieces on
+                        if (!meet(2)) { ok = false; break; }
+                        if (row < 64) bad[(c & 3) * 64 + row] = kPiece;
+                        if (row == 0) any_bad[c & 3] = 0;
                     }
                 }
-                if (poisoned) {
-                    const uint8_t* mark = &bad[(c & 3) * 64];
-#pragma unroll
-                    for (int j = 0; j < kSlice / 2; ++j) {
-                        if (mark[2 * j] <= row) w[j] |= 0x7fffu;
-                        if (mark[2 * j + 1] <= row) w[j] |= 0x7fffu << 16;
-                    }
-                }
-                if (row < n) {
-                    if (sectors) {
-#pragma unroll
-                        for (int j = 0; j < kSlice / 2; j += 8)
-                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + j * 4), "r"(w[j]),
-                                         "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]), "r"(w[j + 5]), "r"(w[j + 6]),
-                                         "r"(w[j + 7])
-                                         : "memory");
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kSlice / 2; j += 4)
-                            *reinterpret_cast<uint4*>(out + j * 4) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-                    }
-                }
-                out += kPiece * pitch;
-                if (poisoned) {  // the columns' marks are used again four pieces on
-                    if (!meet(2)) { ok = false; break; }
-                    if (row < 64) bad[(c & 3) * 64 + row] = kPiece;
-                    if (row == 0) any_bad[c & 3] = 0;
-                }
-            }
+            } while (more());
         }
     } else {
         registers_down<48>();  // (one instruction for the four warps)
@@ -757,25 +853,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // ===================== tensor copies =====================
             if (lane == 0) {
                 int issued_qk = 0, issued = 0;
+                read();
+                while (true) {
+                    const int hq = h / (l.n_v / l.n_qk);
 #pragma unroll 1
-                for (int c = 0; c < pieces; ++c) {
-                    const int st = c & 1;
-                    const int y = t0 + c * kPiece;
-                    if (c >= 2 && ((!STATES && !wait1(&q_free[st], (c >> 1) - 1)) || !wait1(&k_free[st], (c >> 1) - 1))) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
+                    for (int c = base; c < base + pieces; ++c) {
+                        const int st = c & 1;
+                        const int y = t0 + (c - base) * kPiece;
+                        if (c >= 2 && ((!STATES && !wait1(&q_free[st], (c >> 1) - 1)) || !wait1(&k_free[st], (c >> 1) - 1))) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&qk_full[st], (STATES ? 1 : 2) * L::QK);
 #pragma unroll 1
-                    for (int p = 0; p < DK / 64; ++p) {
-                        tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
-                        if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
+                        for (int p = 0; p < DK / 64; ++p) {
+                            tma_rows(sbase + L::K + st * L::QK + p * PANEL, &tm_k, hq * DK + p * 64, y, &qk_full[st]);
+                            if (!STATES) tma_rows(sbase + L::Q + st * L::QK + p * PANEL, &tm_q, hq * DK + p * 64, y, &qk_full[st]);
+                        }
+                        issued_qk = c + 1;
+                        if (!STATES && c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&v_full[st], PANEL);
+                        tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
+                        issued = c + 1;
                     }
-                    issued_qk = c + 1;
-                    if (!STATES && c >= 2 && !wait1(&done[st], (c >> 1) - 1)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&v_full[st], PANEL);
-                    tma_rows(sbase + L::V + st * PANEL, &tm_v, h * a.dv + slice * kSlice, y, &v_full[st]);
-                    issued = c + 1;
+                    base += pieces;
+                    if (!steal || !ok) break;
+                    // Ask for the work behind this one now that its last copies are issued, two pieces before it ends. (Asked at
+                    // the front of the work, the first CTAs took work from some that were about to start.)
+                    mbar_arrive_expect_tx(next_full, 16);
+                    asm volatile(
+                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                            sbase + L::NEXT),
+                        "r"(smem_addr(next_full))
+                        : "memory");
+                    if (!wait1(next_full, taken)) { ok = false; break; }
+                    uint32_t yes, block;
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+                        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                        : "=r"(yes), "=r"(block)
+                        : "r"(sbase + L::NEXT)
+                        : "memory");
+                    fence_proxy_async_smem();  // (the next answer is written there)
+                    ++taken;
+                    if (taken >= 2 && !wait1(&work_free[taken & 1], (taken >> 1) - 1)) { ok = false; break; }
+                    ChunkWork w;
+                    w.valid = 0;
+                    if (yes) {
+                        w = work_of((int)block, true);
+                        w.valid = 1;  // (work, if only to be skipped)
+                    }
+                    work[taken & 1] = w;
+                    mbar_arrive(&work_full[taken & 1]);
+                    if (!yes) break;
+                    read();
                 }
                 // no copy is in flight when the CTA leaves
                 for (int c = max(issued - 2, 0); c < issued_qk; ++c) {
@@ -791,42 +923,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const uint64_t dk = umma_desc_sw128(sbase + L::K, 16, 1024);
                 const uint64_t dv = umma_desc_sw128(sbase + L::V, PANEL, 1024);
                 const uint64_t ds = umma_desc_sw128(sbase + L::S, DK * 128, 1024);
-                for (int c = -1; c < pieces; ++c) {
-                    const uint32_t st = (uint32_t)(c & 1);
-                    if (c >= 0) {  // OI = Q S
-                        if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
-                        tcgen05_after_sync();
-                        const uint64_t q = dq + ((st * L::QK) >> 4);
+                begin1();
+                do {
+                    for (int c = base - 1; c < base + pieces; ++c) {
+                        const uint32_t st = (uint32_t)(c & 1);
+                        if (c >= base) {  // OI = Q S
+                            if (!wait1(s_full, c) || (c > 0 && !wait1(o_free, c - 1))) { ok = false; break; }
+                            tcgen05_after_sync();
+                            const uint64_t q = dq + ((st * L::QK) >> 4);
 #pragma unroll
-                        for (int i = 0; i < DK / 16; ++i)
-                            umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
-                                           ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
-                        umma_commit_cg<1>(s_free);
-                        umma_commit_cg<1>(&q_free[st]);
-                        if (!wait1(w_full, c)) { ok = false; break; }
-                    }
-                    if (c + 1 < pieces) {  // P = Q K^T of the next piece
-                        if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
-                        const uint64_t q = dq + (((st ^ 1) * L::QK) >> 4), k = dk + (((st ^ 1) * L::QK) >> 4);
-                        tcgen05_after_sync();
-#pragma unroll
-                        for (int i = 0; i < DK / 16; ++i) {
-                            const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
-                            umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
+                            for (int i = 0; i < DK / 16; ++i)
+                                umma_f16_cg<1>(tmem + OI_COL, q + (((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4),
+                                               ds + (uint32_t)i * (2048 >> 4), IDESC_O, i > 0);
+                            umma_commit_cg<1>(s_free);
+                            umma_commit_cg<1>(&q_free[st]);
+                            if (!wait1(w_full, c)) { ok = false; break; }
                         }
-                        umma_commit_cg<1>(p_full);
-                    }
-                    if (c >= 0) {  // OA = P' V
-                        if (!wait1(&v_clean[st], c >> 1)) { ok = false; break; }
-                        tcgen05_after_sync();
-                        const uint64_t v = dv + ((st * PANEL) >> 4);
+                        if (c + 1 < base + pieces) {  // P = Q K^T of the next piece
+                            if (!wait1(&qk_full[st ^ 1], (c + 1) >> 1)) { ok = false; break; }
+                            const uint64_t q = dq + (((st ^ 1) * L::QK) >> 4), k = dk + (((st ^ 1) * L::QK) >> 4);
+                            tcgen05_after_sync();
 #pragma unroll
-                        for (int i = 0; i < kPiece / 16; ++i)
-                            umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + st * 64 + i * 8, v + (uint32_t)i * (2048 >> 4),
-                                                  IDESC_O, i > 0);
-                        umma_commit_cg<1>(&done[st]);
+                            for (int i = 0; i < DK / 16; ++i) {
+                                const uint32_t off = ((uint32_t)(i >> 2) * PANEL + (uint32_t)(i & 3) * 32) >> 4;
+                                umma_f16_cg<1>(tmem + P_COL, q + off, k + off, IDESC_P, i > 0);
+                            }
+                            umma_commit_cg<1>(p_full);
+                        }
+                        if (c >= base) {  // OA = P' V
+                            if (!wait1(&v_clean[st], c >> 1)) { ok = false; break; }
+                            tcgen05_after_sync();
+                            const uint64_t v = dv + ((st * PANEL) >> 4);
+#pragma unroll
+                            for (int i = 0; i < kPiece / 16; ++i)
+                                umma_f16_tmem_a_cg<1>(tmem + OA_COL, tmem + PW_COL + st * 64 + i * 8, v + (uint32_t)i * (2048 >> 4),
+                                                      IDESC_O, i > 0);
+                            umma_commit_cg<1>(&done[st]);
+                        }
                     }
-                }
+                } while (more1());
                 // every product is done before tensor memory is given back
                 umma_commit_cg<1>(&all_done[0]);
                 ok = wait1(&all_done[0], 0) && ok;
@@ -839,27 +974,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // K^T: 64 rows of the product a panel; at dim_k = 64 the second 64 are the first again
                 const uint64_t dkt = umma_desc_sw128(sbase + L::K, DK == 128 ? PANEL : 0, 1024);
                 const uint64_t dvt = umma_desc_sw128(sbase + L::VT, 4096, 1024);
-                for (int c = 0; c < pieces && ok; ++c) {
-                    const uint32_t st = (uint32_t)(c & 1);
-                    if (!wait1(&qk_full[st], c >> 1) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
-                    uint64_t kt = dkt + ((st * L::QK) >> 4), vt = dvt;
+                begin1();
+                do {
+                    for (int c = base; c < base + pieces && ok; ++c) {
+                        const uint32_t st = (uint32_t)(c & 1);
+                        if (!wait1(&qk_full[st], c >> 1) || (c > 0 && !wait1(u_free, c - 1))) { ok = false; break; }
+                        uint64_t kt = dkt + ((st * L::QK) >> 4), vt = dvt;
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        if (!wait1(&vt_full[q], c)) { ok = false; break; }
-                        tcgen05_after_sync();
+                        for (int q = 0; q < 4; ++q) {
+                            if (!wait1(&vt_full[q], c)) { ok = false; break; }
+                            tcgen05_after_sync();
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint64_t ka = kt + k * (2048 >> 4), vb = vt + k * (2048 >> 4);
-                            umma_f16_cg<1>(tmem + U_COL, ka, vb, IDESC_U, q > 0 || k > 0);
-                            if (NT == 3) umma_f16_cg<1>(tmem + U_COL + 64, ka, vb + (2 * 4096 >> 4), IDESC_U3, true);
+                            for (int k = 0; k < 2; ++k) {
+                                const uint64_t ka = kt + k * (2048 >> 4), vb = vt + k * (2048 >> 4);
+                                umma_f16_cg<1>(tmem + U_COL, ka, vb, IDESC_U, q > 0 || k > 0);
+                                if (NT == 3) umma_f16_cg<1>(tmem + U_COL + 64, ka, vb + (2 * 4096 >> 4), IDESC_U3, true);
+                            }
+                            umma_commit_cg<1>(&vt_free[q]);
+                            kt += 4096 >> 4, vt += L::QUARTER >> 4;
                         }
-                        umma_commit_cg<1>(&vt_free[q]);
-                        kt += 4096 >> 4, vt += L::QUARTER >> 4;
+                        if (!ok) break;
+                        umma_commit_cg<1>(u_full);
+                        umma_commit_cg<1>(&k_free[st]);
                     }
-                    if (!ok) break;
-                    umma_commit_cg<1>(u_full);
-                    umma_commit_cg<1>(&k_free[st]);
-                }
+                } while (more1());
                 umma_commit_cg<1>(&all_done[1]);
                 ok = wait1(&all_done[1], 0) && ok;
                 if (!ok) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
@@ -877,55 +1015,58 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     raw[b] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
                 }
             };
-            fetch(0);
+            begin();
+            do {
+                fetch(0);
 #pragma unroll 1
-            for (int c = 0; c < pieces; ++c) {
-                float front[4], back[4], all[4], grow = 0.f;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums; NaN stays
-                    float y = raw[b] < -104.f ? -104.f : raw[b];
-                    y = (y > 1e4f ? 1e4f : y) * 1.44269504f;
-                    grow += fmaxf(y, 0.f);
-                    front[b] = y;
-                    back[b] = __shfl_down_sync(0xffffffffu, y, 1);
-                    if (lane == 31) back[b] = 0.f;
-                }
-                if (c + 1 < pieces) fetch(c + 1);
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2)
+                for (int c = base; c < base + pieces; ++c) {
+                    float front[4], back[4], all[4], grow = 0.f;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        const float f = __shfl_up_sync(0xffffffffu, front[b], o), k = __shfl_down_sync(0xffffffffu, back[b], o);
-                        if (lane >= o) front[b] += f;
-                        if (lane + o < 32) back[b] += k;
+                        // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums; NaN stays
+                        float y = raw[b] < -104.f ? -104.f : raw[b];
+                        y = (y > 1e4f ? 1e4f : y) * 1.44269504f;
+                        grow += fmaxf(y, 0.f);
+                        front[b] = y;
+                        back[b] = __shfl_down_sync(0xffffffffu, y, 1);
+                        if (lane == 31) back[b] = 0.f;
                     }
+                    if (c + 1 < base + pieces) fetch(c + 1 - base);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[b], 31);
-                if (__any_sync(0xffffffffu, grow != 0.f)) {
+                    for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float f = __shfl_up_sync(0xffffffffu, front[b], o), k = __shfl_down_sync(0xffffffffu, back[b], o);
+                            if (lane >= o) front[b] += f;
+                            if (lane + o < 32) back[b] += k;
+                        }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[b], 31);
+                    if (__any_sync(0xffffffffu, grow != 0.f)) {
 #pragma unroll 1
-                    for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
-                }
-                if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
-                Gates& g = gates[c & 1];
+                        for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
+                    }
+                    if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
+                    Gates& g = gates[c & 1];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    g.hi[b * 32 + lane] = -front[b];
-                    g.col[b * 32 + lane] = ex2_approx(back[b]);
+                    for (int b = 0; b < 4; ++b) {
+                        g.hi[b * 32 + lane] = -front[b];
+                        g.col[b * 32 + lane] = ex2_approx(back[b]);
+                    }
+                    const float sum = (all[0] + all[1]) + (all[2] + all[3]);
+                    if (lane < 4) {
+                        g.block[lane] = lane == 0 ? all[0] : lane == 1 ? all[1] : lane == 2 ? all[2] : all[3];
+                        g.after[lane] = ex2_approx(lane == 0 ? all[1] + (all[2] + all[3]) : lane == 1 ? all[2] + all[3] : lane == 2 ? all[3] : 0.f);
+                    } else if (lane == 4) {
+                        const bool small = sum > -0.7f && sum < 0.7f;
+                        g.keep = small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
+                        g.once = small ? 1.f : 0.f;
+                        g.grow = grow;
+                        g.sum = sum;
+                    }
+                    arrive_warp(&g_full[c & 1]);
                 }
-                const float sum = (all[0] + all[1]) + (all[2] + all[3]);
-                if (lane < 4) {
-                    g.block[lane] = lane == 0 ? all[0] : lane == 1 ? all[1] : lane == 2 ? all[2] : all[3];
-                    g.after[lane] = ex2_approx(lane == 0 ? all[1] + (all[2] + all[3]) : lane == 1 ? all[2] + all[3] : lane == 2 ? all[3] : 0.f);
-                } else if (lane == 4) {
-                    const bool small = sum > -0.7f && sum < 0.7f;
-                    g.keep = small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
-                    g.once = small ? 1.f : 0.f;
-                    g.grow = grow;
-                    g.sum = sum;
-                }
-                arrive_warp(&g_full[c & 1]);
-            }
+            } while (more());
         }
     }
     if (!ok && lane == 0) atomicOr(l.status, (unsigned)PKV_DEV_WAIT_TIMEOUT);
@@ -935,12 +1076,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (warp == 25) tmem_dealloc_cg<1>(tmem, 512);
 }
 
-template <typename T, int DK, bool STATES>
+template <typename T, int DK, bool STATES, bool MORE>
 cudaError_t run_chunk(const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                       cudaStream_t stream) {
     static unsigned long long attr_done = 0;  // one bit a device
     constexpr uint32_t smem = ChunkSmem<T, DK>::ALLOC;
-    auto kern = linear_chunk_kernel<T, DK, STATES>;
+    auto kern = linear_chunk_kernel<T, DK, STATES, MORE>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -963,14 +1104,21 @@ cudaError_t run_chunk(const ChunkArgs& a, const CUtensorMap& q, const CUtensorMa
     return cudaLaunchKernelEx(&cfg, kern, a, q, k, v);
 }
 
+template <typename T, int DK>
+cudaError_t launch_linear_chunk_dim(const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                    cudaStream_t stream) {
+    if (a.take_more) return run_chunk<T, DK, false, true>(a, q, k, v, stream);
+    if (a.n_segs > 1) {
+        const cudaError_t err = run_chunk<T, DK, true, false>(a, q, k, v, stream);
+        if (err != cudaSuccess) return err;
+    }
+    return run_chunk<T, DK, false, false>(a, q, k, v, stream);
+}
+
 template <typename T>
 cudaError_t launch_linear_chunk_dtype(int dk, const ChunkArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                       const CUtensorMap& v, cudaStream_t stream) {
-    if (a.n_segs > 1) {
-        const cudaError_t err = dk == 64 ? run_chunk<T, 64, true>(a, q, k, v, stream) : run_chunk<T, 128, true>(a, q, k, v, stream);
-        if (err != cudaSuccess) return err;
-    }
-    return dk == 64 ? run_chunk<T, 64, false>(a, q, k, v, stream) : run_chunk<T, 128, false>(a, q, k, v, stream);
+    return dk == 64 ? launch_linear_chunk_dim<T, 64>(a, q, k, v, stream) : launch_linear_chunk_dim<T, 128>(a, q, k, v, stream);
 }
 
 }  // namespace pkv
