@@ -172,12 +172,6 @@ __device__ __forceinline__ uint32_t elect_one() {
     return p;
 }
 
-__device__ __forceinline__ float2 f2_get(uint64_t v) {
-    float2 r;
-    f2_unpack(v, r.x, r.y);
-    return r;
-}
-
 // mbar_wait_bounded in few instructions (28 warps of seven roles share the instruction caches): a thread sleeps up to a
 // microsecond in each try, and gives up after as many as make about a second.
 __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {

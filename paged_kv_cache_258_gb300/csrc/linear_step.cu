@@ -20,8 +20,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 128;
-// Tokens staged in shared memory at a time. 16 where a token's latency counts (columns of 32, 500 tokens of 8 heads x 64 x
-// 64 in fp32: 73 us, in steps of 8 83, of 4 106) and where a whole short chunk fits; 8 for many long fp32 rows (256 tokens of
+// Tokens staged in shared memory at a time: 16 where a whole short chunk fits, 8 for many long fp32 rows (256 tokens of
 // 8 x 32 heads x 128 x 128: 172 us against 189).
 template <typename T, int NC>
 constexpr int kStep = sizeof(T) == 2 || NC == 32 ? 16 : 8;
@@ -192,6 +191,247 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
     }
 }
 
+// The same for chunks of few heads, where what counts is how long a token takes one warp: NC is 32 or 16, 16 threads take
+// a row, each with NC / 16 adjacent columns and an eighth of the rows as pairs of rows, which packed arithmetic takes at
+// once (k and q come from shared memory as pairs already, v and decays twice each), four tokens at a time. Tokens are
+// staged in two buffers, one barrier a step: behind it the results of the step before are summed up and the next step's
+// rows are asked for.
+constexpr int kRowLanes = 16;
+constexpr int kGroups = kThreads / kRowLanes;  // row groups
+
+// n adjacent floats
+template <int n>
+struct Floats;
+template <>
+struct Floats<1> {
+    using type = float;
+    __device__ __forceinline__ static void get(float v, float (&x)[1]) { x[0] = v; }
+    __device__ __forceinline__ static float put(const float (&x)[1]) { return x[0]; }
+};
+template <>
+struct Floats<2> {
+    using type = float2;
+    __device__ __forceinline__ static void get(float2 v, float (&x)[2]) { x[0] = v.x, x[1] = v.y; }
+    __device__ __forceinline__ static float2 put(const float (&x)[2]) { return make_float2(x[0], x[1]); }
+};
+template <>
+struct Floats<4> {
+    using type = float4;
+    __device__ __forceinline__ static void get(float4 v, float (&x)[4]) { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+    __device__ __forceinline__ static float4 put(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+};
+
+template <typename T, int DK, int DV, int NC>
+__global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs a) {
+    constexpr int TB = DK * NC <= 2048 ? 16 : 8;  // tokens staged at a time
+    constexpr int SLICES = DV / NC;
+    constexpr int C = NC / kRowLanes;             // columns of a thread
+    constexpr int R = DK / kGroups;               // and rows
+    constexpr int N = Vec16<T>::N;
+    constexpr int QV = TB * DK / N, VV = TB * NC / N;  // 16-byte vectors of a step's q (or k) and v
+    __shared__ __align__(16) float s_q[2][TB][DK];
+    __shared__ __align__(16) float s_k[2][TB][DK];
+    __shared__ __align__(16) float2 s_v[2][TB][NC];  // twice each, as packed products take it
+    // What a token's decay multiplies the state by, and how often the state itself is added: exp(g) and 0, or
+    // exp(g) - 1 and 1.
+    __shared__ __align__(16) float4 s_d[2][TB];  // (twice each)
+    __shared__ __align__(16) float s_o[2][TB][kThreads / 32][NC];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slice = blockIdx.x % SLICES;
+    const long long unit = blockIdx.x / SLICES;
+    const int h = (int)(unit % a.n_v), s = (int)(unit / a.n_v);
+    const int hq = h / (a.n_v / a.n_qk);
+    const int q0 = a.q_start[s], q1 = a.q_start[s + 1];
+    const int src = a.src[s], dst = a.dst[s];
+    const bool bad_range = q0 < 0 || q1 < q0 || q1 > a.n_tokens || q1 - q0 > a.max_query;
+    const bool bad_slot = src >= a.n_slots || dst >= a.n_slots;
+    if (bad_range || bad_slot) {
+        if (h == 0 && slice == 0 && tid == 0)
+            atomicOr(a.status, (bad_range ? (unsigned)PKV_DEV_BAD_QUERY_RANGE : 0u) |
+                                   (bad_slot ? (unsigned)PKV_DEV_BAD_STATE_SLOT : 0u));
+        return;
+    }
+    const int col = (tid % kRowLanes) * C, row0 = (tid / kRowLanes) * R;
+    const size_t head = (size_t)DK * DV;
+    const size_t at = (size_t)row0 * DV + slice * NC + col;
+    using Cols = typename Floats<C>::type;
+    uint64_t x[C][R / 2];  // pairs of rows
+    {
+        float y[R][C];
+        if (src >= 0) {
+            const float* p = a.state + ((size_t)src * a.n_v + h) * head + at;
+#pragma unroll
+            for (int i = 0; i < R; ++i) Floats<C>::get(__ldcs(reinterpret_cast<const Cols*>(p + (size_t)i * DV)), y[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int c = 0; c < C; ++c) y[i][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i)
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[c][i] = f2_pack(y[2 * i][c], y[2 * i + 1][c]);
+    }
+    const T* q = static_cast<const T*>(a.q);
+    const T* k = static_cast<const T*>(a.k);
+    const T* v = static_cast<const T*>(a.v);
+    constexpr int QN = (QV + kThreads - 1) / kThreads, VN = (VV + kThreads - 1) / kThreads;
+    uint4 rq[QN], rk[QN], rv[VN];
+    float rg = 0.f;
+    auto widen = [](const uint4& u, float* to) {
+        float f[N];
+        Vec16<T>::to_float(u, f);
+#pragma unroll
+        for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    };
+    // a step's rows, into registers (tokens past the last are not read) and from there to shared memory
+    auto fetch = [&](int t0) {
+        const int n = min(TB, q1 - t0);
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = (i * kThreads + tid) * N, t = e / DK;
+            if (t < n) {
+                const size_t from = ((size_t)(t0 + t) * a.n_qk + hq) * DK + e % DK;
+                rq[i] = *reinterpret_cast<const uint4*>(q + from);
+                rk[i] = *reinterpret_cast<const uint4*>(k + from);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int e = (i * kThreads + tid) * N, t = e / NC;
+            if (t < n) rv[i] = *reinterpret_cast<const uint4*>(v + ((size_t)(t0 + t) * a.n_v + h) * DV + slice * NC + e % NC);
+        }
+        if (tid < n) rg = a.log_decay ? a.log_decay[(size_t)(t0 + tid) * a.decay_stride + h] : 0.f;
+    };
+    auto stage = [&](int t0, int b) -> bool {  // whether any token's decay is not a slow one
+        const int n = min(TB, q1 - t0);
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = (i * kThreads + tid) * N;
+            if (e / DK < n) {
+                widen(rq[i], &s_q[b][0][0] + e);
+                widen(rk[i], &s_k[b][0][0] + e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int e = (i * kThreads + tid) * N;
+            if (e / NC < n) {
+                float f[N];
+                Vec16<T>::to_float(rv[i], f);
+                float4* to = reinterpret_cast<float4*>(&s_v[b][0][0] + e);
+#pragma unroll
+                for (int j = 0; j < N; j += 2) to[j / 2] = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
+            }
+        }
+        if (tid >= n) return false;
+        const bool slow = rg > -0.5f && rg < 0.5f;
+        const float d = slow ? expm1f(rg) : expf(rg), once = slow ? 1.f : 0.f;
+        s_d[b][tid] = make_float4(d, d, once, once);
+        return !slow;
+    };
+    auto results = [&](int t0, int b) {
+        const int n = min(TB, q1 - t0);
+#pragma unroll 1
+        for (int e = tid; e < n * NC; e += kThreads) {
+            const int t = e / NC, c = e % NC;
+            const float sum = (s_o[b][t][0][c] + s_o[b][t][1][c]) + (s_o[b][t][2][c] + s_o[b][t][3][c]);
+            static_cast<T*>(a.out)[((size_t)(t0 + t) * a.n_v + h) * DV + slice * NC + c] = from_float<T>(sum * a.scale);
+        }
+    };
+    int b = 0;
+    if (q0 < q1) {
+        fetch(q0);
+        bool fast = stage(q0, 0);
+        for (int t0 = q0; t0 < q1; t0 += TB) {
+            const int n = min(TB, q1 - t0);
+            const bool any = __syncthreads_or(fast);
+            if (t0 + TB < q1) fetch(t0 + TB);
+            if (t0 > q0) results(t0 - TB, b ^ 1);
+            // G tokens at once: what they read is on its way before the first is worked out, and a token's products need
+            // only the state that the one before left
+            auto tokens = [&](auto slow, auto count, int t) {
+                constexpr bool SLOW = decltype(slow)::value;
+                constexpr int G = decltype(count)::value;
+                uint64_t d2[G], once2[G], v2[G][C], o2[G][C];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s_d[b][t + g]);
+                    d2[g] = d.x, once2[g] = d.y;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) v2[g][c] = reinterpret_cast<const uint64_t*>(&s_v[b][t + g][col])[c];
+                }
+#pragma unroll
+                for (int i = 0; i < R; i += 4) {
+                    ulonglong2 k4[G], q4[G];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        k4[g] = *reinterpret_cast<const ulonglong2*>(&s_k[b][t + g][row0 + i]);
+                        q4[g] = *reinterpret_cast<const ulonglong2*>(&s_q[b][t + g][row0 + i]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint64_t kk = j == 0 ? k4[g].x : k4[g].y, qq = j == 0 ? q4[g].x : q4[g].y;
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                uint64_t& y = x[c][i / 2 + j];
+                                y = f2_fma(y, d2[g], f2_fma(kk, v2[g][c], SLOW ? y : f2_mul(y, once2[g])));
+                                o2[g][c] = i + j == 0 ? f2_mul(qq, y) : f2_fma(qq, y, o2[g][c]);
+                            }
+                        }
+                }
+                float o[G][C];
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float2 y = f2_get(o2[g][c]);
+                        o[g][c] = y.x + y.y;
+                    }
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) o[g][c] += __shfl_xor_sync(0xffffffffu, o[g][c], kRowLanes);
+                if (lane < kRowLanes) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) *reinterpret_cast<Cols*>(&s_o[b][t + g][warp][col]) = Floats<C>::put(o[g]);
+                }
+            };
+            auto all = [&](auto slow) {
+                int t = 0;
+#pragma unroll 1
+                for (; t + 4 <= n; t += 4) tokens(slow, std::integral_constant<int, 4>{}, t);
+#pragma unroll 1
+                for (; t < n; ++t) tokens(slow, std::integral_constant<int, 1>{}, t);
+            };
+            if (!any)
+                all(std::true_type{});
+            else
+                all(std::false_type{});
+            if (t0 + TB < q1) fast = stage(t0 + TB, b ^ 1);
+            b ^= 1;
+        }
+        __syncthreads();
+        results(q0 + (q1 - 1 - q0) / TB * TB, b ^ 1);
+    }
+    if (dst >= 0) {
+        float* p = a.state + ((size_t)dst * a.n_v + h) * head + at;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float y[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float2 z = f2_get(x[c][i / 2]);
+                y[c] = i % 2 ? z.y : z.x;
+            }
+            __stcs(reinterpret_cast<Cols*>(p + (size_t)i * DV), Floats<C>::put(y));
+        }
+    }
+}
+
 template <typename T, int DK, int DV, int NC>
 cudaError_t run(const LinearArgs& a, cudaStream_t stream) {
     const unsigned ctas = (unsigned)a.n_seqs * a.n_v * (DV / NC);
@@ -202,10 +442,24 @@ cudaError_t run(const LinearArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <typename T, int DK, int DV, int NC>
+cudaError_t walk(const LinearArgs& a, cudaStream_t stream) {
+    linear_walk_kernel<T, DK, DV, NC><<<(unsigned)a.n_seqs * a.n_v * (DV / NC), kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, int DK, int DV>
 cudaError_t pick(int sms, const LinearArgs& a, cudaStream_t stream) {
-    // columns of 64 while there are enough of them to fill the GPU, else of 32
-    return (long long)a.n_seqs * a.n_v * (DV / 64) >= 2LL * sms ? run<T, DK, DV, 64>(a, stream) : run<T, DK, DV, 32>(a, stream);
+    // In units of 64 columns: columns of 64 from two units an SM on, else of 32. Chunks of up to two units for three SMs
+    // take columns of 16 and packed pairs of rows (500 tokens of 24 units of 64 x 64 in fp32: 43 us, against 73 in columns of
+    // 32; 256 tokens of 64 units of 128 x 64: 38.5 and 46.2; of 128 units 72.8 and 65.1), and at dim_k = 64 the others pairs
+    // in columns of 32 (500 tokens of 128 units 71 us against 91; at 128 rows nothing is gained).
+    const long long units = (long long)a.n_seqs * a.n_v * (DV / 64);
+    if (a.q_start && units * 3 <= 2LL * sms) return walk<T, DK, DV, 16>(a, stream);
+    if (units >= 2LL * sms) return run<T, DK, DV, 64>(a, stream);
+    if constexpr (DK == 64)
+        if (a.q_start) return walk<T, DK, DV, 32>(a, stream);
+    return run<T, DK, DV, 32>(a, stream);
 }
 
 template <typename T>
