@@ -11,6 +11,11 @@
 // exp(g) S is taken as S + S expm1(g) while exp(g) > 0.6: exp(g) itself, rounded to 24 bits, is off by up to 2^-25
 // whatever g, the same way at every token, which a slow decay (g = -1e-4) would make 2^-11 of what it keeps; expm1
 // is as exact as g is.
+//
+// What bounds it: decode, the states' bytes (bf16, 250 sequences of 32 heads x 128 x 64: 80 us, 6.6 TB/s; fp16, 64 of 32 x
+// 128 x 128: 43.3 us, 6.25 TB/s; one of 48 x 128 x 128: 3 us on the device, a trip to memory and back). Chunks of many
+// sequences, the products' instructions (32 sequences of 16 tokens, 48 x 128 x 128: 68 us, 5.9e12 updates of a state element
+// a second); chunks of few heads, one warp's latency (85 ns a token).
 #include <type_traits>
 
 #include "common.cuh"

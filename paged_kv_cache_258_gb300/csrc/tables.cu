@@ -10,9 +10,11 @@
 // row by bisection (once for the whole warp where the 32 lie in one row). A fresh block's table entry is written
 // with its first token, which this call always holds. Lengths and totals may be written over what they were read
 // from, so one CTA alone writes them: behind its tokens where it does the whole call, in a launch of its own behind the
-// CTAs that share many tokens.
+// CTAs that share many tokens, which counts while they work and writes when they are done.
 //
-// Bound by latency: the counts, the scan, free ids, stores one after the other.
+// Bound by latency: the counts, the scan, free ids, stores one after the other. 64 rows of a token each 3 us on the device,
+// 1,000 rows of 288,070 tokens 5.6 (41 by one CTA; 7.4 where the rows' launch does not begin early). Calls behind one another
+// take 6 and 8 us.
 #include "common.cuh"
 #include "linear.h"
 
@@ -58,6 +60,7 @@ __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a
     __shared__ unsigned s_block[kRows]; // its first free block, counted from `used`
     __shared__ int s_first;             // the tile's first row that does not fit
     __shared__ unsigned s_tok, s_blk;   // tokens and blocks up to the tile's end
+    if (!ROWS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the rows' launch may begin to count
     const int tid = threadIdx.x, lane = tid & 31;
     const int cta = blockIdx.x, ctas = gridDim.x;
     const unsigned warp_of_all = cta * (kRows / 32) + (tid >> 5), warps = ctas * (kRows / 32);
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(kRows) extend_tables_kernel(const ExtendArgs a
     if (flags && (cta == 0 || (flags & ~row_flags))) atomicOr(a.status, flags);
     if constexpr (ROWS) {
         if (tid == 0) a.query_start[a.n_seqs] = (int)tok;
+        if (!TOKENS) grid_dependency_wait();  // the tokens' CTAs have read the lengths and `used`
         __syncthreads();  // the lengths and `used` have been read, query_start is written
         if (a.n_seqs <= kRows) {
             if (tid < a.n_seqs) a.new_lens[tid] = my_len + my_new;
@@ -175,7 +179,17 @@ cudaError_t launch_extend_tables(const ExtendArgs& a, cudaStream_t stream, int s
     } else {
         const long long ctas = ((long long)a.max_tokens + kEach - 1) / kEach;
         extend_tables_kernel<true, false><<<(unsigned)(ctas < sms ? ctas : sms), kRows, 0, stream>>>(a);
-        extend_tables_kernel<false, true><<<1, kRows, 0, stream>>>(a);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(kRows);
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t err = cudaLaunchKernelEx(&cfg, extend_tables_kernel<false, true>, a);
+        if (err != cudaSuccess) return err;
         *n_launches = 2;
     }
     return cudaGetLastError();
