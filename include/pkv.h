@@ -593,7 +593,7 @@ uint64_t pkv_linear_state_bytes(const pkv_linear_desc* desc);
  *   dst_slots     device int32 [n_seqs]: the slot its state after the call goes to; negative: it is not kept. May
  *                 be its src slot. No two sequences write one slot and none reads a slot that another one writes
  *                 (else those states are unspecified); any number may read one slot, as forks of a prefix do
- *   q, k, v, out  16-byte aligned
+ *   q, k, v, out  16-byte aligned; out overlaps none of the inputs
  * A sequence with a slot >= n_slots is skipped whole, its row of out left unwritten, and sets
  * PKV_DEV_BAD_STATE_SLOT. Sums and the state are fp32; out is rounded to desc->dtype. n_seqs at most 65,535.
  */
@@ -618,7 +618,8 @@ size_t pkv_linear_prefill_workspace_bytes(const pkv_linear_desc* desc, int32_t n
  * of the current device (else PKV_ERR_INVALID_ARG). In pieces the weight of a pair of tokens and the state as q reads
  * it are rounded to the type once each, as attention weights are; the state itself stays fp32. An infinity in v counts
  * as NaN there. What is not finite reaches its own and later tokens of its sequence only, v in its own columns.
- * An empty chunk leaves its sequence's state in dst_slots as it was. A
+ * An empty chunk leaves its sequence's state in dst_slots as it was
+ * (without any token q, k, v and out may be NULL). A
  * sequence whose range is outside [0, n_tokens], negative or longer than max_query_len is skipped whole and sets
  * PKV_DEV_BAD_QUERY_RANGE; one with a bad slot, PKV_DEV_BAD_STATE_SLOT.
  */

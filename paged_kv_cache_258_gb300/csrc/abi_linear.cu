@@ -10,11 +10,11 @@ size_t layer_floats(const pkv_linear_desc* d) {
     return (size_t)d->n_slots * d->n_v_heads * d->dim_k * d->dim_v;
 }
 
-// What decode and prefill check alike; layer's arguments into a.
+// What decode and prefill check alike; layer's arguments into a. rows: whether there are any tokens.
 int linear_args(const pkv_linear_desc* d, int32_t layer, const void* q, const void* k, const void* v,
                 const float* log_decay, int64_t decay_stride, float* state, const int32_t* src, const int32_t* dst,
-                int32_t n_seqs, float scale, void* out, pkv::LinearArgs* a) {
-    if (!q || !k || !v || !state || !src || !dst || !out) return PKV_ERR_INVALID_ARG;
+                int32_t n_seqs, float scale, void* out, bool rows, pkv::LinearArgs* a) {
+    if ((rows && (!q || !k || !v || !out)) || !state || !src || !dst) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state) || !aligned4(src) ||
         !aligned4(dst))
         return PKV_ERR_INVALID_ARG;
@@ -126,7 +126,7 @@ int pkv_linear_decode(const pkv_linear_desc* d, int32_t layer, const void* q, co
     if (layer < 0 || layer >= d->n_layers || n_seqs < 0) return PKV_ERR_INVALID_ARG;
     if (n_seqs == 0) return PKV_OK;
     pkv::LinearArgs a;
-    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, &a);
+    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, true, &a);
     if (rc != PKV_OK) return rc;
     a.q_start = nullptr;
     a.n_tokens = n_seqs;
@@ -161,9 +161,11 @@ int pkv_linear_prefill(const pkv_linear_desc* d, int32_t layer, const void* q, c
     if (layer < 0 || layer >= d->n_layers || n_seqs < 0 || n_tokens < 0 || max_query_len < 0 || max_query_len > n_tokens)
         return PKV_ERR_INVALID_ARG;
     if (n_seqs == 0) return PKV_OK;
+    if (n_tokens > 0x7fffff00) return PKV_ERR_UNSUPPORTED;  // (tokens are counted in whole pieces, in 32 bits)
     if (!query_start || !aligned4(query_start)) return PKV_ERR_INVALID_ARG;
     pkv::LinearArgs a;
-    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, &a);
+    rc = linear_args(d, layer, q, k, v, log_decay, decay_stride, state, src_slots, dst_slots, n_seqs, scale, out, n_tokens > 0,
+                     &a);
     if (rc != PKV_OK) return rc;
     a.q_start = query_start;
     a.n_tokens = n_tokens;

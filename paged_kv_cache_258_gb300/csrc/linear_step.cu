@@ -440,10 +440,11 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
 template <typename T, int DK, int DV, int NC>
 cudaError_t run(const LinearArgs& a, cudaStream_t stream) {
     const unsigned ctas = (unsigned)a.n_seqs * a.n_v * (DV / NC);
-    if (a.q_start)
-        linear_step_kernel<T, DK, DV, NC, false><<<ctas, kThreads, 0, stream>>>(a);
-    else
+    if (!a.q_start) {
         linear_step_kernel<T, DK, DV, NC, true><<<ctas, kThreads, 0, stream>>>(a);
+    } else if constexpr (DK == 128 || NC == 64) {  // (others walk)
+        linear_step_kernel<T, DK, DV, NC, false><<<ctas, kThreads, 0, stream>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -511,8 +511,15 @@ class LinearStates:
         self._free.append(self._slot.pop(seq_id))
         self._begun.discard(seq_id)
 
+    def restart(self, seq_id: int) -> None:
+        """seq_id starts from zeros in the next step that lists it."""
+        if seq_id not in self._slot:
+            raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"restart({seq_id})")
+        self._begun.discard(seq_id)
+
     def slots(self, seq_ids):
-        """(src_slots, dst_slots), int32 [n] on the device, for one step over distinct sequences."""
+        """(src_slots, dst_slots), int32 [n] on the device, for one step over distinct sequences. The step counts as
+        run: should it not be, `restart` those that were to begin with it."""
         import torch
         ids = [int(x) for x in seq_ids]
         if len(set(ids)) != len(ids) or any(x not in self._slot for x in ids):

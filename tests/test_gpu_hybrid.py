@@ -176,3 +176,16 @@ def test_states_of_sequences():
     assert states._slot[9] == a
     one([9])
     assert torch.equal(states.state[0, a], first)
+
+
+def test_a_step_that_was_not_run_can_be_taken_back():
+    _, ldesc, _, states = model("f16", 3, 4)
+    states.state.fill_(3.0)                             # what earlier sequences left
+    states.add(1)
+    states.slots([1])                                   # the step that was to begin it is not run
+    states.restart(1)
+    src, dst = states.slots([1])
+    assert src.tolist() == [-1] and dst.tolist() == [states._slot[1]]
+    assert states.slots([1])[0].tolist() == dst.tolist()
+    with pytest.raises(pkv.PkvError):
+        states.restart(2)

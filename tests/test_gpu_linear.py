@@ -351,3 +351,82 @@ def test_offsets_past_32_bits():
     one = run("bf16", q[:1], k[:1], v[:1], d, state, [n_slots - 1], [0], None, decode=True)
     two = run("bf16", q[:1], k[:1], v[:1], d, small, [1], [0], None, decode=True)
     assert torch.equal(one, two) and torch.equal(state[1, 0], small[1, 0])
+
+
+RAGGED = [0, 1, 128, 129, 300, 7, 260, 64]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_more_units_than_the_gpu_holds(dtype, dk, dv):
+    """CTAs go on with others' work: short, empty and long sequences one after the other in one CTA, none of which leaves
+    anything to the next."""
+    n = 24
+    q, k, v, d, state, starts = inputs(dtype, [RAGGED[i % 8] for i in range(n)], 4, 8, dk, dv, seed=31)
+    src, dst = [i if i % 3 else -1 for i in range(n)], [(i + 5) % n if i % 5 else -1 for i in range(n)]
+    src = [x if x < 0 or dst.count(x) == 0 or dst[i] == x else -1 for i, x in enumerate(src)]  # none reads what another writes
+    was = state.clone()
+    first = check(dtype, q, k, v, d, state, src, dst, starts)
+    for _ in range(3):
+        again = was.clone()
+        assert torch.equal(run(dtype, q, k, v, d, again, src, dst, starts), first) and torch.equal(again, state)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_more_units_than_the_gpu_holds_with_bad_ones_among_them(dtype):
+    n = 24
+    q, k, v, d, state, starts = inputs(dtype, [RAGGED[i % 8] for i in range(n)], 4, 8, 64, 64, "head", seed=32)
+    was, own = state.clone(), list(range(n))
+    base = run(dtype, q, k, v, d, state, own, own, starts)
+    # sequences 3 and 12 have no such slot: skipped whole
+    st, src, dst = was.clone(), list(own), list(own)
+    src[3], dst[12] = n + 2, n + 9
+    out = run(dtype, q, k, v, d, st, src, dst, starts)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_STATE_SLOT
+    for s in range(n):
+        rows = slice(int(starts[s]), int(starts[s + 1]))
+        assert torch.equal(out[rows], torch.full_like(out[rows], 7.0) if s in (3, 12) else base[rows])
+        assert torch.equal(st[1, s], was[1, s] if s in (3, 12) else state[1, s])
+    # ranges that end before they start, and longer than said
+    bad = starts.copy()
+    bad[7] = bad[6] - 1
+    out = run(dtype, q, k, v, d, was.clone(), own, own, bad, longest=300)
+    assert pkv.pkv_get_device_status() == pkv.PKV_DEV_BAD_QUERY_RANGE
+    rows = slice(int(starts[8]), int(starts[n]))
+    assert torch.equal(out[rows], base[rows])
+    # what is not finite stays in its sequence, and in v in its column
+    v2, at = v.clone(), int(starts[12]) + 200
+    v2[at, 2, 3] = float("nan")
+    st = was.clone()
+    out = run(dtype, q, k, v2, d, st, own, own, starts)
+    touched = torch.zeros_like(out, dtype=torch.bool)
+    touched[at:int(starts[13]), 2, 3] = True
+    assert torch.isnan(out[touched]).all() and torch.equal(out[~touched], base[~touched])
+    k2 = k.clone()
+    k2[int(starts[4]):int(starts[5])] = float("inf")
+    out = run(dtype, q, k2, v, d, was.clone(), own, own, starts)
+    rest = torch.ones(int(starts[n]), dtype=torch.bool, device="cuda")
+    rest[int(starts[4]):int(starts[5])] = False
+    assert torch.equal(out[:int(starts[n])][rest], base[:int(starts[n])][rest])
+    assert pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("dk,dv,n,n_v", [(64, 64, 30, 4), (64, 128, 30, 4), (128, 64, 20, 4), (128, 128, 30, 4), (64, 64, 4, 2),
+                                         (128, 128, 8, 3)])
+def test_token_after_token_of_some(dtype, dk, dv, n, n_v):
+    """Short chunks of every length up to 33, from few (sequence, head) pairs to some for each multiprocessor."""
+    lens = [(i * 13) % 34 for i in range(1, n + 1)]
+    q, k, v, d, state, starts = inputs(dtype, lens, n_v, n_v, dk, dv, seed=33 + n)
+    check(dtype, q, k, v, d, state, list(range(n)), list(range(n)), starts)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_token_at_all(dtype):
+    """Empty chunks alone: states go from slot to slot, or to zeros."""
+    q, k, v, d, state, starts = inputs(dtype, [0, 0, 0], 1, 2, 64, 64, behind=0)
+    was = state.clone()
+    run(dtype, q, k, v, d, state, [0, -1, 2], [3, 1, -1], starts)
+    want = was.clone()
+    want[1, 3], want[1, 1] = was[1, 0], 0
+    assert torch.equal(state, want) and pkv.pkv_get_device_status() == 0

@@ -196,3 +196,29 @@ def test_replayed_from_a_graph():
         graph.replay()
         want = expect(500, free, want[4][0], want[0], want[3], np.ones(n, dtype=np.int64), n)
         same([x.cpu().numpy() for x in (tt, slots, start, tl, totals)], want)
+
+
+def test_calls_behind_one_another():
+    """Many tokens a call, lengths and the count of blocks in place, without waiting between the calls: what a call's
+    launches read must still be there although the next ones write it."""
+    n, steps = 300, 6
+    rng = np.random.default_rng(9)
+    tables = np.full((n, 30), -1, dtype=np.int64)
+    free = rng.permutation(n * 20)
+    new = [rng.integers(20, 70, n) for _ in range(steps)]
+    most = 70 * n
+    tt = torch.tensor(tables, dtype=torch.int32, device="cuda")
+    tf = torch.tensor(free, dtype=torch.int32, device="cuda")
+    tn = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in new]
+    tl, totals = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (n, 3))
+    slots = [torch.empty(most, dtype=torch.int64, device="cuda") for _ in range(steps)]
+    start = torch.empty(n + 1, dtype=torch.int32, device="cuda")
+    launches = [pkv.extend_tables_launcher(n * 20, tf, totals[:1], tt, tl, x, s, start, tl, totals) for x, s in zip(tn, slots)]
+    for launch in launches:
+        launch()
+    want = (tables, None, None, np.zeros(n, dtype=np.int64), [0])
+    for x, s in zip(new, slots):
+        want = expect(n * 20, free, want[4][0], want[0], want[3], x, most)
+        assert np.array_equal(s.cpu().numpy(), np.asarray(want[1]))
+    same([x.cpu().numpy() for x in (tt, slots[-1], start, tl, totals)], want)
+    assert pkv.pkv_get_device_status() == 0

@@ -106,3 +106,13 @@ def test_overlapping_lengths_are_refused():
     t, lens = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="overlap"):
         pkv.pkv_extend_tables(9, lens, lens[:1], t, lens[:2], None, torch.zeros(4, dtype=torch.int64), lens, lens[1:], lens)
+
+
+def test_rows_may_be_null_without_tokens_only():
+    for bad in (dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(out=NULL)):
+        assert prefill(desc_of(), tok=1, mq=1, **bad) == pkv.PKV_ERR_INVALID_ARG
+    assert prefill(desc_of(), tok=0, mq=0, q=NULL, k=NULL, v=NULL, out=NULL, state=NULL) == pkv.PKV_ERR_INVALID_ARG
+
+
+def test_token_counts_that_32_bits_cannot_round_up_are_refused():
+    assert prefill(desc_of(), tok=2 ** 31 - 1, mq=2 ** 31 - 1) == pkv.PKV_ERR_UNSUPPORTED
