@@ -563,13 +563,13 @@ class DeviceTables:
             self.slots = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=dev)
             self.query_start = torch.zeros(self.n + 1, dtype=torch.int32, device=dev)
             self.totals = torch.zeros(3, dtype=torch.int32, device=dev)  # blocks taken, rows served, new tokens
+        self.stream.synchronize()  # (steps may run on any stream)
 
     def extend(self, new_tokens=None, stream=None) -> None:
         """One step's new tokens: int32 [n] on the device, or one for each row. tables, lens, slots, query_start and
-        totals are those of the step when the launch has run. May be captured."""
+        totals are those of the step when the launch has run: on `stream`, else on the current one, which may be capturing."""
         pkv.pkv_extend_tables(self.cache.desc.num_blocks, self.free, self.totals[:1], self.tables, self.lens, new_tokens,
-                              self.slots, self.query_start, self.lens, self.totals,
-                              stream=self.stream if stream is None else stream)
+                              self.slots, self.query_start, self.lens, self.totals, stream=stream)
 
     def follow(self, new_tokens=None) -> int:
         """The manager's part of one extend, with the same counts (host integers); returns the rows served."""

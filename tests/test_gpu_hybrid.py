@@ -189,3 +189,21 @@ def test_a_step_that_was_not_run_can_be_taken_back():
     assert states.slots([1])[0].tolist() == dst.tolist()
     with pytest.raises(pkv.PkvError):
         states.restart(2)
+
+
+def test_a_step_is_captured_on_the_current_stream():
+    _, _, cache, _ = model("f16", 2, 40)
+    for x in (1, 2):
+        cache.add_sequence(x, 0)
+    tables = DeviceTables(cache, [1, 2], 8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tables.extend()
+    assert tables.lens.tolist() == [0, 0]               # captured, not run
+    for _ in range(40):
+        graph.replay()
+    assert tables.lens.tolist() == [40, 40] and tables.totals.tolist() == [6, 2, 2]
+    for _ in range(40):
+        assert tables.follow() == 2
+    rc, host, lens = cache.mgr.pack_tables([1, 2], 8)
+    assert np.array_equal(tables.tables.cpu().numpy(), host) and list(lens) == [40, 40]
