@@ -15,7 +15,7 @@
 // What bounds it: decode, the states' bytes (bf16, 250 sequences of 32 heads x 128 x 64: 80 us, 6.6 TB/s; fp16, 64 of 32 x
 // 128 x 128: 43.3 us, 6.25 TB/s; one of 48 x 128 x 128: 3 us on the device, a trip to memory and back). Chunks of many
 // sequences, the products' instructions (32 sequences of 16 tokens, 48 x 128 x 128: 68 us, 5.9e12 updates of a state element
-// a second); chunks of few heads, one warp's latency (85 ns a token).
+// a second); chunks of few heads, one warp's latency (60 ns a token).
 #include <type_traits>
 
 #include "common.cuh"
@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearArgs 
 // a row, each with NC / 16 adjacent columns and an eighth of the rows as pairs of rows, which packed arithmetic takes at
 // once (k and q come from shared memory as pairs already, v and decays twice each), four tokens at a time. Tokens are
 // staged in two buffers, one barrier a step: behind it the results of the step before are summed up and the next step's
-// rows are asked for.
+// rows are asked for. HELPERS more threads do both for the four warps that walk, where there is room: a step of 16 tokens
+// takes those 0.7 us and everything else 0.65.
 constexpr int kRowLanes = 16;
 constexpr int kGroups = kThreads / kRowLanes;  // row groups
 
@@ -226,8 +227,8 @@ struct Floats<4> {
     __device__ __forceinline__ static float4 put(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
 };
 
-template <typename T, int DK, int DV, int NC>
-__global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs a) {
+template <typename T, int DK, int DV, int NC, int HELPERS>
+__global__ void __launch_bounds__(kThreads + HELPERS, HELPERS ? 2 : 0) linear_walk_kernel(const LinearArgs a) {
     constexpr int TB = DK * NC <= 2048 ? 16 : 8;  // tokens staged at a time
     constexpr int SLICES = DV / NC;
     constexpr int C = NC / kRowLanes;             // columns of a thread
@@ -242,6 +243,9 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
     __shared__ __align__(16) float4 s_d[2][TB];  // (twice each)
     __shared__ __align__(16) float s_o[2][TB][kThreads / 32][NC];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int STAGERS = HELPERS ? HELPERS : kThreads;  // threads that stage and sum up
+    const int help = HELPERS ? tid - kThreads : tid;
+    const bool walker = !HELPERS || help < 0;
     const int slice = blockIdx.x % SLICES;
     const long long unit = blockIdx.x / SLICES;
     const int h = (int)(unit % a.n_v), s = (int)(unit / a.n_v);
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
     uint64_t x[C][R / 2];  // pairs of rows
     {
         float y[R][C];
-        if (src >= 0) {
+        if (src >= 0 && walker) {
             const float* p = a.state + ((size_t)src * a.n_v + h) * head + at;
 #pragma unroll
             for (int i = 0; i < R; ++i) Floats<C>::get(__ldcs(reinterpret_cast<const Cols*>(p + (size_t)i * DV)), y[i]);
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
     const T* q = static_cast<const T*>(a.q);
     const T* k = static_cast<const T*>(a.k);
     const T* v = static_cast<const T*>(a.v);
-    constexpr int QN = (QV + kThreads - 1) / kThreads, VN = (VV + kThreads - 1) / kThreads;
+    constexpr int QN = (QV + STAGERS - 1) / STAGERS, VN = (VV + STAGERS - 1) / STAGERS;
     uint4 rq[QN], rk[QN], rv[VN];
     float rg = 0.f;
     auto widen = [](const uint4& u, float* to) {
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
         const int n = min(TB, q1 - t0);
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int e = (i * kThreads + tid) * N, t = e / DK;
+            const int e = (i * STAGERS + help) * N, t = e / DK;
             if (t < n) {
                 const size_t from = ((size_t)(t0 + t) * a.n_qk + hq) * DK + e % DK;
                 rq[i] = *reinterpret_cast<const uint4*>(q + from);
@@ -304,16 +308,16 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
         }
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int e = (i * kThreads + tid) * N, t = e / NC;
+            const int e = (i * STAGERS + help) * N, t = e / NC;
             if (t < n) rv[i] = *reinterpret_cast<const uint4*>(v + ((size_t)(t0 + t) * a.n_v + h) * DV + slice * NC + e % NC);
         }
-        if (tid < n) rg = a.log_decay ? a.log_decay[(size_t)(t0 + tid) * a.decay_stride + h] : 0.f;
+        if (help < n) rg = a.log_decay ? a.log_decay[(size_t)(t0 + help) * a.decay_stride + h] : 0.f;
     };
     auto stage = [&](int t0, int b) -> bool {  // whether any token's decay is not a slow one
         const int n = min(TB, q1 - t0);
 #pragma unroll
         for (int i = 0; i < QN; ++i) {
-            const int e = (i * kThreads + tid) * N;
+            const int e = (i * STAGERS + help) * N;
             if (e / DK < n) {
                 widen(rq[i], &s_q[b][0][0] + e);
                 widen(rk[i], &s_k[b][0][0] + e);
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
         }
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int e = (i * kThreads + tid) * N;
+            const int e = (i * STAGERS + help) * N;
             if (e / NC < n) {
                 float f[N];
                 Vec16<T>::to_float(rv[i], f);
@@ -330,16 +334,16 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
                 for (int j = 0; j < N; j += 2) to[j / 2] = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
             }
         }
-        if (tid >= n) return false;
+        if (help >= n) return false;
         const bool slow = rg > -0.5f && rg < 0.5f;
         const float d = slow ? expm1f(rg) : expf(rg), once = slow ? 1.f : 0.f;
-        s_d[b][tid] = make_float4(d, d, once, once);
+        s_d[b][help] = make_float4(d, d, once, once);
         return !slow;
     };
     auto results = [&](int t0, int b) {
         const int n = min(TB, q1 - t0);
-#pragma unroll 1
-        for (int e = tid; e < n * NC; e += kThreads) {
+#pragma unroll(HELPERS ? 4 : 1)
+        for (int e = help; e < n * NC; e += STAGERS) {
             const int t = e / NC, c = e % NC;
             const float sum = (s_o[b][t][0][c] + s_o[b][t][1][c]) + (s_o[b][t][2][c] + s_o[b][t][3][c]);
             static_cast<T*>(a.out)[((size_t)(t0 + t) * a.n_v + h) * DV + slice * NC + c] = from_float<T>(sum * a.scale);
@@ -347,13 +351,24 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
     };
     int b = 0;
     if (q0 < q1) {
-        fetch(q0);
-        bool fast = stage(q0, 0);
-        for (int t0 = q0; t0 < q1; t0 += TB) {
+        bool fast = false;
+        if (!HELPERS || help >= 0) {
+            fetch(q0);
+            fast = stage(q0, 0);
+            if (HELPERS && q0 + TB < q1) fetch(q0 + TB);
+        }
+        for (int t0 = q0; t0 < q1; t0 += TB, b ^= 1) {
             const int n = min(TB, q1 - t0);
             const bool any = __syncthreads_or(fast);
-            if (t0 + TB < q1) fetch(t0 + TB);
-            if (t0 > q0) results(t0 - TB, b ^ 1);
+            if (!HELPERS) {
+                if (t0 + TB < q1) fetch(t0 + TB);
+                if (t0 > q0) results(t0 - TB, b ^ 1);
+            } else if (help >= 0) {
+                if (t0 + TB < q1) fast = stage(t0 + TB, b ^ 1);
+                if (t0 + 2 * TB < q1) fetch(t0 + 2 * TB);
+                if (t0 > q0) results(t0 - TB, b ^ 1);
+                continue;
+            }
             // G tokens at once: what they read is on its way before the first is worked out, and a token's products need
             // only the state that the one before left
             auto tokens = [&](auto slow, auto count, int t) {
@@ -416,13 +431,12 @@ __global__ void __launch_bounds__(kThreads) linear_walk_kernel(const LinearArgs 
                 all(std::true_type{});
             else
                 all(std::false_type{});
-            if (t0 + TB < q1) fast = stage(t0 + TB, b ^ 1);
-            b ^= 1;
+            if (!HELPERS && t0 + TB < q1) fast = stage(t0 + TB, b ^ 1);
         }
         __syncthreads();
-        results(q0 + (q1 - 1 - q0) / TB * TB, b ^ 1);
+        if (!HELPERS || help >= 0) results(q0 + (q1 - 1 - q0) / TB * TB, b ^ 1);
     }
-    if (dst >= 0) {
+    if (dst >= 0 && walker) {
         float* p = a.state + ((size_t)dst * a.n_v + h) * head + at;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -448,23 +462,25 @@ cudaError_t run(const LinearArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <typename T, int DK, int DV, int NC>
+template <typename T, int DK, int DV, int NC, int HELPERS>
 cudaError_t walk(const LinearArgs& a, cudaStream_t stream) {
-    linear_walk_kernel<T, DK, DV, NC><<<(unsigned)a.n_seqs * a.n_v * (DV / NC), kThreads, 0, stream>>>(a);
+    linear_walk_kernel<T, DK, DV, NC, HELPERS><<<(unsigned)a.n_seqs * a.n_v * (DV / NC), kThreads + HELPERS, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int DK, int DV>
 cudaError_t pick(int sms, const LinearArgs& a, cudaStream_t stream) {
     // In units of 64 columns: columns of 64 from two units an SM on, else of 32. Chunks of up to two units for three SMs
-    // take columns of 16 and packed pairs of rows (500 tokens of 24 units of 64 x 64 in fp32: 43 us, against 73 in columns of
-    // 32; 256 tokens of 64 units of 128 x 64: 38.5 and 46.2; of 128 units 72.8 and 65.1), and at dim_k = 64 the others pairs
-    // in columns of 32 (500 tokens of 128 units 71 us against 91; at 128 rows nothing is gained).
+    // take columns of 16 and packed pairs of rows (256 tokens of 96 units of 128 x 64 in fp32: 52 us, against 65 in columns
+    // of 32; of 128 units 73 and 65), with helpers up to a unit for two SMs (500 tokens of 24 units of 64 x 64: 32 us, 43
+    // without, 73 in columns of 32; with two CTAs of 192 threads an SM: 96 units 72 and 66), and at dim_k = 64 the others
+    // pairs in columns of 32 (500 tokens of 128 units 70 us against 91; at 128 rows nothing is gained).
     const long long units = (long long)a.n_seqs * a.n_v * (DV / 64);
-    if (a.q_start && units * 3 <= 2LL * sms) return walk<T, DK, DV, 16>(a, stream);
+    if (a.q_start && units * 2 <= sms) return walk<T, DK, DV, 16, 64>(a, stream);
+    if (a.q_start && units * 3 <= 2LL * sms) return walk<T, DK, DV, 16, 0>(a, stream);
     if (units >= 2LL * sms) return run<T, DK, DV, 64>(a, stream);
     if constexpr (DK == 64)
-        if (a.q_start) return walk<T, DK, DV, 32>(a, stream);
+        if (a.q_start) return walk<T, DK, DV, 32, 0>(a, stream);
     return run<T, DK, DV, 32>(a, stream);
 }
 
