@@ -40,8 +40,7 @@ int linear_args(const pkv_linear_desc* d, int32_t layer, const void* q, const vo
 }
 
 constexpr int kPiece = 128;          // tokens the tensor-core kernel takes at once
-constexpr int kMinSegment = 2 * kPiece;
-constexpr int kMinShared = 10 * kPiece;  // shortest chunk that is shared out along its length
+constexpr int kMinShared = 6 * kPiece;  // shortest chunk that is shared out along its length
 
 // Whether a prefill goes by pieces of 128 tokens on the tensor cores or token after token, by what each is estimated to
 // take, in microseconds; fp32 has no choice. (dim_k 128; where 64 differs, it follows in brackets.)
@@ -71,23 +70,26 @@ bool by_pieces(const pkv_linear_desc* d, int n_seqs, int n_tokens, int max_query
     return pieces < (small ? 2.4 : 2.8) + (work > longest ? work : longest);
 }
 
-// How a call's sequences are shared out along their length: while the (sequence, head, 64 columns) units fill no more
-// than half the GPU, in as many segments as it holds CTAs, but no more than kMaxSegments, each of which reads what all
-// before it leave. 8 heads x 128 x 64: 9,005 tokens 139 us whole, 32 in segments of two pieces or more, 34 of four, 44 of
-// eight; 1,024 tokens 22 whole and 24 in segments, 1,500 tokens 29 and 26.
+// How a call's sequences are shared out along their length: in as many segments as the GPU holds CTAs for them, but no more
+// than kMaxSegments, each of which reads what all before it leave. Two passes of p / n pieces are estimated at 12 us + 3.3 for
+// each piece (fp16 3.6) + 0.25 for each segment, one of p pieces at 6 us + 1.83 (2.25). bf16, 8 heads x 128 x 64: 1,024,
+// 1,536 and 9,005 tokens 20.6, 27.3 and 128 us whole, 18.2, 19.7 and 28.8 in segments of 1, 1 and 4 pieces; 32 heads x 128 x
+// 128, two segments: 1,280 and 16,384 tokens 25.3 and 223 whole, 29.3 and 212 in segments.
 constexpr int kMaxSegments = 32;
 struct Segments {
     int n, tokens;
 };
 Segments segments_of(const pkv_linear_desc* d, int n_seqs, int max_query, int sms) {
     const long long units = (long long)n_seqs * d->n_v_heads * (d->dim_v / 64);
-    long long n = units * 2 <= sms && max_query >= kMinShared ? sms / units : 1;
-    if (n > max_query / kMinSegment) n = max_query / kMinSegment;
-    if (n > kMaxSegments) n = kMaxSegments;
-    if (n < 2) return {1, (max_query + kPiece - 1) / kPiece * kPiece};
     const int pieces = (max_query + kPiece - 1) / kPiece;
-    const int tokens = (int)((pieces + n - 1) / n) * kPiece;
-    return {(max_query + tokens - 1) / tokens, tokens};
+    const Segments whole = {1, pieces * kPiece};
+    if (units * 2 > sms || max_query < kMinShared) return whole;
+    long long n = sms / units < kMaxSegments ? sms / units : kMaxSegments;
+    const int each = (int)((pieces + n - 1) / n);
+    n = (pieces + each - 1) / each;
+    const bool bf16 = d->dtype == PKV_BF16;
+    if (12.0 + (bf16 ? 3.3 : 3.6) * each + 0.25 * (double)n >= 6.0 + (bf16 ? 1.83 : 2.25) * pieces) return whole;
+    return {(int)n, each * kPiece};
 }
 
 // Workspace of a shared-out call, in floats: units of 64 columns are at most sms / segments, so sms of them hold all

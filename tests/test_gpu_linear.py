@@ -430,3 +430,24 @@ def test_no_token_at_all(dtype):
     want = was.clone()
     want[1, 3], want[1, 1] = was[1, 0], 0
     assert torch.equal(state, want) and pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("lens", [[1000, 20, 0, 129, 513], [1025], [1408, 1409]])
+def test_segments_of_few_pieces(dtype, dk, dv, lens):
+    """Shared out along the longest: others take fewer segments, one, or none; NaN in one stays in it."""
+    q, k, v, d, state, starts = inputs(dtype, lens, 2, 2, dk, dv, seed=41 + len(lens))
+    n, was = len(lens), state.clone()
+    src = [i if i % 2 == 0 else -1 for i in range(n)]
+    base = check(dtype, q, k, v, d, state, src, list(range(n)), starts)
+    at = lens[0] - 300
+    v2 = v.clone()
+    v2[at, 1, 5] = float("nan")
+    st = was.clone()
+    out = run(dtype, q, k, v2, d, st, src, list(range(n)), starts)
+    touched = torch.zeros_like(out, dtype=torch.bool)
+    touched[at:lens[0], 1, 5] = True
+    assert torch.isnan(out[touched]).all() and torch.equal(out[~touched], base[~touched])
+    assert torch.isnan(st[1, 0, 1, :, 5]).all() and torch.equal(st[1, 1:], state[1, 1:])
+    assert pkv.pkv_get_device_status() == 0
