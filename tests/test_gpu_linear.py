@@ -95,7 +95,7 @@ def test_decode_of_many(dtype):
 def test_prefill_matches(dtype, dk, dv, lens):
     q, k, v, d, state, starts = inputs(dtype, lens, 1, 3, dk, dv, "token", seed=sum(lens) + dk)
     n = len(lens)
-    check(dtype, q, k, v, d, state, [i if i % 2 == 0 else -1 for i in range(n)], [n + 1 - i for i in range(n)], starts)
+    check(dtype, q, k, v, d, state, [i if i % 2 == 0 else -1 for i in range(n)], [n + 1 - i if i < 3 else 1 for i in range(n)], starts)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -267,7 +267,7 @@ def test_captured_and_replayed_with_other_inputs(dtype):
     q, k, v, d, state, starts = [x.clone() if torch.is_tensor(x) else x for x in sets[0]]
     desc = pkv.make_linear_desc(dtype, *state.shape[:2], 1, 2, 128, 64)
     i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
-    src, dst, st = i32([0, 1]), i32([1, 0]), i32(starts)
+    src, dst, st = i32([0, 1]), i32([2, 3]), i32(starts)
     ws = pkv.alloc_linear_prefill_workspace(desc, 2, q.shape[0], 2000)
     outs = [torch.zeros_like(v) for _ in range(3)]
 
@@ -450,4 +450,45 @@ def test_segments_of_few_pieces(dtype, dk, dv, lens):
     touched[at:lens[0], 1, 5] = True
     assert torch.isnan(out[touched]).all() and torch.equal(out[~touched], base[~touched])
     assert torch.isnan(st[1, 0, 1, :, 5]).all() and torch.equal(st[1, 1:], state[1, 1:])
+    assert pkv.pkv_get_device_status() == 0
+
+
+def test_more_units_than_the_gpu_holds_on_two_streams_and_from_graphs():
+    """Two such calls at once, and two captured ones replayed in turns: each goes on with its own work only."""
+    lens = [RAGGED[i % 8] for i in range(24)]
+    own = list(range(24))
+    a, b = (inputs("bf16", lens, 4, 8, 64, 128, seed=s) for s in (51, 52))
+    T = sum(lens)
+    want = []
+    for x in (a, b):
+        st = x[4].clone()
+        want.append((run("bf16", *x[:4], st, own, own, x[5])[:T], st))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    states = [[x[4].clone() for x in (a, b)] for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for pair in states:
+        for st, x, state in zip(streams, (a, b), pair):
+            with torch.cuda.stream(st):
+                got.append((run("bf16", *x[:4], state, own, own, x[5])[:T], state))
+    torch.cuda.synchronize()
+    for i, (out, state) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(state, want[i % 2][1])
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    desc = pkv.make_linear_desc("bf16", 2, 26, 4, 8, 64, 128)
+    slots, start = i32(own), i32(a[5])
+    graphs, outs, after = [], [], []
+    for x in (a, b):
+        outs.append(torch.zeros_like(x[2]))
+        after.append(x[4].clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pkv.pkv_linear_prefill(desc, 1, *x[:4], after[-1], slots, slots, start, 300, SCALE, outs[-1])
+    for _ in range(3):
+        for x, state in zip((a, b), after):
+            state.copy_(x[4])
+        for graph in graphs:
+            graph.replay()
+        for out, state, w in zip(outs, after, want):
+            assert torch.equal(out[:T], w[0]) and torch.equal(state, w[1])
     assert pkv.pkv_get_device_status() == 0
