@@ -26,8 +26,9 @@
 //   warp 27      sums of the log decays, for all the others
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
-// fp16 cannot hold their range: rows of P' and the copy of S are then brought to 2^14 by a power of two each, which the
-// sums undo in fp32.
+// fp16 cannot hold their range: the largest number of each row of P', of V~ and of the copy of S is then brought to 2^14 by a
+// power of two, which the sums undo in fp32. It is the largest as weighted by the decays: their own largest alone says
+// little, growing ones may weigh what is 0, and what is large may be what they leave nothing of.
 //
 // Fewer units than the GPU holds: a long sequence is shared out along its length in segments, a first pass leaving what
 // each adds to the state (STATES). More: a CTA goes on with others' work (MORE), its roles without a pause, so that a
@@ -54,7 +55,7 @@ namespace pkv {
 constexpr int kPiece = 128;   // tokens of a piece: the M of a product
 constexpr int kSlice = 64;    // columns of v of a CTA
 // fp16: the second number of a value of V~ is this times what the first lacks of it: at most the value, so it fits, and
-// the two are within 2^-22 of a value, or within 2^-36 where that is more.
+// the two are within 2^-22 of a value, or within 2^-50 of the piece's largest where that is more.
 constexpr float kSecond = 2048.f;
 constexpr int kChunkThreads = 7 * 128;
 
@@ -96,8 +97,15 @@ struct __align__(16) PieceGates {
     float block[4];                // sum over each block
     float after[4];                // 2^(sum over the blocks behind it)
     float keep, once;              // S' = S + (U + S * keep) with 2^(sum over all) - 1 where that is small, once = 1,
-    float grow;                    // else S * keep + U, once = 0; sum of the positive ones
-    float sum;                     // over all
+    float sum;                     // else S * keep + U, once = 0; the sum over all
+};
+
+// fp16: the powers of two that bring what its products take into its range.
+struct __align__(16) HalfScales {
+    float row_unit[4][kPiece];     // of the rows of P', undone: 2^-shift
+    float row_most[2][2][kPiece];  // largest weighted pair of a row's even and odd halves
+    float v_most[2][8];            // largest number of V~ that a warp has
+    float v_back[4];               // of V~, undone
 };
 
 // The work of one CTA of the grid: a sequence (or a segment of it), a head, 64 columns of v.
@@ -121,12 +129,12 @@ struct ChunkSmem {
     using Gates = PieceGates;
     static constexpr uint32_t GATES = S + DK * 128;        // [2]
     static constexpr uint32_t BAD = GATES + 2 * sizeof(Gates);  // bytes [4][64]: first token whose v is not finite
-    static constexpr uint32_t ROW = BAD + 4 * 64;      // fp16: float [4][128], 2^-e of P's rows
-    static constexpr uint32_t MISC = ROW + (BF ? 0 : 4 * 128 * 4);  // any_bad[4] s_unit[2] - part[2][4]
+    static constexpr uint32_t HALF = BAD + 4 * 64;     // fp16: HalfScales
+    static constexpr uint32_t MISC = HALF + (BF ? 0 : sizeof(HalfScales));  // any_bad[4] s_unit[2] - part[2][4]
     static constexpr uint32_t NEXT = MISC + 64;            // 16 bytes: the answer to a request for another CTA's work
     static constexpr uint32_t WORK = NEXT + 16;            // [2]
     static constexpr uint32_t BARS = WORK + 2 * sizeof(ChunkWork);
-    static constexpr int NBARS = 10 * 2 + 2 * 4 + 7 + 3 + 2 + 2;
+    static constexpr int NBARS = 10 * 2 + 2 * 4 + 7 + 3 + 2 + 2 + (BF ? 0 : 4);
     static constexpr uint32_t TADDR = BARS + NBARS * 8;
     static constexpr uint32_t TOTAL = TADDR + 16;
     static constexpr uint32_t ALLOC = TOTAL;               // (on a 1,024-byte boundary: the array is declared so)
@@ -203,15 +211,22 @@ __device__ __forceinline__ void byte_min(uint8_t* p, int x) {
     }
 }
 
-// What keeps values of fp16 that gates with sums of positive parts `grow` weigh within fp16: a power of two.
-__device__ __forceinline__ float down_by(float grow) { return ex2_approx(-ceilf(fminf(grow, 100.f))); }
+// The largest of 16 fp16 numbers' absolute values, as bits: infinity and NaN are above the others.
+__device__ __forceinline__ uint32_t largest_half(const uint4 (&x)[2]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu)),
+                       __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+    return max(top & 0xffffu, top >> 16);
+}
 
 // 2^e, e clamped to what a normal number holds
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
-// e with 2^(14 - e) bringing x into [2^14, 2^15); 14 (no change) for 0
+// e with 2^(14 - e) bringing x into [2^14, 2^15), if x >= 2^-100; 14 (no change) for 0
 __device__ __forceinline__ int exponent14(float x) {
     const int e = (int)((__float_as_uint(x) >> 23) & 255u) - 127;
-    return x == 0.f ? 14 : min(max(e, -100), 120);
+    return x == 0.f ? 14 : min(max(e, -100), 127);
 }
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -245,7 +260,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     using Gates = typename L::Gates;
     Gates* gates = reinterpret_cast<Gates*>(smem + L::GATES);
     uint8_t* bad = smem + L::BAD;
-    float* row_unit = reinterpret_cast<float*>(smem + L::ROW);
+    HalfScales& half = *reinterpret_cast<HalfScales*>(smem + L::HALF);  // (fp16 alone)
     int* any_bad = reinterpret_cast<int*>(smem + L::MISC);
     float* s_unit = reinterpret_cast<float*>(smem + L::MISC + 16);
     float* part = reinterpret_cast<float*>(smem + L::MISC + 32);
@@ -272,6 +287,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* next_full = begun + 1;   // an answer has come
     uint64_t* work_full = next_full + 1;  // [2] work is written
     uint64_t* work_free = work_full + 2;  // [2] and read
+    uint64_t* halves = work_free + 2;     // [4] fp16: the two warps of 32 rows of P have their largest
     uint32_t* taddr_s = reinterpret_cast<uint32_t*>(smem + L::TADDR);
 
     if (STATES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second pass may set itself up
@@ -345,6 +361,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(&work_free[i], 8 + 8 + 4 + 4 + 3);  // warps, or the one thread of a warp
         }
         for (int i = 0; i < 3; ++i) mbar_init(&role[i], i == 0 ? 8 : 4);
+        if (!BF)
+            for (int i = 0; i < 4; ++i) mbar_init(&halves[i], 2);
         fence_mbar_init();
     }
     if (threadIdx.x < 4 * 64) bad[threadIdx.x] = kPiece;
@@ -473,44 +491,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (!wait(p_full, c)) { ok = false; break; }
                     tcgen05_after_sync();
                     float shift = 0.f;  // log2 of what the row is multiplied by
-                    if constexpr (!BF) {
-                        float m0 = 0.f, m1 = 0.f;
-                        uint32_t x[32];
-#pragma unroll 1
-                        for (int b = 0; b < w4; ++b) {
-                            tmem_ld32(lanes + P_COL + b * 32, x);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                m0 = fmax3(m0, fabsf(__uint_as_float(x[j])), fabsf(__uint_as_float(x[j + 1])));
-                                m1 = fmax3(m1, fabsf(__uint_as_float(x[j + 2])), fabsf(__uint_as_float(x[j + 3])));
-                            }
-                        }
-                        tmem_ld32(lanes + P_COL + w4 * 32, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) m0 = fmaxf(m0, j <= lane ? fabsf(__uint_as_float(x[j])) : 0.f);
-                        const int e = exponent14(fmaxf(m0, m1)) + (int)ceilf(fminf(g.grow, 200.f));
-                        shift = (float)(14 - e);
-                        if (side == 0) row_unit[(c & 3) * kPiece + row] = ex2_approx(-shift);
-                    }
                     uint32_t p[16], w[8];
                     float* pf = reinterpret_cast<float*>(p);
+                    // what the pairs of block b, at [.][side ..], are weighted by: 2^(the sum from the block's end to the row) = f
+                    // times 2^(that from a token to the block's end)
+                    auto weights = [&](int b, float f, uint64_t (&x)[8]) {
+                        const uint64_t f2 = f2_pack(f, f);
+                        const ulonglong2* gc = reinterpret_cast<const ulonglong2*>(&g.col[b * 32 + side]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const ulonglong2 y = gc[j];
+                            x[2 * j] = f2_mul(y.x, f2), x[2 * j + 1] = f2_mul(y.y, f2);
+                        }
+                    };
+                    float most = 0.f;  // fp16: the largest of the row, as weighted
+                    if constexpr (!BF) {
+                        float from = mine;
+#pragma unroll 1
+                        for (int b = w4 - 1; b >= 0; --b) {
+                            tmem_ld16(from_col + b * 32, *reinterpret_cast<float(*)[16]>(pf));
+                            uint64_t x[8];
+                            weights(b, ex2_approx(from), x);
+                            from += g.block[b];
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 y = f2_get(f2_mul(x[j], f2_pack(pf[2 * j], pf[2 * j + 1])));
+                                most = fmax3(most, fabsf(y.x), fabsf(y.y));
+                            }
+                        }
+                    }
                     tmem_ld16(from_col + w4 * 32, *reinterpret_cast<float(*)[16]>(pf));
                     // P' of the piece before the last has been read
                     if (c > 1 && !wait(&done[c & 1], (c >> 1) - 1)) { ok = false; break; }
                     to_col = lanes + PW_COL + (c & 1) * 64 + side / 2;
                     tcgen05_after_sync();
                     {  // the block on the diagonal: an exponential for each pair
-                        const uint64_t hi2 = f2_pack(mine, mine), shift2 = f2_pack(shift, shift);
+                        const uint64_t hi2 = f2_pack(mine, mine);
                         const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
                         float x[16];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const ulonglong2 y = gh[j];
-                            uint64_t e0 = f2_add(hi2, y.x), e1 = f2_add(hi2, y.y);
-                            if constexpr (!BF) e0 = f2_add(e0, shift2), e1 = f2_add(e1, shift2);
-                            const float2 d0 = f2_get(e0), d1 = f2_get(e1);
+                            const float2 d0 = f2_get(f2_add(hi2, y.x)), d1 = f2_get(f2_add(hi2, y.y));
                             x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
                             x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
                         }
@@ -518,6 +541,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float2 y = f2_get(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), f2_pack(pf[2 * j], pf[2 * j + 1])));
+                            if constexpr (BF)
+                                w[j] = M::pack(y.x, y.y) & seen[j];
+                            else
+                                pf[2 * j] = y.x, pf[2 * j + 1] = y.y;
+                        }
+                    }
+                    if constexpr (!BF) {  // the row's largest, of both halves, goes to 2^14
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) most = fmaxf(most, j <= lane - side ? fabsf(pf[j]) : 0.f);
+                        half.row_most[c & 1][side >> 4][row] = most;  // (the other warp has read those of two pieces ago: it met since)
+                        arrive_warp(&halves[w4]);
+                        if (!wait(&halves[w4], c)) { ok = false; break; }
+                        const int e = exponent14(fmaxf(most, half.row_most[c & 1][(side >> 4) ^ 1][row]));
+                        shift = (float)(14 - e);
+                        if (side == 0) half.row_unit[c & 3][row] = pow2i(e - 14);
+                        const uint64_t up = f2_pack(pow2i(14 - e), pow2i(14 - e));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 y = f2_get(f2_mul(f2_pack(pf[2 * j], pf[2 * j + 1]), up));
                             w[j] = M::pack(y.x, y.y) & seen[j];
                         }
                     }
@@ -526,16 +568,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     for (int b = w4 - 1; b >= 0; --b) {
                         tmem_ld16(from_col + b * 32, *reinterpret_cast<float(*)[16]>(pf));
                         put(b + 1, w);
-                        const float f = ex2_approx(from);
-                        from += g.block[b];
-                        const uint64_t f2 = f2_pack(f, f);
-                        const ulonglong2* gc = reinterpret_cast<const ulonglong2*>(&g.col[b * 32 + side]);
                         uint64_t x[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const ulonglong2 y = gc[j];
-                            x[2 * j] = f2_mul(y.x, f2), x[2 * j + 1] = f2_mul(y.y, f2);
-                        }
+                        weights(b, ex2_approx(from), x);
+                        from += g.block[b];
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -556,7 +591,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         registers_down<MORE ? 64 : 56>();
         begin();
         const int tid = threadIdx.x - 256;
-        const int half = tid >> 7;  // quarters 0 and 2, or 1 and 3
+        const int odd = tid >> 7;  // quarters 0 and 2, or 1 and 3
         const int r = (tid & 127) >> 2;
         // which four 16-byte units of its row: two threads' rows share the banks of half a row otherwise
         const int u0 = (tid & 3) + 4 * (r & 1);
@@ -582,9 +617,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     fence_proxy_async_smem();
                     if (!meet(0)) { ok = false; break; }
                 }
-                const float unit = BF ? 1.f : down_by(g.grow);
+                float unit = 1.f;
+                if constexpr (!BF) {  // the largest number of V~ goes to 2^14
+                    float most = 0.f;
 #pragma unroll 1
-                for (int q = half; q < 4; q += 2) {
+                    for (int q = odd; q < 4; q += 2) {
+                        const unsigned char* from = v + (q * 32 + r) * 128;
+                        uint4 x[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+                        uint32_t top = largest_half(x);
+                        if (top >= 0x7c00u) {  // one is not finite
+                            top = 0;
+#pragma unroll 1
+                            for (int j = 0; j < 16; ++j) {
+                                const uint32_t y = reinterpret_cast<const uint16_t*>(from + (j < 8 ? at[0] : at[1]))[j & 7] & 0x7fffu;
+                                top = max(top, y < 0x7c00u ? y : 0u);
+                            }
+                        }
+                        most = fmaxf(most, g.col[q * 32 + r] * g.after[q] * __half2float(__ushort_as_half((unsigned short)top)));
+                    }
+                    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (not negative)
+                    if (lane == 0) half.v_most[c & 1][warp - 8] = most;
+                    if (!meet(0)) { ok = false; break; }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) most = fmaxf(most, half.v_most[c & 1][i]);
+                    const int e = exponent14(most);
+                    unit = pow2i(14 - e);
+                    if (tid == 0) half.v_back[c & 3] = pow2i(e - 14);  // (the state's warps have read that of four pieces ago)
+                }
+#pragma unroll 1
+                for (int q = odd; q < 4; q += 2) {
                     const int row = q * 32 + r;
                     unsigned char* from = v + row * 128;
                     uint4 x[2];
@@ -729,13 +792,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 const Gates& g = gates[c & 1];
                 if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-                const float unit_v = BF ? 1.f : down_by(g.grow);
                 const uint64_t keep = f2_pack(g.keep, g.keep), once = f2_pack(g.once, g.once);
                 if (STATES) sum += g.sum;
                 arrive_warp(&g_free[c & 1]);
                 if (!wait(u_full, c)) { ok = false; break; }
                 tcgen05_after_sync();
-                const float back = BF ? 1.f : 1.f / unit_v, back2 = back / kSecond;
+                const float back = BF ? 1.f : half.v_back[c & 3], back2 = back / kSecond;
 #pragma unroll
                 for (int i = 0; i < NC / 2; i += 8) {
                     float u[2][16];  // the first numbers' product, and the others'
@@ -794,7 +856,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (c + 1 < base + pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
                     if constexpr (!BF) {
                         fi *= s_unit[c & 1];
-                        fa *= row_unit[(c & 3) * kPiece + row];
+                        fa *= half.row_unit[c & 3][row];
                     }
                     const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
                     const bool poisoned = any_bad[c & 3] != 0;
@@ -1027,13 +1089,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fetch(0);
 #pragma unroll 1
                 for (int c = base; c < base + pieces; ++c) {
-                    float front[4], back[4], all[4], grow = 0.f;
+                    float front[4], back[4], all[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums; NaN stays
                         float y = raw[b] < -104.f ? -104.f : raw[b];
                         y = (y > 1e4f ? 1e4f : y) * 1.44269504f;
-                        grow += fmaxf(y, 0.f);
                         front[b] = y;
                         back[b] = __shfl_down_sync(0xffffffffu, y, 1);
                         if (lane == 31) back[b] = 0.f;
@@ -1049,10 +1110,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         }
 #pragma unroll
                     for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[b], 31);
-                    if (__any_sync(0xffffffffu, grow != 0.f)) {
-#pragma unroll 1
-                        for (int o = 16; o > 0; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
-                    }
                     if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
                     Gates& g = gates[c & 1];
 #pragma unroll
@@ -1068,7 +1125,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         const bool small = sum > -0.7f && sum < 0.7f;
                         g.keep = small ? expm1f(sum * 0.693147181f) : ex2_approx(sum);
                         g.once = small ? 1.f : 0.f;
-                        g.grow = grow;
                         g.sum = sum;
                     }
                     arrive_warp(&g_full[c & 1]);

@@ -1,0 +1,146 @@
+"""Linear attention where numbers leave the range of the rows' type, on the GPU against the recurrence in 64 bits: decays of
+both signs, keys and queries that single a token out."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from linear_oracle import linear
+from paged_kv_cache_258_gb300 import pkv
+from test_gpu_linear import RAGGED, SCALE, inputs, per_token, run
+
+pytestmark = pytest.mark.gpu
+LARGEST = {"f32": 3.4028234e38, "f16": 65504.0, "bf16": 3.3895e38}
+
+
+def sums_error(g, starts):
+    """Relative error of a weight exp(G_i - G_j) that comes from its sum in fp32. A log decay is turned to base 2 (half a
+    step: 2^-24 |g|), then summed over a piece of 128 tokens: five additions of a scan, up to four of blocks and three
+    differences, each off by half a step of a partial sum, which is at most M, the largest sum between two tokens of
+    the piece: 12 * 2^-24 M. Both count once for each piece that a term passes. What passes a token that all but forgets
+    (below -60) has no part in the bounds, nor have those. Returned for each sequence."""
+    out = []
+    for a, b in zip(starts[:-1], starts[1:]):
+        x = g[a:b].double().cpu()
+        x = torch.where(x < -60.0, 0.0, x)
+        total = x.abs().sum(0)
+        for p in range(0, b - a, 128):
+            f = torch.cumsum(torch.cat([torch.zeros_like(x[:1]), x[p:p + 128]]), 0)
+            total = total + 12 * (f.max(0).values - f.min(0).values)
+        out.append(float(total.max()) * 2.0 ** -24 if b > a else 0.0)
+    return out
+
+
+def check(dtype, q, k, v, d, state, src, dst, starts):
+    """As in test_gpu_linear, where the tolerance also holds the sums' errors, and a result past the type's largest number
+    is infinite."""
+    was = state.clone()
+    out = run(dtype, q, k, v, d, state, src, dst, starts)
+    g = per_token(d, v)
+    want, tol, after, after_tol = linear(q, k, v, g, was[1], src, dst, starts, SCALE, dtype)
+    reach, _, most, _ = linear(q.abs(), k.abs(), v.abs(), g, was[1].abs(), src, dst, starts, SCALE, dtype)
+    got, state_got = out.double().cpu(), state[1].double().cpu()
+    for s, e in enumerate(sums_error(g, starts)):
+        rows = slice(int(starts[s]), int(starts[s + 1]))
+        w, t = want[rows], tol[rows] + e * reach[rows]
+        x = got[rows]  # infinite where a value within the tolerance is past the largest number
+        past = (x == math.inf) & (w + t >= LARGEST[dtype]) | (x == -math.inf) & (w - t <= -LARGEST[dtype])
+        assert bool(torch.all(((x - w).abs() <= t) | past)), s
+        if dst[s] >= 0:
+            assert torch.all((state_got[dst[s]] - after[dst[s]]).abs() <= after_tol[dst[s]] + e * most[dst[s]]), s
+    T = int(starts[-1])
+    assert torch.all(out[T:] == 7.0) and pkv.pkv_get_device_status() == 0
+    return out
+
+
+def gates_of(kind, T, n_v, seed):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.arange(T)
+    if kind == "alternating":
+        d = torch.where(t % 2 == 0, 0.5, -0.5)[:, None].expand(T, n_v)
+    elif kind == "normal":
+        d = torch.randn((T, n_v), generator=g)
+    elif kind == "growing":
+        d = torch.full((T, n_v), 0.3)
+    elif kind == "waves":
+        d = torch.where(t // 40 % 2 == 0, 0.3, -0.3)[:, None] * torch.linspace(0.5, 1.5, n_v)
+    else:                                      # strong decays with bursts between them
+        d = torch.where(torch.rand((T, n_v), generator=g) < 0.1, 6.0, -1.0)
+    return d.contiguous()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("kind", ["alternating", "normal", "growing", "waves", "bursts"])
+@pytest.mark.parametrize("dk,dv,lens", [(64, 64, [230, 64, 129]), (128, 128, [250]), (128, 64, [130, 0, 200])])
+def test_decays_of_both_signs(dtype, kind, dk, dv, lens):
+    q, k, v, _, state, starts = inputs(dtype, lens, 1, 2, dk, dv, "none", seed=60 + len(lens))
+    d = torch.cat([gates_of(kind, sum(lens), 2, 61), torch.full((3, 2), math.nan)]).cuda()
+    n = len(lens)
+    check(dtype, q, k, v, d, state, [i if i % 2 == 0 else -1 for i in range(n)], list(range(n)), starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["alternating", "normal", "waves"])
+def test_decays_of_both_signs_shared_out(dtype, kind):
+    q, k, v, _, state, starts = inputs(dtype, [1100, 900], 1, 1, 64, 64, "none", seed=62)
+    d = torch.cat([gates_of(kind, 2000, 1, 63), torch.full((3, 1), math.nan)]).cuda()
+    check(dtype, q, k, v, d, state, [0, -1], [0, 1], starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["alternating", "normal"])
+def test_decays_of_both_signs_of_more_units_than_the_gpu_holds(dtype, kind):
+    lens = [RAGGED[i % 8] for i in range(24)]
+    q, k, v, _, state, starts = inputs(dtype, lens, 4, 8, 64, 128, "none", seed=64)
+    d = torch.cat([gates_of(kind, sum(lens), 8, 65), torch.full((3, 8), math.nan)]).cuda()
+    check(dtype, q, k, v, d, state, list(range(24)), list(range(24)), starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("decay,far,key,value", [(-0.35, 100, 2.0 ** 13, 2.0 ** 13), (0.2, 0, 2.0 ** -6, 1.0)])
+def test_a_query_that_meets_one_token(dtype, decay, far, key, value):
+    """A row's only term: of a product of 2^26 that the decays leave 2^-50 of, or of a weight of 1 where the tokens before, which
+    the query does not meet, have weights up to 2^36."""
+    T, dk = 128, 128
+    q, k, v, _, state, starts = inputs(dtype, [T], 1, 1, dk, 64, "none", seed=66, behind=0)
+    k.zero_(), q.zero_()
+    t = torch.arange(T)
+    k[t, 0, t] = key
+    q[t, 0, (t - far).clamp(min=0)] = key
+    v.copy_(torch.randn(v.shape, generator=torch.Generator().manual_seed(67)) * value)
+    check(dtype, q, k, v, torch.full((T, 1), decay, device="cuda"), state, [-1], [-1], starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -18, 2.0 ** 11])
+def test_the_state_of_small_and_large_rows(dtype, size):
+    """Values of a few bits above the type's smallest, and near its largest: the state has 22 bits of them all the same."""
+    q, k, v, d, state, starts = inputs(dtype, [260], 1, 1, 64, 64, "head", seed=68)
+    v *= size
+    q *= 2.0 ** -6
+    k *= 0.25
+    check(dtype, q, k, v, d, state, [-1], [0], starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n_v", [1, 3])
+def test_states_near_the_largest_number(dtype, n_v):
+    """Elements of 2^125 and of 2^-125: a copy of the state for the queries is within the type either way."""
+    q, k, v, d, state, starts = inputs(dtype, [200], 1, n_v, 64, 64, "head", seed=71)
+    for scale in (2.0 ** 122, 2.0 ** -122):
+        st = state * scale
+        q2 = q * (2.0 ** -7)
+        check(dtype, q2, k, v, d, st, [0], [0], starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_decode_of_growing_decays(dtype):
+    n = 5
+    q, k, v, _, state, starts = inputs(dtype, [1] * n, 2, 4, 64, 64, "none", seed=78, behind=0)
+    d = torch.randn((n, 4), generator=torch.Generator().manual_seed(79)).cuda() * 3
+    was = state.clone()
+    out = run(dtype, q, k, v, d, state, list(range(n)), list(range(n)), starts, decode=True)
+    want, tol, after, after_tol = linear(q, k, v, d, was[1], list(range(n)), list(range(n)), starts, SCALE, dtype)
+    assert torch.all((out.double().cpu() - want).abs() <= tol)
+    assert torch.all((state[1].double().cpu() - after).abs() <= after_tol)
