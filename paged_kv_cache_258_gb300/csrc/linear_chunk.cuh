@@ -26,9 +26,10 @@
 //   warp 27      sums of the log decays, for all the others
 //
 // Rounded to 16 bits are P' and the copy of S that Q meets, each term of a result once, as attention weights are.
-// fp16 cannot hold their range: the largest number of each row of P', of V~ and of the copy of S is then brought to 2^14 by a
-// power of two, which the sums undo in fp32. It is the largest as weighted by the decays: their own largest alone says
-// little, growing ones may weigh what is 0, and what is large may be what they leave nothing of.
+// fp16 cannot hold their range: the largest number of each row of P', of V~ and of the copy of S (of its columns, where they
+// are far apart) is then brought to 2^14 by a power of two, which the sums undo in fp32. It is the largest as weighted by the
+// decays: their own largest alone says little, growing ones may weigh what is 0, and what is large may be what they leave
+// nothing of.
 //
 // Fewer units than the GPU holds: a long sequence is shared out along its length in segments, a first pass leaving what
 // each adds to the state (STATES). More: a CTA goes on with others' work (MORE), its roles without a pause, so that a
@@ -106,6 +107,11 @@ struct __align__(16) HalfScales {
     float row_most[2][2][kPiece];  // largest weighted pair of a row's even and odd halves
     float v_most[2][8];            // largest number of V~ that a warp has
     float v_back[4];               // of V~, undone
+    float s_most[2][4][2];         // of a warp's part of S: the largest number, the largest of its rows' smallest
+    float s_back[4];               // of the copy of S, undone, where its columns have one power of two,
+    int s_columns[4];              // else, of each column:
+    float col_most[4][kSlice];     // the largest number that a warp has
+    float col_up[kSlice], col_back[4][kSlice];
 };
 
 // The work of one CTA of the grid: a sequence (or a segment of it), a head, 64 columns of v.
@@ -130,8 +136,8 @@ struct ChunkSmem {
     static constexpr uint32_t GATES = S + DK * 128;        // [2]
     static constexpr uint32_t BAD = GATES + 2 * sizeof(Gates);  // bytes [4][64]: first token whose v is not finite
     static constexpr uint32_t HALF = BAD + 4 * 64;     // fp16: HalfScales
-    static constexpr uint32_t MISC = HALF + (BF ? 0 : sizeof(HalfScales));  // any_bad[4] s_unit[2] - part[2][4]
-    static constexpr uint32_t NEXT = MISC + 64;            // 16 bytes: the answer to a request for another CTA's work
+    static constexpr uint32_t MISC = HALF + (BF ? 0 : sizeof(HalfScales));  // any_bad[4]
+    static constexpr uint32_t NEXT = MISC + 16;            // 16 bytes: the answer to a request for another CTA's work
     static constexpr uint32_t WORK = NEXT + 16;            // [2]
     static constexpr uint32_t BARS = WORK + 2 * sizeof(ChunkWork);
     static constexpr int NBARS = 10 * 2 + 2 * 4 + 7 + 3 + 2 + 2 + (BF ? 0 : 4);
@@ -221,6 +227,20 @@ __device__ __forceinline__ uint32_t largest_half(const uint4 (&x)[2]) {
     return max(top & 0xffffu, top >> 16);
 }
 
+// max(|x|) over the warp; NaN counts only where nothing else is
+__device__ __forceinline__ float warp_most(float x) {
+    float y;
+    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// min(a, b, c) in one instruction
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 2^e, e clamped to what a normal number holds
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 // e with 2^(14 - e) bringing x into [2^14, 2^15), if x >= 2^-100; 14 (no change) for 0
@@ -262,8 +282,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint8_t* bad = smem + L::BAD;
     HalfScales& half = *reinterpret_cast<HalfScales*>(smem + L::HALF);  // (fp16 alone)
     int* any_bad = reinterpret_cast<int*>(smem + L::MISC);
-    float* s_unit = reinterpret_cast<float*>(smem + L::MISC + 16);
-    float* part = reinterpret_cast<float*>(smem + L::MISC + 32);
     uint64_t* qk_full = reinterpret_cast<uint64_t*>(smem + L::BARS);  // [2] Q and K of a piece have landed
     uint64_t* v_full = qk_full + 2;                                   // [2]
     uint64_t* done = v_full + 2;       // [2] P, OI and OA of a piece are done: V, P' and results
@@ -752,40 +770,82 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 arrive_warp(begun);
             }
             float sum = 0.f;
+            // fp16: the largest and the smallest of the row, kept up to date as the row is written (two of each, as such chains are
+            // long)
+            float row_most[2], row_least[2];
+            auto none_yet = [&]() { row_most[0] = row_most[1] = 0.f, row_least[0] = row_least[1] = 3.4028234e38f; };
+            auto count = [&](int i) {
+                const float2 y = f2_get(x[i]);
+                row_most[i & 1] = fmax3(row_most[i & 1], fabsf(y.x), fabsf(y.y));
+                row_least[i & 1] = fmin3(row_least[i & 1], fabsf(y.x), fabsf(y.y));
+            };
+            if (!BF && !STATES) {
+                none_yet();
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) count(i);
+            }
 #pragma unroll 1
             for (int c = base; c < base + pieces; ++c) {
                 if constexpr (!STATES) {  // the copy that Q meets
-                    uint64_t unit2 = 0;
-                    float back_s = 1.f;
-                    if constexpr (!BF) {
-                        float most = 0.f;
-#pragma unroll
-                        for (int i = 0; i < NC / 2; ++i) {
-                            const float2 y = f2_get(x[i]);
-                            most = fmax3(most, fabsf(y.x), fabsf(y.y));
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                        float* mine = part + (c & 1) * 4;  // (read for piece c by all before any of them meets for c + 1)
-                        if (lane == 0) mine[warp - 16] = most;
-                        if (!meet(1)) { ok = false; break; }
-                        const int e = exponent14(fmaxf(fmaxf(mine[0], mine[1]), fmaxf(mine[2], mine[3])));
-                        unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
-                        back_s = pow2i(e - 14);
-                    }
-                    if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
-                    // (Q S of the piece before is done: it began when the results of the one before that had been read)
-                    if (!BF && tid == 0) s_unit[c & 1] = back_s;
                     unsigned char* to = smem + L::S + row * 128;
+                    auto copy = [&](auto up) {  // up(i): what pair i of columns is multiplied by
 #pragma unroll
-                    for (int i = 0; i < NC / 2; i += 4) {
-                        uint32_t w[4];
+                        for (int i = 0; i < NC / 2; i += 4) {
+                            uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 y = f2_get(BF ? x[i + j] : f2_mul(x[i + j], unit2));
-                            w[j] = M::pack(y.x, y.y);
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 y = f2_get(BF ? x[i + j] : f2_mul(x[i + j], up(i + j)));
+                                w[j] = M::pack(y.x, y.y);
+                            }
+                            *reinterpret_cast<uint4*>(to + ((((c0 + 2 * i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        *reinterpret_cast<uint4*>(to + ((((c0 + 2 * i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    };
+                    if constexpr (BF) {
+                        if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
+                        copy([](int) { return uint64_t(0); });
+                    } else {
+                        // One power of two for all columns serves where each has a number of 2^-16 of the largest: what is lost
+                        // below fp16's normal numbers is then 2^-23 of a column's largest. That is so where a row has no
+                        // smaller ones, which costs a comparison a number. (A column's own largest, always: packed prompts
+                        // 234 us for 193.)
+                        float most = warp_most(fmaxf(row_most[0], row_most[1]));
+                        const float least = warp_most(fminf(row_least[0], row_least[1]));
+                        float(*part)[2] = half.s_most[c & 1];  // (read for piece c by all before any of them meets for c + 1)
+                        if (lane == 0) part[warp - 16][0] = most, part[warp - 16][1] = least;
+                        if (!meet(1)) { ok = false; break; }
+                        most = fmaxf(fmaxf(part[0][0], part[1][0]), fmaxf(part[2][0], part[3][0]));
+                        const float l0 = fmaxf(part[0][1], part[1][1]), l1 = fmaxf(part[2][1], part[3][1]);
+                        // (at dim_k = 64 two warps have one half of the columns, two the other)
+                        const bool one = (DK == 128 ? fmaxf(l0, l1) : fminf(l0, l1)) >= most * 0x1p-16f;
+                        // (of four buffers each: the results of four pieces ago have been read)
+                        if (tid == 0) half.s_columns[c & 3] = !one;
+                        if (one) {
+                            const int e = exponent14(most);
+                            if (tid == 0) half.s_back[c & 3] = pow2i(e - 14);
+                            if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
+                            const uint64_t unit2 = f2_pack(pow2i(14 - e), pow2i(14 - e));
+                            copy([&](int) { return unit2; });
+                        } else {  // nothing of an infinite or far larger column may reach another
+#pragma unroll
+                            for (int i = 0; i < NC / 2; i += 2) {
+                                const float2 y = f2_get(x[i]), z = f2_get(x[i + 1]);
+                                const float4 m = make_float4(warp_most(y.x), warp_most(y.y), warp_most(z.x), warp_most(z.y));
+                                if (lane == 0) *reinterpret_cast<float4*>(&half.col_most[warp - 16][c0 + 2 * i]) = m;
+                            }
+                            if (!meet(1)) { ok = false; break; }
+                            if (tid < kSlice) {
+                                const float(*m)[kSlice] = &half.col_most[DK == 128 ? 0 : tid >> 5 << 1];
+                                most = fmaxf(m[0][tid], m[1][tid]);
+                                if (DK == 128) most = fmaxf(most, fmaxf(m[2][tid], m[3][tid]));
+                                const int e = exponent14(most);
+                                half.col_up[tid] = pow2i(14 - e);
+                                half.col_back[c & 3][tid] = pow2i(e - 14);
+                            }
+                            if (!meet(1)) { ok = false; break; }
+                            if (c > 0 && !wait(s_free, c - 1)) { ok = false; break; }
+                            const uint64_t* up = reinterpret_cast<const uint64_t*>(&half.col_up[c0]);
+                            copy([&](int i) { return up[i]; });
+                        }
                     }
                     fence_proxy_async_smem();
                     arrive_warp(s_full);
@@ -798,6 +858,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!wait(u_full, c)) { ok = false; break; }
                 tcgen05_after_sync();
                 const float back = BF ? 1.f : half.v_back[c & 3], back2 = back / kSecond;
+                if (!BF && !STATES) none_yet();
 #pragma unroll
                 for (int i = 0; i < NC / 2; i += 8) {
                     float u[2][16];  // the first numbers' product, and the others'
@@ -810,6 +871,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         const uint64_t y = BF ? f2_add(first, other)
                                               : f2_fma(first, f2_pack(back, back), f2_mul(other, f2_pack(back2, back2)));
                         x[i + j] = f2_fma(x[i + j], keep, f2_fma(x[i + j], once, y));
+                        if (!BF && !STATES) count(i + j);
                     }
                 }
                 tcgen05_before_sync();
@@ -854,8 +916,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     tcgen05_after_sync();
                     float fi = ex2_approx(sum) * l.scale, fa = l.scale;
                     if (c + 1 < base + pieces && !decays(c + 1)) { ok = false; break; }  // (early: their buffer is waited for)
+                    bool columns = false;
                     if constexpr (!BF) {
-                        fi *= s_unit[c & 1];
+                        columns = half.s_columns[c & 3];
+                        if (!columns) fi *= half.s_back[c & 3];
                         fa *= half.row_unit[c & 3][row];
                     }
                     const uint64_t fi2 = f2_pack(fi, fi), fa2 = f2_pack(fa, fa);
@@ -863,9 +927,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     // All of a row is read before any of it is stored, for the next product waits for that (117 us for 64 pieces,
                     // in slices 142); where a CTA goes on with other work, whose loop wants registers too, in slices (packed
                     // prompts 277 us, whole 317).
-                    constexpr int WORDS = MORE ? 8 : kSlice / 2;
-                    uint32_t w[WORDS];
-                    auto out_words = [&](char* to) {
+                    // A slice of 16 columns, words at w0 .. of w; factor(j): what pair j of OI's columns is multiplied by.
+                    auto slice_of = [&](int c0, auto& w, int w0, auto factor) {
+                        float x[16], y[16];
+                        tmem_ld16(lanes + OI_COL + c0, x);
+                        tmem_ld16(lanes + OA_COL + c0, y);
+                        tmem_wait_ld();
+                        if (c0 + 16 == kSlice) {
+                            tcgen05_before_sync();
+                            arrive_warp(o_free);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), factor(c0 + j), f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
+                            w[w0 + j / 2] = M::pack(z.x, z.y);
+                        }
+                        if (poisoned) {
+                            const uint8_t* mark = &bad[(c & 3) * 64 + c0];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (mark[j] <= row) w[w0 + j / 2] |= 0x7fffu << (16 * (j & 1));
+                        }
+                    };
+                    auto out_words = [&](char* to, auto& w) {
+                        constexpr int WORDS = sizeof(w) / 4;
                         if (row < n) {
                             if (sectors) {
 #pragma unroll
@@ -881,32 +966,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             }
                         }
                     };
-                    constexpr int AT_ONCE = MORE ? 1 : kSlice / 16;
-#pragma unroll AT_ONCE
-                    for (int c0 = 0; c0 < kSlice; c0 += 16) {
-                        float x[16], y[16];
-                        tmem_ld16(lanes + OI_COL + c0, x);
-                        tmem_ld16(lanes + OA_COL + c0, y);
-                        tmem_wait_ld();
-                        if (c0 + 16 == kSlice) {
-                            tcgen05_before_sync();
-                            arrive_warp(o_free);
+                    if (!BF && columns) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kSlice; c0 += 16) {
+                            uint32_t w[8];
+                            slice_of(c0, w, 0, [&](int j) { return f2_mul(fi2, *reinterpret_cast<const uint64_t*>(&half.col_back[c & 3][j])); });
+                            out_words(out + c0 * sizeof(T), w);
                         }
-                        const int w0 = MORE ? 0 : c0 / 2;
+                    } else if constexpr (MORE) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kSlice; c0 += 16) {
+                            uint32_t w[8];
+                            slice_of(c0, w, 0, [&](int) { return fi2; });
+                            out_words(out + c0 * sizeof(T), w);
+                        }
+                    } else {
+                        uint32_t w[kSlice / 2];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 z = f2_get(f2_fma(f2_pack(x[j], x[j + 1]), fi2, f2_mul(f2_pack(y[j], y[j + 1]), fa2)));
-                            w[w0 + j / 2] = M::pack(z.x, z.y);
-                        }
-                        if (poisoned) {
-                            const uint8_t* mark = &bad[(c & 3) * 64 + c0];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (mark[j] <= row) w[w0 + j / 2] |= 0x7fffu << (16 * (j & 1));
-                        }
-                        if (MORE) out_words(out + c0 * sizeof(T));
+                        for (int c0 = 0; c0 < kSlice; c0 += 16) slice_of(c0, w, c0 / 2, [&](int) { return fi2; });
+                        out_words(out, w);
                     }
-                    if (!MORE) out_words(out);
                     out += kPiece * pitch;
                     if (poisoned) {  // the columns' marks are used again four pieces on
                         if (!meet(2)) { ok = false; break; }

@@ -1,5 +1,5 @@
 """Linear attention where numbers leave the range of the rows' type, on the GPU against the recurrence in 64 bits: decays of
-both signs, keys and queries that single a token out."""
+both signs, keys and queries that single a token out, states with columns of very different size."""
 import math
 
 import numpy as np
@@ -144,3 +144,44 @@ def test_decode_of_growing_decays(dtype):
     want, tol, after, after_tol = linear(q, k, v, d, was[1], list(range(n)), list(range(n)), starts, SCALE, dtype)
     assert torch.all((out.double().cpu() - want).abs() <= tol)
     assert torch.all((state[1].double().cpu() - after).abs() <= after_tol)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("n,length", [(1, 300), (1, 1100), (24, 200)])
+def test_a_column_of_the_state_leaves_the_others_alone(dtype, dk, dv, n, length):
+    """Infinite, NaN, or 2^30 larger than the others: their results are those of a state without it."""
+    n_v = 1 if n == 1 else 8
+    q, k, v, d, state, starts = inputs(dtype, [length] * n, 1, n_v, dk, dv, "head", seed=69)
+    own, T = list(range(n)), n * length
+    was = state.clone()
+    base = run(dtype, q, k, v, d, state, own, own, starts)[:T]
+    rest = torch.arange(dv, device="cuda") != 5
+    for value in (math.inf, math.nan, None):
+        st = was.clone()
+        if value is None:
+            st[1, :, 0, :, 5] *= 2.0 ** 30
+        else:
+            st[1, :, 0, 3, 5] = value
+        out = run(dtype, q, k, v, d, st, own, own, starts)[:T]
+        assert torch.equal(out[:, :, rest], base[:, :, rest]) and torch.equal(out[:, 1:], base[:, 1:])
+        assert torch.equal(st[1, :n, 0][..., rest], state[1, :n, 0][..., rest]) and torch.equal(st[1, :n, 1:], state[1, :n, 1:])
+        if value is not None:
+            assert not torch.isfinite(out[:, 0, 5]).any() and not torch.isfinite(st[1, :n, 0, 3, 5]).any()
+    assert pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_an_infinity_that_a_short_call_left(dtype):
+    """A decode step's infinite v stays in its column of the state; the next long chunk's other columns are as without it."""
+    q, k, v, d, state, starts = inputs(dtype, [300], 1, 2, 128, 64, "head", seed=70, behind=0)
+    other = state.clone()
+    v2 = v[:1].clone()
+    v2[0, 1, 7] = math.inf
+    run(dtype, q[:1], k[:1], v[:1], d, state, [0], [0], None, decode=True)
+    run(dtype, q[:1], k[:1], v2, d, other, [0], [0], None, decode=True)
+    assert torch.isinf(other[1, 0, 1, :, 7]).all()
+    a, b = (run(dtype, q, k, v, d, st, [0], [0], starts) for st in (state, other))
+    touched = torch.zeros_like(a, dtype=torch.bool)
+    touched[:, 1, 7] = True
+    assert torch.equal(a[~touched], b[~touched]) and not torch.isfinite(b[touched]).any()
