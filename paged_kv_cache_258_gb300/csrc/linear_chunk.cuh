@@ -93,7 +93,8 @@ struct Pair16<__nv_bfloat16> {
 
 // A piece's 128 log decays, as the roles need them.
 struct __align__(16) PieceGates {
-    float hi[kPiece];              // minus the sum from the start of a token's block of 32 to it, base 2
+    float hi[kPiece];              // minus the sum from the start of a token's block of 32 to it, base 2 (fp16: or from behind the
+                                   // last token up to it that forgets; HalfScales::front is from the start)
     float col[kPiece];             // 2^(sum from behind the token to its block's end)
     float block[4];                // sum over each block
     float after[4];                // 2^(sum over the blocks behind it)
@@ -103,6 +104,8 @@ struct __align__(16) PieceGates {
 
 // fp16: the powers of two that bring what its products take into its range.
 struct __align__(16) HalfScales {
+    uint32_t forgotten[2][kPiece]; // of a token's block of 32: those that it, or one between, forgets
+    float front[2][kPiece];        // sums from a token's block's start all the same
     float row_unit[4][kPiece];     // of the rows of P', undone: 2^-shift
     float row_most[2][2][kPiece];  // largest weighted pair of a row's even and odd halves
     float v_most[2][8];            // largest number of V~ that a warp has
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
             const uint32_t from_col = lanes + P_COL + side;
             uint32_t to_col = lanes + PW_COL + side / 2;  // of two buffers
-            uint32_t seen[8];  // of the block on the diagonal: the pairs of columns up to the row
+            uint32_t seen[8];  // bf16, of the block on the diagonal: the pairs of columns up to the row
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 seen[j] = (lane >= side + 2 * j ? 0xffffu : 0u) | (lane > side + 2 * j ? 0xffff0000u : 0u);
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 for (int c = base; c < base + pieces; ++c) {
                     const Gates& g = gates[c & 1];
                     if (!wait(&g_full[c & 1], c >> 1)) { ok = false; break; }
-                    const float mine = -g.hi[row];
+                    const float mine = BF ? -g.hi[row] : half.front[c & 1][row];
                     if (!wait(p_full, c)) { ok = false; break; }
                     tcgen05_after_sync();
                     float shift = 0.f;  // log2 of what the row is multiplied by
@@ -545,7 +548,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     to_col = lanes + PW_COL + (c & 1) * 64 + side / 2;
                     tcgen05_after_sync();
                     {  // the block on the diagonal: an exponential for each pair
-                        const uint64_t hi2 = f2_pack(mine, mine);
+                        const float hi = BF ? mine : -g.hi[row];
+                        const uint64_t hi2 = f2_pack(hi, hi);
                         const ulonglong2* gh = reinterpret_cast<const ulonglong2*>(&g.hi[w4 * 32 + side]);
                         float x[16];
 #pragma unroll
@@ -554,6 +558,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             const float2 d0 = f2_get(f2_add(hi2, y.x)), d1 = f2_get(f2_add(hi2, y.y));
                             x[4 * j] = ex2_approx(d0.x), x[4 * j + 1] = ex2_approx(d0.y);
                             x[4 * j + 2] = ex2_approx(d1.x), x[4 * j + 3] = ex2_approx(d1.y);
+                        }
+                        if constexpr (!BF) {
+                            const uint32_t forgotten = half.forgotten[c & 1][row] >> side;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] = forgotten & (1u << j) ? 0.f : x[j];
                         }
                         tmem_wait_ld();
 #pragma unroll
@@ -567,7 +576,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     if constexpr (!BF) {  // the row's largest, of both halves, goes to 2^14
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) most = fmaxf(most, j <= lane - side ? fabsf(pf[j]) : 0.f);
+                        for (int j = 0; j < 16; ++j) {
+                            pf[j] = j <= lane - side ? pf[j] : 0.f;
+                            most = fmaxf(most, fabsf(pf[j]));
+                        }
                         half.row_most[c & 1][side >> 4][row] = most;  // (the other warp has read those of two pieces ago: it met since)
                         arrive_warp(&halves[w4]);
                         if (!wait(&halves[w4], c)) { ok = false; break; }
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float2 y = f2_get(f2_mul(f2_pack(pf[2 * j], pf[2 * j + 1]), up));
-                            w[j] = M::pack(y.x, y.y) & seen[j];
+                            w[j] = M::pack(y.x, y.y);
                         }
                     }
                     float from = mine + shift;  // the sum from the end of block b to the row
@@ -899,7 +911,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             auto decays = [&](int c) -> bool {
                 if (!wait(&g_full[c & 1], c >> 1)) return false;
                 const Gates& g = gates[c & 1];
-                sum = -g.hi[row];
+                sum = BF ? -g.hi[row] : half.front[c & 1][row];
 #pragma unroll 1
                 for (int i = 0; i < w4; ++i) sum += g.block[i];
                 arrive_warp(&g_free[c & 1]);
@@ -1152,15 +1164,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             __syncwarp();
         } else {
-            // ===================== sums of the log decays: lane = token of a block of 32 =====================
+            // ===================== sums of the log decays: lane = four tokens, eight lanes a block of 32 =====================
             // Sums from a block's front and from its back are added up apart: a difference of two front sums would lose
-            // what comes behind a token that forgets.
+            // what comes behind a token that forgets. The pairs inside a block do take a difference of two front sums. For fp16
+            // those begin anew behind a token that forgets, and what it makes forgotten is masked. bf16, which has no room
+            // left for that, bears it: 32 that forget make sums of -4,800, whose last bit is 2^-11, and so its weights are
+            // off by up to 2^-10 where they are rounded by 2^-9 (as are fp16's in a block of 32 decays of 2^-140 each).
+            const int sub = lane & 7;
             float raw[4];
             auto fetch = [&](int c) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int t = c * kPiece + b * 32 + lane;
-                    raw[b] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const int t = c * kPiece + lane * 4 + i;
+                    raw[i] = l.log_decay && t < tokens ? l.log_decay[(size_t)(t0 + t) * l.decay_stride + h] : 0.f;
                 }
             };
             begin();
@@ -1168,34 +1184,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fetch(0);
 #pragma unroll 1
                 for (int c = base; c < base + pieces; ++c) {
-                    float front[4], back[4], all[4];
+                    float y[4], front[4], back[4], all[4];
+                    uint32_t forgets = 0;  // fp16: of the lane's four
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    for (int i = 0; i < 4; ++i) {
                         // 2^-150 is 0 in fp32, 2^(10^4) infinite: a token that forgets (-infinity) takes part in sums; NaN stays
-                        float y = raw[b] < -104.f ? -104.f : raw[b];
-                        y = (y > 1e4f ? 1e4f : y) * 1.44269504f;
-                        front[b] = y;
-                        back[b] = __shfl_down_sync(0xffffffffu, y, 1);
-                        if (lane == 31) back[b] = 0.f;
+                        if (!BF && raw[i] < -104.f) forgets |= 1u << i;
+                        y[i] = raw[i] < -104.f ? -104.f : raw[i];
+                        y[i] = (y[i] > 1e4f ? 1e4f : y[i]) * 1.44269504f;
                     }
                     if (c + 1 < base + pieces) fetch(c + 1 - base);
+                    // sums over the block's lanes up to this one and from it on, then those before and behind it
+                    float up = (y[0] + y[1]) + (y[2] + y[3]), down = up;
 #pragma unroll
-                    for (int o = 1; o < 32; o *= 2)
+                    for (int o = 1; o < 8; o *= 2) {
+                        const float f = __shfl_up_sync(0xffffffffu, up, o, 8), k = __shfl_down_sync(0xffffffffu, down, o, 8);
+                        if (sub >= o) up += f;
+                        if (sub + o < 8) down += k;
+                    }
+                    up = __shfl_up_sync(0xffffffffu, up, 1, 8), down = __shfl_down_sync(0xffffffffu, down, 1, 8);
+                    front[0] = (sub > 0 ? up : 0.f) + y[0];
+                    back[3] = sub < 7 ? down : 0.f;
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float f = __shfl_up_sync(0xffffffffu, front[b], o), k = __shfl_down_sync(0xffffffffu, back[b], o);
-                            if (lane >= o) front[b] += f;
-                            if (lane + o < 32) back[b] += k;
-                        }
+                    for (int i = 1; i < 4; ++i) front[i] = front[i - 1] + y[i], back[3 - i] = back[4 - i] + y[4 - i];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[b], 31);
+                    for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(0xffffffffu, front[3], b * 8 + 7);
                     if (c >= 2 && !wait(&g_free[c & 1], (c >> 1) - 1)) { ok = false; break; }
                     Gates& g = gates[c & 1];
+                    if constexpr (!BF) {
+                        *reinterpret_cast<float4*>(&half.front[c & 1][lane * 4]) = make_float4(front[0], front[1], front[2], front[3]);
+                        uint32_t gone[4] = {0u, 0u, 0u, 0u};
+                        if (__any_sync(0xffffffffu, forgets != 0)) {
+                            uint32_t block = forgets << sub * 4;  // of the block's 32
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        g.hi[b * 32 + lane] = -front[b];
-                        g.col[b * 32 + lane] = ex2_approx(back[b]);
+                            for (int o = 1; o < 8; o *= 2) block |= __shfl_xor_sync(0xffffffffu, block, o);
+                            const uint32_t before = block & ((1u << sub * 4) - 1);  // in lanes before this one
+                            const int last = forgets ? sub : before ? (31 - __clz(before)) / 4 : 0;  // the lane of the last
+                            // sums from behind the last one: over the lane, then from lane to lane
+                            float since = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) since = forgets & (1u << i) ? 0.f : since + y[i];
+#pragma unroll
+                            for (int o = 1; o < 8; o *= 2) {
+                                const float f = __shfl_up_sync(0xffffffffu, since, o, 8);
+                                if (sub - last >= o) since += f;
+                            }
+                            since = __shfl_up_sync(0xffffffffu, since, 1, 8);
+                            if (sub == 0) since = 0.f;
+                            uint32_t mask = before ? (1u << (31 - __clz(before))) - 1 : 0u;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                since += y[i];
+                                if (forgets & (1u << i)) since = 0.f, mask = (1u << (sub * 4 + i)) - 1;
+                                front[i] = since;
+                                gone[i] = mask;
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(&half.forgotten[c & 1][lane * 4]) = make_uint4(gone[0], gone[1], gone[2], gone[3]);
                     }
+                    *reinterpret_cast<float4*>(&g.hi[lane * 4]) = make_float4(-front[0], -front[1], -front[2], -front[3]);
+                    *reinterpret_cast<float4*>(&g.col[lane * 4]) =
+                        make_float4(ex2_approx(back[0]), ex2_approx(back[1]), ex2_approx(back[2]), ex2_approx(back[3]));
                     const float sum = (all[0] + all[1]) + (all[2] + all[3]);
                     if (lane < 4) {
                         g.block[lane] = lane == 0 ? all[0] : lane == 1 ? all[1] : lane == 2 ? all[2] : all[3];

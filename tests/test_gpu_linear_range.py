@@ -1,12 +1,12 @@
 """Linear attention where numbers leave the range of the rows' type, on the GPU against the recurrence in 64 bits: decays of
-both signs, keys and queries that single a token out, states with columns of very different size."""
+both signs, keys and queries that single a token out, states with columns of very different size, many tokens that forget."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from linear_oracle import linear
+from linear_oracle import HALF_STEP, linear
 from paged_kv_cache_258_gb300 import pkv
 from test_gpu_linear import RAGGED, SCALE, inputs, per_token, run
 
@@ -185,3 +185,53 @@ def test_an_infinity_that_a_short_call_left(dtype):
     touched = torch.zeros_like(a, dtype=torch.bool)
     touched[:, 1, 7] = True
     assert torch.equal(a[~touched], b[~touched]) and not torch.isfinite(b[touched]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_many_tokens_that_forget(dtype):
+    lens = [320, 150]
+    q, k, v, _, state, starts = inputs(dtype, lens, 2, 4, 64, 64, "none", seed=72)
+    g = torch.Generator().manual_seed(73)
+    T = sum(lens)
+    d = -0.01 * torch.rand((T + 3, 4), generator=g)
+    t = torch.arange(T + 3)
+    d[t % 32 < 20] = -math.inf
+    d[(t % 32 > 22) & (t % 5 == 0), 1] = -90.0
+    check(dtype, q, k, v, d.cuda(), state, [0, -1], [0, 1], starts)
+
+
+def test_weights_behind_tokens_that_forget():
+    """Each result is one term: exp(g_i) v_(i-1), v = 1 and products of 1, so that the weight's rounding to fp16 is the only one
+    (its result is then a number of the type already): half a step, and 2^-20 for the sums, exponential and products in
+    fp32. Twenty tokens of each 32 forget."""
+    T, dk = 320, 64
+    q, k, v, _, state, starts = inputs("f16", [T], 1, 4, dk, 64, "none", seed=74)
+    k.zero_(), q.zero_(), v.fill_(1.0)
+    t = torch.arange(T)
+    k[t, 0, t % dk] = 1.0
+    q[t, 0, (t - 1) % dk] = 1.0
+    d = -0.7 * torch.rand((T, 4), generator=torch.Generator().manual_seed(75))
+    d[t % 32 < 20] = -math.inf
+    gates = torch.cat([d, torch.zeros(3, 4)]).cuda()
+    out = run("f16", q, k, v, gates, state, [-1], [-1], starts)[:T].double().cpu()
+    want = SCALE * torch.exp(d.double())[:, :, None].expand(-1, -1, 64)
+    rows = (t % 32 >= 20) & (t > 0)
+    assert torch.all((out[rows] - want[rows]).abs() <= (HALF_STEP["f16"] + 2.0 ** -20) * want[rows])
+    assert pkv.pkv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_what_is_not_finite_stays_behind_a_token_that_forgets(dtype, value):
+    """0 times it is NaN: a key's infinity or NaN, in the forgetting token's own block of 32, an earlier one, or an earlier piece."""
+    q, k, v, d, state, starts = inputs(dtype, [200], 1, 2, 64, 64, "token", seed=80, behind=0)
+    d.clamp_(min=-0.1)
+    d[[40, 60, 100, 101, 190]] = -math.inf
+    base = run(dtype, q, k, v, d, state.clone(), [0], [0], starts)
+    for at in (33, 58, 99, 10):
+        k2 = k.clone()
+        k2[at, 0, 3] = value
+        st = state.clone()
+        out = run(dtype, q, k2, v, d, st, [0], [0], starts)
+        assert torch.equal(out[:at], base[:at]) and not torch.isfinite(out[at:]).any()
+        assert not torch.isfinite(st[1, 0, :, 3]).any()
