@@ -468,7 +468,8 @@ class LinearStates:
     """The states of a hybrid model's linear layers ("PagedAttention e continuous batching", "01 - Conceito", paragraph
     2: beside the paged cache, a memory of fixed size for each sequence): a slot of ``state`` for each sequence, all
     layers of it. ``slots`` gives what pkv_linear_prefill and pkv_linear_decode take; a sequence that has not been
-    listed there yet starts from zeros, whatever its slot held."""
+    listed there yet starts from zeros, whatever its slot held. ``slots`` and ``fork`` work on `stream`, else on the current
+    one, as those calls do: steps that follow one another on several streams are the caller's to order."""
 
     def __init__(self, desc: pkv.LinearDesc, device=None, stream=None):
         import torch
@@ -477,12 +478,16 @@ class LinearStates:
             raise pkv.PkvError(rc, "LinearStates")
         self.desc = desc
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self._on(stream)):
             self.state = torch.zeros(pkv.linear_state_shape(desc), device=self.device)
+        self._on(stream).synchronize()  # (steps may run on any stream)
         self._slot: dict = {}
         self._free = list(range(desc.n_slots))
         self._begun: set = set()
+
+    def _on(self, stream):
+        import torch
+        return stream if stream is not None else torch.cuda.current_stream(self.device)
 
     def add(self, seq_id: int) -> int:
         """A slot for a new sequence; PkvError (no blocks) if all are taken."""
@@ -493,14 +498,14 @@ class LinearStates:
         self._slot[seq_id] = self._free.pop(0)
         return self._slot[seq_id]
 
-    def fork(self, parent: int, child: int) -> int:
+    def fork(self, parent: int, child: int, stream=None) -> int:
         """child starts with parent's state as it is behind what the stream holds so far (prefix sharing)."""
         import torch
         if parent not in self._slot:
             raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"fork({parent}, {child})")
         slot = self.add(child)
         if parent in self._begun:
-            with torch.cuda.stream(self.stream):
+            with torch.cuda.stream(self._on(stream)):
                 self.state[:, slot].copy_(self.state[:, self._slot[parent]])
             self._begun.add(child)
         return slot
@@ -517,9 +522,9 @@ class LinearStates:
             raise pkv.PkvError(pkv.PKV_ERR_INVALID_ARG, f"restart({seq_id})")
         self._begun.discard(seq_id)
 
-    def slots(self, seq_ids):
+    def slots(self, seq_ids, stream=None):
         """(src_slots, dst_slots), int32 [n] on the device, for one step over distinct sequences. The step counts as
-        run: should it not be, `restart` those that were to begin with it."""
+        run: should it not be, `restart` those that were to begin with it. For calls on the same stream."""
         import torch
         ids = [int(x) for x in seq_ids]
         if len(set(ids)) != len(ids) or any(x not in self._slot for x in ids):
@@ -527,7 +532,7 @@ class LinearStates:
         dst = [self._slot[x] for x in ids]
         src = [d if x in self._begun else -1 for x, d in zip(ids, dst)]
         self._begun.update(ids)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self._on(stream)):
             both = torch.tensor([src, dst], dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
         return both[0], both[1]
 
