@@ -652,7 +652,7 @@ int pkv_linear_prefill(const pkv_linear_desc* desc, int32_t layer, const void* q
  * A length outside [0, max_blocks_per_seq*16] sets PKV_DEV_BAD_CONTEXT_LEN, a negative count PKV_DEV_BAD_QUERY_RANGE:
  * such a row gets no tokens and counts as served. `used` outside [0, n_free] counts as nothing left and sets
  * PKV_DEV_BAD_FREE_LIST, as does a fresh id outside [0, num_blocks); an old one sets PKV_DEV_BAD_BLOCK_ID.
- * n_seqs at most 65,535. Arrays other than those named do not overlap.
+ * n_seqs at most 65,535, max_tokens at most 2^31 - 2. Arrays other than those named do not overlap.
  */
 int pkv_extend_tables(int32_t num_blocks, const int32_t* free_blocks, int32_t n_free, const int32_t* used,
                       int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,

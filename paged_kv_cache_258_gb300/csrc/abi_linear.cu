@@ -215,6 +215,7 @@ int pkv_extend_tables(int32_t num_blocks, const int32_t* free_blocks, int32_t n_
     if (num_blocks <= 0 || n_free < 0 || n_seqs < 0 || max_tokens < 0) return PKV_ERR_INVALID_ARG;
     if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24)) return PKV_ERR_INVALID_ARG;
     if (n_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (max_tokens > 0x7ffffffe) return PKV_ERR_UNSUPPORTED;  // (2^31 - 1 is what a sum past it saturates at)
     if ((n_free > 0 && !free_blocks) || !used || !query_start || !totals || (max_tokens > 0 && !slot_mapping))
         return PKV_ERR_INVALID_ARG;
     if (n_seqs > 0 && (!block_tables || !context_lens || !new_lens)) return PKV_ERR_INVALID_ARG;

@@ -3,7 +3,8 @@
 // What pkv_mgr_extend does row after row on the host is a prefix sum on the device: with need_i = the blocks that
 // row i's new tokens take beyond its last one, row i gets the free blocks behind those of the rows before it, and its
 // tokens the places behind theirs. A row is served if the sums up to it fit; sums only grow, so the rows served are
-// those before the first that does not fit. Sums saturate at 2^31 - 1, which no limit reaches: a saturated row fails.
+// those before the first that does not fit. Sums saturate at 2^31 - 1, above the largest max_tokens: a row whose tokens saturate
+// fails, and blocks, never more than tokens, saturate no earlier.
 //
 // Everything that a row decides (its first token, its first free block) is worked out by every CTA for itself, 1,024
 // rows at a time, and kept in shared memory; the tokens are then shared out by warps, 32 at a time, each finding its
