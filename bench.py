@@ -894,7 +894,7 @@ def run_e2e(args, batch, cache, state, bufs, scale, device) -> dict:
 
 DECODE_SOURCES = ("decode.cuh", "decode_mma.cuh", "common.cuh")
 COPY_SOURCES = ("append_copy.cu", "common.cuh")
-PREFILL_SOURCES = ("prefill_umma.cuh", "umma.cuh", "decode_mma.cuh", "common.cuh", "prefill_bf16.cu")
+PREFILL_SOURCES = ("prefill_umma.cuh", "umma.cuh", "decode_mma.cuh", "common.cuh", "arith.cuh", "prefill_bf16.cu")
 
 
 def traffic_per_launch(config: str, algorithmic: float, profile: str | None = None,

@@ -47,6 +47,7 @@
 
 #include <type_traits>
 
+#include "arith.cuh"
 #include "common.cuh"
 #include "linear.h"
 #include "umma.cuh"

@@ -18,6 +18,7 @@
 // a second); chunks of few heads, one warp's latency (60 ns a token).
 #include <type_traits>
 
+#include "arith.cuh"
 #include "common.cuh"
 #include "linear.h"
 

@@ -52,6 +52,7 @@
 
 #include <type_traits>
 
+#include "arith.cuh"
 #include "common.cuh"
 #include "decode_mma.cuh"
 #include "internal.h"
