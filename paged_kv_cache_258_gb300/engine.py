@@ -542,8 +542,10 @@ class DeviceTables:
     captured in a graph and replayed, or that are to run ahead of the host.
 
     The batch takes blocks in the order of the manager's free list, row by row, as the manager itself would; ``follow``
-    then brings the manager to the same state. Until it has, nothing else may be done with the manager. A sequence whose
-    last block is partly filled and shared is refused: its copy on write is the manager's.
+    then brings the manager to the same state. Whatever else is done with the manager (a sequence admitted, forked, freed or
+    appended to) makes the tables stale, for their list of free blocks is a copy: `extend` and `follow` then refuse
+    (ValueError), and new tables have to be made. A sequence whose last block is partly filled and shared is refused: its copy
+    on write is the manager's.
     """
 
     def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, max_tokens: int | None = None, stream=None):
@@ -562,6 +564,7 @@ class DeviceTables:
             if c % pkv.BLOCK and cache.mgr.refcount(int(tables[i, c // pkv.BLOCK])) > 1:
                 raise ValueError(f"sequence {int(self.seq_ids[i])}: its last block is partly filled and shared")
         free = np.asarray(cache.mgr.free_list(), dtype=np.int32)
+        self._order, self._taken, self._seen = free, 0, self._manager()  # as the manager is brought along
         dev = cache.device
         with torch.cuda.stream(self.stream):
             self.tables, self.lens, self.free = (torch.from_numpy(x.copy()).to(dev) for x in (tables, lens, free))
@@ -570,18 +573,35 @@ class DeviceTables:
             self.totals = torch.zeros(3, dtype=torch.int32, device=dev)  # blocks taken, rows served, new tokens
         self.stream.synchronize()  # (steps may run on any stream)
 
+    def _manager(self) -> bytes:
+        """The manager's counts (blocks, sequences, forks, copies), which everything but adding and freeing like amounts moves."""
+        return self.cache.mgr.stats_image()
+
+    def _check_manager(self) -> None:
+        if self._manager() != self._seen:
+            raise ValueError("the manager has changed by other than follow: these tables are stale, make new ones")
+
     def extend(self, new_tokens=None, stream=None) -> None:
         """One step's new tokens: int32 [n] on the device, or one for each row. tables, lens, slots, query_start and
         totals are those of the step when the launch has run: on `stream`, else on the current one, which may be capturing."""
+        self._check_manager()
         pkv.pkv_extend_tables(self.cache.desc.num_blocks, self.free, self.totals[:1], self.tables, self.lens, new_tokens,
                               self.slots, self.query_start, self.lens, self.totals, stream=stream)
 
     def follow(self, new_tokens=None) -> int:
-        """The manager's part of one extend, with the same counts (host integers); returns the rows served."""
+        """The manager's part of one extend, with the same counts (host integers); returns the rows served. ValueError if the
+        manager gives other blocks than the device took (sequences were added and freed in between)."""
         mgr = self.cache.mgr
         counts = [1] * self.n if new_tokens is None else [int(x) for x in new_tokens]
         if len(counts) != self.n:
             raise ValueError("one count for each row")
+        self._check_manager()
+        try:
+            return self._follow(mgr, counts)
+        finally:
+            self._seen = self._manager()
+
+    def _follow(self, mgr, counts) -> int:
         total = 0
         for i, m in enumerate(counts):
             sid = int(self.seq_ids[i])
@@ -592,11 +612,15 @@ class DeviceTables:
             if m > 0:
                 if total > self.max_tokens or -(-(ctx + m) // pkv.BLOCK) > self.max_blocks:
                     return i
-                rc = mgr.extend(sid, m)[0]
+                rc, slots, _, _ = mgr.extend(sid, m)
                 if rc == pkv.PKV_ERR_NO_BLOCKS:
                     return i
                 if rc != pkv.PKV_OK:
                     raise pkv.PkvError(rc, f"extend({sid}, {m})")
+                fresh = slots[-ctx % pkv.BLOCK::pkv.BLOCK] // pkv.BLOCK
+                if not np.array_equal(fresh, self._order[self._taken:self._taken + len(fresh)]):
+                    raise ValueError(f"sequence {sid}: the manager's blocks are not those that the device took")
+                self._taken += len(fresh)
         return self.n
 
 

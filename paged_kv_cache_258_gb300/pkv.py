@@ -1276,6 +1276,12 @@ class BlockManager:
         _check(lib().pkv_mgr_stats(self._h, ctypes.byref(st)), "pkv_mgr_stats")
         return st.as_dict()
 
+    def stats_image(self) -> bytes:
+        """The same as bytes, to see at little cost whether anything moved."""
+        st = Stats()
+        _check(lib().pkv_mgr_stats(self._h, ctypes.byref(st)), "pkv_mgr_stats")
+        return bytes(st)
+
     def refcount(self, block: int) -> int:
         return int(lib().pkv_mgr_refcount(self._h, int(block)))
 
