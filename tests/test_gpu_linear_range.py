@@ -235,3 +235,19 @@ def test_what_is_not_finite_stays_behind_a_token_that_forgets(dtype, value):
         out = run(dtype, q, k2, v, d, st, [0], [0], starts)
         assert torch.equal(out[:at], base[:at]) and not torch.isfinite(out[at:]).any()
         assert not torch.isfinite(st[1, 0, :, 3]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n_qk,group", [(1, 16), (2, 40), (1, 64), (33, 1)])
+@pytest.mark.parametrize("lens", [[1, 30], [200, 130]])
+def test_many_heads_and_large_groups(dtype, n_qk, group, lens):
+    q, k, v, d, state, starts = inputs(dtype, lens, n_qk, n_qk * group, 64, 64, "token", seed=76)
+    check(dtype, q, k, v, d, state, [0, -1], [1, 2], starts)
+
+
+@pytest.mark.parametrize("dk,dv,n,n_v", [(64, 64, 30, 4), (64, 128, 30, 4), (128, 64, 20, 4), (128, 128, 30, 4), (64, 64, 4, 2),
+                                         (128, 128, 8, 3)])
+def test_short_chunks_of_bf16(dk, dv, n, n_v):
+    lens = [(i * 13) % 34 for i in range(1, n + 1)]
+    q, k, v, d, state, starts = inputs("bf16", lens, n_v, n_v, dk, dv, seed=77 + n)
+    check("bf16", q, k, v, d, state, list(range(n)), list(range(n)), starts)
