@@ -43,28 +43,32 @@ constexpr int kPiece = 128;          // tokens the tensor-core kernel takes at o
 constexpr int kMinShared = 6 * kPiece;  // shortest chunk that is shared out along its length
 
 // Whether a prefill goes by pieces of 128 tokens on the tensor cores or token after token, by what each is estimated to
-// take, in microseconds; fp32 has no choice. (dim_k 128; where 64 differs, it follows in brackets.)
-// With units of (sequence, head, 64 columns):
+// take, in microseconds; fp32 has no choice. With units of (sequence, head, 64 columns), dim_k 128 [64]:
 //   tokens  2.8 [2.4] and a token of the longest sequence 0.05 + 0.0016 a unit [0.035 + 0.0008], of which 40 to 150
-//           count; or over all sequences 0.17 for each million state elements (heads x dim_k x dim_v)
-//   pieces  9.4 [8.0] and 2 [1.4] for each piece of the longest sequence but its first; and where the GPU holds fewer
-//           units, 5 [4.2] and for each round of them 4.5 [3.7] and 2.3 [1.9] for each more piece
-// 48 heads x 128 x 128, bf16: 16, 24 and 64 tokens 6.1, 8.1 and 16 against 9.4; 4 sequences of 16, 32 and 64 tokens
-// 12.0, 20.1 and 36.2 against 18.6; 32 sequences of 16 and 32 tokens 68 and 120 against 97 and 99. 32 heads x 64 x 64,
-// fp16: 16, 32 and 64 tokens 3.2, 4.3 and 6.5 against 7.8; 32 sequences of 32 and 64 tokens 24.3 and 44.9 against 30.
+//           count; or over all sequences 0.17 for each million state elements (heads x dim_k x dim_v), at dim_k 128 from
+//           six units an SM on 0.135, and 9
+//   pieces  bf16 9.4 [7.7] and 1.7 for each piece of the longest sequence but its first, fp16 10.2 [8.2] and 2.4; and where
+//           the GPU holds fewer units, 5 [4.2] and for each round of them bf16 4.5 [3.1] and 2.3 [1.9] for each more
+//           piece, fp16 6.0 [4.2] and 2.5 [2.2]
+// fp16, tokens against pieces: 48 heads x 128 x 128, 16, 32 and 64 tokens 6.6, 9.8 and 16.4 against 10.4; 4 sequences of 16, 32
+// and 64 tokens 12.5, 20.9 and 37.4 against 21.6; 32 sequences of 16, 32 and 64 tokens 69, 123 and 227 against 131 (bf16:
+// 98). 32 heads x 64 x 64, 32, 64 and 100 tokens 4.2, 6.4 and 8.7 against 7.7 to 8.2; 32 sequences of 16, 32 and 64 tokens
+// 14.6, 26.9 and 48.3 against 33 (bf16: 26).
 bool by_pieces(const pkv_linear_desc* d, int n_seqs, int n_tokens, int max_query, int sms) {
     if (d->dtype == PKV_F32 || max_query < 2) return false;
-    const bool small = d->dim_k == 64;
+    const bool small = d->dim_k == 64, half = d->dtype == PKV_F16;
     const double tokens = n_tokens < (double)n_seqs * max_query ? n_tokens : (double)n_seqs * max_query;
     const double elements = (double)d->n_v_heads * d->dim_k * d->dim_v * 1e-6;
     const double units = (double)n_seqs * d->n_v_heads * (d->dim_v / 64);
     const double some = units < 40 ? 40 : units < 150 ? units : 150;
     const double each = small ? 0.035 + 0.0008 * some : 0.05 + 0.0016 * some;
-    const double work = 0.17 * tokens * elements, longest = each * max_query;
-    double pieces = (small ? 8.0 : 9.4) + (small ? 1.4 : 2.0) * ((max_query - 1) / kPiece);
+    const double work = small || units < 6.0 * sms ? 0.17 * tokens * elements : 9 + 0.135 * tokens * elements;
+    const double longest = each * max_query;
+    double pieces = (small ? (half ? 8.2 : 7.7) : (half ? 10.2 : 9.4)) + (half ? 2.4 : 1.7) * ((max_query - 1) / kPiece);
     if (units > sms) {
         const double rounds = (double)(((long long)units + sms - 1) / sms), more = tokens / n_seqs / kPiece - 1;
-        const double all = (small ? 4.2 : 5.0) + rounds * ((small ? 3.7 : 4.5) + (small ? 1.9 : 2.3) * (more > 0 ? more : 0));
+        const double first = small ? (half ? 4.2 : 3.1) : (half ? 6.0 : 4.5), next = small ? (half ? 2.2 : 1.9) : (half ? 2.5 : 2.3);
+        const double all = (small ? 4.2 : 5.0) + rounds * (first + next * (more > 0 ? more : 0));
         pieces = all > pieces ? all : pieces;
     }
     return pieces < (small ? 2.4 : 2.8) + (work > longest ? work : longest);
