@@ -21,7 +21,7 @@ A cache with ``storage="q8"`` holds its rows in 8 bits (half the bytes; pkv_q8_*
 with ``scored=True`` sums every cached position's attention weight, and its ``evict`` shortens the
 sequences to the positions used most (pkv_evict_tokens). Both work together.
 
-A hybrid model's linear layers keep a state of fixed size a sequence: ``LinearStates``. ``DeviceTables`` grows a
+Layers of linear attention (no delta rule) keep a state of fixed size a sequence: ``LinearStates``. ``DeviceTables`` grows a
 batch's block tables on the device, so that a captured graph of whole steps can be replayed without the host.
 
 All device work is in libpkv's kernels; this module only moves arguments.
@@ -465,9 +465,9 @@ class DecodeBatch:
 
 
 class LinearStates:
-    """The states of a hybrid model's linear layers ("PagedAttention e continuous batching", "01 - Conceito", paragraph
-    2: beside the paged cache, a memory of fixed size for each sequence): a slot of ``state`` for each sequence, all
-    layers of it. ``slots`` gives what pkv_linear_prefill and pkv_linear_decode take; a sequence that has not been
+    """The states of layers of linear attention ("PagedAttention e continuous batching", "01 - Conceito", paragraph 2: beside
+    the paged cache, a memory of fixed size for each sequence; there of DeltaNet layers, whose delta rule the calls
+    here do not compute): a slot of ``state`` for each sequence, all layers of it. ``slots`` gives what pkv_linear_prefill and pkv_linear_decode take; a sequence that has not been
     listed there yet starts from zeros, whatever its slot held. ``slots`` and ``fork`` work on `stream`, else on the current
     one, as those calls do: steps that follow one another on several streams are the caller's to order."""
 
