@@ -75,10 +75,12 @@ bool by_pieces(const pkv_linear_desc* d, int n_seqs, int n_tokens, int max_query
 }
 
 // How a call's sequences are shared out along their length: in as many segments as the GPU holds CTAs for them, but no more
-// than kMaxSegments, each of which reads what all before it leave. Two passes of p / n pieces are estimated at 12 us + 3.3 for
-// each piece (fp16 3.6) + 0.25 for each segment, one of p pieces at 6 us + 1.83 (2.25). bf16, 8 heads x 128 x 64: 1,024,
-// 1,536 and 9,005 tokens 20.6, 27.3 and 128 us whole, 18.2, 19.7 and 28.8 in segments of 1, 1 and 4 pieces; 32 heads x 128 x
-// 128, two segments: 1,280 and 16,384 tokens 25.3 and 223 whole, 29.3 and 212 in segments.
+// than kMaxSegments, each of which reads what all before it leave. dim_k 128 [64], in microseconds: two passes of p / n pieces are
+// estimated at 13.5 [10] + 3.1 [2.5] for each piece (fp16 4.1 [3.7]) + 0.25 for each segment, one of p pieces at 6.2 [7.2] + 1.73
+// [1.5] (fp16 2.5 [2.25]). Whole against segments, calls behind one another in a graph: 8 heads x 128 x 64, bf16, 768, 1,024, 1,536 and
+// 9,005 tokens 16.7, 20.1, 26.8 and 121 against 18.0, 18.4, 19.5 and 30.5, fp16 21.9, 26.8, 36.3 and 169 against 19.4, 19.9, 20.8
+// and 34.8; 32 heads x 128 x 128, two segments, 2,048 and 16,384 tokens bf16 35.1 and 219 against 39.7 and 207, fp16 47.2 and 313
+// against 48.7 and 283; 16 heads x 64 x 64, bf16, 768 tokens 16.0 against 14.0.
 constexpr int kMaxSegments = 32;
 struct Segments {
     int n, tokens;
@@ -91,8 +93,9 @@ Segments segments_of(const pkv_linear_desc* d, int n_seqs, int max_query, int sm
     long long n = sms / units < kMaxSegments ? sms / units : kMaxSegments;
     const int each = (int)((pieces + n - 1) / n);
     n = (pieces + each - 1) / each;
-    const bool bf16 = d->dtype == PKV_BF16;
-    if (12.0 + (bf16 ? 3.3 : 3.6) * each + 0.25 * (double)n >= 6.0 + (bf16 ? 1.83 : 2.25) * pieces) return whole;
+    const bool bf16 = d->dtype == PKV_BF16, small = d->dim_k == 64;
+    const double shared = (small ? 10.0 : 13.5) + (small ? (bf16 ? 2.5 : 3.7) : (bf16 ? 3.1 : 4.1)) * each + 0.25 * (double)n;
+    if (shared >= (small ? 7.2 : 6.2) + (small ? (bf16 ? 1.5 : 2.25) : (bf16 ? 1.73 : 2.5)) * pieces) return whole;
     return {(int)n, each * kPiece};
 }
 

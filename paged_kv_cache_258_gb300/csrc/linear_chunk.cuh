@@ -14,9 +14,9 @@
 //                both at most 1 for decays, and one exponential a row and block; only the block on the diagonal takes
 //                one for each pair. A thread takes a row's even or odd halves of 32 columns
 //   warps 8-15   V~, in quarters of 32 rows, four warps on every other one: split into numbers of the type that add up
-//                to it (two of fp16: 2^-22 is left; three of bf16: exact), two beside one another along N, so that one
-//                product of N = 128 gives both sums (the third is added to the second's), and the state keeps fp32's
-//                precision
+//                to it (two of fp16: 2^-22 is left, or 2^-50 of the piece's largest; three of bf16: exact), two beside one
+//                another along N, so that one product of N = 128 gives both sums (the third is added to the second's), and
+//                the state is not rounded to the type
 //   warps 16-19  the state: S in fp32 registers, a thread a row (of dim_k; at dim_k = 64 half a row, the product's 128
 //                rows being K's 64 twice), decays it, adds U and hands the tensor cores a rounded copy
 //   warps 20-23  results: exp(G_i) OI + OA, whole 32-byte sectors of a row from its thread
@@ -37,8 +37,9 @@
 //
 // What bounds it: the walk along a sequence. A piece takes 1.8 us of a CTA, twice what its products take alone: U, the
 // state's sum and rounding, OI and the reading of results follow one another, and the roles' instructions share four
-// schedulers. 48 heads x 128 x 128, bf16, decays of a head and token: 8,192 tokens of one sequence 117 us (2.3 TB/s of
-// q, k, v and results, 0.77 PFLOP/s of products), 4 x 2,048 113 us, 8 x 64 tokens 31 us.
+// schedulers. 48 heads x 128 x 128, bf16: 8,192 tokens of one sequence 115 us (2.3 TB/s of q, k, v and results, 0.78 PFLOP/s
+// of products), 4 x 2,048 112 us, 8 x 64 tokens 32 us. fp16, whose largest numbers are looked for and whose longer loops wait
+// for instructions: 172, 131 and 40 us.
 //
 // A piece past the sequence's end: rows of K and V behind it are zeroed in shared memory (another sequence's rows, or
 // nobody's, NaN perhaps). A non-finite v would reach earlier tokens of its piece through 0 x NaN: it is taken
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (!STATES && a.n_segs > 1) grid_dependency_wait();  // the first pass is done
     if (!STATES && seg > 0) {
         // The state before a later segment: what those before leave, each decayed over the ones behind it. All threads
-        // add it up, a thread's two or three places at once, a dozen loads in flight (9,005 tokens in 18 segments 28.6 us;
-        // place after place 31.4; with a launch of its own for the sums 30).
+        // add it up, a thread's two or three places at once, a dozen loads in flight (9,005 tokens of 8 heads in 18 segments,
+        // calls behind one another in a graph, 28.6 us; place after place 31.4; with a launch of its own for the sums 30).
         float4* to = reinterpret_cast<float4*>(smem + L::VT);
         const size_t step = (size_t)l.n_v * head, at0 = ((size_t)first.s * (a.n_segs - 1) * l.n_v + first.h);
         constexpr int QUADS = DK * kSlice / 4, E = (QUADS + kChunkThreads - 1) / kChunkThreads;

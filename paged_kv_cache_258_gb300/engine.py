@@ -467,9 +467,10 @@ class DecodeBatch:
 class LinearStates:
     """The states of layers of linear attention ("PagedAttention e continuous batching", "01 - Conceito", paragraph 2: beside
     the paged cache, a memory of fixed size for each sequence; there of DeltaNet layers, whose delta rule the calls
-    here do not compute): a slot of ``state`` for each sequence, all layers of it. ``slots`` gives what pkv_linear_prefill and pkv_linear_decode take; a sequence that has not been
-    listed there yet starts from zeros, whatever its slot held. ``slots`` and ``fork`` work on `stream`, else on the current
-    one, as those calls do: steps that follow one another on several streams are the caller's to order."""
+    here do not compute): a slot of ``state`` for each sequence, all layers of it. ``slots`` gives what pkv_linear_prefill
+    and pkv_linear_decode take; a sequence that has not been listed there yet starts from zeros, whatever its slot held.
+    ``slots`` and ``fork`` work on `stream`, else on the current one, as those calls do: steps that follow one another on
+    several streams are the caller's to order."""
 
     def __init__(self, desc: pkv.LinearDesc, device=None, stream=None):
         import torch
