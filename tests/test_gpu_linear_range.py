@@ -251,3 +251,48 @@ def test_short_chunks_of_bf16(dk, dv, n, n_v):
     lens = [(i * 13) % 34 for i in range(1, n + 1)]
     q, k, v, d, state, starts = inputs("bf16", lens, n_v, n_v, dk, dv, seed=77 + n)
     check("bf16", q, k, v, d, state, list(range(n)), list(range(n)), starts)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[900, 333], [2000], [RAGGED[i % 8] for i in range(24)]])
+def test_repeats_beside_other_work(dtype, lens):
+    """Bit for bit, on two streams at once and from a graph: far-apart columns, forgetting tokens, decays of both signs."""
+    n, n_v = len(lens), 8 if len(lens) > 2 else 2
+    own, T = list(range(n)), sum(lens)
+    sets = []
+    for seed in (81, 82):
+        q, k, v, _, state, starts = inputs(dtype, lens, 2, n_v, 64, 128, "none", seed=seed)
+        d = torch.cat([gates_of("normal", T, n_v, seed) * 0.3, torch.full((3, n_v), math.nan)]).cuda()
+        d[:T][torch.arange(T) % 37 == 5] = -math.inf
+        state[1, ::2, 0, :, 3] *= 2.0 ** 30
+        state[1, ::3, 1, 4, 60] = math.inf
+        sets.append((q, k, v, d, state))
+    want = []
+    for x in sets:
+        st = x[4].clone()
+        want.append((run(dtype, *x[:4], st, own, own, starts)[:T], st))
+    same = lambda a, b: torch.equal(a.view(torch.int16 if a.element_size() == 2 else torch.int32), b.view(torch.int16 if b.element_size() == 2 else torch.int32))
+    streams = [torch.cuda.Stream() for _ in sets]
+    states = [[x[4].clone() for x in sets] for _ in range(6)]
+    torch.cuda.synchronize()
+    got = []
+    for pair in states:
+        for st, x, state in zip(streams, sets, pair):
+            with torch.cuda.stream(st):
+                got.append((run(dtype, *x[:4], state, own, own, starts)[:T], state))
+    torch.cuda.synchronize()
+    for i, (out, state) in enumerate(got):
+        assert same(out, want[i % 2][0]) and same(state, want[i % 2][1])
+    desc = pkv.make_linear_desc(dtype, 2, n + 2, 2, n_v, 64, 128)
+    slots, start = (torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda") for x in (own, starts))
+    ws = pkv.alloc_linear_prefill_workspace(desc, n, T + 3, max(lens))
+    buf = [x.clone() for x in sets[0]]
+    out, graph = torch.zeros_like(buf[2]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.pkv_linear_prefill(desc, 1, *buf, slots, slots, start, max(lens), SCALE, out, ws)
+    for i in (1, 0, 1):
+        for to, frm in zip(buf, sets[i]):
+            to.copy_(frm)
+        graph.replay()
+        assert same(out[:T], want[i][0]) and same(buf[4], want[i][1])
+    assert pkv.pkv_get_device_status() == 0
