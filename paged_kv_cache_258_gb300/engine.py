@@ -543,10 +543,11 @@ class DeviceTables:
     captured in a graph and replayed, or that are to run ahead of the host.
 
     The batch takes blocks in the order of the manager's free list, row by row, as the manager itself would; ``follow``
-    then brings the manager to the same state. Whatever else is done with the manager (a sequence admitted, forked, freed or
-    appended to) makes the tables stale, for their list of free blocks is a copy: `extend` and `follow` then refuse
-    (ValueError), and new tables have to be made. A sequence whose last block is partly filled and shared is refused: its copy
-    on write is the manager's.
+    then brings the manager to the same state. The list of free blocks is a copy: once the manager has given blocks to others
+    (a sequence admitted or appended to), or a row of the batch has been changed, freed or forked with its last block
+    partly filled, the tables are stale. `extend` and `follow` then refuse (ValueError), and new tables have to be made.
+    Blocks that others free are not seen. A sequence whose last block is partly filled and shared is refused: its copy on
+    write is the manager's.
     """
 
     def __init__(self, cache: PagedKVCache, seq_ids, max_blocks: int, max_tokens: int | None = None, stream=None):
@@ -561,11 +562,12 @@ class DeviceTables:
         rc, tables, lens = cache.mgr.pack_tables(self.seq_ids, self.max_blocks)
         if rc != pkv.PKV_OK:
             raise pkv.PkvError(rc, "pack_tables (is max_blocks wide enough?)")
-        for i, c in enumerate(lens):
-            if c % pkv.BLOCK and cache.mgr.refcount(int(tables[i, c // pkv.BLOCK])) > 1:
-                raise ValueError(f"sequence {int(self.seq_ids[i])}: its last block is partly filled and shared")
+        i = self._shared_tail(tables, lens)
+        if i is not None:
+            raise ValueError(f"sequence {int(self.seq_ids[i])}: its last block is partly filled and shared")
         free = np.asarray(cache.mgr.free_list(), dtype=np.int32)
-        self._order, self._taken, self._seen = free, 0, self._manager()  # as the manager is brought along
+        # as follow has brought the manager along: blocks taken of the list, the rows' lengths, the manager's counts
+        self._order, self._taken, self._lens, self._seen = free, 0, lens.copy(), cache.mgr.stats_image()
         dev = cache.device
         with torch.cuda.stream(self.stream):
             self.tables, self.lens, self.free = (torch.from_numpy(x.copy()).to(dev) for x in (tables, lens, free))
@@ -574,13 +576,26 @@ class DeviceTables:
             self.totals = torch.zeros(3, dtype=torch.int32, device=dev)  # blocks taken, rows served, new tokens
         self.stream.synchronize()  # (steps may run on any stream)
 
-    def _manager(self) -> bytes:
-        """The manager's counts (blocks, sequences, forks, copies), which everything but adding and freeing like amounts moves."""
-        return self.cache.mgr.stats_image()
+    def _shared_tail(self, tables, lens):
+        """The first row whose last block is partly filled and shared, or None."""
+        for i, c in enumerate(lens):
+            if c % pkv.BLOCK and self.cache.mgr.refcount(int(tables[i, c // pkv.BLOCK])) > 1:
+                return i
+        return None
 
     def _check_manager(self) -> None:
-        if self._manager() != self._seen:
+        """Refuses tables that are stale. Where the manager's counts are those that follow left, nothing was done (or as many
+        blocks were taken and given back, which follow finds)."""
+        mgr = self.cache.mgr
+        seen = mgr.stats_image()
+        if seen == self._seen:
+            return
+        left = self._order[self._taken:]
+        rc, tables, lens = mgr.pack_tables(self.seq_ids, self.max_blocks)
+        if (rc != pkv.PKV_OK or not np.array_equal(lens, self._lens) or self._shared_tail(tables, lens) is not None or
+                not np.array_equal(np.asarray(mgr.free_list(), dtype=np.int32)[:len(left)], left)):
             raise ValueError("the manager has changed by other than follow: these tables are stale, make new ones")
+        self._seen = seen
 
     def extend(self, new_tokens=None, stream=None) -> None:
         """One step's new tokens: int32 [n] on the device, or one for each row. tables, lens, slots, query_start and
@@ -600,18 +615,17 @@ class DeviceTables:
         try:
             return self._follow(mgr, counts)
         finally:
-            self._seen = self._manager()
+            self._seen = mgr.stats_image()
 
     def _follow(self, mgr, counts) -> int:
         total = 0
         for i, m in enumerate(counts):
-            sid = int(self.seq_ids[i])
-            rc, table, ctx = mgr.block_table(sid)
-            if rc != pkv.PKV_OK:
-                raise pkv.PkvError(rc, f"block_table({sid})")
+            sid, ctx = int(self.seq_ids[i]), int(self._lens[i])
             total += max(m, 0)
             if m > 0:
-                if total > self.max_tokens or -(-(ctx + m) // pkv.BLOCK) > self.max_blocks:
+                want = -(-(ctx + m) // pkv.BLOCK)
+                need = want + -ctx // pkv.BLOCK
+                if total > self.max_tokens or want > self.max_blocks or need > len(self._order) - self._taken:
                     return i
                 rc, slots, _, _ = mgr.extend(sid, m)
                 if rc == pkv.PKV_ERR_NO_BLOCKS:
@@ -619,9 +633,10 @@ class DeviceTables:
                 if rc != pkv.PKV_OK:
                     raise pkv.PkvError(rc, f"extend({sid}, {m})")
                 fresh = slots[-ctx % pkv.BLOCK::pkv.BLOCK] // pkv.BLOCK
-                if not np.array_equal(fresh, self._order[self._taken:self._taken + len(fresh)]):
+                if not np.array_equal(fresh, self._order[self._taken:self._taken + need]):
                     raise ValueError(f"sequence {sid}: the manager's blocks are not those that the device took")
-                self._taken += len(fresh)
+                self._taken += need
+                self._lens[i] += m
         return self.n
 
 

@@ -45,6 +45,25 @@ def test_blocks_that_moved_in_the_free_list_are_found_by_follow():
         tables.follow()
 
 
+def test_blocks_that_others_free_are_not_seen():
+    """A sequence beside the batch ends, or a row whose blocks are full is forked: the tables go on, with the blocks they know."""
+    cache, _ = made(nb=9)
+    cache.add_sequence(9, 60)                          # 2 + 1 + 0 + 4 blocks of 9
+    tables = DeviceTables(cache, [1, 2, 3], 8, max_tokens=100)
+    cache.mgr.free_seq(9)
+    for counts, served in (([13, 0, 2], 3), ([0, 1, 0], 1), ([0, 0, 14], 3), ([0, 0, 1], 2)):
+        tables.extend(torch.tensor(counts, dtype=torch.int32, device="cuda"))
+        assert tables.totals[1].item() == served == tables.follow(counts)
+        rc, host, lens = cache.mgr.pack_tables([1, 2, 3], 8)
+        assert np.array_equal(tables.tables.cpu().numpy(), host) and np.array_equal(tables.lens.cpu().numpy(), lens)
+    cache.fork(2, 10)                                  # 16 tokens: a whole block
+    tables.extend(torch.tensor([1, 0, 0], dtype=torch.int32, device="cuda"))
+    assert tables.follow([1, 0, 0]) == 3
+    cache.fork(1, 11)                                  # 34 tokens
+    with pytest.raises(ValueError, match="stale"):
+        tables.extend()
+
+
 def test_rows_that_do_not_fit_leave_the_tables_usable():
     cache, tables = made(nb=6, max_tokens=100)
     counts = [[1, 1, 1], [20, 20, 20], [3, 1, 2]]
