@@ -104,7 +104,7 @@ struct __align__(16) PieceGates {
     float sum;                     // else S * keep + U, once = 0; the sum over all
 };
 
-// fp16: the powers of two that bring what its products take into its range.
+// fp16: what tokens forget, and the powers of two that bring what the products take into its range.
 struct __align__(16) HalfScales {
     uint32_t forgotten[2][kPiece]; // of a token's block of 32: those that it, or one between, forgets
     float front[2][kPiece];        // sums from a token's block's start all the same
@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             pf[j] = j <= lane - side ? pf[j] : 0.f;
                             most = fmaxf(most, fabsf(pf[j]));
                         }
-                        half.row_most[c & 1][side >> 4][row] = most;  // (the other warp has read those of two pieces ago: it met since)
+                        // (the other warp has read that of two pieces ago: it met since)
+                        half.row_most[c & 1][side >> 4][row] = most;
                         arrive_warp(&halves[w4]);
                         if (!wait(&halves[w4], c)) { ok = false; break; }
                         const int e = exponent14(fmaxf(most, half.row_most[c & 1][(side >> 4) ^ 1][row]));
@@ -984,7 +985,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
                         for (int c0 = 0; c0 < kSlice; c0 += 16) {
                             uint32_t w[8];
-                            slice_of(c0, w, 0, [&](int j) { return f2_mul(fi2, *reinterpret_cast<const uint64_t*>(&half.col_back[c & 3][j])); });
+                            const float* back = half.col_back[c & 3];
+                            slice_of(c0, w, 0, [&](int j) { return f2_mul(fi2, *reinterpret_cast<const uint64_t*>(back + j)); });
                             out_words(out + c0 * sizeof(T), w);
                         }
                     } else if constexpr (MORE) {
